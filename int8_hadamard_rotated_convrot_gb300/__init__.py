@@ -7,17 +7,19 @@ identically rotated per-row-quantized int8 weights with exact integer
 accumulation, and reconstruct Y = A * s_x * s_w + b.
 
 Everything runs in libconvrot's CUDA kernels (C ABI in include/convrot.h);
-``convrot`` is the ctypes binding, ``inputs`` the seeded synthetic workloads.
+``convrot`` is the ctypes binding, ``inputs`` the seeded synthetic workloads,
+``block`` the binding of the operators around the linears of a transformer
+block (include/convrot_block.h).
 """
 
 from . import inputs  # noqa: F401
 
-__all__ = ["inputs", "convrot"]
+__all__ = ["inputs", "convrot", "block"]
 
 
 def __getattr__(name):
-    if name == "convrot":
+    if name in ("convrot", "block"):
         import importlib
 
-        return importlib.import_module(__name__ + ".convrot")
+        return importlib.import_module(__name__ + "." + name)
     raise AttributeError(name)

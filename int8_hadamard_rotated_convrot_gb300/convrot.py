@@ -41,6 +41,17 @@ EXPORTED = [
     "convrot_gemm_i32",
     "convrot_wait_check",
     "convrot_status_string",
+    # the operators around the linears (bound in block.py)
+    "convrot_fp8_pack_activations",
+    "convrot_fp8_quantize_weights",
+    "convrot_fp8_linear",
+    "convrot_fp8_pack_linear_work_bytes",
+    "convrot_fp8_pack_linear",
+    "convrot_gated_norm",
+    "convrot_gated_norm_backward_work_bytes",
+    "convrot_gated_norm_backward",
+    "convrot_rotary",
+    "convrot_rotary_table",
 ]
 
 
@@ -112,6 +123,16 @@ def load() -> ctypes.CDLL:
         lib.convrot_gemm_i32.restype = ctypes.c_int
         lib.convrot_wait_check.argtypes = [vp, ctypes.c_uint64, i32, vp]
         lib.convrot_wait_check.restype = ctypes.c_int
+        lib.convrot_fp8_pack_activations.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
+        lib.convrot_fp8_quantize_weights.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp]
+        lib.convrot_fp8_pack_linear_work_bytes.argtypes = [i64, i64, i64]
+        lib.convrot_gated_norm_backward_work_bytes.argtypes = [i64, i64, i64]
+        for name in ("convrot_fp8_pack_linear_work_bytes", "convrot_gated_norm_backward_work_bytes"):
+            getattr(lib, name).restype = i64
+        for name in ("convrot_fp8_linear", "convrot_fp8_pack_linear", "convrot_gated_norm",
+                     "convrot_gated_norm_backward", "convrot_rotary"):
+            getattr(lib, name).argtypes = [ctypes.c_char_p, vp]  # one packed struct of arguments
+        lib.convrot_rotary_table.argtypes = [vp, i64, i32, vp, vp, i32, ctypes.c_double, vp, vp, i64, vp]
         lib.convrot_status_string.argtypes = [ctypes.c_int]
         lib.convrot_status_string.restype = ctypes.c_char_p
         _lib = lib
