@@ -50,6 +50,52 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// N consecutive elements as one access of up to 16 bytes (N * sizeof(T) a power
+// of two); the address is aligned to it. kStream: the line is not needed again
+// (evict-first); the loads stay coherent, so an output may be its own input.
+template <int kBytes>
+struct Bits;
+template <>
+struct Bits<2> { using type = unsigned short; };
+template <>
+struct Bits<4> { using type = unsigned int; };
+template <>
+struct Bits<8> { using type = uint2; };
+template <>
+struct Bits<16> { using type = uint4; };
+
+template <typename T, int N>
+struct Raw {
+    static constexpr int kBytes = N * static_cast<int>(sizeof(T));
+    static constexpr int kParts = kBytes > 16 ? kBytes / 16 : 1;
+    using B = typename Bits<(kBytes > 16 ? 16 : kBytes)>::type;
+    B bits[kParts];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) bits[i] = reinterpret_cast<const B *>(p)[i];
+    }
+    __device__ __forceinline__ void load_stream(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) bits[i] = __ldcs(reinterpret_cast<const B *>(p) + i);
+    }
+    __device__ __forceinline__ void store(T *p) const
+    {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) reinterpret_cast<B *>(p)[i] = bits[i];
+    }
+    __device__ __forceinline__ void store_stream(T *p) const
+    {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) __stcs(reinterpret_cast<B *>(p) + i, bits[i]);
+    }
+    __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const T *>(bits)[i]); }
+    __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T *>(bits)[i] = from_f32<T>(v); }
+};
+
+inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 constexpr float kFp8Max = 448.0f;
 constexpr float kFp8AmaxFloor = 1.2621774483536189e-29f;  // 2^-96: no block's scale is 0 or its inverse infinite
 
