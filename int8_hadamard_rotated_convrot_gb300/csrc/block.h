@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/convrot_block.h"
 
@@ -50,6 +51,43 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
+// Two fp32 values that one instruction works on (fma.rn.f32x2 and its kin:
+// each half rounded as the single operation would be).
+struct F2 {
+    unsigned long long v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+    __device__ __forceinline__ float lo() const
+    {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return a;
+    }
+    __device__ __forceinline__ float hi() const
+    {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return b;
+    }
+    __device__ __forceinline__ float sum() const { return lo() + hi(); }
+};
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a.v) : "l"(a.v), "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(c.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return c;
+}
+
 // N consecutive elements as one access of up to 16 bytes (N * sizeof(T) a power
 // of two); the address is aligned to it. kStream: the line is not needed again
 // (evict-first); the loads stay coherent, so an output may be its own input.
@@ -90,9 +128,86 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) __stcs(reinterpret_cast<B *>(p) + i, bits[i]);
     }
-    __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const T *>(bits)[i]); }
-    __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T *>(bits)[i] = from_f32<T>(v); }
+    // All N values; 16-bit types two at a time (one operation a value to widen
+    // bf16, one for two values to round).
+    __device__ __forceinline__ void unpack(float (&v)[N]) const
+    {
+        if constexpr (N == 1) {
+            v[0] = to_f32(*reinterpret_cast<const T *>(bits));
+        } else {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(bits);
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    v[i] = __uint_as_float(w[i]);
+                } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(F2 *v) const
+    {
+        float f[N];
+        unpack(f);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) v[i] = F2(f[2 * i], f[2 * i + 1]);
+    }
+    __device__ __forceinline__ void pack(const F2 *v)
+    {
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            f[2 * i] = v[i].lo();
+            f[2 * i + 1] = v[i].hi();
+        }
+        pack(f);
+    }
+    __device__ __forceinline__ void pack(const float (&v)[N])
+    {
+        if constexpr (N == 1) {
+            *reinterpret_cast<T *>(bits) = from_f32<T>(v[0]);
+        } else {
+            uint32_t *w = reinterpret_cast<uint32_t *>(bits);
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(v[i]);
+                } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                } else {
+                    const __half2 b = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+            }
+        }
+    }
 };
+
+// 16 bytes from global to shared memory without a register between.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of this thread's groups but the last kPending have landed.
+template <int kPending>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
 
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 

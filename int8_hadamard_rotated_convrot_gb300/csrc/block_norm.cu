@@ -27,8 +27,7 @@ __device__ __forceinline__ void params(const void *p, int64_t i, float otherwise
     if (p) {
         Raw<P, kVec> r;
         r.load(static_cast<const P *>(p) + i);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = r.get(e);
+        r.unpack(v);
     } else {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[e] = otherwise;
@@ -42,13 +41,20 @@ template <bool kWarp>
 struct RowSum {
     float2 *slots;  // [2][32]
     int turn = 0;
+    // Two sums at once: the first step leaves a's on one half of the warp and
+    // b's on the other, the next four serve both.
+    static __device__ __forceinline__ void warp_sum(float &a, float &b)
+    {
+        const bool upper = threadIdx.x & 16;
+        float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        a = __shfl_sync(0xffffffffu, v, 0);
+        b = __shfl_sync(0xffffffffu, v, 16);
+    }
     __device__ __forceinline__ void operator()(float &a, float &b)
     {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
+        warp_sum(a, b);
         if (kWarp || blockDim.x == 32) return;
         float2 *s = slots + 32 * turn;
         turn ^= 1;
@@ -58,16 +64,21 @@ struct RowSum {
         const float2 v = lane < warps ? s[lane] : make_float2(0.0f, 0.0f);
         a = v.x;
         b = v.y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, o);
-            b += __shfl_xor_sync(0xffffffffu, b, o);
-        }
+        warp_sum(a, b);
     }
     __device__ __forceinline__ float operator()(float a)
     {
-        float b = 0.0f;
-        (*this)(a, b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (kWarp || blockDim.x == 32) return a;
+        float2 *s = slots + 32 * turn;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5].x = a;
+        __syncthreads();
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        a = lane < warps ? s[lane].x : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
         return a;
     }
 };
@@ -85,7 +96,7 @@ __device__ __forceinline__ void normalize(float (&v)[kNv][kVec], int d, int kind
         for (int j = 0; j < kNv; ++j)
 #pragma unroll
             for (int e = 0; e < kVec; ++e) s += v[j][e];
-        mean = sum(s) / d;
+        mean = sum(s) * (1.0f / d);
     }
     float s = 0.0f;
 #pragma unroll
@@ -97,13 +108,47 @@ __device__ __forceinline__ void normalize(float (&v)[kNv][kVec], int d, int kind
             s = fmaf(v[j][e], v[j][e], s);
         }
     }
-    const float inv = 1.0f / sqrtf(sum(s) / d + eps);
+    const float inv = rsqrtf(fmaf(sum(s), 1.0f / d, eps));
 #pragma unroll
     for (int j = 0; j < kNv; ++j)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[j][e] *= inv;
 }
 
+// Codes and scales of a row of n in 16-byte pieces: 128 / kVec threads hold a
+// block of 128 values (a thread's pieces are nt apart, a multiple of 32, so the
+// same threads share each block). Values past the row are zero.
+template <int kVec, int kNv>
+__device__ __forceinline__ void pack_row(const convrot_gated_norm_args &a, int64_t r, int d, int tid, int nt, const float (&h)[kNv][kVec])
+{
+    uint8_t *q = static_cast<uint8_t *>(a.q) + r * a.ldq;
+    auto at = [&](int j) { return (tid + j * nt) * kVec; };
+#pragma unroll
+    for (int j = 0; j < kNv; ++j) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) m = fmaxf(m, fabsf(h[j][e]));
+#pragma unroll
+        for (int o = 64 / kVec; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (!at(j) < d) continue;
+        m = fmaxf(m, kFp8AmaxFloor);
+        if (at(j) % 128 == 0) a.q_scale[(at(j) >> 7) * a.ld_q_scale + r] = m / kFp8Max;
+        const float up = fp8_up(m);
+        uint32_t w[kVec / 4];
+#pragma unroll
+        for (int e = 0; e < kVec; e += 4)
+            w[e / 4] = e4m3x4(h[j][e] * up, h[j][e + 1] * up, h[j][e + 2] * up, h[j][e + 3] * up);
+        if constexpr (kVec == 8)
+            *reinterpret_cast<uint2 *>(q + at(j)) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(q + at(j)) = w[0];
+    }
+}
+
+// Rows of a sample in 32 bits (row numbers have 31).
+__device__ __forceinline__ uint32_t sample_rows(int64_t rows) { return rows < 0x7fffffff ? static_cast<uint32_t>(rows) : 0x7fffffffu; }
+
+constexpr int kSms = 152;
 constexpr int kRowThreads = 512;  // 128 registers a thread: up to 32 values of a row in each
 
 template <typename T, typename P, int kVec, int kNv, bool kWarp>
@@ -114,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nt = kWarp ? 32 : blockDim.x;
     const int64_t r = kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (kWarp && r >= a.m) return;
-    const int64_t b = r / a.rows_per_batch;
+    const int64_t b = static_cast<uint32_t>(r) / sample_rows(a.rows_per_batch);
     const int d = static_cast<int>(a.d);
     RowSum<kWarp> sum{slots};
     auto at = [&](int j) { return (tid + j * nt) * kVec; };
@@ -131,9 +176,14 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
     float h[kNv][kVec];
     if (a.y) {
 #pragma unroll
-        for (int j = 0; j < kNv; ++j)
+        for (int j = 0; j < kNv; ++j) {
+            if (in_row(j)) {
+                yr[j].unpack(h[j]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = in_row(j) ? yr[j].get(e) : 0.0f;
+                for (int e = 0; e < kVec; ++e) h[j][e] = 0.0f;
+            }
+        }
         normalize(h, d, a.post, a.eps, sum, in_row);
     }
 #pragma unroll
@@ -144,6 +194,8 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
             continue;
         }
         const int i = at(j);
+        float xv[kVec];
+        xr[j].unpack(xv);
         if (a.y) {
             float p[kVec];
             if (a.post_weight) {
@@ -158,14 +210,13 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
             }
             params<P>(a.gate, b * a.ldgate + i, 1.0f, p);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = fmaf(a.res_scale, xr[j].get(e), p[e] * h[j][e]);
+            for (int e = 0; e < kVec; ++e) h[j][e] = fmaf(a.res_scale, xv[e], p[e] * h[j][e]);
         } else {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = a.res_scale * xr[j].get(e);
+            for (int e = 0; e < kVec; ++e) h[j][e] = a.res_scale * xv[e];
         }
         if (a.h) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) xr[j].set(e, h[j][e]);
+            xr[j].pack(h[j]);
             xr[j].store(static_cast<T *>(a.h) + r * a.ldh + i);
         }
     }
@@ -189,7 +240,7 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
         if (a.scale) {
             params<P>(a.scale, b * a.ldscale + i, 0.0f, p);
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] *= 1.0f + p[e];
+            for (int e = 0; e < kVec; ++e) h[j][e] = fmaf(h[j][e], p[e], h[j][e]);
         }
         if (a.shift) {
             params<P>(a.shift, b * a.ldshift + i, 0.0f, p);
@@ -197,15 +248,12 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
             for (int e = 0; e < kVec; ++e) h[j][e] += p[e];
         }
         if (a.n) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) xr[j].set(e, h[j][e]);
+            xr[j].pack(h[j]);
             xr[j].store(static_cast<T *>(a.n) + r * a.ldn + i);
         }
     }
     if (!a.q) return;
-    // n's pack: 128 / kVec threads hold a block of 128 values (a thread's vectors are blockDim vectors apart, a
-    // multiple of 32 of them, so the groups of threads are the same for each); single elements of a block lie in
-    // four warps, which meet in shared memory.
+    // n's pack; single elements of a block of 128 lie in four warps, which meet in shared memory
     uint8_t *q = static_cast<uint8_t *>(a.q) + r * a.ldq;
     if constexpr (kVec == 1 && kWarp) {
         // one warp, single elements: a block is vectors 4 jb .. 4 jb + 3 of every lane
@@ -243,25 +291,189 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
             q[at(j)] = e4m3(h[j][0] * fp8_up(m));
         }
     } else {
+        pack_row<kVec, kNv>(a, r, d, tid, nt, h);
+    }
+}
+
+// The same for many rows: each block takes a run of them, and each thread
+// copies its own 16-byte pieces of the next rows into its own places in shared
+// memory (cp.async), kStages rows ahead. What a thread copied it reads back
+// itself, so the ring needs no barrier; HBM stays busy through the sums around
+// the block. Row pointers and the sample's vectors are stepped, not computed.
+template <typename T, typename P, int kNv, int kStages>
+__global__ void __launch_bounds__(kRowThreads) gated_norm_ring_kernel(const __grid_constant__ convrot_gated_norm_args a, int32_t rows)
+{
+    constexpr int kVec = 16 / sizeof(T), kPairs = kVec / 2;
+    extern __shared__ uint4 ring[];  // [kStages][x, y][kNv][blockDim]
+    __shared__ float2 slots[64];
+    const int nt = blockDim.x, d = static_cast<int>(a.d);
+    const float inv_d = 1.0f / d;
+    RowSum<false> sum{slots};
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
+    const uint32_t step = nt * 16, stage_bytes = step * kNv * (a.y ? 2 : 1);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
+    const int count = static_cast<int>(a.m - first < rows ? a.m - first : rows);
+    auto at = [&](int j) { return (static_cast<int>(threadIdx.x) + j * nt) * kVec; };
+    auto in_row = [&](int j) { return at(j) < d; };
+
+    const T *x = static_cast<const T *>(a.x) + first * a.ldx + at(0), *y = static_cast<const T *>(a.y) + first * a.ldy + at(0);
+    T *h_out = a.h ? static_cast<T *>(a.h) + first * a.ldh + at(0) : nullptr;
+    T *n_out = a.n ? static_cast<T *>(a.n) + first * a.ldn + at(0) : nullptr;
+    auto fetch = [&](int stage) {
+        uint32_t to = mine + stage * stage_bytes;
+#pragma unroll
+        for (int j = 0; j < kNv; ++j)
+            if (in_row(j)) {
+                copy16(to + j * step, x + j * nt * kVec);
+                if (a.y) copy16(to + (kNv + j) * step, y + j * nt * kVec);
+            }
+        x += a.ldx;
+        y += a.ldy;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        if (s < count) fetch(s);
+        copy_commit();
+    }
+    uint32_t sample = static_cast<uint32_t>(first) / sample_rows(a.rows_per_batch);
+    int64_t left = (sample + 1ll) * a.rows_per_batch - first;  // rows of this sample
+    int stage = 0, ahead = kStages - 1;
+    for (int r = 0; r < count; ++r) {
+        if (r + kStages - 1 < count) fetch(ahead);
+        copy_commit();
+        if (++ahead == kStages) ahead = 0;
+        copy_wait<kStages - 1>();
+        const uint32_t from = mine + stage * stage_bytes;
+        if (++stage == kStages) stage = 0;
+
+        F2 h[kNv][kPairs];
+        auto normalize = [&](int kind) {
+            if (kind == CONVROT_NORM_NONE) return;
+            if (kind == CONVROT_NORM_LAYER) {
+                F2 s(0.0f);
+#pragma unroll
+                for (int j = 0; j < kNv; ++j)
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) s = s + h[j][e];
+                const F2 mean(-sum(s.sum()) * inv_d);
+#pragma unroll
+                for (int j = 0; j < kNv; ++j)
+                    if (in_row(j))
+#pragma unroll
+                        for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + mean;
+            }
+            F2 s(0.0f);
+#pragma unroll
+            for (int j = 0; j < kNv; ++j)
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) s = fma2(h[j][e], h[j][e], s);
+            const F2 inv(rsqrtf(fmaf(sum(s.sum()), inv_d, a.eps)));
+#pragma unroll
+            for (int j = 0; j < kNv; ++j)
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * inv;
+        };
+        // v * p, v + p and v + v p with the vector p of this thread's columns
+        auto vec = [&](const void *p, int64_t offset, int j, F2 (&v)[kPairs]) {
+            Raw<P, kVec> raw;
+            raw.load(static_cast<const P *>(p) + offset + at(j));
+            raw.unpack(v);
+        };
+        if (a.y) {
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) {
+                Raw<T, kVec> raw{};
+                if (in_row(j)) raw.bits[0] = shared16(from + (kNv + j) * step);
+                raw.unpack(h[j]);
+            }
+            normalize(a.post);
+        }
 #pragma unroll
         for (int j = 0; j < kNv; ++j) {
-            float m = 0.0f;
+            if (!in_row(j)) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) m = fmaxf(m, fabsf(h[j][e]));
+                for (int e = 0; e < kPairs; ++e) h[j][e] = F2(0.0f);
+                continue;
+            }
+            Raw<T, kVec> raw;
+            F2 xv[kPairs], p[kPairs];
+            raw.bits[0] = shared16(from + j * step);
+            raw.unpack(xv);
+            const F2 res(a.res_scale);
+            if (a.y) {
+                if (a.post_weight) {
+                    vec(a.post_weight, 0, j, p);
 #pragma unroll
-            for (int o = 64 / kVec; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
+                }
+                if (a.post_bias) {
+                    vec(a.post_bias, 0, j, p);
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
+                }
+                if (a.gate) {
+                    vec(a.gate, sample * a.ldgate, j, p);
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
+                }
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = fma2(res, xv[e], h[j][e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = res * xv[e];
+            }
+            if (h_out) {
+                raw.pack(h[j]);
+                raw.store(h_out + j * nt * kVec);
+            }
+        }
+        if (h_out) h_out += a.ldh;
+        normalize(a.pre);
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) {
             if (!in_row(j)) continue;
-            m = fmaxf(m, kFp8AmaxFloor);
-            if (at(j) % 128 == 0) a.q_scale[(at(j) >> 7) * a.ld_q_scale + r] = m / kFp8Max;
-            const float up = fp8_up(m);
-            uint32_t w[kVec / 4];
+            F2 p[kPairs];
+            if (a.pre_weight) {
+                vec(a.pre_weight, 0, j, p);
 #pragma unroll
-            for (int e = 0; e < kVec; e += 4)
-                w[e / 4] = e4m3x4(h[j][e] * up, h[j][e + 1] * up, h[j][e + 2] * up, h[j][e + 3] * up);
-            if constexpr (kVec == 8)
-                *reinterpret_cast<uint2 *>(q + at(j)) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<uint32_t *>(q + at(j)) = w[0];
+                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
+            }
+            if (a.pre_bias) {
+                vec(a.pre_bias, 0, j, p);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
+            }
+            if (a.scale) {
+                vec(a.scale, sample * a.ldscale, j, p);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = fma2(h[j][e], p[e], h[j][e]);
+            }
+            if (a.shift) {
+                vec(a.shift, sample * a.ldshift, j, p);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
+            }
+            if (n_out) {
+                Raw<T, kVec> raw;
+                raw.pack(h[j]);
+                raw.store(n_out + j * nt * kVec);
+            }
+        }
+        if (n_out) n_out += a.ldn;
+        if (a.q) {
+            float v[kNv][kVec];
+#pragma unroll
+            for (int j = 0; j < kNv; ++j)
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) {
+                    v[j][2 * e] = h[j][e].lo();
+                    v[j][2 * e + 1] = h[j][e].hi();
+                }
+            pack_row<kVec, kNv>(a, first + r, d, threadIdx.x, nt, v);
+        }
+        if (--left == 0) {
+            ++sample;
+            left = a.rows_per_batch;
         }
     }
 }
@@ -290,8 +502,6 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
 constexpr int kGradCols = 8;           // columns a thread
 constexpr int kGradThreads = 640;      // of one block: 96 registers a thread
 constexpr int kGradWidth = kGradCols * kGradThreads;
-constexpr int kSms = 152;
-
 // How rows are split: the same on the host that sizes the workspace and at the launch.
 struct GradSplit {
     int cluster;        // blocks that share a row
@@ -357,12 +567,23 @@ struct GradSum {
     }
 };
 
+// Rows of the ring: 4 tensors of 16 bytes a thread and row (32 for 32-bit
+// types), 160 KB for the widest block.
+template <typename T>
+constexpr int grad_stages()
+{
+    return sizeof(T) == 2 ? 4 : 2;
+}
+
 template <typename T, typename P, int kVec, int kCluster>
 __global__ void __launch_bounds__(kGradThreads, 1)
     norm_grad_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, const __grid_constant__ GradSplit split, float *part)
 {
-    constexpr int kNv = kGradCols / kVec;
-    constexpr bool kAhead = sizeof(T) == 2;
+    // Eight columns a thread, in kNv pieces of kVec; four pairs of them for the packed arithmetic. 16-byte pieces
+    // come through a ring of rows in shared memory that each thread fills for itself, single elements directly.
+    constexpr int kNv = kGradCols / kVec, kPairs = kGradCols / 2, kStages = grad_stages<T>();
+    constexpr bool kRing = kVec > 1;
+    extern __shared__ uint4 ring[];  // [kStages][h, y, dh, dn][kNv][blockDim]
     __shared__ float2 slots[64];
     __shared__ float2 peers[2 * kCluster];
     GradSum<kCluster> sum{{slots}, peers};
@@ -372,166 +593,227 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     int64_t last = first + split.rows_per_chunk;
     if (last > (b + 1) * a.rows_per_batch) last = (b + 1) * a.rows_per_batch;
     if (last > a.m) last = a.m;
+    const int count = last > first ? static_cast<int>(last - first) : 0;
     const int c0 = kCluster > 1 ? static_cast<int>(cluster_rank()) * split.width : 0;
     const int end = c0 + split.width < a.d ? c0 + split.width : static_cast<int>(a.d);
-    const int d = static_cast<int>(a.d);
-    auto at = [&](int j) { return c0 + (static_cast<int>(threadIdx.x) + j * static_cast<int>(blockDim.x)) * kVec; };
+    const float inv_d = 1.0f / static_cast<float>(a.d);
+    const int nt = blockDim.x;
+    auto at = [&](int j) { return c0 + (static_cast<int>(threadIdx.x) + j * nt) * kVec; };
     auto inside = [&](int j) { return at(j) < end; };
 
-    struct Row {
-        Raw<T, kVec> h[kNv], y[kNv], dh[kNv], dn[kNv];
+    const T *in[4] = {static_cast<const T *>(a.h) + first * a.ldh + at(0),
+                      a.y ? static_cast<const T *>(a.y) + first * a.ldy + at(0) : nullptr,
+                      a.dh ? static_cast<const T *>(a.dh) + first * a.lddh + at(0) : nullptr,
+                      a.dn ? static_cast<const T *>(a.dn) + first * a.lddn + at(0) : nullptr};
+    auto advance = [&]() {
+        in[0] += a.ldh;
+        if (in[1]) in[1] += a.ldy;
+        if (in[2]) in[2] += a.lddh;
+        if (in[3]) in[3] += a.lddn;
     };
-    auto load = [&](Row &v, int64_t r) {
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
+    const uint32_t piece = nt * 16;
+    auto fetch = [&](int stage) {
 #pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            if (!inside(j)) continue;
-            v.h[j].load_stream(static_cast<const T *>(a.h) + r * a.ldh + at(j));
-            if (a.y) v.y[j].load_stream(static_cast<const T *>(a.y) + r * a.ldy + at(j));
-            if (a.dh) v.dh[j].load_stream(static_cast<const T *>(a.dh) + r * a.lddh + at(j));
-            if (a.dn) v.dn[j].load_stream(static_cast<const T *>(a.dn) + r * a.lddn + at(j));
+        for (int k = 0; k < 4; ++k)
+            if (in[k])
+#pragma unroll
+                for (int j = 0; j < kNv; ++j)
+                    if (inside(j)) copy16(mine + ((stage * 4 + k) * kNv + j) * piece, in[k] + j * nt * kVec);
+        advance();
+    };
+    int stage = 0, ahead = kStages - 1;
+    // this thread's values of tensor k in the current row, zero where there are none
+    auto get = [&](int k, F2 (&v)[kPairs]) {
+        if constexpr (kRing) {
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) {
+                Raw<T, kVec> raw{};
+                if (in[k] && inside(j)) raw.bits[0] = shared16(mine + ((stage * 4 + k) * kNv + j) * piece);
+                raw.unpack(v + j * kVec / 2);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e)
+                v[e] = F2(in[k] && inside(2 * e) ? to_f32(in[k][2 * e * nt]) : 0.0f,
+                          in[k] && inside(2 * e + 1) ? to_f32(in[k][(2 * e + 1) * nt]) : 0.0f);
         }
     };
-
-    float s0[kNv][kVec] = {}, s1[kNv][kVec] = {}, t0[kNv][kVec] = {}, t1[kNv][kVec] = {};
-    Row row;
-    if (kAhead && first < last) load(row, first);
-    for (int64_t r = first; r < last; ++r) {
-        float h[kNv][kVec], y[kNv][kVec], dh[kNv][kVec];
-        Raw<T, kVec> dnr[kNv];
-        if (!kAhead) load(row, r);
-#pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            const bool in = inside(j);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                h[j][e] = in ? row.h[j].get(e) : 0.0f;
-                y[j][e] = in && a.y ? row.y[j].get(e) : 0.0f;
-                dh[j][e] = in && a.dh ? row.dh[j].get(e) : 0.0f;
-            }
-            if (in && a.dn) {
-                dnr[j] = row.dn[j];
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) dnr[j].set(e, 0.0f);
-            }
-        }
-        if (kAhead && r + 1 < last) load(row, r + 1);
-
-        // h^ and y^
-        float hm = 0.0f, ym = 0.0f;
-        if (a.pre == CONVROT_NORM_LAYER || (a.y && a.post == CONVROT_NORM_LAYER)) {
-#pragma unroll
-            for (int j = 0; j < kNv; ++j)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    hm += h[j][e];
-                    ym += y[j][e];
-                }
-            sum(hm, ym);
-            hm = a.pre == CONVROT_NORM_LAYER ? hm / d : 0.0f;
-            ym = a.post == CONVROT_NORM_LAYER ? ym / d : 0.0f;
-        }
-        float hv = 0.0f, yv = 0.0f;
-        const bool stats = a.pre != CONVROT_NORM_NONE || (a.y && a.post != CONVROT_NORM_NONE);
-        if (stats) {
+    auto put = [&](T *p, const F2 (&v)[kPairs]) {
+        if constexpr (kRing) {
 #pragma unroll
             for (int j = 0; j < kNv; ++j) {
                 if (!inside(j)) continue;
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    h[j][e] -= hm;
-                    y[j][e] -= ym;
-                    hv = fmaf(h[j][e], h[j][e], hv);
-                    yv = fmaf(y[j][e], y[j][e], yv);
-                }
+                Raw<T, kVec> raw;
+                raw.pack(v + j * kVec / 2);
+                raw.store_stream(p + j * nt * kVec);
             }
-            sum(hv, yv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                if (inside(2 * e)) p[2 * e * nt] = from_f32<T>(v[e].lo());
+                if (inside(2 * e + 1)) p[(2 * e + 1) * nt] = from_f32<T>(v[e].hi());
+            }
         }
-        const float inv = a.pre != CONVROT_NORM_NONE ? 1.0f / sqrtf(hv / d + a.eps) : 1.0f;
-        const float inv_y = a.post != CONVROT_NORM_NONE ? 1.0f / sqrtf(yv / d + a.eps) : 1.0f;
+    };
+    // the columns' factors, the same for the whole run: (1 + scale) w_pre and gate w_post
+    auto column = [&](const void *p, int64_t offset, int i, float otherwise) {
+        const int j = i / kVec;
+        return inside(j) ? param<P>(p, offset + at(j) + i % kVec, otherwise) : 0.0f;
+    };
+    F2 w_pre[kPairs], w_post[kPairs], s0[kPairs], s1[kPairs], t0[kPairs], t1[kPairs];
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+        float u[2], v[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u[i] = (1.0f + column(a.scale, b * a.ldscale, 2 * e + i, 0.0f)) * column(a.pre_weight, 0, 2 * e + i, 1.0f);
+            v[i] = column(a.gate, b * a.ldgate, 2 * e + i, 1.0f) * column(a.post_weight, 0, 2 * e + i, 1.0f);
+        }
+        w_pre[e] = F2(u[0], u[1]);
+        w_post[e] = F2(v[0], v[1]);
+        s0[e] = s1[e] = t0[e] = t1[e] = F2(0.0f);
+    }
+    T *dx = a.dx ? static_cast<T *>(a.dx) + first * a.lddx + at(0) : nullptr;
+    T *dy = a.dy ? static_cast<T *>(a.dy) + first * a.lddy + at(0) : nullptr;
+    const bool y_layer = a.y && a.post == CONVROT_NORM_LAYER;
 
-        // dH and the means that pre's gradient subtracts
-        float g[kNv][kVec], mg = 0.0f, mgh = 0.0f;
+    if constexpr (kRing) {
 #pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            if (!inside(j)) continue;
-            float up[kVec], w[kVec];
-            params<P>(a.scale, b * a.ldscale + at(j), 0.0f, up);
-            params<P>(a.pre_weight, at(j), 1.0f, w);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const float dn = dnr[j].get(e);
-                h[j][e] *= inv;
-                y[j][e] *= inv_y;
-                s0[j][e] += dn;
-                s1[j][e] = fmaf(dn, h[j][e], s1[j][e]);
-                g[j][e] = dn * (1.0f + up[e]) * w[e];
-                mg += g[j][e];
-                mgh = fmaf(g[j][e], h[j][e], mgh);
-            }
-        }
-        if (a.pre != CONVROT_NORM_NONE) {
-            sum(mg, mgh);
-            mg = a.pre == CONVROT_NORM_LAYER ? mg / d : 0.0f;
-            mgh /= d;
-        } else {
-            mg = mgh = 0.0f;
-        }
-        float mq = 0.0f, mqy = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            if (!inside(j)) continue;
-            Raw<T, kVec> out;
-            float gate[kVec], w[kVec];
-            if (a.y) {
-                params<P>(a.gate, b * a.ldgate + at(j), 1.0f, gate);
-                params<P>(a.post_weight, at(j), 1.0f, w);
-            }
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                dh[j][e] = fmaf(inv, g[j][e] - mg - h[j][e] * mgh, dh[j][e]);
-                out.set(e, a.res_scale * dh[j][e]);
-                if (a.y) {
-                    t0[j][e] += dh[j][e];
-                    t1[j][e] = fmaf(dh[j][e], y[j][e], t1[j][e]);
-                    g[j][e] = dh[j][e] * gate[e] * w[e];
-                    mq += g[j][e];
-                    mqy = fmaf(g[j][e], y[j][e], mqy);
-                }
-            }
-            if (a.dx) out.store_stream(static_cast<T *>(a.dx) + r * a.lddx + at(j));
-        }
-        if (!a.dy) continue;
-        if (a.post != CONVROT_NORM_NONE) {
-            sum(mq, mqy);
-            mq = a.post == CONVROT_NORM_LAYER ? mq / d : 0.0f;
-            mqy /= d;
-        } else {
-            mq = mqy = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            if (!inside(j)) continue;
-            Raw<T, kVec> out;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) out.set(e, inv_y * (g[j][e] - mq - y[j][e] * mqy));
-            out.store_stream(static_cast<T *>(a.dy) + r * a.lddy + at(j));
+        for (int s = 0; s < kStages - 1; ++s) {
+            if (s < count) fetch(s);
+            copy_commit();
         }
     }
-    float *to = part + unit * 4 * a.d;
-#pragma unroll
-    for (int j = 0; j < kNv; ++j) {
-        if (!inside(j)) continue;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            to[at(j) + e] = s0[j][e];
-            to[a.d + at(j) + e] = s1[j][e];
-            to[2 * a.d + at(j) + e] = t0[j][e];
-            to[3 * a.d + at(j) + e] = t1[j][e];
+    for (int r = 0; r < count; ++r) {
+        if constexpr (kRing) {
+            if (r + kStages - 1 < count) fetch(ahead);
+            copy_commit();
+            if (++ahead == kStages) ahead = 0;
+            copy_wait<kStages - 1>();
         }
+        F2 h[kPairs], y[kPairs], g[kPairs], v[kPairs];
+        get(0, h);
+        get(1, y);
+        // h^ and y^
+        if (a.pre == CONVROT_NORM_LAYER || y_layer) {
+            F2 hs(0.0f), ys(0.0f);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                hs = hs + h[e];
+                ys = ys + y[e];
+            }
+            float hm = hs.sum(), ym = ys.sum();
+            sum(hm, ym);
+            hm = a.pre == CONVROT_NORM_LAYER ? -hm * inv_d : 0.0f;
+            ym = y_layer ? -ym * inv_d : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                const bool lo = inside(2 * e / kVec), hi = inside((2 * e + 1) / kVec);
+                h[e] = h[e] + F2(lo ? hm : 0.0f, hi ? hm : 0.0f);
+                y[e] = y[e] + F2(lo ? ym : 0.0f, hi ? ym : 0.0f);
+            }
+        }
+        float inv = 1.0f, inv_y = 1.0f;
+        if (a.pre != CONVROT_NORM_NONE || (a.y && a.post != CONVROT_NORM_NONE)) {
+            F2 hs(0.0f), ys(0.0f);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                hs = fma2(h[e], h[e], hs);
+                ys = fma2(y[e], y[e], ys);
+            }
+            float hv = hs.sum(), yv = ys.sum();
+            sum(hv, yv);
+            if (a.pre != CONVROT_NORM_NONE) inv = rsqrtf(fmaf(hv, inv_d, a.eps));
+            if (a.post != CONVROT_NORM_NONE) inv_y = rsqrtf(fmaf(yv, inv_d, a.eps));
+        }
+        // dH and the means that pre's gradient subtracts
+        get(3, v);
+        F2 ms(0.0f), mhs(0.0f);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            h[e] = h[e] * F2(inv);
+            y[e] = y[e] * F2(inv_y);
+            s0[e] = s0[e] + v[e];
+            s1[e] = fma2(v[e], h[e], s1[e]);
+            g[e] = v[e] * w_pre[e];
+            ms = ms + g[e];
+            mhs = fma2(g[e], h[e], mhs);
+        }
+        float mg = 0.0f, mgh = 0.0f;
+        if (a.pre != CONVROT_NORM_NONE) {
+            mg = ms.sum();
+            mgh = mhs.sum();
+            sum(mg, mgh);
+            mg = a.pre == CONVROT_NORM_LAYER ? -mg * inv_d : 0.0f;
+            mgh *= -inv_d;
+        }
+        get(2, v);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            v[e] = fma2(F2(inv), fma2(h[e], F2(mgh), g[e] + F2(mg)), v[e]);
+            g[e] = v[e] * F2(a.res_scale);
+        }
+        if (dx) {
+            put(dx, g);
+            dx += a.lddx;
+        }
+        if (a.y) {
+            F2 ms(0.0f), mys(0.0f);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                t0[e] = t0[e] + v[e];
+                t1[e] = fma2(v[e], y[e], t1[e]);
+                g[e] = v[e] * w_post[e];
+                ms = ms + g[e];
+                mys = fma2(g[e], y[e], mys);
+            }
+            if (dy) {
+                float mq = 0.0f, mqy = 0.0f;
+                if (a.post != CONVROT_NORM_NONE) {
+                    mq = ms.sum();
+                    mqy = mys.sum();
+                    sum(mq, mqy);
+                    mq = a.post == CONVROT_NORM_LAYER ? -mq * inv_d : 0.0f;
+                    mqy *= -inv_d;
+                }
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) g[e] = F2(inv_y) * fma2(y[e], F2(mqy), g[e] + F2(mq));
+                put(dy, g);
+                dy += a.lddy;
+            }
+        }
+        if constexpr (kRing) {
+            if (++stage == kStages) stage = 0;
+        } else {
+            advance();
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    float *to = part + unit * 4 * a.d;
+    auto put_sums = [&](float *p, const F2 (&v)[kPairs]) {
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) {
+            if (!inside(j)) continue;
+            if constexpr (kRing) {
+                Raw<float, kVec> raw;
+                raw.pack(v + j * kVec / 2);
+                raw.store(p + at(j));
+            } else {
+                p[at(j)] = j % 2 ? v[j / 2].hi() : v[j / 2].lo();
+            }
+        }
+    };
+    put_sums(to, s0);
+    put_sums(to + a.d, s1);
+    if (a.y) {
+        put_sums(to + 2 * a.d, t0);
+        put_sums(to + 3 * a.d, t1);
     }
     if constexpr (kCluster > 1) cluster_barrier();  // no block leaves while a peer may still write into it
 }
+
+constexpr int kSumWarps = 8;
 
 // Adds up one sample's partials (block (x, y): 32 columns of sample y; warps
 // take chunks in turn) and writes that sample's gradients. What the sample adds
@@ -541,9 +823,10 @@ template <typename P>
 __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, int64_t chunks,
                                         const float *part, float *weights)
 {
-    __shared__ float4 sums[32][33];
+    __shared__ float4 sums[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t i = blockIdx.x * 32ll + lane, b = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are another kernel's
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < a.d)
 #pragma unroll 4
@@ -551,8 +834,10 @@ __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_no
             const float *p = part + (b * chunks + c) * 4 * a.d + i;
             v.x += p[0];
             v.y += p[a.d];
-            v.z += p[2 * a.d];
-            v.w += p[3 * a.d];
+            if (a.y) {
+                v.z += p[2 * a.d];
+                v.w += p[3 * a.d];
+            }
         }
     sums[warp][lane] = v;
     __syncthreads();
@@ -567,6 +852,7 @@ __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_no
     if (a.dshift) a.dshift[b * a.d + i] = v.x;
     if (a.dscale) a.dscale[b * a.d + i] = param<P>(a.pre_weight, i, 1.0f) * v.y + param<P>(a.pre_bias, i, 0.0f) * v.x;
     if (a.dgate) a.dgate[b * a.d + i] = param<P>(a.post_weight, i, 1.0f) * v.w + param<P>(a.post_bias, i, 0.0f) * v.z;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const float up = 1.0f + param<P>(a.scale, b * a.ldscale + i, 0.0f), gate = param<P>(a.gate, b * a.ldgate + i, 1.0f);
     const float out[4] = {up * v.y, up * v.x, gate * v.w, gate * v.z};
     float *const to[4] = {a.dpre_weight, a.dpre_bias, a.dpost_weight, a.dpost_bias};
@@ -583,7 +869,7 @@ __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_no
 __global__ void norm_grad_weights_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, int64_t batches,
                                          const float *weights)
 {
-    __shared__ float sums[32][33];
+    __shared__ float sums[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, k = blockIdx.y;
     const int64_t i = blockIdx.x * 32ll + lane;
     float *const all[4] = {a.dpre_weight, a.dpre_bias, a.dpost_weight, a.dpost_bias};
@@ -591,6 +877,7 @@ __global__ void norm_grad_weights_kernel(const __grid_constant__ convrot_gated_n
 #pragma unroll
     for (int j = 1; j < 4; ++j)
         if (j == k) to = all[j];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!to) return;
     float v = 0.0f;
     if (i < a.d)
@@ -631,6 +918,32 @@ cudaError_t launch_block_rows(const convrot_gated_norm_args &a, cudaStream_t str
     return cudaGetLastError();
 }
 
+constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; the rest stays L1 for the vectors
+
+// Runs of rows through the ring, if there are enough of them (eight a block, so
+// that filling the ring is a small part) and the ring fits.
+template <typename T, typename P, int kNv>
+bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
+{
+    constexpr int kVec = 16 / sizeof(T), kStages = 4;
+    const int threads = static_cast<int>((a.d / kVec + kNv - 1) / kNv + 31) / 32 * 32;
+    const int bytes = kStages * (a.y ? 2 : 1) * kNv * threads * 16;
+    int per_sm = kRingBytes / bytes;
+    const int by_threads = 1024 / threads;
+    if (per_sm > by_threads) per_sm = by_threads;
+    if (per_sm > 16) per_sm = 16;
+    if (per_sm < 1 || threads > kRowThreads) return false;
+    const int64_t blocks = static_cast<int64_t>(per_sm) * kSms;
+    if (a.m < 8 * blocks) return false;
+    auto kernel = gated_norm_ring_kernel<T, P, kNv, kStages>;
+    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (*e != cudaSuccess) return true;
+    const int64_t rows = (a.m + blocks - 1) / blocks;
+    kernel<<<static_cast<unsigned>((a.m + rows - 1) / rows), threads, bytes, stream>>>(a, static_cast<int32_t>(rows));
+    *e = cudaGetLastError();
+    return true;
+}
+
 // A warp for each row, four rows a block.
 template <typename T, typename P, int kVec, int kNv>
 cudaError_t launch_warp_rows(const convrot_gated_norm_args &a, cudaStream_t stream)
@@ -656,6 +969,8 @@ cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t str
                           vectors(a.pre_bias, 1, a.d, kVec, kP);
         if (wide) {
             const int64_t n = a.d / kVec;
+            cudaError_t e;
+            if (n > 256 ? launch_ring<T, P, 16 / kVec>(a, stream, &e) : launch_ring<T, P, 1>(a, stream, &e)) return e;
             if (n <= 32) return launch_warp_rows<T, P, kVec, 1>(a, stream);
             if (n <= kRowThreads) return launch_block_rows<T, P, kVec, 1>(a, stream);
             if (n <= 2 * kRowThreads) return launch_block_rows<T, P, kVec, 2>(a, stream);
@@ -674,19 +989,41 @@ int64_t gated_norm_backward_work_bytes(int64_t m, int64_t d, int64_t rows_per_ba
     return (s.units() + (s.batches > 1 ? s.batches : 0)) * 4 * d * static_cast<int64_t>(sizeof(float));
 }
 
+// A launch with a cluster size, or (dependent) one that may start while the
+// kernel before it drains: its griddepcontrol.wait holds it until that is done.
+template <typename... A>
+cudaError_t launch_with(void (*kernel)(A...), dim3 grid, unsigned threads, size_t bytes, cudaStream_t stream,
+                        unsigned cluster, bool dependent, A... args)
+{
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    cudaLaunchAttribute attrs[2]{};
+    if (cluster > 1) {
+        attrs[config.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attrs[config.numAttrs++].val.clusterDim = {cluster, 1, 1};
+    }
+    if (dependent) {
+        attrs[config.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[config.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    config.attrs = attrs;
+    return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 template <typename T, typename P, int kVec, int kCluster>
 cudaError_t launch_grad(const convrot_gated_norm_backward_args &a, const GradSplit &s, float *part, cudaStream_t stream)
 {
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>(s.units() * kCluster));
-    config.blockDim = dim3(s.threads);
-    config.stream = stream;
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim = {kCluster, 1, 1};
-    config.attrs = &cluster;
-    config.numAttrs = kCluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&config, norm_grad_kernel<T, P, kVec, kCluster>, a, s, part);
+    const int bytes = kVec == 1 ? 0 : grad_stages<T>() * 4 * (kGradCols / kVec) * s.threads * 16;
+    auto kernel = norm_grad_kernel<T, P, kVec, kCluster>;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_with(kernel, dim3(static_cast<unsigned>(s.units() * kCluster)), static_cast<unsigned>(s.threads), bytes,
+                       stream, kCluster, false, a, s, part);
 }
 
 cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a, cudaStream_t stream)
@@ -713,7 +1050,7 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
         const bool per_weight = a.dpre_weight || a.dpre_bias || a.dpost_weight || a.dpost_bias;
         if (!per_weight && !a.dshift && !a.dscale && !a.dgate) return cudaSuccess;
         const unsigned tiles = static_cast<unsigned>((a.d + 31) / 32);
-        const unsigned warps = static_cast<unsigned>(s.chunks < 32 ? s.chunks : 32);
+        const unsigned warps = static_cast<unsigned>(s.chunks < kSumWarps ? s.chunks : kSumWarps);
         for (int64_t b0 = 0; b0 < s.batches; b0 += 65535) {  // (the grid's second dimension has 16 bits)
             convrot_gated_norm_backward_args g = a;
             const int64_t n = s.batches - b0 < 65535 ? s.batches - b0 : 65535;
@@ -725,13 +1062,16 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
                 if (g.scale) g.scale = static_cast<const P *>(a.scale) + b0 * a.ldscale;
                 if (g.gate) g.gate = static_cast<const P *>(a.gate) + b0 * a.ldgate;
             }
-            norm_grad_sample_kernel<P><<<dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream>>>(
-                g, s.chunks, part + b0 * s.chunks * 4 * a.d, s.batches > 1 ? weights + b0 * 4 * a.d : nullptr);
+            e = launch_with(norm_grad_sample_kernel<P>, dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream, 1,
+                            b0 == 0, g, s.chunks, static_cast<const float *>(part + b0 * s.chunks * 4 * a.d),
+                            s.batches > 1 ? weights + b0 * 4 * a.d : nullptr);
+            if (e != cudaSuccess) return e;
         }
         if (per_weight && s.batches > 1)
-            norm_grad_weights_kernel<<<dim3(tiles, 4), static_cast<unsigned>(s.batches < 32 ? s.batches : 32) * 32, 0,
-                                       stream>>>(a, s.batches, weights);
-        return cudaGetLastError();
+            return launch_with(norm_grad_weights_kernel, dim3(tiles, 4),
+                               static_cast<unsigned>(s.batches < kSumWarps ? s.batches : kSumWarps) * 32, 0, stream, 1, true, a,
+                               s.batches, static_cast<const float *>(weights));
+        return cudaSuccess;
     });
 }
 

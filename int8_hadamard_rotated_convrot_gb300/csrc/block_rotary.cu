@@ -77,10 +77,9 @@ __global__ void __launch_bounds__(512) rotary_kernel(const __grid_constant__ con
                     Raw<float, (kPairs % 4 ? 4 : kPairs)> cr, sr;
                     cr.load(cp);
                     sr.load(sp);
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) {
-                        c[e] = cr.get(e);
-                        n[e] = sr.get(e);
+                    if constexpr (kPairs % 4 == 0) {
+                        cr.unpack(c);
+                        sr.unpack(n);
                     }
                 } else {
 #pragma unroll
@@ -108,20 +107,19 @@ __global__ void __launch_bounds__(512) rotary_kernel(const __grid_constant__ con
                 v0[j].store(p + e0);
                 continue;
             }
+            float x[kVec], y[kVec];
+            v0[j].unpack(x);
+            if (kSplit) v1[j].unpack(y);
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
-                const float x = kSplit ? v0[j].get(e) : v0[j].get(2 * e);
-                const float y = kSplit ? v1[j].get(e) : v0[j].get(2 * e + 1);
+                float &pa = kSplit ? x[e] : x[2 * e], &pb = kSplit ? y[e] : x[2 * e + 1];
+                const float va = pa, vb = pb;
                 // (which product is rounded on its own is fixed, so that every form gives the same bits)
-                const float xr = fmaf(x, c[e], -__fmul_rn(y, n[e])), yr = fmaf(y, c[e], __fmul_rn(x, n[e]));
-                if (kSplit) {
-                    v0[j].set(e, xr);
-                    v1[j].set(e, yr);
-                } else {
-                    v0[j].set(2 * e, xr);
-                    v0[j].set(2 * e + 1, yr);
-                }
+                pa = fmaf(va, c[e], -__fmul_rn(vb, n[e]));
+                pb = fmaf(vb, c[e], __fmul_rn(va, n[e]));
             }
+            v0[j].pack(x);
+            if (kSplit) v1[j].pack(y);
             v0[j].store(p + e0);
             if (kSplit) v1[j].store(p + e1);
         }

@@ -292,7 +292,7 @@ def norm_bounds(v, how):
 NORMS = [
     (1, 1, 1), (3, 2, 1), (2, 7, 2), (5, 64, 2), (4, 127, 4), (9, 128, 3), (7, 130, 5), (33, 1024, 10), (6, 1155, 6),
     (5, 2048, 5), (3, 4096, 1), (4, 5120, 3), (3, 8191, 2), (2, 8192, 2), (2, 12296, 1), (3, 16384, 2), (2, 16383, 2),
-    (1030, 256, 500), (700, 1536, 233)]
+    (1030, 256, 500), (700, 1536, 233), (19500, 256, 7000), (6200, 1536, 6200), (2500, 4104, 999)]
 
 
 @pytest.mark.parametrize("dtype,pdtype", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)],
