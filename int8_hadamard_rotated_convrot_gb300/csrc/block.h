@@ -190,10 +190,11 @@ struct Raw {
     }
 };
 
-// 16 bytes from global to shared memory without a register between.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+// 16 bytes from global to shared memory without a register between; with
+// bytes = 0 nothing is read and the 16 bytes become zero.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All of this thread's groups but the last kPending have landed.

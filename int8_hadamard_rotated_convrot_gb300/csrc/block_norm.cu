@@ -149,6 +149,7 @@ __device__ __forceinline__ void pack_row(const convrot_gated_norm_args &a, int64
 __device__ __forceinline__ uint32_t sample_rows(int64_t rows) { return rows < 0x7fffffff ? static_cast<uint32_t>(rows) : 0x7fffffffu; }
 
 constexpr int kSms = 152;
+constexpr int kRingThreads = 640;  // 96 registers a thread, so that 640 threads share an SM
 constexpr int kRowThreads = 512;  // 128 registers a thread: up to 32 values of a row in each
 
 template <typename T, typename P, int kVec, int kNv, bool kWarp>
@@ -297,181 +298,182 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
 
 // The same for many rows: each block takes a run of them, and each thread
 // copies its own 16-byte pieces of the next rows into its own places in shared
-// memory (cp.async), kStages rows ahead. What a thread copied it reads back
-// itself, so the ring needs no barrier; HBM stays busy through the sums around
-// the block. Row pointers and the sample's vectors are stepped, not computed.
-template <typename T, typename P, int kNv, int kStages>
-__global__ void __launch_bounds__(kRowThreads) gated_norm_ring_kernel(const __grid_constant__ convrot_gated_norm_args a, int32_t rows)
+// memory (cp.async), kStages - 1 rows ahead. What a thread copied it reads back
+// itself, so the ring needs no barrier, and HBM stays busy through the sums
+// around the block. Per row the instructions count as much as the bytes (44 a
+// value are what HBM's rate leaves), so everything that a sample's rows share
+// is prepared once, in registers: gate w_post, (1 + scale) w_pre and (1 +
+// scale) b_pre + shift; pieces past the row are zeros and need no branch.
+template <typename T, typename P, int kNv, int kStages, bool kBranch>
+__global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const __grid_constant__ convrot_gated_norm_args a, int32_t rows)
 {
-    constexpr int kVec = 16 / sizeof(T), kPairs = kVec / 2;
+    constexpr int kVec = 16 / sizeof(T), kPieces = kNv * (kBranch ? 2 : 1), kPairs = kNv * kVec / 2, kHalf = kVec / 2;
     extern __shared__ uint4 ring[];  // [kStages][x, y][kNv][blockDim]
     __shared__ float2 slots[64];
     const int nt = blockDim.x, d = static_cast<int>(a.d);
     const float inv_d = 1.0f / d;
     RowSum<false> sum{slots};
     const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
-    const uint32_t step = nt * 16, stage_bytes = step * kNv * (a.y ? 2 : 1);
+    const uint32_t step = nt * 16, stage_bytes = step * kPieces;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
     const int count = static_cast<int>(a.m - first < rows ? a.m - first : rows);
-    auto at = [&](int j) { return (static_cast<int>(threadIdx.x) + j * nt) * kVec; };
-    auto in_row = [&](int j) { return at(j) < d; };
-
-    const T *x = static_cast<const T *>(a.x) + first * a.ldx + at(0), *y = static_cast<const T *>(a.y) + first * a.ldy + at(0);
-    T *h_out = a.h ? static_cast<T *>(a.h) + first * a.ldh + at(0) : nullptr;
-    T *n_out = a.n ? static_cast<T *>(a.n) + first * a.ldn + at(0) : nullptr;
-    auto fetch = [&](int stage) {
-        uint32_t to = mine + stage * stage_bytes;
+    const int pitch = nt * kVec, col = static_cast<int>(threadIdx.x) * kVec;  // piece j: columns col + j pitch on
+    bool inside[kNv];
+    uint32_t bytes[kNv];
 #pragma unroll
-        for (int j = 0; j < kNv; ++j)
-            if (in_row(j)) {
-                copy16(to + j * step, x + j * nt * kVec);
-                if (a.y) copy16(to + (kNv + j) * step, y + j * nt * kVec);
-            }
+    for (int j = 0; j < kNv; ++j) {
+        inside[j] = col + j * pitch < d;
+        bytes[j] = inside[j] ? 16 : 0;
+    }
+    // (a piece past the row reads nothing, but its address stays inside)
+    const T *x = static_cast<const T *>(a.x) + first * a.ldx, *y = static_cast<const T *>(a.y) + first * a.ldy;
+    T *h_out = static_cast<T *>(a.h) + first * a.ldh + col, *n_out = static_cast<T *>(a.n) + first * a.ldn + col;
+    auto fetch = [&](uint32_t to) {
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) {
+            copy16(to + j * step, x + (inside[j] ? col + j * pitch : 0), bytes[j]);
+            if constexpr (kBranch) copy16(to + (kNv + j) * step, y + (inside[j] ? col + j * pitch : 0), bytes[j]);
+        }
         x += a.ldx;
-        y += a.ldy;
+        if constexpr (kBranch) y += a.ldy;
     };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
-        if (s < count) fetch(s);
+        if (s < count) fetch(mine + s * stage_bytes);
         copy_commit();
     }
     uint32_t sample = static_cast<uint32_t>(first) / sample_rows(a.rows_per_batch);
     int64_t left = (sample + 1ll) * a.rows_per_batch - first;  // rows of this sample
-    int stage = 0, ahead = kStages - 1;
-    for (int r = 0; r < count; ++r) {
-        if (r + kStages - 1 < count) fetch(ahead);
-        copy_commit();
-        if (++ahead == kStages) ahead = 0;
-        copy_wait<kStages - 1>();
-        const uint32_t from = mine + stage * stage_bytes;
-        if (++stage == kStages) stage = 0;
-
-        F2 h[kNv][kPairs];
-        auto normalize = [&](int kind) {
-            if (kind == CONVROT_NORM_NONE) return;
-            if (kind == CONVROT_NORM_LAYER) {
-                F2 s(0.0f);
-#pragma unroll
-                for (int j = 0; j < kNv; ++j)
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) s = s + h[j][e];
-                const F2 mean(-sum(s.sum()) * inv_d);
-#pragma unroll
-                for (int j = 0; j < kNv; ++j)
-                    if (in_row(j))
-#pragma unroll
-                        for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + mean;
-            }
-            F2 s(0.0f);
-#pragma unroll
-            for (int j = 0; j < kNv; ++j)
-#pragma unroll
-                for (int e = 0; e < kPairs; ++e) s = fma2(h[j][e], h[j][e], s);
-            const F2 inv(rsqrtf(fmaf(sum(s.sum()), inv_d, a.eps)));
-#pragma unroll
-            for (int j = 0; j < kNv; ++j)
-#pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * inv;
-        };
-        // v * p, v + p and v + v p with the vector p of this thread's columns
-        auto vec = [&](const void *p, int64_t offset, int j, F2 (&v)[kPairs]) {
-            Raw<P, kVec> raw;
-            raw.load(static_cast<const P *>(p) + offset + at(j));
-            raw.unpack(v);
-        };
-        if (a.y) {
-#pragma unroll
-            for (int j = 0; j < kNv; ++j) {
-                Raw<T, kVec> raw{};
-                if (in_row(j)) raw.bits[0] = shared16(from + (kNv + j) * step);
-                raw.unpack(h[j]);
-            }
-            normalize(a.post);
-        }
-#pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            if (!in_row(j)) {
-#pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = F2(0.0f);
-                continue;
-            }
-            Raw<T, kVec> raw;
-            F2 xv[kPairs], p[kPairs];
-            raw.bits[0] = shared16(from + j * step);
-            raw.unpack(xv);
-            const F2 res(a.res_scale);
-            if (a.y) {
-                if (a.post_weight) {
-                    vec(a.post_weight, 0, j, p);
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
-                }
-                if (a.post_bias) {
-                    vec(a.post_bias, 0, j, p);
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
-                }
-                if (a.gate) {
-                    vec(a.gate, sample * a.ldgate, j, p);
-#pragma unroll
-                    for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
-                }
-#pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = fma2(res, xv[e], h[j][e]);
+    F2 w_post[kPairs], w_pre[kPairs], b_pre[kPairs];
+    auto prepare = [&]() {
+        auto vec = [&](const void *p, int64_t offset, float otherwise, float (&v)[kVec], int j) {
+            if (inside[j]) {
+                params<P>(p, offset + col + j * pitch, otherwise, v);
             } else {
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = res * xv[e];
+                for (int e = 0; e < kVec; ++e) v[e] = 0.0f;
             }
-            if (h_out) {
-                raw.pack(h[j]);
-                raw.store(h_out + j * nt * kVec);
-            }
-        }
-        if (h_out) h_out += a.ldh;
-        normalize(a.pre);
+        };
 #pragma unroll
         for (int j = 0; j < kNv; ++j) {
-            if (!in_row(j)) continue;
-            F2 p[kPairs];
-            if (a.pre_weight) {
-                vec(a.pre_weight, 0, j, p);
+            float u[kVec], v[kVec], w[kVec];
+            vec(a.gate, sample * a.ldgate, 1.0f, u, j);
+            vec(a.post_weight, 0, 1.0f, v, j);
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] * p[e];
-            }
-            if (a.pre_bias) {
-                vec(a.pre_bias, 0, j, p);
+            for (int e = 0; e < kHalf; ++e) w_post[j * kHalf + e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
+            vec(a.scale, sample * a.ldscale, 0.0f, u, j);
+            vec(a.pre_weight, 0, 1.0f, v, j);
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
-            }
-            if (a.scale) {
-                vec(a.scale, sample * a.ldscale, j, p);
+            for (int e = 0; e < kVec; ++e) u[e] += 1.0f;
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = fma2(h[j][e], p[e], h[j][e]);
-            }
-            if (a.shift) {
-                vec(a.shift, sample * a.ldshift, j, p);
+            for (int e = 0; e < kHalf; ++e) w_pre[j * kHalf + e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
+            vec(a.pre_bias, 0, 0.0f, v, j);
+            vec(a.shift, sample * a.ldshift, 0.0f, w, j);
 #pragma unroll
-                for (int e = 0; e < kPairs; ++e) h[j][e] = h[j][e] + p[e];
-            }
-            if (n_out) {
-                Raw<T, kVec> raw;
-                raw.pack(h[j]);
-                raw.store(n_out + j * nt * kVec);
+            for (int e = 0; e < kHalf; ++e)
+                b_pre[j * kHalf + e] = F2(fmaf(u[2 * e], v[2 * e], w[2 * e]), fmaf(u[2 * e + 1], v[2 * e + 1], w[2 * e + 1]));
+        }
+    };
+    F2 h[kPairs];
+    // mean out of h (layer norm), then 1 / deviation
+    auto deviation = [&](int kind) {
+        if (kind == CONVROT_NORM_LAYER) {
+            F2 s = h[0];
+#pragma unroll
+            for (int e = 1; e < kPairs; ++e) s = s + h[e];
+            const float mean = -sum(s.sum()) * inv_d;
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) {
+                const F2 m(inside[j] ? mean : 0.0f);
+#pragma unroll
+                for (int e = 0; e < kHalf; ++e) h[j * kHalf + e] = h[j * kHalf + e] + m;
             }
         }
-        if (n_out) n_out += a.ldn;
+        F2 s = h[0] * h[0];
+#pragma unroll
+        for (int e = 1; e < kPairs; ++e) s = fma2(h[e], h[e], s);
+        return rsqrtf(fmaf(sum(s.sum()), inv_d, a.eps));
+    };
+    uint32_t stage = mine, ahead = mine + (kStages - 1) * stage_bytes;
+    const uint32_t ring_end = mine + kStages * stage_bytes;
+    bool fresh = true;
+    for (int r = 0; r < count; ++r) {
+        if (fresh) prepare();
+        if (r + kStages - 1 < count) fetch(ahead);
+        copy_commit();
+        if ((ahead += stage_bytes) == ring_end) ahead = mine;
+        copy_wait<kStages - 1>();
+        auto piece = [&](int k, F2 *v) {
+            Raw<T, kVec> raw;
+            raw.bits[0] = shared16(stage + k * step);
+            raw.unpack(v);
+        };
+        if constexpr (kBranch) {
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) piece(kNv + j, h + j * kHalf);
+            if (a.post != CONVROT_NORM_NONE) {
+                const F2 inv(deviation(a.post));
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) h[e] = h[e] * inv;
+            }
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) h[e] = h[e] * w_post[e];
+            if (a.post_bias) {
+#pragma unroll
+                for (int j = 0; j < kNv; ++j) {
+                    if (!inside[j]) continue;
+                    float u[kVec], v[kVec];
+                    params<P>(a.gate, sample * a.ldgate + col + j * pitch, 1.0f, u);
+                    params<P>(a.post_bias, col + j * pitch, 0.0f, v);
+#pragma unroll
+                    for (int e = 0; e < kHalf; ++e)
+                        h[j * kHalf + e] = fma2(F2(u[2 * e], u[2 * e + 1]), F2(v[2 * e], v[2 * e + 1]), h[j * kHalf + e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) {
+            F2 xv[kHalf];
+            piece(j, xv);
+            const F2 res(a.res_scale);
+#pragma unroll
+            for (int e = 0; e < kHalf; ++e) h[j * kHalf + e] = kBranch ? fma2(res, xv[e], h[j * kHalf + e]) : res * xv[e];
+        }
+        auto put = [&](T *p) {
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) {
+                Raw<T, kVec> raw;
+                raw.pack(h + j * kHalf);
+                if (inside[j]) raw.store(p + j * pitch);
+            }
+        };
+        if (a.h) {
+            put(h_out);
+            h_out += a.ldh;
+        }
+        if (a.pre != CONVROT_NORM_NONE) {
+            const F2 inv(deviation(a.pre));
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) h[e] = h[e] * inv;
+        }
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) h[e] = fma2(h[e], w_pre[e], b_pre[e]);
+        if (a.n) {
+            put(n_out);
+            n_out += a.ldn;
+        }
         if (a.q) {
             float v[kNv][kVec];
 #pragma unroll
-            for (int j = 0; j < kNv; ++j)
-#pragma unroll
-                for (int e = 0; e < kPairs; ++e) {
-                    v[j][2 * e] = h[j][e].lo();
-                    v[j][2 * e + 1] = h[j][e].hi();
-                }
+            for (int e = 0; e < kPairs; ++e) {
+                v[e / kHalf][e % kHalf * 2] = h[e].lo();
+                v[e / kHalf][e % kHalf * 2 + 1] = h[e].hi();
+            }
             pack_row<kVec, kNv>(a, first + r, d, threadIdx.x, nt, v);
         }
-        if (--left == 0) {
+        if ((stage += stage_bytes) == ring_end) stage = mine;
+        fresh = --left == 0;
+        if (fresh) {
             ++sample;
             left = a.rows_per_batch;
         }
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             if (in[k])
 #pragma unroll
                 for (int j = 0; j < kNv; ++j)
-                    if (inside(j)) copy16(mine + ((stage * 4 + k) * kNv + j) * piece, in[k] + j * nt * kVec);
+                    copy16(mine + ((stage * 4 + k) * kNv + j) * piece, in[k] + (inside(j) ? j * nt * kVec : -at(0)), inside(j) ? 16 : 0);
         advance();
     };
     int stage = 0, ahead = kStages - 1;
@@ -629,7 +631,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int j = 0; j < kNv; ++j) {
                 Raw<T, kVec> raw{};
-                if (in[k] && inside(j)) raw.bits[0] = shared16(mine + ((stage * 4 + k) * kNv + j) * piece);
+                if (in[k]) raw.bits[0] = shared16(mine + ((stage * 4 + k) * kNv + j) * piece);
                 raw.unpack(v + j * kVec / 2);
             }
         } else {
@@ -922,26 +924,31 @@ constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; 
 
 // Runs of rows through the ring, if there are enough of them (eight a block, so
 // that filling the ring is a small part) and the ring fits.
-template <typename T, typename P, int kNv>
+template <typename T, typename P, int kNv, bool kBranch>
 bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
 {
     constexpr int kVec = 16 / sizeof(T), kStages = 4;
     const int threads = static_cast<int>((a.d / kVec + kNv - 1) / kNv + 31) / 32 * 32;
-    const int bytes = kStages * (a.y ? 2 : 1) * kNv * threads * 16;
+    const int bytes = kStages * (kBranch ? 2 : 1) * kNv * threads * 16;
     int per_sm = kRingBytes / bytes;
-    const int by_threads = 1024 / threads;
+    const int by_threads = kRingThreads / threads;
     if (per_sm > by_threads) per_sm = by_threads;
-    if (per_sm > 16) per_sm = 16;
-    if (per_sm < 1 || threads > kRowThreads) return false;
+    if (per_sm < 1) return false;
     const int64_t blocks = static_cast<int64_t>(per_sm) * kSms;
     if (a.m < 8 * blocks) return false;
-    auto kernel = gated_norm_ring_kernel<T, P, kNv, kStages>;
+    auto kernel = gated_norm_ring_kernel<T, P, kNv, kStages, kBranch>;
     *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (*e != cudaSuccess) return true;
     const int64_t rows = (a.m + blocks - 1) / blocks;
     kernel<<<static_cast<unsigned>((a.m + rows - 1) / rows), threads, bytes, stream>>>(a, static_cast<int32_t>(rows));
     *e = cudaGetLastError();
     return true;
+}
+
+template <typename T, typename P, int kNv>
+bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
+{
+    return a.y ? launch_ring<T, P, kNv, true>(a, stream, e) : launch_ring<T, P, kNv, false>(a, stream, e);
 }
 
 // A warp for each row, four rows a block.
