@@ -497,9 +497,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 // eight columns of every row, so the four sums of its columns stay in its
 // registers; they leave once per unit as a partial, and small kernels add the
 // partials up in a fixed order. Four reads and two writes of a value, each
-// tensor moved once. The next row's values are loaded before this one's three
-// or four sums around the block, which would otherwise leave HBM idle (16-bit
-// types; 32-bit rows are twice as long and have no registers to spare).
+// tensor moved once.
+//
+// Registers for the four sums of a whole row allow one block an SM, so nothing
+// hides a trip around the block: the sums of a row are gathered in as few of
+// them as possible. g does not depend on pre's statistics, so mean(g h^) is inv
+// sum(g h) / d in the same trip as sum h^2; and dH is linear in them, so with
+// W = gate w_post, for an RMS post norm
+//   sum gy y = inv sum g W y - inv mean(g) sum W y - inv^2 mean(g h^) sum h W y + sum dh W y
+// goes along too. One trip for RMS norms, one more for the means of a layer
+// norm, and one more if post is one.
 
 constexpr int kGradCols = 8;           // columns a thread
 constexpr int kGradThreads = 640;      // of one block: 96 registers a thread
@@ -540,32 +547,61 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Sums over the blocks of a cluster that share a row: each block's sum goes to
-// a slot in every peer's shared memory (two sets in turn, as in RowSum).
+// Eight sums at once over the threads that share a row: within a warp each of
+// three steps halves the values that a lane carries, a block's warps meet in
+// shared memory (two buffers in turn, as in RowSum), and a cluster's blocks
+// write theirs into every peer's.
 template <int kCluster>
 struct GradSum {
-    RowSum<false> block;
-    float2 *peers;  // [2][kCluster]
+    float *slots;  // [2][8][36]: value, warp (36 keeps the 32 lanes' reads apart)
+    float *peers;  // [2][kCluster][8]
     int turn = 0;
-    __device__ __forceinline__ void operator()(float &a, float &b)
+    __device__ __forceinline__ void operator()(float (&v)[8])
     {
-        block(a, b);
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n], o);
+        }
+        float s = v[0];
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        const int which = lane >> 2, part = lane & 3;  // the value that this lane ended up with
+        if (blockDim.x > 32) {
+            float *to = slots + (turn * 8 + which) * 36;
+            if (part == 0) to[threadIdx.x >> 5] = s;
+            __syncthreads();
+            const int warps = blockDim.x >> 5;
+            s = 0.0f;
+            for (int w = part; w < warps; w += 4) s += to[w];
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+        }
         if constexpr (kCluster > 1) {
-            float2 *mine = peers + turn * kCluster;
-            turn ^= 1;
-            if (threadIdx.x < kCluster) {
-                uint32_t to, at = static_cast<uint32_t>(__cvta_generic_to_shared(mine + cluster_rank()));
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(threadIdx.x));
-                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(a), "f"(b) : "memory");
+            float *mine = peers + turn * kCluster * 8;
+            if (threadIdx.x < 32) {  // a value's four lanes write it to up to four blocks
+                const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine + cluster_rank() * 8 + which));
+                uint32_t to;
+                if (part < kCluster) {
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(at), "r"(part));
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(s) : "memory");
+                }
             }
             cluster_barrier();
-            a = b = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kCluster; ++i) {
-                a += mine[i].x;
-                b += mine[i].y;
+            for (int i = 0; i < 8; ++i) {
+                v[i] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kCluster; ++c) v[i] += mine[c * 8 + i];
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
         }
+        turn ^= 1;
     }
 };
 
@@ -586,9 +622,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     constexpr int kNv = kGradCols / kVec, kPairs = kGradCols / 2, kStages = grad_stages<T>();
     constexpr bool kRing = kVec > 1;
     extern __shared__ uint4 ring[];  // [kStages][h, y, dh, dn][kNv][blockDim]
-    __shared__ float2 slots[64];
-    __shared__ float2 peers[2 * kCluster];
-    GradSum<kCluster> sum{{slots}, peers};
+    __shared__ float slots[2 * 8 * 36];
+    __shared__ float peers[2 * kCluster * 8];
+    GradSum<kCluster> sum{slots, peers};
     const int64_t unit = blockIdx.x / kCluster;
     const int64_t b = unit / split.chunks, chunk = unit - b * split.chunks;
     const int64_t first = b * a.rows_per_batch + chunk * split.rows_per_chunk;
@@ -679,6 +715,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     T *dx = a.dx ? static_cast<T *>(a.dx) + first * a.lddx + at(0) : nullptr;
     T *dy = a.dy ? static_cast<T *>(a.dy) + first * a.lddy + at(0) : nullptr;
     const bool y_layer = a.y && a.post == CONVROT_NORM_LAYER;
+    const bool trip = a.pre != CONVROT_NORM_NONE || (a.y && a.post != CONVROT_NORM_NONE);
 
     if constexpr (kRing) {
 #pragma unroll
@@ -695,9 +732,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             copy_wait<kStages - 1>();
         }
         F2 h[kPairs], y[kPairs], g[kPairs], v[kPairs];
+        float m[8];
         get(0, h);
         get(1, y);
-        // h^ and y^
         if (a.pre == CONVROT_NORM_LAYER || y_layer) {
             F2 hs(0.0f), ys(0.0f);
 #pragma unroll
@@ -705,10 +742,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 hs = hs + h[e];
                 ys = ys + y[e];
             }
-            float hm = hs.sum(), ym = ys.sum();
-            sum(hm, ym);
-            hm = a.pre == CONVROT_NORM_LAYER ? -hm * inv_d : 0.0f;
-            ym = y_layer ? -ym * inv_d : 0.0f;
+            m[0] = hs.sum();
+            m[1] = ys.sum();
+            m[2] = m[3] = m[4] = m[5] = m[6] = m[7] = 0.0f;
+            sum(m);
+            const float hm = a.pre == CONVROT_NORM_LAYER ? -m[0] * inv_d : 0.0f, ym = y_layer ? -m[1] * inv_d : 0.0f;
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
                 const bool lo = inside(2 * e / kVec), hi = inside((2 * e + 1) / kVec);
@@ -716,44 +754,52 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 y[e] = y[e] + F2(lo ? ym : 0.0f, hi ? ym : 0.0f);
             }
         }
-        float inv = 1.0f, inv_y = 1.0f;
-        if (a.pre != CONVROT_NORM_NONE || (a.y && a.post != CONVROT_NORM_NONE)) {
-            F2 hs(0.0f), ys(0.0f);
+        get(3, g);
+        float inv = 1.0f, inv_y = 1.0f, mg = 0.0f, mgh = 0.0f, mqy = 0.0f;
+        if (trip) {
+            F2 hh(0.0f), yy(0.0f), gs(0.0f), gh(0.0f), gwy(0.0f), wys(0.0f), hwy(0.0f), dwy(0.0f);
+            get(2, v);
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
-                hs = fma2(h[e], h[e], hs);
-                ys = fma2(y[e], y[e], ys);
+                const F2 u = g[e] * w_pre[e];
+                hh = fma2(h[e], h[e], hh);
+                gs = gs + u;
+                gh = fma2(u, h[e], gh);
+                const F2 wy = w_post[e] * y[e];
+                yy = fma2(y[e], y[e], yy);
+                gwy = fma2(u, wy, gwy);
+                wys = wys + wy;
+                hwy = fma2(h[e], wy, hwy);
+                dwy = fma2(v[e], wy, dwy);
             }
-            float hv = hs.sum(), yv = ys.sum();
-            sum(hv, yv);
-            if (a.pre != CONVROT_NORM_NONE) inv = rsqrtf(fmaf(hv, inv_d, a.eps));
-            if (a.post != CONVROT_NORM_NONE) inv_y = rsqrtf(fmaf(yv, inv_d, a.eps));
-        }
-        // dH and the means that pre's gradient subtracts
-        get(3, v);
-        F2 ms(0.0f), mhs(0.0f);
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) {
-            h[e] = h[e] * F2(inv);
-            y[e] = y[e] * F2(inv_y);
-            s0[e] = s0[e] + v[e];
-            s1[e] = fma2(v[e], h[e], s1[e]);
-            g[e] = v[e] * w_pre[e];
-            ms = ms + g[e];
-            mhs = fma2(g[e], h[e], mhs);
-        }
-        float mg = 0.0f, mgh = 0.0f;
-        if (a.pre != CONVROT_NORM_NONE) {
-            mg = ms.sum();
-            mgh = mhs.sum();
-            sum(mg, mgh);
-            mg = a.pre == CONVROT_NORM_LAYER ? -mg * inv_d : 0.0f;
-            mgh *= -inv_d;
+            m[0] = hh.sum();
+            m[1] = yy.sum();
+            m[2] = gs.sum();
+            m[3] = gh.sum();
+            m[4] = gwy.sum();
+            m[5] = wys.sum();
+            m[6] = hwy.sum();
+            m[7] = dwy.sum();
+            sum(m);
+            if (a.pre != CONVROT_NORM_NONE) {
+                inv = rsqrtf(fmaf(m[0], inv_d, a.eps));
+                mgh = -m[3] * inv * inv_d;
+                if (a.pre == CONVROT_NORM_LAYER) mg = -m[2] * inv_d;
+            }
+            if (a.post != CONVROT_NORM_NONE) {
+                inv_y = rsqrtf(fmaf(m[1], inv_d, a.eps));
+                mqy = -(inv * (m[4] + mg * m[5] + inv * mgh * m[6]) + m[7]) * inv_y * inv_d;
+            }
         }
         get(2, v);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) {
-            v[e] = fma2(F2(inv), fma2(h[e], F2(mgh), g[e] + F2(mg)), v[e]);
+            h[e] = h[e] * F2(inv);
+            y[e] = y[e] * F2(inv_y);
+            s0[e] = s0[e] + g[e];
+            s1[e] = fma2(g[e], h[e], s1[e]);
+            g[e] = fma2(g[e], w_pre[e], F2(mg));
+            v[e] = fma2(F2(inv), fma2(h[e], F2(mgh), g[e]), v[e]);  // dH
             g[e] = v[e] * F2(a.res_scale);
         }
         if (dx) {
@@ -761,23 +807,27 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             dx += a.lddx;
         }
         if (a.y) {
-            F2 ms(0.0f), mys(0.0f);
+            F2 gs(0.0f), gy(0.0f);
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
                 t0[e] = t0[e] + v[e];
                 t1[e] = fma2(v[e], y[e], t1[e]);
                 g[e] = v[e] * w_post[e];
-                ms = ms + g[e];
-                mys = fma2(g[e], y[e], mys);
             }
             if (dy) {
-                float mq = 0.0f, mqy = 0.0f;
-                if (a.post != CONVROT_NORM_NONE) {
-                    mq = ms.sum();
-                    mqy = mys.sum();
-                    sum(mq, mqy);
-                    mq = a.post == CONVROT_NORM_LAYER ? -mq * inv_d : 0.0f;
-                    mqy *= -inv_d;
+                float mq = 0.0f;
+                if (y_layer) {
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        gs = gs + g[e];
+                        gy = fma2(g[e], y[e], gy);
+                    }
+                    m[0] = gs.sum();
+                    m[1] = gy.sum();
+                    m[2] = m[3] = m[4] = m[5] = m[6] = m[7] = 0.0f;
+                    sum(m);
+                    mq = -m[0] * inv_d;
+                    mqy = -m[1] * inv_d;
                 }
 #pragma unroll
                 for (int e = 0; e < kPairs; ++e) g[e] = F2(inv_y) * fma2(y[e], F2(mqy), g[e] + F2(mq));
