@@ -212,6 +212,8 @@ __device__ __forceinline__ uint4 shared16(uint32_t at)
 
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
+constexpr int kSms = 152;
+
 constexpr float kFp8Max = 448.0f;
 constexpr float kFp8AmaxFloor = 1.2621774483536189e-29f;  // 2^-96: no block's scale is 0 or its inverse infinite
 

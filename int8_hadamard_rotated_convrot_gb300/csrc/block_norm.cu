@@ -148,7 +148,6 @@ __device__ __forceinline__ void pack_row(const convrot_gated_norm_args &a, int64
 // Rows of a sample in 32 bits (row numbers have 31).
 __device__ __forceinline__ uint32_t sample_rows(int64_t rows) { return rows < 0x7fffffff ? static_cast<uint32_t>(rows) : 0x7fffffffu; }
 
-constexpr int kSms = 152;
 constexpr int kRingThreads = 640;  // 96 registers a thread, so that 640 threads share an SM
 constexpr int kRowThreads = 512;  // 128 registers a thread: up to 32 values of a row in each
 
