@@ -18,6 +18,11 @@ cudaError_t launch_fp8_pack(const void *x, int dtype, int64_t m, int64_t k, int6
 cudaError_t launch_fp8_quantize_weights(const void *w, int dtype, int64_t n, int64_t k, int64_t ldw, void *q,
                                         int64_t ldq, float *scale, int64_t lds, cudaStream_t stream);
 cudaError_t launch_fp8_gemm(const convrot_fp8_linear_args &a, cudaStream_t stream);
+// Few rows: whether that kernel takes the sizes, and whether it quantizes x itself.
+bool fp8_few_takes(int64_t m, int64_t n, int64_t k);
+bool fp8_few_quantizes(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_fp8_few(const convrot_fp8_linear_args &a, cudaStream_t stream);           // packed x
+cudaError_t launch_fp8_few_quantize(const convrot_fp8_linear_args &a, cudaStream_t stream);  // x as rows
 
 cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t stream);
 cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a, cudaStream_t stream);

@@ -18,6 +18,11 @@ constexpr int64_t kMaxRows = INT_MAX;  // rows and row blocks are counted in 32 
 
 int64_t groups(int64_t v, int64_t size) { return (v + size - 1) / size; }
 
+cudaError_t run_linear(const convrot_fp8_linear_args &a, cudaStream_t stream)
+{
+    return fp8_few_takes(a.m, a.n, a.k) ? launch_fp8_few(a, stream) : launch_fp8_gemm(a, stream);
+}
+
 convrot_status done(cudaError_t e) { return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA; }
 
 // A matrix [rows, cols] of elements of `bytes` bytes.
@@ -113,12 +118,12 @@ convrot_status convrot_fp8_linear(const convrot_fp8_linear_args *a, cudaStream_t
     if (st == CONVROT_OK)
         st = first_of({check_codes(a->x, a->m, a->k, a->ldx), check_matrix(a->x_scale, a->m, a->m, a->ld_x_scale, 4)});
     if (st != CONVROT_OK || a->m == 0 || a->n == 0) return st;
-    return done(launch_fp8_gemm(*a, stream));
+    return done(run_linear(*a, stream));
 }
 
 int64_t convrot_fp8_pack_linear_work_bytes(int64_t m, int64_t n, int64_t k)
 {
-    if (m < 1 || n < 1 || k < 1 || m > kMaxRows || k > CONVROT_MAX_K) return 0;
+    if (m < 1 || n < 1 || k < 1 || m > kMaxRows || k > CONVROT_MAX_K || fp8_few_quantizes(m, n, k)) return 0;
     return round256(m * work_ldq(k)) + round256(groups(k, 128) * work_lds(m) * 4);
 }
 
@@ -133,6 +138,7 @@ convrot_status convrot_fp8_pack_linear(const convrot_fp8_linear_args *a, cudaStr
     const int64_t need = convrot_fp8_pack_linear_work_bytes(a->m, a->n, a->k);
     if (need > 0 && (!a->work || a->work_bytes < need)) return CONVROT_ERR_INVALID_ARG;
     if (need > 0 && !aligned(a->work, 256)) return CONVROT_ERR_ALIGNMENT;
+    if (need == 0) return done(launch_fp8_few_quantize(*a, stream));
     convrot_fp8_linear_args g = *a;
     g.ldx = work_ldq(a->k);
     g.ld_x_scale = work_lds(a->m);
@@ -140,7 +146,7 @@ convrot_status convrot_fp8_pack_linear(const convrot_fp8_linear_args *a, cudaStr
     g.x = a->work;
     g.x_scale = scale;
     st = done(launch_fp8_pack(a->x, a->x_dtype, a->m, a->k, a->ldx, a->work, g.ldx, scale, g.ld_x_scale, stream));
-    return st == CONVROT_OK ? done(launch_fp8_gemm(g, stream)) : st;
+    return st == CONVROT_OK ? done(run_linear(g, stream)) : st;
 }
 
 convrot_status convrot_gated_norm(const convrot_gated_norm_args *a, cudaStream_t stream)

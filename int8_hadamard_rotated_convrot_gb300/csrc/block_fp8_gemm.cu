@@ -7,17 +7,25 @@
 // with fp32 accumulators in tensor memory. The scales are general fp32 numbers,
 // so each block of 128 features is one accumulation of its own (four K = 32
 // instructions) whose sums are drained, multiplied by the row's and the
-// block's scale and added up in fp32 registers. A drained value costs a tensor
-// memory read and half a packed fma; a 128 x 256 tile of one block takes the
-// tensor cores 512 cycles and its drain has to fit under that.
+// block's scale and added up in fp32 registers.
 //
-// fp8_pair_kernel (m > kSmallRows): a CTA pair (cluster of 2, cta_group::2),
+// fp8_pair_kernel (more than 64 rows): a CTA pair (cluster of 2, cta_group::2),
 // persistent over 256 x kBN output tiles, with the roles and the ring of the
 // int8 GEMM:
 //   warp 0      TMA producer of each CTA: a block's codes of its 128 rows of x
 //               and kBN / 2 rows of w, 128 bytes a row, 128-byte swizzled
 //   warp 1      tensor memory; in the even CTA one thread issues the MMAs
 //   warps 4-19  drain: four warps a lane quadrant, kBN / 4 columns each
+// What bounds it is the turn of the two accumulators: a block's MMAs take 512
+// cycles, and then its sums are announced, read (two 32-column loads a warp,
+// ~130 cycles each on a quarter of the SM), scaled (64 fmas a thread) and the
+// buffer handed back, ~1900 cycles in all. Measured on one GB300: 1200 cycles a
+// block and pair, 2.16 PFLOP/s without the activation (M32760 K5120 N13824),
+// at 1380 W of 1400; the MMAs and copies alone would take 800 cycles, where L2
+// feeds 12.6 TB/s. Not faster: slices of 128 columns with four accumulators
+// (x's codes read twice; 3.46 ms against 2.48), one CTA on its own (half as
+// much again from L2; 2.90), 16-column loads (2.87), scales through shared
+// memory (2.70).
 // A TMA map ends at column k, so a short last block is filled with zeros.
 // Every wait is bounded: one that runs out writes CONVROT_ERR_TIMEOUT to the
 // status word and the CTA winds down (copies and MMAs in flight are waited
@@ -37,12 +45,12 @@ using namespace tc;
 constexpr int kBK = 128;             // codes of one block: 128 bytes, one swizzle span
 constexpr int kBM = 128;             // rows of x (and of the accumulators) per CTA
 constexpr int kMmaK = 32;
-constexpr int kEpiWarps = 16;
-constexpr int kPairThreads = 128 + kEpiWarps * 32;
-// Registers a thread: launched at 96, warpgroup 0 gives some to the drain
-// warps: 4 x 32 x 40 + 16 x 32 x 104 = 58368 <= 640 x 96.
-constexpr int kRegsWg0 = 40, kRegsEpi = 104;
-static_assert(4 * 32 * kRegsWg0 + kEpiWarps * 32 * kRegsEpi <= kPairThreads * 96, "register split");
+constexpr int kDrainWarps = 16;
+constexpr int kPairThreads = 128 + kDrainWarps * 32;
+// Registers a thread: launched at 96, warpgroup 0 leaves most of its own to the
+// drain warps (64 sums, 32 values on the way): 4 x 32 x 32 + 16 x 32 x 112 = 640 x 96.
+constexpr int kRegsWg0 = 32, kRegsDrain = 112;
+static_assert(4 * 32 * kRegsWg0 + kDrainWarps * 32 * kRegsDrain <= kPairThreads * 96, "register split");
 
 template <int kBN>
 struct Cfg {
@@ -51,12 +59,15 @@ struct Cfg {
     static constexpr int OUT_WARP = 32 * 80;
     static constexpr int BUFS = 512 / kBN;  // accumulators of a block in tensor memory
     static constexpr int BAR_BYTES = 256;
-    static constexpr int FIT = (232448 - 1024 - kEpiWarps * OUT_WARP - BAR_BYTES) / STAGE_BYTES;
+    static constexpr int FIT = (232448 - 1024 - kDrainWarps * OUT_WARP - BAR_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + kEpiWarps * OUT_WARP + BAR_BYTES;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + kDrainWarps * OUT_WARP + BAR_BYTES;
     // kind::f8f6f4: D fp32, A and B e4m3, K-major, M = 256 over both CTAs, N = kBN
     static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(kBN >> 3) << 17) | (uint32_t(256 >> 4) << 24);
-    static_assert(8 * (2 * STAGES + 2 * BUFS + 1) + 8 <= BAR_BYTES, "barriers fit");
+    static_assert(8 * (2 * STAGES + BUFS + 1) + 8 <= BAR_BYTES, "barriers fit");
+    // a drain warp reads a block's end off its stage's barrier: that may not come round again before every warp has
+    // seen it, and block j + STAGES waits for the drains of block j + STAGES - BUFS
+    static_assert(STAGES >= BUFS, "stages outlast accumulators");
 };
 
 struct Fp8Params {
@@ -124,9 +135,13 @@ __device__ __forceinline__ void commit_local(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// A drained buffer is handed back without a release: this warp wrote nothing
+// that the MMA thread reads, and its tensor-memory loads have completed
+// (wait::ld) before it arrives. (With a release at cluster scope, which
+// waits for everything this thread has in flight: 4.70 ms instead of 2.63.)
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // Tiles in bands of kBand row blocks, columns fastest between bands: the tiles
@@ -145,15 +160,12 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t t
 // One warp's 32 rows of finished sums (lane: row), 64 bytes of each,
 // activated and stored: staged in shared memory and written four lanes a row.
 template <typename T, int kAct>
-__device__ __forceinline__ void store_box(const Fp8Params &p, uint32_t out, int lane, int64_t row0, int64_t col0, const F2 *acc)
+__device__ __forceinline__ void store_box(const Fp8Params &p, uint32_t out, int lane, int64_t row0, int64_t col0, const float *acc)
 {
     constexpr int kBox = 64 / sizeof(T);
     float v[kBox];
 #pragma unroll
-    for (int i = 0; i < kBox / 2; ++i) {
-        v[2 * i] = acc[i].lo();
-        v[2 * i + 1] = acc[i].hi();
-    }
+    for (int i = 0; i < kBox; ++i) v[i] = acc[i];
     if (p.bias) {
         if (p.vec_bias && col0 + kBox <= p.n) {
 #pragma unroll
@@ -217,14 +229,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kOut = C::STAGES * C::STAGE_BYTES, kBars = kOut + kEpiWarps * C::OUT_WARP;
+    constexpr int kOut = C::STAGES * C::STAGE_BYTES, kBars = kOut + kDrainWarps * C::OUT_WARP;
     const uint32_t bars = base + kBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
-    auto accf_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
-    auto acce_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + C::BUFS + b); };
-    const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 2 * C::BUFS);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * (2 * C::STAGES + 2 * C::BUFS + 1));
+    auto acce_bar = [&](int b) { return bars + 8u * (2 * C::STAGES + b); };
+    const uint32_t done_bar = bars + 8u * (2 * C::STAGES + C::BUFS);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * (2 * C::STAGES + C::BUFS + 1));
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const uint32_t rank = cluster_rank();
@@ -237,10 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int b = 0; b < C::BUFS; ++b) {
-            mbar_init(accf_bar(b), 1);
-            mbar_init(acce_bar(b), 2 * kEpiWarps);
-        }
+        for (int b = 0; b < C::BUFS; ++b) mbar_init(acce_bar(b), 2 * kDrainWarps);
         mbar_init(done_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -260,6 +268,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t tmem = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // x's codes and scales are the pack's
 
+    // Bounded; gives up early once another role has.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer();
+        for (;;) {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (*abort_flag || globaltimer() - t0 > kTimeoutNs) return false;
+        }
+    };
     auto fail = [&]() {
         *abort_flag = 1;
         if (p.dev_status) atomicExch(p.dev_status, static_cast<int32_t>(CONVROT_ERR_TIMEOUT));
@@ -276,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 tile_at(t, p.tiles_m, p.tiles_n, mt, nt);
                 const int xrow = static_cast<int>(mt * 2 * kBM + rank * kBM), wrow = static_cast<int>(nt * kBN + rank * (kBN / 2));
                 for (int j = 0; j < p.blocks; ++j) {
-                    if (*abort_flag || !mbar_wait(empty_bar(stage), phase ^ 1u)) {
+                    if (!wait(empty_bar(stage), phase ^ 1u)) {
                         ok = false;
                         break;
                     }
@@ -311,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             bool ok = true;
             for (uint32_t t = pair; t < tiles && ok; t += pairs) {
                 for (int j = 0; j < p.blocks; ++j) {
-                    if (*abort_flag || !mbar_wait(acce_bar(buf), buf_phase ^ 1u) || !mbar_wait(full_bar(stage), phase)) {
+                    if ((!wait(acce_bar(buf), buf_phase ^ 1u)) || !wait(full_bar(stage), phase)) {
                         ok = false;
                         break;
                     }
@@ -321,8 +340,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < kBK / kMmaK; ++kk)  // 32 bytes along K inside the swizzle span
                         mma_pair(d, da + 2u * kk, db + 2u * kk, C::IDESC, kk > 0 ? 1u : 0u);
-                    commit_both(empty_bar(stage));
-                    commit_both(accf_bar(buf));
+                    commit_both(empty_bar(stage));  // the stage is free, and the block's sums are there
                     if (++stage == C::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -339,11 +357,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsDrain));
         const int q = warp & 3, part = (warp - 4) >> 2;  // lane quadrant, column slice
         const uint32_t out = base + kOut + (warp - 4) * C::OUT_WARP;
         const uint32_t taddr0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + part * kCols;
-        uint32_t buf = 0, buf_phase = 0;
+        uint32_t buf = 0, stage = 0, phase = 0;
         const uint32_t acce0 = map_to_rank(acce_bar(0), 0);
         bool ok = true;
         for (uint32_t t = pair; t < tiles && ok; t += pairs) {
@@ -353,46 +371,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // this lane's row and this slice's columns share one scale in each block of k
             const bool row_in = row0 + lane < p.m, col_in = col0 < p.n;
             const float *sx = p.x_scale + (row_in ? row0 + lane : 0), *sw = p.w_scale + (col_in ? col0 / 128 * p.ld_w_scale : 0);
-            F2 acc[kCols / 2];
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < kCols / 2; ++i) acc[i] = F2(0.0f);
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
             float next_x = __ldg(sx), next_w = __ldg(sw);
             for (int j = 0; j < p.blocks; ++j) {
-                const F2 scale(next_x * next_w);
+                const float scale = next_x * next_w;
                 if (j + 1 < p.blocks) {  // the next block's scales arrive under this block's wait
                     sx += p.ld_x_scale;
                     next_x = __ldg(sx);
                     next_w = __ldg(++sw);
                 }
-                if (*abort_flag || !mbar_wait(accf_bar(buf), buf_phase)) {
+                if (!wait(empty_bar(stage), phase)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t taddr = taddr0 + buf * kBN;
 #pragma unroll
-                for (int c = 0; c < kCols / 16; ++c) {
-                    uint32_t r[16];
-                    tmem_ld16(taddr + c * 16, r);
-                    if (c == kCols / 16 - 1) {  // read to the end: the buffer is free
+                for (int c = 0; c < kCols / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(taddr + c * 32, r);
+                    if (c == kCols / 32 - 1) {  // read to the end: the buffer is free
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_remote(acce0 + 8u * buf);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        acc[c * 8 + i] = fma2(F2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), scale, acc[c * 8 + i]);
+                    for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), scale, acc[c * 32 + i]);
                 }
-                if (++buf == C::BUFS) {
-                    buf = 0;
-                    buf_phase ^= 1u;
+                if (++buf == C::BUFS) buf = 0;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
             if (!ok) break;
             if (row0 < p.m) {
 #pragma unroll
                 for (int c = 0; c < kCols / kBox; ++c)
-                    if (col0 + c * kBox < p.n) store_box<T, kAct>(p, out, lane, row0, col0 + c * kBox, acc + c * kBox / 2);
+                    if (col0 + c * kBox < p.n) store_box<T, kAct>(p, out, lane, row0, col0 + c * kBox, acc + c * kBox);
             }
         }
         if (!ok) fail();
