@@ -131,7 +131,7 @@ def load() -> ctypes.CDLL:
             getattr(lib, name).restype = i64
         for name in ("convrot_fp8_linear", "convrot_fp8_pack_linear", "convrot_gated_norm",
                      "convrot_gated_norm_backward", "convrot_rotary"):
-            getattr(lib, name).argtypes = [ctypes.c_char_p, vp]  # one packed struct of arguments
+            getattr(lib, name).argtypes = [vp, vp]  # (a struct of arguments, stream)
         lib.convrot_rotary_table.argtypes = [vp, i64, i32, vp, vp, i32, ctypes.c_double, vp, vp, i64, vp]
         lib.convrot_status_string.argtypes = [ctypes.c_int]
         lib.convrot_status_string.restype = ctypes.c_char_p

@@ -1,0 +1,453 @@
+// Argument marshalling of block.py's calls: torch tensors to the C structs of
+// include/convrot_block.h. A call checks a dozen tensors; through torch's
+// Python attributes that took 8 to 12 us, more than the kernels of the smallest
+// calls, and here it takes a fraction of one.
+//
+// Every function takes its arguments by position from block.py, raises
+// TypeError or ValueError for what the C side cannot check (types, shapes,
+// strides, device), and returns the C call's status.
+#include <Python.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/convrot_block.h"
+
+namespace {
+
+using at::Tensor;
+
+struct Matrix {
+    void *p = nullptr;
+    int64_t ld = 0;
+};
+
+bool raise(PyObject *kind, const char *name, const char *what)
+{
+    PyErr_Format(kind, "%s %s", name, what);
+    return false;
+}
+
+const Tensor *tensor(PyObject *o, const char *name)
+{
+    if (!THPVariable_Check(o)) {
+        raise(PyExc_TypeError, name, "must be a tensor");
+        return nullptr;
+    }
+    const Tensor &t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) {
+        raise(PyExc_TypeError, name, "must be a CUDA tensor");
+        return nullptr;
+    }
+    return &t;
+}
+
+bool dtype_of(const Tensor &t, const char *name, int32_t &code)
+{
+    switch (t.scalar_type()) {
+    case at::kFloat: code = CONVROT_F32; return true;
+    case at::kBFloat16: code = CONVROT_BF16; return true;
+    case at::kHalf: code = CONVROT_F16; return true;
+    default: return raise(PyExc_TypeError, name, "must be float32, bfloat16 or float16");
+    }
+}
+
+// A [rows, cols] tensor of the type with contiguous rows. One row has no
+// leading dimension of its own, so any that holds it will do.
+bool matrix(PyObject *o, const char *name, at::ScalarType type, int64_t rows, int64_t cols, Matrix &m)
+{
+    const Tensor *t = tensor(o, name);
+    if (!t) return false;
+    if (t->scalar_type() != type) {
+        PyErr_Format(PyExc_TypeError, "%s must be a tensor of %s, not %s", name, c10::toString(type), c10::toString(t->scalar_type()));
+        return false;
+    }
+    if (t->dim() != 2 || t->size(0) != rows || t->size(1) != cols) {
+        PyErr_Format(PyExc_ValueError, "%s must have the shape [%lld, %lld]", name, static_cast<long long>(rows), static_cast<long long>(cols));
+        return false;
+    }
+    if (cols > 1 && t->stride(1) != 1) return raise(PyExc_ValueError, name, "must have contiguous rows");
+    m.p = t->data_ptr();
+    m.ld = rows > 1 ? t->stride(0) : t->stride(0) > cols ? t->stride(0) : cols;
+    return true;
+}
+
+bool optional_matrix(PyObject *o, const char *name, at::ScalarType type, int64_t rows, int64_t cols, Matrix &m)
+{
+    m = Matrix{nullptr, cols};
+    return o == Py_None || matrix(o, name, type, rows, cols, m);
+}
+
+// A contiguous vector of n elements, or None.
+bool vector(PyObject *o, const char *name, at::ScalarType type, int64_t n, const void **p)
+{
+    *p = nullptr;
+    if (o == Py_None) return true;
+    const Tensor *t = tensor(o, name);
+    if (!t) return false;
+    if (t->scalar_type() != type || t->dim() != 1 || t->size(0) != n || (n > 1 && t->stride(0) != 1)) {
+        PyErr_Format(PyExc_TypeError, "%s must be a contiguous tensor of %lld elements of %s", name, static_cast<long long>(n), c10::toString(type));
+        return false;
+    }
+    *p = t->data_ptr();
+    return true;
+}
+
+bool status_word(PyObject *o, int32_t **p) { return vector(o, "dev_status", at::kInt, 1, const_cast<const void **>(reinterpret_cast<void **>(p))); }
+
+// A workspace: 1-D, contiguous, uint8, or None.
+bool workspace(PyObject *o, void **p, int64_t *bytes)
+{
+    *p = nullptr;
+    *bytes = 0;
+    if (o == Py_None) return true;
+    const Tensor *t = tensor(o, "work");
+    if (!t) return false;
+    if (t->scalar_type() != at::kByte || t->dim() != 1 || !t->is_contiguous()) return raise(PyExc_ValueError, "work", "must be a contiguous 1-D uint8 tensor");
+    *p = t->data_ptr();
+    *bytes = t->numel();
+    return true;
+}
+
+// The stream's handle: None is torch's current stream of the tensor's device.
+bool stream_of(PyObject *o, const Tensor &t, cudaStream_t &s)
+{
+    if (o == Py_None) {
+        s = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+        return true;
+    }
+    PyObject *v = PyObject_GetAttrString(o, "cuda_stream");
+    if (!v) return false;
+    s = static_cast<cudaStream_t>(PyLong_AsVoidPtr(v));
+    Py_DECREF(v);
+    return !PyErr_Occurred();
+}
+
+bool integer(PyObject *o, int64_t &v)
+{
+    v = PyLong_AsLongLong(o);
+    return !(v == -1 && PyErr_Occurred());
+}
+
+bool integer(PyObject *o, int32_t &v)
+{
+    int64_t w;
+    if (!integer(o, w)) return false;
+    v = static_cast<int32_t>(w);
+    return v == w || raise(PyExc_OverflowError, "integer", "does not fit 32 bits");
+}
+
+bool real(PyObject *o, float &v)
+{
+    v = static_cast<float>(PyFloat_AsDouble(o));
+    return !PyErr_Occurred();
+}
+
+PyObject *status(convrot_status s) { return PyLong_FromLong(s); }
+
+bool count(Py_ssize_t got, Py_ssize_t want)
+{
+    if (got == want) return true;
+    PyErr_Format(PyExc_TypeError, "%zd arguments expected, %zd given", want, got);
+    return false;
+}
+
+#define REQUIRE(x)                   \
+    do {                             \
+        if (!(x)) return nullptr;    \
+    } while (0)
+
+// Codes: rows that start on 16 bytes. One row needs no leading dimension, but the C side asks for a multiple of 16.
+bool codes(PyObject *o, const char *name, int64_t rows, int64_t cols, Matrix &m)
+{
+    if (!matrix(o, name, at::kFloat8_e4m3fn, rows, cols, m)) return false;
+    if (rows <= 1) m.ld = (cols + 15) / 16 * 16;
+    return true;
+}
+
+int64_t blocks(int64_t v) { return (v + CONVROT_FP8_BLOCK - 1) / CONVROT_FP8_BLOCK; }
+
+// (x or q, x_scale or None, w.q, w.scale, bias, act, out, work, dev_status, stream); x_scale None: x is rows to pack
+PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 10));
+    const bool pack = v[1] == Py_None;
+    const Tensor *x = tensor(v[0], pack ? "X" : "x.q"), *w = tensor(v[2], "w.q"), *out = tensor(v[6], "out");
+    REQUIRE(x && w && out);
+    if (x->dim() != 2 || w->dim() != 2) {
+        raise(PyExc_TypeError, "x and w", "must be 2-D tensors");
+        return nullptr;
+    }
+    convrot_fp8_linear_args a{};
+    a.m = x->size(0);
+    a.k = x->size(1);
+    a.n = w->size(0);
+    Matrix mx, ms{nullptr, a.m}, mw, mws, my;
+    if (pack) {
+        REQUIRE(dtype_of(*x, "X", a.x_dtype) && matrix(v[0], "X", x->scalar_type(), a.m, a.k, mx));
+    } else {
+        REQUIRE(codes(v[0], "x.q", a.m, a.k, mx) && matrix(v[1], "x.scale", at::kFloat, blocks(a.k), a.m, ms));
+    }
+    REQUIRE(codes(v[2], "w.q", a.n, a.k, mw) && matrix(v[3], "w.scale", at::kFloat, blocks(a.n), blocks(a.k), mws));
+    REQUIRE(dtype_of(*out, "out", a.y_dtype) && matrix(v[6], "out", out->scalar_type(), a.m, a.n, my));
+    const void *bias;
+    cudaStream_t stream;
+    REQUIRE(vector(v[4], "bias", at::kFloat, a.n, &bias) && integer(v[5], a.act) && workspace(v[7], &a.work, &a.work_bytes));
+    REQUIRE(status_word(v[8], &a.dev_status) && stream_of(v[9], *out, stream));
+    a.x = mx.p;
+    a.ldx = mx.ld;
+    a.x_scale = static_cast<const float *>(ms.p);
+    a.ld_x_scale = ms.ld;
+    a.w = mw.p;
+    a.ldw = mw.ld;
+    a.w_scale = static_cast<const float *>(mws.p);
+    a.ld_w_scale = mws.ld;
+    a.bias = static_cast<const float *>(bias);
+    a.y = my.p;
+    a.ldy = my.ld;
+    return status(pack ? convrot_fp8_pack_linear(&a, stream) : convrot_fp8_linear(&a, stream));
+}
+
+// (X, q, scale, stream)
+PyObject *pack_activations(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 4));
+    const Tensor *x = tensor(v[0], "X");
+    REQUIRE(x);
+    if (x->dim() != 2) {
+        raise(PyExc_TypeError, "X", "must be a 2-D tensor");
+        return nullptr;
+    }
+    const int64_t m = x->size(0), k = x->size(1);
+    int32_t dtype;
+    Matrix mx, mq, ms;
+    cudaStream_t stream;
+    REQUIRE(dtype_of(*x, "X", dtype) && matrix(v[0], "X", x->scalar_type(), m, k, mx) && codes(v[1], "q", m, k, mq));
+    REQUIRE(matrix(v[2], "scale", at::kFloat, blocks(k), m, ms) && stream_of(v[3], *x, stream));
+    return status(convrot_fp8_pack_activations(mx.p, dtype, m, k, mx.ld, mq.p, mq.ld, static_cast<float *>(ms.p), ms.ld, stream));
+}
+
+// The one type of the parameters that are given: float32 or the tensors' own.
+bool param_type(at::ScalarType own, std::initializer_list<PyObject *> all, at::ScalarType &type)
+{
+    type = at::kFloat;
+    for (PyObject *o : all) {
+        if (o == Py_None) continue;
+        const Tensor *t = tensor(o, "parameters");
+        if (!t) return false;
+        type = t->scalar_type();
+        return type == at::kFloat || type == own || raise(PyExc_TypeError, "parameters", "must be float32 or of x's type");
+    }
+    return true;
+}
+
+int32_t code_of(at::ScalarType t) { return t == at::kFloat ? CONVROT_F32 : t == at::kBFloat16 ? CONVROT_BF16 : CONVROT_F16; }
+
+// (x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
+//  out_h, out_n, q, q_scale, stream)
+PyObject *gated_norm(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 19));
+    const Tensor *x = tensor(v[0], "x");
+    REQUIRE(x);
+    if (x->dim() != 2) {
+        raise(PyExc_TypeError, "x", "must be a 2-D tensor");
+        return nullptr;
+    }
+    convrot_gated_norm_args a{};
+    const at::ScalarType t = x->scalar_type();
+    at::ScalarType p;
+    REQUIRE(dtype_of(*x, "x", a.dtype) && param_type(t, {v[2], v[3], v[4], v[8], v[9], v[11], v[12]}, p));
+    a.param_dtype = code_of(p);
+    a.m = x->size(0);
+    a.d = x->size(1);
+    a.rows_per_batch = a.m > 0 ? a.m : 1;
+    if (v[5] != Py_None) REQUIRE(integer(v[5], a.rows_per_batch));
+    if (a.rows_per_batch < 1) return status(CONVROT_ERR_INVALID_ARG);
+    const int64_t m = a.m, d = a.d, batches = (m + a.rows_per_batch - 1) / a.rows_per_batch;
+    Matrix mx, my, mg, mc, mf, mh, mn, mq{nullptr, 0}, ms{nullptr, 0};
+    cudaStream_t stream;
+    REQUIRE(matrix(v[0], "x", t, m, d, mx) && optional_matrix(v[1], "y", t, m, d, my) && optional_matrix(v[2], "gate", p, batches, d, mg));
+    REQUIRE(optional_matrix(v[3], "scale", p, batches, d, mc) && optional_matrix(v[4], "shift", p, batches, d, mf));
+    REQUIRE(real(v[6], a.res_scale) && integer(v[7], a.post) && vector(v[8], "post_weight", p, d, &a.post_weight));
+    REQUIRE(vector(v[9], "post_bias", p, d, &a.post_bias) && integer(v[10], a.pre) && vector(v[11], "pre_weight", p, d, &a.pre_weight));
+    REQUIRE(vector(v[12], "pre_bias", p, d, &a.pre_bias) && real(v[13], a.eps));
+    REQUIRE(optional_matrix(v[14], "out_h", t, m, d, mh) && optional_matrix(v[15], "out_n", t, m, d, mn));
+    if (v[16] != Py_None) REQUIRE(codes(v[16], "q", m, d, mq) && matrix(v[17], "scale", at::kFloat, blocks(d), m, ms));
+    REQUIRE(stream_of(v[18], *x, stream));
+    a.x = mx.p;
+    a.ldx = mx.ld;
+    a.y = my.p;
+    a.ldy = my.ld;
+    a.gate = mg.p;
+    a.ldgate = mg.ld;
+    a.scale = mc.p;
+    a.ldscale = mc.ld;
+    a.shift = mf.p;
+    a.ldshift = mf.ld;
+    a.h = mh.p;
+    a.ldh = mh.ld;
+    a.n = mn.p;
+    a.ldn = mn.ld;
+    a.q = mq.p;
+    a.ldq = mq.ld;
+    a.q_scale = static_cast<float *>(ms.p);
+    a.ld_q_scale = ms.ld;
+    return status(convrot_gated_norm(&a, stream));
+}
+
+// (h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
+//  dx, dy, dgate, dscale, dshift, dpost_weight, dpost_bias, dpre_weight, dpre_bias, work, stream); the gradients are dense
+PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 27));
+    const Tensor *h = tensor(v[0], "h");
+    REQUIRE(h);
+    if (h->dim() != 2) {
+        raise(PyExc_TypeError, "h", "must be a 2-D tensor");
+        return nullptr;
+    }
+    convrot_gated_norm_backward_args a{};
+    const at::ScalarType t = h->scalar_type();
+    at::ScalarType p;
+    REQUIRE(dtype_of(*h, "h", a.dtype) && param_type(t, {v[4], v[5], v[6], v[10], v[11], v[13], v[14]}, p));
+    a.param_dtype = code_of(p);
+    a.m = h->size(0);
+    a.d = h->size(1);
+    a.rows_per_batch = a.m > 0 ? a.m : 1;
+    if (v[7] != Py_None) REQUIRE(integer(v[7], a.rows_per_batch));
+    if (a.rows_per_batch < 1) return status(CONVROT_ERR_INVALID_ARG);
+    const int64_t m = a.m, d = a.d, batches = (m + a.rows_per_batch - 1) / a.rows_per_batch;
+    Matrix mh, my, mdh, mdn, mg, mc, mf, mx, mdy, m_dg, m_dc, m_df;
+    cudaStream_t stream;
+    REQUIRE(matrix(v[0], "h", t, m, d, mh) && optional_matrix(v[1], "y", t, m, d, my) && optional_matrix(v[2], "dh", t, m, d, mdh));
+    REQUIRE(optional_matrix(v[3], "dn", t, m, d, mdn) && optional_matrix(v[4], "gate", p, batches, d, mg));
+    REQUIRE(optional_matrix(v[5], "scale", p, batches, d, mc) && optional_matrix(v[6], "shift", p, batches, d, mf));
+    REQUIRE(real(v[8], a.res_scale) && integer(v[9], a.post) && vector(v[10], "post_weight", p, d, &a.post_weight));
+    REQUIRE(vector(v[11], "post_bias", p, d, &a.post_bias) && integer(v[12], a.pre) && vector(v[13], "pre_weight", p, d, &a.pre_weight));
+    REQUIRE(vector(v[14], "pre_bias", p, d, &a.pre_bias) && real(v[15], a.eps));
+    REQUIRE(optional_matrix(v[16], "dx", t, m, d, mx) && optional_matrix(v[17], "dy", t, m, d, mdy));
+    REQUIRE(optional_matrix(v[18], "dgate", at::kFloat, batches, d, m_dg) && optional_matrix(v[19], "dscale", at::kFloat, batches, d, m_dc));
+    REQUIRE(optional_matrix(v[20], "dshift", at::kFloat, batches, d, m_df));
+    const void *g[4];
+    const char *const names[4] = {"dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias"};
+    for (int i = 0; i < 4; ++i) REQUIRE(vector(v[21 + i], names[i], at::kFloat, d, &g[i]));
+    REQUIRE(workspace(v[25], &a.work, &a.work_bytes) && stream_of(v[26], *h, stream));
+    a.h = mh.p;
+    a.ldh = mh.ld;
+    a.y = my.p;
+    a.ldy = my.ld;
+    a.dh = mdh.p;
+    a.lddh = mdh.ld;
+    a.dn = mdn.p;
+    a.lddn = mdn.ld;
+    a.gate = mg.p;
+    a.ldgate = mg.ld;
+    a.scale = mc.p;
+    a.ldscale = mc.ld;
+    a.dx = mx.p;
+    a.lddx = mx.ld;
+    a.dy = mdy.p;
+    a.lddy = mdy.ld;
+    a.dgate = static_cast<float *>(m_dg.p);
+    a.dscale = static_cast<float *>(m_dc.p);
+    a.dshift = static_cast<float *>(m_df.p);
+    a.dpost_weight = static_cast<float *>(const_cast<void *>(g[0]));
+    a.dpost_bias = static_cast<float *>(const_cast<void *>(g[1]));
+    a.dpre_weight = static_cast<float *>(const_cast<void *>(g[2]));
+    a.dpre_bias = static_cast<float *>(const_cast<void *>(g[3]));
+    return status(convrot_gated_norm_backward(&a, stream));
+}
+
+// A [batch, tokens, heads, head_dim] tensor like `like` but for its heads.
+bool heads(PyObject *o, const char *name, const Tensor &like, void **p, int64_t &n, int64_t (&strides)[3])
+{
+    const Tensor *t = tensor(o, name);
+    if (!t) return false;
+    if (t->dim() != 4 || t->scalar_type() != like.scalar_type()) return raise(PyExc_TypeError, name, "must be 4-D and of q's type");
+    if (t->size(0) != like.size(0) || t->size(1) != like.size(1) || t->size(3) != like.size(3))
+        return raise(PyExc_ValueError, name, "must have q's batch, tokens and head_dim");
+    if (t->size(3) > 1 && t->stride(3) != 1) return raise(PyExc_ValueError, name, "must have a contiguous last dimension");
+    *p = t->data_ptr();
+    n = t->size(2);
+    for (int i = 0; i < 3; ++i) strides[i] = t->stride(i);
+    return true;
+}
+
+// (q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream)
+PyObject *rotary(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 11));
+    const Tensor *q = tensor(v[0], "q"), *cos = tensor(v[2], "cos");
+    REQUIRE(q && cos);
+    if (q->dim() != 4 || cos->dim() != 2) {
+        raise(PyExc_TypeError, "q and cos", "must be [batch, tokens, heads, head_dim] and [rows, pairs]");
+        return nullptr;
+    }
+    convrot_rotary_args a{};
+    REQUIRE(dtype_of(*q, "q", a.dtype));
+    a.batch = q->size(0);
+    a.tokens = q->size(1);
+    if (q->size(3) > INT32_MAX || cos->size(1) > INT32_MAX / 2) return status(CONVROT_ERR_UNSUPPORTED);
+    a.head_dim = static_cast<int32_t>(q->size(3));
+    a.rot_dim = static_cast<int32_t>(2 * cos->size(1));
+    a.table_rows = cos->size(0);
+    void *qp, *kp = nullptr, *oq, *ok = nullptr;
+    int64_t out_heads;
+    REQUIRE(heads(v[0], "q", *q, &qp, a.q_heads, a.q_strides) && heads(v[7], "out_q", *q, &oq, out_heads, a.out_q_strides));
+    bool same = out_heads == a.q_heads;
+    if (v[1] != Py_None) {
+        REQUIRE(heads(v[1], "k", *q, &kp, a.k_heads, a.k_strides) && heads(v[8], "out_k", *q, &ok, out_heads, a.out_k_strides));
+        same = same && out_heads == a.k_heads;
+    }
+    if (!same) {
+        raise(PyExc_ValueError, "outputs", "must have as many heads as their inputs");
+        return nullptr;
+    }
+    Matrix mc, ms;
+    REQUIRE(matrix(v[2], "cos", at::kFloat, a.table_rows, cos->size(1), mc) && matrix(v[3], "sin", at::kFloat, a.table_rows, cos->size(1), ms));
+    if (mc.ld != ms.ld) {
+        raise(PyExc_ValueError, "cos and sin", "must have the same leading dimension");
+        return nullptr;
+    }
+    if (v[4] != Py_None) {
+        const Tensor *t = tensor(v[4], "positions");
+        REQUIRE(t);
+        if (t->scalar_type() != at::kInt && t->scalar_type() != at::kLong) {
+            raise(PyExc_TypeError, "positions", "must be int32 or int64");
+            return nullptr;
+        }
+        const bool shared = t->dim() == 1 && t->size(0) == a.tokens;
+        if (!shared && !(t->dim() == 2 && t->size(0) == a.batch && t->size(1) == a.tokens)) {
+            raise(PyExc_ValueError, "positions", "must be [batch, tokens] or [tokens]");
+            return nullptr;
+        }
+        if (a.tokens > 1 && t->stride(t->dim() - 1) != 1) {
+            raise(PyExc_ValueError, "positions", "must be contiguous along tokens");
+            return nullptr;
+        }
+        a.positions = t->data_ptr();
+        a.position_bits = t->scalar_type() == at::kLong ? 64 : 32;
+        a.pos_stride = shared ? 0 : t->stride(0);
+    }
+    const int inverse = PyObject_IsTrue(v[6]);
+    cudaStream_t stream;
+    REQUIRE(integer(v[5], a.layout) && inverse >= 0 && status_word(v[9], &a.dev_status) && stream_of(v[10], *q, stream));
+    a.inverse = inverse;
+    a.q = qp;
+    a.k = kp;
+    a.out_q = oq;
+    a.out_k = ok;
+    a.cos = static_cast<const float *>(mc.p);
+    a.sin = static_cast<const float *>(ms.p);
+    a.ldt = mc.ld;
+    return status(convrot_rotary(&a, stream));
+}
+
+#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {METHOD(linear), METHOD(pack_activations), METHOD(gated_norm), METHOD(gated_norm_backward), METHOD(rotary),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__block() { return PyModule_Create(&module); }

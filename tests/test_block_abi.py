@@ -2,6 +2,7 @@
 and the rotary frequencies. No call here reaches a kernel."""
 
 import math
+import struct
 
 import pytest
 import torch
@@ -11,6 +12,12 @@ from int8_hadamard_rotated_convrot_gb300 import build as cbuild
 from int8_hadamard_rotated_convrot_gb300 import convrot as cr
 
 FAKE = 0x10000  # aligned and never dereferenced on these paths
+
+# the argument structs of include/convrot_block.h, field by field
+LINEAR = struct.Struct("@8P3q5qq4i")
+NORM = struct.Struct("@13P3q9q2f4i")
+NORM_BACKWARD = struct.Struct("@20Pq3q8q2f4i")
+ROTARY = struct.Struct("@8P4q12q3q6i")
 
 
 @pytest.fixture(scope="module")
@@ -23,7 +30,7 @@ def linear_args(**kw):
     v = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, bias=0, y=FAKE, work=FAKE, status=0, m=4, n=8, k=256, ldx=256, ldxs=4,
              ldw=256, ldws=2, ldy=8, work_bytes=1 << 30, x_dtype=bl.BF16, y_dtype=bl.BF16, act=0, reserved=0)
     assert set(kw) <= set(v)
-    return bl._LINEAR.pack(*(v | kw).values())
+    return LINEAR.pack(*(v | kw).values())
 
 
 LINEAR_BAD = [
@@ -94,7 +101,7 @@ def norm_args(**kw):
              m=4, d=64, rows=4, ldx=64, ldy=64, ldgate=64, ldscale=64, ldshift=64, ldh=64, ldn=64, ldq=64, ldqs=4,
              res_scale=1.0, eps=1e-6, post=0, pre=1, dtype=bl.BF16, p=bl.F32)
     assert set(kw) <= set(v)
-    return bl._NORM.pack(*(v | kw).values())
+    return NORM.pack(*(v | kw).values())
 
 
 NORM_BAD = [
@@ -128,7 +135,7 @@ def grad_args(**kw):
              m=4, d=64, rows=4, ldh=64, ldy=64, lddh=64, lddn=64, ldgate=64, ldscale=64, lddx=64, lddy=64,
              res_scale=1.0, eps=1e-6, post=0, pre=1, dtype=bl.BF16, p=bl.F32)
     assert set(kw) <= set(v)
-    return bl._NORM_BACKWARD.pack(*(v | kw).values())
+    return NORM_BACKWARD.pack(*(v | kw).values())
 
 
 GRAD_BAD = [
@@ -160,7 +167,7 @@ def rotary_args(**kw):
     flat = []
     for x in (v | kw).values():
         flat += x if isinstance(x, tuple) else [x]
-    return bl._ROTARY.pack(*flat)
+    return ROTARY.pack(*flat)
 
 
 ROTARY_BAD = [
