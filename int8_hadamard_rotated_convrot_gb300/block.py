@@ -165,14 +165,8 @@ def convrot_fp8_pack_linear(X: torch.Tensor, w: Fp8Weights, bias: torch.Tensor |
                             stream=None) -> torch.Tensor:
     """Y [m, n] = act(pack(X) w^T + b): convrot_fp8_pack_activations and convrot_fp8_linear in one call.
     Y has out's, out_dtype's or X's type. ``work`` (uint8) is allocated here when not given."""
-    m, k = X.shape
-    n = w.q.shape[0]
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype or X.dtype, device=X.device)
-    if work is None:
-        need = fp8_pack_linear_work_bytes(m, n, k)
-        if need:
-            work = torch.empty(need, dtype=torch.uint8, device=X.device)
+        out = torch.empty((X.shape[0], w.q.shape[0]), dtype=out_dtype or X.dtype, device=X.device)
     _check(_library().linear(X, None, w.q, w.scale, bias, act, out, work, dev_status, stream), "convrot_fp8_pack_linear")
     return out
 
@@ -234,28 +228,11 @@ def convrot_gated_norm_backward(h: torch.Tensor, y: torch.Tensor | None, dh: tor
     """The gradients of convrot_gated_norm's inputs, from its output h, its input y and the gradients dh and dn
     of its outputs (None: zero). A dict with dx, dy (of h's type) and, in float32, dgate, dscale, dshift [batches, d]
     and dpost_weight, dpost_bias, dpre_weight, dpre_bias [d]: None for each input that was not given."""
-    m, d = h.shape
-    dtype, dev = h.dtype, h.device
-    rows = rows_per_batch or max(m, 1)
-    batches = -(-m // rows)
-    if y is None and not (gate is None and post_weight is None and post_bias is None):
-        raise ValueError("gate, post_weight and post_bias belong to a branch y")
-    dx = torch.empty((m, d), dtype=dtype, device=dev)
-    dy = None if y is None else torch.empty((m, d), dtype=dtype, device=dev)
-    # the small gradients are views of one buffer, the samples' first
-    by_sample = [t is not None for t in (gate, scale, shift)]
-    by_weight = [t is not None for t in (post_weight, post_bias, pre_weight, pre_bias)]
-    small = torch.empty((sum(by_sample) * batches + sum(by_weight), d), dtype=torch.float32, device=dev)
-    parts = list(small.split([batches] * sum(by_sample) + [1] * sum(by_weight)))
-    of_samples = [parts.pop(0) if wanted else None for wanted in by_sample]
-    of_weights = [parts.pop(0)[0] if wanted else None for wanted in by_weight]
-    if work is None:
-        work = torch.empty(_cr.load().convrot_gated_norm_backward_work_bytes(m, d, rows), dtype=torch.uint8, device=dev)
-    _check(_library().gated_norm_backward(h, y, dh, dn, gate, scale, shift, rows, res_scale, post, post_weight, post_bias, pre,
-                                          pre_weight, pre_bias, eps, dx, dy, *of_samples, *of_weights, work, stream),
-           "convrot_gated_norm_backward")
-    names = ("dgate", "dscale", "dshift", "dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias")
-    return {"dx": dx, "dy": dy, **dict(zip(names, of_samples + of_weights))}
+    got = _library().gated_norm_backward(h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight,
+                                         post_bias, pre, pre_weight, pre_bias, eps, work, stream)
+    if not isinstance(got, dict):
+        raise ConvrotError(got, "convrot_gated_norm_backward")
+    return got
 
 
 # ---------------------------------------------------------------- rotary positions

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -32,6 +33,9 @@ cudaError_t launch_rotary(const convrot_rotary_args &a, cudaStream_t stream);
 cudaError_t launch_rotary_table(const double *positions, int64_t rows, int32_t axes, const double *freq,
                                 const int32_t *axis, int32_t pairs, double factor, float *cos, float *sin,
                                 int64_t ldt, cudaStream_t stream);
+
+constexpr int kSms = 152;
+constexpr int kMaxShared = 227 * 1024;  // shared memory of a block
 
 // Calls f with a null pointer of the element type that the dtype names.
 template <typename F>
@@ -215,9 +219,27 @@ __device__ __forceinline__ uint4 shared16(uint32_t at)
     return v;
 }
 
+// Allows a kernel the shared memory of a whole SM, once for each kernel (Tag)
+// and device: the attribute stays, and setting it costs about as much as a launch.
+template <typename Tag, typename K>
+cudaError_t allow_shared(K *kernel)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared - static_cast<int>(attr.sharedSizeBytes));
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-constexpr int kSms = 152;
 
 constexpr float kFp8Max = 448.0f;
 constexpr float kFp8AmaxFloor = 1.2621774483536189e-29f;  // 2^-96: no block's scale is 0 or its inverse infinite

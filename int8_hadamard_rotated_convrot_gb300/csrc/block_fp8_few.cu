@@ -11,8 +11,8 @@
 //
 //   warp 0      TMA producer: 16 KB of w a block into a ring of kStages
 //   warp 1      tensor memory; one thread issues the MMAs
-//   warps 2-5   quantize x (kQuantize: at most 16 rows; a call is one launch),
-//               then drain: lane = row of w, 16 to 64 sums in registers
+//   warps 2-9   quantize x (kQuantize: at most 16 rows; a call is one launch)
+//   warps 2-5   drain: lane = row of w, 16 to 64 sums in registers
 //
 // Bound: the weights' bytes over HBM (or L2, where they stay there between
 // calls), and the latency of one launch.
@@ -30,7 +30,8 @@ using namespace tc;
 
 constexpr int kBK = 128, kBM = 128, kMmaK = 32;
 constexpr int kStages = 4, kStageBytes = kBM * kBK;
-constexpr int kThreads = 192;
+constexpr int kXWarps = 8;       // that prepare x
+constexpr int kThreads = 64 + 32 * kXWarps;
 constexpr int kMaxBlocks = 32;   // a CTA's share of k: 512 columns of tensor memory / 16
 constexpr int kMaxSplit = 8;     // CTAs of a cluster
 constexpr int kStaticBytes = 1024 + 2048;  // the system's shared memory and the scales, at least
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads)
             mbar_init(empty_bar(s), 1);
         }
         for (int j = 0; j < count; ++j) {
-            mbar_init(x_bar(j), kQuantize ? 4 : 1);
+            mbar_init(x_bar(j), kQuantize ? kXWarps : 1);
             mbar_init(sum_bar(j), 1);
         }
         mbar_init(done_bar, 1);
@@ -210,72 +211,93 @@ __global__ void __launch_bounds__(kThreads)
         const int w = warp - 2;
         const float *sw = p.w_scale + static_cast<int64_t>(tile) * p.ld_w_scale + j0;
         if constexpr (kQuantize) {
-            // one row's block at a time, four values a lane, into the swizzled layout (16-byte chunk c of row r at c ^ (r & 7))
-            for (int j = 0; j < count; ++j) {
-                const int c0 = (j0 + j) * kBK;
-                for (int r = w; r < p.m; r += 4) {
-                    const TX *row = static_cast<const TX *>(p.x) + r * p.ldx + c0 + lane * 4;
-                    float v[4];
-                    if (p.wide_x && c0 + kBK <= p.k) {
+            // A row's block is a warp's at a time, four values a lane; kBatch of them are loaded together. Codes go to
+            // the layout that the MMA reads (16-byte chunk c of row r at c ^ (r & 7)).
+            constexpr int kBatch = 4;
+            const int units = count * p.m;
+            int arrived = 0;  // blocks that this warp has nothing left to add to
+            for (int u0 = w; u0 - w < units || arrived < count; u0 += kXWarps * kBatch) {
+                float v[kBatch][4], sw_j[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int u = u0 + i * kXWarps, j = u / p.m, r = u - j * p.m, c = (j0 + j) * kBK + lane * 4;
+                    if (u >= units) break;
+                    const TX *from = static_cast<const TX *>(p.x) + r * p.ldx + c;
+                    sw_j[i] = __ldg(sw + j);
+                    if (p.wide_x && c + 4 <= p.k) {
                         Raw<TX, 4> four;
-                        four.load(row);
-                        four.unpack(v);
+                        four.load(from);
+                        four.unpack(v[i]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = c0 + lane * 4 + e < p.k ? to_f32(row[e]) : 0.0f;
+                        for (int e = 0; e < 4; ++e) v[i][e] = c + e < p.k ? to_f32(from[e]) : 0.0f;
                     }
-                    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int u = u0 + i * kXWarps, j = u / p.m, r = u - j * p.m;
+                    if (u >= units) break;
+                    float amax = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     amax = fmaxf(amax, kFp8AmaxFloor);
                     const float up = fp8_up(amax);
                     const uint32_t to = xtiles + j * kTile + r * kBK + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(e4m3x4(v[0] * up, v[1] * up, v[2] * up, v[3] * up)) : "memory");
-                    if (lane == 0) scales[j * kTok + r] = (amax / kFp8Max) * __ldg(sw + j);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(e4m3x4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up))
+                                 : "memory");
+                    if (lane == 0) scales[j * kTok + r] = (amax / kFp8Max) * sw_j[i];
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read these bytes
-                __syncwarp();
-                if (lane == 0) mbar_arrive(x_bar(j));
+                // blocks before the next batch's first are done as far as this warp goes
+                const int next = u0 + kXWarps * kBatch, until = next < units ? next / p.m : count;
+                if (arrived < until) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read these bytes
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int j = arrived; j < until; ++j) mbar_arrive(x_bar(j));
+                    arrived = until;
+                }
             }
         } else {
-            for (int i = threadIdx.x - 64; i < count * kTok; i += 128) {
+            for (int i = threadIdx.x - 64; i < count * kTok; i += 32 * kXWarps) {
                 const int j = i / kTok, r = i % kTok;
                 scales[i] = r < p.m ? __ldg(p.x_scale + (j0 + j) * p.ld_x_scale + r) * __ldg(sw + j) : 0.0f;
             }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // every row's scales, among these four warps
-        const int q = warp & 3;  // tensor-memory lanes of this warp
-        float acc[kTok];
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kXWarps) : "memory");  // every row's scales, among these warps
+        if (w < 4) {
+            const int q = warp & 3;  // tensor-memory lanes of this warp
+            float acc[kTok];
 #pragma unroll
-        for (int i = 0; i < kTok; ++i) acc[i] = 0.0f;
-        bool ok = true;
-        for (int j = 0; j < count; ++j) {
-            if (!wait(sum_bar(j), 0)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
+            for (int i = 0; i < kTok; ++i) acc[i] = 0.0f;
+            bool ok = true;
+            for (int j = 0; j < count; ++j) {
+                if (!wait(sum_bar(j), 0)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < kTok; c += 16) {
-                if (c >= p.m) break;
-                uint32_t r[16];
-                tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + j * kTok + c, r);
+                for (int c = 0; c < kTok; c += 16) {
+                    if (c >= p.m) break;
+                    uint32_t r[16];
+                    tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + j * kTok + c, r);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 s = *reinterpret_cast<const float4 *>(&scales[j * kTok + c + i]);
-                    acc[c + i] = fmaf(__uint_as_float(r[i]), s.x, acc[c + i]);
-                    acc[c + i + 1] = fmaf(__uint_as_float(r[i + 1]), s.y, acc[c + i + 1]);
-                    acc[c + i + 2] = fmaf(__uint_as_float(r[i + 2]), s.z, acc[c + i + 2]);
-                    acc[c + i + 3] = fmaf(__uint_as_float(r[i + 3]), s.w, acc[c + i + 3]);
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 s = *reinterpret_cast<const float4 *>(&scales[j * kTok + c + i]);
+                        acc[c + i] = fmaf(__uint_as_float(r[i]), s.x, acc[c + i]);
+                        acc[c + i + 1] = fmaf(__uint_as_float(r[i + 1]), s.y, acc[c + i + 1]);
+                        acc[c + i + 2] = fmaf(__uint_as_float(r[i + 2]), s.z, acc[c + i + 2]);
+                        acc[c + i + 3] = fmaf(__uint_as_float(r[i + 3]), s.w, acc[c + i + 3]);
+                    }
                 }
             }
-        }
-        if (!ok) fail();
-        // this CTA's sums, [row of x][row of w], over the ring's first stages: the last MMA has read them (sum_bar)
-        const uint32_t sums = base + (q * 32 + lane) * 4;
+            if (!ok) fail();
+            // this CTA's sums, [row of x][row of w], over the ring's first stages: the last MMA has read them (sum_bar)
+            const uint32_t sums = base + (q * 32 + lane) * 4;
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < p.m && ok) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + i * kBM * 4), "f"(acc[i]) : "memory");
+            for (int i = 0; i < kTok; ++i)
+                if (i < p.m && ok) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + i * kBM * 4), "f"(acc[i]) : "memory");
+        }
     }
 
     tc_fence_before();
@@ -288,7 +310,7 @@ __global__ void __launch_bounds__(kThreads)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
     } else if (warp > 1) {
         // the cluster's warps share out the outputs, 32 rows of w of one row of x at a time
-        for (int u = static_cast<int>(rank) * 4 + warp - 2; u < p.m * 4; u += static_cast<int>(split) * 4) {
+        for (int u = static_cast<int>(rank) * kXWarps + warp - 2; u < p.m * 4; u += static_cast<int>(split) * kXWarps) {
             const int r = u >> 2, o = (u & 3) * 32 + lane;
             const uint32_t at = base + (r * kBM + o) * 4;
             float v = 0.0f;
@@ -305,6 +327,9 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (split > 1) cluster_sync();  // a CTA's sums stay until its peers have read them
 }
+
+template <int kTok, typename TX, typename T, int kAct>
+struct kernel_tag;
 
 template <int kTok, typename TX, typename T, int kAct>
 cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_t stream)
@@ -341,7 +366,7 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_
     const int part = static_cast<int>(p.tmem_cols) * (228 * 1024 / 512);
     if (bytes < part - kStaticBytes) bytes = part - kStaticBytes;
     auto kernel = fp8_few_kernel<kTok, TX, T, kAct>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_shared<kernel_tag<kTok, TX, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t config{};
     config.gridDim = dim3(static_cast<unsigned>((a.n + kBM - 1) / kBM * split));

@@ -424,6 +424,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 template <int kBN, typename T, int kAct>
+struct pair_tag;
+
+template <int kBN, typename T, int kAct>
 cudaError_t launch_pair(const convrot_fp8_linear_args &a, cudaStream_t stream)
 {
     using C = Cfg<kBN>;
@@ -448,7 +451,7 @@ cudaError_t launch_pair(const convrot_fp8_linear_args &a, cudaStream_t stream)
     p.vec_y = aligned_to(a.y, 16) && a.ldy * sizeof(T) % 16 == 0;
     p.vec_bias = aligned_to(a.bias, 16);
     auto kernel = fp8_pair_kernel<kBN, T, kAct>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = allow_shared<pair_tag<kBN, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;

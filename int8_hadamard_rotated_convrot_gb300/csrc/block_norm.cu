@@ -971,6 +971,9 @@ cudaError_t launch_block_rows(const convrot_gated_norm_args &a, cudaStream_t str
 
 constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; the rest stays L1 for the vectors
 
+template <typename T, typename P, int kNv, bool kBranch>
+struct ring_tag;
+
 // Runs of rows through the ring, if there are enough of them (eight a block, so
 // that filling the ring is a small part) and the ring fits.
 template <typename T, typename P, int kNv, bool kBranch>
@@ -986,7 +989,7 @@ bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaErro
     const int64_t blocks = static_cast<int64_t>(per_sm) * kSms;
     if (a.m < 8 * blocks) return false;
     auto kernel = gated_norm_ring_kernel<T, P, kNv, kStages, kBranch>;
-    *e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    *e = allow_shared<ring_tag<T, P, kNv, kBranch>>(kernel);
     if (*e != cudaSuccess) return true;
     const int64_t rows = (a.m + blocks - 1) / blocks;
     kernel<<<static_cast<unsigned>((a.m + rows - 1) / rows), threads, bytes, stream>>>(a, static_cast<int32_t>(rows));
@@ -1033,8 +1036,9 @@ cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t str
             return launch_block_rows<T, P, kVec, 32 / kVec>(a, stream);
         }
         if (a.d <= 128) return launch_warp_rows<T, P, 1, 4>(a, stream);
-        if (a.d <= 4 * kRowThreads) return launch_block_rows<T, P, 1, 4>(a, stream);
-        if (a.d <= 12 * kRowThreads) return launch_block_rows<T, P, 1, 12>(a, stream);
+        // single elements: blocks of 128 to 512 threads, enough values in each that the sums' cost is spread
+        if (a.d <= 2048) return launch_block_rows<T, P, 1, 8>(a, stream);
+        if (a.d <= 8192) return launch_block_rows<T, P, 1, 16>(a, stream);
         return launch_block_rows<T, P, 1, 32>(a, stream);
     });
 }
@@ -1070,12 +1074,15 @@ cudaError_t launch_with(void (*kernel)(A...), dim3 grid, unsigned threads, size_
 }
 
 template <typename T, typename P, int kVec, int kCluster>
+struct grad_tag;
+
+template <typename T, typename P, int kVec, int kCluster>
 cudaError_t launch_grad(const convrot_gated_norm_backward_args &a, const GradSplit &s, float *part, cudaStream_t stream)
 {
     const int bytes = kVec == 1 ? 0 : grad_stages<T>() * 4 * (kGradCols / kVec) * s.threads * 16;
     auto kernel = norm_grad_kernel<T, P, kVec, kCluster>;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t e = allow_shared<grad_tag<T, P, kVec, kCluster>>(kernel);
         if (e != cudaSuccess) return e;
     }
     return launch_with(kernel, dim3(static_cast<unsigned>(s.units() * kCluster)), static_cast<unsigned>(s.threads), bytes,

@@ -7,6 +7,7 @@
 // TypeError or ValueError for what the C side cannot check (types, shapes,
 // strides, device), and returns the C call's status.
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -204,6 +205,19 @@ PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
     a.bias = static_cast<const float *>(bias);
     a.y = my.p;
     a.ldy = my.ld;
+    Tensor work;
+    if (pack && !a.work) {
+        a.work_bytes = convrot_fp8_pack_linear_work_bytes(a.m, a.n, a.k);
+        if (a.work_bytes) {
+            try {
+                work = at::empty({a.work_bytes}, out->options().dtype(at::kByte));
+            } catch (const std::exception &e) {
+                PyErr_SetString(PyExc_RuntimeError, e.what());
+                return nullptr;
+            }
+            a.work = work.data_ptr();
+        }
+    }
     return status(pack ? convrot_fp8_pack_linear(&a, stream) : convrot_fp8_linear(&a, stream));
 }
 
@@ -295,11 +309,20 @@ PyObject *gated_norm(PyObject *, PyObject *const *v, Py_ssize_t n)
     return status(convrot_gated_norm(&a, stream));
 }
 
+// A contiguous tensor of the sizes at an offset of another's memory, without a trip through the dispatcher.
+Tensor part_of(const Tensor &whole, int64_t offset, at::IntArrayRef sizes)
+{
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    return t;
+}
+
 // (h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
-//  dx, dy, dgate, dscale, dshift, dpost_weight, dpost_bias, dpre_weight, dpre_bias, work, stream); the gradients are dense
+//  work, stream) -> status, or the dict of gradients. They are allocated here, the small ones as parts of one buffer.
 PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
 {
-    REQUIRE(count(n, 27));
+    REQUIRE(count(n, 18));
     const Tensor *h = tensor(v[0], "h");
     REQUIRE(h);
     if (h->dim() != 2) {
@@ -317,7 +340,7 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
     if (v[7] != Py_None) REQUIRE(integer(v[7], a.rows_per_batch));
     if (a.rows_per_batch < 1) return status(CONVROT_ERR_INVALID_ARG);
     const int64_t m = a.m, d = a.d, batches = (m + a.rows_per_batch - 1) / a.rows_per_batch;
-    Matrix mh, my, mdh, mdn, mg, mc, mf, mx, mdy, m_dg, m_dc, m_df;
+    Matrix mh, my, mdh, mdn, mg, mc, mf;
     cudaStream_t stream;
     REQUIRE(matrix(v[0], "h", t, m, d, mh) && optional_matrix(v[1], "y", t, m, d, my) && optional_matrix(v[2], "dh", t, m, d, mdh));
     REQUIRE(optional_matrix(v[3], "dn", t, m, d, mdn) && optional_matrix(v[4], "gate", p, batches, d, mg));
@@ -325,13 +348,45 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
     REQUIRE(real(v[8], a.res_scale) && integer(v[9], a.post) && vector(v[10], "post_weight", p, d, &a.post_weight));
     REQUIRE(vector(v[11], "post_bias", p, d, &a.post_bias) && integer(v[12], a.pre) && vector(v[13], "pre_weight", p, d, &a.pre_weight));
     REQUIRE(vector(v[14], "pre_bias", p, d, &a.pre_bias) && real(v[15], a.eps));
-    REQUIRE(optional_matrix(v[16], "dx", t, m, d, mx) && optional_matrix(v[17], "dy", t, m, d, mdy));
-    REQUIRE(optional_matrix(v[18], "dgate", at::kFloat, batches, d, m_dg) && optional_matrix(v[19], "dscale", at::kFloat, batches, d, m_dc));
-    REQUIRE(optional_matrix(v[20], "dshift", at::kFloat, batches, d, m_df));
-    const void *g[4];
-    const char *const names[4] = {"dpost_weight", "dpost_bias", "dpre_weight", "dpre_bias"};
-    for (int i = 0; i < 4; ++i) REQUIRE(vector(v[21 + i], names[i], at::kFloat, d, &g[i]));
-    REQUIRE(workspace(v[25], &a.work, &a.work_bytes) && stream_of(v[26], *h, stream));
+    REQUIRE(workspace(v[16], &a.work, &a.work_bytes) && stream_of(v[17], *h, stream));
+    if (v[1] == Py_None && (v[4] != Py_None || v[10] != Py_None || v[11] != Py_None)) {
+        raise(PyExc_ValueError, "gate, post_weight and post_bias", "belong to a branch y");
+        return nullptr;
+    }
+    struct Small {
+        const char *name;
+        PyObject *of;
+        bool of_samples;
+        float **to;
+        Tensor grad;
+    } small[7] = {{"dgate", v[4], true, &a.dgate, {}},           {"dscale", v[5], true, &a.dscale, {}},
+                  {"dshift", v[6], true, &a.dshift, {}},         {"dpost_weight", v[10], false, &a.dpost_weight, {}},
+                  {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
+                  {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
+    Tensor dx, dy, work;
+    try {
+        const auto like = h->options().requires_grad(c10::nullopt);
+        dx = at::empty({m, d}, like);
+        if (v[1] != Py_None) dy = at::empty({m, d}, like);
+        int64_t rows = 0;
+        for (const Small &s : small) rows += s.of == Py_None ? 0 : s.of_samples ? batches : 1;
+        const Tensor all = at::empty({rows, d}, like.dtype(at::kFloat));
+        rows = 0;
+        for (Small &s : small) {
+            if (s.of == Py_None) continue;
+            s.grad = s.of_samples ? part_of(all, rows * d, {batches, d}) : part_of(all, rows * d, {d});
+            *s.to = static_cast<float *>(s.grad.data_ptr());
+            rows += s.of_samples ? batches : 1;
+        }
+        if (v[16] == Py_None) {
+            a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
+            work = at::empty({a.work_bytes}, like.dtype(at::kByte));
+            a.work = work.data_ptr();
+        }
+    } catch (const std::exception &e) {  // out of memory, for one
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
     a.h = mh.p;
     a.ldh = mh.ld;
     a.y = my.p;
@@ -344,18 +399,23 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
     a.ldgate = mg.ld;
     a.scale = mc.p;
     a.ldscale = mc.ld;
-    a.dx = mx.p;
-    a.lddx = mx.ld;
-    a.dy = mdy.p;
-    a.lddy = mdy.ld;
-    a.dgate = static_cast<float *>(m_dg.p);
-    a.dscale = static_cast<float *>(m_dc.p);
-    a.dshift = static_cast<float *>(m_df.p);
-    a.dpost_weight = static_cast<float *>(const_cast<void *>(g[0]));
-    a.dpost_bias = static_cast<float *>(const_cast<void *>(g[1]));
-    a.dpre_weight = static_cast<float *>(const_cast<void *>(g[2]));
-    a.dpre_bias = static_cast<float *>(const_cast<void *>(g[3]));
-    return status(convrot_gated_norm_backward(&a, stream));
+    a.dx = dx.data_ptr();
+    a.lddx = d;
+    a.dy = dy.defined() ? dy.data_ptr() : nullptr;
+    a.lddy = d;
+    const convrot_status st = convrot_gated_norm_backward(&a, stream);
+    if (st != CONVROT_OK) return status(st);
+    PyObject *dict = PyDict_New();
+    auto put = [&](const char *name, const Tensor &grad) {
+        PyObject *o = grad.defined() ? THPVariable_Wrap(grad) : Py_NewRef(Py_None);
+        const bool ok = o && PyDict_SetItemString(dict, name, o) == 0;
+        Py_XDECREF(o);
+        return ok;
+    };
+    bool ok = dict && put("dx", dx) && put("dy", dy);
+    for (const Small &s : small) ok = ok && put(s.name, s.grad);
+    if (!ok) Py_CLEAR(dict);
+    return dict;
 }
 
 // A [batch, tokens, heads, head_dim] tensor like `like` but for its heads.
