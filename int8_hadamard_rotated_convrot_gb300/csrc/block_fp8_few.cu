@@ -34,7 +34,6 @@ constexpr int kXWarps = 8;       // that prepare x
 constexpr int kThreads = 64 + 32 * kXWarps;
 constexpr int kMaxBlocks = 32;   // a CTA's share of k: 512 columns of tensor memory / 16
 constexpr int kMaxSplit = 8;     // CTAs of a cluster
-constexpr int kStaticBytes = 1024 + 2048;  // the system's shared memory and the scales, at least
 
 struct FewParams {
     int32_t m, n, k, blocks, split;
@@ -361,10 +360,11 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_
     while (static_cast<int>(p.tmem_cols) < share * kTok) p.tmem_cols *= 2;
     // An allocation of tensor memory waits until there is room, and CTAs of two clusters that wait for each other's
     // room on two SMs would wait for ever. So a CTA takes at least the part of an SM's shared memory (228 KB) that it
-    // takes of its 512 columns: what fits side by side has its columns, whichever launches it comes from.
+    // takes of its 512 columns, less 4 KB: of such CTAs, each of 64 KB at least and of a multiple of 32 columns, three
+    // at most fit side by side, and their columns would need 544 x 456 B - 3 x 4 KB > 228 KB to be too many.
     int bytes = 1024 + kStages * kStageBytes + share * kTok * kBK;
-    const int part = static_cast<int>(p.tmem_cols) * (228 * 1024 / 512);
-    if (bytes < part - kStaticBytes) bytes = part - kStaticBytes;
+    const int part = static_cast<int>(p.tmem_cols) * (228 * 1024 / 512) - 4096;
+    if (bytes < part) bytes = part;
     auto kernel = fp8_few_kernel<kTok, TX, T, kAct>;
     cudaError_t e = allow_shared<kernel_tag<kTok, TX, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
