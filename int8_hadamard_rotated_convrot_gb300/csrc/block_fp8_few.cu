@@ -1,21 +1,22 @@
-// The block-scaled linear for few rows (include/convrot_block.h): at most 64,
-// where reading the weights once is all the work.
+// The block-scaled linear for few rows (include/convrot_block.h), where reading
+// the weights and the latency of it all count, not the arithmetic.
 //
-// The weights are the MMA's M side: a CTA takes 128 rows of w and all rows of
-// x as the N side (16, 32 or 64 columns), so no tensor-core row is wasted and
-// an accumulator of one block of 128 features is 16 to 64 columns of tensor
-// memory. k is split over a cluster of up to eight CTAs, so that a projection
-// of a few thousand rows fills the GPU; their partial sums meet in distributed
-// shared memory, added in a fixed order. Every block of k has its accumulator
-// (at most 512 columns for a CTA's share), so nothing waits for a drain.
+// The weights are the MMA's M side: a CTA takes 128 rows of w and 16, 32 or 64
+// rows of x as the N side, so no tensor-core row is wasted and the accumulator
+// of one block of 128 features is 16 to 64 columns of tensor memory, four to
+// eight of them in turn. k is split over a cluster of up to eight CTAs, so that
+// a projection of a few thousand rows fills the GPU; their partial sums meet in
+// distributed shared memory, added in a fixed order.
 //
-//   warp 0      TMA producer: 16 KB of w a block into a ring of kStages
+//   warp 0      TMA producer: a block of w (16 KB), and of packed x, a stage
 //   warp 1      tensor memory; one thread issues the MMAs
 //   warps 2-9   quantize x (kQuantize: at most 16 rows; a call is one launch)
 //   warps 2-5   drain: lane = row of w, 16 to 64 sums in registers
 //
-// Bound: the weights' bytes over HBM (or L2, where they stay there between
-// calls), and the latency of one launch.
+// Bound by the weights' bytes over HBM (or L2, where they stay there between
+// calls) and by its own start and end: at M1 K5120 N5120, weights in L2, the
+// first block arrives after 2 us, the ten blocks of a CTA take 3.4 us (7.7
+// TB/s), the cluster's sums 0.6 us; 9.1 us a call with the launch.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -32,11 +33,17 @@ constexpr int kBK = 128, kBM = 128, kMmaK = 32;
 constexpr int kStages = 4, kStageBytes = kBM * kBK;
 constexpr int kXWarps = 8;       // that prepare x
 constexpr int kThreads = 64 + 32 * kXWarps;
-constexpr int kMaxBlocks = 32;   // a CTA's share of k: 512 columns of tensor memory / 16
+constexpr int kMaxShare = 128;   // blocks of k a CTA takes: their scales are in shared memory
+constexpr int kMaxQuantize = 32; // where it quantizes x: the codes of all its blocks are, too
 constexpr int kMaxSplit = 8;     // CTAs of a cluster
+// Blocks of rows that a CTA quantizes at most, two rounds of its eight warps; above, a launch of its own (2.4 us) is
+// cheaper (M8 K5120 N13824, 160 of them: 22.6 us in one launch, 15.2 in two).
+constexpr int kQuantizeUnits = 64;
 
 struct FewParams {
     int32_t m, n, k, blocks, split;
+    int32_t groups;       // of kTok rows of x
+    int32_t share;        // blocks of k a CTA takes at most
     const void *x;        // kQuantize: the rows
     int64_t ldx;
     int32_t wide_x;       // its rows can be read 4 elements at a time
@@ -47,7 +54,6 @@ struct FewParams {
     void *y;
     int64_t ldy;
     int32_t *dev_status;
-    uint32_t tmem_cols;
 };
 
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
@@ -81,34 +87,45 @@ __device__ __forceinline__ float remote_f32(uint32_t local, uint32_t rank)
     return v;
 }
 
+template <int kTok, bool kQuantize>
+struct Shape {
+    static constexpr int TILE = kTok * kBK;  // x's codes of one block
+    static constexpr int STAGE = kStageBytes + (kQuantize ? 0 : TILE);
+    static constexpr int COLS = kTok == 16 ? 128 : 256, BUFS = COLS / kTok;
+};
+
 // kTok: columns of an accumulator (rows of x, rounded up); TX: type of the rows
 // that are quantized here (void: x is packed); T: type of y.
 template <int kTok, typename TX, typename T, int kAct>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ FewParams p)
 {
     constexpr bool kQuantize = !std::is_void_v<TX>;
-    constexpr int kTile = kTok * kBK;  // x's codes of one block
+    using S = Shape<kTok, kQuantize>;
     // kind::f8f6f4: D fp32, A and B e4m3, K-major, M = 128, N = kTok
     constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(kTok >> 3) << 17) | (uint32_t(kBM >> 4) << 24);
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * kMaxBlocks + 1];
-    __shared__ __align__(16) float scales[512];  // [block][row of x]: s_x s_w
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 2 * S::BUFS + (kQuantize ? kMaxQuantize : 0) + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int abort_flag;
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
-    const uint32_t xtiles = base + kStages * kStageBytes;
+    const uint32_t xtiles = base + kStages * S::STAGE;  // kQuantize: x's codes of every block
+    // [block][row of x]: s_x s_w
+    float *scales = reinterpret_cast<float *>(smem_raw + (xtiles - raw) + (kQuantize ? p.share * S::TILE : 0));
     const uint32_t bar0 = static_cast<uint32_t>(__cvta_generic_to_shared(bars));
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kStages + s); };
-    auto x_bar = [&](int j) { return bar0 + 8u * (2 * kStages + j); };                  // x's codes of the block are there
-    auto sum_bar = [&](int j) { return bar0 + 8u * (2 * kStages + kMaxBlocks + j); };   // the block's sums are
-    const uint32_t done_bar = bar0 + 8u * (2 * kStages + 2 * kMaxBlocks);
+    auto sum_bar = [&](int b) { return bar0 + 8u * (2 * kStages + b); };              // an accumulator is finished
+    auto drained_bar = [&](int b) { return bar0 + 8u * (2 * kStages + S::BUFS + b); };  // and free again
+    const uint32_t done_bar = bar0 + 8u * (2 * kStages + 2 * S::BUFS);
+    auto x_bar = [&](int j) { return done_bar + 8u * (1 + j); };                      // kQuantize: x's codes of the block are there
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t split = static_cast<uint32_t>(p.split), rank = split > 1 ? cluster_rank() : 0;
-    const int tile = static_cast<int>(blockIdx.x / split);
+    const uint32_t unit = blockIdx.x / split, groups = static_cast<uint32_t>(p.groups);
+    const int tile = static_cast<int>(unit / groups), row0 = static_cast<int>(unit % groups) * kTok;
+    const int m = p.m - row0 < kTok ? p.m - row0 : kTok;  // this CTA's rows of x
     const int j0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / split);
     const int count = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / split) - j0;
 
@@ -117,10 +134,12 @@ __global__ void __launch_bounds__(kThreads)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int j = 0; j < count; ++j) {
-            mbar_init(x_bar(j), kQuantize ? kXWarps : 1);
-            mbar_init(sum_bar(j), 1);
+        for (int b = 0; b < S::BUFS; ++b) {
+            mbar_init(sum_bar(b), 1);
+            mbar_init(drained_bar(b), 4);
         }
+        if constexpr (kQuantize)
+            for (int j = 0; j < count; ++j) mbar_init(x_bar(j), kXWarps);
         mbar_init(done_bar, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -130,7 +149,7 @@ __global__ void __launch_bounds__(kThreads)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          static_cast<uint32_t>(__cvta_generic_to_shared(&tmem_slot))),
-                     "r"(p.tmem_cols)
+                     "r"(static_cast<uint32_t>(S::COLS))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -159,28 +178,22 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) {
             bool ok = true;
             int issued = 0;
-            if constexpr (!kQuantize) {
-                for (int j = 0; j < count; ++j) {  // all of this CTA's x at once
-                    mbar_arrive_expect_tx(x_bar(j), kTile);
-                    tma_load_2d(xtiles + j * kTile, &tmX, (j0 + j) * kBK, 0, x_bar(j));
-                }
-            }
             for (int j = 0; j < count; ++j) {
                 const int s = j % kStages;
                 if (!wait(empty_bar(s), (j / kStages + 1) & 1)) {
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(full_bar(s), kStageBytes);
-                tma_load_2d(base + s * kStageBytes, &tmW, (j0 + j) * kBK, tile * kBM, full_bar(s));
+                const uint32_t sa = base + s * S::STAGE;
+                mbar_arrive_expect_tx(full_bar(s), S::STAGE);
+                tma_load_2d(sa, &tmW, (j0 + j) * kBK, tile * kBM, full_bar(s));
+                if constexpr (!kQuantize) tma_load_2d(sa + kStageBytes, &tmX, (j0 + j) * kBK, row0, full_bar(s));
                 ++issued;
             }
             if (!ok) {
                 fail();
                 // copies in flight land before shared memory goes away
                 for (int j = issued > kStages ? issued - kStages : 0; j < issued; ++j) mbar_wait(full_bar(j % kStages), (j / kStages) & 1);
-                if constexpr (!kQuantize)
-                    for (int j = 0; j < count; ++j) mbar_wait(x_bar(j), 0);
             }
         }
         __syncwarp();
@@ -188,18 +201,20 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) {
             bool ok = true;
             for (int j = 0; j < count; ++j) {
-                const int s = j % kStages;
-                if (!wait(x_bar(j), 0) || !wait(full_bar(s), (j / kStages) & 1)) {
+                const int s = j % kStages, buf = j % S::BUFS;
+                if (kQuantize && !wait(x_bar(j), 0)) ok = false;
+                if (!ok || !wait(drained_bar(buf), (j / S::BUFS + 1) & 1) || !wait(full_bar(s), (j / kStages) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t da = smem_desc(base + s * kStageBytes), db = smem_desc(xtiles + j * kTile);
+                const uint32_t sa = base + s * S::STAGE;
+                const uint64_t da = smem_desc(sa), db = smem_desc(kQuantize ? xtiles + j * S::TILE : sa + kStageBytes);
 #pragma unroll
                 for (int kk = 0; kk < kBK / kMmaK; ++kk)  // 32 bytes along K inside the swizzle span
-                    mma(tmem + j * kTok, da + 2u * kk, db + 2u * kk, kIdesc, kk > 0 ? 1u : 0u);
+                    mma(tmem + buf * kTok, da + 2u * kk, db + 2u * kk, kIdesc, kk > 0 ? 1u : 0u);
                 mma_commit(empty_bar(s));
-                mma_commit(sum_bar(j));
+                mma_commit(sum_bar(buf));
             }
             if (!ok) fail();
             mma_commit(done_bar);
@@ -213,13 +228,13 @@ __global__ void __launch_bounds__(kThreads)
             // A row's block is a warp's at a time, four values a lane; kBatch of them are loaded together. Codes go to
             // the layout that the MMA reads (16-byte chunk c of row r at c ^ (r & 7)).
             constexpr int kBatch = 4;
-            const int units = count * p.m;
+            const int units = count * m;
             int arrived = 0;  // blocks that this warp has nothing left to add to
             for (int u0 = w; u0 - w < units || arrived < count; u0 += kXWarps * kBatch) {
                 float v[kBatch][4], sw_j[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int u = u0 + i * kXWarps, j = u / p.m, r = u - j * p.m, c = (j0 + j) * kBK + lane * 4;
+                    const int u = u0 + i * kXWarps, j = u / m, r = u - j * m, c = (j0 + j) * kBK + lane * 4;
                     if (u >= units) break;
                     const TX *from = static_cast<const TX *>(p.x) + r * p.ldx + c;
                     sw_j[i] = __ldg(sw + j);
@@ -234,20 +249,20 @@ __global__ void __launch_bounds__(kThreads)
                 }
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int u = u0 + i * kXWarps, j = u / p.m, r = u - j * p.m;
+                    const int u = u0 + i * kXWarps, j = u / m, r = u - j * m;
                     if (u >= units) break;
                     float amax = fmaxf(fmaxf(fabsf(v[i][0]), fabsf(v[i][1])), fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     amax = fmaxf(amax, kFp8AmaxFloor);
                     const float up = fp8_up(amax);
-                    const uint32_t to = xtiles + j * kTile + r * kBK + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
+                    const uint32_t to = xtiles + j * S::TILE + r * kBK + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(e4m3x4(v[i][0] * up, v[i][1] * up, v[i][2] * up, v[i][3] * up))
                                  : "memory");
                     if (lane == 0) scales[j * kTok + r] = (amax / kFp8Max) * sw_j[i];
                 }
                 // blocks before the next batch's first are done as far as this warp goes
-                const int next = u0 + kXWarps * kBatch, until = next < units ? next / p.m : count;
+                const int next = u0 + kXWarps * kBatch, until = next < units ? next / m : count;
                 if (arrived < until) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read these bytes
                     __syncwarp();
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(kThreads)
         } else {
             for (int i = threadIdx.x - 64; i < count * kTok; i += 32 * kXWarps) {
                 const int j = i / kTok, r = i % kTok;
-                scales[i] = r < p.m ? __ldg(p.x_scale + (j0 + j) * p.ld_x_scale + r) * __ldg(sw + j) : 0.0f;
+                scales[i] = r < m ? __ldg(p.x_scale + (j0 + j) * p.ld_x_scale + row0 + r) * __ldg(sw + j) : 0.0f;
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kXWarps) : "memory");  // every row's scales, among these warps
@@ -270,16 +285,17 @@ __global__ void __launch_bounds__(kThreads)
             for (int i = 0; i < kTok; ++i) acc[i] = 0.0f;
             bool ok = true;
             for (int j = 0; j < count; ++j) {
-                if (!wait(sum_bar(j), 0)) {
+                const int buf = j % S::BUFS;
+                if (!wait(sum_bar(buf), (j / S::BUFS) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kTok; c += 16) {
-                    if (c >= p.m) break;
+                    if (c >= m) break;
                     uint32_t r[16];
-                    tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + j * kTok + c, r);
+                    tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kTok + c, r);
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const float4 s = *reinterpret_cast<const float4 *>(&scales[j * kTok + c + i]);
@@ -289,13 +305,16 @@ __global__ void __launch_bounds__(kThreads)
                         acc[c + i + 3] = fmaf(__uint_as_float(r[i + 3]), s.w, acc[c + i + 3]);
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(drained_bar(buf));
             }
             if (!ok) fail();
-            // this CTA's sums, [row of x][row of w], over the ring's first stages: the last MMA has read them (sum_bar)
+            // this CTA's sums, [row of x][row of w], over the ring's stages: the last MMA has read them (sum_bar)
             const uint32_t sums = base + (q * 32 + lane) * 4;
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
-                if (i < p.m && ok) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + i * kBM * 4), "f"(acc[i]) : "memory");
+                if (i < m && ok) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sums + i * kBM * 4), "f"(acc[i]) : "memory");
         }
     }
 
@@ -306,10 +325,10 @@ __global__ void __launch_bounds__(kThreads)
         __syncthreads();
     tc_fence_after();
     if (warp == 1) {
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(S::COLS)) : "memory");
     } else if (warp > 1) {
         // the cluster's warps share out the outputs, 32 rows of w of one row of x at a time
-        for (int u = static_cast<int>(rank) * kXWarps + warp - 2; u < p.m * 4; u += static_cast<int>(split) * kXWarps) {
+        for (int u = static_cast<int>(rank) * kXWarps + warp - 2; u < m * 4; u += static_cast<int>(split) * kXWarps) {
             const int r = u >> 2, o = (u & 3) * 32 + lane;
             const uint32_t at = base + (r * kBM + o) * 4;
             float v = 0.0f;
@@ -321,7 +340,7 @@ __global__ void __launch_bounds__(kThreads)
             const int64_t col = static_cast<int64_t>(tile) * kBM + o;
             if (col >= p.n) continue;
             if (p.bias) v += __ldg(p.bias + col);
-            static_cast<T *>(p.y)[r * p.ldy + col] = from_f32<T>(apply_act_t<kAct>(v));
+            static_cast<T *>(p.y)[(row0 + r) * p.ldy + col] = from_f32<T>(apply_act_t<kAct>(v));
         }
     }
     if (split > 1) cluster_sync();  // a CTA's sums stay until its peers have read them
@@ -330,23 +349,31 @@ __global__ void __launch_bounds__(kThreads)
 template <int kTok, typename TX, typename T, int kAct>
 struct kernel_tag;
 
+// How a call is cut: groups of tok rows of x, and CTAs that share k.
+struct Cut {
+    int tok = 0, groups = 0, split = 0, share = 0;
+};
+
 template <int kTok, typename TX, typename T, int kAct>
-cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_t stream)
+cudaError_t launch_form(const convrot_fp8_linear_args &a, const Cut &cut, cudaStream_t stream)
 {
+    constexpr bool kQuantize = !std::is_void_v<TX>;
+    using S = Shape<kTok, kQuantize>;
     CUtensorMap tmX{}, tmW;
     if (!make_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, a.n, a.k, a.ldw, kBK, kBM)) return cudaErrorInvalidValue;
-    if constexpr (std::is_void_v<TX>)
+    if constexpr (!kQuantize)
         if (!make_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.x, a.m, a.k, a.ldx, kBK, kTok)) return cudaErrorInvalidValue;
     FewParams p{};
     p.m = static_cast<int32_t>(a.m);
     p.n = static_cast<int32_t>(a.n);
     p.k = static_cast<int32_t>(a.k);
     p.blocks = static_cast<int32_t>((a.k + kBK - 1) / kBK);
-    p.split = split;
+    p.split = cut.split;
+    p.groups = cut.groups;
+    p.share = cut.share;
     p.x = a.x;
     p.ldx = a.ldx;
-    if constexpr (!std::is_void_v<TX>)
-        p.wide_x = aligned_to(a.x, 4 * sizeof(TX)) && (a.m <= 1 || a.ldx % 4 == 0);
+    if constexpr (kQuantize) p.wide_x = aligned_to(a.x, 4 * sizeof(TX)) && (a.m <= 1 || a.ldx % 4 == 0);
     p.x_scale = a.x_scale;
     p.ld_x_scale = a.ld_x_scale;
     p.w_scale = a.w_scale;
@@ -355,21 +382,18 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_
     p.y = a.y;
     p.ldy = a.ldy;
     p.dev_status = a.dev_status;
-    const int share = (p.blocks + split - 1) / split;
-    p.tmem_cols = 32;
-    while (static_cast<int>(p.tmem_cols) < share * kTok) p.tmem_cols *= 2;
     // An allocation of tensor memory waits until there is room, and CTAs of two clusters that wait for each other's
     // room on two SMs would wait for ever. So a CTA takes at least the part of an SM's shared memory (228 KB) that it
     // takes of its 512 columns, less 4 KB: of such CTAs, each of 64 KB at least and of a multiple of 32 columns, three
     // at most fit side by side, and their columns would need 544 x 456 B - 3 x 4 KB > 228 KB to be too many.
-    int bytes = 1024 + kStages * kStageBytes + share * kTok * kBK;
-    const int part = static_cast<int>(p.tmem_cols) * (228 * 1024 / 512) - 4096;
-    if (bytes < part) bytes = part;
+    int bytes = 1024 + kStages * S::STAGE + cut.share * (kQuantize ? S::TILE : 0) + cut.share * kTok * 4;
+    constexpr int kPart = S::COLS * (228 * 1024 / 512) - 4096;
+    if (bytes < kPart) bytes = kPart;
     auto kernel = fp8_few_kernel<kTok, TX, T, kAct>;
     cudaError_t e = allow_shared<kernel_tag<kTok, TX, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>((a.n + kBM - 1) / kBM * split));
+    config.gridDim = dim3(static_cast<unsigned>((a.n + kBM - 1) / kBM * cut.groups * cut.split));
     config.blockDim = dim3(kThreads);
     config.dynamicSmemBytes = bytes;
     config.stream = stream;
@@ -377,57 +401,75 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, int split, cudaStream_
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[0].val.programmaticStreamSerializationAllowed = 1;
     attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+    attrs[1].val.clusterDim = {static_cast<unsigned>(cut.split), 1, 1};
     config.attrs = attrs;
-    config.numAttrs = split > 1 ? 2 : 1;
+    config.numAttrs = cut.split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&config, kernel, tmX, tmW, p);
 }
 
-// CTAs that share k: the widest cluster (1, 2, 4 or 8) that still lets every CTA be resident, two an SM, and keeps
-// two blocks for each; more where a CTA's blocks would not have an accumulator each. 0: no split does.
-int choose_split(int64_t n, int64_t blocks, int tok)
+// CTAs that are resident together, two an SM: clusters of 4 and 8 leave some SMs of a GPC over (36 and 15 of them fit
+// at one CTA an SM).
+int resident(int split) { return split <= 2 ? 2 * kSms : split == 4 ? 2 * 36 * 4 : 2 * 15 * 8; }
+
+// The widest cluster (1, 2, 4 or 8) with which every CTA is still resident and has two blocks of k. Up to 64 rows
+// this kernel takes any call whose shares fit; more rows only where all groups of them are resident together.
+Cut cut_of(int64_t m, int64_t n, int64_t k)
 {
-    const int64_t tiles = (n + kBM - 1) / kBM;
-    const int64_t most = 512 / tok < kMaxBlocks ? 512 / tok : kMaxBlocks;
-    int split = 1;
-    while (split < kMaxSplit && ((tiles * 2 * split <= 2 * kSms && blocks >= 4 * split) || (blocks + split - 1) / split > most)) split *= 2;
-    return (blocks + split - 1) / split <= most ? split : 0;
+    const int64_t tiles = (n + kBM - 1) / kBM, blocks = (k + kBK - 1) / kBK;
+    Cut best;
+    for (int tok : {16, 32, 64}) {
+        if (tok == 16 && m > 16) continue;
+        Cut c;
+        c.tok = tok;
+        c.groups = static_cast<int>((m + tok - 1) / tok);
+        const int64_t units = c.groups * tiles;
+        if (c.groups > 1 && units > resident(1)) continue;
+        c.split = 1;
+        while (c.split < kMaxSplit &&
+               ((units * 2 * c.split <= resident(2 * c.split) && blocks >= 4 * c.split) || (blocks + c.split - 1) / c.split > kMaxShare))
+            c.split *= 2;
+        c.share = static_cast<int>((blocks + c.split - 1) / c.split);
+        if (c.share > kMaxShare) continue;
+        // a CTA's time is that of its blocks, the wider ones a little longer
+        if (!best.tok || c.share * (64 + c.tok) < best.share * (64 + best.tok)) best = c;
+        if (m <= tok) break;
+    }
+    return best;
 }
 
 template <int kTok, typename TX>
-cudaError_t launch_types(const convrot_fp8_linear_args &a, int split, cudaStream_t stream)
+cudaError_t launch_types(const convrot_fp8_linear_args &a, const Cut &cut, cudaStream_t stream)
 {
     return with_dtype(a.y_dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
-        if (a.act == CONVROT_ACT_GELU_ERF) return launch_form<kTok, TX, T, 1>(a, split, stream);
-        if (a.act == CONVROT_ACT_GELU_TANH) return launch_form<kTok, TX, T, 2>(a, split, stream);
-        return launch_form<kTok, TX, T, 0>(a, split, stream);
+        if (a.act == CONVROT_ACT_GELU_ERF) return launch_form<kTok, TX, T, 1>(a, cut, stream);
+        if (a.act == CONVROT_ACT_GELU_TANH) return launch_form<kTok, TX, T, 2>(a, cut, stream);
+        return launch_form<kTok, TX, T, 0>(a, cut, stream);
     });
 }
 
-int tokens_of(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 64; }
-
 }  // namespace
 
-bool fp8_few_takes(int64_t m, int64_t n, int64_t k)
-{
-    return m <= 64 && choose_split(n, (k + kBK - 1) / kBK, tokens_of(m)) > 0;
-}
+bool fp8_few_takes(int64_t m, int64_t n, int64_t k) { return cut_of(m, n, k).tok > 0; }
 
-bool fp8_few_quantizes(int64_t m, int64_t n, int64_t k) { return m <= 16 && fp8_few_takes(m, n, k); }
+bool fp8_few_quantizes(int64_t m, int64_t n, int64_t k)
+{
+    const Cut c = cut_of(m, n, k);
+    return c.tok == 16 && c.share <= kMaxQuantize && c.share * m <= kQuantizeUnits;
+}
 
 cudaError_t launch_fp8_few(const convrot_fp8_linear_args &a, cudaStream_t stream)
 {
-    const int tok = tokens_of(a.m), split = choose_split(a.n, (a.k + kBK - 1) / kBK, tok);
-    if (tok == 16) return launch_types<16, void>(a, split, stream);
-    if (tok == 32) return launch_types<32, void>(a, split, stream);
-    return launch_types<64, void>(a, split, stream);
+    const Cut c = cut_of(a.m, a.n, a.k);
+    if (c.tok == 16) return launch_types<16, void>(a, c, stream);
+    if (c.tok == 32) return launch_types<32, void>(a, c, stream);
+    return launch_types<64, void>(a, c, stream);
 }
 
 cudaError_t launch_fp8_few_quantize(const convrot_fp8_linear_args &a, cudaStream_t stream)
 {
-    const int split = choose_split(a.n, (a.k + kBK - 1) / kBK, 16);
-    return with_dtype(a.x_dtype, [&](auto *tag) { return launch_types<16, std::remove_pointer_t<decltype(tag)>>(a, split, stream); });
+    const Cut c = cut_of(a.m, a.n, a.k);
+    return with_dtype(a.x_dtype, [&](auto *tag) { return launch_types<16, std::remove_pointer_t<decltype(tag)>>(a, c, stream); });
 }
 
 }  // namespace convrot
