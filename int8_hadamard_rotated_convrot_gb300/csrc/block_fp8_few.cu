@@ -53,6 +53,7 @@ struct FewParams {
     int64_t ld_w_scale;
     void *y;
     int64_t ldy;
+    int32_t vec_y;        // four elements of a row of y are aligned to their size
     int32_t *dev_status;
 };
 
@@ -78,12 +79,12 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float remote_f32(uint32_t local, uint32_t rank)
+__device__ __forceinline__ float4 remote16(uint32_t local, uint32_t rank)
 {
     uint32_t at;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 
@@ -327,20 +328,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == 1) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(S::COLS)) : "memory");
     } else if (warp > 1) {
-        // the cluster's warps share out the outputs, 32 rows of w of one row of x at a time
-        for (int u = static_cast<int>(rank) * kXWarps + warp - 2; u < m * 4; u += static_cast<int>(split) * kXWarps) {
-            const int r = u >> 2, o = (u & 3) * 32 + lane;
-            const uint32_t at = base + (r * kBM + o) * 4;
-            float v = 0.0f;
-            if (split > 1) {
-                for (uint32_t c = 0; c < split; ++c) v += remote_f32(at, c);
-            } else {
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+        // the cluster's warps share out the rows of x, four columns of y a lane; a row's partial sums are all in flight
+        const int64_t col = static_cast<int64_t>(tile) * kBM + lane * 4;
+        float bias[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[e] = p.bias && col + e < p.n ? __ldg(p.bias + col + e) : 0.0f;
+        for (int r = static_cast<int>(rank) * kXWarps + warp - 2; r < m; r += static_cast<int>(split) * kXWarps) {
+            const uint32_t at = base + (r * kBM + lane * 4) * 4;
+            float4 part[kMaxSplit];
+#pragma unroll
+            for (uint32_t c = 0; c < kMaxSplit; ++c)
+                if (c < split) part[c] = remote16(at, split > 1 ? c : 0);
+            float v[4] = {};
+#pragma unroll
+            for (uint32_t c = 0; c < kMaxSplit; ++c) {
+                if (c >= split) break;
+                v[0] += part[c].x;
+                v[1] += part[c].y;
+                v[2] += part[c].z;
+                v[3] += part[c].w;
             }
-            const int64_t col = static_cast<int64_t>(tile) * kBM + o;
-            if (col >= p.n) continue;
-            if (p.bias) v += __ldg(p.bias + col);
-            static_cast<T *>(p.y)[(row0 + r) * p.ldy + col] = from_f32<T>(apply_act_t<kAct>(v));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = apply_act_t<kAct>(v[e] + bias[e]);
+            T *y = static_cast<T *>(p.y) + (row0 + r) * p.ldy + col;
+            if (p.vec_y && col + 4 <= p.n) {
+                Raw<T, 4> raw;
+                raw.pack(v);
+                raw.store(y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < p.n) y[e] = from_f32<T>(v[e]);
+            }
         }
     }
     if (split > 1) cluster_sync();  // a CTA's sums stay until its peers have read them
@@ -381,6 +400,7 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, const Cut &cut, cudaSt
     p.bias = a.bias;
     p.y = a.y;
     p.ldy = a.ldy;
+    p.vec_y = aligned_to(a.y, 4 * sizeof(T)) && (a.m <= 1 || a.ldy % 4 == 0);
     p.dev_status = a.dev_status;
     // An allocation of tensor memory waits until there is room, and CTAs of two clusters that wait for each other's
     // room on two SMs would wait for ever. So a CTA takes at least the part of an SM's shared memory (228 KB) that it

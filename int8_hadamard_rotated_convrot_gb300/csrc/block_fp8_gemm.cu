@@ -474,9 +474,13 @@ cudaError_t launch_fp8_gemm(const convrot_fp8_linear_args &a, cudaStream_t strea
 {
     return with_dtype(a.y_dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
-        // 256 columns a tile where that gives every pair of SMs one, 128 where it would leave some without
-        const int64_t tiles = (a.m + 255) / 256 * ((a.n + 255) / 256);
-        const bool wide = tiles >= kSms / 2;
+        // Tiles of 256 or 128 columns, by the rounds that the 76 pairs take over them: a block of k costs 0.59 us in a
+        // wide tile and 0.48 us in a narrow one (M32760 K5120 N13824 and M256 K5120 N13824), so narrow ones pay only
+        // where they save a round in five or spread a lone round over idle pairs.
+        const int64_t rows = (a.m + 255) / 256, pairs = kSms / 2;
+        const int64_t rounds_wide = (rows * ((a.n + 255) / 256) + pairs - 1) / pairs;
+        const int64_t rounds_narrow = (rows * ((a.n + 127) / 128) + pairs - 1) / pairs;
+        const bool wide = rounds_wide * 59 <= rounds_narrow * 48;
         if (a.act == CONVROT_ACT_GELU_ERF) return wide ? launch_pair<256, T, 1>(a, stream) : launch_pair<128, T, 1>(a, stream);
         if (a.act == CONVROT_ACT_GELU_TANH) return wide ? launch_pair<256, T, 2>(a, stream) : launch_pair<128, T, 2>(a, stream);
         return wide ? launch_pair<256, T, 0>(a, stream) : launch_pair<128, T, 0>(a, stream);
