@@ -149,6 +149,7 @@ __device__ __forceinline__ void pack_row(const convrot_gated_norm_args &a, int64
 __device__ __forceinline__ uint32_t sample_rows(int64_t rows) { return rows < 0x7fffffff ? static_cast<uint32_t>(rows) : 0x7fffffffu; }
 
 constexpr int kRingThreads = 640;  // 96 registers a thread, so that 640 threads share an SM
+constexpr int kRingStages = 3;
 constexpr int kRowThreads = 512;  // 128 registers a thread: up to 32 values of a row in each
 
 template <typename T, typename P, int kVec, int kNv, bool kWarp>
@@ -295,21 +296,24 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
     }
 }
 
-// The same for many rows: each block takes a run of them, and each thread
-// copies its own 16-byte pieces of the next rows into its own places in shared
-// memory (cp.async), kStages - 1 rows ahead. What a thread copied it reads back
-// itself, so the ring needs no barrier, and HBM stays busy through the sums
-// around the block. Per row the instructions count as much as the bytes (44 a
-// value are what HBM's rate leaves), so everything that a sample's rows share
-// is prepared once, in registers: gate w_post, (1 + scale) w_pre and (1 +
-// scale) b_pre + shift; pieces past the row are zeros and need no branch.
-template <typename T, typename P, int kNv, int kStages, bool kBranch>
+// The same for many rows: each block takes a run of them. Per row the
+// instructions count as much as the bytes (44 a value are what HBM's rate
+// leaves), so everything that a sample's rows share is prepared once, in
+// registers: gate w_post, (1 + scale) w_pre and (1 + scale) b_pre + shift;
+// values past the row are zeros and need no branch.
+// kWide: each thread copies its own 16-byte pieces of the next rows into its
+// own places in shared memory (cp.async), kStages - 1 rows ahead. What a thread
+// copied it reads back itself, so the ring needs no barrier, and HBM stays busy
+// through the sums around the block. Otherwise single elements, kThreads apart,
+// the next row's loaded into registers before this one's sums.
+template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
 __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const __grid_constant__ convrot_gated_norm_args a, int32_t rows)
 {
-    constexpr int kVec = 16 / sizeof(T), kPieces = kNv * (kBranch ? 2 : 1), kPairs = kNv * kVec / 2, kHalf = kVec / 2;
-    extern __shared__ uint4 ring[];  // [kStages][x, y][kNv][blockDim]
+    constexpr int kVec = kWide ? 16 / static_cast<int>(sizeof(T)) : 1;
+    constexpr int kStages = kRingStages, kPieces = kNv * (kBranch ? 2 : 1), kValues = kNv * kVec, kPairs = kValues / 2;
+    extern __shared__ uint4 ring[];  // kWide: [kStages][x, y][kNv][blockDim]
     __shared__ float2 slots[64];
-    const int nt = blockDim.x, d = static_cast<int>(a.d);
+    const int nt = kThreads ? kThreads : blockDim.x, d = static_cast<int>(a.d);
     const float inv_d = 1.0f / d;
     RowSum<false> sum{slots};
     const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
@@ -318,60 +322,67 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
     const int count = static_cast<int>(a.m - first < rows ? a.m - first : rows);
     const int pitch = nt * kVec, col = static_cast<int>(threadIdx.x) * kVec;  // piece j: columns col + j pitch on
     bool inside[kNv];
-    uint32_t bytes[kNv];
 #pragma unroll
-    for (int j = 0; j < kNv; ++j) {
-        inside[j] = col + j * pitch < d;
-        bytes[j] = inside[j] ? 16 : 0;
-    }
-    // (a piece past the row reads nothing, but its address stays inside)
+    for (int j = 0; j < kNv; ++j) inside[j] = col + j * pitch < d;
     const T *x = static_cast<const T *>(a.x) + first * a.ldx, *y = static_cast<const T *>(a.y) + first * a.ldy;
     T *h_out = static_cast<T *>(a.h) + first * a.ldh + col, *n_out = static_cast<T *>(a.n) + first * a.ldn + col;
+    T ahead_x[kWide ? 1 : kNv], ahead_y[kWide || !kBranch ? 1 : kNv];
     auto fetch = [&](uint32_t to) {
 #pragma unroll
         for (int j = 0; j < kNv; ++j) {
-            copy16(to + j * step, x + (inside[j] ? col + j * pitch : 0), bytes[j]);
-            if constexpr (kBranch) copy16(to + (kNv + j) * step, y + (inside[j] ? col + j * pitch : 0), bytes[j]);
+            if constexpr (kWide) {
+                // (a piece past the row reads nothing, but its address stays inside)
+                const int at = inside[j] ? col + j * pitch : 0;
+                const uint32_t bytes = inside[j] ? 16 : 0;
+                copy16(to + j * step, x + at, bytes);
+                if constexpr (kBranch) copy16(to + (kNv + j) * step, y + at, bytes);
+            } else {
+                ahead_x[j] = inside[j] ? x[col + j * pitch] : from_f32<T>(0.0f);
+                if constexpr (kBranch) ahead_y[j] = inside[j] ? y[col + j * pitch] : from_f32<T>(0.0f);
+            }
         }
         x += a.ldx;
         if constexpr (kBranch) y += a.ldy;
     };
+    if constexpr (kWide) {
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (s < count) fetch(mine + s * stage_bytes);
-        copy_commit();
+        for (int s = 0; s < kStages - 1; ++s) {
+            if (s < count) fetch(mine + s * stage_bytes);
+            copy_commit();
+        }
+    } else if (count > 0) {
+        fetch(0);
     }
     uint32_t sample = static_cast<uint32_t>(first) / sample_rows(a.rows_per_batch);
     int64_t left = (sample + 1ll) * a.rows_per_batch - first;  // rows of this sample
-    F2 w_post[kPairs], w_pre[kPairs], b_pre[kPairs];
-    auto prepare = [&]() {
-        auto vec = [&](const void *p, int64_t offset, float otherwise, float (&v)[kVec], int j) {
-            if (inside[j]) {
-                params<P>(p, offset + col + j * pitch, otherwise, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[e] = 0.0f;
-            }
-        };
+    // kValues of a vector of columns, or `otherwise`; 0 past the row
+    auto vector = [&](const void *p, int64_t offset, float otherwise, float (&v)[kValues]) {
 #pragma unroll
         for (int j = 0; j < kNv; ++j) {
-            float u[kVec], v[kVec], w[kVec];
-            vec(a.gate, sample * a.ldgate, 1.0f, u, j);
-            vec(a.post_weight, 0, 1.0f, v, j);
+            float piece[kVec] = {};
+            if (inside[j]) params<P>(p, offset + col + j * pitch, otherwise, piece);
 #pragma unroll
-            for (int e = 0; e < kHalf; ++e) w_post[j * kHalf + e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
-            vec(a.scale, sample * a.ldscale, 0.0f, u, j);
-            vec(a.pre_weight, 0, 1.0f, v, j);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) u[e] += 1.0f;
-#pragma unroll
-            for (int e = 0; e < kHalf; ++e) w_pre[j * kHalf + e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
-            vec(a.pre_bias, 0, 0.0f, v, j);
-            vec(a.shift, sample * a.ldshift, 0.0f, w, j);
-#pragma unroll
-            for (int e = 0; e < kHalf; ++e)
-                b_pre[j * kHalf + e] = F2(fmaf(u[2 * e], v[2 * e], w[2 * e]), fmaf(u[2 * e + 1], v[2 * e + 1], w[2 * e + 1]));
+            for (int e = 0; e < kVec; ++e) v[j * kVec + e] = piece[e];
         }
+    };
+    F2 w_post[kPairs], w_pre[kPairs], b_pre[kPairs];
+    auto prepare = [&]() {
+        float u[kValues], v[kValues], w[kValues];
+        vector(a.gate, sample * a.ldgate, 1.0f, u);
+        vector(a.post_weight, 0, 1.0f, v);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) w_post[e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
+        vector(a.scale, sample * a.ldscale, 0.0f, u);
+        vector(a.pre_weight, 0, 1.0f, v);
+#pragma unroll
+        for (int e = 0; e < kValues; ++e) u[e] += 1.0f;
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) w_pre[e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
+        vector(a.pre_bias, 0, 0.0f, v);
+        vector(a.shift, sample * a.ldshift, 0.0f, w);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e)
+            b_pre[e] = F2(fmaf(u[2 * e], v[2 * e], w[2 * e]), fmaf(u[2 * e + 1], v[2 * e + 1], w[2 * e + 1]));
     };
     F2 h[kPairs];
     // mean out of h (layer norm), then 1 / deviation
@@ -382,11 +393,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
             for (int e = 1; e < kPairs; ++e) s = s + h[e];
             const float mean = -sum(s.sum()) * inv_d;
 #pragma unroll
-            for (int j = 0; j < kNv; ++j) {
-                const F2 m(inside[j] ? mean : 0.0f);
-#pragma unroll
-                for (int e = 0; e < kHalf; ++e) h[j * kHalf + e] = h[j * kHalf + e] + m;
-            }
+            for (int e = 0; e < kPairs; ++e)
+                h[e] = h[e] + F2(inside[2 * e / kVec] ? mean : 0.0f, inside[(2 * e + 1) / kVec] ? mean : 0.0f);
         }
         F2 s = h[0] * h[0];
 #pragma unroll
@@ -398,18 +406,38 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
     bool fresh = true;
     for (int r = 0; r < count; ++r) {
         if (fresh) prepare();
-        if (r + kStages - 1 < count) fetch(ahead);
-        copy_commit();
-        if ((ahead += stage_bytes) == ring_end) ahead = mine;
-        copy_wait<kStages - 1>();
-        auto piece = [&](int k, F2 *v) {
-            Raw<T, kVec> raw;
-            raw.bits[0] = shared16(stage + k * step);
-            raw.unpack(v);
+        T now_x[kWide ? 1 : kNv], now_y[kWide || !kBranch ? 1 : kNv];
+        if constexpr (kWide) {
+            if (r + kStages - 1 < count) fetch(ahead);
+            copy_commit();
+            if ((ahead += stage_bytes) == ring_end) ahead = mine;
+            copy_wait<kStages - 1>();
+        } else {
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) {
+                now_x[j] = ahead_x[j];
+                if constexpr (kBranch) now_y[j] = ahead_y[j];
+            }
+            if (r + 1 < count) fetch(0);
+        }
+        // this row's values of x (k = 0) or y (k = 1)
+        auto row = [&](int k, F2 (&v)[kPairs]) {
+            if constexpr (kWide) {
+#pragma unroll
+                for (int j = 0; j < kNv; ++j) {
+                    Raw<T, kVec> raw;
+                    raw.bits[0] = shared16(stage + (k * kNv + j) * step);
+                    raw.unpack(v + j * kVec / 2);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    v[e] = k ? F2(to_f32(now_y[kBranch ? 2 * e : 0]), to_f32(now_y[kBranch ? 2 * e + 1 : 0]))
+                             : F2(to_f32(now_x[2 * e]), to_f32(now_x[2 * e + 1]));
+            }
         };
         if constexpr (kBranch) {
-#pragma unroll
-            for (int j = 0; j < kNv; ++j) piece(kNv + j, h + j * kHalf);
+            row(1, h);
             if (a.post != CONVROT_NORM_NONE) {
                 const F2 inv(deviation(a.post));
 #pragma unroll
@@ -418,32 +446,30 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) h[e] = h[e] * w_post[e];
             if (a.post_bias) {
+                float u[kValues], v[kValues];
+                vector(a.gate, sample * a.ldgate, 1.0f, u);
+                vector(a.post_bias, 0, 0.0f, v);
 #pragma unroll
-                for (int j = 0; j < kNv; ++j) {
-                    if (!inside[j]) continue;
-                    float u[kVec], v[kVec];
-                    params<P>(a.gate, sample * a.ldgate + col + j * pitch, 1.0f, u);
-                    params<P>(a.post_bias, col + j * pitch, 0.0f, v);
-#pragma unroll
-                    for (int e = 0; e < kHalf; ++e)
-                        h[j * kHalf + e] = fma2(F2(u[2 * e], u[2 * e + 1]), F2(v[2 * e], v[2 * e + 1]), h[j * kHalf + e]);
-                }
+                for (int e = 0; e < kPairs; ++e) h[e] = fma2(F2(u[2 * e], u[2 * e + 1]), F2(v[2 * e], v[2 * e + 1]), h[e]);
             }
         }
-#pragma unroll
-        for (int j = 0; j < kNv; ++j) {
-            F2 xv[kHalf];
-            piece(j, xv);
+        {
+            F2 xv[kPairs];
+            row(0, xv);
             const F2 res(a.res_scale);
 #pragma unroll
-            for (int e = 0; e < kHalf; ++e) h[j * kHalf + e] = kBranch ? fma2(res, xv[e], h[j * kHalf + e]) : res * xv[e];
+            for (int e = 0; e < kPairs; ++e) h[e] = kBranch ? fma2(res, xv[e], h[e]) : res * xv[e];
         }
         auto put = [&](T *p) {
 #pragma unroll
             for (int j = 0; j < kNv; ++j) {
-                Raw<T, kVec> raw;
-                raw.pack(h + j * kHalf);
-                if (inside[j]) raw.store(p + j * pitch);
+                if constexpr (kWide) {
+                    Raw<T, kVec> raw;
+                    raw.pack(h + j * kVec / 2);
+                    if (inside[j]) raw.store_stream(p + j * pitch);
+                } else {
+                    if (inside[j]) p[j * pitch] = from_f32<T>(j % 2 ? h[j / 2].hi() : h[j / 2].lo());
+                }
             }
         };
         if (a.h) {
@@ -461,16 +487,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
             put(n_out);
             n_out += a.ldn;
         }
-        if (a.q) {
-            float v[kNv][kVec];
+        if constexpr (kWide) {
+            if (a.q) {
+                float v[kNv][kVec];
 #pragma unroll
-            for (int e = 0; e < kPairs; ++e) {
-                v[e / kHalf][e % kHalf * 2] = h[e].lo();
-                v[e / kHalf][e % kHalf * 2 + 1] = h[e].hi();
+                for (int e = 0; e < kPairs; ++e) {
+                    v[2 * e / kVec][2 * e % kVec] = h[e].lo();
+                    v[2 * e / kVec][2 * e % kVec + 1] = h[e].hi();
+                }
+                pack_row<kVec, kNv>(a, first + r, d, threadIdx.x, nt, v);
             }
-            pack_row<kVec, kNv>(a, first + r, d, threadIdx.x, nt, v);
+            if ((stage += stage_bytes) == ring_end) stage = mine;
         }
-        if ((stage += stage_bytes) == ring_end) stage = mine;
         fresh = --left == 0;
         if (fresh) {
             ++sample;
@@ -493,7 +521,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 //
 // One kernel does rows and sums: a unit (a block of threads, or a cluster of
 // them for wide rows) takes a run of rows of one sample, each thread the same
-// eight columns of every row, so the four sums of its columns stay in its
+// columns of every row, so the four sums of its columns stay in its
 // registers; they leave once per unit as a partial, and small kernels add the
 // partials up in a fixed order. Four reads and two writes of a value, each
 // tensor moved once.
@@ -507,8 +535,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 // goes along too. One trip for RMS norms, one more for the means of a layer
 // norm, and one more if post is one.
 
-constexpr int kGradCols = 8;           // columns a thread
-constexpr int kGradThreads = 640;      // of one block: 96 registers a thread
+// Columns a thread: 16 spread a row's trip around the block over twice the
+// values of 8 (146 against 166 us; M8190 D5120 in bf16, RMS norms).
+constexpr int kGradCols = 16;
+constexpr int kGradThreads = 320;      // of one block: 168 registers a thread
 constexpr int kGradWidth = kGradCols * kGradThreads;
 // How rows are split: the same on the host that sizes the workspace and at the launch.
 struct GradSplit {
@@ -523,7 +553,7 @@ struct GradSplit {
         threads = ((width + kGradCols - 1) / kGradCols + 31) / 32 * 32;
         batches = (m + rows - 1) / rows;
         // one wave of resident blocks, and no unit without a row
-        const int64_t resident = kSms * (threads >= kGradThreads ? 1 : kGradThreads / threads < 24 ? kGradThreads / threads : 24);
+        const int64_t resident = kSms * (threads >= kGradThreads ? 1 : kGradThreads / threads);
         const int64_t longest = rows < m ? rows : m;
         chunks = resident / cluster / batches;
         if (chunks > longest) chunks = longest;
@@ -604,7 +634,7 @@ struct GradSum {
     }
 };
 
-// Rows of the ring: 4 tensors of 16 bytes a thread and row (32 for 32-bit
+// Rows of the ring: 4 tensors of 32 bytes a thread and row (64 for 32-bit
 // types), 160 KB for the widest block.
 template <typename T>
 constexpr int grad_stages()
@@ -616,7 +646,7 @@ template <typename T, typename P, int kVec, int kCluster>
 __global__ void __launch_bounds__(kGradThreads, 1)
     norm_grad_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, const __grid_constant__ GradSplit split, float *part)
 {
-    // Eight columns a thread, in kNv pieces of kVec; four pairs of them for the packed arithmetic. 16-byte pieces
+    // kGradCols columns a thread, in kNv pieces of kVec, and in pairs for the packed arithmetic. 16-byte pieces
     // come through a ring of rows in shared memory that each thread fills for itself, single elements directly.
     constexpr int kNv = kGradCols / kVec, kPairs = kGradCols / 2, kStages = grad_stages<T>();
     constexpr bool kRing = kVec > 1;
@@ -971,25 +1001,24 @@ cudaError_t launch_block_rows(const convrot_gated_norm_args &a, cudaStream_t str
 
 constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; the rest stays L1 for the vectors
 
-template <typename T, typename P, int kNv, bool kBranch>
+template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
 struct ring_tag;
 
-// Runs of rows through the ring, if there are enough of them (eight a block, so
-// that filling the ring is a small part) and the ring fits.
-template <typename T, typename P, int kNv, bool kBranch>
+// Runs of rows, if there are enough of them: four a block, so that preparing the sample's vectors (and filling the
+// ring, which has to fit) is a small part.
+template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
 bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
 {
-    constexpr int kVec = 16 / sizeof(T), kStages = 4;
-    const int threads = static_cast<int>((a.d / kVec + kNv - 1) / kNv + 31) / 32 * 32;
-    const int bytes = kStages * (kBranch ? 2 : 1) * kNv * threads * 16;
-    int per_sm = kRingBytes / bytes;
-    const int by_threads = kRingThreads / threads;
-    if (per_sm > by_threads) per_sm = by_threads;
+    constexpr int kVec = kWide ? 16 / static_cast<int>(sizeof(T)) : 1;
+    const int threads = kThreads ? kThreads : static_cast<int>((a.d / kVec + kNv - 1) / kNv + 31) / 32 * 32;
+    const int bytes = kWide ? kRingStages * (kBranch ? 2 : 1) * kNv * threads * 16 : 0;
+    int per_sm = kRingThreads / threads;
+    if (kWide && kRingBytes / bytes < per_sm) per_sm = kRingBytes / bytes;
     if (per_sm < 1) return false;
     const int64_t blocks = static_cast<int64_t>(per_sm) * kSms;
-    if (a.m < 8 * blocks) return false;
-    auto kernel = gated_norm_ring_kernel<T, P, kNv, kStages, kBranch>;
-    *e = allow_shared<ring_tag<T, P, kNv, kBranch>>(kernel);
+    if (a.m < 4 * blocks) return false;
+    auto kernel = gated_norm_ring_kernel<T, P, kNv, kWide, kThreads, kBranch>;
+    *e = allow_shared<ring_tag<T, P, kNv, kWide, kThreads, kBranch>>(kernel);
     if (*e != cudaSuccess) return true;
     const int64_t rows = (a.m + blocks - 1) / blocks;
     kernel<<<static_cast<unsigned>((a.m + rows - 1) / rows), threads, bytes, stream>>>(a, static_cast<int32_t>(rows));
@@ -997,10 +1026,10 @@ bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaErro
     return true;
 }
 
-template <typename T, typename P, int kNv>
+template <typename T, typename P, int kNv, bool kWide, int kThreads = 0>
 bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
 {
-    return a.y ? launch_ring<T, P, kNv, true>(a, stream, e) : launch_ring<T, P, kNv, false>(a, stream, e);
+    return a.y ? launch_ring<T, P, kNv, kWide, kThreads, true>(a, stream, e) : launch_ring<T, P, kNv, kWide, kThreads, false>(a, stream, e);
 }
 
 // A warp for each row, four rows a block.
@@ -1029,13 +1058,28 @@ cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t str
         if (wide) {
             const int64_t n = a.d / kVec;
             cudaError_t e;
-            if (n > 256 ? launch_ring<T, P, 16 / kVec>(a, stream, &e) : launch_ring<T, P, 1>(a, stream, &e)) return e;
+            if (n > 256 ? launch_ring<T, P, 16 / kVec, true>(a, stream, &e) : launch_ring<T, P, 1, true>(a, stream, &e)) return e;
             if (n <= 32) return launch_warp_rows<T, P, kVec, 1>(a, stream);
             if (n <= kRowThreads) return launch_block_rows<T, P, kVec, 1>(a, stream);
             if (n <= 2 * kRowThreads) return launch_block_rows<T, P, kVec, 2>(a, stream);
             return launch_block_rows<T, P, kVec, 32 / kVec>(a, stream);
         }
         if (a.d <= 128) return launch_warp_rows<T, P, 1, 4>(a, stream);
+        cudaError_t e;
+        if (!a.q) {
+            bool done = false;
+            if (a.d <= 512)
+                done = launch_ring<T, P, 8, false, 64>(a, stream, &e);
+            else if (a.d <= 1024)
+                done = launch_ring<T, P, 8, false, 128>(a, stream, &e);
+            else if (a.d <= 1536)
+                done = launch_ring<T, P, 12, false, 128>(a, stream, &e);
+            else if (a.d <= 3072)
+                done = launch_ring<T, P, 12, false, 256>(a, stream, &e);
+            else if (a.d <= 6144)
+                done = launch_ring<T, P, 12, false, 512>(a, stream, &e);
+            if (done) return e;
+        }
         // single elements: blocks of 128 to 512 threads, enough values in each that the sums' cost is spread
         if (a.d <= 2048) return launch_block_rows<T, P, 1, 8>(a, stream);
         if (a.d <= 8192) return launch_block_rows<T, P, 1, 16>(a, stream);
