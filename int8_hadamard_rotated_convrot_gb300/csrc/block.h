@@ -238,6 +238,37 @@ cudaError_t allow_shared(K *kernel)
     return e;
 }
 
+template <typename T>
+struct Same {
+    using type = T;
+};
+
+// A launch that may start while the kernel before it drains (and a cluster
+// size). Its threads all call after_previous() before they touch global memory:
+// that waits until the kernel before is complete and its writes are seen. A
+// kernel that calls let_next_start() lets the next such launch set up meanwhile.
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned threads, size_t bytes, cudaStream_t stream, unsigned cluster,
+                         typename Same<A>::type... args)
+{
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = bytes;
+    config.stream = stream;
+    cudaLaunchAttribute attrs[2]{};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim = {cluster, 1, 1};
+    config.attrs = attrs;
+    config.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 

@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the kernel before wrote is there
+    after_previous();  // what the kernel before wrote is there
+    let_next_start();
 
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -412,19 +413,8 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, const Cut &cut, cudaSt
     auto kernel = fp8_few_kernel<kTok, TX, T, kAct>;
     cudaError_t e = allow_shared<kernel_tag<kTok, TX, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>((a.n + kBM - 1) / kBM * cut.groups * cut.split));
-    config.blockDim = dim3(kThreads);
-    config.dynamicSmemBytes = bytes;
-    config.stream = stream;
-    cudaLaunchAttribute attrs[2]{};
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim = {static_cast<unsigned>(cut.split), 1, 1};
-    config.attrs = attrs;
-    config.numAttrs = cut.split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&config, kernel, tmX, tmW, p);
+    return launch_after(kernel, dim3(static_cast<unsigned>((a.n + kBM - 1) / kBM * cut.groups * cut.split)), kThreads, bytes, stream,
+                        static_cast<unsigned>(cut.split), tmX, tmW, p);
 }
 
 // CTAs that are resident together, two an SM: clusters of 4 and 8 leave some SMs of a GPC over (36 and 15 of them fit

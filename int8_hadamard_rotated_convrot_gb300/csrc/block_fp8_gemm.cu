@@ -266,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     cluster_sync();  // both CTAs' barriers and tensor memory are there before any remote use
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // x's codes and scales are the pack's
+    after_previous();  // x's codes and scales are the pack's
 
     // Bounded; gives up early once another role has.
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -455,17 +455,7 @@ cudaError_t launch_pair(const convrot_fp8_linear_args &a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    config.blockDim = dim3(kPairThreads);
-    config.dynamicSmemBytes = C::SMEM;
-    config.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    config.attrs = &attr;
-    config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kernel, tmX, tmW, p);
+    return launch_after(kernel, dim3(static_cast<unsigned>(2 * pairs)), kPairThreads, C::SMEM, stream, 1, tmX, tmW, p);
 }
 
 }  // namespace

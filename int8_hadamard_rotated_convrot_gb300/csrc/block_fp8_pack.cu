@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(const T *x, int32_t m, in
     const uint32_t rows4 = group / static_cast<uint32_t>(blocks);
     const int j = static_cast<int>(group - rows4 * blocks);
     const int64_t r0 = static_cast<int64_t>(rows4) * kPackRows;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    after_previous();
+    let_next_start();
     if (r0 >= m) return;  // whole groups of lanes
     const int i0 = j * 128 + (kWide ? lane * kVec : lane);
     float v[kPackRows][kVec];
@@ -119,10 +120,9 @@ cudaError_t launch_fp8_pack(const void *x, int dtype, int64_t m, int64_t k, int6
         const bool wide = k % kVec == 0 && aligned_to(x, 16) && (m <= 1 || ldx % kVec == 0);
         const int64_t items = groups * (wide ? 128 / kVec : 32);
         const int scale4 = aligned_to(scale, 16) && lds % 4 == 0;
-        (wide ? fp8_pack_kernel<T, true> : fp8_pack_kernel<T, false>)<<<static_cast<unsigned>((items + 255) / 256), 256, 0, stream>>>(
-            static_cast<const T *>(x), static_cast<int32_t>(m), static_cast<int32_t>(k), ldx, static_cast<uint8_t *>(q), ldq, scale,
-            lds, static_cast<int32_t>(blocks), scale4);
-        return cudaGetLastError();
+        return launch_after(wide ? fp8_pack_kernel<T, true> : fp8_pack_kernel<T, false>, dim3(static_cast<unsigned>((items + 255) / 256)),
+                            256, 0, stream, 1, static_cast<const T *>(x), static_cast<int32_t>(m), static_cast<int32_t>(k), ldx,
+                            static_cast<uint8_t *>(q), ldq, scale, lds, static_cast<int32_t>(blocks), scale4);
     });
 }
 

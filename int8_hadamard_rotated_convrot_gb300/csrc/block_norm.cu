@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
 {
     __shared__ float2 slots[kWarp ? 1 : 64];
     __shared__ float amax32[kVec == 1 ? 512 : 1];  // largest magnitude of each 32 values (single elements, packing)
+    after_previous();
+    let_next_start();
     const int tid = kWarp ? threadIdx.x & 31 : threadIdx.x, nt = kWarp ? 32 : blockDim.x;
     const int64_t r = kWarp ? blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (kWarp && r >= a.m) return;
@@ -313,6 +315,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
     constexpr int kStages = kRingStages, kPieces = kNv * (kBranch ? 2 : 1), kValues = kNv * kVec, kPairs = kValues / 2;
     extern __shared__ uint4 ring[];  // kWide: [kStages][x, y][kNv][blockDim]
     __shared__ float2 slots[64];
+    after_previous();
+    let_next_start();
     const int nt = kThreads ? kThreads : blockDim.x, d = static_cast<int>(a.d);
     const float inv_d = 1.0f / d;
     RowSum<false> sum{slots};
@@ -654,6 +658,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __shared__ float slots[2 * 8 * 36];
     __shared__ float peers[2 * kCluster * 8];
     GradSum<kCluster> sum{slots, peers};
+    after_previous();
     const int64_t unit = blockIdx.x / kCluster;
     const int64_t b = unit / split.chunks, chunk = unit - b * split.chunks;
     const int64_t first = b * a.rows_per_batch + chunk * split.rows_per_chunk;
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             advance();
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     float *to = part + unit * 4 * a.d;
     auto put_sums = [&](float *p, const F2 (&v)[kPairs]) {
 #pragma unroll
@@ -907,7 +912,7 @@ __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_no
     __shared__ float4 sums[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t i = blockIdx.x * 32ll + lane, b = blockIdx.y;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are another kernel's
+    after_previous();  // the partials are another kernel's
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i < a.d)
 #pragma unroll 4
@@ -933,7 +938,7 @@ __global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_no
     if (a.dshift) a.dshift[b * a.d + i] = v.x;
     if (a.dscale) a.dscale[b * a.d + i] = param<P>(a.pre_weight, i, 1.0f) * v.y + param<P>(a.pre_bias, i, 0.0f) * v.x;
     if (a.dgate) a.dgate[b * a.d + i] = param<P>(a.post_weight, i, 1.0f) * v.w + param<P>(a.post_bias, i, 0.0f) * v.z;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_start();
     const float up = 1.0f + param<P>(a.scale, b * a.ldscale + i, 0.0f), gate = param<P>(a.gate, b * a.ldgate + i, 1.0f);
     const float out[4] = {up * v.y, up * v.x, gate * v.w, gate * v.z};
     float *const to[4] = {a.dpre_weight, a.dpre_bias, a.dpost_weight, a.dpost_bias};
@@ -958,7 +963,7 @@ __global__ void norm_grad_weights_kernel(const __grid_constant__ convrot_gated_n
 #pragma unroll
     for (int j = 1; j < 4; ++j)
         if (j == k) to = all[j];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     if (!to) return;
     float v = 0.0f;
     if (i < a.d)
@@ -994,9 +999,7 @@ template <typename T, typename P, int kVec, int kNv>
 cudaError_t launch_block_rows(const convrot_gated_norm_args &a, cudaStream_t stream)
 {
     const int64_t per = (a.d + kVec * kNv - 1) / (kVec * kNv);
-    gated_norm_kernel<T, P, kVec, kNv, false>
-        <<<static_cast<unsigned>(a.m), static_cast<unsigned>((per + 31) / 32 * 32), 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(gated_norm_kernel<T, P, kVec, kNv, false>, dim3(static_cast<unsigned>(a.m)), static_cast<unsigned>((per + 31) / 32 * 32), 0, stream, 1, a);
 }
 
 constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; the rest stays L1 for the vectors
@@ -1021,8 +1024,8 @@ bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaErro
     *e = allow_shared<ring_tag<T, P, kNv, kWide, kThreads, kBranch>>(kernel);
     if (*e != cudaSuccess) return true;
     const int64_t rows = (a.m + blocks - 1) / blocks;
-    kernel<<<static_cast<unsigned>((a.m + rows - 1) / rows), threads, bytes, stream>>>(a, static_cast<int32_t>(rows));
-    *e = cudaGetLastError();
+    *e = launch_after(kernel, dim3(static_cast<unsigned>((a.m + rows - 1) / rows)), static_cast<unsigned>(threads), bytes, stream, 1, a,
+                      static_cast<int32_t>(rows));
     return true;
 }
 
@@ -1036,8 +1039,7 @@ bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaErro
 template <typename T, typename P, int kVec, int kNv>
 cudaError_t launch_warp_rows(const convrot_gated_norm_args &a, cudaStream_t stream)
 {
-    gated_norm_kernel<T, P, kVec, kNv, true><<<static_cast<unsigned>((a.m + 3) / 4), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(gated_norm_kernel<T, P, kVec, kNv, true>, dim3(static_cast<unsigned>((a.m + 3) / 4)), 128, 0, stream, 1, a);
 }
 
 }  // namespace
@@ -1093,30 +1095,6 @@ int64_t gated_norm_backward_work_bytes(int64_t m, int64_t d, int64_t rows_per_ba
     return (s.units() + (s.batches > 1 ? s.batches : 0)) * 4 * d * static_cast<int64_t>(sizeof(float));
 }
 
-// A launch with a cluster size, or (dependent) one that may start while the
-// kernel before it drains: its griddepcontrol.wait holds it until that is done.
-template <typename... A>
-cudaError_t launch_with(void (*kernel)(A...), dim3 grid, unsigned threads, size_t bytes, cudaStream_t stream,
-                        unsigned cluster, bool dependent, A... args)
-{
-    cudaLaunchConfig_t config{};
-    config.gridDim = grid;
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = bytes;
-    config.stream = stream;
-    cudaLaunchAttribute attrs[2]{};
-    if (cluster > 1) {
-        attrs[config.numAttrs].id = cudaLaunchAttributeClusterDimension;
-        attrs[config.numAttrs++].val.clusterDim = {cluster, 1, 1};
-    }
-    if (dependent) {
-        attrs[config.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attrs[config.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-    }
-    config.attrs = attrs;
-    return cudaLaunchKernelEx(&config, kernel, args...);
-}
-
 template <typename T, typename P, int kVec, int kCluster>
 struct grad_tag;
 
@@ -1129,8 +1107,8 @@ cudaError_t launch_grad(const convrot_gated_norm_backward_args &a, const GradSpl
         const cudaError_t e = allow_shared<grad_tag<T, P, kVec, kCluster>>(kernel);
         if (e != cudaSuccess) return e;
     }
-    return launch_with(kernel, dim3(static_cast<unsigned>(s.units() * kCluster)), static_cast<unsigned>(s.threads), bytes,
-                       stream, kCluster, false, a, s, part);
+    return launch_after(kernel, dim3(static_cast<unsigned>(s.units() * kCluster)), static_cast<unsigned>(s.threads), bytes, stream,
+                        kCluster, a, s, part);
 }
 
 cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a, cudaStream_t stream)
@@ -1169,15 +1147,14 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
                 if (g.scale) g.scale = static_cast<const P *>(a.scale) + b0 * a.ldscale;
                 if (g.gate) g.gate = static_cast<const P *>(a.gate) + b0 * a.ldgate;
             }
-            e = launch_with(norm_grad_sample_kernel<P>, dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream, 1,
-                            b0 == 0, g, s.chunks, static_cast<const float *>(part + b0 * s.chunks * 4 * a.d),
-                            s.batches > 1 ? weights + b0 * 4 * a.d : nullptr);
+            e = launch_after(norm_grad_sample_kernel<P>, dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream, 1, g, s.chunks,
+                             static_cast<const float *>(part + b0 * s.chunks * 4 * a.d), s.batches > 1 ? weights + b0 * 4 * a.d : nullptr);
             if (e != cudaSuccess) return e;
         }
         if (per_weight && s.batches > 1)
-            return launch_with(norm_grad_weights_kernel, dim3(tiles, 4),
-                               static_cast<unsigned>(s.batches < kSumWarps ? s.batches : kSumWarps) * 32, 0, stream, 1, true, a,
-                               s.batches, static_cast<const float *>(weights));
+            return launch_after(norm_grad_weights_kernel, dim3(tiles, 4),
+                                static_cast<unsigned>(s.batches < kSumWarps ? s.batches : kSumWarps) * 32, 0, stream, 1, a, s.batches,
+                                static_cast<const float *>(weights));
         return cudaSuccess;
     });
 }

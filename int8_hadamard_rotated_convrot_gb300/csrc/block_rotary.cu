@@ -38,6 +38,8 @@ __global__ void __launch_bounds__(kRotaryThreads, sizeof(T) == 2 && kVec == 8 &&
     // Whether a's and b's are apart: in the half layout, and where single elements are all that is aligned.
     constexpr bool kSplit = !kInterleaved || kVec == 1;
     constexpr int kPairs = kSplit ? kVec : kVec / 2;  // pairs a thread turns in one head
+    after_previous();
+    let_next_start();
     const int per_row = s.slots * s.head_groups;
     for (int i = threadIdx.x; i < per_row * s.rows_per_block; i += blockDim.x) {
         const int local = i / per_row, rest = i - local * per_row;
@@ -162,8 +164,7 @@ cudaError_t launch_form(const convrot_rotary_args &a, cudaStream_t stream)
     const int64_t items = best * per_row, rounds = (items + kRotaryThreads - 1) / kRotaryThreads;
     const unsigned threads = static_cast<unsigned>(((items + rounds - 1) / rounds + 31) / 32 * 32);
     const unsigned blocks = (s.rows + best - 1) / best;
-    rotary_kernel<T, kVec, kInterleaved, kHeads><<<blocks, threads, 0, stream>>>(a, s);
-    return cudaGetLastError();
+    return launch_after(rotary_kernel<T, kVec, kInterleaved, kHeads>, dim3(blocks), threads, 0, stream, 1, a, s);
 }
 
 template <typename T, int kVec>
