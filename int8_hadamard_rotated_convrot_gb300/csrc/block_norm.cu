@@ -130,7 +130,7 @@ __device__ __forceinline__ void pack_row(const convrot_gated_norm_args &a, int64
         for (int e = 0; e < kVec; ++e) m = fmaxf(m, fabsf(h[j][e]));
 #pragma unroll
         for (int o = 64 / kVec; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (!at(j) < d) continue;
+        if (at(j) >= d) continue;
         m = fmaxf(m, kFp8AmaxFloor);
         if (at(j) % 128 == 0) a.q_scale[(at(j) >> 7) * a.ld_q_scale + r] = m / kFp8Max;
         const float up = fp8_up(m);

@@ -338,6 +338,28 @@ def test_gated_norm_pack(m, d):
     check_linear(bl.convrot_fp8_linear(packed, w, out_dtype=F32), packed, w, None, 0, F32)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16], ids=["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,d", [(3, 8), (5, 128), (9, 200), (300, 640), (4, 5120), (2, 8200), (3, 16384), (19500, 256), (6200, 1536), (2500, 4104)])
+def test_gated_norm_pack_of_aligned_tensors(m, d, dtype):
+    """The same where every tensor allows 16-byte accesses: few rows, and runs of many."""
+    v, how = norm_case(m, d, max(1, m // 2), dtype, F32, 2, 1, True)
+    v = {n: t.contiguous() for n, t in v.items()}
+    h, n, e_h, e_n = norm_bounds(v, how)
+    q, q_intact = framed(m, -(-d // 16) * 16, torch.uint8, 16, fill=7)
+    out = bl.Fp8Rows(q[:, :d].view(torch.float8_e4m3fn), torch.full((-(-d // 128), m), float("nan"), device="cuda"))
+    oh, packed = bl.convrot_gated_norm_pack(v["x"], v["y"], **params(v), **own_args(how), out=out)
+    assert packed is out
+    q_intact()
+    assert torch.all(q[:, d:] == 7)
+    close(oh, h, rounded(h, dtype, e_h), "h")
+    scale, _ = ref.block_scales(n)
+    kb = scale.shape[1]
+    e_block = torch.nn.functional.pad(e_n.expand_as(n), (0, kb * 128 - d)).view(m, kb, 128).amax(2)
+    close(packed.scale.t()[:m], scale.double(), e_block / 448 + 4 * U * scale.double(), "scales")
+    s = ref.spread(scale.double(), m, d)
+    close(packed.dequantize(), n, 2.0**-4 * n.abs() * 1.01 + 2.0**-10 * s + 2 * e_n, "codes")
+
+
 def test_gated_norm_special_rows():
     """A row of zeros gives 0 (eps holds the division), and NaN or infinity stays in its row."""
     x = randn(gen(2), 6, 1000, dtype=BF16)
