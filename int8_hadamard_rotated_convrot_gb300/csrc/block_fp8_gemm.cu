@@ -15,17 +15,18 @@
 //   warp 0      TMA producer of each CTA: a block's codes of its 128 rows of x
 //               and kBN / 2 rows of w, 128 bytes a row, 128-byte swizzled
 //   warp 1      tensor memory; in the even CTA one thread issues the MMAs
-//   warps 4-19  drain: four warps a lane quadrant, kBN / 4 columns each
+//   warps 4-11  drain: two warps a lane quadrant, kBN / 2 columns each
 // What bounds it is the turn of the two accumulators: a block's MMAs take 512
-// cycles, and then its sums are announced, read (two 32-column loads a warp,
-// ~130 cycles each on a quarter of the SM), scaled (64 fmas a thread) and the
-// buffer handed back, ~1900 cycles in all. Measured on one GB300: 1200 cycles a
-// block and pair, 2.16 PFLOP/s without the activation (M32760 K5120 N13824),
-// at 1380 W of 1400; the MMAs and copies alone would take 800 cycles, where L2
-// feeds 12.6 TB/s. Not faster: slices of 128 columns with four accumulators
-// (x's codes read twice; 3.46 ms against 2.48), one CTA on its own (half as
-// much again from L2; 2.90), 16-column loads (2.87), scales through shared
-// memory (2.70).
+// cycles, and then its sums are announced, read (two 64-column loads a warp),
+// scaled (128 fmas a thread) and the buffer handed back, ~1600 cycles in all.
+// Measured on one GB300: 1070 cycles a block and pair, 2.3 PFLOP/s without the
+// activation and 2.05 with the tanh form of GELU (M32760 K5120 N13824, 2.10 and
+// 2.35 ms with the pack), at 1380 W of 1400; the MMAs and copies alone would
+// take 800 cycles, where L2 feeds 12.6 TB/s. Not faster: sixteen drain warps
+// (more loads of fewer columns; 2.48 ms), slices of 128 columns with four
+// accumulators (x's codes read twice; 3.46), one CTA on its own (half as much
+// again from L2; 2.90), 16-column loads (2.87), scales through shared memory
+// (2.70), scales fetched two or four blocks ahead (2.37, 2.44).
 // A TMA map ends at column k, so a short last block is filled with zeros.
 // Every wait is bounded: one that runs out writes CONVROT_ERR_TIMEOUT to the
 // status word and the CTA winds down (copies and MMAs in flight are waited
@@ -45,12 +46,12 @@ using namespace tc;
 constexpr int kBK = 128;             // codes of one block: 128 bytes, one swizzle span
 constexpr int kBM = 128;             // rows of x (and of the accumulators) per CTA
 constexpr int kMmaK = 32;
-constexpr int kDrainWarps = 16;
+constexpr int kDrainWarps = 8;
 constexpr int kPairThreads = 128 + kDrainWarps * 32;
-// Registers a thread: launched at 96, warpgroup 0 leaves most of its own to the
-// drain warps (64 sums, 32 values on the way): 4 x 32 x 32 + 16 x 32 x 112 = 640 x 96.
-constexpr int kRegsWg0 = 32, kRegsDrain = 112;
-static_assert(4 * 32 * kRegsWg0 + kDrainWarps * 32 * kRegsDrain <= kPairThreads * 96, "register split");
+// Registers a thread: launched at 168, warpgroup 0 leaves most of its own to the
+// drain warps (128 sums, 64 values on the way): 4 x 32 x 40 + 8 x 32 x 232 = 384 x 168.
+constexpr int kRegsWg0 = 40, kRegsDrain = 232;
+static_assert(4 * 32 * kRegsWg0 + kDrainWarps * 32 * kRegsDrain <= kPairThreads * 168, "register split");
 
 template <int kBN>
 struct Cfg {
@@ -157,6 +158,26 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t t
     nt = local / rows;
 }
 
+// 32 lanes x 64 consecutive 32-bit columns; thread i of the warp gets lane (base + i).
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,"
+        "%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,"
+        "%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // One warp's 32 rows of finished sums (lane: row), 64 bytes of each,
 // activated and stored: staged in shared memory and written four lanes a row.
 template <typename T, int kAct>
@@ -224,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const __grid_constant__ Fp8Params p)
 {
     using C = Cfg<kBN>;
-    constexpr int kCols = kBN / 4, kBox = 64 / sizeof(T);  // columns of a drain warp, and of a staged box
+    constexpr int kCols = kBN / 2, kBox = 64 / sizeof(T);  // columns of a drain warp, and of a staged box
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
@@ -389,16 +410,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 tc_fence_after();
                 const uint32_t taddr = taddr0 + buf * kBN;
 #pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32(taddr + c * 32, r);
-                    if (c == kCols / 32 - 1) {  // read to the end: the buffer is free
+                for (int c = 0; c < kCols / 64; ++c) {
+                    uint32_t r[64];
+                    tmem_ld64(taddr + c * 64, r);
+                    if (c == kCols / 64 - 1) {  // read to the end: the buffer is free
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_remote(acce0 + 8u * buf);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(__uint_as_float(r[i]), scale, acc[c * 32 + i]);
+                    for (int i = 0; i < 64; ++i) acc[c * 64 + i] = fmaf(__uint_as_float(r[i]), scale, acc[c * 64 + i]);
                 }
                 if (++buf == C::BUFS) buf = 0;
                 if (++stage == C::STAGES) {
