@@ -899,7 +899,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if constexpr (kCluster > 1) cluster_barrier();  // no block leaves while a peer may still write into it
 }
 
-constexpr int kSumWarps = 8;
+// Warps of a block that adds partials up: 8 where that gives every SM two blocks, up to 32 where few columns and
+// samples leave a warp many partials to go through.
+constexpr int kSumWarps = 32;
+int sum_warps(int64_t blocks, int64_t partials)
+{
+    const int64_t most = blocks >= 2 * kSms ? 8 : kSumWarps;
+    return static_cast<int>(partials < most ? partials : most);
+}
 
 // Adds up one sample's partials (block (x, y): 32 columns of sample y; warps
 // take chunks in turn) and writes that sample's gradients. What the sample adds
@@ -1135,7 +1142,7 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
         const bool per_weight = a.dpre_weight || a.dpre_bias || a.dpost_weight || a.dpost_bias;
         if (!per_weight && !a.dshift && !a.dscale && !a.dgate) return cudaSuccess;
         const unsigned tiles = static_cast<unsigned>((a.d + 31) / 32);
-        const unsigned warps = static_cast<unsigned>(s.chunks < kSumWarps ? s.chunks : kSumWarps);
+        const unsigned warps = static_cast<unsigned>(sum_warps(tiles * s.batches, s.chunks));
         for (int64_t b0 = 0; b0 < s.batches; b0 += 65535) {  // (the grid's second dimension has 16 bits)
             convrot_gated_norm_backward_args g = a;
             const int64_t n = s.batches - b0 < 65535 ? s.batches - b0 : 65535;
@@ -1153,7 +1160,7 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
         }
         if (per_weight && s.batches > 1)
             return launch_after(norm_grad_weights_kernel, dim3(tiles, 4),
-                                static_cast<unsigned>(s.batches < kSumWarps ? s.batches : kSumWarps) * 32, 0, stream, 1, a, s.batches,
+                                static_cast<unsigned>(sum_warps(4 * tiles, s.batches)) * 32, 0, stream, 1, a, s.batches,
                                 static_cast<const float *>(weights));
         return cudaSuccess;
     });
