@@ -908,55 +908,64 @@ int sum_warps(int64_t blocks, int64_t partials)
     return static_cast<int>(partials < most ? partials : most);
 }
 
-// Adds up one sample's partials (block (x, y): 32 columns of sample y; warps
-// take chunks in turn) and writes that sample's gradients. What the sample adds
-// to the weights' gradients goes to `weights` [batches][4][d], or straight to
-// them if there is one sample.
+constexpr int64_t kFewPartials = 128;  // that one block adds up for all samples, instead of a launch more
+
+// Adds up a sample's partials (block (x, y): 32 columns of sample y; warps take
+// chunks in turn) and writes that sample's gradients. What the sample adds to
+// the weights' gradients goes to `weights` [batches][4][d]; without that (few
+// partials) block x goes through the samples in turn and writes the sums itself.
 template <typename P>
-__global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, int64_t chunks,
+__global__ void norm_grad_sample_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, int64_t chunks, int64_t samples,
                                         const float *part, float *weights)
 {
     __shared__ float4 sums[kSumWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t i = blockIdx.x * 32ll + lane, b = blockIdx.y;
+    const int64_t i = blockIdx.x * 32ll + lane;
+    const bool in = i < a.d;
     after_previous();  // the partials are another kernel's
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (i < a.d)
-#pragma unroll 4
-        for (int64_t c = warp; c < chunks; c += warps) {
-            const float *p = part + (b * chunks + c) * 4 * a.d + i;
-            v.x += p[0];
-            v.y += p[a.d];
-            if (a.y) {
-                v.z += p[2 * a.d];
-                v.w += p[3 * a.d];
-            }
-        }
-    sums[warp][lane] = v;
-    __syncthreads();
-    if (warp != 0 || i >= a.d) return;
-    for (int w = 1; w < warps; ++w) {
-        const float4 o = sums[w][lane];
-        v.x += o.x;
-        v.y += o.y;
-        v.z += o.z;
-        v.w += o.w;
-    }
-    if (a.dshift) a.dshift[b * a.d + i] = v.x;
-    if (a.dscale) a.dscale[b * a.d + i] = param<P>(a.pre_weight, i, 1.0f) * v.y + param<P>(a.pre_bias, i, 0.0f) * v.x;
-    if (a.dgate) a.dgate[b * a.d + i] = param<P>(a.post_weight, i, 1.0f) * v.w + param<P>(a.post_bias, i, 0.0f) * v.z;
     let_next_start();
-    const float up = 1.0f + param<P>(a.scale, b * a.ldscale + i, 0.0f), gate = param<P>(a.gate, b * a.ldgate + i, 1.0f);
-    const float out[4] = {up * v.y, up * v.x, gate * v.w, gate * v.z};
     float *const to[4] = {a.dpre_weight, a.dpre_bias, a.dpost_weight, a.dpost_bias};
+    float total[4] = {};
+    const int64_t first = weights ? blockIdx.y : 0, last = weights ? first + 1 : samples;
+    for (int64_t b = first; b < last; ++b) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in)
+#pragma unroll 4
+            for (int64_t c = warp; c < chunks; c += warps) {
+                const float *p = part + (b * chunks + c) * 4 * a.d + i;
+                v.x += p[0];
+                v.y += p[a.d];
+                if (a.y) {
+                    v.z += p[2 * a.d];
+                    v.w += p[3 * a.d];
+                }
+            }
+        if (b > first) __syncthreads();  // the sums before have been read
+        sums[warp][lane] = v;
+        __syncthreads();
+        if (warp != 0 || !in) continue;
+        for (int w = 1; w < warps; ++w) {
+            const float4 o = sums[w][lane];
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+        }
+        if (a.dshift) a.dshift[b * a.d + i] = v.x;
+        if (a.dscale) a.dscale[b * a.d + i] = param<P>(a.pre_weight, i, 1.0f) * v.y + param<P>(a.pre_bias, i, 0.0f) * v.x;
+        if (a.dgate) a.dgate[b * a.d + i] = param<P>(a.post_weight, i, 1.0f) * v.w + param<P>(a.post_bias, i, 0.0f) * v.z;
+        const float up = 1.0f + param<P>(a.scale, b * a.ldscale + i, 0.0f), gate = param<P>(a.gate, b * a.ldgate + i, 1.0f);
+        const float adds[4] = {up * v.y, up * v.x, gate * v.w, gate * v.z};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (!to[k]) continue;
-        if (!weights)
-            to[k][i] = out[k];
-        else
-            weights[(b * 4 + k) * a.d + i] = out[k];
+        for (int k = 0; k < 4; ++k) {
+            total[k] += adds[k];
+            if (weights && to[k]) weights[(b * 4 + k) * a.d + i] = adds[k];
+        }
     }
+    if (weights || warp != 0 || !in) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (to[k]) to[k][i] = total[k];
 }
 
 __global__ void norm_grad_weights_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, int64_t batches,
@@ -1142,6 +1151,9 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
         const bool per_weight = a.dpre_weight || a.dpre_bias || a.dpost_weight || a.dpost_bias;
         if (!per_weight && !a.dshift && !a.dscale && !a.dgate) return cudaSuccess;
         const unsigned tiles = static_cast<unsigned>((a.d + 31) / 32);
+        if (s.batches == 1 || s.units() <= kFewPartials)
+            return launch_after(norm_grad_sample_kernel<P>, dim3(tiles), static_cast<unsigned>(sum_warps(tiles, s.chunks)) * 32, 0, stream,
+                                1, a, s.chunks, s.batches, static_cast<const float *>(part), static_cast<float *>(nullptr));
         const unsigned warps = static_cast<unsigned>(sum_warps(tiles * s.batches, s.chunks));
         for (int64_t b0 = 0; b0 < s.batches; b0 += 65535) {  // (the grid's second dimension has 16 bits)
             convrot_gated_norm_backward_args g = a;
@@ -1154,11 +1166,11 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
                 if (g.scale) g.scale = static_cast<const P *>(a.scale) + b0 * a.ldscale;
                 if (g.gate) g.gate = static_cast<const P *>(a.gate) + b0 * a.ldgate;
             }
-            e = launch_after(norm_grad_sample_kernel<P>, dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream, 1, g, s.chunks,
-                             static_cast<const float *>(part + b0 * s.chunks * 4 * a.d), s.batches > 1 ? weights + b0 * 4 * a.d : nullptr);
+            e = launch_after(norm_grad_sample_kernel<P>, dim3(tiles, static_cast<unsigned>(n)), warps * 32, 0, stream, 1, g, s.chunks, n,
+                             static_cast<const float *>(part + b0 * s.chunks * 4 * a.d), weights + b0 * 4 * a.d);
             if (e != cudaSuccess) return e;
         }
-        if (per_weight && s.batches > 1)
+        if (per_weight)
             return launch_after(norm_grad_weights_kernel, dim3(tiles, 4),
                                 static_cast<unsigned>(sum_warps(4 * tiles, s.batches)) * 32, 0, stream, 1, a, s.batches,
                                 static_cast<const float *>(weights));

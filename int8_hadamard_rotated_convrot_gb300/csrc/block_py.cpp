@@ -309,6 +309,8 @@ PyObject *gated_norm(PyObject *, PyObject *const *v, Py_ssize_t n)
     return status(convrot_gated_norm(&a, stream));
 }
 
+constexpr int64_t kWorkBehind = 2 << 20;
+
 // A contiguous tensor of the sizes at an offset of another's memory, without a trip through the dispatcher.
 Tensor part_of(const Tensor &whole, int64_t offset, at::IntArrayRef sizes)
 {
@@ -368,18 +370,28 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
         const auto like = h->options().requires_grad(c10::nullopt);
         dx = at::empty({m, d}, like);
         if (v[1] != Py_None) dy = at::empty({m, d}, like);
-        int64_t rows = 0;
-        for (const Small &s : small) rows += s.of == Py_None ? 0 : s.of_samples ? batches : 1;
-        const Tensor all = at::empty({rows, d}, like.dtype(at::kFloat));
-        rows = 0;
+        int64_t floats = 0;
+        for (const Small &s : small) floats += s.of == Py_None ? 0 : (s.of_samples ? batches : 1) * d;
+        // An allocation costs about as much as a launch: a small workspace goes behind the small gradients, in one.
+        const bool own_work = v[16] == Py_None;
+        int64_t behind = 0;
+        if (own_work) {
+            a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
+            if (a.work_bytes <= kWorkBehind) behind = (a.work_bytes + 255) / 256 * 64 + 64;
+        }
+        const int64_t start = (floats + 63) / 64 * 64;
+        const Tensor all = at::empty({behind ? start + behind : floats}, like.dtype(at::kFloat));
+        floats = 0;
         for (Small &s : small) {
             if (s.of == Py_None) continue;
-            s.grad = s.of_samples ? part_of(all, rows * d, {batches, d}) : part_of(all, rows * d, {d});
+            s.grad = s.of_samples ? part_of(all, floats, {batches, d}) : part_of(all, floats, {d});
             *s.to = static_cast<float *>(s.grad.data_ptr());
-            rows += s.of_samples ? batches : 1;
+            floats += (s.of_samples ? batches : 1) * d;
         }
-        if (v[16] == Py_None) {
-            a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
+        if (behind) {
+            const auto at = reinterpret_cast<uintptr_t>(static_cast<float *>(all.data_ptr()) + start);
+            a.work = reinterpret_cast<void *>((at + 255) / 256 * 256);
+        } else if (own_work) {
             work = at::empty({a.work_bytes}, like.dtype(at::kByte));
             a.work = work.data_ptr();
         }

@@ -69,12 +69,12 @@ def test_stretch_between_attentions(example, batch, tokens, width, heads, hidden
     wide = [t.double().requires_grad_() for t in (x, attention)]
     want = plain(net, *wide, modulation, tables)
     for name, a, b in zip(("residual", "q", "k", "v"), got, want):
-        off = float((a.double() - b).norm() / b.norm())
+        off = float((a.double() - b.detach()).norm() / b.detach().norm())
         assert off < 0.10, f"{name}: {off:.3f}"
     up = [0.1 * normal(*t.shape).bfloat16() for t in got]
     dx = net.input_gradient(saved, modulation, tables, *up)
     for name, a, b in zip(("x", "attention"), dx, torch.autograd.grad(want, wide, [u.double() for u in up])):
-        off = float((a.double() - b).norm() / b.norm())
+        off = float((a.double() - b.detach()).norm() / b.detach().norm())
         assert off < 0.15, f"gradient of {name}: {off:.3f}"
 
 
