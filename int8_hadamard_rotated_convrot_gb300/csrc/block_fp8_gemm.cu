@@ -80,7 +80,6 @@ struct Fp8Params {
     int64_t ldy;
     int32_t *dev_status;
     int32_t vec_y;    // rows of y start on 16 bytes
-    int32_t vec_bias;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -180,27 +179,19 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64])
 
 // One warp's 32 rows of finished sums (lane: row), 64 bytes of each,
 // activated and stored: staged in shared memory and written four lanes a row.
+// Lane i has the bias of the slice's columns 4 i .. 4 i + 3; the box starts at
+// its column `first`.
 template <typename T, int kAct>
-__device__ __forceinline__ void store_box(const Fp8Params &p, uint32_t out, int lane, int64_t row0, int64_t col0, const float *acc)
+__device__ __forceinline__ void store_box(const Fp8Params &p, uint32_t out, int lane, int64_t row0, int64_t col0, const float *acc,
+                                          const float (&bias)[4], int first)
 {
     constexpr int kBox = 64 / sizeof(T);
     float v[kBox];
 #pragma unroll
     for (int i = 0; i < kBox; ++i) v[i] = acc[i];
     if (p.bias) {
-        if (p.vec_bias && col0 + kBox <= p.n) {
 #pragma unroll
-            for (int i = 0; i < kBox / 4; ++i) {
-                const float4 b = __ldg(reinterpret_cast<const float4 *>(p.bias + col0) + i);
-                v[4 * i] += b.x;
-                v[4 * i + 1] += b.y;
-                v[4 * i + 2] += b.z;
-                v[4 * i + 3] += b.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kBox; ++i) v[i] += col0 + i < p.n ? __ldg(p.bias + col0 + i) : 0.0f;
-        }
+        for (int i = 0; i < kBox; ++i) v[i] += __shfl_sync(0xffffffffu, bias[i % 4], (first + i) / 4);
     }
     if constexpr (kAct != 0) {
 #pragma unroll
@@ -392,6 +383,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             // this lane's row and this slice's columns share one scale in each block of k
             const bool row_in = row0 + lane < p.m, col_in = col0 < p.n;
             const float *sx = p.x_scale + (row_in ? row0 + lane : 0), *sw = p.w_scale + (col_in ? col0 / 128 * p.ld_w_scale : 0);
+            float bias[4];  // read now, used after the tile's last block
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bias[e] = p.bias && lane * 4 < kCols && col0 + lane * 4 + e < p.n ? __ldg(p.bias + col0 + lane * 4 + e) : 0.0f;
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
@@ -431,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (row0 < p.m) {
 #pragma unroll
                 for (int c = 0; c < kCols / kBox; ++c)
-                    if (col0 + c * kBox < p.n) store_box<T, kAct>(p, out, lane, row0, col0 + c * kBox, acc + c * kBox);
+                    if (col0 + c * kBox < p.n) store_box<T, kAct>(p, out, lane, row0, col0 + c * kBox, acc + c * kBox, bias, c * kBox);
             }
         }
         if (!ok) fail();
@@ -470,7 +464,6 @@ cudaError_t launch_pair(const convrot_fp8_linear_args &a, cudaStream_t stream)
     p.ldy = a.ldy;
     p.dev_status = a.dev_status;
     p.vec_y = aligned_to(a.y, 16) && a.ldy * sizeof(T) % 16 == 0;
-    p.vec_bias = aligned_to(a.bias, 16);
     auto kernel = fp8_pair_kernel<kBN, T, kAct>;
     cudaError_t e = allow_shared<pair_tag<kBN, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
