@@ -97,6 +97,47 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
     return c;
 }
 
+// 2^x and 1 / x, approximate (2 and 1 units in the last place).
+__device__ __forceinline__ float ex2(float x)
+{
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+    return x;
+}
+__device__ __forceinline__ float rcp(float x)
+{
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+    return x;
+}
+
+// GELU of two values (convrot_activation), the forms of internal.h's apply_act
+// with their multiplications and additions in pairs, so that the two special
+// functions a value are what it costs:
+//   tanh form  v / (1 + e^(-2u)), -2u log2(e) = v (c0 + c1 v^2)
+//   erf form   v (1/2 + sign(v) (1/2 - q/2)), q = 1 - erf(|v| / sqrt(2)) by Abramowitz & Stegun 7.1.26
+template <int kAct>
+__device__ __forceinline__ F2 act2(F2 v)
+{
+    if constexpr (kAct == CONVROT_ACT_GELU_TANH) {
+        const F2 z = v * fma2(v * v, F2(-0.10294324f), F2(-2.3022082f));
+        const F2 e = F2(ex2(z.lo()), ex2(z.hi())) + F2(1.0f);
+        return v * F2(rcp(e.lo()), rcp(e.hi()));
+    } else if constexpr (kAct == CONVROT_ACT_GELU_ERF) {
+        const F2 x = F2(fabsf(v.lo()), fabsf(v.hi())) * F2(0.70710678f);
+        const F2 u = fma2(x, F2(0.3275911f), F2(1.0f));
+        const F2 t(rcp(u.lo()), rcp(u.hi()));
+        // half of the polynomial: q / 2
+        F2 h = fma2(t, F2(0.5f * 1.061405429f), F2(0.5f * -1.453152027f));
+        h = fma2(t, h, F2(0.5f * 1.421413741f));
+        h = fma2(t, h, F2(0.5f * -0.284496736f));
+        h = fma2(t, h, F2(0.5f * 0.254829592f)) * t;
+        const F2 z = x * x * F2(-1.4426950f);
+        h = fma2(h, F2(-ex2(z.lo()), -ex2(z.hi())), F2(0.5f));
+        return v * (F2(copysignf(h.lo(), v.lo()), copysignf(h.hi(), v.hi())) + F2(0.5f));
+    } else {
+        return v;
+    }
+}
+
 // N consecutive elements as one access of up to 16 bytes (N * sizeof(T) a power
 // of two); the address is aligned to it. kStream: the line is not needed again
 // (evict-first); the loads stay coherent, so an output may be its own input.

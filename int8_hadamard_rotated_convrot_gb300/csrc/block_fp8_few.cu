@@ -21,7 +21,6 @@
 #include <cudaTypedefs.h>
 
 #include "block.h"
-#include "internal.h"
 #include "tc_common.cuh"
 
 namespace convrot {
@@ -350,7 +349,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 v[3] += part[c].w;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = apply_act_t<kAct>(v[e] + bias[e]);
+            for (int e = 0; e < 4; e += 2) {
+                const F2 two = act2<kAct>(F2(v[e] + bias[e], v[e + 1] + bias[e + 1]));
+                v[e] = two.lo();
+                v[e + 1] = two.hi();
+            }
             T *y = static_cast<T *>(p.y) + (row0 + r) * p.ldy + col;
             if (p.vec_y && col + 4 <= p.n) {
                 Raw<T, 4> raw;

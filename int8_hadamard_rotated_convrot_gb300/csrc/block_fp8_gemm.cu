@@ -35,7 +35,6 @@
 #include <cudaTypedefs.h>
 
 #include "block.h"
-#include "internal.h"
 #include "tc_common.cuh"
 
 namespace convrot {
@@ -195,7 +194,11 @@ __device__ __forceinline__ void store_box(const Fp8Params &p, uint32_t out, int 
     }
     if constexpr (kAct != 0) {
 #pragma unroll
-        for (int i = 0; i < kBox; ++i) v[i] = apply_act_t<kAct>(v[i]);
+        for (int i = 0; i < kBox; i += 2) {
+            const F2 two = act2<kAct>(F2(v[i], v[i + 1]));
+            v[i] = two.lo();
+            v[i + 1] = two.hi();
+        }
     }
     Raw<T, kBox> raw;
     raw.pack(v);
