@@ -35,7 +35,7 @@ _E4M3 = torch.float8_e4m3fn
 _native = None
 
 
-def _library():
+def load():
     """The native marshalling module, loaded (with libconvrot) on first use."""
     global _native
     if _native is None:
@@ -127,7 +127,7 @@ def convrot_fp8_pack_activations(X: torch.Tensor, out: Fp8Rows | None = None, st
     """Codes and scales of X [m, k] (float32, bfloat16 or float16), one scale for 128 features of a row."""
     if out is None:
         out = empty_fp8_rows(*X.shape, X.device)
-    _check(_library().pack_activations(X, out.q, out.scale, stream), "convrot_fp8_pack_activations")
+    _check(load().pack_activations(X, out.q, out.scale, stream), "convrot_fp8_pack_activations")
     return out
 
 
@@ -138,7 +138,7 @@ def convrot_fp8_quantize_weights(W: torch.Tensor, stream=None) -> Fp8Weights:
     n, k = W.shape
     q = fp8_codes(n, k, W.device)
     scale = torch.empty((_blocks(n), _blocks(k)), dtype=torch.float32, device=W.device)
-    _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, max(W.stride(0), k), q.data_ptr(),
+    _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, W.stride(0) if n > 1 else k, q.data_ptr(),
                                                    -(-k // 16) * 16, scale.data_ptr(), _blocks(k), _stream(W.device, stream)),
            "convrot_fp8_quantize_weights")
     return Fp8Weights(q, scale)
@@ -150,7 +150,7 @@ def convrot_fp8_linear(x: Fp8Rows, w: Fp8Weights, bias: torch.Tensor | None = No
     """Y [m, n] = act(x w^T + b) from packed activations; bias fp32 [n]. Y has out's or out_dtype's type."""
     if out is None:
         out = torch.empty((x.q.shape[0], w.q.shape[0]), dtype=out_dtype, device=x.q.device)
-    _check(_library().linear(x.q, x.scale, w.q, w.scale, bias, act, out, None, dev_status, stream), "convrot_fp8_linear")
+    _check(load().linear(x.q, x.scale, w.q, w.scale, bias, act, out, None, dev_status, stream), "convrot_fp8_linear")
     return out
 
 
@@ -167,7 +167,7 @@ def convrot_fp8_pack_linear(X: torch.Tensor, w: Fp8Weights, bias: torch.Tensor |
     Y has out's, out_dtype's or X's type. ``work`` (uint8) is allocated here when not given."""
     if out is None:
         out = torch.empty((X.shape[0], w.q.shape[0]), dtype=out_dtype or X.dtype, device=X.device)
-    _check(_library().linear(X, None, w.q, w.scale, bias, act, out, work, dev_status, stream), "convrot_fp8_pack_linear")
+    _check(load().linear(X, None, w.q, w.scale, bias, act, out, work, dev_status, stream), "convrot_fp8_pack_linear")
     return out
 
 
@@ -191,7 +191,7 @@ def convrot_gated_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: 
     if out_n is None:
         out_n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
-    _check(_library().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
+    _check(load().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
                                  pre_weight, pre_bias, eps, write_h, out_n, None, None, stream),
            "convrot_gated_norm")
     return out_h, out_n
@@ -211,7 +211,7 @@ def convrot_gated_norm_pack(x: torch.Tensor, y: torch.Tensor | None = None, *, g
     if out is None:
         out = empty_fp8_rows(*x.shape, x.device)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
-    _check(_library().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
+    _check(load().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
                                  pre_weight, pre_bias, eps, write_h, None, out.q, out.scale, stream),
            "convrot_gated_norm")
     return out_h, out
@@ -228,7 +228,7 @@ def convrot_gated_norm_backward(h: torch.Tensor, y: torch.Tensor | None, dh: tor
     """The gradients of convrot_gated_norm's inputs, from its output h, its input y and the gradients dh and dn
     of its outputs (None: zero). A dict with dx, dy (of h's type) and, in float32, dgate, dscale, dshift [batches, d]
     and dpost_weight, dpost_bias, dpre_weight, dpre_bias [d]: None for each input that was not given."""
-    got = _library().gated_norm_backward(h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight,
+    got = load().gated_norm_backward(h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight,
                                          post_bias, pre, pre_weight, pre_bias, eps, work, stream)
     if not isinstance(got, dict):
         raise ConvrotError(got, "convrot_gated_norm_backward")
@@ -254,7 +254,7 @@ def convrot_rotary(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, s
         out_k = None
     elif out_k is None:
         out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _check(_library().rotary(q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream), "convrot_rotary")
+    _check(load().rotary(q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream), "convrot_rotary")
     return out_q, out_k
 
 

@@ -97,6 +97,18 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
     return c;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // 2^x and 1 / x, approximate (2 and 1 units in the last place).
 __device__ __forceinline__ float ex2(float x)
 {

@@ -4,11 +4,15 @@
 //
 // Forward: two reads and two writes of a value for about ten operations on it,
 // so HBM is the bound. A row stays in the registers of one block of threads
-// (of one warp, up to 32 x 4 vectors) from its load to its store: every tensor
-// is moved once, in 16-byte accesses where all addresses allow it and in
+// (of one warp, where 32 pieces hold it) from its load to its store: every
+// tensor is moved once, in 16-byte accesses where all addresses allow it and in
 // coalesced single elements otherwise. The statistics are two-pass (mean, then
 // squares about it), which costs one more trip around the block than a
 // one-pass sum of squares and keeps layer norms of rows with a large mean.
+// Measured on one GB300, 32760 x 5120 in bf16 with RMS norms on both sides: 219
+// us, 6.1 TB/s, 90 % of a measured copy; 4097 x 1155 in f16, single elements:
+// 10.7 us, 2.7 TB/s, bound by instructions. One block a row, without the runs
+// of rows below, takes 316 and 24 us.
 #include "block.h"
 
 namespace convrot {
@@ -537,7 +541,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 // W = gate w_post, for an RMS post norm
 //   sum gy y = inv sum g W y - inv mean(g) sum W y - inv^2 mean(g h^) sum h W y + sum dh W y
 // goes along too. One trip for RMS norms, one more for the means of a layer
-// norm, and one more if post is one.
+// norm, and one more if post is one. Measured at 8190 x 5120 in bf16 with RMS
+// norms: 142 us with the sums, 3.5 TB/s (52 % of a copy); issue slots are 39 %
+// busy, the rest is the latency of the trips. Clusters of two blocks with two of
+// them an SM, for two rows under way: 190 us.
 
 // Columns a thread: 16 spread a row's trip around the block over twice the
 // values of 8 (146 against 166 us; M8190 D5120 in bf16, RMS norms).
@@ -567,18 +574,6 @@ struct GradSplit {
     }
     int64_t units() const { return batches * chunks; }
 };
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_barrier()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 // Eight sums at once over the threads that share a row: within a warp each of
 // three steps halves the values that a lane carries, a block's warps meet in
@@ -623,7 +618,7 @@ struct GradSum {
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(s) : "memory");
                 }
             }
-            cluster_barrier();
+            cluster_sync();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[i] = 0.0f;
@@ -896,7 +891,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         put_sums(to + 2 * a.d, t0);
         put_sums(to + 3 * a.d, t1);
     }
-    if constexpr (kCluster > 1) cluster_barrier();  // no block leaves while a peer may still write into it
+    if constexpr (kCluster > 1) cluster_sync();  // no block leaves while a peer may still write into it
 }
 
 // Warps of a block that adds partials up: 8 where that gives every SM two blocks, up to 32 where few columns and
@@ -1119,10 +1114,8 @@ cudaError_t launch_grad(const convrot_gated_norm_backward_args &a, const GradSpl
 {
     const int bytes = kVec == 1 ? 0 : grad_stages<T>() * 4 * (kGradCols / kVec) * s.threads * 16;
     auto kernel = norm_grad_kernel<T, P, kVec, kCluster>;
-    if (bytes > 48 * 1024) {
-        const cudaError_t e = allow_shared<grad_tag<T, P, kVec, kCluster>>(kernel);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared<grad_tag<T, P, kVec, kCluster>>(kernel);
+    if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(static_cast<unsigned>(s.units() * kCluster)), static_cast<unsigned>(s.threads), bytes, stream,
                         kCluster, a, s, part);
 }

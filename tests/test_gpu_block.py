@@ -106,6 +106,16 @@ def test_quantize_weights(n, k, dtype):
     assert torch.equal(w.q.view(torch.uint8), ref.e4m3_codes(W.float() * ref.spread(up, n, k, weights=True)))
 
 
+def test_rows_that_overlap_are_refused():
+    one = torch.ones(1, 64, device="cuda").expand(4, 64)
+    w = bl.convrot_fp8_quantize_weights(torch.ones(8, 64, device="cuda"))
+    for call in (lambda: bl.convrot_fp8_quantize_weights(one), lambda: bl.convrot_fp8_pack_activations(one),
+                 lambda: bl.convrot_fp8_pack_linear(one, w), lambda: bl.convrot_gated_norm(one)):
+        with pytest.raises(cr.ConvrotError) as e:
+            call()
+        assert e.value.status == cr.ERR_INVALID_ARG
+
+
 def test_nan_and_infinity_stay_in_their_rows():
     g = gen(3)
     X = randn(g, 130, 384, dtype=BF16)
@@ -492,6 +502,21 @@ def test_gated_norm_backward_against_differences():
             size = (got["d" + name].double() * way).abs().sum()
             # differences: step^2 of the third derivative, about 1e-8 here; gradient: h rounded to 32 bits
             assert abs(float(change - slope)) < 1e-5 * float(size), name
+
+
+def test_first_call_of_a_process():
+    """Sizes whose shared memory is just under or over a launch's default limit, each as the first call of a process
+    (a limit that an earlier call raised stays raised)."""
+    import os
+    import subprocess
+    import sys
+
+    code = ("import torch; from int8_hadamard_rotated_convrot_gb300 import block as bl; x = torch.ones(%d, %d, device='cuda').bfloat16(); "
+            "bl.convrot_gated_norm_backward(x, x, x, x); bl.convrot_gated_norm(x, x); "
+            "bl.convrot_fp8_pack_linear(x, bl.convrot_fp8_quantize_weights(x)); torch.cuda.synchronize()")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for m, d in ((8, 1536), (8, 1024), (7000, 768)):
+        subprocess.run([sys.executable, "-c", code % (m, d)], cwd=root, check=True, timeout=120)
 
 
 def test_gated_norm_backward_without_dh_or_dn_and_empty():
