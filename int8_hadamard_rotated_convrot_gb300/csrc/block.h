@@ -190,6 +190,20 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) __stcs(reinterpret_cast<B *>(p) + i, bits[i]);
     }
+    // N == 1: the value
+    __device__ __forceinline__ float value() const
+    {
+        static_assert(N == 1);
+        float v[1];
+        unpack(v);
+        return v[0];
+    }
+    __device__ __forceinline__ void set(float f)
+    {
+        static_assert(N == 1);
+        const float v[1] = {f};
+        pack(v);
+    }
     // All N values; 16-bit types two at a time (one operation a value to widen
     // bf16, one for two values to round).
     __device__ __forceinline__ void unpack(float (&v)[N]) const
@@ -252,11 +266,15 @@ struct Raw {
     }
 };
 
-// 16 bytes from global to shared memory without a register between; with
-// bytes = 0 nothing is read and the 16 bytes become zero.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, uint32_t bytes)
+// kBytes (4 or 16) from global to shared memory without a register between;
+// with bytes = 0 nothing is read and they become zero.
+template <int kBytes>
+__device__ __forceinline__ void copy_piece(uint32_t to, const void *from, uint32_t bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All of this thread's groups but the last kPending have landed.
@@ -321,6 +339,12 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned threads, size
 
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ void load_shared(uint32_t at, uint4 &v) { v = shared16(at); }
+__device__ __forceinline__ void load_shared(uint32_t at, unsigned int &v)
+{
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+}
 
 inline bool aligned_to(const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 

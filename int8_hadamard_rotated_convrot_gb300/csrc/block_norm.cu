@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
                 // (a piece past the row reads nothing, but its address stays inside)
                 const int at = inside[j] ? col + j * pitch : 0;
                 const uint32_t bytes = inside[j] ? 16 : 0;
-                copy16(to + j * step, x + at, bytes);
-                if constexpr (kBranch) copy16(to + (kNv + j) * step, y + at, bytes);
+                copy_piece<16>(to + j * step, x + at, bytes);
+                if constexpr (kBranch) copy_piece<16>(to + (kNv + j) * step, y + at, bytes);
             } else {
                 ahead_x[j] = inside[j] ? x[col + j * pitch] : from_f32<T>(0.0f);
                 if constexpr (kBranch) ahead_y[j] = inside[j] ? y[col + j * pitch] : from_f32<T>(0.0f);
@@ -645,11 +645,12 @@ template <typename T, typename P, int kVec, int kCluster>
 __global__ void __launch_bounds__(kGradThreads, 1)
     norm_grad_kernel(const __grid_constant__ convrot_gated_norm_backward_args a, const __grid_constant__ GradSplit split, float *part)
 {
-    // kGradCols columns a thread, in kNv pieces of kVec, and in pairs for the packed arithmetic. 16-byte pieces
-    // come through a ring of rows in shared memory that each thread fills for itself, single elements directly.
+    // kGradCols columns a thread, in kNv pieces of kVec, and in pairs for the packed arithmetic. Pieces of 16 or 4
+    // bytes come through a ring of rows in shared memory that each thread fills for itself, 2-byte ones directly.
     constexpr int kNv = kGradCols / kVec, kPairs = kGradCols / 2, kStages = grad_stages<T>();
-    constexpr bool kRing = kVec > 1;
-    extern __shared__ uint4 ring[];  // [kStages][h, y, dh, dn][kNv][blockDim]
+    constexpr int kPiece = kVec * static_cast<int>(sizeof(T));
+    constexpr bool kRing = kPiece >= 4;
+    extern __shared__ uint4 ring[];  // [kStages][h, y, dh, dn][kNv][blockDim] pieces
     __shared__ float slots[2 * 8 * 36];
     __shared__ float peers[2 * kCluster * 8];
     GradSum<kCluster> sum{slots, peers};
@@ -678,15 +679,16 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         if (in[2]) in[2] += a.lddh;
         if (in[3]) in[3] += a.lddn;
     };
-    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
-    const uint32_t piece = nt * 16;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * kPiece;
+    const uint32_t piece = nt * kPiece;
     auto fetch = [&](int stage) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (in[k])
 #pragma unroll
                 for (int j = 0; j < kNv; ++j)
-                    copy16(mine + ((stage * 4 + k) * kNv + j) * piece, in[k] + (inside(j) ? j * nt * kVec : -at(0)), inside(j) ? 16 : 0);
+                    copy_piece<kRing ? kPiece : 4>(mine + ((stage * 4 + k) * kNv + j) * piece, in[k] + (inside(j) ? j * nt * kVec : -at(0)),
+                                                   inside(j) ? kPiece : 0);
         advance();
     };
     int stage = 0, ahead = kStages - 1;
@@ -696,14 +698,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
             for (int j = 0; j < kNv; ++j) {
                 Raw<T, kVec> raw{};
-                if (in[k]) raw.bits[0] = shared16(mine + ((stage * 4 + k) * kNv + j) * piece);
-                raw.unpack(v + j * kVec / 2);
+                if (in[k]) load_shared(mine + ((stage * 4 + k) * kNv + j) * piece, raw.bits[0]);
+                if constexpr (kVec > 1) {
+                    raw.unpack(v + j * kVec / 2);
+                } else {
+                    if (j % 2) v[j / 2] = F2(v[j / 2].lo(), raw.value());
+                    else v[j / 2] = F2(raw.value(), 0.0f);
+                }
             }
         } else {
+            // all loads first, from the row's start where there is no such column
+            T raw[2 * kPairs];
+#pragma unroll
+            for (int j = 0; j < kNv; ++j) raw[j] = in[k] ? in[k][inside(j) ? j * nt : -at(0)] : from_f32<T>(0.0f);
 #pragma unroll
             for (int e = 0; e < kPairs; ++e)
-                v[e] = F2(in[k] && inside(2 * e) ? to_f32(in[k][2 * e * nt]) : 0.0f,
-                          in[k] && inside(2 * e + 1) ? to_f32(in[k][(2 * e + 1) * nt]) : 0.0f);
+                v[e] = F2(inside(2 * e) ? to_f32(raw[2 * e]) : 0.0f, inside(2 * e + 1) ? to_f32(raw[2 * e + 1]) : 0.0f);
         }
     };
     auto put = [&](T *p, const F2 (&v)[kPairs]) {
@@ -712,7 +722,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             for (int j = 0; j < kNv; ++j) {
                 if (!inside(j)) continue;
                 Raw<T, kVec> raw;
-                raw.pack(v + j * kVec / 2);
+                if constexpr (kVec > 1)
+                    raw.pack(v + j * kVec / 2);
+                else
+                    raw.set(j % 2 ? v[j / 2].hi() : v[j / 2].lo());
                 raw.store_stream(p + j * nt * kVec);
             }
         } else {
@@ -876,7 +889,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
         for (int j = 0; j < kNv; ++j) {
             if (!inside(j)) continue;
-            if constexpr (kRing) {
+            if constexpr (kVec > 1) {
                 Raw<float, kVec> raw;
                 raw.pack(v + j * kVec / 2);
                 raw.store(p + at(j));
@@ -1112,7 +1125,7 @@ struct grad_tag;
 template <typename T, typename P, int kVec, int kCluster>
 cudaError_t launch_grad(const convrot_gated_norm_backward_args &a, const GradSplit &s, float *part, cudaStream_t stream)
 {
-    const int bytes = kVec == 1 ? 0 : grad_stages<T>() * 4 * (kGradCols / kVec) * s.threads * 16;
+    const int bytes = kVec * sizeof(T) < 4 ? 0 : grad_stages<T>() * 4 * kGradCols * static_cast<int>(sizeof(T)) * s.threads;
     auto kernel = norm_grad_kernel<T, P, kVec, kCluster>;
     const cudaError_t e = allow_shared<grad_tag<T, P, kVec, kCluster>>(kernel);
     if (e != cudaSuccess) return e;
@@ -1125,21 +1138,29 @@ cudaError_t launch_gated_norm_backward(const convrot_gated_norm_backward_args &a
     return with_types(a.dtype, a.param_dtype, [&](auto *tt, auto *pp) -> cudaError_t {
         using T = std::remove_pointer_t<decltype(tt)>;
         using P = std::remove_pointer_t<decltype(pp)>;
-        constexpr int kVec = 16 / sizeof(T), kT = sizeof(T), kP = sizeof(P);
+        constexpr int kVec = 16 / sizeof(T), kT = sizeof(T);
         const GradSplit s(a.m, a.d, a.rows_per_batch);
         float *part = static_cast<float *>(a.work), *weights = part + s.units() * 4 * a.d;
-        const bool wide = a.d % kVec == 0 && vectors(a.h, a.m, a.ldh, kVec, kT) && vectors(a.y, a.m, a.ldy, kVec, kT) &&
-                          vectors(a.dh, a.m, a.lddh, kVec, kT) && vectors(a.dn, a.m, a.lddn, kVec, kT) &&
-                          vectors(a.dx, a.m, a.lddx, kVec, kT) && vectors(a.dy, a.m, a.lddy, kVec, kT) &&
-                          vectors(a.gate, s.batches, a.ldgate, kVec, kP) && vectors(a.scale, s.batches, a.ldscale, kVec, kP) &&
-                          vectors(a.post_weight, 1, a.d, kVec, kP) && vectors(a.pre_weight, 1, a.d, kVec, kP);
+        // the rows' pieces: 16 bytes, 4, or single 16-bit elements
+        auto pieces = [&](int vec) {
+            return a.d % vec == 0 && vectors(a.h, a.m, a.ldh, vec, kT) && vectors(a.y, a.m, a.ldy, vec, kT) &&
+                   vectors(a.dh, a.m, a.lddh, vec, kT) && vectors(a.dn, a.m, a.lddn, vec, kT) &&
+                   vectors(a.dx, a.m, a.lddx, vec, kT) && vectors(a.dy, a.m, a.lddy, vec, kT);
+        };
+        auto launch = [&](auto vec) {
+            constexpr int kV = decltype(vec)::value;
+            if (s.cluster == 1) return launch_grad<T, P, kV, 1>(a, s, part, stream);
+            if (s.cluster == 2) return launch_grad<T, P, kV, 2>(a, s, part, stream);
+            return launch_grad<T, P, kV, 4>(a, s, part, stream);
+        };
+        constexpr int kSmall = 4 / kT;
         cudaError_t e;
-        if (s.cluster == 1)
-            e = wide ? launch_grad<T, P, kVec, 1>(a, s, part, stream) : launch_grad<T, P, 1, 1>(a, s, part, stream);
-        else if (s.cluster == 2)
-            e = wide ? launch_grad<T, P, kVec, 2>(a, s, part, stream) : launch_grad<T, P, 1, 2>(a, s, part, stream);
+        if (pieces(kVec))
+            e = launch(std::integral_constant<int, kVec>{});
+        else if (pieces(kSmall))
+            e = launch(std::integral_constant<int, kSmall>{});
         else
-            e = wide ? launch_grad<T, P, kVec, 4>(a, s, part, stream) : launch_grad<T, P, 1, 4>(a, s, part, stream);
+            e = launch(std::integral_constant<int, 1>{});
         if (e != cudaSuccess) return e;
         const bool per_weight = a.dpre_weight || a.dpre_bias || a.dpost_weight || a.dpost_bias;
         if (!per_weight && !a.dshift && !a.dscale && !a.dgate) return cudaSuccess;
