@@ -174,12 +174,14 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
 
     Raw<T, kVec> xr[kNv], yr[kNv];
     const T *x = static_cast<const T *>(a.x) + r * a.ldx, *y = static_cast<const T *>(a.y) + r * a.ldy;
+    // (a piece past the row loads the row's start: loads behind branches would wait for one another)
+    auto clamped = [&](int j) { return in_row(j) ? at(j) : 0; };
 #pragma unroll
-    for (int j = 0; j < kNv; ++j)
-        if (in_row(j)) {
-            xr[j].load_stream(x + at(j));
-            if (a.y) yr[j].load_stream(y + at(j));
-        }
+    for (int j = 0; j < kNv; ++j) xr[j].load_stream(x + clamped(j));
+    if (a.y) {
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) yr[j].load_stream(y + clamped(j));
+    }
     float h[kNv][kVec];
     if (a.y) {
 #pragma unroll
@@ -193,70 +195,49 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
         }
         normalize(h, d, a.post, a.eps, sum, in_row);
     }
+    // h[j][e] = f(h[j][e], p[column]) for a vector of columns, if there is one
+    auto apply = [&](const void *p, int64_t offset, auto f) {
+        if (!p) return;
+        float v[kNv][kVec];
+#pragma unroll
+        for (int j = 0; j < kNv; ++j) params<P>(p, offset + clamped(j), 0.0f, v[j]);
+#pragma unroll
+        for (int j = 0; j < kNv; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) h[j][e] = f(h[j][e], v[j][e]);
+    };
+    auto times = [](float v, float p) { return v * p; };
+    auto plus = [](float v, float p) { return v + p; };
+    if (a.y) {
+        apply(a.post_weight, 0, times);
+        apply(a.post_bias, 0, plus);
+        apply(a.gate, b * a.ldgate, times);
+    }
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
-        if (!in_row(j)) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = 0.0f;
-            continue;
-        }
-        const int i = at(j);
         float xv[kVec];
         xr[j].unpack(xv);
-        if (a.y) {
-            float p[kVec];
-            if (a.post_weight) {
-                params<P>(a.post_weight, i, 1.0f, p);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) h[j][e] *= p[e];
-            }
-            if (a.post_bias) {
-                params<P>(a.post_bias, i, 0.0f, p);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) h[j][e] += p[e];
-            }
-            params<P>(a.gate, b * a.ldgate + i, 1.0f, p);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = fmaf(a.res_scale, xv[e], p[e] * h[j][e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = a.res_scale * xv[e];
-        }
-        if (a.h) {
+        for (int e = 0; e < kVec; ++e) h[j][e] = !in_row(j) ? 0.0f : a.y ? fmaf(a.res_scale, xv[e], h[j][e]) : a.res_scale * xv[e];
+        if (a.h && in_row(j)) {
             xr[j].pack(h[j]);
-            xr[j].store(static_cast<T *>(a.h) + r * a.ldh + i);
+            xr[j].store(static_cast<T *>(a.h) + r * a.ldh + at(j));
         }
     }
     if (!a.n && !a.q) return;
     normalize(h, d, a.pre, a.eps, sum, in_row);
+    apply(a.pre_weight, 0, times);
+    apply(a.pre_bias, 0, plus);
+    apply(a.scale, b * a.ldscale, [](float v, float p) { return fmaf(v, p, v); });
+    apply(a.shift, b * a.ldshift, plus);
 #pragma unroll
     for (int j = 0; j < kNv; ++j) {
-        if (!in_row(j)) continue;
-        const int i = at(j);
-        float p[kVec];
-        if (a.pre_weight) {
-            params<P>(a.pre_weight, i, 1.0f, p);
+        if (!in_row(j)) {  // stays out of the packed block's maximum
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] *= p[e];
-        }
-        if (a.pre_bias) {
-            params<P>(a.pre_bias, i, 0.0f, p);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] += p[e];
-        }
-        if (a.scale) {
-            params<P>(a.scale, b * a.ldscale + i, 0.0f, p);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] = fmaf(h[j][e], p[e], h[j][e]);
-        }
-        if (a.shift) {
-            params<P>(a.shift, b * a.ldshift + i, 0.0f, p);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) h[j][e] += p[e];
-        }
-        if (a.n) {
+            for (int e = 0; e < kVec; ++e) h[j][e] = 0.0f;
+        } else if (a.n) {
             xr[j].pack(h[j]);
-            xr[j].store(static_cast<T *>(a.n) + r * a.ldn + i);
+            xr[j].store(static_cast<T *>(a.n) + r * a.ldn + at(j));
         }
     }
     if (!a.q) return;
@@ -307,25 +288,26 @@ __global__ void __launch_bounds__(kRowThreads) gated_norm_kernel(const __grid_co
 // leaves), so everything that a sample's rows share is prepared once, in
 // registers: gate w_post, (1 + scale) w_pre and (1 + scale) b_pre + shift;
 // values past the row are zeros and need no branch.
-// kWide: each thread copies its own 16-byte pieces of the next rows into its
-// own places in shared memory (cp.async), kStages - 1 rows ahead. What a thread
+// kVec > 0: each thread copies its own pieces (16 or 4 bytes) of the next rows
+// into its own places in shared memory (cp.async), kStages - 1 rows ahead. What a thread
 // copied it reads back itself, so the ring needs no barrier, and HBM stays busy
 // through the sums around the block. Otherwise single elements, kThreads apart,
 // the next row's loaded into registers before this one's sums.
-template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
+template <typename T, typename P, int kNv, int kVec, int kThreads, bool kBranch>
 __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const __grid_constant__ convrot_gated_norm_args a, int32_t rows)
 {
-    constexpr int kVec = kWide ? 16 / static_cast<int>(sizeof(T)) : 1;
+    constexpr int kPiece = kVec * static_cast<int>(sizeof(T));
+    constexpr bool kWide = kPiece >= 4;  // through shared memory
     constexpr int kStages = kRingStages, kPieces = kNv * (kBranch ? 2 : 1), kValues = kNv * kVec, kPairs = kValues / 2;
-    extern __shared__ uint4 ring[];  // kWide: [kStages][x, y][kNv][blockDim]
+    extern __shared__ uint4 ring[];  // kWide: [kStages][x, y][kNv][blockDim] pieces
     __shared__ float2 slots[64];
     after_previous();
     let_next_start();
     const int nt = kThreads ? kThreads : blockDim.x, d = static_cast<int>(a.d);
     const float inv_d = 1.0f / d;
     RowSum<false> sum{slots};
-    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * 16;
-    const uint32_t step = nt * 16, stage_bytes = step * kPieces;
+    const uint32_t mine = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + threadIdx.x * kPiece;
+    const uint32_t step = nt * kPiece, stage_bytes = step * kPieces;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * rows;
     const int count = static_cast<int>(a.m - first < rows ? a.m - first : rows);
     const int pitch = nt * kVec, col = static_cast<int>(threadIdx.x) * kVec;  // piece j: columns col + j pitch on
@@ -341,9 +323,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
             if constexpr (kWide) {
                 // (a piece past the row reads nothing, but its address stays inside)
                 const int at = inside[j] ? col + j * pitch : 0;
-                const uint32_t bytes = inside[j] ? 16 : 0;
-                copy_piece<16>(to + j * step, x + at, bytes);
-                if constexpr (kBranch) copy_piece<16>(to + (kNv + j) * step, y + at, bytes);
+                const uint32_t bytes = inside[j] ? kPiece : 0;
+                copy_piece<kPiece>(to + j * step, x + at, bytes);
+                if constexpr (kBranch) copy_piece<kPiece>(to + (kNv + j) * step, y + at, bytes);
             } else {
                 ahead_x[j] = inside[j] ? x[col + j * pitch] : from_f32<T>(0.0f);
                 if constexpr (kBranch) ahead_y[j] = inside[j] ? y[col + j * pitch] : from_f32<T>(0.0f);
@@ -434,8 +416,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
 #pragma unroll
                 for (int j = 0; j < kNv; ++j) {
                     Raw<T, kVec> raw;
-                    raw.bits[0] = shared16(stage + (k * kNv + j) * step);
-                    raw.unpack(v + j * kVec / 2);
+                    load_shared(stage + (k * kNv + j) * step, raw.bits[0]);
+                    if constexpr (kVec > 1)
+                        raw.unpack(v + j * kVec / 2);
+                    else
+                        v[j / 2] = j % 2 ? F2(v[j / 2].lo(), raw.value()) : F2(raw.value(), 0.0f);
                 }
             } else {
 #pragma unroll
@@ -471,7 +456,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
         auto put = [&](T *p) {
 #pragma unroll
             for (int j = 0; j < kNv; ++j) {
-                if constexpr (kWide) {
+                if constexpr (kVec > 1) {
                     Raw<T, kVec> raw;
                     raw.pack(h + j * kVec / 2);
                     if (inside[j]) raw.store_stream(p + j * pitch);
@@ -495,7 +480,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
             put(n_out);
             n_out += a.ldn;
         }
-        if constexpr (kWide) {
+        if constexpr (kPiece == 16) {
             if (a.q) {
                 float v[kNv][kVec];
 #pragma unroll
@@ -505,6 +490,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
                 }
                 pack_row<kVec, kNv>(a, first + r, d, threadIdx.x, nt, v);
             }
+        }
+        if constexpr (kWide) {
             if ((stage += stage_bytes) == ring_end) stage = mine;
         }
         fresh = --left == 0;
@@ -709,8 +696,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         } else {
             // all loads first, from the row's start where there is no such column
             T raw[2 * kPairs];
+            if (in[k]) {
 #pragma unroll
-            for (int j = 0; j < kNv; ++j) raw[j] = in[k] ? in[k][inside(j) ? j * nt : -at(0)] : from_f32<T>(0.0f);
+                for (int j = 0; j < kNv; ++j) raw[j] = in[k][inside(j) ? j * nt : -at(0)];
+            } else {
+#pragma unroll
+                for (int j = 0; j < kNv; ++j) raw[j] = from_f32<T>(0.0f);
+            }
 #pragma unroll
             for (int e = 0; e < kPairs; ++e)
                 v[e] = F2(inside(2 * e) ? to_f32(raw[2 * e]) : 0.0f, inside(2 * e + 1) ? to_f32(raw[2 * e + 1]) : 0.0f);
@@ -1028,24 +1020,24 @@ cudaError_t launch_block_rows(const convrot_gated_norm_args &a, cudaStream_t str
 
 constexpr int kRingBytes = 192 * 1024;  // shared memory an SM gives its rings; the rest stays L1 for the vectors
 
-template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
+template <typename T, typename P, int kNv, int kVec, int kThreads, bool kBranch>
 struct ring_tag;
 
 // Runs of rows, if there are enough of them: four a block, so that preparing the sample's vectors (and filling the
 // ring, which has to fit) is a small part.
-template <typename T, typename P, int kNv, bool kWide, int kThreads, bool kBranch>
+template <typename T, typename P, int kNv, int kVec, int kThreads, bool kBranch>
 bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
 {
-    constexpr int kVec = kWide ? 16 / static_cast<int>(sizeof(T)) : 1;
+    constexpr int kPiece = kVec * static_cast<int>(sizeof(T));
     const int threads = kThreads ? kThreads : static_cast<int>((a.d / kVec + kNv - 1) / kNv + 31) / 32 * 32;
-    const int bytes = kWide ? kRingStages * (kBranch ? 2 : 1) * kNv * threads * 16 : 0;
+    const int bytes = kPiece >= 4 ? kRingStages * (kBranch ? 2 : 1) * kNv * threads * kPiece : 0;
     int per_sm = kRingThreads / threads;
-    if (kWide && kRingBytes / bytes < per_sm) per_sm = kRingBytes / bytes;
+    if (bytes && kRingBytes / bytes < per_sm) per_sm = kRingBytes / bytes;
     if (per_sm < 1) return false;
     const int64_t blocks = static_cast<int64_t>(per_sm) * kSms;
     if (a.m < 4 * blocks) return false;
-    auto kernel = gated_norm_ring_kernel<T, P, kNv, kWide, kThreads, kBranch>;
-    *e = allow_shared<ring_tag<T, P, kNv, kWide, kThreads, kBranch>>(kernel);
+    auto kernel = gated_norm_ring_kernel<T, P, kNv, kVec, kThreads, kBranch>;
+    *e = allow_shared<ring_tag<T, P, kNv, kVec, kThreads, kBranch>>(kernel);
     if (*e != cudaSuccess) return true;
     const int64_t rows = (a.m + blocks - 1) / blocks;
     *e = launch_after(kernel, dim3(static_cast<unsigned>((a.m + rows - 1) / rows)), static_cast<unsigned>(threads), bytes, stream, 1, a,
@@ -1053,10 +1045,10 @@ bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaErro
     return true;
 }
 
-template <typename T, typename P, int kNv, bool kWide, int kThreads = 0>
+template <typename T, typename P, int kNv, int kVec, int kThreads = 0>
 bool launch_ring(const convrot_gated_norm_args &a, cudaStream_t stream, cudaError_t *e)
 {
-    return a.y ? launch_ring<T, P, kNv, kWide, kThreads, true>(a, stream, e) : launch_ring<T, P, kNv, kWide, kThreads, false>(a, stream, e);
+    return a.y ? launch_ring<T, P, kNv, kVec, kThreads, true>(a, stream, e) : launch_ring<T, P, kNv, kVec, kThreads, false>(a, stream, e);
 }
 
 // A warp for each row, four rows a block.
@@ -1084,7 +1076,7 @@ cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t str
         if (wide) {
             const int64_t n = a.d / kVec;
             cudaError_t e;
-            if (n > 256 ? launch_ring<T, P, 16 / kVec, true>(a, stream, &e) : launch_ring<T, P, 1, true>(a, stream, &e)) return e;
+            if (n > 256 ? launch_ring<T, P, 16 / kVec, kVec>(a, stream, &e) : launch_ring<T, P, 1, kVec>(a, stream, &e)) return e;
             if (n <= 32) return launch_warp_rows<T, P, kVec, 1>(a, stream);
             if (n <= kRowThreads) return launch_block_rows<T, P, kVec, 1>(a, stream);
             if (n <= 2 * kRowThreads) return launch_block_rows<T, P, kVec, 2>(a, stream);
@@ -1093,17 +1085,24 @@ cudaError_t launch_gated_norm(const convrot_gated_norm_args &a, cudaStream_t str
         if (a.d <= 128) return launch_warp_rows<T, P, 1, 4>(a, stream);
         cudaError_t e;
         if (!a.q) {
-            bool done = false;
-            if (a.d <= 512)
-                done = launch_ring<T, P, 8, false, 64>(a, stream, &e);
-            else if (a.d <= 1024)
-                done = launch_ring<T, P, 8, false, 128>(a, stream, &e);
-            else if (a.d <= 1536)
-                done = launch_ring<T, P, 12, false, 128>(a, stream, &e);
-            else if (a.d <= 3072)
-                done = launch_ring<T, P, 12, false, 256>(a, stream, &e);
-            else if (a.d <= 6144)
-                done = launch_ring<T, P, 12, false, 512>(a, stream, &e);
+            // pieces of 4 bytes where rows start on 4, single elements otherwise
+            constexpr int kSmall = 4 / kT;
+            const bool small = a.d % kSmall == 0 && vectors(a.x, a.m, a.ldx, kSmall, kT) && vectors(a.y, a.m, a.ldy, kSmall, kT) &&
+                               vectors(a.h, a.m, a.ldh, kSmall, kT) && vectors(a.n, a.m, a.ldn, kSmall, kT) &&
+                               vectors(a.gate, batches, a.ldgate, kSmall, kP) && vectors(a.scale, batches, a.ldscale, kSmall, kP) &&
+                               vectors(a.shift, batches, a.ldshift, kSmall, kP) && vectors(a.post_weight, 1, a.d, kSmall, kP) &&
+                               vectors(a.post_bias, 1, a.d, kSmall, kP) && vectors(a.pre_weight, 1, a.d, kSmall, kP) &&
+                               vectors(a.pre_bias, 1, a.d, kSmall, kP);
+            auto runs = [&](auto vec) {
+                constexpr int kV = decltype(vec)::value;
+                if (a.d <= 512) return launch_ring<T, P, 8 / kV, kV, 64>(a, stream, &e);
+                if (a.d <= 1024) return launch_ring<T, P, 8 / kV, kV, 128>(a, stream, &e);
+                if (a.d <= 1536) return launch_ring<T, P, 12 / kV, kV, 128>(a, stream, &e);
+                if (a.d <= 3072) return launch_ring<T, P, 12 / kV, kV, 256>(a, stream, &e);
+                if (a.d <= 6144) return launch_ring<T, P, 12 / kV, kV, 512>(a, stream, &e);
+                return false;
+            };
+            const bool done = small ? runs(std::integral_constant<int, kSmall>{}) : runs(std::integral_constant<int, 1>{});
             if (done) return e;
         }
         // single elements: blocks of 128 to 512 threads, enough values in each that the sums' cost is spread
