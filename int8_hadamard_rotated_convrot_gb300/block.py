@@ -269,9 +269,12 @@ def rotary_frequencies(pairs: int, base: float = 10000.0, *, scaling: str = "non
       "ntk"     the base raised by factor^(pairs / (pairs - 1)): the fastest pair keeps its frequency and the slowest
                 is divided by factor
       "yarn"    pairs that turn more than beta_fast times over original_length keep their frequency, those that turn
-                less than beta_slow times are divided by factor, a linear ramp over the pair index in between; the
-                attention factor is 0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window Extension of
-                Large Language Models", sections 3.2 to 3.4)."""
+                less than beta_slow times are divided by factor, with a linear ramp over the pair index in between
+                (from pair 0 on, where even that one turns less than beta_fast times); the attention factor is
+                0.1 ln(factor) + 1. The method, its two limits and the factor are Peng et al.'s, "YaRN: Efficient
+                Context Window Extension of Large Language Models", sections 3.2 to 3.4. Their text's ramp is linear
+                in the number of turns; the one over the pair index, between the whole indices around both limits, is
+                that of their released models, whose checkpoints need it."""
     if pairs < 1 or base <= 0 or factor < 1:
         raise ValueError("pairs >= 1, base > 0 and factor >= 1 are needed")
     if scaling == "ntk" and pairs > 1:
@@ -289,10 +292,13 @@ def rotary_frequencies(pairs: int, base: float = 10000.0, *, scaling: str = "non
     def pair_of(turns: float) -> float:  # the (real) pair index that turns this often over original_length
         return pairs * math.log(original_length / (turns * 2 * math.pi)) / math.log(base)
 
-    low = max(math.floor(pair_of(beta_fast)), 0)
-    high = min(math.ceil(pair_of(beta_slow)), pairs - 1)
-    ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(pairs)]
-    return [f * (1 - r) + f / factor * r for f, r in zip(freq, ramp)], 0.1 * math.log(factor) + 1.0
+    # the ramp's ends, not cut off at the last pair: where even that one turns more than beta_slow times it is part way up
+    start, end = max(math.floor(pair_of(beta_fast)), 0), math.ceil(pair_of(beta_slow))
+
+    def divided(i: int) -> float:  # 0: kept, 1: divided by factor
+        return min(max(i - start, 0) / (end - start), 1.0) if end > start else float(i > start)
+
+    return [f * (1 - divided(i)) + f / factor * divided(i) for i, f in enumerate(freq)], 0.1 * math.log(factor) + 1.0
 
 
 def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: float = 1.0, device=None,

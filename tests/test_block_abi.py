@@ -239,3 +239,20 @@ def test_rotary_frequencies():
     for bad in (dict(pairs=0), dict(pairs=4, factor=0.5), dict(pairs=4, scaling="yarn"), dict(pairs=4, scaling="other")):
         with pytest.raises(ValueError):
             bl.rotary_frequencies(**bad)
+
+
+@pytest.mark.parametrize("pairs,base,length,factor", [
+    (64, 10000.0, 4096, 16.0), (64, 10000.0, 131072, 8.0), (32, 10000.0, 1 << 20, 4.0), (48, 500000.0, 8192, 8.0), (8, 100.0, 100000, 2.0)])
+def test_yarn_ramp_of_long_trained_lengths(pairs, base, length, factor):
+    """Each pair's frequency from the definition: also where even the slowest pair turns more than beta_slow times."""
+    got, _ = bl.rotary_frequencies(pairs, base, scaling="yarn", factor=factor, original_length=length)
+    at = lambda turns: pairs * math.log(length / (2 * math.pi * turns), base)
+    start, end = max(math.floor(at(32.0)), 0), math.ceil(at(1.0))
+    for i, f in enumerate(got):
+        plain = base ** (-i / pairs)
+        t = (i - start) / (end - start)
+        t = 0.0 if t < 0 else 1.0 if t > 1 else t
+        assert math.isclose(f, plain * ((1 - t) + t / factor), rel_tol=1e-9), i
+        turns = length * plain / (2 * math.pi)
+        if turns > 1.0 and i < end:
+            assert f > plain / factor * (1 + 1e-9), f"pair {i} turns {turns:.2f} times and is divided by the whole factor"
