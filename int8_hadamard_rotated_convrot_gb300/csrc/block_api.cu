@@ -79,6 +79,9 @@ int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t work_ldq(int64_t k) { return groups(k, 16) * 16; }
 int64_t work_lds(int64_t m) { return groups(m, 4) * 4; }
 
+// Rows of a sample, with no more than there are (so that sums of rows stay far from 64 bits).
+int64_t sample_of(int64_t m, int64_t rows) { return rows < m ? rows : m > 1 ? m : 1; }
+
 convrot_status check_norm(int64_t m, int64_t d, int64_t rows, int dtype, int param_dtype, int post, int pre, float eps)
 {
     if (m < 0 || m > kMaxRows || d < 1 || rows < 1 || !known(dtype)) return CONVROT_ERR_INVALID_ARG;
@@ -155,7 +158,7 @@ convrot_status convrot_gated_norm(const convrot_gated_norm_args *a, cudaStream_t
     convrot_status st = check_norm(a->m, a->d, a->rows_per_batch, a->dtype, a->param_dtype, a->post, a->pre, a->eps);
     if (st != CONVROT_OK) return st;
     const int s = size_of(a->dtype), p = size_of(a->param_dtype);
-    const int64_t m = a->m, d = a->d, batches = groups(m, a->rows_per_batch);
+    const int64_t m = a->m, d = a->d, rows = sample_of(m, a->rows_per_batch), batches = groups(m, rows);
     st = first_of({check_matrix(a->x, m, d, a->ldx, s), check_optional(a->y, m, d, a->ldy, s),
                    check_optional(a->gate, batches, d, a->ldgate, p), check_optional(a->scale, batches, d, a->ldscale, p),
                    check_optional(a->shift, batches, d, a->ldshift, p), check_optional(a->post_weight, 1, d, d, p),
@@ -166,13 +169,15 @@ convrot_status convrot_gated_norm(const convrot_gated_norm_args *a, cudaStream_t
     if (st != CONVROT_OK || m == 0) return st;
     if (a->h == a->x && a->ldh != a->ldx) return CONVROT_ERR_INVALID_ARG;
     if (!a->h && !a->n && !a->q) return CONVROT_OK;
-    return done(launch_gated_norm(*a, stream));
+    convrot_gated_norm_args b = *a;
+    b.rows_per_batch = rows;
+    return done(launch_gated_norm(b, stream));
 }
 
 int64_t convrot_gated_norm_backward_work_bytes(int64_t m, int64_t d, int64_t rows_per_batch)
 {
     if (m < 1 || m > kMaxRows || d < 1 || d > CONVROT_NORM_MAX_D || rows_per_batch < 1) return 0;
-    return round256(gated_norm_backward_work_bytes(m, d, rows_per_batch));
+    return round256(gated_norm_backward_work_bytes(m, d, sample_of(m, rows_per_batch)));
 }
 
 convrot_status convrot_gated_norm_backward(const convrot_gated_norm_backward_args *a, cudaStream_t stream)
@@ -181,7 +186,7 @@ convrot_status convrot_gated_norm_backward(const convrot_gated_norm_backward_arg
     convrot_status st = check_norm(a->m, a->d, a->rows_per_batch, a->dtype, a->param_dtype, a->post, a->pre, a->eps);
     if (st != CONVROT_OK) return st;
     const int s = size_of(a->dtype), p = size_of(a->param_dtype);
-    const int64_t m = a->m, d = a->d, batches = groups(m, a->rows_per_batch);
+    const int64_t m = a->m, d = a->d, rows = sample_of(m, a->rows_per_batch), batches = groups(m, rows);
     st = first_of({check_matrix(a->h, m, d, a->ldh, s), check_optional(a->y, m, d, a->ldy, s),
                    check_optional(a->dh, m, d, a->lddh, s), check_optional(a->dn, m, d, a->lddn, s),
                    check_optional(a->gate, batches, d, a->ldgate, p), check_optional(a->scale, batches, d, a->ldscale, p),
@@ -197,9 +202,11 @@ convrot_status convrot_gated_norm_backward(const convrot_gated_norm_backward_arg
             if (v && cudaMemsetAsync(v, 0, d * 4, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
         return CONVROT_OK;
     }
-    if (!a->work || a->work_bytes < convrot_gated_norm_backward_work_bytes(m, d, a->rows_per_batch)) return CONVROT_ERR_INVALID_ARG;
+    if (!a->work || a->work_bytes < convrot_gated_norm_backward_work_bytes(m, d, rows)) return CONVROT_ERR_INVALID_ARG;
     if (!aligned(a->work, 256)) return CONVROT_ERR_ALIGNMENT;
-    return done(launch_gated_norm_backward(*a, stream));
+    convrot_gated_norm_backward_args b = *a;
+    b.rows_per_batch = rows;
+    return done(launch_gated_norm_backward(b, stream));
 }
 
 convrot_status convrot_rotary(const convrot_rotary_args *a, cudaStream_t stream)

@@ -143,6 +143,19 @@ bool real(PyObject *o, float &v)
     return !PyErr_Occurred();
 }
 
+// Rows of a sample: all m of them by default, and at most.
+bool sample_rows(PyObject *o, int64_t m, int64_t &rows)
+{
+    const int64_t all = m > 0 ? m : 1;
+    if (o == Py_None) {
+        rows = all;
+        return true;
+    }
+    if (!integer(o, rows)) return false;
+    if (rows > all) rows = all;
+    return true;
+}
+
 PyObject *status(convrot_status s) { return PyLong_FromLong(s); }
 
 bool count(Py_ssize_t got, Py_ssize_t want)
@@ -274,8 +287,7 @@ PyObject *gated_norm(PyObject *, PyObject *const *v, Py_ssize_t n)
     a.param_dtype = code_of(p);
     a.m = x->size(0);
     a.d = x->size(1);
-    a.rows_per_batch = a.m > 0 ? a.m : 1;
-    if (v[5] != Py_None) REQUIRE(integer(v[5], a.rows_per_batch));
+    REQUIRE(sample_rows(v[5], a.m, a.rows_per_batch));
     if (a.rows_per_batch < 1) return status(CONVROT_ERR_INVALID_ARG);
     const int64_t m = a.m, d = a.d, batches = (m + a.rows_per_batch - 1) / a.rows_per_batch;
     Matrix mx, my, mg, mc, mf, mh, mn, mq{nullptr, 0}, ms{nullptr, 0};
@@ -338,8 +350,7 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
     a.param_dtype = code_of(p);
     a.m = h->size(0);
     a.d = h->size(1);
-    a.rows_per_batch = a.m > 0 ? a.m : 1;
-    if (v[7] != Py_None) REQUIRE(integer(v[7], a.rows_per_batch));
+    REQUIRE(sample_rows(v[7], a.m, a.rows_per_batch));
     if (a.rows_per_batch < 1) return status(CONVROT_ERR_INVALID_ARG);
     const int64_t m = a.m, d = a.d, batches = (m + a.rows_per_batch - 1) / a.rows_per_batch;
     Matrix mh, my, mdh, mdn, mg, mc, mf;

@@ -256,3 +256,13 @@ def test_yarn_ramp_of_long_trained_lengths(pairs, base, length, factor):
         turns = length * plain / (2 * math.pi)
         if turns > 1.0 and i < end:
             assert f > plain / factor * (1 + 1e-9), f"pair {i} turns {turns:.2f} times and is divided by the whole factor"
+
+
+@pytest.mark.parametrize("rows", [41, 1 << 31, (1 << 63) - 40, (1 << 63) - 1])
+def test_samples_longer_than_the_call(lib, rows):
+    """Any number of rows a sample: what is past the last row does not count."""
+    assert lib.convrot_gated_norm_backward_work_bytes(40, 64, rows) == lib.convrot_gated_norm_backward_work_bytes(40, 64, 40) > 0
+    for bad in (dict(gate=FAKE, ldgate=8), dict(scale=FAKE, ldscale=8)):
+        assert lib.convrot_gated_norm_backward(grad_args(**bad, rows=rows), None) == cr.ERR_INVALID_ARG
+        assert lib.convrot_gated_norm(norm_args(**bad, rows=rows), None) == cr.ERR_INVALID_ARG
+    assert lib.convrot_gated_norm_backward(grad_args(rows=rows, work_bytes=0), None) == cr.ERR_INVALID_ARG
