@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     __shared__ float slots[2 * 8 * 36];
     __shared__ float peers[2 * kCluster * 8];
     GradSum<kCluster> sum{slots, peers};
+    // A peer's shared memory may be written once it is known to run (the first sum does): met under the wait below.
+    if constexpr (kCluster > 1) cluster_sync();
     after_previous();
     const int64_t unit = blockIdx.x / kCluster;
     const int64_t b = unit / split.chunks, chunk = unit - b * split.chunks;

@@ -637,3 +637,20 @@ def test_rotary_table():
     assert torch.isnan(cos[:, 31]).all() and torch.isfinite(cos[:, :31]).all()
     cos, sin = bl.convrot_rotary_table(0, freq, device="cuda")
     assert cos.shape == (0, 32)
+
+
+@pytest.mark.parametrize("d", [5121, 8200, 10248, 16384])
+def test_wide_gradient_of_a_row_a_cluster(d):
+    """One row for each cluster, so that every sum is the first that its blocks exchange: many clusters, back to back."""
+    m = 304
+    g = gen(d)
+    h, y, dh, dn = (randn(g, m, d, dtype=BF16) for _ in range(4))
+    got = [bl.convrot_gated_norm_backward(h, y, dh, dn, rows_per_batch=1, post=bl.NORM_RMS, pre=bl.NORM_RMS) for _ in range(20)]
+    v = {"x": h, "y": y}
+    how = {"rows": 1, "res_scale": 1.0, "post": 1, "pre": 1}
+    want, d_h = grad_reference(v, how, dh, dn)
+    sizes = grad_bounds(v, how, dh, dn, d_h)
+    for name in ("dx", "dy"):
+        close(got[0][name], want[name], rounded(want[name], BF16, C32 * sizes[name]), name)
+        for other in got[1:]:
+            assert torch.equal(other[name], got[0][name]), name
