@@ -22,6 +22,8 @@ cudaError_t launch_fp8_gemm(const convrot_fp8_linear_args &a, cudaStream_t strea
 // Few rows: whether that kernel takes the sizes, and whether it quantizes x itself.
 bool fp8_few_takes(int64_t m, int64_t n, int64_t k);
 bool fp8_few_quantizes(int64_t m, int64_t n, int64_t k);
+// Shared memory and tensor-memory columns of its CTAs (sizes that it takes).
+int fp8_few_shared(int64_t m, int64_t n, int64_t k, bool quantize, int *columns);
 cudaError_t launch_fp8_few(const convrot_fp8_linear_args &a, cudaStream_t stream);           // packed x
 cudaError_t launch_fp8_few_quantize(const convrot_fp8_linear_args &a, cudaStream_t stream);  // x as rows
 

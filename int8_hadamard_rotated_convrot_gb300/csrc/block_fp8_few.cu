@@ -80,6 +80,12 @@ struct Shape {
     static constexpr int TILE = kTok * kBK;  // x's codes of one block
     static constexpr int STAGE = kStageBytes + (kQuantize ? 0 : TILE);
     static constexpr int COLS = kTok == 16 ? 128 : 256, BUFS = COLS / kTok;
+    // Shared memory of a CTA that takes up to `share` blocks of k.
+    static int bytes(int share)
+    {
+        const int used = 1024 + kStages * STAGE + share * (kQuantize ? TILE : 0) + share * kTok * 4;
+        return used > tmem_share(COLS) ? used : tmem_share(COLS);
+    }
 };
 
 // kTok: columns of an accumulator (rows of x, rounded up); TX: type of the rows
@@ -394,13 +400,7 @@ cudaError_t launch_form(const convrot_fp8_linear_args &a, const Cut &cut, cudaSt
     p.ldy = a.ldy;
     p.vec_y = aligned_to(a.y, 4 * sizeof(T)) && (a.m <= 1 || a.ldy % 4 == 0);
     p.dev_status = a.dev_status;
-    // An allocation of tensor memory waits until there is room, and CTAs of two clusters that wait for each other's
-    // room on two SMs would wait for ever. So a CTA takes at least the part of an SM's shared memory (228 KB) that it
-    // takes of its 512 columns, less 4 KB: of such CTAs, each of 64 KB at least and of a multiple of 32 columns, three
-    // at most fit side by side, and their columns would need 544 x 456 B - 3 x 4 KB > 228 KB to be too many.
-    int bytes = 1024 + kStages * S::STAGE + cut.share * (kQuantize ? S::TILE : 0) + cut.share * kTok * 4;
-    constexpr int kPart = S::COLS * (228 * 1024 / 512) - 4096;
-    if (bytes < kPart) bytes = kPart;
+    const int bytes = S::bytes(cut.share);
     auto kernel = fp8_few_kernel<kTok, TX, T, kAct>;
     cudaError_t e = allow_shared<kernel_tag<kTok, TX, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
@@ -457,6 +457,15 @@ bool fp8_few_quantizes(int64_t m, int64_t n, int64_t k)
 {
     const Cut c = cut_of(m, n, k);
     return c.tok == 16 && c.share <= kMaxQuantize && c.share * m <= kQuantizeUnits;
+}
+
+int fp8_few_shared(int64_t m, int64_t n, int64_t k, bool quantize, int *columns)
+{
+    const Cut c = cut_of(m, n, k);
+    *columns = c.tok == 16 ? Shape<16, true>::COLS : Shape<32, false>::COLS;
+    static_assert(Shape<32, false>::COLS == Shape<64, false>::COLS);
+    if (c.tok == 16) return quantize ? Shape<16, true>::bytes(c.share) : Shape<16, false>::bytes(c.share);
+    return c.tok == 32 ? Shape<32, false>::bytes(c.share) : Shape<64, false>::bytes(c.share);
 }
 
 cudaError_t launch_fp8_few(const convrot_fp8_linear_args &a, cudaStream_t stream)

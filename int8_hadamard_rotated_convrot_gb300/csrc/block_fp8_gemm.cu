@@ -64,6 +64,7 @@ struct Cfg {
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + kDrainWarps * OUT_WARP + BAR_BYTES;
     // kind::f8f6f4: D fp32, A and B e4m3, K-major, M = 256 over both CTAs, N = kBN
     static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(kBN >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+    static_assert(SMEM > kTmemAlone, "no other tensor memory on this SM");
     static_assert(8 * (2 * STAGES + BUFS + 1) + 8 <= BAR_BYTES, "barriers fit");
     // a drain warp reads a block's end off its stage's barrier: that may not come round again before every warp has
     // seen it, and block j + STAGES waits for the drains of block j + STAGES - BUFS

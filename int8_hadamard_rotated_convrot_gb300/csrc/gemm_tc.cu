@@ -68,6 +68,7 @@ constexpr int OUT_BUF_BYTES = OUT_BOX * OUT_BOX * 4;
 constexpr int OUT_WARP_BYTES = 2 * OUT_BUF_BYTES;
 constexpr int OUT_BYTES = 8 * OUT_WARP_BYTES;
 constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + OUT_BYTES + BAR_BYTES;
+static_assert(SMEM_BYTES > kTmemAlone, "no other tensor memory on this SM");
 
 // instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major, M = 128, N = 256
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(BN >> 3) << 17) |
@@ -576,6 +577,7 @@ struct Cfg {
     static constexpr uint32_t kIdescF16 = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(256 >> 4) << 24);
     static_assert(STAGE_BYTES % 1024 == 0, "stages stay 1024-byte aligned for the 128-byte swizzle");
     static_assert(SMEM_BYTES_I8 <= 232448, "I8 rings fit the shared memory of one CTA");
+    static_assert(SMEM_BYTES > kTmemAlone && SMEM_BYTES_I8 > kTmemAlone, "no other tensor memory on this SM");
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()

@@ -67,6 +67,8 @@ cudaError_t launch_lora_prepare(const float *B, int64_t n, int32_t r, int64_t ld
                                 int64_t lde, cudaStream_t stream);
 cudaError_t launch_lora_prepare_down(const float *A, int32_t r, int32_t k, int64_t lda, float *out, int64_t ldo,
                                      cudaStream_t stream);
+// Shared memory of a CTA of lora_down, which takes all of its SM's tensor memory.
+int lora_down_shared(int r);
 cudaError_t launch_lora_down(const float *X, int64_t m, int32_t k, int64_t ldx, const float *A_ext, int32_t r,
                              int64_t lda, void *t, int64_t ldt, int32_t *dev_status, cudaStream_t stream);
 

@@ -71,6 +71,17 @@ constexpr uint32_t LD_TMEM_COLS = 512;
 constexpr uint32_t LD_XRING_COL = 256;
 constexpr uint32_t LD_XRING_STAGE_COLS = 64;
 
+constexpr int LD_FIXED_BYTES = 1024 + 256;  // alignment slack, barriers, TMEM slot and flag
+
+bool down_xh_smem(int r) { return r <= 128; }  // hi(X) read from the X slice (see launch_lora_down)
+int down_stage_bytes(int r) { return LD_X_BYTES + 2 * r * LD_BK * 4; }
+int down_stages(int r)
+{
+    const int fit = (LD_SMEM_LIMIT - LD_FIXED_BYTES) / down_stage_bytes(r);
+    const int most = down_xh_smem(r) ? LD_MAX_STAGES_LO : LD_MAX_STAGES;  // what the TMEM ring holds
+    return fit < most ? fit : most;
+}
+
 // kind::tf32: D fp32 (bit 4), A and B TF32 (format 2 at bits 7 and 10), both K-major, M = 128, N = n
 __host__ __device__ constexpr uint32_t tf32_idesc(int n)
 {
@@ -567,6 +578,12 @@ __global__ void lora_prepare_kernel(const float *B, int64_t n, int32_t r, int64_
 
 int lora_cols(int r) { return (3 * r + 63) / 64 * 64; }
 
+int lora_down_shared(int r)
+{
+    const int bytes = LD_FIXED_BYTES + down_stages(r) * down_stage_bytes(r);
+    return bytes > tmem_share(LD_TMEM_COLS) ? bytes : tmem_share(LD_TMEM_COLS);
+}
+
 cudaError_t launch_lora_prepare(const float *B, int64_t n, int32_t r, int64_t ldb, float scale, void *out,
                                 int64_t lde, cudaStream_t stream)
 {
@@ -605,12 +622,9 @@ cudaError_t launch_lora_down(const float *X, int64_t m, int32_t k, int64_t ldx, 
     p.r = r;
     p.kstages = (k + LD_BK - 1) / LD_BK;
     p.a_bytes = static_cast<uint32_t>(r) * LD_BK * 4;
-    p.stage_bytes = LD_X_BYTES + 2u * p.a_bytes;
-    const bool xh_smem = r <= 128;  // hi(X) read from the X slice (see below)
-    const int fixed = 1024 + 256;  // alignment slack, barriers, TMEM slot and flag
-    int stages = (LD_SMEM_LIMIT - fixed) / static_cast<int>(p.stage_bytes);
-    const int max_stages = xh_smem ? LD_MAX_STAGES_LO : LD_MAX_STAGES;  // what the TMEM ring holds
-    stages = stages > max_stages ? max_stages : stages;
+    p.stage_bytes = static_cast<uint32_t>(down_stage_bytes(r));
+    const bool xh_smem = down_xh_smem(r);
+    const int stages = down_stages(r);
     if (stages < 2) return cudaErrorInvalidValue;
     // the partial-T tile [128][r + 4] fp32 reuses the ring once the K loop is done
     if (static_cast<int64_t>(LD_BM) * (r + 4) * 4 > static_cast<int64_t>(stages) * p.stage_bytes)
@@ -626,7 +640,7 @@ cudaError_t launch_lora_down(const float *X, int64_t m, int32_t k, int64_t ldx, 
     p.ldt = ldt;
     p.t_cols = lora_cols(r);
     p.dev_status = dev_status;
-    const int smem = fixed + stages * static_cast<int>(p.stage_bytes);
+    const int smem = lora_down_shared(r);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t row_blocks = (m + LD_BM - 1) / LD_BM;

@@ -79,6 +79,20 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
+// An allocation of tensor memory (512 columns an SM) waits, without a limit,
+// until there is room. Blocks of clusters that wait for one another's room on
+// two SMs (of two kernels on two streams, too) would wait for ever, so room is
+// never what a block waits for: every kernel that allocates asks for at least
+// the part of an SM's shared memory that it takes of its columns, less 4 KB.
+// Each takes 128 columns or a multiple, and an SM keeps 1 KB for each block, so
+// blocks with C >= 640 columns together, C / 128 of them at most, would need
+// C x 456 - C / 128 x 3 KB >= 276480 bytes of its 233472: those that fit side
+// by side always have 512 columns or fewer.
+constexpr int kSmShared = 228 * 1024;
+constexpr int tmem_share(int columns) { return columns * (kSmShared / 512) - 4096; }
+// The kernels that allocate all 512 columns need no more than what keeps the smallest other allocation off their SM.
+constexpr int kTmemAlone = kSmShared - 2 * 1024 - tmem_share(128);
+
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
 {
