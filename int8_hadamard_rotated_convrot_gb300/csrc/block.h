@@ -342,6 +342,15 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, unsigned threads, size
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// An ordinary load. A kernel that starts before the one ahead of it ends reads what that one writes, so its loads may not
+// take the read-only path, which is for data that nobody writes while the kernel runs.
+__device__ __forceinline__ float load_f32(const float *p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ void load_shared(uint32_t at, uint4 &v) { v = shared16(at); }
 __device__ __forceinline__ void load_shared(uint32_t at, unsigned int &v)
 {

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int u = u0 + i * kXWarps, j = u / m, r = u - j * m, c = (j0 + j) * kBK + lane * 4;
                     if (u >= units) break;
                     const TX *from = static_cast<const TX *>(p.x) + r * p.ldx + c;
-                    sw_j[i] = __ldg(sw + j);
+                    sw_j[i] = load_f32(sw + j);
                     if (p.wide_x && c + 4 <= p.k) {
                         Raw<TX, 4> four;
                         four.load(from);
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         } else {
             for (int i = threadIdx.x - 64; i < count * kTok; i += 32 * kXWarps) {
                 const int j = i / kTok, r = i % kTok;
-                scales[i] = r < m ? __ldg(p.x_scale + (j0 + j) * p.ld_x_scale + row0 + r) * __ldg(sw + j) : 0.0f;
+                scales[i] = r < m ? load_f32(p.x_scale + (j0 + j) * p.ld_x_scale + row0 + r) * load_f32(sw + j) : 0.0f;
             }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kXWarps) : "memory");  // every row's scales, among these warps
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int64_t col = static_cast<int64_t>(tile) * kBM + lane * 4;
         float bias[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) bias[e] = p.bias && col + e < p.n ? __ldg(p.bias + col + e) : 0.0f;
+        for (int e = 0; e < 4; ++e) bias[e] = p.bias && col + e < p.n ? load_f32(p.bias + col + e) : 0.0f;
         for (int r = static_cast<int>(rank) * kXWarps + warp - 2; r < m; r += static_cast<int>(split) * kXWarps) {
             const uint32_t at = base + (r * kBM + lane * 4) * 4;
             float4 part[kMaxSplit];

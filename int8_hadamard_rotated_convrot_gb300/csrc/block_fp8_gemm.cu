@@ -377,17 +377,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const float *sx = p.x_scale + (row_in ? row0 + lane : 0), *sw = p.w_scale + (col_in ? col0 / 128 * p.ld_w_scale : 0);
             float bias[4];  // read now, used after the tile's last block
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bias[e] = p.bias && lane * 4 < kCols && col0 + lane * 4 + e < p.n ? __ldg(p.bias + col0 + lane * 4 + e) : 0.0f;
+            for (int e = 0; e < 4; ++e) bias[e] = p.bias && lane * 4 < kCols && col0 + lane * 4 + e < p.n ? load_f32(p.bias + col0 + lane * 4 + e) : 0.0f;
             float acc[kCols];
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-            float next_x = __ldg(sx), next_w = __ldg(sw);
+            float next_x = load_f32(sx), next_w = load_f32(sw);
             for (int j = 0; j < p.blocks; ++j) {
                 const float scale = next_x * next_w;
                 if (j + 1 < p.blocks) {  // the next block's scales arrive under this block's wait
                     sx += p.ld_x_scale;
-                    next_x = __ldg(sx);
-                    next_w = __ldg(++sw);
+                    next_x = load_f32(sx);
+                    next_w = load_f32(++sw);
                 }
                 if (!wait(empty_bar(stage), phase)) {
                     ok = false;

@@ -654,3 +654,31 @@ def test_wide_gradient_of_a_row_a_cluster(d):
         close(got[0][name], want[name], rounded(want[name], BF16, C32 * sizes[name]), name)
         for other in got[1:]:
             assert torch.equal(other[name], got[0][name]), name
+
+
+@pytest.mark.parametrize("m,k,n", [(20, 1024, 2048), (64, 5120, 640), (300, 1024, 2048)])
+def test_linears_read_what_the_call_before_wrote(m, k, n):
+    """Packs and linears back to back over the same buffers, each starting while the one before drains."""
+    g = gen(m)
+    X = [randn(g, m, k, dtype=BF16) * 2.0**i for i in range(8)]
+    w = bl.convrot_fp8_quantize_weights(randn(g, n, k, std=0.05))
+    biases = torch.empty(8, n, device="cuda")
+    want = []
+    for i, x in enumerate(X):
+        packed = bl.convrot_fp8_pack_activations(x)
+        torch.cuda.synchronize()
+        want.append(bl.convrot_fp8_linear(packed, w, out_dtype=F32))
+        torch.cuda.synchronize()
+        # a linear's outputs as the next one's bias, too
+        biases[i] = want[-1][0]
+        want[-1] = (want[-1], bl.convrot_fp8_linear(packed, w, biases[i], out_dtype=F32))
+    packed = bl.empty_fp8_rows(m, k)
+    y, z = (torch.empty(8, m, n, device="cuda") for _ in range(2))
+    for _ in range(5):
+        y.zero_(), z.zero_()
+        for i, x in enumerate(X):
+            bl.convrot_fp8_pack_activations(x, out=packed)
+            bl.convrot_fp8_linear(packed, w, out=y[i])
+            bl.convrot_fp8_linear(packed, w, y[i][0], out=z[i])
+        for i in range(8):
+            assert torch.equal(y[i], want[i][0]) and torch.equal(z[i], want[i][1])
