@@ -9,6 +9,7 @@
 #include <Python.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/convrot_block.h"
@@ -181,7 +182,7 @@ bool codes(PyObject *o, const char *name, int64_t rows, int64_t cols, Matrix &m)
 int64_t blocks(int64_t v) { return (v + CONVROT_FP8_BLOCK - 1) / CONVROT_FP8_BLOCK; }
 
 // (x or q, x_scale or None, w.q, w.scale, bias, act, out, work, dev_status, stream); x_scale None: x is rows to pack
-PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
+PyObject *linear(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 10));
     const bool pack = v[1] == Py_None;
@@ -222,12 +223,7 @@ PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
     if (pack && !a.work) {
         a.work_bytes = convrot_fp8_pack_linear_work_bytes(a.m, a.n, a.k);
         if (a.work_bytes) {
-            try {
-                work = at::empty({a.work_bytes}, out->options().dtype(at::kByte));
-            } catch (const std::exception &e) {
-                PyErr_SetString(PyExc_RuntimeError, e.what());
-                return nullptr;
-            }
+            work = at::empty({a.work_bytes}, out->options().dtype(at::kByte));
             a.work = work.data_ptr();
         }
     }
@@ -235,7 +231,7 @@ PyObject *linear(PyObject *, PyObject *const *v, Py_ssize_t n)
 }
 
 // (X, q, scale, stream)
-PyObject *pack_activations(PyObject *, PyObject *const *v, Py_ssize_t n)
+PyObject *pack_activations(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 4));
     const Tensor *x = tensor(v[0], "X");
@@ -271,7 +267,7 @@ int32_t code_of(at::ScalarType t) { return t == at::kFloat ? CONVROT_F32 : t == 
 
 // (x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
 //  out_h, out_n, q, q_scale, stream)
-PyObject *gated_norm(PyObject *, PyObject *const *v, Py_ssize_t n)
+PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 19));
     const Tensor *x = tensor(v[0], "x");
@@ -334,7 +330,7 @@ Tensor part_of(const Tensor &whole, int64_t offset, at::IntArrayRef sizes)
 
 // (h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
 //  work, stream) -> status, or the dict of gradients. They are allocated here, the small ones as parts of one buffer.
-PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
+PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 18));
     const Tensor *h = tensor(v[0], "h");
@@ -377,38 +373,33 @@ PyObject *gated_norm_backward(PyObject *, PyObject *const *v, Py_ssize_t n)
                   {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
                   {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
     Tensor dx, dy, work;
-    try {
-        const auto like = h->options().requires_grad(c10::nullopt);
-        dx = at::empty({m, d}, like);
-        if (v[1] != Py_None) dy = at::empty({m, d}, like);
-        int64_t floats = 0;
-        for (const Small &s : small) floats += s.of == Py_None ? 0 : (s.of_samples ? batches : 1) * d;
-        // An allocation costs about as much as a launch: a small workspace goes behind the small gradients, in one.
-        const bool own_work = v[16] == Py_None;
-        int64_t behind = 0;
-        if (own_work) {
-            a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
-            if (a.work_bytes <= kWorkBehind) behind = (a.work_bytes + 255) / 256 * 64 + 64;
-        }
-        const int64_t start = (floats + 63) / 64 * 64;
-        const Tensor all = at::empty({behind ? start + behind : floats}, like.dtype(at::kFloat));
-        floats = 0;
-        for (Small &s : small) {
-            if (s.of == Py_None) continue;
-            s.grad = s.of_samples ? part_of(all, floats, {batches, d}) : part_of(all, floats, {d});
-            *s.to = static_cast<float *>(s.grad.data_ptr());
-            floats += (s.of_samples ? batches : 1) * d;
-        }
-        if (behind) {
-            const auto at = reinterpret_cast<uintptr_t>(static_cast<float *>(all.data_ptr()) + start);
-            a.work = reinterpret_cast<void *>((at + 255) / 256 * 256);
-        } else if (own_work) {
-            work = at::empty({a.work_bytes}, like.dtype(at::kByte));
-            a.work = work.data_ptr();
-        }
-    } catch (const std::exception &e) {  // out of memory, for one
-        PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
+    const auto like = h->options().requires_grad(c10::nullopt);
+    dx = at::empty({m, d}, like);
+    if (v[1] != Py_None) dy = at::empty({m, d}, like);
+    int64_t floats = 0;
+    for (const Small &s : small) floats += s.of == Py_None ? 0 : (s.of_samples ? batches : 1) * d;
+    // An allocation costs about as much as a launch: a small workspace goes behind the small gradients, in one.
+    const bool own_work = v[16] == Py_None;
+    int64_t behind = 0;
+    if (own_work) {
+        a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
+        if (a.work_bytes <= kWorkBehind) behind = (a.work_bytes + 255) / 256 * 64 + 64;
+    }
+    const int64_t start = (floats + 63) / 64 * 64;
+    const Tensor all = at::empty({behind ? start + behind : floats}, like.dtype(at::kFloat));
+    floats = 0;
+    for (Small &s : small) {
+        if (s.of == Py_None) continue;
+        s.grad = s.of_samples ? part_of(all, floats, {batches, d}) : part_of(all, floats, {d});
+        *s.to = static_cast<float *>(s.grad.data_ptr());
+        floats += (s.of_samples ? batches : 1) * d;
+    }
+    if (behind) {
+        const auto at = reinterpret_cast<uintptr_t>(static_cast<float *>(all.data_ptr()) + start);
+        a.work = reinterpret_cast<void *>((at + 255) / 256 * 256);
+    } else if (own_work) {
+        work = at::empty({a.work_bytes}, like.dtype(at::kByte));
+        a.work = work.data_ptr();
     }
     a.h = mh.p;
     a.ldh = mh.ld;
@@ -457,7 +448,7 @@ bool heads(PyObject *o, const char *name, const Tensor &like, void **p, int64_t 
 }
 
 // (q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream)
-PyObject *rotary(PyObject *, PyObject *const *v, Py_ssize_t n)
+PyObject *rotary(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 11));
     const Tensor *q = tensor(v[0], "q"), *cos = tensor(v[2], "cos");
@@ -526,7 +517,20 @@ PyObject *rotary(PyObject *, PyObject *const *v, Py_ssize_t n)
     return status(convrot_rotary(&a, stream));
 }
 
-#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(f)), METH_FASTCALL, nullptr}
+// A call as Python makes it. torch's C++ side throws (out of memory, or a tensor without memory of its own, as under
+// torch.vmap): what it throws becomes the Python exception that torch itself would raise, and does not leave here.
+template <PyObject *(*kCall)(PyObject *const *, Py_ssize_t)>
+PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n)
+{
+    try {
+        return kCall(v, n);
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
+        return nullptr;
+    }
+}
+
+#define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(linear), METHOD(pack_activations), METHOD(gated_norm), METHOD(gated_norm_backward), METHOD(rotary),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -2,7 +2,10 @@
 and the rotary frequencies. No call here reaches a kernel."""
 
 import math
+import os
 import struct
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -11,6 +14,7 @@ from int8_hadamard_rotated_convrot_gb300 import block as bl
 from int8_hadamard_rotated_convrot_gb300 import build as cbuild
 from int8_hadamard_rotated_convrot_gb300 import convrot as cr
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000  # aligned and never dereferenced on these paths
 
 # the argument structs of include/convrot_block.h, field by field
@@ -217,6 +221,39 @@ def test_binding_refuses_tensors_the_c_side_cannot_check(lib):
         bl.convrot_rotary(torch.zeros(2, 3, 8), None, x, x)
     with pytest.raises(TypeError):
         bl.convrot_rotary_table(torch.zeros(4), [1.0])
+
+
+# calls with tensors that have no memory of their own, each in a process: "plain" ones, and the slices that vmap hands out
+WITHOUT_MEMORY = """
+import sys, torch
+from torch._subclasses import FakeTensorMode
+from int8_hadamard_rotated_convrot_gb300 import block as bl
+name, batched = sys.argv[1], sys.argv[2] == "vmap"
+with FakeTensorMode():
+    like = dict(device="cuda", dtype=torch.bfloat16)
+    x, vec, table = torch.empty(4, 64, **like), torch.empty(64, **like), torch.empty(4, 8, device="cuda")
+    w = bl.Fp8Weights(bl.fp8_codes(16, 64), torch.empty(1, 1, device="cuda"))
+    call = {
+        "norm": lambda t: bl.convrot_gated_norm(t, pre_weight=vec)[1],
+        "vector": lambda t: bl.convrot_gated_norm(x, pre_weight=t[0], out_n=x)[1],
+        "norm pack": lambda t: bl.convrot_gated_norm_pack(t)[1].scale,
+        "gradient": lambda t: bl.convrot_gated_norm_backward(t, None, t, t)["dx"],
+        "pack": lambda t: bl.convrot_fp8_pack_activations(t).scale,
+        "linear": lambda t: bl.convrot_fp8_pack_linear(t, w),
+        "rotary": lambda t: bl.convrot_rotary(t.view(1, 4, 2, 32), None, table, table)[0],
+    }[name]
+    try:
+        torch.vmap(call)(torch.empty(3, 4, 64, **like)) if batched else call(x)
+    except Exception as e:
+        print("raised", type(e).__name__)
+"""
+
+
+@pytest.mark.parametrize("how", ["plain", "vmap"])
+@pytest.mark.parametrize("name", ["norm", "vector", "norm pack", "gradient", "pack", "linear", "rotary"])
+def test_tensors_without_memory_raise(lib, name, how):
+    r = subprocess.run([sys.executable, "-c", WITHOUT_MEMORY, name, how], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("raised"), r.stdout + r.stderr[-2000:]
 
 
 def test_rotary_frequencies():
