@@ -138,9 +138,10 @@ def convrot_fp8_quantize_weights(W: torch.Tensor, stream=None) -> Fp8Weights:
     n, k = W.shape
     q = fp8_codes(n, k, W.device)
     scale = torch.empty((_blocks(n), _blocks(k)), dtype=torch.float32, device=W.device)
-    _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, W.stride(0) if n > 1 else k, q.data_ptr(),
-                                                   -(-k // 16) * 16, scale.data_ptr(), _blocks(k), _stream(W.device, stream)),
-           "convrot_fp8_quantize_weights")
+    with torch.cuda.device(W.device):
+        _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, W.stride(0) if n > 1 else k,
+                                                       q.data_ptr(), -(-k // 16) * 16, scale.data_ptr(), _blocks(k),
+                                                       _stream(W.device, stream)), "convrot_fp8_quantize_weights")
     return Fp8Weights(q, scale)
 
 
@@ -324,7 +325,8 @@ def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: floa
         if axis.numel() != pairs:
             raise ValueError("axis must name one axis for each frequency")
     cos, sin = (torch.empty((count, pairs), dtype=torch.float32, device=device) for _ in range(2))
-    _check(_cr.load().convrot_rotary_table(_cr._ptr(positions), count, axes, freq.data_ptr(), _cr._ptr(axis), pairs,
-                                            float(factor), cos.data_ptr(), sin.data_ptr(), pairs, _stream(device, stream)),
-           "convrot_rotary_table")
+    with torch.cuda.device(device):
+        _check(_cr.load().convrot_rotary_table(_cr._ptr(positions), count, axes, freq.data_ptr(), _cr._ptr(axis), pairs,
+                                               float(factor), cos.data_ptr(), sin.data_ptr(), pairs,
+                                               _stream(device, stream)), "convrot_rotary_table")
     return cos, sin

@@ -5,9 +5,11 @@
 //
 // Every function takes its arguments by position from block.py, raises
 // TypeError or ValueError for what the C side cannot check (types, shapes,
-// strides, device), and returns the C call's status.
+// strides, one device for all), and returns the C call's status, made with that
+// device current.
 #include <Python.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -41,6 +43,21 @@ const Tensor *tensor(PyObject *o, const char *name)
         return nullptr;
     }
     return &t;
+}
+
+// Every CUDA tensor of the call is on the device of `first`: the C side sees addresses alone.
+bool one_device(PyObject *const *v, Py_ssize_t n, const Tensor &first)
+{
+    for (Py_ssize_t i = 0; i < n; ++i) {
+        if (!THPVariable_Check(v[i])) continue;
+        const Tensor &t = THPVariable_Unpack(v[i]);
+        if (t.is_cuda() && t.device() != first.device()) {
+            PyErr_Format(PyExc_ValueError, "the tensors of a call must be on one device, not on cuda:%d and cuda:%d",
+                         static_cast<int>(first.device().index()), static_cast<int>(t.device().index()));
+            return false;
+        }
+    }
+    return true;
 }
 
 bool dtype_of(const Tensor &t, const char *name, int32_t &code)
@@ -187,7 +204,7 @@ PyObject *linear(PyObject *const *v, Py_ssize_t n)
     REQUIRE(count(n, 10));
     const bool pack = v[1] == Py_None;
     const Tensor *x = tensor(v[0], pack ? "X" : "x.q"), *w = tensor(v[2], "w.q"), *out = tensor(v[6], "out");
-    REQUIRE(x && w && out);
+    REQUIRE(x && w && out && one_device(v, n, *x));
     if (x->dim() != 2 || w->dim() != 2) {
         raise(PyExc_TypeError, "x and w", "must be 2-D tensors");
         return nullptr;
@@ -208,6 +225,7 @@ PyObject *linear(PyObject *const *v, Py_ssize_t n)
     cudaStream_t stream;
     REQUIRE(vector(v[4], "bias", at::kFloat, a.n, &bias) && integer(v[5], a.act) && workspace(v[7], &a.work, &a.work_bytes));
     REQUIRE(status_word(v[8], &a.dev_status) && stream_of(v[9], *out, stream));
+    const c10::cuda::CUDAGuard device(x->device());
     a.x = mx.p;
     a.ldx = mx.ld;
     a.x_scale = static_cast<const float *>(ms.p);
@@ -235,7 +253,7 @@ PyObject *pack_activations(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 4));
     const Tensor *x = tensor(v[0], "X");
-    REQUIRE(x);
+    REQUIRE(x && one_device(v, n, *x));
     if (x->dim() != 2) {
         raise(PyExc_TypeError, "X", "must be a 2-D tensor");
         return nullptr;
@@ -246,6 +264,7 @@ PyObject *pack_activations(PyObject *const *v, Py_ssize_t n)
     cudaStream_t stream;
     REQUIRE(dtype_of(*x, "X", dtype) && matrix(v[0], "X", x->scalar_type(), m, k, mx) && codes(v[1], "q", m, k, mq));
     REQUIRE(matrix(v[2], "scale", at::kFloat, blocks(k), m, ms) && stream_of(v[3], *x, stream));
+    const c10::cuda::CUDAGuard device(x->device());
     return status(convrot_fp8_pack_activations(mx.p, dtype, m, k, mx.ld, mq.p, mq.ld, static_cast<float *>(ms.p), ms.ld, stream));
 }
 
@@ -271,7 +290,7 @@ PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 19));
     const Tensor *x = tensor(v[0], "x");
-    REQUIRE(x);
+    REQUIRE(x && one_device(v, n, *x));
     if (x->dim() != 2) {
         raise(PyExc_TypeError, "x", "must be a 2-D tensor");
         return nullptr;
@@ -296,6 +315,7 @@ PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
     REQUIRE(optional_matrix(v[14], "out_h", t, m, d, mh) && optional_matrix(v[15], "out_n", t, m, d, mn));
     if (v[16] != Py_None) REQUIRE(codes(v[16], "q", m, d, mq) && matrix(v[17], "scale", at::kFloat, blocks(d), m, ms));
     REQUIRE(stream_of(v[18], *x, stream));
+    const c10::cuda::CUDAGuard device(x->device());
     a.x = mx.p;
     a.ldx = mx.ld;
     a.y = my.p;
@@ -334,7 +354,7 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 18));
     const Tensor *h = tensor(v[0], "h");
-    REQUIRE(h);
+    REQUIRE(h && one_device(v, n, *h));
     if (h->dim() != 2) {
         raise(PyExc_TypeError, "h", "must be a 2-D tensor");
         return nullptr;
@@ -372,6 +392,7 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
                   {"dshift", v[6], true, &a.dshift, {}},         {"dpost_weight", v[10], false, &a.dpost_weight, {}},
                   {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
                   {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
+    const c10::cuda::CUDAGuard device(h->device());
     Tensor dx, dy, work;
     const auto like = h->options().requires_grad(c10::nullopt);
     dx = at::empty({m, d}, like);
@@ -452,7 +473,7 @@ PyObject *rotary(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 11));
     const Tensor *q = tensor(v[0], "q"), *cos = tensor(v[2], "cos");
-    REQUIRE(q && cos);
+    REQUIRE(q && cos && one_device(v, n, *q));
     if (q->dim() != 4 || cos->dim() != 2) {
         raise(PyExc_TypeError, "q and cos", "must be [batch, tokens, heads, head_dim] and [rows, pairs]");
         return nullptr;
@@ -506,6 +527,7 @@ PyObject *rotary(PyObject *const *v, Py_ssize_t n)
     const int inverse = PyObject_IsTrue(v[6]);
     cudaStream_t stream;
     REQUIRE(integer(v[5], a.layout) && inverse >= 0 && status_word(v[9], &a.dev_status) && stream_of(v[10], *q, stream));
+    const c10::cuda::CUDAGuard device(q->device());
     a.inverse = inverse;
     a.q = qp;
     a.k = kp;

@@ -256,6 +256,30 @@ def test_tensors_without_memory_raise(lib, name, how):
     assert r.returncode == 0 and r.stdout.startswith("raised"), r.stdout + r.stderr[-2000:]
 
 
+def test_tensors_of_two_devices_are_refused(lib):
+    from torch._subclasses import FakeTensorMode
+
+    with FakeTensorMode():
+        a, b = (dict(device=f"cuda:{i}") for i in (0, 1))
+        x, y = torch.empty(4, 64, **a), torch.empty(4, 64, **b)
+        vec, one, work = torch.empty(64, **b), torch.empty(1, dtype=torch.int32, **b), torch.empty(64, dtype=torch.uint8, **b)
+        w = bl.Fp8Weights(bl.fp8_codes(16, 64, "cuda:0"), torch.empty(1, 1, **a))
+        other = bl.Fp8Weights(w.q, torch.empty(1, 1, **b))
+        packed = bl.empty_fp8_rows(4, 64, "cuda:1")
+        q, table = torch.empty(1, 4, 2, 16, **a), torch.empty(4, 8, **a)
+        calls = [lambda: bl.convrot_fp8_pack_activations(x, out=packed), lambda: bl.convrot_fp8_pack_linear(x, other),
+                 lambda: bl.convrot_fp8_linear(packed, w), lambda: bl.convrot_fp8_pack_linear(x, w, out=torch.empty(4, 16, **b)),
+                 lambda: bl.convrot_fp8_pack_linear(x, w, dev_status=one), lambda: bl.convrot_fp8_pack_linear(x, w, work=work),
+                 lambda: bl.convrot_gated_norm(x, y), lambda: bl.convrot_gated_norm(x, pre_weight=vec),
+                 lambda: bl.convrot_gated_norm(x, out_n=y), lambda: bl.convrot_gated_norm_pack(x, out=packed),
+                 lambda: bl.convrot_gated_norm_backward(x, None, x, y), lambda: bl.convrot_gated_norm_backward(x, None, x, x, work=work),
+                 lambda: bl.convrot_rotary(q, None, table, torch.empty(4, 8, **b)),
+                 lambda: bl.convrot_rotary(q, None, table, table, torch.empty(4, dtype=torch.int64, **b))]
+        for call in calls:
+            with pytest.raises(ValueError, match="one device"):
+                call()
+
+
 def test_rotary_frequencies():
     plain, one = bl.rotary_frequencies(8, 10000.0)
     assert one == 1.0 and plain == [10000.0 ** (-i / 8) for i in range(8)]
