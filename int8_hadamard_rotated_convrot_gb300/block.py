@@ -186,7 +186,8 @@ def convrot_gated_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: 
 
     gate, scale and shift are [batches, d], row r taking sample r // rows_per_batch (default: one sample); norms
     are NORM_NONE, NORM_RMS or NORM_LAYER with optional weight and bias [d]. All parameters have one type, float32
-    or x's. Without y and with res_scale 1 and no out_h, the returned h is x itself. out_h may be x (in place)."""
+    or x's. Without y there is no gate and no post norm's weight or bias (ValueError); without y and with res_scale 1
+    and no out_h, the returned h is x itself. out_h may be x (in place)."""
     if out_h is None:
         out_h = x if y is None and res_scale == 1.0 else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if out_n is None:

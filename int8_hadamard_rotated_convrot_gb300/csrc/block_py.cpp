@@ -282,6 +282,14 @@ bool param_type(at::ScalarType own, std::initializer_list<PyObject *> all, at::S
     return true;
 }
 
+// Without a branch y there is nothing that its gate, weight and bias could apply to.
+bool branch_for(PyObject *y, std::initializer_list<PyObject *> all)
+{
+    for (PyObject *o : all)
+        if (y == Py_None && o != Py_None) return raise(PyExc_ValueError, "gate, post_weight and post_bias", "belong to a branch y");
+    return true;
+}
+
 int32_t code_of(at::ScalarType t) { return t == at::kFloat ? CONVROT_F32 : t == at::kBFloat16 ? CONVROT_BF16 : CONVROT_F16; }
 
 // (x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
@@ -295,6 +303,7 @@ PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
         raise(PyExc_TypeError, "x", "must be a 2-D tensor");
         return nullptr;
     }
+    REQUIRE(branch_for(v[1], {v[2], v[8], v[9]}));
     convrot_gated_norm_args a{};
     const at::ScalarType t = x->scalar_type();
     at::ScalarType p;
@@ -359,6 +368,7 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
         raise(PyExc_TypeError, "h", "must be a 2-D tensor");
         return nullptr;
     }
+    REQUIRE(branch_for(v[1], {v[4], v[10], v[11]}));
     convrot_gated_norm_backward_args a{};
     const at::ScalarType t = h->scalar_type();
     at::ScalarType p;
@@ -378,10 +388,6 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
     REQUIRE(vector(v[11], "post_bias", p, d, &a.post_bias) && integer(v[12], a.pre) && vector(v[13], "pre_weight", p, d, &a.pre_weight));
     REQUIRE(vector(v[14], "pre_bias", p, d, &a.pre_bias) && real(v[15], a.eps));
     REQUIRE(workspace(v[16], &a.work, &a.work_bytes) && stream_of(v[17], *h, stream));
-    if (v[1] == Py_None && (v[4] != Py_None || v[10] != Py_None || v[11] != Py_None)) {
-        raise(PyExc_ValueError, "gate, post_weight and post_bias", "belong to a branch y");
-        return nullptr;
-    }
     struct Small {
         const char *name;
         PyObject *of;

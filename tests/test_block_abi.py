@@ -280,6 +280,18 @@ def test_tensors_of_two_devices_are_refused(lib):
                 call()
 
 
+def test_gate_and_post_norm_belong_to_a_branch(lib):
+    from torch._subclasses import FakeTensorMode
+
+    with FakeTensorMode():
+        x, gate, vec = (torch.empty(*shape, device="cuda") for shape in ((4, 64), (1, 64), (64,)))
+        for kw in (dict(gate=gate), dict(post_weight=vec), dict(post_bias=vec)):
+            for call in (lambda: bl.convrot_gated_norm(x, **kw), lambda: bl.convrot_gated_norm_pack(x, **kw),
+                         lambda: bl.convrot_gated_norm_backward(x, None, x, x, **kw)):
+                with pytest.raises(ValueError, match="belong to a branch"):
+                    call()
+
+
 def test_rotary_frequencies():
     plain, one = bl.rotary_frequencies(8, 10000.0)
     assert one == 1.0 and plain == [10000.0 ** (-i / 8) for i in range(8)]
