@@ -59,6 +59,18 @@ def _stream(device: torch.device, stream) -> int:
     return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An uninitialized tensor that a call on ``stream`` writes and the caller uses on its own, the current one. It
+    belongs to the former, behind whatever used its memory before, and is kept until the latter is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 # ---------------------------------------------------------------- the block-scaled linear
 
 
@@ -101,15 +113,15 @@ def _blocks(v: int) -> int:
     return -(-v // FP8_BLOCK)
 
 
-def fp8_codes(rows: int, k: int, device=None) -> torch.Tensor:
+def fp8_codes(rows: int, k: int, device=None, stream=None) -> torch.Tensor:
     """An uninitialized [rows, k] code tensor whose rows start on 16 bytes."""
-    return torch.empty((rows, -(-k // 16) * 16), dtype=_E4M3, device=device or "cuda")[:, :k]
+    return _empty((rows, -(-k // 16) * 16), _E4M3, device or "cuda", stream)[:, :k]
 
 
-def empty_fp8_rows(m: int, k: int, device=None) -> Fp8Rows:
+def empty_fp8_rows(m: int, k: int, device=None, stream=None) -> Fp8Rows:
     """Allocates (with torch) the buffers that a pack fills."""
-    scale = torch.empty((_blocks(k), -(-m // 4) * 4), dtype=torch.float32, device=device or "cuda")
-    return Fp8Rows(fp8_codes(m, k, device), scale[:, :m])
+    scale = _empty((_blocks(k), -(-m // 4) * 4), torch.float32, device or "cuda", stream)
+    return Fp8Rows(fp8_codes(m, k, device, stream), scale[:, :m])
 
 
 def fp8_weights_from_codes(q: torch.Tensor, scale: torch.Tensor) -> Fp8Weights:
@@ -126,7 +138,7 @@ def fp8_weights_from_codes(q: torch.Tensor, scale: torch.Tensor) -> Fp8Weights:
 def convrot_fp8_pack_activations(X: torch.Tensor, out: Fp8Rows | None = None, stream=None) -> Fp8Rows:
     """Codes and scales of X [m, k] (float32, bfloat16 or float16), one scale for 128 features of a row."""
     if out is None:
-        out = empty_fp8_rows(*X.shape, X.device)
+        out = empty_fp8_rows(*X.shape, X.device, stream)
     _check(load().pack_activations(X, out.q, out.scale, stream), "convrot_fp8_pack_activations")
     return out
 
@@ -136,8 +148,8 @@ def convrot_fp8_quantize_weights(W: torch.Tensor, stream=None) -> Fp8Weights:
     if W.dtype not in _DTYPE or not W.is_cuda or W.dim() != 2 or (W.shape[1] > 1 and W.stride(1) != 1):
         raise TypeError("W must be a 2-D row-major float32, bfloat16 or float16 CUDA tensor")
     n, k = W.shape
-    q = fp8_codes(n, k, W.device)
-    scale = torch.empty((_blocks(n), _blocks(k)), dtype=torch.float32, device=W.device)
+    q = fp8_codes(n, k, W.device, stream)
+    scale = _empty((_blocks(n), _blocks(k)), torch.float32, W.device, stream)
     with torch.cuda.device(W.device):
         _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, W.stride(0) if n > 1 else k,
                                                        q.data_ptr(), -(-k // 16) * 16, scale.data_ptr(), _blocks(k),
@@ -150,7 +162,7 @@ def convrot_fp8_linear(x: Fp8Rows, w: Fp8Weights, bias: torch.Tensor | None = No
                        dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [m, n] = act(x w^T + b) from packed activations; bias fp32 [n]. Y has out's or out_dtype's type."""
     if out is None:
-        out = torch.empty((x.q.shape[0], w.q.shape[0]), dtype=out_dtype, device=x.q.device)
+        out = _empty((x.q.shape[0], w.q.shape[0]), out_dtype, x.q.device, stream)
     _check(load().linear(x.q, x.scale, w.q, w.scale, bias, act, out, None, dev_status, stream), "convrot_fp8_linear")
     return out
 
@@ -167,7 +179,7 @@ def convrot_fp8_pack_linear(X: torch.Tensor, w: Fp8Weights, bias: torch.Tensor |
     """Y [m, n] = act(pack(X) w^T + b): convrot_fp8_pack_activations and convrot_fp8_linear in one call.
     Y has out's, out_dtype's or X's type. ``work`` (uint8) is allocated here when not given."""
     if out is None:
-        out = torch.empty((X.shape[0], w.q.shape[0]), dtype=out_dtype or X.dtype, device=X.device)
+        out = _empty((X.shape[0], w.q.shape[0]), out_dtype or X.dtype, X.device, stream)
     _check(load().linear(X, None, w.q, w.scale, bias, act, out, work, dev_status, stream), "convrot_fp8_pack_linear")
     return out
 
@@ -189,9 +201,9 @@ def convrot_gated_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: 
     or x's. Without y there is no gate and no post norm's weight or bias (ValueError); without y and with res_scale 1
     and no out_h, the returned h is x itself. out_h may be x (in place)."""
     if out_h is None:
-        out_h = x if y is None and res_scale == 1.0 else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out_h = x if y is None and res_scale == 1.0 else _empty(x.shape, x.dtype, x.device, stream)
     if out_n is None:
-        out_n = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out_n = _empty(x.shape, x.dtype, x.device, stream)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
     _check(load().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
                                  pre_weight, pre_bias, eps, write_h, out_n, None, None, stream),
@@ -209,9 +221,9 @@ def convrot_gated_norm_pack(x: torch.Tensor, y: torch.Tensor | None = None, *, g
                             stream=None) -> tuple[torch.Tensor, Fp8Rows]:
     """convrot_gated_norm with n written as the packed input of convrot_fp8_linear instead: (h, packed n)."""
     if out_h is None:
-        out_h = x if y is None and res_scale == 1.0 else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out_h = x if y is None and res_scale == 1.0 else _empty(x.shape, x.dtype, x.device, stream)
     if out is None:
-        out = empty_fp8_rows(*x.shape, x.device)
+        out = empty_fp8_rows(*x.shape, x.device, stream)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
     _check(load().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
                                  pre_weight, pre_bias, eps, write_h, None, out.q, out.scale, stream),
@@ -251,11 +263,11 @@ def convrot_rotary(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, s
     (default: token t uses row t). A position outside the table gives NaN and ERR_INVALID_ARG in dev_status.
     inverse turns by the opposite angles (the gradient). Any batch, token and head strides; out_q may be q itself."""
     if out_q is None:
-        out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out_q = _empty(q.shape, q.dtype, q.device, stream)
     if k is None:
         out_k = None
     elif out_k is None:
-        out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        out_k = _empty(k.shape, k.dtype, k.device, stream)
     _check(load().rotary(q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream), "convrot_rotary")
     return out_q, out_k
 

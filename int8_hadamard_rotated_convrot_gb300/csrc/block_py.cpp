@@ -9,6 +9,7 @@
 // device current.
 #include <Python.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -141,6 +142,25 @@ bool stream_of(PyObject *o, const Tensor &t, cudaStream_t &s)
     return !PyErr_Occurred();
 }
 
+// Memory that a call allocates belongs to the stream that the call runs on: there, what used a block before has been
+// queued before, and what is freed is used again only behind this call's kernels. Outputs, which the caller reads and
+// frees on its own stream, are marked as used on that one too (record).
+class OnStream {
+public:
+    OnStream(cudaStream_t launch, const Tensor &like) : here_(c10::cuda::getCurrentCUDAStream(like.device().index()))
+    {
+        if (here_.stream() != launch) guard_.reset_stream(c10::cuda::getStreamFromExternal(launch, like.device().index()));
+    }
+    void record(const Tensor &t) const
+    {
+        if (guard_.current_stream() && t.defined()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), here_);
+    }
+
+private:
+    c10::cuda::CUDAStream here_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
+
 bool integer(PyObject *o, int64_t &v)
 {
     v = PyLong_AsLongLong(o);
@@ -241,6 +261,7 @@ PyObject *linear(PyObject *const *v, Py_ssize_t n)
     if (pack && !a.work) {
         a.work_bytes = convrot_fp8_pack_linear_work_bytes(a.m, a.n, a.k);
         if (a.work_bytes) {
+            const OnStream allocate(stream, *out);
             work = at::empty({a.work_bytes}, out->options().dtype(at::kByte));
             a.work = work.data_ptr();
         }
@@ -399,10 +420,13 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
                   {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
                   {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
     const c10::cuda::CUDAGuard device(h->device());
+    const OnStream allocate(stream, *h);
     Tensor dx, dy, work;
     const auto like = h->options().requires_grad(c10::nullopt);
     dx = at::empty({m, d}, like);
     if (v[1] != Py_None) dy = at::empty({m, d}, like);
+    allocate.record(dx);
+    allocate.record(dy);
     int64_t floats = 0;
     for (const Small &s : small) floats += s.of == Py_None ? 0 : (s.of_samples ? batches : 1) * d;
     // An allocation costs about as much as a launch: a small workspace goes behind the small gradients, in one.
@@ -414,6 +438,7 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
     }
     const int64_t start = (floats + 63) / 64 * 64;
     const Tensor all = at::empty({behind ? start + behind : floats}, like.dtype(at::kFloat));
+    allocate.record(all);
     floats = 0;
     for (Small &s : small) {
         if (s.of == Py_None) continue;

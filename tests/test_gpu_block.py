@@ -682,3 +682,87 @@ def test_linears_read_what_the_call_before_wrote(m, k, n):
             bl.convrot_fp8_linear(packed, w, y[i][0], out=z[i])
         for i in range(8):
             assert torch.equal(y[i], want[i][0]) and torch.equal(z[i], want[i][1])
+
+
+# ---------------------------------------------------------------- streams
+
+
+def stream_calls():
+    """name -> call(stream) for every call that allocates, its inputs made and finished beforehand"""
+    g = gen(21)
+    X, W = randn(g, 300, 1024, dtype=BF16), randn(g, 640, 1024, std=0.05)
+    w = bl.convrot_fp8_quantize_weights(W)
+    packed = bl.convrot_fp8_pack_activations(X)
+    forms = {}
+    for name, (m, d) in {"small": (40, 1024), "large": (900, 3000)}.items():  # workspaces under and over 2 MB
+        v, how = norm_case(m, d, 50, BF16, F32, 1, 2, True)
+        dh, dn = randn(g, m, d, dtype=BF16), randn(g, m, d, dtype=BF16)
+        forms["gradient, " + name] = lambda s, v=v, how=how, dh=dh, dn=dn: list(bl.convrot_gated_norm_backward(
+            v["x"], v["y"], dh, dn, **params(v), **own_args(how), stream=s).values())
+        forms["norm, " + name] = lambda s, v=v, how=how: list(bl.convrot_gated_norm(
+            v["x"], v["y"], **params(v), **own_args(how), stream=s))
+
+    def rows(p):
+        return [p.q.view(torch.uint8), p.scale]
+
+    cos, sin = bl.convrot_rotary_table(500, bl.rotary_frequencies(32)[0])
+    q, k = randn(g, 2, 500, 6, 64), randn(g, 2, 500, 2, 64)
+    return forms | {
+        "norm pack": lambda s: rows(bl.convrot_gated_norm_pack(X, stream=s)[1]),
+        "pack": lambda s: rows(bl.convrot_fp8_pack_activations(X, stream=s)),
+        "quantize": lambda s: rows(bl.convrot_fp8_quantize_weights(W, stream=s)),
+        "linear": lambda s: [bl.convrot_fp8_linear(packed, w, stream=s)],
+        "pack and linear": lambda s: [bl.convrot_fp8_pack_linear(X, w, stream=s)],
+        "rotary": lambda s: list(bl.convrot_rotary(q, k, cos, sin, stream=s)),
+    }
+
+
+STREAM_CALLS = ["gradient, small", "norm, small", "gradient, large", "norm, large", "norm pack", "pack", "quantize", "linear",
+                "pack and linear", "rotary"]
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_memory_of_a_call_on_another_stream(name):
+    """The call's stream is late: what the caller allocates and fills meanwhile is not the call's workspace. Then the
+    caller's stream is late: what it still writes into freed memory does not reach the call's outputs."""
+    call = stream_calls()[name]
+    want = [t.clone() for t in call(None) if t is not None]
+    sizes = [max(256, t.numel() * t.element_size()) for t in want] + [1 << 20, 3 << 20, 300 * 1024 + (300 * 8 * 4), 12 << 20]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def fill():
+        return [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+
+    for late in (side, torch.cuda.current_stream()):
+        for _ in range(3):
+            torch.cuda.empty_cache()
+            with torch.cuda.stream(late):
+                torch.cuda._sleep(20_000_000)  # 10 ms
+            if late is side:
+                got = [t for t in call(side) if t is not None]
+                kept = fill()
+            else:
+                kept = fill()
+                del kept  # their memory is free for the current stream's next tensors, behind the fills
+                got = [t for t in call(side) if t is not None]
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want, strict=True))
+
+
+def test_outputs_of_another_stream_outlive_their_last_use():
+    """An output freed while the caller's stream still has to read it: the call's stream does not write over it."""
+    g = gen(22)
+    X, w = randn(g, 300, 1024, dtype=BF16), bl.convrot_fp8_quantize_weights(randn(g, 640, 1024, std=0.05))
+    want = bl.convrot_fp8_pack_linear(X, w)
+    side, zero = torch.cuda.Stream(), torch.zeros_like(X)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        y = bl.convrot_fp8_pack_linear(X, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(20_000_000)
+        copy = y.clone()
+        del y
+        others = [bl.convrot_fp8_pack_linear(zero, w, stream=side) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want) and not any(o.any() for o in others)
