@@ -50,9 +50,10 @@ const Tensor *tensor(PyObject *o, const char *name)
 bool one_device(PyObject *const *v, Py_ssize_t n, const Tensor &first)
 {
     for (Py_ssize_t i = 0; i < n; ++i) {
-        if (!THPVariable_Check(v[i])) continue;
+        // (asking whether something is a tensor is slow where it is none)
+        if (v[i] == Py_None || PyLong_Check(v[i]) || PyFloat_Check(v[i]) || !THPVariable_Check(v[i])) continue;
         const Tensor &t = THPVariable_Unpack(v[i]);
-        if (t.is_cuda() && t.device() != first.device()) {
+        if (t.is_cuda() && t.device().index() != first.device().index()) {
             PyErr_Format(PyExc_ValueError, "the tensors of a call must be on one device, not on cuda:%d and cuda:%d",
                          static_cast<int>(first.device().index()), static_cast<int>(t.device().index()));
             return false;
@@ -141,6 +142,18 @@ bool stream_of(PyObject *o, const Tensor &t, cudaStream_t &s)
     Py_DECREF(v);
     return !PyErr_Occurred();
 }
+
+// The tensor's device is current while this lives (asking which one is costs a fraction of torch's own guard).
+class DeviceOf {
+public:
+    explicit DeviceOf(const Tensor &t)
+    {
+        if (c10::cuda::current_device() != t.device().index()) guard_.set_index(t.device().index());
+    }
+
+private:
+    c10::cuda::OptionalCUDAGuard guard_;
+};
 
 // Memory that a call allocates belongs to the stream that the call runs on: there, what used a block before has been
 // queued before, and what is freed is used again only behind this call's kernels. Outputs, which the caller reads and
@@ -245,7 +258,7 @@ PyObject *linear(PyObject *const *v, Py_ssize_t n)
     cudaStream_t stream;
     REQUIRE(vector(v[4], "bias", at::kFloat, a.n, &bias) && integer(v[5], a.act) && workspace(v[7], &a.work, &a.work_bytes));
     REQUIRE(status_word(v[8], &a.dev_status) && stream_of(v[9], *out, stream));
-    const c10::cuda::CUDAGuard device(x->device());
+    const DeviceOf device(*x);
     a.x = mx.p;
     a.ldx = mx.ld;
     a.x_scale = static_cast<const float *>(ms.p);
@@ -285,7 +298,7 @@ PyObject *pack_activations(PyObject *const *v, Py_ssize_t n)
     cudaStream_t stream;
     REQUIRE(dtype_of(*x, "X", dtype) && matrix(v[0], "X", x->scalar_type(), m, k, mx) && codes(v[1], "q", m, k, mq));
     REQUIRE(matrix(v[2], "scale", at::kFloat, blocks(k), m, ms) && stream_of(v[3], *x, stream));
-    const c10::cuda::CUDAGuard device(x->device());
+    const DeviceOf device(*x);
     return status(convrot_fp8_pack_activations(mx.p, dtype, m, k, mx.ld, mq.p, mq.ld, static_cast<float *>(ms.p), ms.ld, stream));
 }
 
@@ -345,7 +358,7 @@ PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
     REQUIRE(optional_matrix(v[14], "out_h", t, m, d, mh) && optional_matrix(v[15], "out_n", t, m, d, mn));
     if (v[16] != Py_None) REQUIRE(codes(v[16], "q", m, d, mq) && matrix(v[17], "scale", at::kFloat, blocks(d), m, ms));
     REQUIRE(stream_of(v[18], *x, stream));
-    const c10::cuda::CUDAGuard device(x->device());
+    const DeviceOf device(*x);
     a.x = mx.p;
     a.ldx = mx.ld;
     a.y = my.p;
@@ -419,7 +432,7 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
                   {"dshift", v[6], true, &a.dshift, {}},         {"dpost_weight", v[10], false, &a.dpost_weight, {}},
                   {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
                   {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
-    const c10::cuda::CUDAGuard device(h->device());
+    const DeviceOf device(*h);
     const OnStream allocate(stream, *h);
     Tensor dx, dy, work;
     const auto like = h->options().requires_grad(c10::nullopt);
@@ -558,7 +571,7 @@ PyObject *rotary(PyObject *const *v, Py_ssize_t n)
     const int inverse = PyObject_IsTrue(v[6]);
     cudaStream_t stream;
     REQUIRE(integer(v[5], a.layout) && inverse >= 0 && status_word(v[9], &a.dev_status) && stream_of(v[10], *q, stream));
-    const c10::cuda::CUDAGuard device(q->device());
+    const DeviceOf device(*q);
     a.inverse = inverse;
     a.q = qp;
     a.k = kp;
