@@ -321,23 +321,26 @@ def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: floa
 
     rows: a count (row p is position p), or positions [rows] or [rows, axes] (one for each axis of an image or a
     video; integer or floating point). freq: [pairs] (rotary_frequencies); axis: the axis of each pair."""
-    positions = None
     if isinstance(rows, torch.Tensor):
         device = rows.device
-        positions = rows.to(torch.float64).reshape(rows.shape[0], -1).contiguous()
-        count, axes = positions.shape
-    else:
-        count, axes = int(rows), 1
     device = torch.device(device or "cuda")
     if device.type != "cuda":
         raise TypeError("positions must be a CUDA tensor")
-    freq = torch.as_tensor(freq, dtype=torch.float64).to(device).contiguous()
-    pairs = freq.numel()
-    if axis is not None:
-        axis = torch.as_tensor(axis, dtype=torch.int32).to(device).contiguous()
-        if axis.numel() != pairs:
-            raise ValueError("axis must name one axis for each frequency")
-    cos, sin = (torch.empty((count, pairs), dtype=torch.float32, device=device) for _ in range(2))
+    # what is converted here is converted, read and freed on the one stream
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        positions = None
+        if isinstance(rows, torch.Tensor):
+            positions = rows.to(torch.float64).reshape(rows.shape[0], -1).contiguous()
+            count, axes = positions.shape
+        else:
+            count, axes = int(rows), 1
+        freq = torch.as_tensor(freq, dtype=torch.float64).to(device).contiguous()
+        pairs = freq.numel()
+        if axis is not None:
+            axis = torch.as_tensor(axis, dtype=torch.int32).to(device).contiguous()
+            if axis.numel() != pairs:
+                raise ValueError("axis must name one axis for each frequency")
+    cos, sin = (_empty((count, pairs), torch.float32, device, stream) for _ in range(2))
     with torch.cuda.device(device):
         _check(_cr.load().convrot_rotary_table(_cr._ptr(positions), count, axes, freq.data_ptr(), _cr._ptr(axis), pairs,
                                                float(factor), cos.data_ptr(), sin.data_ptr(), pairs,

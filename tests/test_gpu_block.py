@@ -766,3 +766,22 @@ def test_outputs_of_another_stream_outlive_their_last_use():
         others = [bl.convrot_fp8_pack_linear(zero, w, stream=side) for _ in range(4)]
         torch.cuda.synchronize()
         assert torch.equal(copy, want) and not any(o.any() for o in others)
+
+
+def test_tables_on_another_stream():
+    """Positions that the call's stream makes, converted where it reads them, and not overwritten while it does."""
+    freq, _ = bl.rotary_frequencies(64)
+    axis = [i % 3 for i in range(64)]
+    side = torch.cuda.Stream()
+    want = bl.convrot_rotary_table(torch.arange(30000, device="cuda").view(-1, 3), freq, axis)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda.empty_cache()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+            at = torch.arange(30000, device="cuda").view(-1, 3)
+        got = bl.convrot_rotary_table(at, freq, axis, stream=side)
+        kept = [torch.full((n,), 3.0, dtype=torch.float64, device="cuda") for n in (30000, 64, 32, 10000 * 32) for _ in range(2)]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del kept
