@@ -59,18 +59,6 @@ def _stream(device: torch.device, stream) -> int:
     return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
 
 
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """An uninitialized tensor that a call on ``stream`` writes and the caller uses on its own, the current one. It
-    belongs to the former, behind whatever used its memory before, and is kept until the latter is done with it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(here)
-    return t
-
-
 # ---------------------------------------------------------------- the block-scaled linear
 
 
@@ -115,12 +103,12 @@ def _blocks(v: int) -> int:
 
 def fp8_codes(rows: int, k: int, device=None, stream=None) -> torch.Tensor:
     """An uninitialized [rows, k] code tensor whose rows start on 16 bytes."""
-    return _empty((rows, -(-k // 16) * 16), _E4M3, device or "cuda", stream)[:, :k]
+    return _cr._empty((rows, -(-k // 16) * 16), _E4M3, device or "cuda", stream)[:, :k]
 
 
 def empty_fp8_rows(m: int, k: int, device=None, stream=None) -> Fp8Rows:
     """Allocates (with torch) the buffers that a pack fills."""
-    scale = _empty((_blocks(k), -(-m // 4) * 4), torch.float32, device or "cuda", stream)
+    scale = _cr._empty((_blocks(k), -(-m // 4) * 4), torch.float32, device or "cuda", stream)
     return Fp8Rows(fp8_codes(m, k, device, stream), scale[:, :m])
 
 
@@ -149,7 +137,7 @@ def convrot_fp8_quantize_weights(W: torch.Tensor, stream=None) -> Fp8Weights:
         raise TypeError("W must be a 2-D row-major float32, bfloat16 or float16 CUDA tensor")
     n, k = W.shape
     q = fp8_codes(n, k, W.device, stream)
-    scale = _empty((_blocks(n), _blocks(k)), torch.float32, W.device, stream)
+    scale = _cr._empty((_blocks(n), _blocks(k)), torch.float32, W.device, stream)
     with torch.cuda.device(W.device):
         _check(_cr.load().convrot_fp8_quantize_weights(W.data_ptr(), _DTYPE[W.dtype], n, k, W.stride(0) if n > 1 else k,
                                                        q.data_ptr(), -(-k // 16) * 16, scale.data_ptr(), _blocks(k),
@@ -162,7 +150,7 @@ def convrot_fp8_linear(x: Fp8Rows, w: Fp8Weights, bias: torch.Tensor | None = No
                        dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [m, n] = act(x w^T + b) from packed activations; bias fp32 [n]. Y has out's or out_dtype's type."""
     if out is None:
-        out = _empty((x.q.shape[0], w.q.shape[0]), out_dtype, x.q.device, stream)
+        out = _cr._empty((x.q.shape[0], w.q.shape[0]), out_dtype, x.q.device, stream)
     _check(load().linear(x.q, x.scale, w.q, w.scale, bias, act, out, None, dev_status, stream), "convrot_fp8_linear")
     return out
 
@@ -179,7 +167,7 @@ def convrot_fp8_pack_linear(X: torch.Tensor, w: Fp8Weights, bias: torch.Tensor |
     """Y [m, n] = act(pack(X) w^T + b): convrot_fp8_pack_activations and convrot_fp8_linear in one call.
     Y has out's, out_dtype's or X's type. ``work`` (uint8) is allocated here when not given."""
     if out is None:
-        out = _empty((X.shape[0], w.q.shape[0]), out_dtype or X.dtype, X.device, stream)
+        out = _cr._empty((X.shape[0], w.q.shape[0]), out_dtype or X.dtype, X.device, stream)
     _check(load().linear(X, None, w.q, w.scale, bias, act, out, work, dev_status, stream), "convrot_fp8_pack_linear")
     return out
 
@@ -201,9 +189,9 @@ def convrot_gated_norm(x: torch.Tensor, y: torch.Tensor | None = None, *, gate: 
     or x's. Without y there is no gate and no post norm's weight or bias (ValueError); without y and with res_scale 1
     and no out_h, the returned h is x itself. out_h may be x (in place)."""
     if out_h is None:
-        out_h = x if y is None and res_scale == 1.0 else _empty(x.shape, x.dtype, x.device, stream)
+        out_h = x if y is None and res_scale == 1.0 else _cr._empty(x.shape, x.dtype, x.device, stream)
     if out_n is None:
-        out_n = _empty(x.shape, x.dtype, x.device, stream)
+        out_n = _cr._empty(x.shape, x.dtype, x.device, stream)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
     _check(load().gated_norm(x, y, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre,
                                  pre_weight, pre_bias, eps, write_h, out_n, None, None, stream),
@@ -221,7 +209,7 @@ def convrot_gated_norm_pack(x: torch.Tensor, y: torch.Tensor | None = None, *, g
                             stream=None) -> tuple[torch.Tensor, Fp8Rows]:
     """convrot_gated_norm with n written as the packed input of convrot_fp8_linear instead: (h, packed n)."""
     if out_h is None:
-        out_h = x if y is None and res_scale == 1.0 else _empty(x.shape, x.dtype, x.device, stream)
+        out_h = x if y is None and res_scale == 1.0 else _cr._empty(x.shape, x.dtype, x.device, stream)
     if out is None:
         out = empty_fp8_rows(*x.shape, x.device, stream)
     write_h = None if out_h is x and y is None and res_scale == 1.0 else out_h
@@ -263,11 +251,11 @@ def convrot_rotary(q: torch.Tensor, k: torch.Tensor | None, cos: torch.Tensor, s
     (default: token t uses row t). A position outside the table gives NaN and ERR_INVALID_ARG in dev_status.
     inverse turns by the opposite angles (the gradient). Any batch, token and head strides; out_q may be q itself."""
     if out_q is None:
-        out_q = _empty(q.shape, q.dtype, q.device, stream)
+        out_q = _cr._empty(q.shape, q.dtype, q.device, stream)
     if k is None:
         out_k = None
     elif out_k is None:
-        out_k = _empty(k.shape, k.dtype, k.device, stream)
+        out_k = _cr._empty(k.shape, k.dtype, k.device, stream)
     _check(load().rotary(q, k, cos, sin, positions, layout, inverse, out_q, out_k, dev_status, stream), "convrot_rotary")
     return out_q, out_k
 
@@ -340,7 +328,7 @@ def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: floa
             axis = torch.as_tensor(axis, dtype=torch.int32).to(device).contiguous()
             if axis.numel() != pairs:
                 raise ValueError("axis must name one axis for each frequency")
-    cos, sin = (_empty((count, pairs), torch.float32, device, stream) for _ in range(2))
+    cos, sin = (_cr._empty((count, pairs), torch.float32, device, stream) for _ in range(2))
     with torch.cuda.device(device):
         _check(_cr.load().convrot_rotary_table(_cr._ptr(positions), count, axes, freq.data_ptr(), _cr._ptr(axis), pairs,
                                                float(factor), cos.data_ptr(), sin.data_ptr(), pairs,

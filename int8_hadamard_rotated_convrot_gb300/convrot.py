@@ -176,13 +176,25 @@ class Packed:
         return q if self.codes == CODES_I8 else q.to(torch.int8)
 
 
-def empty_packed(rows: int, k: int, codes: int = CODES_I8, device=None) -> Packed:
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """An uninitialized tensor that a call on ``stream`` writes and the caller uses on its own, the current one. It
+    belongs to the former, behind whatever used its memory before, and is kept until the latter is done with it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def empty_packed(rows: int, k: int, codes: int = CODES_I8, device=None, stream=None) -> Packed:
     """Allocates (with torch) the buffers a pack call fills."""
     ldq = convrot_ldq(k)
     dtype = torch.int8 if codes == CODES_I8 else torch.bfloat16
     device = device or torch.device("cuda", torch.cuda.current_device())
-    q = torch.empty((rows, ldq), dtype=dtype, device=device)
-    s = torch.empty((rows,), dtype=torch.float32, device=device)
+    q = _empty((rows, ldq), dtype, device, stream)
+    s = _empty((rows,), torch.float32, device, stream)
     return Packed(q, s, rows, k, 0, codes)
 
 
@@ -200,10 +212,10 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-def _padded_out(m: int, n: int, dtype, device) -> torch.Tensor:
+def _padded_out(m: int, n: int, dtype, device, stream) -> torch.Tensor:
     """[m, n] output whose row pitch is a multiple of 4 elements (16-byte rows), as the ABI asks."""
     ld = (n + 3) // 4 * 4
-    return torch.empty((m, ld), dtype=dtype, device=device)[:, :n]
+    return _empty((m, ld), dtype, device, stream)[:, :n]
 
 
 def _pack(fn, X: torch.Tensor, G: int, codes: int, out: Packed | None, dev_status, stream,
@@ -211,7 +223,7 @@ def _pack(fn, X: torch.Tensor, G: int, codes: int, out: Packed | None, dev_statu
     if X.dtype != torch.float32 or not X.is_cuda or X.dim() != 2 or X.stride(1) != 1:
         raise TypeError("X must be a 2-D row-major float32 CUDA tensor")
     rows, k = X.shape
-    out = out or empty_packed(rows, k, codes, X.device)
+    out = out or empty_packed(rows, k, codes, X.device, stream)
     st = out.struct()
     _check(fn(_ptr(X), rows, k, X.stride(0), int(G), ctypes.byref(st), _ptr(dev_status), _stream(stream)),
            what)
@@ -237,7 +249,7 @@ def convrot_linear(x: Packed, w: Packed, bias: torch.Tensor | None = None, out: 
                    dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [m, n] fp32 = (Q_x Q_w^T) * s_x s_w + b."""
     if out is None:
-        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device)
+        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device, stream)
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda):
         raise TypeError("bias must be a float32 CUDA tensor")
     xs, ws = x.struct(), w.struct()
@@ -255,7 +267,7 @@ def convrot_linear_act(x: Packed, w: Packed, bias: torch.Tensor | None, act: int
                        stream=None) -> torch.Tensor:
     """Y [m, n] fp32 = act((Q_x Q_w^T) * s_x s_w + b), act one of ACT_*."""
     if out is None:
-        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device)
+        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device, stream)
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda):
         raise TypeError("bias must be a float32 CUDA tensor")
     xs, ws = x.struct(), w.struct()
@@ -283,10 +295,10 @@ def convrot_linear_act_pack(x: Packed, w: Packed, bias: torch.Tensor | None, act
     m, n = x.rows, w.rows
     need = linear_pack_work_bytes(m, n)
     if work is None:
-        work = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.q.device)
+        work = _empty((max(need, 1),), torch.uint8, x.q.device, stream)
     elif work.dtype != torch.uint8 or not work.is_cuda or work.dim() != 1 or work.numel() < need:
         raise ValueError(f"work must be a 1-D uint8 CUDA tensor of at least {need} bytes")
-    out = out or empty_packed(m, n, codes, x.q.device)
+    out = out or empty_packed(m, n, codes, x.q.device, stream)
     xs, ws, os_ = x.struct(), w.struct(), out.struct()
     _check(load().convrot_linear_act_pack(ctypes.byref(xs), ctypes.byref(ws), _ptr(bias), int(act), int(G),
                                           _ptr(work), int(work.numel()), ctypes.byref(os_), _ptr(dev_status),
@@ -300,11 +312,11 @@ def lora_cols(r: int) -> int:
     return int(load().convrot_lora_cols(int(r)))
 
 
-def _lora_out(rows: int, r: int, device) -> torch.Tensor:
+def _lora_out(rows: int, r: int, device, stream) -> torch.Tensor:
     cols = lora_cols(r)
     if cols == 0:
         raise ConvrotError(ERR_INVALID_ARG, "lora rank")
-    return torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    return _empty((rows, cols), torch.bfloat16, device, stream)
 
 
 def convrot_lora_prepare(B: torch.Tensor, scale: float, out: torch.Tensor | None = None,
@@ -315,7 +327,7 @@ def convrot_lora_prepare(B: torch.Tensor, scale: float, out: torch.Tensor | None
         raise TypeError("B must be a 2-D row-major float32 CUDA tensor")
     n, r = B.shape
     if out is None:
-        out = _lora_out(n, r, B.device)
+        out = _lora_out(n, r, B.device, stream)
     _check(load().convrot_lora_prepare(_ptr(B), n, r, B.stride(0), float(scale), _ptr(out), out.stride(0),
                                        _stream(stream)), "convrot_lora_prepare")
     return out
@@ -327,7 +339,9 @@ def convrot_lora_prepare_down(A: torch.Tensor, stream=None) -> torch.Tensor:
     if A.dtype != torch.float32 or not A.is_cuda or A.dim() != 2 or A.stride(1) != 1:
         raise TypeError("A must be a 2-D row-major float32 CUDA tensor")
     r, k = A.shape
-    out = torch.zeros((2 * r, (k + 3) // 4 * 4), dtype=torch.float32, device=A.device)
+    out = _empty((2 * r, (k + 3) // 4 * 4), torch.float32, A.device, stream)
+    with torch.cuda.stream(stream):
+        out.zero_()
     _check(load().convrot_lora_prepare_down(_ptr(A), r, k, A.stride(0), _ptr(out), out.stride(0), _stream(stream)),
            "convrot_lora_prepare_down")
     return out
@@ -343,7 +357,7 @@ def convrot_lora_down(X: torch.Tensor, A_ext: torch.Tensor, out: torch.Tensor | 
     m, k = X.shape
     r = A_ext.shape[0] // 2
     if out is None:
-        out = _lora_out(m, r, X.device)
+        out = _lora_out(m, r, X.device, stream)
     _check(load().convrot_lora_down(_ptr(X), m, k, X.stride(0), _ptr(A_ext), r, A_ext.stride(0), _ptr(out),
                                     out.stride(0), _ptr(dev_status), _stream(stream)), "convrot_lora_down")
     return out
@@ -382,7 +396,7 @@ def convrot_linear_lora(x: Packed, w: Packed, bias: torch.Tensor | None, act: in
     _check_matrix(t_ext, "T_ext", torch.bfloat16, x.rows, lora_cols(r))
     _check_cuda(T_ext=t_ext, B_ext=b_ext)
     if out is None:
-        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device)
+        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device, stream)
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda):
         raise TypeError("bias must be a float32 CUDA tensor")
     xs, ws = x.struct(), w.struct()
@@ -413,7 +427,7 @@ def convrot_linear_lora_noalloc(x: Packed, w: Packed, bias: torch.Tensor | None,
     _check_lora_up(w, b_ext, r)
     _check_cuda(X=X, A_ext=A_ext, B_ext=b_ext)
     if out is None:
-        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device)
+        out = _padded_out(x.rows, w.rows, torch.float32, x.q.device, stream)
     if bias is not None and (bias.dtype != torch.float32 or not bias.is_cuda):
         raise TypeError("bias must be a float32 CUDA tensor")
     xs, ws = x.struct(), w.struct()
@@ -429,7 +443,7 @@ def convrot_gemm_i32(x: Packed, w: Packed, out: torch.Tensor | None = None,
                      dev_status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """A [m, n] int32 = Q_x Q_w^T."""
     if out is None:
-        out = _padded_out(x.rows, w.rows, torch.int32, x.q.device)
+        out = _padded_out(x.rows, w.rows, torch.int32, x.q.device, stream)
     xs, ws = x.struct(), w.struct()
     _check(load().convrot_gemm_i32(ctypes.byref(xs), ctypes.byref(ws), _ptr(out),
                                    out.stride(0) if out.dim() == 2 else 0, _ptr(dev_status),
@@ -461,7 +475,7 @@ def quantize_weights_grouped(Ws, G: int, codes: int = CODES_I8, stream=None) -> 
     if any(W.shape[1] != k for W in Ws):
         raise ValueError("grouped weights need the same input features")
     rows = sum(W.shape[0] for W in Ws)
-    out = empty_packed(rows, k, codes, Ws[0].device)
+    out = empty_packed(rows, k, codes, Ws[0].device, stream)
     r0 = 0
     for W in Ws:
         n = W.shape[0]
