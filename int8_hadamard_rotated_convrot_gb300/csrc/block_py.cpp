@@ -8,6 +8,7 @@
 // strides, one device for all), and returns the C call's status, made with that
 // device current.
 #include <Python.h>
+#include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -166,12 +167,31 @@ public:
     }
     void record(const Tensor &t) const
     {
-        if (guard_.current_stream() && t.defined()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), here_);
+        if (guard_.current_stream() && t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), here_);
     }
 
 private:
     c10::cuda::CUDAStream here_;
     c10::cuda::OptionalCUDAStreamGuard guard_;
+};
+
+// A workspace of the call alone: of its stream's memory, and back to it when the call is queued.
+class Workspace {
+public:
+    Workspace() = default;
+    Workspace(const Workspace &) = delete;
+    ~Workspace()
+    {
+        if (p_) c10::cuda::CUDACachingAllocator::raw_delete(p_);
+    }
+    void *get(int64_t bytes, cudaStream_t stream)
+    {
+        if (bytes > 0) p_ = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(static_cast<size_t>(bytes), stream);
+        return p_;
+    }
+
+private:
+    void *p_ = nullptr;
 };
 
 bool integer(PyObject *o, int64_t &v)
@@ -380,19 +400,9 @@ PyObject *gated_norm(PyObject *const *v, Py_ssize_t n)
     return status(convrot_gated_norm(&a, stream));
 }
 
-constexpr int64_t kWorkBehind = 2 << 20;
-
-// A contiguous tensor of the sizes at an offset of another's memory, without a trip through the dispatcher.
-Tensor part_of(const Tensor &whole, int64_t offset, at::IntArrayRef sizes)
-{
-    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
-    t.unsafeGetTensorImpl()->set_storage_offset(offset);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
-    return t;
-}
-
 // (h, y, dh, dn, gate, scale, shift, rows_per_batch, res_scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
-//  work, stream) -> status, or the dict of gradients. They are allocated here, the small ones as parts of one buffer.
+//  work, stream) -> status, or the dict of gradients. They are allocated here, each for itself: whoever
+// keeps one of them keeps no more than that.
 PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
 {
     REQUIRE(count(n, 18));
@@ -423,48 +433,44 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
     REQUIRE(vector(v[14], "pre_bias", p, d, &a.pre_bias) && real(v[15], a.eps));
     REQUIRE(workspace(v[16], &a.work, &a.work_bytes) && stream_of(v[17], *h, stream));
     struct Small {
-        const char *name;
+        PyObject *name;
         PyObject *of;
         bool of_samples;
         float **to;
         Tensor grad;
-    } small[7] = {{"dgate", v[4], true, &a.dgate, {}},           {"dscale", v[5], true, &a.dscale, {}},
-                  {"dshift", v[6], true, &a.dshift, {}},         {"dpost_weight", v[10], false, &a.dpost_weight, {}},
-                  {"dpost_bias", v[11], false, &a.dpost_bias, {}}, {"dpre_weight", v[13], false, &a.dpre_weight, {}},
-                  {"dpre_bias", v[14], false, &a.dpre_bias, {}}};
+    };
+    static PyObject *const names[7] = {
+        PyUnicode_InternFromString("dgate"),     PyUnicode_InternFromString("dscale"),     PyUnicode_InternFromString("dshift"),
+        PyUnicode_InternFromString("dpost_weight"), PyUnicode_InternFromString("dpost_bias"), PyUnicode_InternFromString("dpre_weight"),
+        PyUnicode_InternFromString("dpre_bias")};
+    Small small[7] = {{names[0], v[4], true, &a.dgate, {}},         {names[1], v[5], true, &a.dscale, {}},
+                      {names[2], v[6], true, &a.dshift, {}},        {names[3], v[10], false, &a.dpost_weight, {}},
+                      {names[4], v[11], false, &a.dpost_bias, {}},  {names[5], v[13], false, &a.dpre_weight, {}},
+                      {names[6], v[14], false, &a.dpre_bias, {}}};
     const DeviceOf device(*h);
     const OnStream allocate(stream, *h);
-    Tensor dx, dy, work;
-    const auto like = h->options().requires_grad(c10::nullopt);
-    dx = at::empty({m, d}, like);
-    if (v[1] != Py_None) dy = at::empty({m, d}, like);
-    allocate.record(dx);
-    allocate.record(dy);
-    int64_t floats = 0;
-    for (const Small &s : small) floats += s.of == Py_None ? 0 : (s.of_samples ? batches : 1) * d;
-    // An allocation costs about as much as a launch: a small workspace goes behind the small gradients, in one.
-    const bool own_work = v[16] == Py_None;
-    int64_t behind = 0;
-    if (own_work) {
-        a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
-        if (a.work_bytes <= kWorkBehind) behind = (a.work_bytes + 255) / 256 * 64 + 64;
-    }
-    const int64_t start = (floats + 63) / 64 * 64;
-    const Tensor all = at::empty({behind ? start + behind : floats}, like.dtype(at::kFloat));
-    allocate.record(all);
-    floats = 0;
+    // (straight from the allocator: a trip through the dispatcher for each costs as much as a launch)
+    c10::Allocator *const allocator = c10::cuda::CUDACachingAllocator::get();
+    auto fresh = [&](at::IntArrayRef sizes, at::ScalarType type) {
+        size_t bytes = c10::elementSize(type);
+        for (int64_t n : sizes) bytes *= static_cast<size_t>(n);
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, allocator->allocate(bytes), allocator, true),
+            c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        allocate.record(t);
+        return t;
+    };
+    Tensor dx = fresh({m, d}, t), dy = v[1] != Py_None ? fresh({m, d}, t) : Tensor();
     for (Small &s : small) {
         if (s.of == Py_None) continue;
-        s.grad = s.of_samples ? part_of(all, floats, {batches, d}) : part_of(all, floats, {d});
+        s.grad = s.of_samples ? fresh({batches, d}, at::kFloat) : fresh({d}, at::kFloat);
         *s.to = static_cast<float *>(s.grad.data_ptr());
-        floats += (s.of_samples ? batches : 1) * d;
     }
-    if (behind) {
-        const auto at = reinterpret_cast<uintptr_t>(static_cast<float *>(all.data_ptr()) + start);
-        a.work = reinterpret_cast<void *>((at + 255) / 256 * 256);
-    } else if (own_work) {
-        work = at::empty({a.work_bytes}, like.dtype(at::kByte));
-        a.work = work.data_ptr();
+    Workspace work;
+    if (v[16] == Py_None) {
+        a.work_bytes = convrot_gated_norm_backward_work_bytes(m, d, a.rows_per_batch);
+        a.work = work.get(a.work_bytes, stream);
     }
     a.h = mh.p;
     a.ldh = mh.ld;
@@ -485,14 +491,17 @@ PyObject *gated_norm_backward(PyObject *const *v, Py_ssize_t n)
     const convrot_status st = convrot_gated_norm_backward(&a, stream);
     if (st != CONVROT_OK) return status(st);
     PyObject *dict = PyDict_New();
-    auto put = [&](const char *name, const Tensor &grad) {
-        PyObject *o = grad.defined() ? THPVariable_Wrap(grad) : Py_NewRef(Py_None);
-        const bool ok = o && PyDict_SetItemString(dict, name, o) == 0;
+    bool ok = dict != nullptr;
+    auto put = [&](PyObject *name, Tensor &grad) {
+        if (!ok) return;
+        PyObject *o = grad.defined() ? THPVariable_Wrap(std::move(grad)) : Py_NewRef(Py_None);
+        ok = o && PyDict_SetItem(dict, name, o) == 0;
         Py_XDECREF(o);
-        return ok;
     };
-    bool ok = dict && put("dx", dx) && put("dy", dy);
-    for (const Small &s : small) ok = ok && put(s.name, s.grad);
+    static PyObject *const dx_name = PyUnicode_InternFromString("dx"), *const dy_name = PyUnicode_InternFromString("dy");
+    put(dx_name, dx);
+    put(dy_name, dy);
+    for (Small &s : small) put(s.name, s.grad);
     if (!ok) Py_CLEAR(dict);
     return dict;
 }

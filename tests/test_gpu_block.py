@@ -785,3 +785,18 @@ def test_tables_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         del kept
+
+
+def test_kept_gradients_hold_their_own_memory_alone():
+    import io
+
+    v, how = norm_case(60, 1024, 20, BF16, F32, 2, 2, True)
+    dh, dn = randn(gen(1), 60, 1024, dtype=BF16), randn(gen(2), 60, 1024, dtype=BF16)
+    got = bl.convrot_gated_norm_backward(v["x"], v["y"], dh, dn, **params(v), **own_args(how))
+    assert len({t.untyped_storage().data_ptr() for t in got.values()}) == len(got)
+    for name, t in got.items():
+        assert t.is_contiguous() and t.untyped_storage().nbytes() == t.numel() * t.element_size(), name
+        assert not t.requires_grad and t.device == v["x"].device
+    saved = io.BytesIO()
+    torch.save(got["dpre_weight"], saved)
+    assert saved.tell() < 2 * 4 * 1024
