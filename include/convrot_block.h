@@ -115,7 +115,9 @@ convrot_status convrot_fp8_pack_linear(const convrot_fp8_linear_args *a, cudaStr
  * plus the bias where those are given), CONVROT_NORM_RMS, v / sqrt(mean(v^2)
  * + eps), or CONVROT_NORM_LAYER, (v - mean) / sqrt(var + eps), followed by
  * their weight and bias. Everything between the loads and the one rounding
- * of each result is fp32; n is computed from h before h is rounded.
+ * of each result is fp32; n is computed from h before h is rounded. (Where
+ * scale meets a bias of pre, or gate one of post, an infinite factor may give
+ * NaN for infinity: the products with either part are added up.)
  */
 typedef enum { CONVROT_NORM_NONE = 0, CONVROT_NORM_RMS = 1, CONVROT_NORM_LAYER = 2 } convrot_norm_kind;
 

@@ -348,11 +348,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) gated_norm_ring_kernel(const 
         for (int e = 0; e < kValues; ++e) u[e] += 1.0f;
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) w_pre[e] = F2(u[2 * e] * v[2 * e], u[2 * e + 1] * v[2 * e + 1]);
-        vector(a.pre_bias, 0, 0.0f, v);
         vector(a.shift, sample * a.ldshift, 0.0f, w);
+        if (a.pre_bias) {  // (an infinite scale times a bias that is not there would be NaN)
+            vector(a.pre_bias, 0, 0.0f, v);
 #pragma unroll
-        for (int e = 0; e < kPairs; ++e)
-            b_pre[e] = F2(fmaf(u[2 * e], v[2 * e], w[2 * e]), fmaf(u[2 * e + 1], v[2 * e + 1], w[2 * e + 1]));
+            for (int e = 0; e < kValues; ++e) w[e] = fmaf(u[e], v[e], w[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) b_pre[e] = F2(w[2 * e], w[2 * e + 1]);
     };
     F2 h[kPairs];
     // mean out of h (layer norm), then 1 / deviation

@@ -800,3 +800,25 @@ def test_kept_gradients_hold_their_own_memory_alone():
     saved = io.BytesIO()
     torch.save(got["dpre_weight"], saved)
     assert saved.tell() < 2 * 4 * 1024
+
+
+# ---------------------------------------------------------------- infinite values
+
+
+@pytest.mark.parametrize("pre", [0, 1, 2])
+@pytest.mark.parametrize("m,d,pad", [(5, 256, 0), (19500, 256, 0), (19500, 258, 0), (19500, 257, 0), (6200, 1536, 8)])
+def test_gated_norm_of_an_infinite_scale(m, d, pad, pre):
+    """(1 + scale) times a finite value, then a finite shift: infinite with the value's sign, in every form of the kernel."""
+    g = gen(m + d)
+    x = randn(g, m, d + pad, dtype=BF16)[:, :d]
+    scale, shift = randn(g, 1, d), randn(g, 1, d)
+    scale[0, 3], scale[0, d - 1] = float("inf"), float("-inf")
+    for kw in (dict(shift=shift), dict(), dict(shift=shift, pre_weight=randn(g, d))):
+        _, n = bl.convrot_gated_norm(x, scale=scale, pre=pre, **kw)
+        _, want = ref.gated_norm(x.double(), scale=scale.double(), pre=pre, **{k: t.double() for k, t in kw.items()})
+        for c in (3, d - 1):
+            keep = torch.isinf(want[:, c])  # (a value of exactly zero times infinity is NaN)
+            assert keep.sum() >= m - m // 50 - 1 and torch.equal(n[keep, c].double(), want[keep, c])
+        rest = torch.ones(d, dtype=torch.bool, device="cuda")
+        rest[[3, d - 1]] = False
+        assert torch.isfinite(n[:, rest]).all()
