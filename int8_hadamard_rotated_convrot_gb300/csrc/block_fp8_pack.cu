@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_weights_kernel(const T *w, i
                                                                    int64_t ldq, float *scale, int64_t lds)
 {
     __shared__ float part[8];
-    const int64_t j = blockIdx.x, p = blockIdx.y;
+    const int64_t p = blockIdx.x, j = blockIdx.y;  // (the grid's second dimension has 16 bits: k's blocks fit)
     float amax = 0.0f;
     for (int i = threadIdx.x; i < 128 * 128; i += 256) {
         const int64_t r = p * 128 + i / 128, c = j * 128 + i % 128;
@@ -129,7 +129,7 @@ cudaError_t launch_fp8_pack(const void *x, int dtype, int64_t m, int64_t k, int6
 cudaError_t launch_fp8_quantize_weights(const void *w, int dtype, int64_t n, int64_t k, int64_t ldw, void *q,
                                         int64_t ldq, float *scale, int64_t lds, cudaStream_t stream)
 {
-    const dim3 grid(static_cast<unsigned>((k + 127) / 128), static_cast<unsigned>((n + 127) / 128));
+    const dim3 grid(static_cast<unsigned>((n + 127) / 128), static_cast<unsigned>((k + 127) / 128));
     return with_dtype(dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
         fp8_quantize_weights_kernel<T><<<grid, 256, 0, stream>>>(static_cast<const T *>(w), n, k, ldw,

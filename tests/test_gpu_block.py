@@ -841,3 +841,17 @@ def test_gradient_of_a_residual_stream_that_overflowed(m, d, post):
     assert torch.isfinite(want["dx"]).all() and torch.isfinite(want["dy"]).all()
     assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dy"], want["dy"])
     assert torch.isinf(got["dscale"][0, [5, d - 1, 0]]).all()
+
+
+# ---------------------------------------------------------------- sizes past a grid's limit, none, and one
+
+
+def test_quantize_weights_of_very_many_rows():
+    n = 65535 * 128 + 130
+    W = torch.zeros(n, 1, device="cuda", dtype=BF16)
+    W[::1000] = 3.0
+    W[-1] = -5.0
+    w = bl.convrot_fp8_quantize_weights(W)
+    scale, up = ref.block_scales(W, weights=True)
+    assert torch.equal(w.scale, scale)
+    assert torch.equal(w.q.view(torch.uint8), ref.e4m3_codes(W.float() * ref.spread(up, n, 1, weights=True)))
