@@ -318,7 +318,7 @@ def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: floa
     with torch.cuda.device(device), torch.cuda.stream(stream):
         positions = None
         if isinstance(rows, torch.Tensor):
-            positions = rows.to(torch.float64).reshape(rows.shape[0], -1).contiguous()
+            positions = rows.to(torch.float64).reshape(rows.shape[0], math.prod(rows.shape[1:])).contiguous()
             count, axes = positions.shape
         else:
             count, axes = int(rows), 1

@@ -247,7 +247,7 @@ convrot_status convrot_rotary_table(const double *positions, int64_t rows, int32
                                     int64_t ldt, cudaStream_t stream)
 {
     if (rows < 0 || rows > kMaxRows || axes < 1 || pairs < 1 || pairs > CONVROT_ROTARY_MAX_D / 2) return CONVROT_ERR_INVALID_ARG;
-    if (!positions && axes != 1) return CONVROT_ERR_INVALID_ARG;
+    if (!positions && axes != 1 && rows > 0) return CONVROT_ERR_INVALID_ARG;
     convrot_status st = first_of({check_matrix(freq, 1, pairs, pairs, 8), check_optional(positions, 1, 1, 1, 8),
                                   check_optional(axis, 1, 1, 1, 4), check_matrix(cos, rows, pairs, ldt, 4),
                                   check_matrix(sin, rows, pairs, ldt, 4)});

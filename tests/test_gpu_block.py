@@ -855,3 +855,12 @@ def test_quantize_weights_of_very_many_rows():
     scale, up = ref.block_scales(W, weights=True)
     assert torch.equal(w.scale, scale)
     assert torch.equal(w.q.view(torch.uint8), ref.e4m3_codes(W.float() * ref.spread(up, n, 1, weights=True)))
+
+
+def test_rotary_table_of_no_positions():
+    freq, _ = bl.rotary_frequencies(8)
+    for at in (torch.empty(0, device="cuda"), torch.empty(0, 1, device="cuda", dtype=torch.int64)):
+        cos, sin = bl.convrot_rotary_table(at, freq)
+        assert cos.shape == sin.shape == (0, 8)
+    cos, _ = bl.convrot_rotary_table(torch.empty(0, 3, device="cuda"), freq, [0, 1, 2, 0, 1, 2, 0, 1])
+    assert cos.shape == (0, 8)
