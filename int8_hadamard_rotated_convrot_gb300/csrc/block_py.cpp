@@ -553,7 +553,7 @@ PyObject *rotary(PyObject *const *v, Py_ssize_t n)
     }
     Matrix mc, ms;
     REQUIRE(matrix(v[2], "cos", at::kFloat, a.table_rows, cos->size(1), mc) && matrix(v[3], "sin", at::kFloat, a.table_rows, cos->size(1), ms));
-    if (mc.ld != ms.ld) {
+    if (a.table_rows > 1 && mc.ld != ms.ld) {
         raise(PyExc_ValueError, "cos and sin", "must have the same leading dimension");
         return nullptr;
     }

@@ -864,3 +864,16 @@ def test_rotary_table_of_no_positions():
         assert cos.shape == sin.shape == (0, 8)
     cos, _ = bl.convrot_rotary_table(torch.empty(0, 3, device="cuda"), freq, [0, 1, 2, 0, 1, 2, 0, 1])
     assert cos.shape == (0, 8)
+
+
+def test_rotary_with_a_table_of_one_row():
+    """One row has no leading dimension: cosines and sines of different strides are the same table."""
+    g = gen(31)
+    q = randn(g, 3, 1, 4, 32)
+    cos, sin = bl.convrot_rotary_table(torch.tensor([7.0], device="cuda"), bl.rotary_frequencies(16)[0])
+    wide = torch.zeros(1, 40, device="cuda")
+    wide[:, 8:24] = cos
+    want, _ = bl.convrot_rotary(q, None, cos, sin)
+    for c, s in ((wide[:, 8:24], sin), (cos, sin.as_strided((1, 16), (3, 1)))):
+        got, _ = bl.convrot_rotary(q, None, c, s)
+        assert torch.equal(got, want)
