@@ -193,8 +193,9 @@ convrot_status convrot_gated_norm_backward(const convrot_gated_norm_backward_arg
  *
  *   q, k       [batch, tokens, heads, head_dim] of type dtype with any batch,
  *              token and head strides (elements; >= 0) and head_dim
- *              contiguous. k may be NULL. out_q / out_k likewise; each may be
- *              its input with the same strides (in place).
+ *              contiguous. k may be NULL. out_q / out_k likewise, their heads
+ *              apart from one another; each may be its input with the same
+ *              strides (in place).
  *   cos, sin   fp32 [table_rows, ldt], ldt >= rot_dim / 2.
  *   positions  the table row of each token: int32 or int64 (position_bits)
  *              [batch, tokens] with pos_stride elements between batches

@@ -82,6 +82,20 @@ int64_t work_lds(int64_t m) { return groups(m, 4) * 4; }
 // Rows of a sample, with no more than there are (so that sums of rows stay far from 64 bits).
 int64_t sample_of(int64_t m, int64_t rows) { return rows < m ? rows : m > 1 ? m : 1; }
 
+// Whether an output's heads lie apart from one another (as far as two neighbours show it), and where the output is the
+// input itself, each head in its own place: threads read and write different heads in any order.
+bool rotary_output(const convrot_rotary_args &a, const void *in, const int64_t *in_strides, const void *out, const int64_t *strides, int64_t heads)
+{
+    const int64_t n[3] = {a.batch, a.tokens, heads};
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (strides[i] < a.head_dim || (in == out && strides[i] != in_strides[i])) return false;
+        for (int j = 0; j < i; ++j)
+            if (n[j] > 1 && strides[i] - strides[j] < a.head_dim && strides[j] - strides[i] < a.head_dim) return false;
+    }
+    return true;
+}
+
 convrot_status check_norm(int64_t m, int64_t d, int64_t rows, int dtype, int param_dtype, int post, int pre, float eps)
 {
     if (m < 0 || m > kMaxRows || d < 1 || rows < 1 || !known(dtype)) return CONVROT_ERR_INVALID_ARG;
@@ -229,6 +243,8 @@ convrot_status convrot_rotary(const convrot_rotary_args *a, cudaStream_t stream)
                                   check_optional(a->k, 1, 1, 1, s), check_matrix(a->out_q, a->q && a->q_heads, 1, 1, s),
                                   check_matrix(a->out_k, a->k && a->k_heads, 1, 1, s)});
     if (st != CONVROT_OK) return st;
+    if (a->q && a->q_heads && !rotary_output(*a, a->q, a->q_strides, a->out_q, a->out_q_strides, a->q_heads)) return CONVROT_ERR_INVALID_ARG;
+    if (a->k && a->k_heads && !rotary_output(*a, a->k, a->k_strides, a->out_k, a->out_k_strides, a->k_heads)) return CONVROT_ERR_INVALID_ARG;
     if (a->positions) {
         if (a->position_bits != 32 && a->position_bits != 64) return CONVROT_ERR_INVALID_ARG;
         if (!aligned(a->positions, a->position_bits / 8)) return CONVROT_ERR_ALIGNMENT;

@@ -339,3 +339,11 @@ def test_samples_longer_than_the_call(lib, rows):
         assert lib.convrot_gated_norm_backward(grad_args(**bad, rows=rows), None) == cr.ERR_INVALID_ARG
         assert lib.convrot_gated_norm(norm_args(**bad, rows=rows), None) == cr.ERR_INVALID_ARG
     assert lib.convrot_gated_norm_backward(grad_args(rows=rows, work_bytes=0), None) == cr.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [
+    dict(oq=FAKE + 4096, oqs=(1536, 512, 0)), dict(oq=FAKE + 4096, oqs=(1536, 0, 128)), dict(oq=FAKE + 4096, oqs=(0, 512, 128)),
+    dict(oq=FAKE + 4096, oqs=(1536, 512, 127)), dict(oq=FAKE + 4096, oqs=(512, 512, 128)), dict(oq=FAKE + 4096, oqs=(600, 512, 128)),
+    dict(ok=FAKE + 4096, oks=(768, 256, 64)), dict(oqs=(4096, 512, 128)), dict(oks=(768, 512, 128))], ids=str)
+def test_rotary_refuses_outputs_over_one_another_or_their_input(lib, kw):
+    assert lib.convrot_rotary(rotary_args(**kw), None) == cr.ERR_INVALID_ARG

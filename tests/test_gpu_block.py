@@ -877,3 +877,18 @@ def test_rotary_with_a_table_of_one_row():
     for c, s in ((wide[:, 8:24], sin), (cos, sin.as_strided((1, 16), (3, 1)))):
         got, _ = bl.convrot_rotary(q, None, c, s)
         assert torch.equal(got, want)
+
+
+def test_rotary_of_single_batches_tokens_and_heads_at_any_strides():
+    """What there is one of has no stride to speak of, in place as well."""
+    g = gen(33)
+    cos, sin = bl.convrot_rotary_table(4, bl.rotary_frequencies(16)[0])
+    for b, t, h in ((1, 4, 3), (2, 1, 3), (2, 4, 1), (1, 1, 1)):
+        q = randn(g, b, t, h, 32)
+        want, _ = bl.convrot_rotary(q, None, cos, sin)
+        strides = [0 if n == 1 else s for n, s in zip(q.shape[:3], q.stride()[:3])] + [1]
+        out = torch.empty_like(q)
+        bl.convrot_rotary(q, None, cos, sin, out_q=out.as_strided(q.shape, strides))
+        assert torch.equal(out, want)
+        bl.convrot_rotary(q, None, cos, sin, out_q=q.as_strided(q.shape, strides))
+        assert torch.equal(q, want)
