@@ -114,7 +114,9 @@ def empty_fp8_rows(m: int, k: int, device=None, stream=None) -> Fp8Rows:
 
 def fp8_weights_from_codes(q: torch.Tensor, scale: torch.Tensor) -> Fp8Weights:
     """A checkpoint's codes [n, k] and scales as Fp8Weights, copied only if the rows of q do not
-    start on 16 bytes."""
+    start on 16 bytes. Codes are torch.float8_e4m3fn (bytes: viewed as that)."""
+    if q.dtype != _E4M3 or q.dim() != 2:
+        raise TypeError("codes must be a 2-D float8_e4m3fn tensor")
     n, k = q.shape
     if q.stride(1) != 1 or q.stride(0) % 16 or q.data_ptr() % 16:
         codes = fp8_codes(n, k, q.device)

@@ -347,3 +347,17 @@ def test_samples_longer_than_the_call(lib, rows):
     dict(ok=FAKE + 4096, oks=(768, 256, 64)), dict(oqs=(4096, 512, 128)), dict(oks=(768, 512, 128))], ids=str)
 def test_rotary_refuses_outputs_over_one_another_or_their_input(lib, kw):
     assert lib.convrot_rotary(rotary_args(**kw), None) == cr.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("k", [48, 50])
+def test_checkpoint_codes_of_another_type_are_refused(k):
+    """Whether or not the rows have to be copied: 8-bit integers or e5m2 values are not e4m3 codes."""
+    scale = torch.ones(1, 1)
+    for dtype in (torch.float8_e5m2, torch.int8, torch.uint8, torch.float32):
+        with pytest.raises(TypeError):
+            bl.fp8_weights_from_codes(torch.zeros(16, k, dtype=dtype), scale)
+    with pytest.raises(TypeError):
+        bl.fp8_weights_from_codes(torch.zeros(16, dtype=torch.float8_e4m3fn), scale)
+    codes = torch.arange(16 * k, dtype=torch.int64).remainder(120).to(torch.uint8).view(16, k).view(torch.float8_e4m3fn)
+    w = bl.fp8_weights_from_codes(codes, scale.bfloat16())
+    assert torch.equal(w.q.view(torch.uint8), codes.view(torch.uint8)) and w.q.stride(0) % 16 == 0 and w.scale.dtype == torch.float32
