@@ -323,8 +323,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             if (a.post != CONVROT_NORM_NONE) {
                 inv_y = rsqrtf(fmaf(m[1], inv_d, a.eps));
-                const float hwy_part = a.pre != CONVROT_NORM_NONE ? inv * mgh * m[6] : 0.0f;
-                mqy = -(inv * (m[4] + mg * m[5] + hwy_part) + m[7]) * inv_y * inv_d;
+                mqy = -(inv * (m[4] + mg * m[5] + inv * mgh * m[6]) + m[7]) * inv_y * inv_d;
             }
         }
         get(2, v);
@@ -335,17 +334,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             s0[e] = s0[e] + g[e];
             s1[e] = fma2(g[e], h[e], s1[e]);
             g[e] = fma2(g[e], w_pre[e], F2(mg));
+            v[e] = fma2(F2(inv), fma2(h[e], F2(mgh), g[e]), v[e]);  // dH
+            g[e] = v[e] * F2(a.res_scale);
         }
-        // dH; without a norm h has no part in it (0 times an infinite h would be NaN)
-        if (a.pre != CONVROT_NORM_NONE) {
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) v[e] = fma2(F2(inv), fma2(h[e], F2(mgh), g[e]), v[e]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kPairs; ++e) v[e] = v[e] + g[e];
-        }
-#pragma unroll
-        for (int e = 0; e < kPairs; ++e) g[e] = v[e] * F2(a.res_scale);
         if (dx) {
             put(dx, g);
             dx += a.lddx;
@@ -373,10 +364,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     mq = -m[0] * inv_d;
                     mqy = -m[1] * inv_d;
                 }
-                if (a.post != CONVROT_NORM_NONE) {
 #pragma unroll
-                    for (int e = 0; e < kPairs; ++e) g[e] = F2(inv_y) * fma2(y[e], F2(mqy), g[e] + F2(mq));
-                }
+                for (int e = 0; e < kPairs; ++e) g[e] = F2(inv_y) * fma2(y[e], F2(mqy), g[e] + F2(mq));
                 put(dy, g);
                 dy += a.lddy;
             }
