@@ -159,7 +159,9 @@ convrot_status convrot_gated_norm(const convrot_gated_norm_args *a, cudaStream_t
  *   dgate, dscale, dshift             fp32 [batches, d], dense
  *   dpost_weight, dpost_bias, dpre_weight, dpre_bias   fp32 [d]
  *
- * each may be NULL (not wanted). The remaining fields are the forward call's;
+ * each may be NULL (not wanted). Infinite values of h, or of y, may make the
+ * gradients of their row NaN, and the sums over rows with them, also where no
+ * norm stands on them. The remaining fields are the forward call's;
  * shift has no part in any gradient. Sums over rows are fp32 in an order that
  * depends on the sizes alone, so results are deterministic.
  *   work       256-byte aligned, convrot_gated_norm_backward_work_bytes(m, d,

@@ -824,6 +824,20 @@ def test_gated_norm_of_an_infinite_scale(m, d, pad, pre):
         assert torch.isfinite(n[:, rest]).all()
 
 
+@pytest.mark.parametrize("pre,post", [(0, 1), (1, 0), (2, 2)])
+@pytest.mark.parametrize("m,d", [(40, 256), (7, 257), (5, 6000)])
+def test_infinite_values_stay_in_their_rows_of_dx_and_dy(m, d, pre, post):
+    g = gen(m + d + post)
+    h, y, dh, dn = (randn(g, m, d, dtype=F16) for _ in range(4))
+    kw = dict(scale=randn(g, 1, d, std=0.3), gate=randn(g, 1, d), pre=pre, post=post, post_weight=randn(g, d))
+    want = bl.convrot_gated_norm_backward(h, y, dh, dn, **kw)
+    h[1, 5], h[2, d - 1], y[4, 0] = float("inf"), float("-inf"), float("inf")
+    got = bl.convrot_gated_norm_backward(h, y, dh, dn, **kw)
+    for r in range(m):
+        if r not in (1, 2, 4):
+            assert torch.equal(got["dx"][r], want["dx"][r]) and torch.equal(got["dy"][r], want["dy"][r])
+
+
 # ---------------------------------------------------------------- sizes past a grid's limit, none, and one
 
 
