@@ -9,9 +9,10 @@
 // instructions) whose sums are drained, multiplied by the row's and the
 // block's scale and added up in fp32 registers.
 //
-// fp8_pair_kernel (more than 64 rows): a CTA pair (cluster of 2, cta_group::2),
-// persistent over 256 x kBN output tiles, with the roles and the ring of the
-// int8 GEMM:
+// fp8_pair_kernel (the calls that block_fp8_few.cu leaves: more than 64 rows,
+// and more tiles than it has resident at once): a CTA pair (cluster of 2,
+// cta_group::2), persistent over 256 x kBN output tiles, with the roles and the
+// ring of the int8 GEMM:
 //   warp 0      TMA producer of each CTA: a block's codes of its 128 rows of x
 //               and kBN / 2 rows of w, 128 bytes a row, 128-byte swizzled
 //   warp 1      tensor memory; in the even CTA one thread issues the MMAs
@@ -125,8 +126,9 @@ __device__ __forceinline__ void commit_local(uint32_t bar)
 
 // A drained buffer is handed back without a release: this warp wrote nothing
 // that the MMA thread reads, and its tensor-memory loads have completed
-// (wait::ld) before it arrives. (With a release at cluster scope, which
-// waits for everything this thread has in flight: 4.70 ms instead of 2.63.)
+// (wait::ld) and are fenced (before_thread_sync) before it arrives: the three
+// stay together. (With a release at cluster scope, which waits for everything
+// this thread has in flight: 4.70 ms instead of 2.63.)
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");

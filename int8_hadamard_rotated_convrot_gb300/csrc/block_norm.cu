@@ -9,10 +9,11 @@
 // coalesced single elements otherwise. The statistics are two-pass (mean, then
 // squares about it), which costs one more trip around the block than a
 // one-pass sum of squares and keeps layer norms of rows with a large mean.
-// Measured on one GB300, 32760 x 5120 in bf16 with RMS norms on both sides: 219
-// us, 6.1 TB/s, 90 % of a measured copy; 4097 x 1155 in f16, single elements:
-// 10.7 us, 2.7 TB/s, bound by instructions. One block a row, without the runs
-// of rows below, takes 316 and 24 us.
+// Measured on one GB300, 32760 x 5120 in bf16 with RMS norms on both sides: 222
+// us, 6.0 TB/s, 89 % of a measured copy (216 us with parameters in f32); 4097 x
+// 1155 in f16, single elements: 10.7 us, 2.7 TB/s, bound by instructions. One
+// block a row, without the runs of rows below, takes 316 and 24 us; its form for
+// single elements of rows above 8192 spills 656 to 760 bytes a thread.
 #include <cfloat>
 
 #include "block_norm.cuh"

@@ -25,8 +25,12 @@
 // goes along too. One trip for RMS norms, one more for the means of a layer
 // norm, and one more if post is one. Measured at 8190 x 5120 in bf16 with RMS
 // norms: 142 us with the sums, 3.5 TB/s (52 % of a copy); issue slots are 39 %
-// busy, the rest is the latency of the trips. Clusters of two blocks with two of
-// them an SM, for two rows under way: 190 us.
+// busy, the rest is the latency of the trips and of spilled registers: ten warps
+// put three on two of an SM's four schedulers, which leaves a thread 168, and
+// every form of the kernel spills (bytes stored a thread: 244 here, 256 in
+// clusters, 324 to 380 in f32, 352 to 748 in unaligned rows). Any statement more
+// in the loop costs (3 to 6 % for one select a value). Clusters of two blocks
+// with two of them an SM, for two rows under way: 190 us.
 #include "block_norm.cuh"
 
 namespace convrot {
@@ -49,7 +53,8 @@ struct GradSplit {
         width = static_cast<int>(((d + cluster - 1) / cluster + 31) / 32 * 32);
         threads = ((width + kGradCols - 1) / kGradCols + 31) / 32 * 32;
         batches = (m + rows - 1) / rows;
-        // one wave of resident blocks, and no unit without a row
+        // one wave of resident blocks, and no unit without a row (counted by threads: of blocks of 128 to 288 threads
+        // registers and shared memory would allow one or two an SM more)
         const int64_t resident = kSms * (threads >= kGradThreads ? 1 : kGradThreads / threads);
         const int64_t longest = rows < m ? rows : m;
         chunks = resident / cluster / batches;

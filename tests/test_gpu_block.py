@@ -887,3 +887,34 @@ def test_rotary_of_single_batches_tokens_and_heads_at_any_strides():
         assert torch.equal(out, want)
         bl.convrot_rotary(q, None, cos, sin, out_q=q.as_strided(q.shape, strides))
         assert torch.equal(q, want)
+
+
+def test_gradients_are_ordinary_tensors_and_capture():
+    v, how = norm_case(60, 1024, 20, BF16, F32, 2, 2, True)
+    dh, dn = randn(gen(1), 60, 1024, dtype=BF16), randn(gen(2), 60, 1024, dtype=BF16)
+    call = lambda: bl.convrot_gated_norm_backward(v["x"], v["y"], dh, dn, **params(v), **own_args(how))
+    want = call()
+    got = call()
+    leaf = got["dpre_weight"].clone().requires_grad_()
+    (leaf * got["dpre_bias"]).sum().backward()  # as a constant of a graph
+    assert torch.equal(leaf.grad, want["dpre_bias"])
+    got["dscale"].add_(1).mul_(2)
+    assert torch.equal(got["dscale"], (want["dscale"] + 1) * 2)
+    weight = torch.nn.Parameter(torch.zeros(1024, device="cuda"))
+    weight.grad = got["dpre_weight"]
+    torch.optim.SGD([weight], lr=1.0).step()
+    assert torch.equal(weight.detach(), -want["dpre_weight"])
+    with torch.inference_mode():
+        assert torch.equal(call()["dgate"], want["dgate"])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    X, w = randn(gen(3), 300, 512), bl.convrot_fp8_quantize_weights(randn(gen(4), 256, 512))
+    y = bl.convrot_fp8_pack_linear(X, w)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):  # with the workspaces that the calls allocate
+        kept, z = call(), bl.convrot_fp8_pack_linear(X, w)
+    for _ in range(3):
+        for t in (*kept.values(), z):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(kept[n], want[n]) for n in want) and torch.equal(z, y)
