@@ -1,7 +1,9 @@
 /*
  * convrot_block.h -- C ABI of the operators that stand between the linears of
  * a transformer block: a linear on 8-bit floating-point codes with block
- * scales, the gated norm with its gradient, and rotary positions.
+ * scales, the gated norm with its gradient, rotary positions, the gated
+ * feed-forward's projections and attention to other states, both with their
+ * gradients.
  *
  * The conventions are convrot.h's: device pointers, row-major layouts with a
  * leading dimension in elements, buffers owned by the caller, arguments
@@ -239,6 +241,154 @@ convrot_status convrot_rotary(const convrot_rotary_args *a, cudaStream_t stream)
 convrot_status convrot_rotary_table(const double *positions, int64_t rows, int32_t axes, const double *freq,
                                     const int32_t *axis, int32_t pairs, double factor, float *cos, float *sin,
                                     int64_t ldt, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The input half of a gated feed-forward on 16-bit weights: both projections,
+ * the activation and the product.
+ *
+ *   g = x w_gate^T + b_gate,  u = x w_up^T + b_up
+ *   y = act(g) * u
+ *
+ * act is a convrot_activation or CONVROT_ACT_SILU, v / (1 + e^-v). The products
+ * run on the tensor cores with fp32 sums; y is rounded once, from the fp32 g and u.
+ *
+ *   x          [m, ldx], w_gate, w_up [n, ldw*], all of type dtype (CONVROT_BF16
+ *              or CONVROT_F16; CONVROT_F32 is CONVROT_ERR_UNSUPPORTED).
+ *   b_gate, b_up   fp32 [n], each may be NULL.
+ *   y          [m, ldy] of type dtype.
+ *   gate, up   NULL, or both: g and u rounded to dtype, for the gradient.
+ *   work       256-byte aligned, convrot_gated_linear_work_bytes(a) bytes: 0
+ *              where the rows of x and of the weights start on 16 bytes, else
+ *              room for copies of those that do not. The function reads the
+ *              tensors' addresses and leading dimensions, and no memory.
+ *   dev_status as for convrot_linear.
+ * m == 0 or n == 0 launches nothing; 1 <= k. Outputs must not overlap inputs.
+ */
+enum { CONVROT_ACT_SILU = 3 };
+
+typedef struct {
+    const void *x, *w_gate, *w_up;
+    const float *b_gate, *b_up;
+    void *y, *gate, *up;
+    void *work;
+    int32_t *dev_status;
+    int64_t m, n, k;
+    int64_t ldx, ldw_gate, ldw_up, ldy, ldgate, ldup;
+    int64_t work_bytes;
+    int32_t dtype, act;
+} convrot_gated_linear_args;
+
+int64_t convrot_gated_linear_work_bytes(const convrot_gated_linear_args *a);
+convrot_status convrot_gated_linear(const convrot_gated_linear_args *a, cudaStream_t stream);
+
+/*
+ * Its gradient, from x, the weights, the kept gate and up and the gradient dy of y:
+ *
+ *   dg = dy u act'(g),  du = dy act(g)
+ *   dx = dg w_gate + du w_up          [m, lddx] of type dtype
+ *   dw_gate = dg^T x, dw_up = du^T x  [n, lddw*] of type dtype
+ *   db_gate, db_up                    column sums of dg and du, fp32 [n]
+ *
+ * dx, the pair dw_* and the pair db_* may be NULL (not wanted; x is then not read where the
+ * weights' gradients are not wanted). dg and du are rounded to dtype for the products, as their
+ * operands have to be; the column sums are those of the unrounded fp32 values, added up in an
+ * order that depends on the sizes alone.
+ *   work       256-byte aligned, convrot_gated_linear_backward_work_bytes(a)
+ *              bytes: dg and du, the partial column sums, and copies of operands
+ *              whose rows do not start on 16 bytes.
+ * m == 0: the gradients of the weights and biases are zero.
+ */
+typedef struct {
+    const void *x, *w_gate, *w_up, *gate, *up, *dy;
+    void *dx, *dw_gate, *dw_up;
+    float *db_gate, *db_up;
+    void *work;
+    int32_t *dev_status;
+    int64_t m, n, k;
+    int64_t ldx, ldw_gate, ldw_up, ldgate, ldup, lddy, lddx, lddw_gate, lddw_up;
+    int64_t work_bytes;
+    int32_t dtype, act;
+} convrot_gated_linear_backward_args;
+
+int64_t convrot_gated_linear_backward_work_bytes(const convrot_gated_linear_backward_args *a);
+convrot_status convrot_gated_linear_backward(const convrot_gated_linear_backward_args *a, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention to states of another length (a prompt's, an encoder's):
+ *
+ *   s_ij = scale q_i . k_j,  lse_i = log(sum_j e^(s_ij))  over the keys that are there
+ *   out_i = sum_j e^(s_ij - lse_i) v_j
+ *
+ * A query without keys (all masked, or kv_tokens == 0) has out 0 and lse -infinity.
+ * What stands in a masked key or value (NaN too) does not reach any result.
+ *
+ *   q, out     [batch, q_tokens, q_heads, head_dim] of type dtype (CONVROT_BF16
+ *              or CONVROT_F16; CONVROT_F32 is CONVROT_ERR_UNSUPPORTED),
+ *   k, v       [batch, kv_tokens, kv_heads, head_dim]: query head h reads head
+ *              h / (q_heads / kv_heads); kv_heads divides q_heads.
+ *              Strides (elements, >= 0) of batch, token and head for each,
+ *              head_dim contiguous; out's heads apart from one another.
+ *   mask       uint8 [batch, kv_tokens] with mask_stride elements between
+ *              batches: 0 where a key is not there; or NULL.
+ *   lse        fp32 [batch, q_heads, q_tokens], dense.
+ *   scale      finite, > 0.
+ *   work       256-byte aligned, convrot_attention_work_bytes(a) bytes: 0, or
+ *              room for the keys that are there (with a mask), and for copies of
+ *              tensors whose heads do not start on 16 bytes, and for partial
+ *              results of calls with few queries.
+ *   dev_status as for convrot_linear.
+ * 1 <= head_dim <= CONVROT_ATTENTION_MAX_D (CONVROT_ERR_UNSUPPORTED above).
+ * Probabilities are rounded to dtype for their product with v, whose operands
+ * have one type; the sums of a softmax are fp32, of the unrounded values.
+ */
+#define CONVROT_ATTENTION_MAX_D 128
+
+typedef struct {
+    const void *q, *k, *v;
+    const uint8_t *mask;
+    void *out;
+    float *lse;
+    void *work;
+    int32_t *dev_status;
+    int64_t batch, q_tokens, kv_tokens, q_heads, kv_heads;
+    int64_t q_strides[3], k_strides[3], v_strides[3], out_strides[3]; /* batch, token, head */
+    int64_t mask_stride, work_bytes;
+    float scale;
+    int32_t head_dim, dtype, reserved; /* 0 */
+} convrot_attention_args;
+
+int64_t convrot_attention_work_bytes(const convrot_attention_args *a);
+convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t stream);
+
+/*
+ * Its gradient, from the forward call's tensors and the gradient dout of out
+ * (with its strides):
+ *
+ *   P_ij = e^(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . out_i)
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ *
+ * dq, dk, dv   dense [batch, tokens, heads, head_dim] of type dtype; dk and dv are
+ *              summed over the query heads that share a head and are 0 at
+ *              masked keys.
+ * P and dS are rounded to dtype for their products. Sums are fp32, in an order
+ * that depends on the sizes (and, with a mask, on the number of keys) alone.
+ */
+typedef struct {
+    const void *q, *k, *v, *out, *dout;
+    const uint8_t *mask;
+    const float *lse;
+    void *dq, *dk, *dv;
+    void *work;
+    int32_t *dev_status;
+    int64_t batch, q_tokens, kv_tokens, q_heads, kv_heads;
+    int64_t q_strides[3], k_strides[3], v_strides[3], out_strides[3], dout_strides[3];
+    int64_t mask_stride, work_bytes;
+    float scale;
+    int32_t head_dim, dtype, reserved; /* 0 */
+} convrot_attention_backward_args;
+
+int64_t convrot_attention_backward_work_bytes(const convrot_attention_backward_args *a);
+convrot_status convrot_attention_backward(const convrot_attention_backward_args *a, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

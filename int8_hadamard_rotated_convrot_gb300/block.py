@@ -2,7 +2,8 @@
 
 What stands between two linears of a transformer block, as CUDA kernels of
 libconvrot: a linear on e4m3 codes with block scales, the gated norm with its
-gradient, and rotary positions. As in ``convrot``, this is argument handling
+gradient, rotary positions, the projections of a gated feed-forward and
+attention to other states, both with their gradients. As in ``convrot``, this is argument handling
 only; there is no fallback, and a refused call raises ``ConvrotError`` (or
 TypeError / ValueError for tensors that the C side, which sees pointers and
 sizes, cannot check). The tensors are taken apart in native code
@@ -23,11 +24,13 @@ from . import convrot as _cr
 from .convrot import ACT_GELU_ERF, ACT_GELU_TANH, ACT_NONE, ConvrotError  # noqa: F401
 
 F32, BF16, F16 = range(3)
+ACT_SILU = 3  # of the gated linear, beside ACT_NONE and the two GELUs
 NORM_NONE, NORM_RMS, NORM_LAYER = range(3)
 ROTARY_HALF, ROTARY_INTERLEAVED = range(2)
 FP8_BLOCK = 128
 NORM_MAX_D = 16384
 ROTARY_MAX_D = 4096
+ATTENTION_MAX_D = 128
 
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _E4M3 = torch.float8_e4m3fn
@@ -336,3 +339,72 @@ def convrot_rotary_table(rows: int | torch.Tensor, freq, axis=None, factor: floa
                                                float(factor), cos.data_ptr(), sin.data_ptr(), pairs,
                                                _stream(device, stream)), "convrot_rotary_table")
     return cos, sin
+
+
+# ---------------------------------------------------------------- the gated feed-forward's projections
+
+
+def convrot_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, b_gate: torch.Tensor | None = None,
+                         b_up: torch.Tensor | None = None, act: int = ACT_SILU, *, keep: bool = False,
+                         out: torch.Tensor | None = None, work: torch.Tensor | None = None,
+                         dev_status: torch.Tensor | None = None, stream=None):
+    """y [m, n] = act(x w_gate^T + b_gate) * (x w_up^T + b_up), in one kernel.
+
+    x [m, k] and the weights [n, k] (two tensors, or the halves of one) are bfloat16 or float16, the biases float32 [n];
+    act is ACT_SILU, ACT_GELU_ERF, ACT_GELU_TANH or ACT_NONE. With ``keep``, (y, gate, up): both projections too, rounded
+    to x's type, as convrot_gated_linear_backward takes them. Rows that do not start on 16 bytes are copied in each call
+    (``work``, uint8, is allocated here when not given)."""
+    m, n = x.shape[0], w_gate.shape[0]
+    if out is None:
+        out = _cr._empty((m, n), x.dtype, x.device, stream)
+    gate, up = (_cr._empty((m, n), x.dtype, x.device, stream) for _ in range(2)) if keep else (None, None)
+    _check(load().gated_linear(x, w_gate, w_up, b_gate, b_up, act, out, gate, up, work, dev_status, stream), "convrot_gated_linear")
+    return (out, gate, up) if keep else out
+
+
+def convrot_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
+                                  up: torch.Tensor, dy: torch.Tensor, act: int = ACT_SILU, *, input: bool = True,
+                                  weights: bool = True, biases: bool = False, work: torch.Tensor | None = None,
+                                  dev_status: torch.Tensor | None = None, stream=None) -> dict[str, torch.Tensor | None]:
+    """The gradients of convrot_gated_linear's inputs, from its kept gate and up and the gradient dy of y: a dict with dx,
+    dw_gate, dw_up (of x's type) and db_gate, db_up (float32), None for those that are not wanted (``input``,
+    ``weights``, ``biases``). Through frozen weights: ``weights=False``."""
+    got = load().gated_linear_backward(x, w_gate, w_up, gate, up, dy, act, input, weights, biases, work, dev_status, stream)
+    if not isinstance(got, dict):
+        raise ConvrotError(got, "convrot_gated_linear_backward")
+    return got
+
+
+# ---------------------------------------------------------------- attention to other states
+
+
+def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor | None = None, *,
+                      scale: float | None = None, out: torch.Tensor | None = None, work: torch.Tensor | None = None,
+                      dev_status: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(out, lse): out = softmax(scale q k^T) v for queries [batch, tokens, heads, head_dim] and keys and values [batch,
+    their own tokens, heads that divide the queries', head_dim], bfloat16 or float16, any batch, token and head strides;
+    lse [batch, heads, tokens] float32 is the logarithm of each row's sum, for the gradient.
+
+    mask [batch, keys' tokens] (bool or uint8) says which keys are there; a query without any has out 0 and lse -inf, and
+    what stands at a masked key does not count, whatever it is. scale: head_dim^-0.5 by default. Each query attends to all
+    keys that are there. ``work`` (uint8) is allocated here when not given."""
+    if q.dim() != 4:
+        raise TypeError("q must be [batch, tokens, heads, head_dim]")
+    if out is None:
+        out = _cr._empty(q.shape, q.dtype, q.device, stream)
+    lse = _cr._empty((q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device, stream)
+    _check(load().attention(q, k, v, mask, q.shape[-1]**-0.5 if scale is None else scale, out, lse, work, dev_status, stream),
+           "convrot_attention")
+    return out, lse
+
+
+def convrot_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                               dout: torch.Tensor, mask: torch.Tensor | None = None, *, scale: float | None = None,
+                               work: torch.Tensor | None = None, dev_status: torch.Tensor | None = None,
+                               stream=None) -> dict[str, torch.Tensor]:
+    """The gradients dq, dk and dv (a dict) of convrot_attention's inputs, from its results and the gradient dout of out;
+    mask and scale are the forward call's. dk and dv are those of the shared heads, and 0 at masked keys."""
+    got = load().attention_backward(q, k, v, out, lse, dout, mask, q.shape[-1]**-0.5 if scale is None else scale, work, dev_status, stream)
+    if not isinstance(got, dict):
+        raise ConvrotError(got, "convrot_attention_backward")
+    return got

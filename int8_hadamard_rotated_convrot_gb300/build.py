@@ -1,6 +1,6 @@
 """Builds libconvrot.so in-tree with nvcc for sm_103a.
 
-Each .cu file under csrc/ compiles to an object in parallel, then nvcc links
+Each .cu file under csrc/ and csrc16/ compiles to an object in parallel, then nvcc links
 them into ``_build/libconvrot.so`` next to this file, and the CPython module of
 csrc/block_py.cpp (g++, the installed torch's headers) is linked to it. Rebuilds only when a
 source or header is newer than the library.
@@ -17,6 +17,7 @@ import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
+CSRC16 = os.path.join(HERE, "csrc16")  # attention and the gated linear, on 16-bit tensors
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libconvrot.so")
@@ -37,11 +38,11 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(p for d in (CSRC, CSRC16) for p in glob.glob(os.path.join(d, "*.cu")))
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + [p for d in (CSRC, CSRC16) for e in ("*.h", "*.cuh") for p in glob.glob(os.path.join(d, e))]
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [BLOCK_SOURCE, os.path.abspath(__file__)])
 
 

@@ -52,6 +52,14 @@ EXPORTED = [
     "convrot_gated_norm_backward",
     "convrot_rotary",
     "convrot_rotary_table",
+    "convrot_gated_linear_work_bytes",
+    "convrot_gated_linear",
+    "convrot_gated_linear_backward_work_bytes",
+    "convrot_gated_linear_backward",
+    "convrot_attention_work_bytes",
+    "convrot_attention",
+    "convrot_attention_backward_work_bytes",
+    "convrot_attention_backward",
 ]
 
 
@@ -132,6 +140,10 @@ def load() -> ctypes.CDLL:
         for name in ("convrot_fp8_linear", "convrot_fp8_pack_linear", "convrot_gated_norm",
                      "convrot_gated_norm_backward", "convrot_rotary"):
             getattr(lib, name).argtypes = [vp, vp]  # (a struct of arguments, stream)
+        for name in ("convrot_gated_linear", "convrot_gated_linear_backward", "convrot_attention", "convrot_attention_backward"):
+            getattr(lib, name).argtypes = [vp, vp]
+            work_bytes = getattr(lib, name + "_work_bytes")
+            work_bytes.argtypes, work_bytes.restype = [vp], i64
         lib.convrot_rotary_table.argtypes = [vp, i64, i32, vp, vp, i32, ctypes.c_double, vp, vp, i64, vp]
         lib.convrot_status_string.argtypes = [ctypes.c_int]
         lib.convrot_status_string.restype = ctypes.c_char_p

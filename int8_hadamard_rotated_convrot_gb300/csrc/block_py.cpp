@@ -592,6 +592,263 @@ PyObject *rotary(PyObject *const *v, Py_ssize_t n)
     return status(convrot_rotary(&a, stream));
 }
 
+// A workspace where the caller gave none: of the call alone.
+template <typename A>
+void own_work(A &a, PyObject *given, Workspace &work, int64_t bytes, cudaStream_t stream)
+{
+    if (given != Py_None) return;
+    a.work_bytes = bytes;
+    a.work = work.get(bytes, stream);
+}
+
+// New tensors of a call, each with memory of its own: straight from the allocator (a trip through the dispatcher for each
+// costs as much as a launch), on the call's stream.
+class Fresh {
+public:
+    Fresh(cudaStream_t stream, const Tensor &like) : on_(stream, like), allocator_(c10::cuda::CUDACachingAllocator::get()) {}
+    Tensor operator()(at::IntArrayRef sizes, at::ScalarType type)
+    {
+        size_t bytes = c10::elementSize(type);
+        for (int64_t n : sizes) bytes *= static_cast<size_t>(n);
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes, allocator_->allocate(bytes), allocator_, true),
+            c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        on_.record(t);
+        return t;
+    }
+
+private:
+    OnStream on_;
+    c10::Allocator *allocator_;
+};
+
+// The dict of a call's gradients; None for those that are not defined.
+PyObject *dict_of(std::initializer_list<std::pair<const char *, Tensor *>> all)
+{
+    PyObject *dict = PyDict_New();
+    bool ok = dict != nullptr;
+    for (const auto &[name, t] : all) {
+        if (!ok) break;
+        PyObject *o = t->defined() ? THPVariable_Wrap(std::move(*t)) : Py_NewRef(Py_None);
+        ok = o && PyDict_SetItemString(dict, name, o) == 0;
+        Py_XDECREF(o);
+    }
+    if (!ok) Py_CLEAR(dict);
+    return dict;
+}
+
+// (x, w_gate, w_up, b_gate, b_up, act, out, gate, up, work, dev_status, stream)
+PyObject *gated_linear(PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 12));
+    const Tensor *x = tensor(v[0], "x"), *w = tensor(v[1], "w_gate");
+    REQUIRE(x && w && one_device(v, n, *x));
+    if (x->dim() != 2 || w->dim() != 2) {
+        raise(PyExc_TypeError, "x and w_gate", "must be 2-D tensors");
+        return nullptr;
+    }
+    convrot_gated_linear_args a{};
+    const at::ScalarType t = x->scalar_type();
+    a.m = x->size(0);
+    a.k = x->size(1);
+    a.n = w->size(0);
+    Matrix mx, mg, mu, my, kg, ku;
+    const void *bg, *bu;
+    cudaStream_t stream;
+    REQUIRE(dtype_of(*x, "x", a.dtype) && matrix(v[0], "x", t, a.m, a.k, mx) && matrix(v[1], "w_gate", t, a.n, a.k, mg));
+    REQUIRE(matrix(v[2], "w_up", t, a.n, a.k, mu) && vector(v[3], "b_gate", at::kFloat, a.n, &bg) && vector(v[4], "b_up", at::kFloat, a.n, &bu));
+    REQUIRE(integer(v[5], a.act) && matrix(v[6], "out", t, a.m, a.n, my) && optional_matrix(v[7], "gate", t, a.m, a.n, kg));
+    REQUIRE(optional_matrix(v[8], "up", t, a.m, a.n, ku) && workspace(v[9], &a.work, &a.work_bytes) && status_word(v[10], &a.dev_status));
+    REQUIRE(stream_of(v[11], *x, stream));
+    const DeviceOf device(*x);
+    a.x = mx.p;
+    a.ldx = mx.ld;
+    a.w_gate = mg.p;
+    a.ldw_gate = mg.ld;
+    a.w_up = mu.p;
+    a.ldw_up = mu.ld;
+    a.b_gate = static_cast<const float *>(bg);
+    a.b_up = static_cast<const float *>(bu);
+    a.y = my.p;
+    a.ldy = my.ld;
+    a.gate = kg.p;
+    a.ldgate = kg.ld;
+    a.up = ku.p;
+    a.ldup = ku.ld;
+    Workspace work;
+    own_work(a, v[9], work, convrot_gated_linear_work_bytes(&a), stream);
+    return status(convrot_gated_linear(&a, stream));
+}
+
+// (x, w_gate, w_up, gate, up, dy, act, dx wanted, weights' wanted, biases' wanted, work, dev_status, stream) -> status, or the
+// dict of gradients
+PyObject *gated_linear_backward(PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 13));
+    const Tensor *x = tensor(v[0], "x"), *w = tensor(v[1], "w_gate");
+    REQUIRE(x && w && one_device(v, n, *x));
+    if (x->dim() != 2 || w->dim() != 2) {
+        raise(PyExc_TypeError, "x and w_gate", "must be 2-D tensors");
+        return nullptr;
+    }
+    convrot_gated_linear_backward_args a{};
+    const at::ScalarType t = x->scalar_type();
+    a.m = x->size(0);
+    a.k = x->size(1);
+    a.n = w->size(0);
+    Matrix mx, mwg, mwu, mg, mu, my;
+    cudaStream_t stream;
+    REQUIRE(dtype_of(*x, "x", a.dtype) && matrix(v[0], "x", t, a.m, a.k, mx) && matrix(v[1], "w_gate", t, a.n, a.k, mwg));
+    REQUIRE(matrix(v[2], "w_up", t, a.n, a.k, mwu) && matrix(v[3], "gate", t, a.m, a.n, mg) && matrix(v[4], "up", t, a.m, a.n, mu));
+    REQUIRE(matrix(v[5], "dy", t, a.m, a.n, my) && integer(v[6], a.act) && workspace(v[10], &a.work, &a.work_bytes));
+    const int input = PyObject_IsTrue(v[7]), weights = PyObject_IsTrue(v[8]), biases = PyObject_IsTrue(v[9]);
+    REQUIRE(input >= 0 && weights >= 0 && biases >= 0 && status_word(v[11], &a.dev_status) && stream_of(v[12], *x, stream));
+    const DeviceOf device(*x);
+    Fresh fresh(stream, *x);
+    Tensor dx, dwg, dwu, dbg, dbu;
+    if (a.k < 1 || a.dtype == CONVROT_F32) return status(a.k < 1 ? CONVROT_ERR_INVALID_ARG : CONVROT_ERR_UNSUPPORTED);
+    if (input) a.dx = (dx = fresh({a.m, a.k}, t)).data_ptr();
+    if (weights) {
+        a.dw_gate = (dwg = fresh({a.n, a.k}, t)).data_ptr();
+        a.dw_up = (dwu = fresh({a.n, a.k}, t)).data_ptr();
+    }
+    if (biases) {
+        a.db_gate = static_cast<float *>((dbg = fresh({a.n}, at::kFloat)).data_ptr());
+        a.db_up = static_cast<float *>((dbu = fresh({a.n}, at::kFloat)).data_ptr());
+    }
+    a.x = mx.p;
+    a.ldx = mx.ld;
+    a.w_gate = mwg.p;
+    a.ldw_gate = mwg.ld;
+    a.w_up = mwu.p;
+    a.ldw_up = mwu.ld;
+    a.gate = mg.p;
+    a.ldgate = mg.ld;
+    a.up = mu.p;
+    a.ldup = mu.ld;
+    a.dy = my.p;
+    a.lddy = my.ld;
+    a.lddx = a.lddw_gate = a.lddw_up = a.k;
+    Workspace work;
+    own_work(a, v[10], work, convrot_gated_linear_backward_work_bytes(&a), stream);
+    const convrot_status st = convrot_gated_linear_backward(&a, stream);
+    if (st != CONVROT_OK) return status(st);
+    return dict_of({{"dx", &dx}, {"dw_gate", &dwg}, {"dw_up", &dwu}, {"db_gate", &dbg}, {"db_up", &dbu}});
+}
+
+// A tensor [batch, tokens, heads, head_dim] of `like`'s type, batch and head_dim.
+bool states(PyObject *o, const char *name, const Tensor &like, void **p, int64_t &tokens, int64_t &n, int64_t (&strides)[3])
+{
+    const Tensor *t = tensor(o, name);
+    if (!t) return false;
+    if (t->dim() != 4 || t->scalar_type() != like.scalar_type()) return raise(PyExc_TypeError, name, "must be 4-D and of q's type");
+    if (t->size(0) != like.size(0) || t->size(3) != like.size(3)) return raise(PyExc_ValueError, name, "must have q's batch and head_dim");
+    if (t->size(3) > 1 && t->stride(3) != 1) return raise(PyExc_ValueError, name, "must have a contiguous last dimension");
+    *p = t->data_ptr();
+    tokens = t->size(1);
+    n = t->size(2);
+    for (int i = 0; i < 3; ++i) strides[i] = t->stride(i);
+    return true;
+}
+
+// What both attention calls have in common: q, k, v, mask, scale.
+template <typename A>
+bool attention_inputs(A &a, PyObject *q, PyObject *k, PyObject *v, PyObject *mask, PyObject *scale, const Tensor &like)
+{
+    if (like.dim() != 4) return raise(PyExc_TypeError, "q", "must be [batch, tokens, heads, head_dim]");
+    if (like.size(3) > INT32_MAX) return raise(PyExc_ValueError, "q", "has too large a head_dim");
+    void *pq, *pk, *pv;
+    int64_t v_tokens, v_heads;
+    a.batch = like.size(0);
+    a.head_dim = static_cast<int32_t>(like.size(3));
+    if (!dtype_of(like, "q", a.dtype) || !states(q, "q", like, &pq, a.q_tokens, a.q_heads, a.q_strides) ||
+        !states(k, "k", like, &pk, a.kv_tokens, a.kv_heads, a.k_strides) || !states(v, "v", like, &pv, v_tokens, v_heads, a.v_strides))
+        return false;
+    if (v_tokens != a.kv_tokens || v_heads != a.kv_heads) return raise(PyExc_ValueError, "v", "must have k's tokens and heads");
+    a.q = pq;
+    a.k = pk;
+    a.v = pv;
+    if (mask != Py_None) {
+        const Tensor *t = tensor(mask, "mask");
+        if (!t) return false;
+        if (t->scalar_type() != at::kBool && t->scalar_type() != at::kByte) return raise(PyExc_TypeError, "mask", "must be bool or uint8");
+        if (t->dim() != 2 || t->size(0) != a.batch || t->size(1) != a.kv_tokens) return raise(PyExc_ValueError, "mask", "must be [batch, k's tokens]");
+        if (a.kv_tokens > 1 && t->stride(1) != 1) return raise(PyExc_ValueError, "mask", "must be contiguous along the tokens");
+        a.mask = static_cast<const uint8_t *>(t->data_ptr());
+        a.mask_stride = t->stride(0);
+    }
+    return real(scale, a.scale);
+}
+
+// (q, k, v, mask, scale, out, lse, work, dev_status, stream)
+PyObject *attention(PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 10));
+    const Tensor *q = tensor(v[0], "q"), *lse = tensor(v[6], "lse");
+    REQUIRE(q && lse && one_device(v, n, *q));
+    convrot_attention_args a{};
+    void *out;
+    int64_t tokens, heads;
+    cudaStream_t stream;
+    REQUIRE(attention_inputs(a, v[0], v[1], v[2], v[3], v[4], *q) && states(v[5], "out", *q, &out, tokens, heads, a.out_strides));
+    if (tokens != a.q_tokens || heads != a.q_heads) {
+        raise(PyExc_ValueError, "out", "must have q's shape");
+        return nullptr;
+    }
+    if (lse->scalar_type() != at::kFloat || !lse->is_contiguous() || lse->sizes() != at::IntArrayRef({a.batch, a.q_heads, a.q_tokens})) {
+        raise(PyExc_ValueError, "lse", "must be a contiguous float32 tensor [batch, heads, tokens]");
+        return nullptr;
+    }
+    REQUIRE(workspace(v[7], &a.work, &a.work_bytes) && status_word(v[8], &a.dev_status) && stream_of(v[9], *q, stream));
+    const DeviceOf device(*q);
+    a.out = out;
+    a.lse = static_cast<float *>(lse->data_ptr());
+    Workspace work;
+    own_work(a, v[7], work, convrot_attention_work_bytes(&a), stream);
+    return status(convrot_attention(&a, stream));
+}
+
+// (q, k, v, out, lse, dout, mask, scale, work, dev_status, stream) -> status, or the dict of gradients
+PyObject *attention_backward(PyObject *const *v, Py_ssize_t n)
+{
+    REQUIRE(count(n, 11));
+    const Tensor *q = tensor(v[0], "q"), *lse = tensor(v[4], "lse");
+    REQUIRE(q && lse && one_device(v, n, *q));
+    convrot_attention_backward_args a{};
+    void *out, *dout;
+    int64_t tokens[2], heads[2];
+    cudaStream_t stream;
+    REQUIRE(attention_inputs(a, v[0], v[1], v[2], v[6], v[7], *q) && states(v[3], "out", *q, &out, tokens[0], heads[0], a.out_strides));
+    REQUIRE(states(v[5], "dout", *q, &dout, tokens[1], heads[1], a.dout_strides));
+    for (int i = 0; i < 2; ++i)
+        if (tokens[i] != a.q_tokens || heads[i] != a.q_heads) {
+            raise(PyExc_ValueError, "out and dout", "must have q's shape");
+            return nullptr;
+        }
+    if (lse->scalar_type() != at::kFloat || !lse->is_contiguous() || lse->sizes() != at::IntArrayRef({a.batch, a.q_heads, a.q_tokens})) {
+        raise(PyExc_ValueError, "lse", "must be a contiguous float32 tensor [batch, heads, tokens]");
+        return nullptr;
+    }
+    REQUIRE(workspace(v[8], &a.work, &a.work_bytes) && status_word(v[9], &a.dev_status) && stream_of(v[10], *q, stream));
+    const DeviceOf device(*q);
+    a.out = out;
+    a.dout = dout;
+    a.lse = static_cast<const float *>(lse->data_ptr());
+    Fresh fresh(stream, *q);
+    const at::ScalarType t = q->scalar_type();
+    Tensor dq = fresh({a.batch, a.q_tokens, a.q_heads, a.head_dim}, t), dk = fresh({a.batch, a.kv_tokens, a.kv_heads, a.head_dim}, t);
+    Tensor dv = fresh({a.batch, a.kv_tokens, a.kv_heads, a.head_dim}, t);
+    a.dq = dq.data_ptr();
+    a.dk = dk.data_ptr();
+    a.dv = dv.data_ptr();
+    Workspace work;
+    own_work(a, v[8], work, convrot_attention_backward_work_bytes(&a), stream);
+    const convrot_status st = convrot_attention_backward(&a, stream);
+    if (st != CONVROT_OK) return status(st);
+    return dict_of({{"dq", &dq}, {"dk", &dk}, {"dv", &dv}});
+}
+
 // A call as Python makes it. torch's C++ side throws (out of memory, or a tensor without memory of its own, as under
 // torch.vmap): what it throws becomes the Python exception that torch itself would raise, and does not leave here.
 template <PyObject *(*kCall)(PyObject *const *, Py_ssize_t)>
@@ -607,6 +864,7 @@ PyObject *entry(PyObject *, PyObject *const *v, Py_ssize_t n)
 
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(entry<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(linear), METHOD(pack_activations), METHOD(gated_norm), METHOD(gated_norm_backward), METHOD(rotary),
+                         METHOD(gated_linear), METHOD(gated_linear_backward), METHOD(attention), METHOD(attention_backward),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,86 @@
+// Launch interface between the C-ABI layer (api_attention.cu) and the kernels
+// of attention to other states (include/convrot_block.h).
+#pragma once
+
+#include "../csrc/block.h"
+
+namespace convrot {
+
+// A tensor [batch, tokens, heads, d] of 16-bit elements whose heads start on 16
+// bytes, as the kernels' copies read it. Strides in elements: batch, token, head.
+struct States {
+    const void *p;
+    int64_t tokens, heads;
+    int64_t strides[3];
+};
+
+constexpr int kTileKeys = 128;
+
+// Rows of a gathered sample: whole tiles.
+inline int64_t gathered_rows(int64_t tokens) { return (tokens + kTileKeys - 1) / kTileKeys * kTileKeys; }
+
+// Copies the heads of `count` tensors (1, or keys and values) to [batch, rows, heads, dp], dp = d rounded up to 8. Without a
+// mask, rows = tokens. With one, rows = gathered_rows(tokens): the tokens that are there come first, in order, zeros follow
+// to the end of the last tile that has one; counts[b] is their number and index[b * rows + i] the token of row i; and
+// rows of zero[i] (dense [batch, tokens, heads, d]) at tokens that are not there become zero.
+struct GatherArgs {
+    const void *src[2];
+    int64_t strides[2][3];
+    void *dst[2];
+    void *zero[2];
+    int32_t count;
+    const uint8_t *mask;
+    int64_t mask_stride;
+    int32_t *counts, *index;
+    int64_t batch, tokens, heads, rows;
+    int32_t d, dp;
+};
+cudaError_t launch_gather(const GatherArgs &a, cudaStream_t stream);
+
+struct AttentionArgs {
+    States q, k, v;
+    const int32_t *counts;  // keys of each sample, or null: k.tokens
+    void *out;
+    int64_t out_strides[3];
+    float *lse;
+    int32_t *dev_status;
+    int64_t batch;
+    int64_t kv_tokens;      // at most
+    float scale;
+    int32_t d, dtype;
+};
+cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t stream);
+
+// Rows of each head's statistics in the backward pass: whole tiles of queries.
+constexpr int kTileQueries = 128;
+inline int64_t stat_rows(int64_t tokens) { return (tokens + kTileQueries - 1) / kTileQueries * kTileQueries; }
+// Tokens of one block of the statistics.
+constexpr int kStatTokens = 64;
+
+struct AttentionGradArgs {
+    States q, k, v, dout;     // as the kernels read them
+    const int32_t *counts, *index;
+    int64_t index_rows;       // of a sample in index
+    const void *out, *dout_own;
+    int64_t out_strides[3], dout_own_strides[3];  // the caller's out and dout, for the statistics
+    const float *lse;
+    float *base2, *delta;     // [batch, q_heads, stat_rows]: -lse in base 2, and -dout . out
+    float *amax;              // float16: [batch, kv_heads, blocks] largest |dout|; else null
+    float *partial;           // grad_kv_partial_bytes
+    void *dq, *dk, *dv;
+    int32_t *dev_status;
+    int64_t batch, kv_tokens;
+    float scale;
+    int32_t d, dtype;
+};
+int64_t grad_kv_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads, int d);
+cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stream);
+cudaError_t launch_attention_grad_q(const AttentionGradArgs &a, cudaStream_t stream);
+cudaError_t launch_attention_grad_kv(const AttentionGradArgs &a, cudaStream_t stream);
+
+// Shared memory and tensor-memory columns of every launch form, for the check that no mix of blocks waits for columns.
+int attention_shared(int form, int *columns);  // 0 past the last form
+int attention_grad_q_shared(int form, int *columns);
+int attention_grad_kv_shared(int form, int *columns);
+
+}  // namespace convrot

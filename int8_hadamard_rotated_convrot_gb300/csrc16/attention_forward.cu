@@ -1,0 +1,413 @@
+// Attention to other states on the 5th-generation tensor cores
+// (include/convrot_block.h): one pass over the keys with the running maximum and
+// sum of each row's softmax.
+//
+// A CTA takes 256 queries of a head, two groups of 128 that take turns: while
+// the tensor cores multiply for one, the other's softmax runs. It is persistent
+// over such items.
+//   warp 0       TMA producer: the groups' queries, then the tiles of 128 keys
+//                and values in turn, through one ring
+//   warp 1       tensor memory; one thread issues the MMAs
+//   warps 4-7    the first group's softmax, a row a thread; warps 8-11 the second's
+// Tensor memory: for each group 128 columns of S = Q K^T, whose first half then
+// holds P (16 bits, the A operand of P V, so that P never passes through shared
+// memory), and the sums O.
+//
+// The maximum is a reference only: O and the sum are rescaled when a row's
+// maximum has grown by more than 2^8 since, which is rare after the first tile
+// (probabilities may be up to 2^8 meanwhile, the sums are fp32). float16 has few
+// exponents below 1, so there P is 2^7 times as large, which the division by the
+// sum takes back.
+#include "attention.cuh"
+
+namespace convrot {
+namespace {
+
+using namespace mma16;
+
+constexpr int kGroupRows = 128, kItemRows = 2 * kGroupRows;
+constexpr int kThreads = 384;
+// Registers a thread: launched at 168, warpgroup 0 leaves most of its own to the softmax:
+// 4 x 32 x 80 + 8 x 32 x 208 <= 384 x 168.
+constexpr int kRegsWg0 = 80, kRegsSoftmax = 208;
+static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsSoftmax <= kThreads * 168, "register split");
+constexpr float kGrow = 8.0f;  // log2 of what a row's probabilities may grow to before O is rescaled
+
+template <int kD>
+struct Cfg {
+    static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
+    static constexpr int STAGES = kD == 64 ? 8 : 4;
+    static constexpr int BARS = 2 * STAGES + 2 * 5 + 1;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + 8 * kStageBytes + BAR_BYTES;
+    static constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 g and + kD g
+    static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
+    static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
+};
+
+struct Params {
+    HeadsMap q, k, v;
+    const int32_t *counts;
+    void *out;
+    int64_t out_strides[3];
+    float *lse;
+    int32_t *dev_status;
+    int32_t q_tokens, kv_tokens, q_heads, group;  // query heads that share a head
+    int32_t q_tiles, items;
+    int32_t d, wide;
+    float scale_log2;
+};
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<kD>;
+    constexpr float kShift = std::is_same_v<T, __half> ? 7.0f : 0.0f;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+    const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
+    uint8_t *gbase = smem_raw + (base - raw);
+    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + 8 * kStageBytes;
+    const uint32_t bars = base + kBars;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
+    auto q_full = [&](int g) { return bars + 8u * (2 * C::STAGES + g); };
+    auto q_empty = [&](int g) { return bars + 8u * (2 * C::STAGES + 2 + g); };
+    auto s_full = [&](int g) { return bars + 8u * (2 * C::STAGES + 4 + g); };   // S is there (and P V of the tile before)
+    auto p_ready = [&](int g) { return bars + 8u * (2 * C::STAGES + 6 + g); };  // P is there, and O rescaled
+    auto o_full = [&](int g) { return bars + 8u * (2 * C::STAGES + 8 + g); };
+    const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 10);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
+    const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(q_full(g), 1);
+            mbar_init(q_empty(g), 1);
+            mbar_init(s_full(g), 1);
+            mbar_init(p_ready(g), 4);
+            mbar_init(o_full(g), 1);
+        }
+        mbar_init(done_bar, 1);
+        *wait.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.q.map);
+        if (p.kv_tokens > 0) prefetch_map(&p.k.map);
+        if (p.kv_tokens > 0) prefetch_map(&p.v.map);
+    }
+    if (warp == 1) tmem_alloc<1>(tmem_slot, 512u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    after_previous();
+    let_next_start();
+
+    // item -> (sample, head, first query); the tiles of one head follow each other and share its keys in L2
+    struct Item {
+        int b, h, q0, keys, tiles, groups;
+    };
+    auto item_at = [&](int i) {
+        Item it;
+        const int bh = i / p.q_tiles;
+        it.q0 = (i - bh * p.q_tiles) * kItemRows;
+        it.b = bh / p.q_heads;
+        it.h = bh - it.b * p.q_heads;
+        it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
+        it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
+        it.groups = p.q_tokens - it.q0 > kGroupRows ? 2 : 1;
+        return it;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
+        if (warp == 0 && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, q_phase[2] = {0, 0};
+            uint32_t armed = 0;  // stages and groups whose copies may be in flight
+            bool ok = true;
+            auto load = [&](const HeadsMap &m, int tile, const Item &it) {
+                if (!ok || !wait(empty_bar(stage), phase ^ 1u)) return void(ok = false);
+                mbar_arrive_expect_tx(full_bar(stage), C::TILE);
+                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, tile * kTileKeys, it.h / p.group, it.b, full_bar(stage));
+                armed |= 1u << stage;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const Item it = item_at(i);
+                if (it.tiles == 0) continue;
+                for (int g = 0; g < it.groups && ok; ++g) {
+                    if (!wait(q_empty(g), q_phase[g] ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    q_phase[g] ^= 1u;
+                    mbar_arrive_expect_tx(q_full(g), C::TILE);
+                    load_tile<C::HALVES>(base + g * C::TILE, p.q, it.q0 + g * kGroupRows, it.h, it.b, q_full(g));
+                    armed |= 1u << (16 + g);
+                    if (g == 0) load(p.k, 0, it);
+                }
+                for (int j = 0; j < it.tiles && ok; ++j) {
+                    load(p.v, j, it);
+                    if (j + 1 < it.tiles) load(p.k, j + 1, it);
+                }
+            }
+            if (!ok) {
+                wait.fail();
+                // copies in flight land before shared memory goes away: a stage's last phase, then the groups'
+                for (int s = 0; s < C::STAGES; ++s)
+                    if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
+                for (int g = 0; g < 2; ++g)
+                    if (armed >> (16 + g) & 1u) mbar_wait(q_full(g), q_phase[g] ^ 1u);
+            }
+        } else if (warp == 1 && lane == 0) {
+            const uint32_t kIdS = idesc<T>(128, 128, false, false);
+            const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
+            const uint32_t id_o = idesc<T>(128, n_o, false, true);
+            int stage = 0;
+            uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto next = [&]() {
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
+            auto scores = [&](int g, int at) {  // S = Q K^T
+                const uint64_t a = desc_k(base + g * C::TILE), b = desc_k(base + kRing + at * C::TILE);
+                const uint32_t s = tmem + C::S_COL + 128 * g;
+                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(s, tile_step_k(a, kk), tile_step_k(b, kk), kIdS, kk > 0 ? 1u : 0u);
+                mma_commit(s_full(g));
+            };
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const Item it = item_at(i);
+                if (it.tiles == 0) continue;
+                if (!wait(full_bar(stage), phase)) {
+                    ok = false;
+                    break;
+                }
+                for (int g = 0; g < it.groups; ++g) {
+                    if (!wait(q_full(g), q_phase[g])) {
+                        ok = false;
+                        break;
+                    }
+                    q_phase[g] ^= 1u;
+                    tc_fence_after();
+                    scores(g, stage);
+                    if (it.tiles == 1) mma_commit(q_empty(g));
+                }
+                if (!ok) break;
+                mma_commit(empty_bar(stage));
+                next();
+                for (int j = 0; j < it.tiles; ++j) {
+                    const int v_stage = stage;
+                    const bool last = j + 1 == it.tiles;
+                    if (!wait(full_bar(stage), phase)) {
+                        ok = false;
+                        break;
+                    }
+                    next();
+                    if (!last && !wait(full_bar(stage), phase)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int g = 0; g < it.groups; ++g) {
+                        if (!wait(p_ready(g), p_phase[g])) {
+                            ok = false;
+                            break;
+                        }
+                        p_phase[g] ^= 1u;
+                        tc_fence_after();
+                        const uint64_t b = desc_mn(base + kRing + v_stage * C::TILE, kTileBox);
+                        const uint32_t o = tmem + C::O_COL + kD * g, a = tmem + C::S_COL + 128 * g;
+#pragma unroll
+                        for (int kk = 0; kk < kTileKeys / kMmaK; ++kk)
+                            mma_ts(o, a + kk * (kMmaK / 2), b + kStepMN * kk, id_o, j > 0 || kk > 0 ? 1u : 0u);
+                        if (last) {
+                            mma_commit(o_full(g));
+                        } else {
+                            scores(g, stage);
+                            if (j + 2 == it.tiles) mma_commit(q_empty(g));
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(empty_bar(v_stage));
+                    if (!last) {
+                        mma_commit(empty_bar(stage));
+                        next();
+                    }
+                }
+            }
+            if (!ok) wait.fail();
+            mma_commit(done_bar);
+            mbar_wait(done_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        const int g = (warp - 4) >> 2, quad = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t s_at = lanes + C::S_COL + 128 * g, o_at = lanes + C::O_COL + kD * g;
+        const uint32_t stage = base + kOut + (warp - 4) * kStageBytes;
+        const float c = p.scale_log2;
+        uint32_t s_phase = 0, o_phase = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            const Item it = item_at(i);
+            if (g >= it.groups) continue;
+            float top = neg_inf(), sum = 0.0f;  // the reference, and the sum of 2^(c (s - top) + kShift)
+            for (int j = 0; j < it.tiles; ++j) {
+                if (!wait(s_full(g), s_phase)) {
+                    ok = false;
+                    break;
+                }
+                s_phase ^= 1u;
+                tc_fence_after();
+                uint32_t r[kTileKeys];
+#pragma unroll
+                for (int k = 0; k < kTileKeys; k += 32) tmem_ld32_async(s_at + k, r + k);
+                tmem_ld_wait(r);
+                const int keys = it.keys - j * kTileKeys;
+                if (keys < kTileKeys) {
+#pragma unroll
+                    for (int k = 0; k < kTileKeys; ++k)
+                        if (k >= keys) r[k] = 0xff800000u;
+                }
+                float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+                for (int k = 0; k < kTileKeys; ++k) m[k % 4] = fmaxf(m[k % 4], __uint_as_float(r[k]));
+                const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                if (j == 0) {
+                    top = now;
+                } else if (__any_sync(0xffffffffu, (now - top) * c > kGrow)) {
+                    // P V of the tile before is complete: the same commit told of it
+                    const float next = fmaxf(top, now), factor = next == neg_inf() ? 1.0f : ex2((top - next) * c);
+                    top = next;
+                    sum *= factor;
+#pragma unroll 1
+                    for (int k = 0; k < p.d; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_async(o_at + k, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                        tmem_st16(o_at + k, o);
+                    }
+                }
+                // (a row of infinite scores below: no term at all)
+                const float off = top == neg_inf() ? 0.0f : kShift - top * c;
+                const F2 c2(c), off2(off);
+                F2 add[2] = {F2(0.0f), F2(0.0f)};
+                uint32_t pk[kTileKeys / 2];
+#pragma unroll
+                for (int k = 0; k < kTileKeys; k += 2) {
+                    const F2 x = fma2(F2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, off2);
+                    const F2 e(ex2(x.lo()), ex2(x.hi()));
+                    add[k / 2 % 2] = add[k / 2 % 2] + e;
+                    pk[k / 2] = pack2<T>(e.lo(), e.hi());
+                }
+                sum += add[0].sum() + add[1].sum();
+                tmem_st32(s_at, pk);
+                tmem_st32(s_at + 32, pk + 32);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready(g));
+            }
+            if (!ok) break;
+            const int row0 = it.q0 + g * kGroupRows + quad * 32, rows = p.q_tokens - row0 < 32 ? p.q_tokens - row0 : 32;
+            const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
+            if (lane < rows)
+                p.lse[(static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane] =
+                    sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
+            T *out = static_cast<T *>(p.out) + it.b * p.out_strides[0] + row0 * p.out_strides[1] + it.h * p.out_strides[2];
+            if (it.tiles > 0) {
+                if (!wait(o_full(g), o_phase)) {
+                    ok = false;
+                    break;
+                }
+                o_phase ^= 1u;
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int k = 0; k < p.d; k += 32) {
+                uint32_t o[32];
+                float v[32];
+                if (it.tiles > 0) {
+                    tmem_ld32_async(o_at + k, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = sum == 0.0f ? 0.0f : __uint_as_float(o[e]) * inv;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+                }
+                if (rows > 0) store_rows<T>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+            }
+            tc_fence_before();  // O is read before the next item's first P is announced
+        }
+        if (!ok) wait.fail();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free<1>(tmem, 512u);
+}
+
+template <typename T, int kD>
+struct attention_tag;
+
+template <typename T, int kD>
+cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
+{
+    using C = Cfg<kD>;
+    Params p{};
+    if (!heads_map<T>(&p.q, a.q, a.batch, a.d, kGroupRows)) return cudaErrorInvalidValue;
+    if (a.k.tokens > 0 && (!heads_map<T>(&p.k, a.k, a.batch, a.d, kTileKeys) || !heads_map<T>(&p.v, a.v, a.batch, a.d, kTileKeys)))
+        return cudaErrorInvalidValue;
+    p.counts = a.counts;
+    p.out = a.out;
+    for (int i = 0; i < 3; ++i) p.out_strides[i] = a.out_strides[i];
+    p.lse = a.lse;
+    p.dev_status = a.dev_status;
+    p.q_tokens = static_cast<int32_t>(a.q.tokens);
+    p.kv_tokens = static_cast<int32_t>(a.kv_tokens);
+    p.q_heads = static_cast<int32_t>(a.q.heads);
+    p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
+    p.q_tiles = static_cast<int32_t>((a.q.tokens + kItemRows - 1) / kItemRows);
+    const int64_t items = a.batch * a.q.heads * p.q_tiles;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    p.items = static_cast<int32_t>(items);
+    p.d = a.d;
+    p.wide = heads_wide(a.out, a.out_strides, a.batch, a.q.tokens, a.q.heads);
+    p.scale_log2 = a.scale * kLog2e;
+    auto kernel = attention_kernel<T, kD>;
+    cudaError_t e = allow_shared<attention_tag<T, kD>>(kernel);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t stream)
+{
+    if (a.dtype == CONVROT_BF16) return a.d <= 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
+    return a.d <= 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+}
+
+int attention_shared(int form, int *columns)
+{
+    *columns = 512;
+    return form == 0 ? Cfg<64>::SMEM : form == 1 ? Cfg<128>::SMEM : 0;
+}
+
+}  // namespace convrot

@@ -1,0 +1,483 @@
+// The keys' and values' gradients of attention (include/convrot_block.h), on
+// the 5th-generation tensor cores:
+//
+//   dv_j = sum_i P_ij dout_i,  dk_j = scale sum_i dS_ij q_i
+//   P = 2^(c s + base2),  dS = P (dP + delta),  dP = dout V^T
+//
+// A unit is 128 keys of one head: all queries of the heads that share it pass
+// by, 128 at a time, and dV and dK stay in tensor memory. Everything is made
+// transposed, a key a lane, so that P^T and dS^T are A operands straight from
+// tensor memory and dout and q are read MN-major from the bytes that S^T = K Q^T
+// and dP^T = V dout^T read K-major.
+//   warp 0       TMA producer: the unit's keys and values, then queries, dout
+//                and their statistics, a ring of two or four tiles
+//   warp 1       tensor memory; one thread issues the MMAs: while P^T is made
+//                from S^T the tensor cores do the tile before's dK and the next
+//                dP^T, and while dS^T is made, dV and the next S^T
+//   warps 4-11   P^T and dS^T: a key a thread, half of the tile's queries each
+//
+// The work of all units, laid end to end, is cut into equal runs of tiles, one a
+// CTA, whatever the number of units: a unit that a cut goes through is left as
+// partial sums in fp32 and added up by a second kernel in the order of the
+// cuts, which depends on the sizes alone.
+#include "attention.cuh"
+
+namespace convrot {
+namespace {
+
+using namespace mma16;
+
+constexpr int kThreads = 384;
+constexpr int kRegsWg0 = 80, kRegsMath = 208;
+static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsMath <= kThreads * 168, "register split");
+
+template <int kD>
+struct Cfg {
+    static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
+    static constexpr int STAGES = kD == 64 ? 4 : 2;
+    static constexpr int STATS = 2 * kTileQueries * 4;  // base2 and delta of a tile
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int BARS = 2 * STAGES + 8;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * (STAGE + STATS) + 8 * kStageBytes + BAR_BYTES;
+    static constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 384;
+    static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
+    static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
+};
+
+// How the tiles of all units are cut.
+struct Cut {
+    int64_t units, per_unit, work;
+    int32_t runs;
+    __host__ __device__ int64_t start(int64_t run) const { return run * work / runs; }
+    // the run that a tile is in
+    __host__ __device__ int64_t run_of(int64_t tile) const { return ((tile + 1) * runs - 1) / work; }
+};
+
+struct Params {
+    HeadsMap q, dout, k, v;
+    const int32_t *counts, *index;
+    int64_t index_rows;
+    const float *base2, *delta, *amax;
+    int64_t amax_blocks, stat_rows;
+    float *partial;  // [runs][2][2][128][kD]: a run's first and last unit where they are cut, dV and dK
+    void *dk, *dv;
+    int32_t *dev_status;
+    Cut cut;
+    int32_t kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
+    int32_t d, wide;
+    float scale, scale_log2;
+};
+
+// One unit: sample, head, tile of keys.
+struct Unit {
+    int b, h, tile, keys;  // keys of the sample
+    int64_t row;           // of the first key in dk and dv, or in the index
+};
+
+template <typename P>
+__device__ __forceinline__ Unit unit_at(const P &p, int64_t u)
+{
+    Unit r;
+    const int64_t bh = u / p.key_tiles;
+    r.tile = static_cast<int>(u - bh * p.key_tiles);
+    r.b = static_cast<int>(bh / p.kv_heads);
+    r.h = static_cast<int>(bh - static_cast<int64_t>(r.b) * p.kv_heads);
+    r.keys = p.counts ? static_cast<int>(load_i32(p.counts + r.b)) : p.kv_tokens;
+    return r;
+}
+
+// 32 rows (keys) x 32 values of one of the two gradients, to the caller's tensor.
+template <typename T>
+__device__ __forceinline__ void store_keys(const Params &p, const Unit &u, void *to, int key0, int col, uint32_t stage, int lane, const float (&v)[32])
+{
+    const int rows = u.keys - key0 < 32 ? u.keys - key0 : 32, cols = p.d - col < 32 ? p.d - col : 32;
+    if (rows <= 0) return;
+    const int64_t ld = static_cast<int64_t>(p.kv_heads) * p.d;
+    T *at = static_cast<T *>(to) + (static_cast<int64_t>(u.b) * p.kv_tokens * p.kv_heads + u.h) * p.d + col;
+    if (p.index)
+        store_rows<T>(at, ld, rows, cols, p.wide, stage, lane, v, p.index + u.b * p.index_rows + key0);
+    else
+        store_rows<T>(at + key0 * ld, ld, rows, cols, p.wide, stage, lane, v);
+}
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<kD>;
+    constexpr bool kHalf = std::is_same_v<T, __half>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+    const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
+    uint8_t *gbase = smem_raw + (base - raw);
+    constexpr int kRing = 2 * C::TILE, kStats = kRing + C::STAGES * C::STAGE, kOut = kStats + C::STAGES * C::STATS, kBars = kOut + 8 * kStageBytes;
+    const uint32_t bars = base + kBars;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
+    const uint32_t kv_full = bars + 8u * (2 * C::STAGES), kv_empty = kv_full + 8, s_full = kv_full + 16, dp_full = kv_full + 24;
+    const uint32_t p_ready = kv_full + 32, ds_ready = kv_full + 40;
+    const uint32_t sums_full = kv_full + 48, done_bar = kv_full + 56;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
+    const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1 + 8);  // the MMAs are done, and each math warp has read the statistics
+        }
+        mbar_init(kv_full, 1);
+        mbar_init(kv_empty, 1);
+        mbar_init(s_full, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(p_ready, 8);
+        mbar_init(ds_ready, 8);
+        mbar_init(sums_full, 1);
+        mbar_init(done_bar, 1);
+        *wait.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.q.map);
+        prefetch_map(&p.dout.map);
+        prefetch_map(&p.k.map);
+        prefetch_map(&p.v.map);
+    }
+    if (warp == 1) tmem_alloc<1>(tmem_slot, 512u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    after_previous();
+    let_next_start();
+
+    const int64_t first = p.cut.start(blockIdx.x), last = p.cut.start(blockIdx.x + 1);
+    // calls f(unit, its number, first and last tile of it here) for the units of this run that have keys
+    auto each_unit = [&](auto f) {
+        for (int64_t w = first; w < last;) {
+            const int64_t n = w / p.cut.per_unit, begin = n * p.cut.per_unit, end = begin + p.cut.per_unit;
+            const int64_t to = end < last ? end : last;
+            const Unit u = unit_at(p, n);
+            if (u.tile * kTileKeys < u.keys)
+                if (!f(u, static_cast<int>(w - begin), static_cast<int>(to - begin))) return false;
+            w = to;
+        }
+        return true;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
+        if (warp == 0 && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, kv_phase = 0, armed = 0;
+            const bool ok = each_unit([&](const Unit &u, int t0, int t1) {
+                if (!wait(kv_empty, kv_phase ^ 1u)) return false;
+                kv_phase ^= 1u;
+                mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+                load_tile<C::HALVES>(base, p.k, u.tile * kTileKeys, u.h, u.b, kv_full);
+                load_tile<C::HALVES>(base + C::TILE, p.v, u.tile * kTileKeys, u.h, u.b, kv_full);
+                armed |= 1u << 16;
+                for (int t = t0; t < t1; ++t) {
+                    if (!wait(empty_bar(stage), phase ^ 1u)) return false;
+                    const int h = u.h * p.group + t / p.q_tiles, q0 = t % p.q_tiles * kTileQueries;
+                    const uint32_t at = base + kRing + stage * C::STAGE, stats = base + kStats + stage * C::STATS;
+                    const int64_t row = (static_cast<int64_t>(u.b) * p.q_heads + h) * p.stat_rows + q0;
+                    mbar_arrive_expect_tx(full_bar(stage), C::STAGE + C::STATS);
+                    load_tile<C::HALVES>(at, p.q, q0, h, u.b, full_bar(stage));
+                    load_tile<C::HALVES>(at + C::TILE, p.dout, q0, h, u.b, full_bar(stage));
+                    bulk_load(stats, p.base2 + row, kTileQueries * 4, full_bar(stage));
+                    bulk_load(stats + kTileQueries * 4, p.delta + row, kTileQueries * 4, full_bar(stage));
+                    armed |= 1u << stage;
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                return true;
+            });
+            if (!ok) {
+                wait.fail();
+                for (int s = 0; s < C::STAGES; ++s)  // copies in flight land before shared memory goes away
+                    if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
+                if (armed >> 16) mbar_wait(kv_full, kv_phase ^ 1u);
+            }
+        } else if (warp == 1 && lane == 0) {
+            const uint32_t id_s = idesc<T>(128, 128, false, false);
+            const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
+            const uint32_t id_o = idesc<T>(128, n_o, false, true);
+            int stage = 0;
+            uint32_t phase = 0, kv_phase = 0, p_phase = 0, ds_phase = 0;
+            auto product = [&](uint32_t to, uint32_t rows, uint32_t cols) {
+                const uint64_t a = desc_k(rows), b = desc_k(cols);
+                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(to, tile_step_k(a, kk), tile_step_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+            };
+            // sums += (what a region's halves hold in 16 bits) x a tile, over the queries
+            auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) {
+                const uint64_t b = desc_mn(tile, kTileBox);
+#pragma unroll
+                for (int kk = 0; kk < kTileQueries / kMmaK; ++kk)
+                    mma_ts(sums, region + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b + kStepMN * kk, id_o, !fresh || kk > 0 ? 1u : 0u);
+            };
+            const bool ok = each_unit([&](const Unit &, int t0, int t1) {
+                if (!wait(kv_full, kv_phase) || !wait(full_bar(stage), phase)) return false;
+                kv_phase ^= 1u;
+                tc_fence_after();
+                uint32_t at = base + kRing + stage * C::STAGE;
+                product(tmem + C::S_COL, base, at);
+                mma_commit(s_full);
+                product(tmem + C::DP_COL, base + C::TILE, at + C::TILE);
+                mma_commit(dp_full);
+                for (int t = t0; t < t1; ++t) {
+                    const bool more = t + 1 < t1;
+                    const int here = stage;
+                    if (++stage == C::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    const uint32_t next = base + kRing + stage * C::STAGE;
+                    if (!wait(p_ready, p_phase)) return false;
+                    p_phase ^= 1u;
+                    tc_fence_after();
+                    add(tmem + C::DV_COL, tmem + C::S_COL, at + C::TILE, t == t0);
+                    if (more) {
+                        if (!wait(full_bar(stage), phase)) return false;
+                        tc_fence_after();
+                        product(tmem + C::S_COL, base, next);
+                        mma_commit(s_full);
+                    }
+                    if (!wait(ds_ready, ds_phase)) return false;
+                    ds_phase ^= 1u;
+                    tc_fence_after();
+                    add(tmem + C::DK_COL, tmem + C::DP_COL, at, t == t0);
+                    mma_commit(empty_bar(here));
+                    if (more) {
+                        product(tmem + C::DP_COL, base + C::TILE, next + C::TILE);
+                        mma_commit(dp_full);
+                    } else {
+                        mma_commit(kv_empty);
+                        mma_commit(sums_full);
+                    }
+                    at = next;
+                }
+                return true;
+            });
+            if (!ok) wait.fail();
+            mma_commit(done_bar);
+            mbar_wait(done_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMath));
+        const int half = (warp - 4) >> 2, quad = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t staging = base + kOut + (warp - 4) * kStageBytes;
+        const F2 c2(p.scale_log2);
+        int stage = 0;
+        uint32_t phase = 0, s_phase = 0, dp_phase = 0, sums_phase = 0;
+        const bool ok = each_unit([&](const Unit &u, int t0, int t1) {
+            int exponent = 0;
+            if constexpr (kHalf)
+                exponent = grad_exponent(p.amax + (static_cast<int64_t>(u.b) * p.kv_heads + u.h) * p.amax_blocks, p.amax_blocks, lane);
+            const F2 up(kHalf ? exp2i(exponent) * exp2i(-15) : 1.0f);
+            for (int t = t0; t < t1; ++t) {
+                if (!wait(full_bar(stage), phase) || !wait(s_full, s_phase)) return false;  // the statistics, and S^T
+                s_phase ^= 1u;
+                tc_fence_after();
+                const uint32_t stats = base + kStats + stage * C::STATS + half * 64 * 4;
+                uint32_t s[64], g[64], pk[32];
+                tmem_ld32_async(lanes + C::S_COL + 64 * half, s);
+                tmem_ld32_async(lanes + C::S_COL + 64 * half + 32, s + 32);
+                tmem_ld_wait(s);
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                    const uint4 w = shared16(stats + k * 4);
+                    const F2 x0 = fma2(F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, F2(__uint_as_float(w.x), __uint_as_float(w.y)));
+                    const F2 x1 = fma2(F2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, F2(__uint_as_float(w.z), __uint_as_float(w.w)));
+                    s[k] = __float_as_uint(ex2(x0.lo()));
+                    s[k + 1] = __float_as_uint(ex2(x0.hi()));
+                    s[k + 2] = __float_as_uint(ex2(x1.lo()));
+                    s[k + 3] = __float_as_uint(ex2(x1.hi()));
+                    pk[k / 2] = pack2<T>(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    pk[k / 2 + 1] = pack2<T>(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                }
+                tmem_st32(lanes + C::S_COL + 64 * half, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
+                if (!wait(dp_full, dp_phase)) return false;
+                dp_phase ^= 1u;
+                tc_fence_after();
+                tmem_ld32_async(lanes + C::DP_COL + 64 * half, g);
+                tmem_ld32_async(lanes + C::DP_COL + 64 * half + 32, g + 32);
+                tmem_ld_wait(g);
+#pragma unroll
+                for (int k = 0; k < 64; k += 4) {
+                    const uint4 w = shared16(stats + kTileQueries * 4 + k * 4);
+                    F2 x0 = F2(__uint_as_float(g[k]), __uint_as_float(g[k + 1])) + F2(__uint_as_float(w.x), __uint_as_float(w.y));
+                    F2 x1 = F2(__uint_as_float(g[k + 2]), __uint_as_float(g[k + 3])) + F2(__uint_as_float(w.z), __uint_as_float(w.w));
+                    x0 = x0 * F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    x1 = x1 * F2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
+                    if constexpr (kHalf) {
+                        x0 = x0 * up;
+                        x1 = x1 * up;
+                    }
+                    pk[k / 2] = pack2<T>(x0.lo(), x0.hi());
+                    pk[k / 2 + 1] = pack2<T>(x1.lo(), x1.hi());
+                }
+                tmem_st32(lanes + C::DP_COL + 64 * half, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ds_ready);
+                    mbar_arrive(empty_bar(stage));
+                }
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!wait(sums_full, sums_phase)) return false;
+            sums_phase ^= 1u;
+            tc_fence_after();
+            // the first four warps have dV, the others dK
+            const bool whole = t1 - t0 == p.cut.per_unit;
+            const float down = half == 0 ? (kHalf ? exp2i(-15) : 1.0f) : p.scale * (kHalf ? exp2i(-exponent) : 1.0f);
+            const int key0 = u.tile * kTileKeys + quad * 32;
+            // a run's first unit may start inside, and its last one end inside
+            float *part = p.partial + (((static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * 2 + half) * kTileKeys + quad * 32 + lane) * kD;
+#pragma unroll 1
+            for (int k = 0; k < p.d; k += 32) {
+                uint32_t o[32];
+                tmem_ld32_async(lanes + (half == 0 ? C::DV_COL : C::DK_COL) + k, o);
+                tmem_ld_wait(o);
+                float v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * down;
+                if (whole) {
+                    store_keys<T>(p, u, half == 0 ? p.dv : p.dk, key0, k, staging, lane, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(part + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+            tc_fence_before();  // the sums are read before the next unit's first P is announced
+            return true;
+        });
+        if (!ok) wait.fail();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free<1>(tmem, 512u);
+}
+
+// Units that a cut goes through: block r adds up the one in which run r's end is the first cut. Its eight warps take a
+// quarter of the keys of dV or dK each.
+template <typename T, int kD>
+__global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_constant__ Params p)
+{
+    __shared__ __align__(16) uint8_t staging_s[8 * kStageBytes];
+    after_previous();
+    let_next_start();
+    const int64_t cut_at = p.cut.start(blockIdx.x + 1), n = cut_at / p.cut.per_unit, begin = n * p.cut.per_unit;
+    if (cut_at == begin) return;                     // between units
+    const int64_t r0 = p.cut.run_of(begin), r1 = p.cut.run_of(begin + p.cut.per_unit - 1);
+    if (r0 != blockIdx.x) return;                    // an earlier block's
+    const Unit u = unit_at(p, n);
+    if (u.tile * kTileKeys >= u.keys) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quad = warp & 3;
+    const uint32_t staging = static_cast<uint32_t>(__cvta_generic_to_shared(staging_s)) + warp * kStageBytes;
+    for (int k = 0; k < p.d; k += 32) {
+        float v[32] = {};
+        for (int64_t r = r0; r <= r1; ++r) {
+            // the unit starts in run r0 (its last unit there), and before all others (their first)
+            const bool starts = p.cut.start(r) <= begin;
+            const float *part = p.partial + (((r * 2 + starts) * 2 + half) * kTileKeys + quad * 32 + lane) * kD + k;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const float4 w = __ldcg(reinterpret_cast<const float4 *>(part + e));
+                v[e] += w.x;
+                v[e + 1] += w.y;
+                v[e + 2] += w.z;
+                v[e + 3] += w.w;
+            }
+        }
+        store_keys<T>(p, u, half == 0 ? p.dv : p.dk, u.tile * kTileKeys + quad * 32, k, staging, lane, v);
+    }
+}
+
+Cut cut_of(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads)
+{
+    Cut c{};
+    c.units = batch * kv_heads * ((kv_tokens + kTileKeys - 1) / kTileKeys);
+    c.per_unit = q_heads / kv_heads * ((q_tokens + kTileQueries - 1) / kTileQueries);
+    c.work = c.units * c.per_unit;
+    c.runs = static_cast<int32_t>(c.work < kSms ? c.work : kSms);
+    return c;
+}
+
+template <typename T, int kD>
+struct grad_kv_tag;
+
+template <typename T, int kD>
+cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    using C = Cfg<kD>;
+    Params p{};
+    p.cut = cut_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads, a.k.heads);
+    if (p.cut.work == 0) return cudaSuccess;
+    if (!heads_map<T>(&p.q, a.q, a.batch, a.d, kTileQueries) || !heads_map<T>(&p.dout, a.dout, a.batch, a.d, kTileQueries) ||
+        !heads_map<T>(&p.k, a.k, a.batch, a.d, kTileKeys) || !heads_map<T>(&p.v, a.v, a.batch, a.d, kTileKeys))
+        return cudaErrorInvalidValue;
+    if (p.cut.per_unit > INT32_MAX || p.cut.work > INT64_MAX / 1024) return cudaErrorInvalidValue;
+    p.counts = a.counts;
+    p.index = a.index;
+    p.index_rows = a.index_rows;
+    p.base2 = a.base2;
+    p.delta = a.delta;
+    p.amax = a.amax;
+    p.stat_rows = stat_rows(a.q.tokens);
+    p.amax_blocks = p.stat_rows / kStatTokens;
+    p.partial = a.partial;
+    p.dk = a.dk;
+    p.dv = a.dv;
+    p.dev_status = a.dev_status;
+    p.kv_tokens = static_cast<int32_t>(a.kv_tokens);
+    p.kv_heads = static_cast<int32_t>(a.k.heads);
+    p.q_heads = static_cast<int32_t>(a.q.heads);
+    p.group = p.q_heads / p.kv_heads;
+    p.q_tiles = static_cast<int32_t>((a.q.tokens + kTileQueries - 1) / kTileQueries);
+    p.key_tiles = static_cast<int32_t>((a.kv_tokens + kTileKeys - 1) / kTileKeys);
+    p.d = a.d;
+    p.wide = aligned_to(a.dk, 16) && aligned_to(a.dv, 16) && a.d % 8 == 0;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * kLog2e;
+    auto kernel = attention_grad_kv_kernel<T, kD>;
+    cudaError_t e = allow_shared<grad_kv_tag<T, kD>>(kernel);
+    if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
+    if (e != cudaSuccess || p.cut.runs == 1) return e;
+    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1)), 256, 0, stream, 1, p);
+}
+
+}  // namespace
+
+int64_t grad_kv_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads, int d)
+{
+    const Cut c = cut_of(batch, q_tokens, kv_tokens, q_heads, kv_heads);
+    return int64_t{c.runs} * 2 * 2 * kTileKeys * (d <= 64 ? 64 : 128) * 4;
+}
+
+cudaError_t launch_attention_grad_kv(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    if (a.dtype == CONVROT_BF16) return a.d <= 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
+    return a.d <= 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+}
+
+int attention_grad_kv_shared(int form, int *columns)
+{
+    *columns = 512;
+    return form == 0 ? Cfg<64>::SMEM : form == 1 ? Cfg<128>::SMEM : 0;
+}
+
+}  // namespace convrot

@@ -1,0 +1,386 @@
+// The queries' gradient of attention (include/convrot_block.h), on the
+// 5th-generation tensor cores:
+//
+//   dq_i = scale sum_j dS_ij k_j,  dS = P (dP + delta),  P = 2^(c s + base2),  dP = dout V^T
+//
+// A CTA takes 128 queries of a head and goes over the keys in tiles of 128;
+// it is persistent over such items. No sums of a softmax are needed any more,
+// so a tile's dS depends on nothing before it.
+//   warp 0       TMA producer: the item's queries and dout, then tiles of keys
+//                and values in turn, through one ring
+//   warp 1       tensor memory; one thread issues the MMAs
+//   warps 4-11   dS: a row a thread, half of the tile's keys each
+// Tensor memory: two tiles of S = Q K^T in turn, so that the next one is
+// multiplied while dS is made, dP, whose columns then hold dS (16 bits, the A
+// operand of dS K), and the sums dQ. The tile of keys is read K-major for S
+// and MN-major for dQ from the same bytes.
+#include "attention.cuh"
+
+namespace convrot {
+namespace {
+
+using namespace mma16;
+
+constexpr int kThreads = 384;
+constexpr int kRegsWg0 = 80, kRegsMath = 208;
+static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsMath <= kThreads * 168, "register split");
+
+template <int kD>
+struct Cfg {
+    static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
+    static constexpr int STAGES = kD == 64 ? 8 : 4;
+    static constexpr int BARS = 2 * STAGES + 8;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + 8 * kStageBytes + BAR_BYTES;
+    static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;  // S: + 128 for every other tile
+    static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
+    static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
+};
+
+struct Params {
+    HeadsMap q, dout, k, v;
+    const int32_t *counts;
+    const float *base2, *delta, *amax;
+    int64_t amax_blocks;
+    void *dq;
+    int32_t *dev_status;
+    int32_t q_tokens, stat_rows, kv_tokens, q_heads, group;
+    int32_t q_tiles, items;
+    int32_t d, wide;
+    float scale, scale_log2;
+};
+
+template <typename T, int kD>
+__global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<kD>;
+    constexpr bool kHalf = std::is_same_v<T, __half>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
+    const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
+    uint8_t *gbase = smem_raw + (base - raw);
+    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + 8 * kStageBytes;
+    const uint32_t bars = base + kBars;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
+    auto s_full = [&](int i) { return bars + 8u * (2 * C::STAGES + i); };
+    const uint32_t q_full = bars + 8u * (2 * C::STAGES + 2), q_empty = q_full + 8, dp_full = q_full + 16, ds_ready = q_full + 24;
+    const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
+    const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(s_full(0), 1);
+        mbar_init(s_full(1), 1);
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_ready, 8);
+        mbar_init(dq_full, 1);
+        mbar_init(done_bar, 1);
+        *wait.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.q.map);
+        prefetch_map(&p.dout.map);
+        if (p.kv_tokens > 0) prefetch_map(&p.k.map);
+        if (p.kv_tokens > 0) prefetch_map(&p.v.map);
+    }
+    if (warp == 1) tmem_alloc<1>(tmem_slot, 512u);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    after_previous();
+    let_next_start();
+
+    struct Item {
+        int b, h, q0, keys, tiles;
+    };
+    auto item_at = [&](int i) {
+        Item it;
+        const int bh = i / p.q_tiles;
+        it.q0 = (i - bh * p.q_tiles) * kTileQueries;
+        it.b = bh / p.q_heads;
+        it.h = bh - it.b * p.q_heads;
+        it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
+        it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
+        return it;
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
+        if (warp == 0 && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, q_phase = 0, armed = 0;
+            bool ok = true;
+            auto load = [&](const HeadsMap &m, int tile, const Item &it) {
+                if (!ok || !wait(empty_bar(stage), phase ^ 1u)) return void(ok = false);
+                mbar_arrive_expect_tx(full_bar(stage), C::TILE);
+                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, tile * kTileKeys, it.h / p.group, it.b, full_bar(stage));
+                armed |= 1u << stage;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            };
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const Item it = item_at(i);
+                if (it.tiles == 0) continue;
+                if (!wait(q_empty, q_phase ^ 1u)) {
+                    ok = false;
+                    break;
+                }
+                q_phase ^= 1u;
+                mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+                load_tile<C::HALVES>(base, p.q, it.q0, it.h, it.b, q_full);
+                load_tile<C::HALVES>(base + C::TILE, p.dout, it.q0, it.h, it.b, q_full);
+                armed |= 1u << 16;
+                for (int j = 0; j < it.tiles && ok; ++j) {
+                    load(p.k, j, it);
+                    load(p.v, j, it);
+                }
+            }
+            if (!ok) {
+                wait.fail();
+                for (int s = 0; s < C::STAGES; ++s)  // copies in flight land before shared memory goes away
+                    if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
+                if (armed >> 16) mbar_wait(q_full, q_phase ^ 1u);
+            }
+        } else if (warp == 1 && lane == 0) {
+            const uint32_t id_s = idesc<T>(128, 128, false, false);
+            const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
+            const uint32_t id_o = idesc<T>(128, n_o, false, true);
+            int stage = 0;
+            uint32_t phase = 0, q_phase = 0, ds_phase = 0;
+            int tile_no = 0;  // over all items: which of the two S
+            bool ok = true;
+            auto take = [&]() {  // the next stage of the ring, once it is there
+                if (!wait(full_bar(stage), phase)) return -1;
+                const int at = stage;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                return at;
+            };
+            auto product = [&](uint32_t to, uint32_t rows, int at) {  // rows of the item by a tile, over the head's elements
+                const uint64_t a = desc_k(rows), b = desc_k(base + kRing + at * C::TILE);
+                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(to, tile_step_k(a, kk), tile_step_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+            };
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+                const Item it = item_at(i);
+                if (it.tiles == 0) continue;
+                int k_at, v_at, k_next = 0;
+                if (!wait(q_full, q_phase) || (k_at = take()) < 0 || (v_at = take()) < 0) {
+                    ok = false;
+                    break;
+                }
+                q_phase ^= 1u;
+                tc_fence_after();
+                product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
+                mma_commit(s_full(tile_no & 1));
+                product(tmem + C::DP_COL, base + C::TILE, v_at);
+                mma_commit(dp_full);
+                mma_commit(empty_bar(v_at));
+                for (int j = 0; j < it.tiles; ++j, ++tile_no) {
+                    const bool last = j + 1 == it.tiles;
+                    if (!last) {
+                        if ((k_next = take()) < 0) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
+                        mma_commit(s_full((tile_no + 1) & 1));
+                    }
+                    if (!wait(ds_ready, ds_phase)) {
+                        ok = false;
+                        break;
+                    }
+                    ds_phase ^= 1u;
+                    tc_fence_after();
+                    const uint64_t b = desc_mn(base + kRing + k_at * C::TILE, kTileBox);
+#pragma unroll
+                    for (int kk = 0; kk < kTileKeys / kMmaK; ++kk)  // each half of the keys has its own half of dP's columns
+                        mma_ts(tmem + C::DQ_COL, tmem + C::DP_COL + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b + kStepMN * kk, id_o, j > 0 || kk > 0 ? 1u : 0u);
+                    mma_commit(empty_bar(k_at));
+                    if (last) {
+                        mma_commit(dq_full);
+                        mma_commit(q_empty);
+                    } else {
+                        k_at = k_next;
+                        if ((v_at = take()) < 0) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        product(tmem + C::DP_COL, base + C::TILE, v_at);
+                        mma_commit(dp_full);
+                        mma_commit(empty_bar(v_at));
+                    }
+                }
+            }
+            if (!ok) wait.fail();
+            mma_commit(done_bar);
+            mbar_wait(done_bar, 0);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMath));
+        const int half = (warp - 4) >> 2, quad = warp & 3;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        const uint32_t stage = base + kOut + (warp - 4) * kStageBytes;
+        const F2 c2(p.scale_log2);
+        uint32_t dp_phase = 0, dq_phase = 0;
+        int tile_no = 0;
+        bool ok = true;
+        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            const Item it = item_at(i);
+            const int row0 = it.q0 + quad * 32, rows = p.q_tokens - row0 < 32 ? p.q_tokens - row0 : 32;
+            const int64_t at = (static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.stat_rows + row0 + lane;
+            const float base2 = load_f32(p.base2 + at), delta = load_f32(p.delta + at);
+            int exponent = 0;
+            if constexpr (kHalf) {
+                const int64_t head = static_cast<int64_t>(it.b) * (p.q_heads / p.group) + it.h / p.group;
+                exponent = grad_exponent(p.amax + head * p.amax_blocks, p.amax_blocks, lane);
+            }
+            // what dS is multiplied by: P is 2^15 times as large
+            const F2 up(kHalf ? exp2i(exponent) * exp2i(-15) : 1.0f), off2(base2), delta2(delta);
+            for (int j = 0; j < it.tiles; ++j, ++tile_no) {
+                const int b = tile_no & 1;
+                if (!wait(s_full(b), (tile_no >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t s[64], g[64];
+                tmem_ld32_async(lanes + C::S_COL + 128 * b + 64 * half, s);
+                tmem_ld32_async(lanes + C::S_COL + 128 * b + 64 * half + 32, s + 32);
+                tmem_ld_wait(s);
+                const int keys = it.keys - j * kTileKeys - half * 64;
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const F2 x = fma2(F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, off2);
+                    s[k] = __float_as_uint(ex2(x.lo()));
+                    s[k + 1] = __float_as_uint(ex2(x.hi()));
+                }
+                if (keys < 64) {
+#pragma unroll
+                    for (int k = 0; k < 64; ++k)
+                        if (k >= keys) s[k] = 0u;
+                }
+                if (!wait(dp_full, dp_phase)) {
+                    ok = false;
+                    break;
+                }
+                dp_phase ^= 1u;
+                tc_fence_after();
+                tmem_ld32_async(lanes + C::DP_COL + 64 * half, g);
+                tmem_ld32_async(lanes + C::DP_COL + 64 * half + 32, g + 32);
+                tmem_ld_wait(g);
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    F2 x = F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])) * (F2(__uint_as_float(g[k]), __uint_as_float(g[k + 1])) + delta2);
+                    if constexpr (kHalf) x = x * up;
+                    pk[k / 2] = pack2<T>(x.lo(), x.hi());
+                }
+                tmem_st32(lanes + C::DP_COL + 64 * half, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_ready);
+            }
+            if (!ok) break;
+            if (it.tiles > 0) {
+                if (!wait(dq_full, dq_phase)) {
+                    ok = false;
+                    break;
+                }
+                dq_phase ^= 1u;
+                tc_fence_after();
+            }
+            const float down = kHalf ? p.scale * exp2i(-exponent) : p.scale;
+            T *dq = static_cast<T *>(p.dq) + ((static_cast<int64_t>(it.b) * p.q_tokens + row0) * p.q_heads + it.h) * p.d;
+#pragma unroll 1
+            for (int k = half * 32; k < p.d; k += 64) {
+                uint32_t o[32];
+                float v[32];
+                if (it.tiles > 0) {
+                    tmem_ld32_async(lanes + C::DQ_COL + k, o);
+                    tmem_ld_wait(o);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = it.tiles > 0 ? __uint_as_float(o[e]) * down : 0.0f;
+                if (rows > 0)
+                    store_rows<T>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+            }
+            tc_fence_before();  // dQ is read before the next item's first dS is announced
+        }
+        if (!ok) wait.fail();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free<1>(tmem, 512u);
+}
+
+template <typename T, int kD>
+struct grad_q_tag;
+
+template <typename T, int kD>
+cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    using C = Cfg<kD>;
+    Params p{};
+    if (!heads_map<T>(&p.q, a.q, a.batch, a.d, kTileQueries) || !heads_map<T>(&p.dout, a.dout, a.batch, a.d, kTileQueries))
+        return cudaErrorInvalidValue;
+    if (a.k.tokens > 0 && (!heads_map<T>(&p.k, a.k, a.batch, a.d, kTileKeys) || !heads_map<T>(&p.v, a.v, a.batch, a.d, kTileKeys)))
+        return cudaErrorInvalidValue;
+    p.counts = a.counts;
+    p.base2 = a.base2;
+    p.delta = a.delta;
+    p.amax = a.amax;
+    p.stat_rows = static_cast<int32_t>(stat_rows(a.q.tokens));
+    p.amax_blocks = p.stat_rows / kStatTokens;
+    p.dq = a.dq;
+    p.dev_status = a.dev_status;
+    p.q_tokens = static_cast<int32_t>(a.q.tokens);
+    p.kv_tokens = static_cast<int32_t>(a.kv_tokens);
+    p.q_heads = static_cast<int32_t>(a.q.heads);
+    p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
+    p.q_tiles = static_cast<int32_t>((a.q.tokens + kTileQueries - 1) / kTileQueries);
+    const int64_t items = a.batch * a.q.heads * p.q_tiles;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    p.items = static_cast<int32_t>(items);
+    p.d = a.d;
+    p.wide = aligned_to(a.dq, 16) && a.d % 8 == 0;
+    p.scale = a.scale;
+    p.scale_log2 = a.scale * kLog2e;
+    auto kernel = attention_grad_q_kernel<T, kD>;
+    cudaError_t e = allow_shared<grad_q_tag<T, kD>>(kernel);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_grad_q(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    if (a.dtype == CONVROT_BF16) return a.d <= 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
+    return a.d <= 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+}
+
+int attention_grad_q_shared(int form, int *columns)
+{
+    *columns = 512;
+    return form == 0 ? Cfg<64>::SMEM : form == 1 ? Cfg<128>::SMEM : 0;
+}
+
+}  // namespace convrot
