@@ -9,6 +9,8 @@ namespace convrot {
 
 // y (and gate, up): many rows, and few.
 cudaError_t launch_gated_gemm(const convrot_gated_linear_args &a, cudaStream_t stream);
+bool gated_few_takes(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_gated_few(const convrot_gated_linear_args &a, cudaStream_t stream);
 
 // dx = dg w_gate + du w_up and dw = dg^T x, du^T x from dg and du [m, ldd].
 cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, cudaStream_t stream);
@@ -24,5 +26,6 @@ cudaError_t launch_align_rows(const void *x, int64_t rows, int64_t cols, int64_t
 
 // Shared memory and tensor-memory columns of every launch form, for the check that no mix of blocks waits for columns.
 int gated_gemm_shared(int form, int *columns);  // 0 past the last form
+int gated_few_shared(int form, int *columns);
 
 }  // namespace convrot

@@ -74,19 +74,6 @@ __device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t t
     nt = local / rows;
 }
 
-// act of two values: GELU as in block.h, SiLU through one exponential and one reciprocal.
-template <int kAct>
-__device__ __forceinline__ F2 gate_act2(F2 v)
-{
-    if constexpr (kAct == CONVROT_ACT_SILU) {
-        const F2 z = v * F2(-1.4426950f);
-        const F2 e = F2(ex2(z.lo()), ex2(z.hi())) + F2(1.0f);
-        return v * F2(rcp(e.lo()), rcp(e.hi()));
-    } else {
-        return act2<kAct>(v);
-    }
-}
-
 template <int kMode, int kBN, typename T, int kAct>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gated_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB0,

@@ -193,6 +193,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     }
 }
 
+// act of two values: GELU as in block.h, SiLU through one exponential and one reciprocal.
+template <int kAct>
+__device__ __forceinline__ F2 gate_act2(F2 v)
+{
+    if constexpr (kAct == CONVROT_ACT_SILU) {
+        const F2 z = v * F2(-1.4426950f);
+        const F2 e = F2(ex2(z.lo()), ex2(z.hi())) + F2(1.0f);
+        return v * F2(rcp(e.lo()), rcp(e.hi()));
+    } else {
+        return act2<kAct>(v);
+    }
+}
+
 // The kernels' bounded wait: gives up early once another role of the block has.
 struct Waits {
     volatile int *abort_flag;
