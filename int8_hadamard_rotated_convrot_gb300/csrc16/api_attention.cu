@@ -129,14 +129,22 @@ bool apart(int64_t batch, int64_t tokens, int64_t heads, const int64_t (&strides
 
 struct ForwardWork {
     Operands q, kv;
+    bool few;
+    float *partial = nullptr;
     int64_t bytes;
     explicit ForwardWork(const convrot_attention_args &a, char *base = nullptr)
         : q(a.batch, a.head_dim, states(a.q, a.q_tokens, a.q_heads, a.q_strides)),
           kv(a.batch, a.head_dim, states(a.k, a.kv_tokens, a.kv_heads, a.k_strides), states(a.v, a.kv_tokens, a.kv_heads, a.v_strides))
     {
         Work w{base};
-        q.plan(w, nullptr, 0, false);
-        kv.plan(w, a.mask, a.mask_stride, false);
+        few = a.kv_tokens > 0 && attention_few_takes(a.q_tokens, a.q_heads, a.kv_heads);
+        if (few) {
+            kv.plan(w, nullptr, 0, false);
+            partial = w.take<float>(attention_few_partial_bytes(a.batch, a.kv_tokens, a.kv_heads, a.head_dim) / 4);
+        } else {
+            q.plan(w, nullptr, 0, false);
+            kv.plan(w, a.mask, a.mask_stride, false);
+        }
         bytes = w.used;
     }
 };
@@ -205,7 +213,7 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
     b.scale = a->scale;
     b.d = a->head_dim;
     b.dtype = a->dtype;
-    return done(launch_attention(b, stream));
+    return done(w.few ? launch_attention_few(b, a->mask, a->mask_stride, w.partial, stream) : launch_attention(b, stream));
 }
 
 int64_t convrot_attention_backward_work_bytes(const convrot_attention_backward_args *a)

@@ -51,6 +51,11 @@ struct AttentionArgs {
 };
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t stream);
 
+// Few queries: keys and values whose heads start on 16 bytes (queries may start anywhere), the mask read as it is.
+bool attention_few_takes(int64_t q_tokens, int64_t q_heads, int64_t kv_heads);
+int64_t attention_few_partial_bytes(int64_t batch, int64_t kv_tokens, int64_t kv_heads, int d);
+cudaError_t launch_attention_few(const AttentionArgs &a, const uint8_t *mask, int64_t mask_stride, float *partial, cudaStream_t stream);
+
 // Rows of each head's statistics in the backward pass: whole tiles of queries.
 constexpr int kTileQueries = 128;
 inline int64_t stat_rows(int64_t tokens) { return (tokens + kTileQueries - 1) / kTileQueries * kTileQueries; }

@@ -175,7 +175,8 @@ def test_gated_linear_without_rows(dtype):
 # batch, queries, keys, heads, key heads, head_dim
 SHAPES = [(1, 1, 1, 1, 1, 8), (2, 1, 5, 4, 2, 64), (1, 3, 128, 2, 1, 128), (2, 77, 77, 3, 3, 40), (1, 128, 129, 2, 2, 72), (3, 129, 127, 4, 1, 64),
           (1, 256, 300, 2, 2, 128), (2, 257, 1, 2, 1, 96), (1, 300, 512, 3, 3, 80), (2, 130, 640, 2, 2, 100), (1, 33, 260, 5, 5, 33), (1, 515, 200, 6, 2, 1),
-          (5, 1, 1000, 8, 8, 128), (1, 1, 4096, 8, 1, 64), (2, 5, 257, 16, 2, 128), (70, 40, 30, 9, 3, 16)]
+          (5, 1, 1000, 8, 8, 128), (1, 1, 4096, 8, 1, 64), (2, 5, 257, 16, 2, 128), (70, 40, 30, 9, 3, 16),
+          (1, 1, 70001, 2, 1, 128), (1, 4, 30000, 4, 1, 60), (3, 16, 777, 2, 2, 64), (2, 17, 777, 2, 2, 64)]
 MASKS = ["none", "padded", "scattered"]
 
 

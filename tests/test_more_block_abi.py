@@ -146,7 +146,7 @@ def test_attention_refuses_its_own_operands(lib):
     assert lib.convrot_attention_backward(None, None) == cr.ERR_INVALID_ARG
     for strides in ((768, 256, 0), (768, 32, 64), (0, 256, 64), (768, 256, 256), (64, 256, 64)):  # heads of out over one another
         assert lib.convrot_attention(attention_args(os=strides), None) == cr.ERR_INVALID_ARG
-    assert lib.convrot_attention(attention_args(mask=FAKE), None) == cr.ERR_INVALID_ARG  # needs a workspace
+    assert lib.convrot_attention(attention_args(mask=FAKE, tq=30), None) == cr.ERR_INVALID_ARG  # needs a workspace
     for kw in (dict(dq=0), dict(dk=0), dict(dv=0), dict(dout=0), dict(work=0), dict(work_bytes=64)):
         assert lib.convrot_attention_backward(attention_grad_args(**kw), None) == cr.ERR_INVALID_ARG
     assert lib.convrot_attention_backward(attention_grad_args(work=FAKE + 8), None) == cr.ERR_ALIGNMENT
@@ -162,10 +162,14 @@ def test_empty_attention_launches_nothing(lib):
 
 def test_attention_workspaces(lib):
     assert lib.convrot_attention_work_bytes(attention_args()) == 0
-    rows = 2 * 128 * 2 * 64 * 2
-    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE)) == 256 + 2 * rows
-    assert lib.convrot_attention_work_bytes(attention_args(q=FAKE + 2)) == 2 * 3 * 4 * 64 * 2
-    assert lib.convrot_attention_work_bytes(attention_args(tk=0, mask=FAKE)) == 0
+    many, rows = dict(tq=30), 2 * 128 * 2 * 64 * 2
+    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE, **many)) == 256 + 2 * rows
+    assert lib.convrot_attention_work_bytes(attention_args(q=FAKE + 2, **many)) == 2 * 30 * 4 * 64 * 2
+    assert lib.convrot_attention_work_bytes(attention_args(tk=0, mask=FAKE, **many)) == 0
+    # few queries: the mask is read as it is, unaligned keys are copied, and long states are shared out over clusters
+    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE, q=FAKE + 2)) == 0
+    assert lib.convrot_attention_work_bytes(attention_args(k=FAKE + 2)) == 2 * 5 * 2 * 64 * 2
+    assert lib.convrot_attention_work_bytes(attention_args(tk=1 << 20)) > 0
 
 
 def test_binding_refuses(lib):
@@ -214,6 +218,7 @@ namespace convrot {
 int lora_down_shared(int r);
 int fp8_few_shared(int64_t m, int64_t n, int64_t k, bool quantize, int *columns);
 int gated_gemm_shared(int form, int *columns);
+int gated_few_shared(int form, int *columns);
 int attention_shared(int form, int *columns);
 int attention_grad_q_shared(int form, int *columns);
 int attention_grad_kv_shared(int form, int *columns);
@@ -222,7 +227,7 @@ int main()
 {
     using namespace convrot;
     int columns = 0;
-    for (auto f : {gated_gemm_shared, attention_shared, attention_grad_q_shared, attention_grad_kv_shared})
+    for (auto f : {gated_gemm_shared, gated_few_shared, attention_shared, attention_grad_q_shared, attention_grad_kv_shared})
         for (int form = 0; const int bytes = f(form, &columns); ++form) printf("%d %d\n", columns, bytes);
     // the smallest of the others, by columns
     for (int64_t m : {1, 17, 64}) {
