@@ -71,7 +71,7 @@ struct ForwardWork {
 struct BackwardWork {
     Operand x, wg, wu;
     void *dg, *du;
-    float *partial = nullptr;
+    float *partial = nullptr, *shares = nullptr;
     int64_t bytes, ldd;
     explicit BackwardWork(const convrot_gated_linear_backward_args &a, char *base = nullptr)
         : x(a.x, a.m, a.k, a.ldx), wg(a.w_gate, a.n, a.k, a.ldw_gate), wu(a.w_up, a.n, a.k, a.ldw_up), ldd(pitch(a.n))
@@ -84,6 +84,7 @@ struct BackwardWork {
         if (a.dx) {
             wg.plan(w);
             wu.plan(w);
+            shares = static_cast<float *>(w.take(gated_dx_partial_bytes(a.m, a.n, a.k)));
         }
         bytes = w.used;
     }
@@ -172,7 +173,7 @@ convrot_status convrot_gated_linear_backward(const convrot_gated_linear_backward
     b.ldw_gate = w.wg.ld;
     b.w_up = w.wu.p;
     b.ldw_up = w.wu.ld;
-    if (a->dx && launch_gated_dx(b, w.dg, w.du, w.ldd, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
+    if (a->dx && launch_gated_dx(b, w.dg, w.du, w.ldd, w.shares, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
     if (a->dw_gate && launch_gated_dw(b, w.dg, w.du, w.ldd, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
     return CONVROT_OK;
 }

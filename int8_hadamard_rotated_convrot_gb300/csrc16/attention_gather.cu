@@ -4,15 +4,17 @@
 // that do not start on 16 bytes, which a tensor map cannot describe.
 //
 // A masked key costs the products nothing then, and what stands in it, NaN too,
-// is never an operand. A block takes 32 tokens of a sample. Their places are
-// the number of tokens that are there before them, which each block counts for
-// itself: 4096 bytes of a mask are 16 a thread.
+// is never an operand. A block takes eight tokens of a sample and tensor. Their
+// places are the number of tokens that are there before them, which each block
+// counts for itself: 4096 bytes of a mask are 16 a thread. Latency is all that
+// counts here (2 x 77 tokens of 10 heads of 64: 20 us with 32 tokens a block
+// and a piece at a time).
 #include "attention.h"
 
 namespace convrot {
 namespace {
 
-constexpr int kTokens = 32, kThreads = 256;
+constexpr int kTokens = 8, kThreads = 256, kBatch = 4;  // pieces of a thread in flight
 
 __device__ __forceinline__ bool aligned4(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
@@ -35,7 +37,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
         __syncthreads();
         const uint8_t *mask = a.mask + b * a.mask_stride;
         int before = 0, all = 0;
-        // whole words where they are aligned (a word never crosses t0, a multiple of 32 past the mask's own start)
+        // whole words where they are aligned (a word never crosses t0, a multiple of 8 past the mask's own start)
         const bool words = aligned4(mask);
         const int64_t whole = words ? a.tokens / 4 : 0;
         for (int64_t i = threadIdx.x; i < whole; i += kThreads) {
@@ -56,52 +58,59 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
         }
         __syncthreads();
         total = total_s;
-        if (threadIdx.x < kTokens) {
+        if (threadIdx.x < 32) {
             const int64_t t = t0 + lane;
-            const bool there = t < a.tokens && *reinterpret_cast<const volatile uint8_t *>(mask + t) != 0;
+            const bool there = lane < kTokens && t < a.tokens && *reinterpret_cast<const volatile uint8_t *>(mask + t) != 0;
             const uint32_t all_there = __ballot_sync(0xffffffffu, there);
             const int at = before_s + __popc(all_there & ((1u << lane) - 1u));
-            place[lane] = there ? at : -1;
-            if (there && a.index) a.index[b * a.rows + at] = static_cast<int32_t>(t);
+            if (lane < kTokens) place[lane] = there ? at : -1;
+            if (there && a.index && blockIdx.z == 0) a.index[b * a.rows + at] = static_cast<int32_t>(t);
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) a.counts[b] = static_cast<int32_t>(total);
+        if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.counts[b] = static_cast<int32_t>(total);
         __syncthreads();
     }
     const int groups = a.dp / 8;
     const int64_t per_token = a.heads * groups, work = per_token * kTokens;
     const int64_t end = (total + kTileKeys - 1) / kTileKeys * kTileKeys;
-    for (int s = 0; s < a.count; ++s) {
-        const uint16_t *src = static_cast<const uint16_t *>(a.src[s]) + b * a.strides[s][0];
-        uint16_t *dst = static_cast<uint16_t *>(a.dst[s]) + b * a.rows * a.heads * a.dp;
-        uint16_t *zero = static_cast<uint16_t *>(a.zero[s]);
-        const bool wide = a.d % 8 == 0 && a.strides[s][0] % 8 == 0 && a.strides[s][1] % 8 == 0 && a.strides[s][2] % 8 == 0 &&
-                          reinterpret_cast<uintptr_t>(a.src[s]) % 16 == 0;
-        for (int64_t i = threadIdx.x; i < work; i += kThreads) {
+    const int s = blockIdx.z;
+    const uint16_t *src = static_cast<const uint16_t *>(a.src[s]) + b * a.strides[s][0];
+    uint16_t *dst = static_cast<uint16_t *>(a.dst[s]) + b * a.rows * a.heads * a.dp;
+    uint16_t *zero = static_cast<uint16_t *>(a.zero[s]);
+    const bool wide = a.d % 8 == 0 && a.strides[s][0] % 8 == 0 && a.strides[s][1] % 8 == 0 && a.strides[s][2] % 8 == 0 &&
+                      reinterpret_cast<uintptr_t>(a.src[s]) % 16 == 0;
+    for (int64_t i0 = threadIdx.x; i0 < work; i0 += kThreads * kBatch) {
+        uint4 w[kBatch];
+        int64_t to[kBatch];  // place of the piece, or -1
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            const int64_t i = i0 + n * kThreads;
+            to[n] = -1;
+            if (i >= work) continue;
             const int local = static_cast<int>(i / per_token);
             const int64_t rest = i - local * per_token, h = rest / groups, t = t0 + local;
-            const int e0 = static_cast<int>(rest - h * groups) * 8, n = a.d - e0 < 8 ? a.d - e0 : 8;
-            if (t < a.tokens) {
-                const int64_t row = a.mask ? place[local] : t;
-                if (row >= 0) {
-                    const uint16_t *from = src + t * a.strides[s][1] + h * a.strides[s][2] + e0;
-                    uint4 w;
-                    if (wide) {
-                        w = __ldcg(reinterpret_cast<const uint4 *>(from));
-                    } else {
-                        uint32_t v[8];
+            const int e0 = static_cast<int>(rest - h * groups) * 8, left = a.d - e0 < 8 ? a.d - e0 : 8;
+            const int64_t row = t >= a.tokens ? -1 : a.mask ? place[local] : t;
+            if (row >= 0) {
+                to[n] = (row * a.heads + h) * a.dp + e0;
+                const uint16_t *from = src + t * a.strides[s][1] + h * a.strides[s][2] + e0;
+                if (wide) {
+                    w[n] = __ldcg(reinterpret_cast<const uint4 *>(from));
+                } else {
+                    uint32_t v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = e < n ? *reinterpret_cast<const volatile uint16_t *>(from + e) : 0;
-                        w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                    }
-                    *reinterpret_cast<uint4 *>(dst + (row * a.heads + h) * a.dp + e0) = w;
-                } else if (zero) {
-                    uint16_t *to = zero + ((b * a.tokens + t) * a.heads + h) * a.d + e0;
-                    for (int e = 0; e < n; ++e) to[e] = 0;
+                    for (int e = 0; e < 8; ++e) v[e] = e < left ? *reinterpret_cast<const volatile uint16_t *>(from + e) : 0;
+                    w[n] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
                 }
+            } else if (zero && t < a.tokens) {
+                uint16_t *z = zero + ((b * a.tokens + t) * a.heads + h) * a.d + e0;
+                for (int e = 0; e < left; ++e) z[e] = 0;
             }
             // the rows behind the last one, to the end of its tile
             if (a.mask && t >= total && t < end) *reinterpret_cast<uint4 *>(dst + (t * a.heads + h) * a.dp + e0) = make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n)
+            if (to[n] >= 0) *reinterpret_cast<uint4 *>(dst + to[n]) = w[n];
     }
 }
 
@@ -123,7 +132,7 @@ cudaError_t launch_gather(const GatherArgs &a, cudaStream_t stream)
             part.counts = a.counts + b0;
             if (a.index) part.index = a.index + b0 * a.rows;
         }
-        const cudaError_t e = launch_after(gather_kernel, dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(part.batch)), kThreads, 0, stream, 1, part);
+        const cudaError_t e = launch_after(gather_kernel, dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(part.batch), static_cast<unsigned>(a.count)), kThreads, 0, stream, 1, part);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -372,38 +372,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
     if (warp == 1) tmem_free<1>(tmem, 512u);
 }
 
-// Units that a cut goes through: block r adds up the one in which run r's end is the first cut. Its eight warps take a
-// quarter of the keys of dV or dK each.
+// Units that a cut goes through: the blocks of column r add up the one in which run r's end is the first cut, four
+// elements of dV or dK a thread.
 template <typename T, int kD>
 __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_constant__ Params p)
 {
-    __shared__ __align__(16) uint8_t staging_s[8 * kStageBytes];
     after_previous();
     let_next_start();
     const int64_t cut_at = p.cut.start(blockIdx.x + 1), n = cut_at / p.cut.per_unit, begin = n * p.cut.per_unit;
     if (cut_at == begin) return;                     // between units
     const int64_t r0 = p.cut.run_of(begin), r1 = p.cut.run_of(begin + p.cut.per_unit - 1);
-    if (r0 != blockIdx.x) return;                    // an earlier block's
+    if (r0 != blockIdx.x) return;                    // an earlier column's
     const Unit u = unit_at(p, n);
-    if (u.tile * kTileKeys >= u.keys) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2, quad = warp & 3;
-    const uint32_t staging = static_cast<uint32_t>(__cvta_generic_to_shared(staging_s)) + warp * kStageBytes;
-    for (int k = 0; k < p.d; k += 32) {
-        float v[32] = {};
-        for (int64_t r = r0; r <= r1; ++r) {
-            // the unit starts in run r0 (its last unit there), and before all others (their first)
-            const bool starts = p.cut.start(r) <= begin;
-            const float *part = p.partial + (((r * 2 + starts) * 2 + half) * kTileKeys + quad * 32 + lane) * kD + k;
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
+    const int key = u.tile * kTileKeys + row;
+    if (key >= u.keys || col >= p.d) return;
+    // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
+    const float *first = p.partial + (r0 * 2 + 1) * 2 * kTileKeys * kD + at, *other = p.partial + (r0 + 1) * 4 * kTileKeys * kD + at;
+    float4 sum = __ldcg(reinterpret_cast<const float4 *>(first));
+    const int64_t count = r1 - r0;
+    constexpr int kBatch = 8;
+    for (int64_t r = 0; r < count; r += kBatch) {
+        float4 w[kBatch];
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const float4 w = __ldcg(reinterpret_cast<const float4 *>(part + e));
-                v[e] += w.x;
-                v[e + 1] += w.y;
-                v[e + 2] += w.z;
-                v[e + 3] += w.w;
-            }
+        for (int i = 0; i < kBatch; ++i)
+            if (r + i < count) w[i] = __ldcg(reinterpret_cast<const float4 *>(other + (r + i) * 4 * kTileKeys * kD));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (r + i >= count) break;
+            sum.x += w[i].x;
+            sum.y += w[i].y;
+            sum.z += w[i].z;
+            sum.w += w[i].w;
         }
-        store_keys<T>(p, u, half == 0 ? p.dv : p.dk, u.tile * kTileKeys + quad * 32, k, staging, lane, v);
+    }
+    const int64_t token = p.index ? load_i32(p.index + u.b * p.index_rows + key) : key;
+    T *to = static_cast<T *>(half == 0 ? p.dv : p.dk) + ((static_cast<int64_t>(u.b) * p.kv_tokens + token) * p.kv_heads + u.h) * p.d + col;
+    if (p.wide) {
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
+    } else {
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < p.d) to[e] = from_f32<T>(v[e]);
     }
 }
 
@@ -457,7 +468,7 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     cudaError_t e = allow_shared<grad_kv_tag<T, kD>>(kernel);
     if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.cut.runs == 1) return e;
-    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1)), 256, 0, stream, 1, p);
+    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / 1024), 256, 0, stream, 1, p);
 }
 
 }  // namespace

@@ -2,8 +2,10 @@
 // -lse in base 2, so that a probability is one multiply-add and one exponential,
 // and -delta = -dout . out, so that dS = P (dP - delta) needs no sum over keys.
 //
-// A warp takes one query of one head; a block the queries of kStatTokens tokens
-// and of the heads that share a key head. Rows behind the last query get -infinity
+// A block takes the queries of kStatTokens tokens and of the heads that share a
+// key head; kLanes lanes take one query, 16 bytes of it each, and kBatch of
+// them are loaded together (8190 x 40 heads of 128: 74 us with a query a warp
+// and one in flight). Rows behind the last query get -infinity
 // for the first: their probabilities are 0. Bound by HBM: out and dout once.
 #include "attention.cuh"
 
@@ -23,7 +25,7 @@ struct StatParams {
     float shift;
 };
 
-template <typename T>
+template <typename T, int kD>
 __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_constant__ StatParams p)
 {
     __shared__ float tops[8];
@@ -32,42 +34,60 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t block = blockIdx.x % p.blocks, bh = blockIdx.x / p.blocks, b = bh / p.kv_heads, hk = bh - b * p.kv_heads;
     const int64_t t0 = block * kStatTokens;
+    constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 4, kStride = 8 * kPerWarp;  // queries of a block's round
+    const int sub = lane / kLanes, e0 = lane % kLanes * 8;
+    const int queries = kStatTokens * p.group;
     float top = 0.0f;
-    for (int i = warp; i < kStatTokens * p.group; i += 8) {
-        const int64_t t = t0 + i / p.group, h = hk * p.group + i % p.group;
-        if (t >= p.rows) break;
-        float sum = 0.0f;
-        if (t < p.q_tokens) {
-            const T *o = static_cast<const T *>(p.out) + b * p.out_strides[0] + t * p.out_strides[1] + h * p.out_strides[2];
-            const T *g = static_cast<const T *>(p.dout) + b * p.dout_strides[0] + t * p.dout_strides[1] + h * p.dout_strides[2];
-            if (p.wide) {  // four elements a lane
-                if (lane * 4 < p.d) {
-                    Raw<T, 4> ro, rg;
-                    float vo[4], vg[4];
-                    ro.load(o + lane * 4);
-                    rg.load(g + lane * 4);
-                    ro.unpack(vo);
-                    rg.unpack(vg);
+    for (int i0 = warp * kPerWarp + sub; i0 - sub < queries; i0 += kStride * kBatch) {
+        Raw<T, 8> ro[kBatch], rg[kBatch];
+        float part[kBatch];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sum = fmaf(vo[e], vg[e], sum);
-                        top = fmaxf(top, fabsf(vg[e]));
-                    }
-                }
+        for (int n = 0; n < kBatch; ++n) {
+            const int i = i0 + n * kStride;
+            const int64_t t = t0 + i / p.group, h = hk * p.group + i % p.group;
+            ro[n].bits[0] = rg[n].bits[0] = make_uint4(0, 0, 0, 0);
+            if (i >= queries || t >= p.q_tokens || e0 >= p.d) continue;
+            const T *o = static_cast<const T *>(p.out) + b * p.out_strides[0] + t * p.out_strides[1] + h * p.out_strides[2] + e0;
+            const T *g = static_cast<const T *>(p.dout) + b * p.dout_strides[0] + t * p.dout_strides[1] + h * p.dout_strides[2] + e0;
+            if (p.wide) {
+                ro[n].load_stream(o);
+                rg[n].load(g);
             } else {
-                for (int e = lane; e < p.d; e += 32) {
-                    const float vg = to_f32(g[e]);
-                    sum = fmaf(to_f32(o[e]), vg, sum);
-                    top = fmaxf(top, fabsf(vg));
-                }
-            }
+                float vo[8], vg[8];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+                for (int e = 0; e < 8; ++e) {
+                    vo[e] = e0 + e < p.d ? to_f32(o[e]) : 0.0f;
+                    vg[e] = e0 + e < p.d ? to_f32(g[e]) : 0.0f;
+                }
+                ro[n].pack(vo);
+                rg[n].pack(vg);
+            }
         }
-        if (lane == 0) {
-            const int64_t head = b * p.q_heads + h, at = head * p.rows + t;
-            p.base2[at] = t < p.q_tokens ? fmaf(load_f32(p.lse + head * p.q_tokens + t), -kLog2e, p.shift) : neg_inf();
-            p.delta[at] = -sum;
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+            float vo[8], vg[8];
+            ro[n].unpack(vo);
+            rg[n].unpack(vg);
+            part[n] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                part[n] = fmaf(vo[e], vg[e], part[n]);
+                top = fmaxf(top, fabsf(vg[e]));
+            }
+        }
+#pragma unroll
+        for (int s = kLanes / 2; s > 0; s >>= 1)
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) part[n] += __shfl_xor_sync(0xffffffffu, part[n], s);
+        if (e0 == 0) {
+#pragma unroll
+            for (int n = 0; n < kBatch; ++n) {
+                const int i = i0 + n * kStride;
+                const int64_t t = t0 + i / p.group, head = b * p.q_heads + hk * p.group + i % p.group, at = head * p.rows + t;
+                if (i >= queries || t >= p.rows) continue;
+                p.base2[at] = t < p.q_tokens ? fmaf(load_f32(p.lse + head * p.q_tokens + t), -kLog2e, p.shift) : neg_inf();
+                p.delta[at] = -part[n];
+            }
         }
     }
     if (!p.amax) return;
@@ -88,13 +108,13 @@ cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stre
     StatParams p{};
     p.out = a.out;
     p.dout = a.dout_own;
-    bool wide = a.d % 4 == 0;
+    bool wide = a.d % 8 == 0;
     for (int i = 0; i < 3; ++i) {
         p.out_strides[i] = a.out_strides[i];
         p.dout_strides[i] = a.dout_own_strides[i];
-        wide = wide && a.out_strides[i] % 4 == 0 && a.dout_own_strides[i] % 4 == 0;
+        wide = wide && a.out_strides[i] % 8 == 0 && a.dout_own_strides[i] % 8 == 0;
     }
-    p.wide = wide && aligned_to(a.out, 8) && aligned_to(a.dout_own, 8);
+    p.wide = wide && aligned_to(a.out, 16) && aligned_to(a.dout_own, 16);
     p.lse = a.lse;
     p.base2 = a.base2;
     p.delta = a.delta;
@@ -109,9 +129,10 @@ cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stre
     const int64_t blocks = a.batch * p.kv_heads * p.blocks;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (a.dtype == CONVROT_BF16) return launch_after(attention_stats_kernel<__nv_bfloat16>, grid, 256, 0, stream, 1, p);
+    if (a.dtype == CONVROT_BF16)
+        return launch_after(a.d <= 64 ? attention_stats_kernel<__nv_bfloat16, 64> : attention_stats_kernel<__nv_bfloat16, 128>, grid, 256, 0, stream, 1, p);
     p.shift = kProbShift<__half>;
-    return launch_after(attention_stats_kernel<__half>, grid, 256, 0, stream, 1, p);
+    return launch_after(a.d <= 64 ? attention_stats_kernel<__half, 64> : attention_stats_kernel<__half, 128>, grid, 256, 0, stream, 1, p);
 }
 
 }  // namespace convrot

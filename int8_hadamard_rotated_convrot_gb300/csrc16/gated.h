@@ -12,8 +12,9 @@ cudaError_t launch_gated_gemm(const convrot_gated_linear_args &a, cudaStream_t s
 bool gated_few_takes(int64_t m, int64_t n, int64_t k);
 cudaError_t launch_gated_few(const convrot_gated_linear_args &a, cudaStream_t stream);
 
-// dx = dg w_gate + du w_up and dw = dg^T x, du^T x from dg and du [m, ldd].
-cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, cudaStream_t stream);
+// dx = dg w_gate + du w_up (partial: gated_dx_partial_bytes) and dw = dg^T x, du^T x from dg and du [m, ldd].
+int64_t gated_dx_partial_bytes(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, float *partial, cudaStream_t stream);
 cudaError_t launch_gated_dw(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, cudaStream_t stream);
 
 // dg and du [m, ldd] (ldd a multiple of 8; columns past n become zero) and, where partial is not null, the column sums:

@@ -29,6 +29,8 @@ using namespace mma16;
 
 enum Mode { kForward, kDx, kDw };
 
+constexpr int kMaxSplits = 8;
+
 constexpr int kBK = 64;   // of K a step: one swizzle span, or 64 rows
 constexpr int kBM = 128;  // rows of A (and of the accumulators) per CTA
 constexpr int kDrainWarps = 8, kThreads = 128 + 32 * kDrainWarps;
@@ -52,6 +54,9 @@ struct Params {
     int32_t steps;        // of K, in one operand pair
     int32_t parts;        // operand pairs that one sum runs over (kDx: 2)
     int32_t sections;     // outputs one above the other (kDw: 2)
+    int32_t splits;       // CTA pairs that share the steps of a tile
+    float *partial;       // splits > 1: [splits][rows][ld_partial]
+    int64_t ld_partial;
     void *out[2];         // kForward: y; kDw: dw_gate, dw_up
     int64_t ld[2];
     void *keep[2];        // kForward: gate and up, or null
@@ -102,7 +107,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool leader = rank == 0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t tiles_m = static_cast<uint32_t>(p.tiles_m) * p.sections;
-    const uint32_t tiles = tiles_m * p.tiles_n, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t tiles = tiles_m * p.tiles_n, items = tiles * p.splits, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // item -> tile, and its share of the steps (over all parts)
+    const int all_steps = p.steps * p.parts;
+    auto first_step = [&](uint32_t share) { return static_cast<int>(static_cast<int64_t>(all_steps) * share / p.splits); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -132,18 +140,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+        for (uint32_t t = pair; t < items && ok; t += pairs) {
             uint32_t mt, nt;
-            tile_at(t, tiles_m, p.tiles_n, mt, nt);
+            const uint32_t share = t / tiles;
+            tile_at(t - share * tiles, tiles_m, p.tiles_n, mt, nt);
             const bool second = kMode == kDw && mt >= static_cast<uint32_t>(p.tiles_m);
             if (second) mt -= p.tiles_m;
             const int row = static_cast<int>(mt * 2 * kBM + rank * kBM);
             // kForward: each CTA's rows of its own weight; else its half of the tile's columns
             const int col = static_cast<int>(kMode == kForward ? nt * (kBN / 2) : nt * kBN + rank * (kBN / 2));
-            for (int part = 0; part < p.parts && ok; ++part) {
+            const int end = first_step(share + 1);
+            for (int step = first_step(share); step < end;) {
+                const int part = step >= p.steps, j0 = step - part * p.steps, j1 = end - part * p.steps < p.steps ? end - part * p.steps : p.steps;
                 const CUtensorMap *ma = (kMode == kDx ? part : second) ? &tmA1 : &tmA0;
                 const CUtensorMap *mb = (kMode == kForward ? rank != 0 : kMode == kDx && part) ? &tmB1 : &tmB0;
-                for (int j = 0; j < p.steps; ++j) {
+                for (int j = j0; j < j1; ++j) {
                     if (!wait(empty_bar(stage), phase ^ 1u)) {
                         ok = false;
                         break;
@@ -169,6 +180,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
+                if (!ok) break;
+                step += j1 - j0;
             }
         }
         if (!ok) {
@@ -188,8 +201,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, buf = 0, buf_phase = 0;
         bool ok = true;
-        const int steps = p.steps * p.parts;
-        for (uint32_t t = pair; t < tiles && ok; t += pairs) {
+        for (uint32_t t = pair; t < items && ok; t += pairs) {
+            const uint32_t share = t / tiles;
+            const int steps = first_step(share + 1) - first_step(share);
             if (!wait(drained_bar(buf), buf_phase ^ 1u)) {
                 ok = false;
                 break;
@@ -229,9 +243,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t drained0 = map_to_rank(drained_bar(0), 0);
         uint32_t buf = 0, buf_phase = 0;
         bool ok = true;
-        for (uint32_t t = pair; t < tiles; t += pairs) {
+        for (uint32_t t = pair; t < items; t += pairs) {
             uint32_t mt, nt;
-            tile_at(t, tiles_m, p.tiles_n, mt, nt);
+            const uint32_t share = t / tiles;
+            tile_at(t - share * tiles, tiles_m, p.tiles_n, mt, nt);
             const int second = kMode == kDw && mt >= static_cast<uint32_t>(p.tiles_m);
             if (second) mt -= p.tiles_m;
             const int64_t row0 = static_cast<int64_t>(mt) * 2 * kBM + rank * kBM + q * 32;
@@ -297,7 +312,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
                 }
-                if (rows > 0 && cols > 0) {
+                if (kMode == kDx && p.partial) {
+                    // (columns to the end of a group of four are there)
+                    float *to = p.partial + (static_cast<int64_t>(share) * p.rows + row0 + lane) * p.ld_partial + col0;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (lane < rows && i < cols) *reinterpret_cast<float4 *>(to + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else if (rows > 0 && cols > 0) {
                     T *y = static_cast<T *>(p.out[second]) + row0 * p.ld[second] + col0;
                     store_rows<T>(y, p.ld[second], rows, cols, p.wide_out[second], stage, lane, v);
                 }
@@ -317,6 +338,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_free<2>(tmem, 512u);
 }
 
+// The shares of a split sum, added up in order, four columns a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) join_shares_kernel(const float *partial, int64_t ld, int shares, int64_t rows, int64_t cols, T *out, int64_t ldo, int wide)
+{
+    after_previous();
+    let_next_start();
+    const int64_t per_row = ld / 4, at = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (at >= rows * per_row) return;
+    const int64_t row = at / per_row, col = (at - row * per_row) * 4;
+    const float *from = partial + row * ld + col;
+    float4 w[kMaxSplits], sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i)
+        if (i < shares) w[i] = __ldcg(reinterpret_cast<const float4 *>(from + i * rows * ld));
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i) {
+        if (i >= shares) break;
+        sum.x += w[i].x;
+        sum.y += w[i].y;
+        sum.z += w[i].z;
+        sum.w += w[i].w;
+    }
+    T *to = out + row * ldo + col;
+    if (wide && col + 4 <= cols) {
+        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
+    } else {
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < cols) to[e] = from_f32<T>(v[e]);
+    }
+}
+
+// How a product is cut: accumulator columns of a tile, and pairs that share a tile's steps.
+struct Cut {
+    int bn, splits;
+};
+
+// By the time of the rounds that the 76 pairs take over the items, in steps of a wide tile (0.27 us): a narrow tile's
+// step costs 3/4 of a wide one's (its operands are 3/4 of the bytes, and L2 feeds the tensor cores at their limit), an
+// item's end 8, and a split the second kernel's start (3 us) and the trip of its fp32 shares.
+Cut cut_of(int64_t rows, int64_t cols, int64_t out_cols, int64_t sections, int64_t steps, bool may_split)
+{
+    const int64_t pairs = kSms / 2;
+    Cut best{256, 1};
+    double least = 0.0;
+    for (int bn : {256, 128}) {
+        const int64_t width = out_cols * bn / 256, tiles = (rows + 255) / 256 * sections * ((cols + width - 1) / width);
+        for (int splits = 1; splits <= (may_split ? kMaxSplits : 1); ++splits) {
+            if (splits > 1 && steps / splits < 16) break;
+            const int64_t rounds = (tiles * splits + pairs - 1) / pairs;
+            double cost = static_cast<double>(rounds) * (static_cast<double>((steps + splits - 1) / splits) * (bn == 256 ? 1.0 : 0.75) + 8.0);
+            if (splits > 1) cost += 11.0 + static_cast<double>(splits) * rows * cols * 8.0 / 1.6e6;
+            if (least == 0.0 || cost < least) {
+                least = cost;
+                best = {bn, splits};
+            }
+        }
+    }
+    return best;
+}
+
+Cut cut_of_dx(int64_t m, int64_t n, int64_t k) { return cut_of(m, k, 256, 1, 2 * ((n + kBK - 1) / kBK), true); }
+
+int64_t partial_pitch(int64_t cols) { return (cols + 3) / 4 * 4; }
+
 template <int kMode, int kBN, typename T, int kAct>
 struct gemm_tag;
 
@@ -330,9 +417,9 @@ cudaError_t launch(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorM
     auto kernel = gated_gemm_kernel<kMode, kBN, T, kAct>;
     cudaError_t e = allow_shared<gemm_tag<kMode, kBN, T, kAct>>(kernel);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.sections * p.tiles_n;
-    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    const int64_t pairs = tiles < kSms / 2 ? tiles : kSms / 2;
+    const int64_t items = static_cast<int64_t>(p.tiles_m) * p.sections * p.tiles_n * p.splits;
+    if (items > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t pairs = items < kSms / 2 ? items : kSms / 2;
     return launch_after(kernel, dim3(static_cast<unsigned>(2 * pairs)), kThreads, C::SMEM, stream, 1, a0, a1, b0, b1, p);
 }
 
@@ -350,16 +437,16 @@ cudaError_t launch_gated_gemm(const convrot_gated_linear_args &a, cudaStream_t s
 {
     return with_16bit(a.dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
-        constexpr int kBN = 256;
+        const Cut cut = cut_of(a.m, a.n, 128, 1, (a.k + kBK - 1) / kBK, false);
         CUtensorMap x, wg, wu;
-        if (!matrix_map<T>(&x, a.x, a.m, a.k, a.ldx, kBM) || !matrix_map<T>(&wg, a.w_gate, a.n, a.k, a.ldw_gate, kBN / 2) ||
-            !matrix_map<T>(&wu, a.w_up, a.n, a.k, a.ldw_up, kBN / 2))
+        if (!matrix_map<T>(&x, a.x, a.m, a.k, a.ldx, kBM) || !matrix_map<T>(&wg, a.w_gate, a.n, a.k, a.ldw_gate, cut.bn / 2) ||
+            !matrix_map<T>(&wu, a.w_up, a.n, a.k, a.ldw_up, cut.bn / 2))
             return cudaErrorInvalidValue;
         Params p{};
         p.rows = static_cast<int32_t>(a.m);
         p.cols = static_cast<int32_t>(a.n);
         p.steps = static_cast<int32_t>((a.k + kBK - 1) / kBK);
-        p.parts = p.sections = 1;
+        p.parts = p.sections = p.splits = 1;
         p.out[0] = a.y;
         p.ld[0] = a.ldy;
         p.wide_out[0] = wide(a.y, a.ldy);
@@ -372,14 +459,24 @@ cudaError_t launch_gated_gemm(const convrot_gated_linear_args &a, cudaStream_t s
         p.bias[0] = a.b_gate;
         p.bias[1] = a.b_up;
         p.dev_status = a.dev_status;
-        if (a.act == CONVROT_ACT_SILU) return launch<kForward, kBN, T, 3>(x, x, wg, wu, p, stream);
-        if (a.act == CONVROT_ACT_GELU_TANH) return launch<kForward, kBN, T, 2>(x, x, wg, wu, p, stream);
-        if (a.act == CONVROT_ACT_GELU_ERF) return launch<kForward, kBN, T, 1>(x, x, wg, wu, p, stream);
-        return launch<kForward, kBN, T, 0>(x, x, wg, wu, p, stream);
+        auto run = [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
+            return cut.bn == 256 ? launch<kForward, 256, T, kAct>(x, x, wg, wu, p, stream) : launch<kForward, 128, T, kAct>(x, x, wg, wu, p, stream);
+        };
+        if (a.act == CONVROT_ACT_SILU) return run(std::integral_constant<int, 3>());
+        if (a.act == CONVROT_ACT_GELU_TANH) return run(std::integral_constant<int, 2>());
+        if (a.act == CONVROT_ACT_GELU_ERF) return run(std::integral_constant<int, 1>());
+        return run(std::integral_constant<int, 0>());
     });
 }
 
-cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, cudaStream_t stream)
+int64_t gated_dx_partial_bytes(int64_t m, int64_t n, int64_t k)
+{
+    const Cut cut = cut_of_dx(m, n, k);
+    return cut.splits > 1 ? cut.splits * m * partial_pitch(k) * 4 : 0;
+}
+
+cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const void *dg, const void *du, int64_t ldd, float *partial, cudaStream_t stream)
 {
     return with_16bit(a.dtype, [&](auto *tag) {
         using T = std::remove_pointer_t<decltype(tag)>;
@@ -397,7 +494,16 @@ cudaError_t launch_gated_dx(const convrot_gated_linear_backward_args &a, const v
         p.ld[0] = a.lddx;
         p.wide_out[0] = wide(a.dx, a.lddx);
         p.dev_status = a.dev_status;
-        return launch<kDx, 256, T, 0>(mg, mu, wg, wu, p, stream);
+        const Cut cut = cut_of_dx(a.m, a.n, a.k);
+        p.splits = cut.splits;
+        p.partial = cut.splits > 1 ? partial : nullptr;
+        p.ld_partial = partial_pitch(a.k);
+        const cudaError_t e = cut.bn == 256 ? launch<kDx, 256, T, 0>(mg, mu, wg, wu, p, stream) : launch<kDx, 128, T, 0>(mg, mu, wg, wu, p, stream);
+        if (e != cudaSuccess || cut.splits == 1) return e;
+        const int64_t threads = a.m * (p.ld_partial / 4);
+        return launch_after(join_shares_kernel<T>, dim3(static_cast<unsigned>((threads + 255) / 256)), 256, 0, stream, 1,
+                            static_cast<const float *>(partial), p.ld_partial, cut.splits, a.m, a.k, static_cast<T *>(a.dx), a.lddx,
+                            aligned_to(a.dx, 8) && a.lddx % 4 == 0);
     });
 }
 
@@ -413,7 +519,7 @@ cudaError_t launch_gated_dw(const convrot_gated_linear_backward_args &a, const v
         p.rows = static_cast<int32_t>(a.n);
         p.cols = static_cast<int32_t>(a.k);
         p.steps = static_cast<int32_t>((a.m + kBK - 1) / kBK);
-        p.parts = 1;
+        p.parts = p.splits = 1;
         p.sections = 2;
         p.out[0] = a.dw_gate;
         p.out[1] = a.dw_up;
@@ -422,14 +528,15 @@ cudaError_t launch_gated_dw(const convrot_gated_linear_backward_args &a, const v
         p.wide_out[0] = wide(a.dw_gate, a.lddw_gate);
         p.wide_out[1] = wide(a.dw_up, a.lddw_up);
         p.dev_status = a.dev_status;
-        return launch<kDw, 256, T, 0>(mg, mu, x, x, p, stream);
+        const Cut cut = cut_of(a.n, a.k, 256, 2, (a.m + kBK - 1) / kBK, false);
+        return cut.bn == 256 ? launch<kDw, 256, T, 0>(mg, mu, x, x, p, stream) : launch<kDw, 128, T, 0>(mg, mu, x, x, p, stream);
     });
 }
 
 int gated_gemm_shared(int form, int *columns)
 {
     *columns = 512;
-    return form == 0 ? Cfg<256>::SMEM : 0;
+    return form == 0 ? Cfg<256>::SMEM : form == 1 ? Cfg<128>::SMEM : 0;
 }
 
 }  // namespace convrot
