@@ -354,12 +354,10 @@ def convrot_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     act is ACT_SILU, ACT_GELU_ERF, ACT_GELU_TANH or ACT_NONE. With ``keep``, (y, gate, up): both projections too, rounded
     to x's type, as convrot_gated_linear_backward takes them. Rows that do not start on 16 bytes are copied in each call
     (``work``, uint8, is allocated here when not given)."""
-    m, n = x.shape[0], w_gate.shape[0]
-    if out is None:
-        out = _cr._empty((m, n), x.dtype, x.device, stream)
-    gate, up = (_cr._empty((m, n), x.dtype, x.device, stream) for _ in range(2)) if keep else (None, None)
-    _check(load().gated_linear(x, w_gate, w_up, b_gate, b_up, act, out, gate, up, work, dev_status, stream), "convrot_gated_linear")
-    return (out, gate, up) if keep else out
+    got = load().gated_linear(x, w_gate, w_up, b_gate, b_up, act, out, keep, work, dev_status, stream)
+    if isinstance(got, int):
+        raise ConvrotError(got, "convrot_gated_linear")
+    return got
 
 
 def convrot_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, gate: torch.Tensor,
@@ -388,14 +386,10 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: t
     mask [batch, keys' tokens] (bool or uint8) says which keys are there; a query without any has out 0 and lse -inf, and
     what stands at a masked key does not count, whatever it is. scale: head_dim^-0.5 by default. Each query attends to all
     keys that are there. ``work`` (uint8) is allocated here when not given."""
-    if q.dim() != 4:
-        raise TypeError("q must be [batch, tokens, heads, head_dim]")
-    if out is None:
-        out = _cr._empty(q.shape, q.dtype, q.device, stream)
-    lse = _cr._empty((q.shape[0], q.shape[2], q.shape[1]), torch.float32, q.device, stream)
-    _check(load().attention(q, k, v, mask, q.shape[-1]**-0.5 if scale is None else scale, out, lse, work, dev_status, stream),
-           "convrot_attention")
-    return out, lse
+    got = load().attention(q, k, v, mask, q.shape[-1]**-0.5 if scale is None else scale, out, work, dev_status, stream)
+    if isinstance(got, int):
+        raise ConvrotError(got, "convrot_attention")
+    return got
 
 
 def convrot_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,

@@ -638,10 +638,13 @@ PyObject *dict_of(std::initializer_list<std::pair<const char *, Tensor *>> all)
     return dict;
 }
 
-// (x, w_gate, w_up, b_gate, b_up, act, out, gate, up, work, dev_status, stream)
+// A new reference to what a call returns: the caller's own object, or the tensor that was made for it.
+PyObject *returned(PyObject *given, Tensor &fresh) { return given != Py_None ? Py_NewRef(given) : THPVariable_Wrap(std::move(fresh)); }
+
+// (x, w_gate, w_up, b_gate, b_up, act, out, keep, work, dev_status, stream) -> status, or y, or (y, gate, up)
 PyObject *gated_linear(PyObject *const *v, Py_ssize_t n)
 {
-    REQUIRE(count(n, 12));
+    REQUIRE(count(n, 11));
     const Tensor *x = tensor(v[0], "x"), *w = tensor(v[1], "w_gate");
     REQUIRE(x && w && one_device(v, n, *x));
     if (x->dim() != 2 || w->dim() != 2) {
@@ -653,15 +656,24 @@ PyObject *gated_linear(PyObject *const *v, Py_ssize_t n)
     a.m = x->size(0);
     a.k = x->size(1);
     a.n = w->size(0);
-    Matrix mx, mg, mu, my, kg, ku;
+    Matrix mx, mg, mu, my;
     const void *bg, *bu;
+    const int keep = PyObject_IsTrue(v[7]);
     cudaStream_t stream;
     REQUIRE(dtype_of(*x, "x", a.dtype) && matrix(v[0], "x", t, a.m, a.k, mx) && matrix(v[1], "w_gate", t, a.n, a.k, mg));
     REQUIRE(matrix(v[2], "w_up", t, a.n, a.k, mu) && vector(v[3], "b_gate", at::kFloat, a.n, &bg) && vector(v[4], "b_up", at::kFloat, a.n, &bu));
-    REQUIRE(integer(v[5], a.act) && matrix(v[6], "out", t, a.m, a.n, my) && optional_matrix(v[7], "gate", t, a.m, a.n, kg));
-    REQUIRE(optional_matrix(v[8], "up", t, a.m, a.n, ku) && workspace(v[9], &a.work, &a.work_bytes) && status_word(v[10], &a.dev_status));
-    REQUIRE(stream_of(v[11], *x, stream));
+    REQUIRE(integer(v[5], a.act) && optional_matrix(v[6], "out", t, a.m, a.n, my) && keep >= 0 && workspace(v[8], &a.work, &a.work_bytes));
+    REQUIRE(status_word(v[9], &a.dev_status) && stream_of(v[10], *x, stream));
     const DeviceOf device(*x);
+    Tensor y, gate, up;
+    {
+        Fresh fresh(stream, *x);
+        if (v[6] == Py_None) my = Matrix{(y = fresh({a.m, a.n}, t)).data_ptr(), a.n};
+        if (keep) {
+            a.gate = (gate = fresh({a.m, a.n}, t)).data_ptr();
+            a.up = (up = fresh({a.m, a.n}, t)).data_ptr();
+        }
+    }
     a.x = mx.p;
     a.ldx = mx.ld;
     a.w_gate = mg.p;
@@ -672,13 +684,14 @@ PyObject *gated_linear(PyObject *const *v, Py_ssize_t n)
     a.b_up = static_cast<const float *>(bu);
     a.y = my.p;
     a.ldy = my.ld;
-    a.gate = kg.p;
-    a.ldgate = kg.ld;
-    a.up = ku.p;
-    a.ldup = ku.ld;
+    a.ldgate = a.ldup = a.n;
     Workspace work;
-    own_work(a, v[9], work, convrot_gated_linear_work_bytes(&a), stream);
-    return status(convrot_gated_linear(&a, stream));
+    own_work(a, v[8], work, convrot_gated_linear_work_bytes(&a), stream);
+    const convrot_status st = convrot_gated_linear(&a, stream);
+    if (st != CONVROT_OK) return status(st);
+    PyObject *out = returned(v[6], y);
+    if (!keep || !out) return out;
+    return Py_BuildValue("(NNN)", out, THPVariable_Wrap(std::move(gate)), THPVariable_Wrap(std::move(up)));
 }
 
 // (x, w_gate, w_up, gate, up, dy, act, dx wanted, weights' wanted, biases' wanted, work, dev_status, stream) -> status, or the
@@ -781,32 +794,46 @@ bool attention_inputs(A &a, PyObject *q, PyObject *k, PyObject *v, PyObject *mas
     return real(scale, a.scale);
 }
 
-// (q, k, v, mask, scale, out, lse, work, dev_status, stream)
+// (q, k, v, mask, scale, out, work, dev_status, stream) -> status, or (out, lse)
 PyObject *attention(PyObject *const *v, Py_ssize_t n)
 {
-    REQUIRE(count(n, 10));
-    const Tensor *q = tensor(v[0], "q"), *lse = tensor(v[6], "lse");
-    REQUIRE(q && lse && one_device(v, n, *q));
+    REQUIRE(count(n, 9));
+    const Tensor *q = tensor(v[0], "q");
+    REQUIRE(q && one_device(v, n, *q));
     convrot_attention_args a{};
-    void *out;
+    void *out = nullptr;
     int64_t tokens, heads;
     cudaStream_t stream;
-    REQUIRE(attention_inputs(a, v[0], v[1], v[2], v[3], v[4], *q) && states(v[5], "out", *q, &out, tokens, heads, a.out_strides));
+    REQUIRE(attention_inputs(a, v[0], v[1], v[2], v[3], v[4], *q));
+    if (v[5] == Py_None) {
+        tokens = a.q_tokens;
+        heads = a.q_heads;
+        a.out_strides[2] = a.head_dim;
+        a.out_strides[1] = heads * a.head_dim;
+        a.out_strides[0] = tokens * a.out_strides[1];
+    } else {
+        REQUIRE(states(v[5], "out", *q, &out, tokens, heads, a.out_strides));
+    }
     if (tokens != a.q_tokens || heads != a.q_heads) {
         raise(PyExc_ValueError, "out", "must have q's shape");
         return nullptr;
     }
-    if (lse->scalar_type() != at::kFloat || !lse->is_contiguous() || lse->sizes() != at::IntArrayRef({a.batch, a.q_heads, a.q_tokens})) {
-        raise(PyExc_ValueError, "lse", "must be a contiguous float32 tensor [batch, heads, tokens]");
-        return nullptr;
-    }
-    REQUIRE(workspace(v[7], &a.work, &a.work_bytes) && status_word(v[8], &a.dev_status) && stream_of(v[9], *q, stream));
+    REQUIRE(workspace(v[6], &a.work, &a.work_bytes) && status_word(v[7], &a.dev_status) && stream_of(v[8], *q, stream));
     const DeviceOf device(*q);
+    Tensor new_out, lse;
+    {
+        Fresh fresh(stream, *q);
+        if (v[5] == Py_None) out = (new_out = fresh(q->sizes(), q->scalar_type())).data_ptr();
+        lse = fresh({a.batch, a.q_heads, a.q_tokens}, at::kFloat);
+    }
     a.out = out;
-    a.lse = static_cast<float *>(lse->data_ptr());
+    a.lse = static_cast<float *>(lse.data_ptr());
     Workspace work;
-    own_work(a, v[7], work, convrot_attention_work_bytes(&a), stream);
-    return status(convrot_attention(&a, stream));
+    own_work(a, v[6], work, convrot_attention_work_bytes(&a), stream);
+    const convrot_status st = convrot_attention(&a, stream);
+    if (st != CONVROT_OK) return status(st);
+    PyObject *result = returned(v[5], new_out);
+    return result ? Py_BuildValue("(NN)", result, THPVariable_Wrap(std::move(lse))) : nullptr;
 }
 
 // (q, k, v, out, lse, dout, mask, scale, work, dev_status, stream) -> status, or the dict of gradients

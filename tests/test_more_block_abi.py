@@ -5,6 +5,7 @@ import itertools
 import os
 import struct
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -13,6 +14,7 @@ from int8_hadamard_rotated_convrot_gb300 import block as bl
 from int8_hadamard_rotated_convrot_gb300 import build as cbuild
 from int8_hadamard_rotated_convrot_gb300 import convrot as cr
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 FAKE = 0x10000  # aligned and never dereferenced on these paths
 
 # the argument structs of include/convrot_block.h, field by field
@@ -205,6 +207,38 @@ def test_binding_refuses(lib):
                 (ValueError, lambda: bl.convrot_attention_backward(q, k, k, q, lse, k))]:
             with pytest.raises(error):
                 call()
+
+
+# calls with tensors that have no memory of their own, each in a process: plain ones, and the slices that vmap hands out
+WITHOUT_MEMORY = """
+import sys, torch
+from torch._subclasses import FakeTensorMode
+from int8_hadamard_rotated_convrot_gb300 import block as bl
+name, batched = sys.argv[1], sys.argv[2] == "vmap"
+with FakeTensorMode():
+    like = dict(device="cuda", dtype=torch.bfloat16)
+    x, w, q, lse = torch.empty(4, 64, **like), torch.empty(32, 64, **like), torch.empty(2, 4, 2, 16, **like), torch.empty(2, 2, 4, device="cuda")
+    y = torch.empty(4, 32, **like)
+    call = {
+        "gated": lambda t: bl.convrot_gated_linear(t, w, w),
+        "gated out": lambda t: bl.convrot_gated_linear(t, w, w, keep=True, out=y)[1],
+        "gated gradient": lambda t: bl.convrot_gated_linear_backward(t, w, w, y, y, y)["dx"],
+        "attention": lambda t: bl.convrot_attention(t.view(2, 2, 2, 32), t.view(2, 2, 2, 32), t.view(2, 2, 2, 32))[0],
+        "attention out": lambda t: bl.convrot_attention(q, q, q, out=t.view(2, 4, 2, 16))[0],
+        "attention gradient": lambda t: bl.convrot_attention_backward(q, q, q, q, lse, t.view(2, 4, 2, 16))["dq"],
+    }[name]
+    try:
+        torch.vmap(call)(torch.empty(3, 4, 64, **like)) if batched else call(x)
+    except Exception as e:
+        print("raised", type(e).__name__)
+"""
+
+
+@pytest.mark.parametrize("how", ["plain", "vmap"])
+@pytest.mark.parametrize("name", ["gated", "gated out", "gated gradient", "attention", "attention out", "attention gradient"])
+def test_tensors_without_memory_raise(lib, name, how):
+    r = subprocess.run([sys.executable, "-c", WITHOUT_MEMORY, name, how], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("raised"), r.stdout + r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- tensor memory
