@@ -55,8 +55,33 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const HeadsMap &m, int t
         tma_load_4d(dst + i * kTileBox, &m.map, i * kBoxElems, token, head * m.head_step, batch * m.batch_step, bar);
 }
 
-// A tile as an operand with K along the head's elements: the step to elements 16 i .. 16 i + 15.
-__device__ __forceinline__ uint64_t tile_step_k(uint64_t desc, int i) { return desc + (i / 4) * (kTileBox >> 4) + (i % 4) * kStepK; }
+// D [128 x 128] = rows of one tile by rows of another, over `steps` times 16 of the head's kD elements.
+template <int kD>
+__device__ __forceinline__ void tile_product(uint32_t d, uint32_t rows, uint32_t cols, uint32_t id, int steps)
+{
+    const Desc a(desc_k(rows)), b(desc_k(cols));
+#pragma unroll
+    for (int kk = 0; kk < kD / kMmaK; ++kk) {
+        const uint32_t at = (kk / 4) * (kTileBox >> 4) + (kk % 4) * kStepK;
+        if (kk >= steps) break;
+        if (kk == 0)
+            mma_ss_step<false>(d, a, at, b, at, id);
+        else
+            mma_ss_step<true>(d, a, at, b, at, id);
+    }
+}
+
+// sums (+)= a 16-bit [128 x 128] matrix in tensor memory, its halves of K 64 columns apart, by a tile's rows.
+__device__ __forceinline__ void tile_add(uint32_t sums, uint32_t a, uint32_t tile, uint32_t id, bool fresh)
+{
+    const Desc b(desc_mn(tile, kTileBox));
+    if (fresh)
+        mma_ts_step<false>(sums, a, b, 0, id);
+    else
+        mma_ts_step<true>(sums, a, b, 0, id);
+#pragma unroll
+    for (int kk = 1; kk < 128 / kMmaK; ++kk) mma_ts_step<true>(sums, a + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b, kStepMN * kk, id);
+}
 
 // float16 has 40 binary orders of magnitude, and gradients may be small: the backward pass takes P 2^15 times as large
 // (at most 2^15), and dS by a power of two that brings the largest |dout| of a head to 2^-3 .. 2^-2, both exact and taken back

@@ -8,10 +8,11 @@
 //   warp 0       TMA producer: the groups' queries, then the tiles of 128 keys
 //                and values in turn, through one ring
 //   warp 1       tensor memory; one thread issues the MMAs
-//   warps 4-7    the first group's softmax, a row a thread; warps 8-11 the second's
-// Tensor memory: for each group 128 columns of S = Q K^T, whose first half then
-// holds P (16 bits, the A operand of P V, so that P never passes through shared
-// memory), and the sums O.
+//   warps 4-11   the first group's softmax, warps 12-19 the second's: two threads a
+//                row, 64 of the tile's keys each
+// Tensor memory: for each group 128 columns of S = Q K^T, whose halves' first
+// halves then hold P (16 bits, the A operand of P V, so that P never passes
+// through shared memory), and the sums O.
 //
 // The maximum is a reference only: O and the sum are rescaled when a row's
 // maximum has grown by more than 2^8 since, which is rare after the first tile
@@ -26,11 +27,13 @@ namespace {
 using namespace mma16;
 
 constexpr int kGroupRows = 128, kItemRows = 2 * kGroupRows;
-constexpr int kThreads = 384;
-// Registers a thread: launched at 168, warpgroup 0 leaves most of its own to the softmax:
-// 4 x 32 x 80 + 8 x 32 x 208 <= 384 x 168.
-constexpr int kRegsWg0 = 80, kRegsSoftmax = 208;
-static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsSoftmax <= kThreads * 168, "register split");
+constexpr int kSoftmaxWarps = 16, kThreads = 128 + 32 * kSoftmaxWarps;
+// Registers a thread: launched at 96, warpgroup 0 leaves some of its own to the softmax:
+// 4 x 32 x 64 + 16 x 32 x 104 = 640 x 96.
+constexpr int kRegsWg0 = 64, kRegsSoftmax = 104;
+static_assert(4 * 32 * kRegsWg0 + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * 96, "register split");
+constexpr int kHalfKeys = kTileKeys / 2;
+constexpr int kStageRows = 16, kWarpStage = kStageRows * kStagePitch;  // of a warp's staged outputs
 constexpr float kGrow = 8.0f;  // log2 of what a row's probabilities may grow to before O is rescaled
 
 template <int kD>
@@ -39,7 +42,8 @@ struct Cfg {
     static constexpr int STAGES = kD == 64 ? 8 : 4;
     static constexpr int BARS = 2 * STAGES + 2 * 5 + 1;
     static constexpr int BAR_BYTES = 256;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + 8 * kStageBytes + BAR_BYTES;
+    static constexpr int MEET = 2 * 2 * 4 * 2 * 32 * 4;  // maxima of the two threads of a row: in turn, group, quadrant, half
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + kSoftmaxWarps * kWarpStage + MEET + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 g and + kD g
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + 8 * kStageBytes;
+    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kMeet = kOut + kSoftmaxWarps * kWarpStage, kBars = kMeet + C::MEET;
     const uint32_t bars = base + kBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -79,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 10);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             mbar_init(q_full(g), 1);
             mbar_init(q_empty(g), 1);
             mbar_init(s_full(g), 1);
-            mbar_init(p_ready(g), 4);
+            mbar_init(p_ready(g), 8);
             mbar_init(o_full(g), 1);
         }
         mbar_init(done_bar, 1);
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int g = 0; g < 2; ++g)
                     if (armed >> (16 + g) & 1u) mbar_wait(q_full(g), q_phase[g] ^ 1u);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             const uint32_t kIdS = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
@@ -182,109 +186,113 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 }
             };
             auto scores = [&](int g, int at) {  // S = Q K^T
-                const uint64_t a = desc_k(base + g * C::TILE), b = desc_k(base + kRing + at * C::TILE);
-                const uint32_t s = tmem + C::S_COL + 128 * g;
-                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(s, tile_step_k(a, kk), tile_step_k(b, kk), kIdS, kk > 0 ? 1u : 0u);
+                tile_product<kD>(tmem + C::S_COL + 128 * g, base + g * C::TILE, base + kRing + at * C::TILE, kIdS, steps);
                 mma_commit(s_full(g));
             };
             for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
-                if (!wait(full_bar(stage), phase)) {
-                    ok = false;
-                    break;
-                }
-                for (int g = 0; g < it.groups; ++g) {
-                    if (!wait(q_full(g), q_phase[g])) {
-                        ok = false;
-                        break;
-                    }
+                if (!(ok = wait.together(full_bar(stage), phase))) break;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g >= it.groups) break;
+                    if (!(ok = wait.together(q_full(g), q_phase[g]))) break;
                     q_phase[g] ^= 1u;
                     tc_fence_after();
-                    scores(g, stage);
-                    if (it.tiles == 1) mma_commit(q_empty(g));
+                    if (one_thread()) {
+                        scores(g, stage);
+                        if (it.tiles == 1) mma_commit(q_empty(g));
+                        if (g + 1 == it.groups) mma_commit(empty_bar(stage));
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
-                mma_commit(empty_bar(stage));
                 next();
                 for (int j = 0; j < it.tiles; ++j) {
                     const int v_stage = stage;
                     const bool last = j + 1 == it.tiles;
-                    if (!wait(full_bar(stage), phase)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(ok = wait.together(full_bar(stage), phase))) break;
                     next();
-                    if (!last && !wait(full_bar(stage), phase)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int g = 0; g < it.groups; ++g) {
-                        if (!wait(p_ready(g), p_phase[g])) {
-                            ok = false;
-                            break;
-                        }
+                    if (!last && !(ok = wait.together(full_bar(stage), phase))) break;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (g >= it.groups) break;
+                        if (!(ok = wait.together(p_ready(g), p_phase[g]))) break;
                         p_phase[g] ^= 1u;
                         tc_fence_after();
-                        const uint64_t b = desc_mn(base + kRing + v_stage * C::TILE, kTileBox);
-                        const uint32_t o = tmem + C::O_COL + kD * g, a = tmem + C::S_COL + 128 * g;
-#pragma unroll
-                        for (int kk = 0; kk < kTileKeys / kMmaK; ++kk)
-                            mma_ts(o, a + kk * (kMmaK / 2), b + kStepMN * kk, id_o, j > 0 || kk > 0 ? 1u : 0u);
-                        if (last) {
-                            mma_commit(o_full(g));
-                        } else {
-                            scores(g, stage);
-                            if (j + 2 == it.tiles) mma_commit(q_empty(g));
+                        if (one_thread()) {
+                            tile_add(tmem + C::O_COL + kD * g, tmem + C::S_COL + 128 * g, base + kRing + v_stage * C::TILE, id_o, j == 0);
+                            if (last) {
+                                mma_commit(o_full(g));
+                            } else {
+                                scores(g, stage);
+                                if (j + 2 == it.tiles) mma_commit(q_empty(g));
+                            }
+                            if (g + 1 == it.groups) {
+                                mma_commit(empty_bar(v_stage));
+                                if (!last) mma_commit(empty_bar(stage));
+                            }
                         }
+                        __syncwarp();
                     }
                     if (!ok) break;
-                    mma_commit(empty_bar(v_stage));
-                    if (!last) {
-                        mma_commit(empty_bar(stage));
-                        next();
-                    }
+                    if (!last) next();
                 }
             }
             if (!ok) wait.fail();
-            mma_commit(done_bar);
-            mbar_wait(done_bar, 0);
+            if (one_thread()) {
+                mma_commit(done_bar);
+                mbar_wait(done_bar, 0);
+            }
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        const int g = (warp - 4) >> 2, quad = warp & 3;
+        const int g = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, quad = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t s_at = lanes + C::S_COL + 128 * g, o_at = lanes + C::O_COL + kD * g;
-        const uint32_t stage = base + kOut + (warp - 4) * kStageBytes;
+        const uint32_t s_at = lanes + C::S_COL + 128 * g + kHalfKeys * half, o_at = lanes + C::O_COL + kD * g;
+        const uint32_t stage = base + kOut + (warp - 4) * kWarpStage;
         const float c = p.scale_log2;
+        // What this thread and the one with the row's other keys tell each other. A warp whose wait ran out says so at the
+        // next meeting (kGone, a NaN that no arithmetic gives), and both leave there: neither waits for one that has left.
+        constexpr uint32_t kGone = 0x7fabcdefu;
+        float *meet = reinterpret_cast<float *>(gbase + kMeet) + ((g * 4 + quad) * 2) * 32 + lane;
+        constexpr int kTurn = 2 * 4 * 2 * 32;
+        bool ok = true, gone = false;
+        int turn = 0;  // a place is written again only after the other thread came to the meeting in between
+        auto other = [&](float mine) {
+            meet[turn * kTurn + half * 32] = ok ? mine : __uint_as_float(kGone);
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + g * 4 + quad) : "memory");
+            const float theirs = *reinterpret_cast<volatile float *>(&meet[turn * kTurn + (half ^ 1) * 32]);
+            gone = !ok || __float_as_uint(theirs) == kGone;
+            turn ^= 1;
+            return theirs;
+        };
         uint32_t s_phase = 0, o_phase = 0;
-        bool ok = true;
-        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        for (int i = blockIdx.x; i < p.items && !gone; i += gridDim.x) {
             const Item it = item_at(i);
             if (g >= it.groups) continue;
-            float top = neg_inf(), sum = 0.0f;  // the reference, and the sum of 2^(c (s - top) + kShift)
+            float top = neg_inf(), sum = 0.0f;  // the reference, and this thread's sum of 2^(c (s - top) + kShift)
             for (int j = 0; j < it.tiles; ++j) {
-                if (!wait(s_full(g), s_phase)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, ok && wait(s_full(g), s_phase));
                 s_phase ^= 1u;
                 tc_fence_after();
-                uint32_t r[kTileKeys];
+                uint32_t r[kHalfKeys];
 #pragma unroll
-                for (int k = 0; k < kTileKeys; k += 32) tmem_ld32_async(s_at + k, r + k);
+                for (int k = 0; k < kHalfKeys; k += 32) tmem_ld32_async(s_at + k, r + k);
                 tmem_ld_wait(r);
-                const int keys = it.keys - j * kTileKeys;
-                if (keys < kTileKeys) {
+                const int keys = it.keys - j * kTileKeys - half * kHalfKeys;
+                if (keys < kHalfKeys) {
 #pragma unroll
-                    for (int k = 0; k < kTileKeys; ++k)
+                    for (int k = 0; k < kHalfKeys; ++k)
                         if (k >= keys) r[k] = 0xff800000u;
                 }
                 float m[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-                for (int k = 0; k < kTileKeys; ++k) m[k % 4] = fmaxf(m[k % 4], __uint_as_float(r[k]));
-                const float now = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                for (int k = 0; k < kHalfKeys; ++k) m[k % 4] = fmaxf(m[k % 4], __uint_as_float(r[k]));
+                const float mine = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                const float now = fmaxf(mine, other(mine));
+                if (gone) break;
                 if (j == 0) {
                     top = now;
                 } else if (__any_sync(0xffffffffu, (now - top) * c > kGrow)) {
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     top = next;
                     sum *= factor;
 #pragma unroll 1
-                    for (int k = 0; k < p.d; k += 16) {
+                    for (int k = half * 16; k < p.d; k += 32) {
                         uint32_t o[16];
                         tmem_ld16_async(o_at + k, o);
                         tmem_ld_wait(o);
@@ -306,39 +314,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 const float off = top == neg_inf() ? 0.0f : kShift - top * c;
                 const F2 c2(c), off2(off);
                 F2 add[2] = {F2(0.0f), F2(0.0f)};
-                uint32_t pk[kTileKeys / 2];
 #pragma unroll
-                for (int k = 0; k < kTileKeys; k += 2) {
-                    const F2 x = fma2(F2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, off2);
-                    const F2 e(ex2(x.lo()), ex2(x.hi()));
-                    add[k / 2 % 2] = add[k / 2 % 2] + e;
-                    pk[k / 2] = pack2<T>(e.lo(), e.hi());
+                for (int k0 = 0; k0 < kHalfKeys; k0 += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const F2 x = fma2(F2(__uint_as_float(r[k0 + k]), __uint_as_float(r[k0 + k + 1])), c2, off2);
+                        const F2 e(ex2(x.lo()), ex2(x.hi()));
+                        add[k / 2 % 2] = add[k / 2 % 2] + e;
+                        pk[k / 2] = pack2<T>(e.lo(), e.hi());
+                    }
+                    tmem_st16(s_at + k0 / 2, pk);
                 }
                 sum += add[0].sum() + add[1].sum();
-                tmem_st32(s_at, pk);
-                tmem_st32(s_at + 32, pk + 32);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready(g));
             }
-            if (!ok) break;
+            if (gone) break;
             const int row0 = it.q0 + g * kGroupRows + quad * 32, rows = p.q_tokens - row0 < 32 ? p.q_tokens - row0 : 32;
+            const float theirs = other(sum);
+            if (gone) break;
+            sum = half == 0 ? sum + theirs : theirs + sum;
             const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
-            if (lane < rows)
+            if (half == 0 && lane < rows)
                 p.lse[(static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane] =
                     sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
             T *out = static_cast<T *>(p.out) + it.b * p.out_strides[0] + row0 * p.out_strides[1] + it.h * p.out_strides[2];
             if (it.tiles > 0) {
-                if (!wait(o_full(g), o_phase)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, wait(o_full(g), o_phase));
                 o_phase ^= 1u;
                 tc_fence_after();
             }
 #pragma unroll 1
-            for (int k = 0; k < p.d; k += 32) {
+            for (int k = half * 32; k < p.d; k += 64) {
                 uint32_t o[32];
                 float v[32];
                 if (it.tiles > 0) {
@@ -350,7 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
                 }
-                if (rows > 0) store_rows<T>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+                if (rows > 0 && ok)
+                    store_rows<T, kStageRows>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
             }
             tc_fence_before();  // O is read before the next item's first P is announced
         }

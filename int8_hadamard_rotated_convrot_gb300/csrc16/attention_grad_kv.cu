@@ -205,17 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
             int stage = 0;
             uint32_t phase = 0, kv_phase = 0, p_phase = 0, ds_phase = 0;
-            auto product = [&](uint32_t to, uint32_t rows, uint32_t cols) {
-                const uint64_t a = desc_k(rows), b = desc_k(cols);
-                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(to, tile_step_k(a, kk), tile_step_k(b, kk), id_s, kk > 0 ? 1u : 0u);
-            };
+            auto product = [&](uint32_t to, uint32_t rows, uint32_t cols) { tile_product<kD>(to, rows, cols, id_s, steps); };
             // sums += (what a region's halves hold in 16 bits) x a tile, over the queries
-            auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) {
-                const uint64_t b = desc_mn(tile, kTileBox);
-#pragma unroll
-                for (int kk = 0; kk < kTileQueries / kMmaK; ++kk)
-                    mma_ts(sums, region + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b + kStepMN * kk, id_o, !fresh || kk > 0 ? 1u : 0u);
-            };
+            auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) { tile_add(sums, region, tile, id_o, fresh); };
             const bool ok = each_unit([&](const Unit &, int t0, int t1) {
                 if (!wait(kv_full, kv_phase) || !wait(full_bar(stage), phase)) return false;
                 kv_phase ^= 1u;

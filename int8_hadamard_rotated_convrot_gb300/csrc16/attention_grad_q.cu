@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 return at;
             };
             auto product = [&](uint32_t to, uint32_t rows, int at) {  // rows of the item by a tile, over the head's elements
-                const uint64_t a = desc_k(rows), b = desc_k(base + kRing + at * C::TILE);
-                for (int kk = 0; kk < steps; ++kk) mma_ss<1>(to, tile_step_k(a, kk), tile_step_k(b, kk), id_s, kk > 0 ? 1u : 0u);
+                tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps);
             };
             for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
                 const Item it = item_at(i);
@@ -204,10 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     }
                     ds_phase ^= 1u;
                     tc_fence_after();
-                    const uint64_t b = desc_mn(base + kRing + k_at * C::TILE, kTileBox);
-#pragma unroll
-                    for (int kk = 0; kk < kTileKeys / kMmaK; ++kk)  // each half of the keys has its own half of dP's columns
-                        mma_ts(tmem + C::DQ_COL, tmem + C::DP_COL + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b + kStepMN * kk, id_o, j > 0 || kk > 0 ? 1u : 0u);
+                    // (each half of the keys has its own half of dP's columns)
+                    tile_add(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
                     mma_commit(empty_bar(k_at));
                     if (last) {
                         mma_commit(dq_full);

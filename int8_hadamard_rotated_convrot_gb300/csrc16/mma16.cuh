@@ -64,6 +64,49 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  : "memory");
 }
 
+// The same as parts of a longer sum, for tiles of 128 x 128, whose issue counts: an instruction takes the tensor cores 64
+// cycles, and one thread that computes its operands in a branch of its own took 80 to 140 for its issue. So the issuing
+// warp stays together up to the instruction itself (one_thread), which lets its operands live in uniform registers; the
+// flag is an immediate, the descriptor's upper half is fixed, and the loops that call these are unrolled.
+__device__ __forceinline__ bool one_thread()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+// The number of this thread's warp, the same for all its lanes as far as the compiler sees.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+};
+
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_ss_step(uint32_t d, Desc a, uint32_t a_step, Desc b, uint32_t b_step, uint32_t id)
+{
+    if constexpr (kAccumulate)
+        asm volatile("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t}" ::"r"(d), "r"(a.lo + a_step), "r"(a.hi), "r"(b.lo + b_step), "r"(b.hi), "r"(id)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 0;\n\t}" ::"r"(d), "r"(a.lo + a_step), "r"(a.hi), "r"(b.lo + b_step), "r"(b.hi), "r"(id)
+                     : "memory");
+}
+
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_ts_step(uint32_t d, uint32_t a, Desc b, uint32_t b_step, uint32_t id)
+{
+    if constexpr (kAccumulate)
+        asm volatile("{\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, 1;\n\t}" ::"r"(d), "r"(a), "r"(b.lo + b_step), "r"(b.hi), "r"(id)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .b64 b;\n\tmov.b64 b, {%2, %3};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, 0;\n\t}" ::"r"(d), "r"(a), "r"(b.lo + b_step), "r"(b.hi), "r"(id)
+                     : "memory");
+}
+
 // All of an SM's columns, or a part (a multiple of 128): a launch asks for the
 // shared memory that goes with them (tc_common.cuh).
 template <int kGroup>
@@ -221,6 +264,8 @@ struct Waits {
             if (*abort_flag || globaltimer() - t0 > kTimeoutNs) return false;
         }
     }
+    // by a whole warp: true for all lanes or for none
+    __device__ __forceinline__ bool together(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, (*this)(bar, parity)); }
     __device__ __forceinline__ void fail() const
     {
         *abort_flag = 1;
@@ -231,37 +276,43 @@ struct Waits {
 __device__ __forceinline__ int64_t load_i32(const int32_t *p) { return *reinterpret_cast<const volatile int32_t *>(p); }
 
 // One warp's 32 rows (lane: row) of 32 values each, rounded to T and stored:
-// staged in shared memory (`stage`, 32 x 80 bytes of this warp's own: 16-byte
-// accesses of eight rows meet all banks) and written four lanes a row, 64 bytes
-// of each. `rows` and `cols` of them exist; wide: rows start on 16 bytes; with
+// staged in shared memory (`stage`, kStageRows x 80 bytes of this warp's own:
+// 16-byte accesses of eight rows meet all banks) and written four lanes a row,
+// 64 bytes of each. `rows` and `cols` of them exist; wide: rows start on 16 bytes; with
 // an index, row r goes to y's row index[r].
 constexpr int kStagePitch = 80, kStageBytes = 32 * kStagePitch;
 
-template <typename T>
+template <typename T, int kStageRows = 32>
 __device__ __forceinline__ void store_rows(T *y, int64_t ld, int rows, int cols, bool wide, uint32_t stage, int lane, const float (&v)[32],
                                            const int32_t *index = nullptr)
 {
-    static_assert(sizeof(T) == 2);
-    __syncwarp();  // the last box has been read
+    static_assert(sizeof(T) == 2 && 32 % kStageRows == 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * kStagePitch + 16 * i), "r"(pack2<T>(v[8 * i], v[8 * i + 1])),
-                     "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])), "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
-                     : "memory");
-    __syncwarp();
-    if (wide && cols >= 32) {
+    for (int first = 0; first < 32; first += kStageRows) {
+        __syncwarp();  // the last box has been read
+        if (lane / kStageRows * kStageRows == first) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 8 + lane / 4;
-            const uint4 u = shared16(stage + r * kStagePitch + lane % 4 * 16);
-            if (r < rows) *(reinterpret_cast<uint4 *>(y + (index ? load_i32(index + r) : r) * ld) + lane % 4) = u;
+            for (int i = 0; i < 4; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane % kStageRows * kStagePitch + 16 * i),
+                             "r"(pack2<T>(v[8 * i], v[8 * i + 1])), "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])),
+                             "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
+                             : "memory");
         }
-    } else if (lane < cols) {
+        __syncwarp();
+        if (wide && cols >= 32) {
+#pragma unroll
+            for (int i = 0; i < kStageRows / 8; ++i) {
+                const int at = i * 8 + lane / 4, r = first + at;
+                const uint4 u = shared16(stage + at * kStagePitch + lane % 4 * 16);
+                if (r < rows) *(reinterpret_cast<uint4 *>(y + (index ? load_i32(index + r) : r) * ld) + lane % 4) = u;
+            }
+        } else if (lane < cols) {
 #pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-            unsigned short u;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(stage + r * kStagePitch + lane * 2) : "memory");
-            reinterpret_cast<unsigned short *>(y)[(index ? load_i32(index + r) : r) * ld + lane] = u;
+            for (int at = 0; at < kStageRows && first + at < rows; ++at) {
+                unsigned short u;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(stage + at * kStagePitch + lane * 2) : "memory");
+                reinterpret_cast<unsigned short *>(y)[(index ? load_i32(index + first + at) : first + at) * ld + lane] = u;
+            }
         }
     }
 }
