@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
     const uint32_t sums_full = kv_full + 48, done_bar = kv_full + 56;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
                 if (armed >> 16) mbar_wait(kv_full, kv_phase ^ 1u);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             const uint32_t id_s = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
@@ -209,14 +209,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             // sums += (what a region's halves hold in 16 bits) x a tile, over the queries
             auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) { tile_add(sums, region, tile, id_o, fresh); };
             const bool ok = each_unit([&](const Unit &, int t0, int t1) {
-                if (!wait(kv_full, kv_phase) || !wait(full_bar(stage), phase)) return false;
+                if (!wait.together(kv_full, kv_phase) || !wait.together(full_bar(stage), phase)) return false;
                 kv_phase ^= 1u;
                 tc_fence_after();
                 uint32_t at = base + kRing + stage * C::STAGE;
-                product(tmem + C::S_COL, base, at);
-                mma_commit(s_full);
-                product(tmem + C::DP_COL, base + C::TILE, at + C::TILE);
-                mma_commit(dp_full);
+                if (one_thread()) {
+                    product(tmem + C::S_COL, base, at);
+                    mma_commit(s_full);
+                    product(tmem + C::DP_COL, base + C::TILE, at + C::TILE);
+                    mma_commit(dp_full);
+                }
+                __syncwarp();
                 for (int t = t0; t < t1; ++t) {
                     const bool more = t + 1 < t1;
                     const int here = stage;
@@ -225,35 +228,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                         phase ^= 1u;
                     }
                     const uint32_t next = base + kRing + stage * C::STAGE;
-                    if (!wait(p_ready, p_phase)) return false;
+                    if ((more && !wait.together(full_bar(stage), phase)) || !wait.together(p_ready, p_phase)) return false;
                     p_phase ^= 1u;
                     tc_fence_after();
-                    add(tmem + C::DV_COL, tmem + C::S_COL, at + C::TILE, t == t0);
-                    if (more) {
-                        if (!wait(full_bar(stage), phase)) return false;
-                        tc_fence_after();
-                        product(tmem + C::S_COL, base, next);
-                        mma_commit(s_full);
+                    if (one_thread()) {
+                        add(tmem + C::DV_COL, tmem + C::S_COL, at + C::TILE, t == t0);
+                        if (more) {
+                            product(tmem + C::S_COL, base, next);
+                            mma_commit(s_full);
+                        }
                     }
-                    if (!wait(ds_ready, ds_phase)) return false;
+                    __syncwarp();
+                    if (!wait.together(ds_ready, ds_phase)) return false;
                     ds_phase ^= 1u;
                     tc_fence_after();
-                    add(tmem + C::DK_COL, tmem + C::DP_COL, at, t == t0);
-                    mma_commit(empty_bar(here));
-                    if (more) {
-                        product(tmem + C::DP_COL, base + C::TILE, next + C::TILE);
-                        mma_commit(dp_full);
-                    } else {
-                        mma_commit(kv_empty);
-                        mma_commit(sums_full);
+                    if (one_thread()) {
+                        add(tmem + C::DK_COL, tmem + C::DP_COL, at, t == t0);
+                        mma_commit(empty_bar(here));
+                        if (more) {
+                            product(tmem + C::DP_COL, base + C::TILE, next + C::TILE);
+                            mma_commit(dp_full);
+                        } else {
+                            mma_commit(kv_empty);
+                            mma_commit(sums_full);
+                        }
                     }
+                    __syncwarp();
                     at = next;
                 }
                 return true;
             });
             if (!ok) wait.fail();
-            mma_commit(done_bar);
-            mbar_wait(done_bar, 0);
+            if (one_thread()) {
+                mma_commit(done_bar);
+                mbar_wait(done_bar, 0);
+            }
         }
         __syncwarp();
     } else {

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
                 if (armed >> 16) mbar_wait(q_full, q_phase ^ 1u);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             const uint32_t id_s = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
@@ -159,72 +159,69 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             uint32_t phase = 0, q_phase = 0, ds_phase = 0;
             int tile_no = 0;  // over all items: which of the two S
             bool ok = true;
-            auto take = [&]() {  // the next stage of the ring, once it is there
-                if (!wait(full_bar(stage), phase)) return -1;
-                const int at = stage;
+            auto take = [&](int &at) {  // the next stage of the ring, once it is there
+                ok = wait.together(full_bar(stage), phase);
+                at = stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                return at;
+                return ok;
             };
-            auto product = [&](uint32_t to, uint32_t rows, int at) {  // rows of the item by a tile, over the head's elements
-                tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps);
-            };
+            // rows of the item by a tile, over the head's elements
+            auto product = [&](uint32_t to, uint32_t rows, int at) { tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps); };
             for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
                 int k_at, v_at, k_next = 0;
-                if (!wait(q_full, q_phase) || (k_at = take()) < 0 || (v_at = take()) < 0) {
-                    ok = false;
-                    break;
-                }
+                if (!(ok = wait.together(q_full, q_phase)) || !take(k_at) || !take(v_at)) break;
                 q_phase ^= 1u;
                 tc_fence_after();
-                product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
-                mma_commit(s_full(tile_no & 1));
-                product(tmem + C::DP_COL, base + C::TILE, v_at);
-                mma_commit(dp_full);
-                mma_commit(empty_bar(v_at));
+                if (one_thread()) {
+                    product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
+                    mma_commit(s_full(tile_no & 1));
+                    product(tmem + C::DP_COL, base + C::TILE, v_at);
+                    mma_commit(dp_full);
+                    mma_commit(empty_bar(v_at));
+                }
+                __syncwarp();
                 for (int j = 0; j < it.tiles; ++j, ++tile_no) {
                     const bool last = j + 1 == it.tiles;
                     if (!last) {
-                        if ((k_next = take()) < 0) {
-                            ok = false;
-                            break;
-                        }
+                        if (!take(k_next)) break;
                         tc_fence_after();
-                        product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
-                        mma_commit(s_full((tile_no + 1) & 1));
+                        if (one_thread()) {
+                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
+                            mma_commit(s_full((tile_no + 1) & 1));
+                        }
+                        __syncwarp();
+                        if (!take(v_at)) break;
                     }
-                    if (!wait(ds_ready, ds_phase)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!(ok = wait.together(ds_ready, ds_phase))) break;
                     ds_phase ^= 1u;
                     tc_fence_after();
-                    // (each half of the keys has its own half of dP's columns)
-                    tile_add(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
-                    mma_commit(empty_bar(k_at));
-                    if (last) {
-                        mma_commit(dq_full);
-                        mma_commit(q_empty);
-                    } else {
-                        k_at = k_next;
-                        if ((v_at = take()) < 0) {
-                            ok = false;
-                            break;
+                    if (one_thread()) {
+                        // (each half of the keys has its own half of dP's columns)
+                        tile_add(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
+                        mma_commit(empty_bar(k_at));
+                        if (last) {
+                            mma_commit(dq_full);
+                            mma_commit(q_empty);
+                        } else {
+                            product(tmem + C::DP_COL, base + C::TILE, v_at);
+                            mma_commit(dp_full);
+                            mma_commit(empty_bar(v_at));
                         }
-                        tc_fence_after();
-                        product(tmem + C::DP_COL, base + C::TILE, v_at);
-                        mma_commit(dp_full);
-                        mma_commit(empty_bar(v_at));
                     }
+                    __syncwarp();
+                    k_at = k_next;
                 }
             }
             if (!ok) wait.fail();
-            mma_commit(done_bar);
-            mbar_wait(done_bar, 0);
+            if (one_thread()) {
+                mma_commit(done_bar);
+                mbar_wait(done_bar, 0);
+            }
         }
         __syncwarp();
     } else {
