@@ -71,7 +71,9 @@ __device__ __forceinline__ void tile_product(uint32_t d, uint32_t rows, uint32_t
     }
 }
 
-// sums (+)= a 16-bit [128 x 128] matrix in tensor memory, its halves of K 64 columns apart, by a tile's rows.
+// sums (+)= a 16-bit [128 x 128] matrix in tensor memory, by a tile's rows. Its K is in kParts parts, each in the first
+// half of the columns that its fp32 values had.
+template <int kParts>
 __device__ __forceinline__ void tile_add(uint32_t sums, uint32_t a, uint32_t tile, uint32_t id, bool fresh)
 {
     const Desc b(desc_mn(tile, kTileBox));
@@ -80,7 +82,10 @@ __device__ __forceinline__ void tile_add(uint32_t sums, uint32_t a, uint32_t til
     else
         mma_ts_step<true>(sums, a, b, 0, id);
 #pragma unroll
-    for (int kk = 1; kk < 128 / kMmaK; ++kk) mma_ts_step<true>(sums, a + (kk / 4) * 64 + (kk % 4) * (kMmaK / 2), b, kStepMN * kk, id);
+    for (int kk = 1; kk < 128 / kMmaK; ++kk) {
+        constexpr int kPer = 128 / kMmaK / kParts;
+        mma_ts_step<true>(sums, a + (kk / kPer) * (128 / kParts) + (kk % kPer) * (kMmaK / 2), b, kStepMN * kk, id);
+    }
 }
 
 // float16 has 40 binary orders of magnitude, and gradients may be small: the backward pass takes P 2^15 times as large

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         p_phase[g] ^= 1u;
                         tc_fence_after();
                         if (one_thread()) {
-                            tile_add(tmem + C::O_COL + kD * g, tmem + C::S_COL + 128 * g, base + kRing + v_stage * C::TILE, id_o, j == 0);
+                            tile_add<2>(tmem + C::O_COL + kD * g, tmem + C::S_COL + 128 * g, base + kRing + v_stage * C::TILE, id_o, j == 0);
                             if (last) {
                                 mma_commit(o_full(g));
                             } else {

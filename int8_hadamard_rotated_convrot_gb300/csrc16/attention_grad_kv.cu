@@ -9,12 +9,14 @@
 // transposed, a key a lane, so that P^T and dS^T are A operands straight from
 // tensor memory and dout and q are read MN-major from the bytes that S^T = K Q^T
 // and dP^T = V dout^T read K-major.
-//   warp 0       TMA producer: the unit's keys and values, then queries, dout
-//                and their statistics, a ring of two or four tiles
+//   warp 0       TMA producer: the unit's keys and values, then tiles of queries,
+//                their statistics and dout, a ring each: a tile of queries is
+//                needed to its end, so its ring is one longer (with two of each,
+//                the next S^T waited 1200 cycles a tile for its queries)
 //   warp 1       tensor memory; one thread issues the MMAs: while P^T is made
 //                from S^T the tensor cores do the tile before's dK and the next
 //                dP^T, and while dS^T is made, dV and the next S^T
-//   warps 4-11   P^T and dS^T: a key a thread, half of the tile's queries each
+//   warps 4-19   P^T and dS^T: four threads a key, 32 of the tile's queries each
 //
 // The work of all units, laid end to end, is cut into equal runs of tiles, one a
 // CTA, whatever the number of units: a unit that a cut goes through is left as
@@ -27,19 +29,20 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kThreads = 384;
-constexpr int kRegsWg0 = 80, kRegsMath = 208;
-static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsMath <= kThreads * 168, "register split");
+constexpr int kMathWarps = 16, kThreads = 128 + 32 * kMathWarps;
+// Registers a thread: launched at 96, warpgroup 0 leaves some of its own to the others.
+constexpr int kRegsWg0 = 64, kRegsMath = 104;
+static_assert(4 * 32 * kRegsWg0 + 32 * kMathWarps * kRegsMath <= kThreads * 96, "register split");
+constexpr int kPart = 32;  // columns of a tile that a thread has
 
 template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
-    static constexpr int STAGES = kD == 64 ? 4 : 2;
-    static constexpr int STATS = 2 * kTileQueries * 4;  // base2 and delta of a tile
-    static constexpr int STAGE = 2 * TILE;
-    static constexpr int BARS = 2 * STAGES + 8;
-    static constexpr int BAR_BYTES = 256;
-    static constexpr int SMEM = 1024 + 2 * TILE + STAGES * (STAGE + STATS) + 8 * kStageBytes + BAR_BYTES;
+    static constexpr int QS = kD == 64 ? 5 : 3, DS = kD == 64 ? 4 : 2;  // tiles of queries, and of dout
+    static constexpr int STATS = 2 * kTileQueries * 4;                  // base2 and delta of a tile: DS of them, too
+    static constexpr int BARS = 2 * QS + 4 * DS + 8;
+    static constexpr int BAR_BYTES = 384;
+    static constexpr int SMEM = (2 + QS + DS) * TILE + DS * STATS + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 384;
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
@@ -87,18 +90,12 @@ __device__ __forceinline__ Unit unit_at(const P &p, int64_t u)
     return r;
 }
 
-// 32 rows (keys) x 32 values of one of the two gradients, to the caller's tensor.
+// Where a key's row of a gradient is.
 template <typename T>
-__device__ __forceinline__ void store_keys(const Params &p, const Unit &u, void *to, int key0, int col, uint32_t stage, int lane, const float (&v)[32])
+__device__ __forceinline__ T *key_row(const Params &p, const Unit &u, void *to, int key)
 {
-    const int rows = u.keys - key0 < 32 ? u.keys - key0 : 32, cols = p.d - col < 32 ? p.d - col : 32;
-    if (rows <= 0) return;
-    const int64_t ld = static_cast<int64_t>(p.kv_heads) * p.d;
-    T *at = static_cast<T *>(to) + (static_cast<int64_t>(u.b) * p.kv_tokens * p.kv_heads + u.h) * p.d + col;
-    if (p.index)
-        store_rows<T>(at, ld, rows, cols, p.wide, stage, lane, v, p.index + u.b * p.index_rows + key0);
-    else
-        store_rows<T>(at + key0 * ld, ld, rows, cols, p.wide, stage, lane, v);
+    const int64_t token = p.index ? load_i32(p.index + u.b * p.index_rows + key) : key;
+    return static_cast<T *>(to) + ((static_cast<int64_t>(u.b) * p.kv_tokens + token) * p.kv_heads + u.h) * p.d;
 }
 
 template <typename T, int kD>
@@ -106,32 +103,48 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
 {
     using C = Cfg<kD>;
     constexpr bool kHalf = std::is_same_v<T, __half>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
-    const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
-    uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kRing = 2 * C::TILE, kStats = kRing + C::STAGES * C::STAGE, kOut = kStats + C::STAGES * C::STATS, kBars = kOut + 8 * kStageBytes;
+    extern __shared__ __align__(1024) uint8_t smem_tiles[];  // swizzle atoms are 1024-byte aligned
+    uint8_t *gbase = smem_tiles;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem_tiles));
+    constexpr int kQueries = 2 * C::TILE, kDouts = kQueries + C::QS * C::TILE, kStats = kDouts + C::DS * C::TILE, kBars = kStats + C::DS * C::STATS;
     const uint32_t bars = base + kBars;
-    auto full_bar = [&](int s) { return bars + 8u * s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
-    const uint32_t kv_full = bars + 8u * (2 * C::STAGES), kv_empty = kv_full + 8, s_full = kv_full + 16, dp_full = kv_full + 24;
+    auto q_full = [&](int s) { return bars + 8u * s; };
+    auto q_empty = [&](int s) { return bars + 8u * (C::QS + s); };
+    auto do_full = [&](int s) { return bars + 8u * (2 * C::QS + s); };
+    auto do_empty = [&](int s) { return bars + 8u * (2 * C::QS + C::DS + s); };
+    auto st_full = [&](int s) { return bars + 8u * (2 * C::QS + 2 * C::DS + s); };
+    auto st_empty = [&](int s) { return bars + 8u * (2 * C::QS + 3 * C::DS + s); };
+    const uint32_t kv_full = bars + 8u * (2 * C::QS + 4 * C::DS), kv_empty = kv_full + 8, s_full = kv_full + 16, dp_full = kv_full + 24;
     const uint32_t p_ready = kv_full + 32, ds_ready = kv_full + 40;
     const uint32_t sums_full = kv_full + 48, done_bar = kv_full + 56;
+    // the places of tile t, counted over all units of this run, and the parity of their n-th use
+    auto q_at = [&](int t) { return base + kQueries + t % C::QS * C::TILE; };
+    auto do_at = [&](int t) { return base + kDouts + t % C::DS * C::TILE; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
 
+    if (base & 1023u) {  // (no room to align it here: what the compiler was asked for above)
+        if (threadIdx.x == 0 && p.dev_status) atomicExch(p.dev_status, static_cast<int32_t>(CONVROT_ERR_ALIGNMENT));
+        return;
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1 + 8);  // the MMAs are done, and each math warp has read the statistics
+        for (int s = 0; s < C::QS; ++s) {
+            mbar_init(q_full(s), 1);
+            mbar_init(q_empty(s), 1);
+        }
+        for (int s = 0; s < C::DS; ++s) {
+            mbar_init(do_full(s), 1);
+            mbar_init(do_empty(s), 1);
+            mbar_init(st_full(s), 1);
+            mbar_init(st_empty(s), kMathWarps);
         }
         mbar_init(kv_full, 1);
         mbar_init(kv_empty, 1);
         mbar_init(s_full, 1);
         mbar_init(dp_full, 1);
-        mbar_init(p_ready, 8);
-        mbar_init(ds_ready, 8);
+        mbar_init(p_ready, kMathWarps);
+        mbar_init(ds_ready, kMathWarps);
         mbar_init(sums_full, 1);
         mbar_init(done_bar, 1);
         *wait.abort_flag = 0;
@@ -166,87 +179,91 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
         if (warp == 0 && lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, kv_phase = 0, armed = 0;
+            int n = 0, loaded_q = 0, loaded_st = 0, loaded_do = 0;  // tiles, over all units
+            uint32_t kv_phase = 0;
+            bool kv = false;
             const bool ok = each_unit([&](const Unit &u, int t0, int t1) {
                 if (!wait(kv_empty, kv_phase ^ 1u)) return false;
                 kv_phase ^= 1u;
                 mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
                 load_tile<C::HALVES>(base, p.k, u.tile * kTileKeys, u.h, u.b, kv_full);
                 load_tile<C::HALVES>(base + C::TILE, p.v, u.tile * kTileKeys, u.h, u.b, kv_full);
-                armed |= 1u << 16;
-                for (int t = t0; t < t1; ++t) {
-                    if (!wait(empty_bar(stage), phase ^ 1u)) return false;
-                    const int h = u.h * p.group + t / p.q_tiles, q0 = t % p.q_tiles * kTileQueries;
-                    const uint32_t at = base + kRing + stage * C::STAGE, stats = base + kStats + stage * C::STATS;
+                kv = true;
+                for (int t = t0; t < t1; ++t, ++n) {
+                    const int h = u.h * p.group + t / p.q_tiles, q0 = t % p.q_tiles * kTileQueries, qs = n % C::QS, ds = n % C::DS;
                     const int64_t row = (static_cast<int64_t>(u.b) * p.q_heads + h) * p.stat_rows + q0;
-                    mbar_arrive_expect_tx(full_bar(stage), C::STAGE + C::STATS);
-                    load_tile<C::HALVES>(at, p.q, q0, h, u.b, full_bar(stage));
-                    load_tile<C::HALVES>(at + C::TILE, p.dout, q0, h, u.b, full_bar(stage));
-                    bulk_load(stats, p.base2 + row, kTileQueries * 4, full_bar(stage));
-                    bulk_load(stats + kTileQueries * 4, p.delta + row, kTileQueries * 4, full_bar(stage));
-                    armed |= 1u << stage;
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (!wait(q_empty(qs), (n / C::QS + 1) & 1)) return false;
+                    mbar_arrive_expect_tx(q_full(qs), C::TILE);
+                    load_tile<C::HALVES>(q_at(n), p.q, q0, h, u.b, q_full(qs));
+                    ++loaded_q;
+                    if (!wait(st_empty(ds), (n / C::DS + 1) & 1)) return false;
+                    const uint32_t stats = base + kStats + ds * C::STATS;
+                    mbar_arrive_expect_tx(st_full(ds), C::STATS);
+                    bulk_load(stats, p.base2 + row, kTileQueries * 4, st_full(ds));
+                    bulk_load(stats + kTileQueries * 4, p.delta + row, kTileQueries * 4, st_full(ds));
+                    ++loaded_st;
+                    if (!wait(do_empty(ds), (n / C::DS + 1) & 1)) return false;
+                    mbar_arrive_expect_tx(do_full(ds), C::TILE);
+                    load_tile<C::HALVES>(do_at(n), p.dout, q0, h, u.b, do_full(ds));
+                    ++loaded_do;
                 }
                 return true;
             });
             if (!ok) {
                 wait.fail();
-                for (int s = 0; s < C::STAGES; ++s)  // copies in flight land before shared memory goes away
-                    if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
-                if (armed >> 16) mbar_wait(kv_full, kv_phase ^ 1u);
+                // copies in flight land before shared memory goes away
+                for (int i = loaded_q > C::QS ? loaded_q - C::QS : 0; i < loaded_q; ++i) mbar_wait(q_full(i % C::QS), (i / C::QS) & 1);
+                for (int i = loaded_st > C::DS ? loaded_st - C::DS : 0; i < loaded_st; ++i) mbar_wait(st_full(i % C::DS), (i / C::DS) & 1);
+                for (int i = loaded_do > C::DS ? loaded_do - C::DS : 0; i < loaded_do; ++i) mbar_wait(do_full(i % C::DS), (i / C::DS) & 1);
+                if (kv) mbar_wait(kv_full, kv_phase ^ 1u);
             }
         } else if (warp == 1) {
             const uint32_t id_s = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
-            int stage = 0;
-            uint32_t phase = 0, kv_phase = 0, p_phase = 0, ds_phase = 0;
+            int n = 0;  // tiles, over all units
+            uint32_t kv_phase = 0;
             auto product = [&](uint32_t to, uint32_t rows, uint32_t cols) { tile_product<kD>(to, rows, cols, id_s, steps); };
-            // sums += (what a region's halves hold in 16 bits) x a tile, over the queries
-            auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) { tile_add(sums, region, tile, id_o, fresh); };
+            // sums += (what a region's quarters hold in 16 bits) x a tile, over the queries
+            auto add = [&](uint32_t sums, uint32_t region, uint32_t tile, bool fresh) { tile_add<4>(sums, region, tile, id_o, fresh); };
+            auto q_there = [&](int t) { return wait.together(q_full(t % C::QS), (t / C::QS) & 1); };
+            auto do_there = [&](int t) { return wait.together(do_full(t % C::DS), (t / C::DS) & 1); };
             const bool ok = each_unit([&](const Unit &, int t0, int t1) {
-                if (!wait.together(kv_full, kv_phase) || !wait.together(full_bar(stage), phase)) return false;
+                if (!wait.together(kv_full, kv_phase) || !q_there(n) || !do_there(n)) return false;
                 kv_phase ^= 1u;
                 tc_fence_after();
-                uint32_t at = base + kRing + stage * C::STAGE;
                 if (one_thread()) {
-                    product(tmem + C::S_COL, base, at);
+                    product(tmem + C::S_COL, base, q_at(n));
                     mma_commit(s_full);
-                    product(tmem + C::DP_COL, base + C::TILE, at + C::TILE);
+                    product(tmem + C::DP_COL, base + C::TILE, do_at(n));
                     mma_commit(dp_full);
                 }
                 __syncwarp();
-                for (int t = t0; t < t1; ++t) {
+                for (int t = t0; t < t1; ++t, ++n) {
                     const bool more = t + 1 < t1;
-                    const int here = stage;
-                    if (++stage == C::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    const uint32_t next = base + kRing + stage * C::STAGE;
-                    if ((more && !wait.together(full_bar(stage), phase)) || !wait.together(p_ready, p_phase)) return false;
-                    p_phase ^= 1u;
+                    if (!wait.together(p_ready, n & 1)) return false;
                     tc_fence_after();
                     if (one_thread()) {
-                        add(tmem + C::DV_COL, tmem + C::S_COL, at + C::TILE, t == t0);
-                        if (more) {
-                            product(tmem + C::S_COL, base, next);
-                            mma_commit(s_full);
-                        }
+                        add(tmem + C::DV_COL, tmem + C::S_COL, do_at(n), t == t0);
+                        mma_commit(do_empty(n % C::DS));  // (the tile's dP^T came before)
                     }
                     __syncwarp();
-                    if (!wait.together(ds_ready, ds_phase)) return false;
-                    ds_phase ^= 1u;
+                    if (more) {
+                        if (!q_there(n + 1)) return false;
+                        tc_fence_after();
+                        if (one_thread()) {
+                            product(tmem + C::S_COL, base, q_at(n + 1));
+                            mma_commit(s_full);
+                        }
+                        __syncwarp();
+                    }
+                    if (!wait.together(ds_ready, n & 1) || (more && !do_there(n + 1))) return false;
                     tc_fence_after();
                     if (one_thread()) {
-                        add(tmem + C::DK_COL, tmem + C::DP_COL, at, t == t0);
-                        mma_commit(empty_bar(here));
+                        add(tmem + C::DK_COL, tmem + C::DP_COL, q_at(n), t == t0);
+                        mma_commit(q_empty(n % C::QS));
                         if (more) {
-                            product(tmem + C::DP_COL, base + C::TILE, next + C::TILE);
+                            product(tmem + C::DP_COL, base + C::TILE, do_at(n + 1));
                             mma_commit(dp_full);
                         } else {
                             mma_commit(kv_empty);
@@ -254,7 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                         }
                     }
                     __syncwarp();
-                    at = next;
                 }
                 return true;
             });
@@ -267,28 +283,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMath));
-        const int half = (warp - 4) >> 2, quad = warp & 3;
+        const int part = (warp - 4) >> 2, quad = warp & 3;  // of the tile's queries; of the keys
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t staging = base + kOut + (warp - 4) * kStageBytes;
         const F2 c2(p.scale_log2);
-        int stage = 0;
-        uint32_t phase = 0, s_phase = 0, dp_phase = 0, sums_phase = 0;
+        int n = 0;  // tiles, over all units
+        uint32_t sums_phase = 0;
         const bool ok = each_unit([&](const Unit &u, int t0, int t1) {
             int exponent = 0;
             if constexpr (kHalf)
                 exponent = grad_exponent(p.amax + (static_cast<int64_t>(u.b) * p.kv_heads + u.h) * p.amax_blocks, p.amax_blocks, lane);
             const F2 up(kHalf ? exp2i(exponent) * exp2i(-15) : 1.0f);
-            for (int t = t0; t < t1; ++t) {
-                if (!wait(full_bar(stage), phase) || !wait(s_full, s_phase)) return false;  // the statistics, and S^T
-                s_phase ^= 1u;
+            for (int t = t0; t < t1; ++t, ++n) {
+                const int ds = n % C::DS;
+                if (!wait(st_full(ds), (n / C::DS) & 1) || !wait(s_full, n & 1)) return false;
                 tc_fence_after();
-                const uint32_t stats = base + kStats + stage * C::STATS + half * 64 * 4;
-                uint32_t s[64], g[64], pk[32];
-                tmem_ld32_async(lanes + C::S_COL + 64 * half, s);
-                tmem_ld32_async(lanes + C::S_COL + 64 * half + 32, s + 32);
+                const uint32_t stats = base + kStats + ds * C::STATS + part * kPart * 4;
+                uint32_t s[kPart], g[kPart], pk[kPart / 2];
+                tmem_ld32_async(lanes + C::S_COL + kPart * part, s);
                 tmem_ld_wait(s);
 #pragma unroll
-                for (int k = 0; k < 64; k += 4) {
+                for (int k = 0; k < kPart; k += 4) {
                     const uint4 w = shared16(stats + k * 4);
                     const F2 x0 = fma2(F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, F2(__uint_as_float(w.x), __uint_as_float(w.y)));
                     const F2 x1 = fma2(F2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])), c2, F2(__uint_as_float(w.z), __uint_as_float(w.w)));
@@ -299,19 +313,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     pk[k / 2] = pack2<T>(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
                     pk[k / 2 + 1] = pack2<T>(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3]));
                 }
-                tmem_st32(lanes + C::S_COL + 64 * half, pk);
+                tmem_st16(lanes + C::S_COL + kPart * part, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready);
-                if (!wait(dp_full, dp_phase)) return false;
-                dp_phase ^= 1u;
+                if (!wait(dp_full, n & 1)) return false;
                 tc_fence_after();
-                tmem_ld32_async(lanes + C::DP_COL + 64 * half, g);
-                tmem_ld32_async(lanes + C::DP_COL + 64 * half + 32, g + 32);
+                tmem_ld32_async(lanes + C::DP_COL + kPart * part, g);
                 tmem_ld_wait(g);
 #pragma unroll
-                for (int k = 0; k < 64; k += 4) {
+                for (int k = 0; k < kPart; k += 4) {
                     const uint4 w = shared16(stats + kTileQueries * 4 + k * 4);
                     F2 x0 = F2(__uint_as_float(g[k]), __uint_as_float(g[k + 1])) + F2(__uint_as_float(w.x), __uint_as_float(w.y));
                     F2 x1 = F2(__uint_as_float(g[k + 2]), __uint_as_float(g[k + 3])) + F2(__uint_as_float(w.z), __uint_as_float(w.w));
@@ -324,41 +336,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     pk[k / 2] = pack2<T>(x0.lo(), x0.hi());
                     pk[k / 2 + 1] = pack2<T>(x1.lo(), x1.hi());
                 }
-                tmem_st32(lanes + C::DP_COL + 64 * half, pk);
+                tmem_st16(lanes + C::DP_COL + kPart * part, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(ds_ready);
-                    mbar_arrive(empty_bar(stage));
-                }
-                if (++stage == C::STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
+                    mbar_arrive(st_empty(ds));
                 }
             }
             if (!wait(sums_full, sums_phase)) return false;
             sums_phase ^= 1u;
             tc_fence_after();
-            // the first four warps have dV, the others dK
+            // the first eight warps have dV, the others dK
+            const int half = part >> 1;
             const bool whole = t1 - t0 == p.cut.per_unit;
             const float down = half == 0 ? (kHalf ? exp2i(-15) : 1.0f) : p.scale * (kHalf ? exp2i(-exponent) : 1.0f);
-            const int key0 = u.tile * kTileKeys + quad * 32;
+            const int key = u.tile * kTileKeys + quad * 32 + lane;
+            const bool there = key < u.keys;
+            T *row = whole && there ? key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) : nullptr;
             // a run's first unit may start inside, and its last one end inside
-            float *part = p.partial + (((static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * 2 + half) * kTileKeys + quad * 32 + lane) * kD;
+            float *shares = p.partial + (((static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * 2 + half) * kTileKeys + quad * 32 + lane) * kD;
 #pragma unroll 1
-            for (int k = 0; k < p.d; k += 32) {
+            for (int k = (part & 1) * 32; k < p.d; k += 64) {
                 uint32_t o[32];
                 tmem_ld32_async(lanes + (half == 0 ? C::DV_COL : C::DK_COL) + k, o);
                 tmem_ld_wait(o);
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * down;
-                if (whole) {
-                    store_keys<T>(p, u, half == 0 ? p.dv : p.dk, key0, k, staging, lane, v);
-                } else {
+                // (each lane its own row: these are few bytes beside the queries')
+                if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(part + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(shares + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                } else if (there && p.wide) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (k + e < p.d)
+                            *reinterpret_cast<uint4 *>(row + k + e) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
+                                                                                 pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
+                } else if (there) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (k + e < p.d) row[k + e] = from_f32<T>(v[e]);
                 }
             }
             tc_fence_before();  // the sums are read before the next unit's first P is announced
@@ -407,8 +427,7 @@ __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_c
             sum.w += w[i].w;
         }
     }
-    const int64_t token = p.index ? load_i32(p.index + u.b * p.index_rows + key) : key;
-    T *to = static_cast<T *>(half == 0 ? p.dv : p.dk) + ((static_cast<int64_t>(u.b) * p.kv_tokens + token) * p.kv_heads + u.h) * p.d + col;
+    T *to = key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) + col;
     if (p.wide) {
         *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
     } else {

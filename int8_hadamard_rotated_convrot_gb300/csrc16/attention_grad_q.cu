@@ -9,7 +9,7 @@
 //   warp 0       TMA producer: the item's queries and dout, then tiles of keys
 //                and values in turn, through one ring
 //   warp 1       tensor memory; one thread issues the MMAs
-//   warps 4-11   dS: a row a thread, half of the tile's keys each
+//   warps 4-19   dS: four threads a row, 32 of the tile's keys each
 // Tensor memory: two tiles of S = Q K^T in turn, so that the next one is
 // multiplied while dS is made, dP, whose columns then hold dS (16 bits, the A
 // operand of dS K), and the sums dQ. The tile of keys is read K-major for S
@@ -21,9 +21,12 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kThreads = 384;
-constexpr int kRegsWg0 = 80, kRegsMath = 208;
-static_assert(4 * 32 * kRegsWg0 + 8 * 32 * kRegsMath <= kThreads * 168, "register split");
+constexpr int kMathWarps = 16, kThreads = 128 + 32 * kMathWarps;
+// Registers a thread: launched at 96, warpgroup 0 leaves some of its own to the others.
+constexpr int kRegsWg0 = 64, kRegsMath = 104;
+static_assert(4 * 32 * kRegsWg0 + 32 * kMathWarps * kRegsMath <= kThreads * 96, "register split");
+constexpr int kStageRows = 16, kWarpStage = kStageRows * kStagePitch;  // of a warp's staged outputs
+constexpr int kPart = 32;  // columns of a tile that a thread has
 
 template <int kD>
 struct Cfg {
@@ -31,7 +34,7 @@ struct Cfg {
     static constexpr int STAGES = kD == 64 ? 8 : 4;
     static constexpr int BARS = 2 * STAGES + 8;
     static constexpr int BAR_BYTES = 256;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + 8 * kStageBytes + BAR_BYTES;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + kMathWarps * kWarpStage + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;  // S: + 128 for every other tile
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + 8 * kStageBytes;
+    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + kMathWarps * kWarpStage;
     const uint32_t bars = base + kBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(dp_full, 1);
-        mbar_init(ds_ready, 8);
+        mbar_init(ds_ready, kMathWarps);
         mbar_init(dq_full, 1);
         mbar_init(done_bar, 1);
         *wait.abort_flag = 0;
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
-                int k_at, v_at, k_next = 0;
+                int k_at, v_at;
                 if (!(ok = wait.together(q_full, q_phase)) || !take(k_at) || !take(v_at)) break;
                 q_phase ^= 1u;
                 tc_fence_after();
@@ -187,34 +190,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 __syncwarp();
                 for (int j = 0; j < it.tiles; ++j, ++tile_no) {
                     const bool last = j + 1 == it.tiles;
-                    if (!last) {
-                        if (!take(k_next)) break;
+                    // The next S as soon as its keys are there, which may be before or after this tile's dS: their place
+                    // in the ring became free with the last dQ.
+                    bool next = last;
+                    auto scores = [&]() {
                         tc_fence_after();
                         if (one_thread()) {
-                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
+                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, stage);
                             mma_commit(s_full((tile_no + 1) & 1));
                         }
                         __syncwarp();
-                        if (!take(v_at)) break;
+                        next = true;
+                    };
+                    bool made = false;
+                    for (int tries = 0; tries < 4096 && !made; ++tries) {
+                        if (!next && wait.now(full_bar(stage), phase)) scores();
+                        made = wait.now(ds_ready, ds_phase);
+                        if (next) break;
                     }
-                    if (!(ok = wait.together(ds_ready, ds_phase))) break;
+                    if (!made && !(ok = wait.together(ds_ready, ds_phase))) break;
                     ds_phase ^= 1u;
                     tc_fence_after();
                     if (one_thread()) {
-                        // (each half of the keys has its own half of dP's columns)
-                        tile_add(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
+                        // (each quarter of the keys has its own quarter of dP's columns)
+                        tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
                         mma_commit(empty_bar(k_at));
                         if (last) {
                             mma_commit(dq_full);
                             mma_commit(q_empty);
-                        } else {
-                            product(tmem + C::DP_COL, base + C::TILE, v_at);
-                            mma_commit(dp_full);
-                            mma_commit(empty_bar(v_at));
                         }
                     }
                     __syncwarp();
-                    k_at = k_next;
+                    if (last) continue;
+                    if (!next) {
+                        if (!(ok = wait.together(full_bar(stage), phase))) break;
+                        scores();
+                    }
+                    if (!take(k_at) || !take(v_at)) break;  // (the first is the one that scores() used)
+                    tc_fence_after();
+                    if (one_thread()) {
+                        product(tmem + C::DP_COL, base + C::TILE, v_at);
+                        mma_commit(dp_full);
+                        mma_commit(empty_bar(v_at));
+                    }
+                    __syncwarp();
                 }
             }
             if (!ok) wait.fail();
@@ -226,9 +245,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMath));
-        const int half = (warp - 4) >> 2, quad = warp & 3;
+        const int part = (warp - 4) >> 2, quad = warp & 3;  // of the tile's keys; of the rows
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t stage = base + kOut + (warp - 4) * kStageBytes;
+        const uint32_t stage = base + kOut + (warp - 4) * kWarpStage;
         const F2 c2(p.scale_log2);
         uint32_t dp_phase = 0, dq_phase = 0;
         int tile_no = 0;
@@ -252,20 +271,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     break;
                 }
                 tc_fence_after();
-                uint32_t s[64], g[64];
-                tmem_ld32_async(lanes + C::S_COL + 128 * b + 64 * half, s);
-                tmem_ld32_async(lanes + C::S_COL + 128 * b + 64 * half + 32, s + 32);
+                uint32_t s[kPart], g[kPart];
+                tmem_ld32_async(lanes + C::S_COL + 128 * b + kPart * part, s);
                 tmem_ld_wait(s);
-                const int keys = it.keys - j * kTileKeys - half * 64;
+                const int keys = it.keys - j * kTileKeys - part * kPart;
 #pragma unroll
-                for (int k = 0; k < 64; k += 2) {
+                for (int k = 0; k < kPart; k += 2) {
                     const F2 x = fma2(F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, off2);
                     s[k] = __float_as_uint(ex2(x.lo()));
                     s[k + 1] = __float_as_uint(ex2(x.hi()));
                 }
-                if (keys < 64) {
+                if (keys < kPart) {
 #pragma unroll
-                    for (int k = 0; k < 64; ++k)
+                    for (int k = 0; k < kPart; ++k)
                         if (k >= keys) s[k] = 0u;
                 }
                 if (!wait(dp_full, dp_phase)) {
@@ -274,17 +292,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 }
                 dp_phase ^= 1u;
                 tc_fence_after();
-                tmem_ld32_async(lanes + C::DP_COL + 64 * half, g);
-                tmem_ld32_async(lanes + C::DP_COL + 64 * half + 32, g + 32);
+                tmem_ld32_async(lanes + C::DP_COL + kPart * part, g);
                 tmem_ld_wait(g);
-                uint32_t pk[32];
+                uint32_t pk[kPart / 2];
 #pragma unroll
-                for (int k = 0; k < 64; k += 2) {
+                for (int k = 0; k < kPart; k += 2) {
                     F2 x = F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])) * (F2(__uint_as_float(g[k]), __uint_as_float(g[k + 1])) + delta2);
                     if constexpr (kHalf) x = x * up;
                     pk[k / 2] = pack2<T>(x.lo(), x.hi());
                 }
-                tmem_st32(lanes + C::DP_COL + 64 * half, pk);
+                tmem_st16(lanes + C::DP_COL + kPart * part, pk);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -302,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             const float down = kHalf ? p.scale * exp2i(-exponent) : p.scale;
             T *dq = static_cast<T *>(p.dq) + ((static_cast<int64_t>(it.b) * p.q_tokens + row0) * p.q_heads + it.h) * p.d;
 #pragma unroll 1
-            for (int k = half * 32; k < p.d; k += 64) {
+            for (int k = part * 32; k < p.d; k += 128) {
                 uint32_t o[32];
                 float v[32];
                 if (it.tiles > 0) {
@@ -312,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = it.tiles > 0 ? __uint_as_float(o[e]) * down : 0.0f;
                 if (rows > 0)
-                    store_rows<T>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+                    store_rows<T, kStageRows>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
             }
             tc_fence_before();  // dQ is read before the next item's first dS is announced
         }

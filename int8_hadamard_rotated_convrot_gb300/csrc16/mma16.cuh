@@ -258,14 +258,26 @@ struct Waits {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = globaltimer();
         for (;;) {
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i)
-                if (mbar_try_wait(bar, parity)) return true;
+            if (try_long(bar, parity)) return true;
             if (*abort_flag || globaltimer() - t0 > kTimeoutNs) return false;
         }
     }
+    // A try that may sleep for 0.1 ms: warps that come back to try again take issue slots from those that compute.
+    static __device__ __forceinline__ bool try_long(uint32_t bar, uint32_t parity)
+    {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        return ok != 0;
+    }
     // by a whole warp: true for all lanes or for none
     __device__ __forceinline__ bool together(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, (*this)(bar, parity)); }
+    // whether it is there now
+    __device__ __forceinline__ bool now(uint32_t bar, uint32_t parity) const
+    {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        return __all_sync(0xffffffffu, ok != 0);
+    }
     __device__ __forceinline__ void fail() const
     {
         *abort_flag = 1;
