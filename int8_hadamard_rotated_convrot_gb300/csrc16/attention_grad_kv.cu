@@ -395,6 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
 
 // Units that a cut goes through: the blocks of column r add up the one in which run r's end is the first cut, four
 // elements of dV or dK a thread.
+constexpr int kJoinRounds = 4;  // of a block: what it computes of the cuts costs more than a round
+
 template <typename T, int kD>
 __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_constant__ Params p)
 {
@@ -405,36 +407,39 @@ __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_c
     const int64_t r0 = p.cut.run_of(begin), r1 = p.cut.run_of(begin + p.cut.per_unit - 1);
     if (r0 != blockIdx.x) return;                    // an earlier column's
     const Unit u = unit_at(p, n);
-    const int at = (blockIdx.y * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
-    const int key = u.tile * kTileKeys + row;
-    if (key >= u.keys || col >= p.d) return;
-    // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
-    const float *first = p.partial + (r0 * 2 + 1) * 2 * kTileKeys * kD + at, *other = p.partial + (r0 + 1) * 4 * kTileKeys * kD + at;
-    float4 sum = __ldcg(reinterpret_cast<const float4 *>(first));
     const int64_t count = r1 - r0;
-    constexpr int kBatch = 8;
-    for (int64_t r = 0; r < count; r += kBatch) {
-        float4 w[kBatch];
+#pragma unroll 1
+    for (int i = 0; i < kJoinRounds; ++i) {
+        const int at = ((blockIdx.y * kJoinRounds + i) * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
+        const int key = u.tile * kTileKeys + row;
+        if (key >= u.keys || col >= p.d) continue;
+        // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
+        const float *first = p.partial + (r0 * 2 + 1) * 2 * kTileKeys * kD + at, *other = p.partial + (r0 + 1) * 4 * kTileKeys * kD + at;
+        float4 sum = __ldcg(reinterpret_cast<const float4 *>(first));
+        constexpr int kBatch = 8;
+        for (int64_t r = 0; r < count; r += kBatch) {
+            float4 w[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (r + i < count) w[i] = __ldcg(reinterpret_cast<const float4 *>(other + (r + i) * 4 * kTileKeys * kD));
+            for (int e = 0; e < kBatch; ++e)
+                if (r + e < count) w[e] = __ldcg(reinterpret_cast<const float4 *>(other + (r + e) * 4 * kTileKeys * kD));
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (r + i >= count) break;
-            sum.x += w[i].x;
-            sum.y += w[i].y;
-            sum.z += w[i].z;
-            sum.w += w[i].w;
+            for (int e = 0; e < kBatch; ++e) {
+                if (r + e >= count) break;
+                sum.x += w[e].x;
+                sum.y += w[e].y;
+                sum.z += w[e].z;
+                sum.w += w[e].w;
+            }
         }
-    }
-    T *to = key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) + col;
-    if (p.wide) {
-        *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
-    } else {
-        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+        T *to = key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) + col;
+        if (p.wide) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
+        } else {
+            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (col + e < p.d) to[e] = from_f32<T>(v[e]);
+            for (int e = 0; e < 4; ++e)
+                if (col + e < p.d) to[e] = from_f32<T>(v[e]);
+        }
     }
 }
 
@@ -488,7 +493,7 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     cudaError_t e = allow_shared<grad_kv_tag<T, kD>>(kernel);
     if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.cut.runs == 1) return e;
-    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / 1024), 256, 0, stream, 1, p);
+    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / (1024 * kJoinRounds)), 256, 0, stream, 1, p);
 }
 
 }  // namespace

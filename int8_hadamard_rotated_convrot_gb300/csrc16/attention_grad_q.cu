@@ -25,16 +25,15 @@ constexpr int kMathWarps = 16, kThreads = 128 + 32 * kMathWarps;
 // Registers a thread: launched at 96, warpgroup 0 leaves some of its own to the others.
 constexpr int kRegsWg0 = 64, kRegsMath = 104;
 static_assert(4 * 32 * kRegsWg0 + 32 * kMathWarps * kRegsMath <= kThreads * 96, "register split");
-constexpr int kStageRows = 16, kWarpStage = kStageRows * kStagePitch;  // of a warp's staged outputs
 constexpr int kPart = 32;  // columns of a tile that a thread has
 
 template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
-    static constexpr int STAGES = kD == 64 ? 8 : 4;
+    static constexpr int STAGES = kD == 64 ? 10 : 5;
     static constexpr int BARS = 2 * STAGES + 8;
     static constexpr int BAR_BYTES = 256;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + kMathWarps * kWarpStage + BAR_BYTES;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;  // S: + 128 for every other tile
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
@@ -62,7 +61,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kBars = kOut + kMathWarps * kWarpStage;
+    constexpr int kRing = 2 * C::TILE, kBars = kRing + C::STAGES * C::TILE;
     const uint32_t bars = base + kBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -186,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     product(tmem + C::DP_COL, base + C::TILE, v_at);
                     mma_commit(dp_full);
                     mma_commit(empty_bar(v_at));
+                    if (it.tiles == 1) mma_commit(q_empty);
                 }
                 __syncwarp();
                 for (int j = 0; j < it.tiles; ++j, ++tile_no) {
@@ -215,10 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                         // (each quarter of the keys has its own quarter of dP's columns)
                         tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
                         mma_commit(empty_bar(k_at));
-                        if (last) {
-                            mma_commit(dq_full);
-                            mma_commit(q_empty);
-                        }
+                        if (last) mma_commit(dq_full);
                     }
                     __syncwarp();
                     if (last) continue;
@@ -232,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                         product(tmem + C::DP_COL, base + C::TILE, v_at);
                         mma_commit(dp_full);
                         mma_commit(empty_bar(v_at));
+                        if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
                     }
                     __syncwarp();
                 }
@@ -247,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMath));
         const int part = (warp - 4) >> 2, quad = warp & 3;  // of the tile's keys; of the rows
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t stage = base + kOut + (warp - 4) * kWarpStage;
         const F2 c2(p.scale_log2);
         uint32_t dp_phase = 0, dq_phase = 0;
         int tile_no = 0;
@@ -329,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = it.tiles > 0 ? __uint_as_float(o[e]) * down : 0.0f;
                 if (rows > 0)
-                    store_rows<T, kStageRows>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+                    store_rows_traded<T>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, lane, v);
             }
             tc_fence_before();  // dQ is read before the next item's first dS is announced
         }

@@ -32,7 +32,8 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
     after_previous();
     let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t block = blockIdx.x % p.blocks, bh = blockIdx.x / p.blocks, b = bh / p.kv_heads, hk = bh - b * p.kv_heads;
+    // (the heads of a stretch of tokens lie together, so they are read together)
+    const int64_t bt = blockIdx.x / p.kv_heads, hk = blockIdx.x - bt * p.kv_heads, b = bt / p.blocks, block = bt - b * p.blocks, bh = b * p.kv_heads + hk;
     const int64_t t0 = block * kStatTokens;
     constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 4, kStride = 8 * kPerWarp;  // queries of a block's round
     const int sub = lane / kLanes, e0 = lane % kLanes * 8;

@@ -329,6 +329,46 @@ __device__ __forceinline__ void store_rows(T *y, int64_t ld, int rows, int cols,
     }
 }
 
+// The same without shared memory: four lanes trade their 16-byte pieces until each has one of each one's row.
+template <typename T>
+__device__ __forceinline__ void store_rows_traded(T *y, int64_t ld, int rows, int cols, bool wide, int lane, const float (&v)[32])
+{
+    uint32_t w[4][4];  // pieces of this lane's row
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[i][e] = pack2<T>(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]);
+    if (wide && cols >= 32) {
+        // w[i] of lane l becomes piece l % 4 of the row of lane l / 4 * 4 + i
+#pragma unroll
+        for (int bit = 1; bit <= 2; bit <<= 1) {
+            const bool high = lane & bit;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i & bit) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[i][e] : w[i | bit][e], bit);
+                    if (high)
+                        w[i][e] = got;
+                    else
+                        w[i | bit][e] = got;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = lane / 4 * 4 + i;
+            if (r < rows) *(reinterpret_cast<uint4 *>(y + r * ld) + lane % 4) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
+    } else if (lane < rows) {
+        unsigned short *to = reinterpret_cast<unsigned short *>(y + lane * ld);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (c < cols) to[c] = static_cast<unsigned short>(c % 2 ? w[c / 8][c % 8 / 2] >> 16 : w[c / 8][c % 8 / 2] & 0xffffu);
+    }
+}
+
 // What a tensor map can describe: rows that start on 16 bytes.
 inline bool tma_rows(const void *p, int64_t ld, int64_t rows) { return aligned_to(p, 16) && (rows <= 1 || ld % 8 == 0); }
 
