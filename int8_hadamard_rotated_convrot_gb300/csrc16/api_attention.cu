@@ -143,7 +143,7 @@ struct ForwardWork {
             partial = w.take<float>(attention_few_partial_bytes(a.batch, a.kv_tokens, a.kv_heads, a.head_dim) / 4);
         } else {
             q.plan(w, nullptr, 0, false);
-            kv.plan(w, a.mask, a.mask_stride, false);
+            kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, false);
         }
         bytes = w.used;
     }
@@ -164,7 +164,7 @@ struct BackwardWork {
         if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.kv_heads * (rows / kStatTokens));
         partial = w.take<float>(grad_kv_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.kv_heads, a.head_dim) / 4);
         q.plan(w, nullptr, 0, false);
-        kv.plan(w, a.mask, a.mask_stride, true);
+        kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, true);
         bytes = w.used;
     }
 };
@@ -204,6 +204,10 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
     b.k = w.kv.s[0];
     b.v = w.kv.s[1];
     b.counts = w.kv.counts;
+    if (mask_in_place(a->kv_tokens)) {
+        b.mask = a->mask;
+        b.mask_stride = a->mask_stride;
+    }
     b.out = a->out;
     for (int i = 0; i < 3; ++i) b.out_strides[i] = a->out_strides[i];
     b.lse = a->lse;
@@ -250,6 +254,10 @@ convrot_status convrot_attention_backward(const convrot_attention_backward_args 
     b.k = w.kv.s[0];
     b.v = w.kv.s[1];
     b.counts = w.kv.counts;
+    if (mask_in_place(a->kv_tokens)) {
+        b.mask = a->mask;
+        b.mask_stride = a->mask_stride;
+    }
     b.index = w.kv.index;
     b.index_rows = w.kv.rows;
     b.out = a->out;

@@ -55,6 +55,51 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const HeadsMap &m, int t
         tma_load_4d(dst + i * kTileBox, &m.map, i * kBoxElems, token, head * m.head_step, batch * m.batch_step, bar);
 }
 
+// Which of 32 keys, one a lane, are there.
+__device__ __forceinline__ uint32_t keys_there(const uint8_t *mask, int key, int keys)
+{
+    bool there = false;
+    if (key < keys) there = *reinterpret_cast<const volatile uint8_t *>(mask + key) != 0;
+    return __ballot_sync(0xffffffffu, there);
+}
+
+// Zeros in the rows of a tile whose key is not there, by two warps, half of the rows each: what stands in a masked key must
+// not meet a product over the keys (0 times NaN). The tensor cores see it behind a barrier that each warp's lane 0 arrives at.
+template <int kHalves>
+__device__ __forceinline__ void clean_rows(uint32_t tile, const uint32_t (&there)[2], int which, int lane)
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int first = which * 64 + i * 32;
+        uint32_t gone = ~there[i];
+        while (gone) {  // four rows at a time, eight lanes a row
+            const int mine = __fns(gone, 0, lane / 8 + 1);
+            if (mine >= 0 && mine < 32) {
+                const uint32_t at = tile + (first + mine) * 128 + lane % 8 * 16;
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + h * kTileBox), "r"(0) : "memory");
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) gone &= gone - 1;
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// The cleaning warps' keys of sample b's mask: read again only where the sample changes.
+struct MaskedRows {
+    uint32_t there[2] = {0, 0};
+    int sample = -1;
+    __device__ __forceinline__ void of(const uint8_t *mask, int64_t stride, int b, int keys, int which, int lane)
+    {
+        if (b == sample) return;
+        sample = b;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) there[i] = keys_there(mask + b * stride, which * 64 + i * 32 + lane, keys);
+    }
+};
+
 // D [128 x 128] = rows of one tile by rows of another, over `steps` times 16 of the head's kD elements.
 template <int kD>
 __device__ __forceinline__ void tile_product(uint32_t d, uint32_t rows, uint32_t cols, uint32_t id, int steps)

@@ -37,9 +37,16 @@ struct GatherArgs {
 };
 cudaError_t launch_gather(const GatherArgs &a, cudaStream_t stream);
 
+// Masks of one tile's keys are applied where they are (the gathering kernel's 5 us are more than what a shorter tile saves),
+// longer ones by gathering the keys that are there (3 samples of 1363 queries, 24 heads, a third to all of 333 keys: 22 us with
+// it against 28 over all tiles).
+inline bool mask_in_place(int64_t kv_tokens) { return kv_tokens <= kTileKeys; }
+
 struct AttentionArgs {
     States q, k, v;
     const int32_t *counts;  // keys of each sample, or null: k.tokens
+    const uint8_t *mask;    // of at most kTileKeys keys, where it is to be applied in place; else null
+    int64_t mask_stride;
     void *out;
     int64_t out_strides[3];
     float *lse;
@@ -66,6 +73,8 @@ struct AttentionGradArgs {
     States q, k, v, dout;     // as the kernels read them
     const int32_t *counts, *index;
     int64_t index_rows;       // of a sample in index
+    const uint8_t *mask;      // as in AttentionArgs
+    int64_t mask_stride;
     const void *out, *dout_own;
     int64_t out_strides[3], dout_own_strides[3];  // the caller's out and dout, for the statistics
     const float *lse;

@@ -40,8 +40,8 @@ template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
     static constexpr int STAGES = kD == 64 ? 8 : 4;
-    static constexpr int BARS = 2 * STAGES + 2 * 5 + 1;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int BARS = 3 * STAGES + 2 * 5 + 1;
+    static constexpr int BAR_BYTES = 384;
     static constexpr int MEET = 2 * 2 * 4 * 2 * 32 * 4;  // maxima of the two threads of a row: in turn, group, quadrant, half
     static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + kSoftmaxWarps * kWarpStage + MEET + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 g and + kD g
@@ -52,6 +52,8 @@ struct Cfg {
 struct Params {
     HeadsMap q, k, v;
     const int32_t *counts;
+    const uint8_t *mask;
+    int64_t mask_stride;
     void *out;
     int64_t out_strides[3];
     float *lse;
@@ -81,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     auto p_ready = [&](int g) { return bars + 8u * (2 * C::STAGES + 6 + g); };  // P is there, and O rescaled
     auto o_full = [&](int g) { return bars + 8u * (2 * C::STAGES + 8 + g); };
     const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 10);
+    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of values has its zeros
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(clean_bar(s), 2);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(q_full(g), 1);
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int j = 0; j < it.tiles; ++j) {
                     const int v_stage = stage;
                     const bool last = j + 1 == it.tiles;
-                    if (!(ok = wait.together(full_bar(stage), phase))) break;
+                    if (!(ok = wait.together(p.mask ? clean_bar(stage) : full_bar(stage), phase))) break;
                     next();
                     if (!last && !(ok = wait.together(full_bar(stage), phase))) break;
 #pragma unroll
@@ -244,6 +248,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 mma_commit(done_bar);
                 mbar_wait(done_bar, 0);
             }
+        } else if (warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
+            bool ok = true;
+            int entry = 1;
+            MaskedRows rows;
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2) {
+                const int s = entry % C::STAGES;
+                rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
+                if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
+                clean_rows<C::HALVES>(base + kRing + s * C::TILE, rows.there, warp - 2, lane);
+                if (lane == 0) mbar_arrive(clean_bar(s));
+            }
+            if (!ok) wait.fail();
         }
         __syncwarp();
     } else {
@@ -269,9 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             return theirs;
         };
         uint32_t s_phase = 0, o_phase = 0;
+        uint32_t there[2] = {0, 0};  // a mask's keys of this thread
+        int masked = -1;             // its sample
         for (int i = blockIdx.x; i < p.items && !gone; i += gridDim.x) {
             const Item it = item_at(i);
             if (g >= it.groups) continue;
+            if (p.mask && it.b != masked) {
+                masked = it.b;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) there[n] = keys_there(p.mask + it.b * p.mask_stride, half * kHalfKeys + n * 32 + lane, p.kv_tokens);
+            }
             float top = neg_inf(), sum = 0.0f;  // the reference, and this thread's sum of 2^(c (s - top) + kShift)
             for (int j = 0; j < it.tiles; ++j) {
                 ok = __all_sync(0xffffffffu, ok && wait(s_full(g), s_phase));
@@ -282,7 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int k = 0; k < kHalfKeys; k += 32) tmem_ld32_async(s_at + k, r + k);
                 tmem_ld_wait(r);
                 const int keys = it.keys - j * kTileKeys - half * kHalfKeys;
-                if (keys < kHalfKeys) {
+                if (p.mask) {
+#pragma unroll
+                    for (int k = 0; k < kHalfKeys; ++k)
+                        if (!(there[k / 32] & 1u << k % 32)) r[k] = 0xff800000u;
+                } else if (keys < kHalfKeys) {
 #pragma unroll
                     for (int k = 0; k < kHalfKeys; ++k)
                         if (k >= keys) r[k] = 0xff800000u;
@@ -386,6 +413,8 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
     if (a.k.tokens > 0 && (!heads_map<T>(&p.k, a.k, a.batch, a.d, kTileKeys) || !heads_map<T>(&p.v, a.v, a.batch, a.d, kTileKeys)))
         return cudaErrorInvalidValue;
     p.counts = a.counts;
+    p.mask = a.mask;
+    p.mask_stride = a.mask_stride;
     p.out = a.out;
     for (int i = 0; i < 3; ++i) p.out_strides[i] = a.out_strides[i];
     p.lse = a.lse;

@@ -61,6 +61,8 @@ struct Params {
     HeadsMap q, dout, k, v;
     const int32_t *counts, *index;
     int64_t index_rows;
+    const uint8_t *mask;  // applied here: gradients of keys that are not there are 0 (their rows of S^T and dP^T are theirs alone)
+    int64_t mask_stride;
     const float *base2, *delta, *amax;
     int64_t amax_blocks, stat_rows;
     float *partial;  // [runs][2][2][128][kD]: a run's first and last unit where they are cut, dV and dK
@@ -96,6 +98,11 @@ __device__ __forceinline__ T *key_row(const Params &p, const Unit &u, void *to, 
 {
     const int64_t token = p.index ? load_i32(p.index + u.b * p.index_rows + key) : key;
     return static_cast<T *>(to) + ((static_cast<int64_t>(u.b) * p.kv_tokens + token) * p.kv_heads + u.h) * p.d;
+}
+
+__device__ __forceinline__ bool key_masked(const Params &p, const Unit &u, int key)
+{
+    return p.mask && *reinterpret_cast<const volatile uint8_t *>(p.mask + u.b * p.mask_stride + key) == 0;
 }
 
 template <typename T, int kD>
@@ -354,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             const float down = half == 0 ? (kHalf ? exp2i(-15) : 1.0f) : p.scale * (kHalf ? exp2i(-exponent) : 1.0f);
             const int key = u.tile * kTileKeys + quad * 32 + lane;
             const bool there = key < u.keys;
+            const bool masked = whole && there && key_masked(p, u, key);
             T *row = whole && there ? key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) : nullptr;
             // a run's first unit may start inside, and its last one end inside
             float *shares = p.partial + (((static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * 2 + half) * kTileKeys + quad * 32 + lane) * kD;
@@ -364,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 tmem_ld_wait(o);
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * down;
+                for (int e = 0; e < 32; ++e) v[e] = masked ? 0.0f : __uint_as_float(o[e]) * down;
                 // (each lane its own row: these are few bytes beside the queries')
                 if (!whole) {
 #pragma unroll
@@ -431,6 +439,7 @@ __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_c
                 sum.w += w[e].w;
             }
         }
+        if (key_masked(p, u, key)) sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         T *to = key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) + col;
         if (p.wide) {
             *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
@@ -470,6 +479,8 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     p.counts = a.counts;
     p.index = a.index;
     p.index_rows = a.index_rows;
+    p.mask = a.mask;
+    p.mask_stride = a.mask_stride;
     p.base2 = a.base2;
     p.delta = a.delta;
     p.amax = a.amax;

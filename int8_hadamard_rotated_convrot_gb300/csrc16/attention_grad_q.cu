@@ -31,8 +31,8 @@ template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
     static constexpr int STAGES = kD == 64 ? 10 : 5;
-    static constexpr int BARS = 2 * STAGES + 8;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int BARS = 3 * STAGES + 8;
+    static constexpr int BAR_BYTES = 384;
     static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;  // S: + 128 for every other tile
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
@@ -42,6 +42,8 @@ struct Cfg {
 struct Params {
     HeadsMap q, dout, k, v;
     const int32_t *counts;
+    const uint8_t *mask;
+    int64_t mask_stride;
     const float *base2, *delta, *amax;
     int64_t amax_blocks;
     void *dq;
@@ -68,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     auto s_full = [&](int i) { return bars + 8u * (2 * C::STAGES + i); };
     const uint32_t q_full = bars + 8u * (2 * C::STAGES + 2), q_empty = q_full + 8, dp_full = q_full + 16, ds_ready = q_full + 24;
     const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
+    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of keys has its zeros
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -76,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
+            mbar_init(clean_bar(s), 2);
         }
         mbar_init(s_full(0), 1);
         mbar_init(s_full(1), 1);
@@ -161,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             uint32_t phase = 0, q_phase = 0, ds_phase = 0;
             int tile_no = 0;  // over all items: which of the two S
             bool ok = true;
-            auto take = [&](int &at) {  // the next stage of the ring, once it is there
-                ok = wait.together(full_bar(stage), phase);
+            auto take = [&](int &at, bool clean = false) {  // the next stage of the ring, once it is there
+                ok = wait.together(clean ? clean_bar(stage) : full_bar(stage), phase);
                 at = stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
                 int k_at, v_at;
-                if (!(ok = wait.together(q_full, q_phase)) || !take(k_at) || !take(v_at)) break;
+                if (!(ok = wait.together(q_full, q_phase)) || !take(k_at, p.mask) || !take(v_at)) break;
                 q_phase ^= 1u;
                 tc_fence_after();
                 if (one_thread()) {
@@ -239,6 +243,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 mma_commit(done_bar);
                 mbar_wait(done_bar, 0);
             }
+        } else if (warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
+            bool ok = true;
+            int entry = 0;
+            MaskedRows rows;
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2) {
+                const int s = entry % C::STAGES;
+                rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
+                if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
+                clean_rows<C::HALVES>(base + kRing + s * C::TILE, rows.there, warp - 2, lane);
+                if (lane == 0) mbar_arrive(clean_bar(s));
+            }
+            if (!ok) wait.fail();
         }
         __syncwarp();
     } else {
@@ -247,6 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const F2 c2(p.scale_log2);
         uint32_t dp_phase = 0, dq_phase = 0;
+        uint32_t there = 0;  // a mask's keys of this thread
+        int masked = -1;     // its sample
         int tile_no = 0;
         bool ok = true;
         for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
@@ -261,6 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             }
             // what dS is multiplied by: P is 2^15 times as large
             const F2 up(kHalf ? exp2i(exponent) * exp2i(-15) : 1.0f), off2(base2), delta2(delta);
+            if (p.mask && it.b != masked) {
+                masked = it.b;
+                there = keys_there(p.mask + it.b * p.mask_stride, part * kPart + lane, p.kv_tokens);
+            }
             for (int j = 0; j < it.tiles; ++j, ++tile_no) {
                 const int b = tile_no & 1;
                 if (!wait(s_full(b), (tile_no >> 1) & 1)) {
@@ -297,6 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     F2 x = F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])) * (F2(__uint_as_float(g[k]), __uint_as_float(g[k + 1])) + delta2);
                     if constexpr (kHalf) x = x * up;
                     pk[k / 2] = pack2<T>(x.lo(), x.hi());
+                }
+                if (p.mask) {  // (a masked value may have made dP NaN)
+#pragma unroll
+                    for (int k = 0; k < kPart; k += 2) pk[k / 2] &= (there & 1u << k ? 0xffffu : 0u) | (there & 2u << k ? 0xffff0000u : 0u);
                 }
                 tmem_st16(lanes + C::DP_COL + kPart * part, pk);
                 tmem_st_wait();
@@ -352,6 +378,8 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     if (a.k.tokens > 0 && (!heads_map<T>(&p.k, a.k, a.batch, a.d, kTileKeys) || !heads_map<T>(&p.v, a.v, a.batch, a.d, kTileKeys)))
         return cudaErrorInvalidValue;
     p.counts = a.counts;
+    p.mask = a.mask;
+    p.mask_stride = a.mask_stride;
     p.base2 = a.base2;
     p.delta = a.delta;
     p.amax = a.amax;

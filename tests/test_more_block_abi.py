@@ -148,7 +148,7 @@ def test_attention_refuses_its_own_operands(lib):
     assert lib.convrot_attention_backward(None, None) == cr.ERR_INVALID_ARG
     for strides in ((768, 256, 0), (768, 32, 64), (0, 256, 64), (768, 256, 256), (64, 256, 64)):  # heads of out over one another
         assert lib.convrot_attention(attention_args(os=strides), None) == cr.ERR_INVALID_ARG
-    assert lib.convrot_attention(attention_args(mask=FAKE, tq=30), None) == cr.ERR_INVALID_ARG  # needs a workspace
+    assert lib.convrot_attention(attention_args(mask=FAKE, tq=30, tk=200), None) == cr.ERR_INVALID_ARG  # needs a workspace
     for kw in (dict(dq=0), dict(dk=0), dict(dv=0), dict(dout=0), dict(work=0), dict(work_bytes=64)):
         assert lib.convrot_attention_backward(attention_grad_args(**kw), None) == cr.ERR_INVALID_ARG
     assert lib.convrot_attention_backward(attention_grad_args(work=FAKE + 8), None) == cr.ERR_ALIGNMENT
@@ -164,8 +164,9 @@ def test_empty_attention_launches_nothing(lib):
 
 def test_attention_workspaces(lib):
     assert lib.convrot_attention_work_bytes(attention_args()) == 0
-    many, rows = dict(tq=30), 2 * 128 * 2 * 64 * 2
-    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE, **many)) == 256 + 2 * rows
+    many, rows = dict(tq=30), 2 * 256 * 2 * 64 * 2
+    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE, **many, tk=200)) == 256 + 2 * rows
+    assert lib.convrot_attention_work_bytes(attention_args(mask=FAKE, **many)) == 0  # a tile's mask is applied in place
     assert lib.convrot_attention_work_bytes(attention_args(q=FAKE + 2, **many)) == 2 * 30 * 4 * 64 * 2
     assert lib.convrot_attention_work_bytes(attention_args(tk=0, mask=FAKE, **many)) == 0
     # few queries: the mask is read as it is, unaligned keys are copied, and long states are shared out over clusters
