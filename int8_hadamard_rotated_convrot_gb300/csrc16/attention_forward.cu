@@ -6,7 +6,10 @@
 // the tensor cores multiply for one, the other's softmax runs. It is persistent
 // over such items.
 //   warp 0       TMA producer: the groups' queries, then the tiles of 128 keys
-//                and values in turn, through one ring
+//                and values in turn, through one ring; where one tile holds
+//                all keys and a head has several items (kStay), the keys and
+//                values stay, and the ring is the queries' (each CTA has a
+//                run of items, so that it meets few heads)
 //   warp 1       tensor memory; one thread issues the MMAs
 //   warps 4-11   the first group's softmax, warps 12-19 the second's: two threads a
 //                row, 64 of the tile's keys each
@@ -64,7 +67,7 @@ struct Params {
     float scale_log2;
 };
 
-template <typename T, int kD>
+template <typename T, int kD, bool kStay>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<kD>;
@@ -132,9 +135,121 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         return it;
     };
 
+    // this CTA's items: every so many, or, where the keys stay, a run of them
+    const int begin = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * blockIdx.x / gridDim.x) : static_cast<int>(blockIdx.x);
+    const int end = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * (blockIdx.x + 1) / gridDim.x) : p.items;
+    const int step = kStay ? 1 : static_cast<int>(gridDim.x);
+    // kStay: whether item i's keys are others than those of the item before
+    auto other_keys = [&](const Item &it, const Item &before) { return it.b != before.b || it.h / p.group != before.h / p.group; };
+    const uint32_t kv_full = q_full(0), kv_empty = q_empty(0);  // kStay
+
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
-        if (warp == 0 && lane == 0) {
+        if (kStay && warp == 0 && lane == 0) {
+            int entry = 0, heads = 0;  // tiles of queries, and of keys
+            bool ok = true;
+            Item it{}, before{};
+            for (int i = begin; i < end && ok; ++i, before = it) {
+                it = item_at(i);
+                if (i == begin || other_keys(it, before)) {
+                    if (!(ok = wait(kv_empty, (heads + 1) & 1))) break;
+                    ++heads;
+                    mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+                    load_tile<C::HALVES>(base, p.k, 0, it.h / p.group, it.b, kv_full);
+                    load_tile<C::HALVES>(base + C::TILE, p.v, 0, it.h / p.group, it.b, kv_full);
+                }
+                for (int g = 0; g < it.groups; ++g, ++entry) {
+                    const int s = entry % C::STAGES;
+                    if (!(ok = wait(empty_bar(s), (entry / C::STAGES + 1) & 1))) break;
+                    mbar_arrive_expect_tx(full_bar(s), C::TILE);
+                    load_tile<C::HALVES>(base + kRing + s * C::TILE, p.q, it.q0 + g * kGroupRows, it.h, it.b, full_bar(s));
+                }
+            }
+            if (!ok) {
+                wait.fail();
+                // copies in flight land before shared memory goes away
+                for (int e = entry > C::STAGES ? entry - C::STAGES : 0; e < entry; ++e) mbar_wait(full_bar(e % C::STAGES), (e / C::STAGES) & 1);
+                if (heads > 0) mbar_wait(kv_full, (heads - 1) & 1);
+            }
+        } else if (kStay && warp == 1) {
+            const uint32_t id_s = idesc<T>(128, 128, false, false);
+            const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
+            const uint32_t id_o = idesc<T>(128, n_o, false, true);
+            int entry = 0, heads = 0;
+            uint32_t p_phase[2] = {0, 0};
+            bool ok = true;
+            auto scores = [&](int g) {  // S = Q K^T, once the next tile of queries is there
+                const int s = entry % C::STAGES;
+                if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) return;
+                ++entry;
+                tc_fence_after();
+                if (one_thread()) {
+                    tile_product<kD>(tmem + C::S_COL + 128 * g, base + kRing + s * C::TILE, base, id_s, steps);
+                    mma_commit(s_full(g));
+                    mma_commit(empty_bar(s));
+                }
+                __syncwarp();
+            };
+            Item it{}, next{};
+            if (begin < end) next = item_at(begin);
+            for (int i = begin; i < end && ok; ++i) {
+                it = next;
+                const bool more = i + 1 < end;
+                if (more) next = item_at(i + 1);
+                const bool leave = more && other_keys(next, it);
+                if (i == begin) {
+                    if (!(ok = wait.together(kv_full, 0))) break;
+                    for (int g = 0; g < it.groups && ok; ++g) scores(g);
+                    if (!ok) break;
+                }
+                if (p.mask && !(ok = wait.together(clean_bar(0), heads & 1))) break;  // (done already, but for a head's first item)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (g < it.groups) {
+                        if (!(ok = wait.together(p_ready(g), p_phase[g]))) break;
+                        p_phase[g] ^= 1u;
+                        tc_fence_after();
+                        if (one_thread()) {
+                            tile_add<2>(tmem + C::O_COL + kD * g, tmem + C::S_COL + 128 * g, base + C::TILE, id_o, true);
+                            mma_commit(o_full(g));
+                        }
+                        __syncwarp();
+                    }
+                    if (more && !leave && g < next.groups) {
+                        scores(g);
+                        if (!ok) break;
+                    }
+                }
+                if (!ok) break;
+                if (leave) {
+                    if (one_thread()) mma_commit(kv_empty);
+                    __syncwarp();
+                    ++heads;
+                    if (!(ok = wait.together(kv_full, heads & 1))) break;
+                    for (int g = 0; g < next.groups && ok; ++g) scores(g);
+                }
+            }
+            if (!ok) wait.fail();
+            if (one_thread()) {
+                mma_commit(done_bar);
+                mbar_wait(done_bar, 0);
+            }
+        } else if (kStay && warp >= 2 && p.mask) {
+            bool ok = true;
+            int heads = 0;
+            MaskedRows rows;
+            Item it{}, before{};
+            for (int i = begin; i < end; ++i, before = it) {
+                it = item_at(i);
+                if (i > begin && !other_keys(it, before)) continue;
+                rows.of(p.mask, p.mask_stride, it.b, p.kv_tokens, warp - 2, lane);
+                if (!(ok = wait.together(kv_full, heads & 1))) break;
+                clean_rows<C::HALVES>(base + C::TILE, rows.there, warp - 2, lane);
+                if (lane == 0) mbar_arrive(clean_bar(0));
+                ++heads;
+            }
+            if (!ok) wait.fail();
+        } else if (!kStay && warp == 0 && lane == 0) {
             int stage = 0;
             uint32_t phase = 0, q_phase[2] = {0, 0};
             uint32_t armed = 0;  // stages and groups whose copies may be in flight
@@ -149,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     phase ^= 1u;
                 }
             };
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            for (int i = begin; i < end && ok; i += step) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
                 for (int g = 0; g < it.groups && ok; ++g) {
@@ -176,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int g = 0; g < 2; ++g)
                     if (armed >> (16 + g) & 1u) mbar_wait(q_full(g), q_phase[g] ^ 1u);
             }
-        } else if (warp == 1) {
+        } else if (!kStay && warp == 1) {
             const uint32_t kIdS = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
@@ -193,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 tile_product<kD>(tmem + C::S_COL + 128 * g, base + g * C::TILE, base + kRing + at * C::TILE, kIdS, steps);
                 mma_commit(s_full(g));
             };
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            for (int i = begin; i < end && ok; i += step) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
                 if (!(ok = wait.together(full_bar(stage), phase))) break;
@@ -248,11 +363,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 mma_commit(done_bar);
                 mbar_wait(done_bar, 0);
             }
-        } else if (warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
+        } else if (!kStay && warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
             bool ok = true;
             int entry = 1;
             MaskedRows rows;
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2) {
+            for (int i = begin; i < end && ok; i += step, entry += 2) {
                 const int s = entry % C::STAGES;
                 rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
                 if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
@@ -287,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         uint32_t s_phase = 0, o_phase = 0;
         uint32_t there[2] = {0, 0};  // a mask's keys of this thread
         int masked = -1;             // its sample
-        for (int i = blockIdx.x; i < p.items && !gone; i += gridDim.x) {
+        for (int i = begin; i < end && !gone; i += step) {
             const Item it = item_at(i);
             if (g >= it.groups) continue;
             if (p.mask && it.b != masked) {
@@ -401,11 +516,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (warp == 1) tmem_free<1>(tmem, 512u);
 }
 
-template <typename T, int kD>
+template <typename T, int kD, bool kStay>
 struct attention_tag;
 
-template <typename T, int kD>
-cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
+template <typename T, int kD, bool kStay>
+cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
 {
     using C = Cfg<kD>;
     Params p{};
@@ -430,10 +545,20 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
     p.d = a.d;
     p.wide = heads_wide(a.out, a.out_strides, a.batch, a.q.tokens, a.q.heads);
     p.scale_log2 = a.scale * kLog2e;
-    auto kernel = attention_kernel<T, kD>;
-    cudaError_t e = allow_shared<attention_tag<T, kD>>(kernel);
+    auto kernel = attention_kernel<T, kD, kStay>;
+    cudaError_t e = allow_shared<attention_tag<T, kD, kStay>>(kernel);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+}
+
+// Keys of one tile stay with a CTA where a key head has four items or more: changing heads stops it for a copy (1.5 us),
+// and with a head an item that would be all the time (2 x 4096 queries, 77 keys, 10 heads of 64: 12.6 us through the ring).
+template <typename T, int kD>
+cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
+{
+    const int64_t of_head = a.q.heads / a.k.heads * ((a.q.tokens + kItemRows - 1) / kItemRows);
+    const bool stay = !a.counts && a.kv_tokens > 0 && a.kv_tokens <= kTileKeys && of_head >= 4;
+    return stay ? launch_form<T, kD, true>(a, stream) : launch_form<T, kD, false>(a, stream);
 }
 
 }  // namespace
