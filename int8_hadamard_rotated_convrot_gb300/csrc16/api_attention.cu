@@ -280,9 +280,8 @@ convrot_status convrot_attention_backward(const convrot_attention_backward_args 
     b.scale = a->scale;
     b.d = a->head_dim;
     b.dtype = a->dtype;
-    for (auto step : {launch_attention_stats, launch_attention_grad_kv, launch_attention_grad_q})
-        if (step(b, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
-    return CONVROT_OK;
+    if (launch_attention_stats(b, stream) != cudaSuccess || launch_attention_grad_kv(b, stream) != cudaSuccess) return CONVROT_ERR_CUDA;
+    return grad_kv_makes_dq(b.kv_tokens, b.d) ? CONVROT_OK : done(launch_attention_grad_q(b, stream));
 }
 
 }  // extern "C"

@@ -88,6 +88,8 @@ struct AttentionGradArgs {
     int32_t d, dtype;
 };
 int64_t grad_kv_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads, int d);
+// Whether launch_attention_grad_kv makes dq too.
+bool grad_kv_makes_dq(int64_t kv_tokens, int d);
 cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stream);
 cudaError_t launch_attention_grad_q(const AttentionGradArgs &a, cudaStream_t stream);
 cudaError_t launch_attention_grad_kv(const AttentionGradArgs &a, cudaStream_t stream);

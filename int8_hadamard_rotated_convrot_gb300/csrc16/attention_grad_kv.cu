@@ -18,6 +18,12 @@
 //                dP^T, and while dS^T is made, dV and the next S^T
 //   warps 4-19   P^T and dS^T: four threads a key, 32 of the tile's queries each
 //
+// kAll: where one tile holds all keys and the heads are narrow, dQ = scale dS K is
+// made here too, from dS^T that the same threads leave in shared memory (an
+// MN-major A operand), into one of two places in tensor memory; the threads read
+// it, 16 elements of a query each, while the next tile's products run. Masked
+// keys have zeros in K for it (warps 2 and 3), and in dS^T.
+//
 // The work of all units, laid end to end, is cut into equal runs of tiles, one a
 // CTA, whatever the number of units: a unit that a cut goes through is left as
 // partial sums in fp32 and added up by a second kernel in the order of the
@@ -35,15 +41,17 @@ constexpr int kRegsWg0 = 64, kRegsMath = 104;
 static_assert(4 * 32 * kRegsWg0 + 32 * kMathWarps * kRegsMath <= kThreads * 96, "register split");
 constexpr int kPart = 32;  // columns of a tile that a thread has
 
-template <int kD>
+template <int kD, bool kAll>
 struct Cfg {
+    static_assert(!kAll || kD == 64, "tensor memory");
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
-    static constexpr int QS = kD == 64 ? 5 : 3, DS = kD == 64 ? 4 : 2;  // tiles of queries, and of dout
-    static constexpr int STATS = 2 * kTileQueries * 4;                  // base2 and delta of a tile: DS of them, too
-    static constexpr int BARS = 2 * QS + 4 * DS + 8;
+    static constexpr int QS = kD == 128 ? 3 : kAll ? 4 : 5, DS = kD == 128 ? 2 : kAll ? 3 : 4;  // tiles of queries, and of dout
+    static constexpr int STATS = 2 * kTileQueries * 4;  // base2 and delta of a tile: DS of them, too
+    static constexpr int DST = kAll ? 2 * kTileBox : 0;  // dS^T of a tile: two of them
+    static constexpr int BARS = 2 * QS + 4 * DS + 11;
     static constexpr int BAR_BYTES = 384;
-    static constexpr int SMEM = (2 + QS + DS) * TILE + DS * STATS + BAR_BYTES;
-    static constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 384;
+    static constexpr int SMEM = (2 + QS + DS) * TILE + 2 * DST + DS * STATS + BAR_BYTES;
+    static constexpr uint32_t S_COL = 0, DP_COL = 128, DV_COL = 256, DK_COL = 384, DQ_COL = 320;  // dQ: + 128 for every other tile
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
 };
@@ -66,11 +74,11 @@ struct Params {
     const float *base2, *delta, *amax;
     int64_t amax_blocks, stat_rows;
     float *partial;  // [runs][2][2][128][kD]: a run's first and last unit where they are cut, dV and dK
-    void *dk, *dv;
+    void *dk, *dv, *dq;
     int32_t *dev_status;
     Cut cut;
-    int32_t kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
-    int32_t d, wide;
+    int32_t q_tokens, kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
+    int32_t d, wide, wide_q;
     float scale, scale_log2;
 };
 
@@ -105,15 +113,15 @@ __device__ __forceinline__ bool key_masked(const Params &p, const Unit &u, int k
     return p.mask && *reinterpret_cast<const volatile uint8_t *>(p.mask + u.b * p.mask_stride + key) == 0;
 }
 
-template <typename T, int kD>
+template <typename T, int kD, bool kAll>
 __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __grid_constant__ Params p)
 {
-    using C = Cfg<kD>;
+    using C = Cfg<kD, kAll>;
     constexpr bool kHalf = std::is_same_v<T, __half>;
     extern __shared__ __align__(1024) uint8_t smem_tiles[];  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_tiles;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem_tiles));
-    constexpr int kQueries = 2 * C::TILE, kDouts = kQueries + C::QS * C::TILE, kStats = kDouts + C::DS * C::TILE, kBars = kStats + C::DS * C::STATS;
+    constexpr int kQueries = 2 * C::TILE, kDouts = kQueries + C::QS * C::TILE, kDst = kDouts + C::DS * C::TILE, kStats = kDst + 2 * C::DST, kBars = kStats + C::DS * C::STATS;
     const uint32_t bars = base + kBars;
     auto q_full = [&](int s) { return bars + 8u * s; };
     auto q_empty = [&](int s) { return bars + 8u * (C::QS + s); };
@@ -123,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
     auto st_empty = [&](int s) { return bars + 8u * (2 * C::QS + 3 * C::DS + s); };
     const uint32_t kv_full = bars + 8u * (2 * C::QS + 4 * C::DS), kv_empty = kv_full + 8, s_full = kv_full + 16, dp_full = kv_full + 24;
     const uint32_t p_ready = kv_full + 32, ds_ready = kv_full + 40;
-    const uint32_t sums_full = kv_full + 48, done_bar = kv_full + 56;
+    const uint32_t sums_full = kv_full + 48, done_bar = kv_full + 56, kv_clean = kv_full + 64;
+    auto dq_full = [&](int n) { return kv_full + 72 + 8u * (n & 1); };
     // the places of tile t, counted over all units of this run, and the parity of their n-th use
     auto q_at = [&](int t) { return base + kQueries + t % C::QS * C::TILE; };
     auto do_at = [&](int t) { return base + kDouts + t % C::DS * C::TILE; };
@@ -154,6 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
         mbar_init(ds_ready, kMathWarps);
         mbar_init(sums_full, 1);
         mbar_init(done_bar, 1);
+        mbar_init(kv_clean, 2);
+        mbar_init(dq_full(0), 1);
+        mbar_init(dq_full(1), 1);
         *wait.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.q.map);
@@ -228,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             const uint32_t id_s = idesc<T>(128, 128, false, false);
             const int n_o = (p.d + 15) / 16 * 16, steps = (p.d + kMmaK - 1) / kMmaK;
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
+            const uint32_t id_q = idesc<T>(128, n_o, true, true);
             int n = 0;  // tiles, over all units
             uint32_t kv_phase = 0;
             auto product = [&](uint32_t to, uint32_t rows, uint32_t cols) { tile_product<kD>(to, rows, cols, id_s, steps); };
@@ -237,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             auto do_there = [&](int t) { return wait.together(do_full(t % C::DS), (t / C::DS) & 1); };
             const bool ok = each_unit([&](const Unit &, int t0, int t1) {
                 if (!wait.together(kv_full, kv_phase) || !q_there(n) || !do_there(n)) return false;
+                if (kAll && p.mask && !wait.together(kv_clean, kv_phase)) return false;
                 kv_phase ^= 1u;
                 tc_fence_after();
                 if (one_thread()) {
@@ -269,6 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     if (one_thread()) {
                         add(tmem + C::DK_COL, tmem + C::DP_COL, q_at(n), t == t0);
                         mma_commit(q_empty(n % C::QS));
+                        if constexpr (kAll) {  // dQ = dS K, over the keys
+                            const Desc a(desc_mn(base + kDst + (n & 1) * C::DST, kTileBox)), b(desc_mn(base, kTileBox));
+                            const uint32_t dq = tmem + C::DQ_COL + 128 * (n & 1);
+                            mma_ss_step<false>(dq, a, 0, b, 0, id_q);
+#pragma unroll
+                            for (int kk = 1; kk < kTileKeys / kMmaK; ++kk) mma_ss_step<true>(dq, a, kStepMN * kk, b, kStepMN * kk, id_q);
+                            mma_commit(dq_full(n));
+                        }
                         if (more) {
                             product(tmem + C::DP_COL, base + C::TILE, do_at(n + 1));
                             mma_commit(dp_full);
@@ -286,6 +308,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 mma_commit(done_bar);
                 mbar_wait(done_bar, 0);
             }
+        } else if (kAll && warp >= 2 && p.mask) {
+            uint32_t kv_phase = 0;
+            MaskedRows rows;
+            const bool ok = each_unit([&](const Unit &u, int, int) {
+                rows.of(p.mask, p.mask_stride, u.b, u.keys, warp - 2, lane);
+                if (!wait.together(kv_full, kv_phase)) return false;
+                kv_phase ^= 1u;
+                clean_rows<C::HALVES>(base, rows.there, warp - 2, lane);
+                if (lane == 0) mbar_arrive(kv_clean);
+                return true;
+            });
+            if (!ok) wait.fail();
         }
         __syncwarp();
     } else {
@@ -300,6 +334,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             if constexpr (kHalf)
                 exponent = grad_exponent(p.amax + (static_cast<int64_t>(u.b) * p.kv_heads + u.h) * p.amax_blocks, p.amax_blocks, lane);
             const F2 up(kHalf ? exp2i(exponent) * exp2i(-15) : 1.0f);
+            const int key = u.tile * kTileKeys + quad * 32 + lane;
+            const bool there = key < u.keys, masked = there && key_masked(p, u, key);
+            // dQ of tile t of this unit, the m-th of this run: 16 elements of a query
+            auto read_dq = [&](int t, int m) {
+                if (!wait(dq_full(m), (m >> 1) & 1)) return false;
+                tc_fence_after();
+                const int h = u.h * p.group + t / p.q_tiles, row = t % p.q_tiles * kTileQueries + quad * 32 + lane, col = part * 16;
+                if (col >= p.d) return true;
+                uint32_t o[16];
+                tmem_ld16_async(lanes + C::DQ_COL + 128 * (m & 1) + col, o);
+                tmem_ld_wait(o);
+                tc_fence_before();
+                if (row >= p.q_tokens) return true;
+                const float down = p.scale * (kHalf ? exp2i(-exponent) : 1.0f);
+                T *to = static_cast<T *>(p.dq) + ((static_cast<int64_t>(u.b) * p.q_tokens + row) * p.q_heads + h) * p.d + col;
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * down;
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    if (p.wide_q) {
+                        if (col + e < p.d)
+                            *reinterpret_cast<uint4 *>(to + e) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
+                                                                            pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int c = e; c < e + 8; ++c)
+                            if (col + c < p.d) to[c] = from_f32<T>(v[c]);
+                    }
+                }
+                return true;
+            };
             for (int t = t0; t < t1; ++t, ++n) {
                 const int ds = n % C::DS;
                 if (!wait(st_full(ds), (n / C::DS) & 1) || !wait(s_full, n & 1)) return false;
@@ -343,6 +409,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     pk[k / 2] = pack2<T>(x0.lo(), x0.hi());
                     pk[k / 2 + 1] = pack2<T>(x1.lo(), x1.hi());
                 }
+                if constexpr (kAll) {
+                    if (!there || masked) {
+#pragma unroll
+                        for (int k = 0; k < kPart / 2; ++k) pk[k] = 0;
+                    }
+                    // row: key; 16-byte piece c of it at c ^ (key & 7), as the descriptor's swizzle has it
+                    const uint32_t row = base + kDst + (n & 1) * C::DST + part / 2 * kTileBox + (quad * 32 + lane) * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((part % 2 * 4 + c) ^ (lane & 7)) * 16), "r"(pk[4 * c]), "r"(pk[4 * c + 1]),
+                                     "r"(pk[4 * c + 2]), "r"(pk[4 * c + 3])
+                                     : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
                 tmem_st16(lanes + C::DP_COL + kPart * part, pk);
                 tmem_st_wait();
                 tc_fence_before();
@@ -351,7 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                     mbar_arrive(ds_ready);
                     mbar_arrive(st_empty(ds));
                 }
+                if (kAll && t > t0 && !read_dq(t - 1, n - 1)) return false;
             }
+            if (kAll && !read_dq(t1 - 1, n - 1)) return false;
             if (!wait(sums_full, sums_phase)) return false;
             sums_phase ^= 1u;
             tc_fence_after();
@@ -359,9 +441,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             const int half = part >> 1;
             const bool whole = t1 - t0 == p.cut.per_unit;
             const float down = half == 0 ? (kHalf ? exp2i(-15) : 1.0f) : p.scale * (kHalf ? exp2i(-exponent) : 1.0f);
-            const int key = u.tile * kTileKeys + quad * 32 + lane;
-            const bool there = key < u.keys;
-            const bool masked = whole && there && key_masked(p, u, key);
             T *row = whole && there ? key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) : nullptr;
             // a run's first unit may start inside, and its last one end inside
             float *shares = p.partial + (((static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * 2 + half) * kTileKeys + quad * 32 + lane) * kD;
@@ -462,13 +541,13 @@ Cut cut_of(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, 
     return c;
 }
 
-template <typename T, int kD>
+template <typename T, int kD, bool kAll>
 struct grad_kv_tag;
 
-template <typename T, int kD>
-cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+template <typename T, int kD, bool kAll>
+cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
 {
-    using C = Cfg<kD>;
+    using C = Cfg<kD, kAll>;
     Params p{};
     p.cut = cut_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads, a.k.heads);
     if (p.cut.work == 0) return cudaSuccess;
@@ -489,7 +568,9 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     p.partial = a.partial;
     p.dk = a.dk;
     p.dv = a.dv;
+    p.dq = a.dq;
     p.dev_status = a.dev_status;
+    p.q_tokens = static_cast<int32_t>(a.q.tokens);
     p.kv_tokens = static_cast<int32_t>(a.kv_tokens);
     p.kv_heads = static_cast<int32_t>(a.k.heads);
     p.q_heads = static_cast<int32_t>(a.q.heads);
@@ -498,16 +579,28 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     p.key_tiles = static_cast<int32_t>((a.kv_tokens + kTileKeys - 1) / kTileKeys);
     p.d = a.d;
     p.wide = aligned_to(a.dk, 16) && aligned_to(a.dv, 16) && a.d % 8 == 0;
+    p.wide_q = aligned_to(a.dq, 16) && a.d % 8 == 0;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
-    auto kernel = attention_grad_kv_kernel<T, kD>;
-    cudaError_t e = allow_shared<grad_kv_tag<T, kD>>(kernel);
+    auto kernel = attention_grad_kv_kernel<T, kD, kAll>;
+    cudaError_t e = allow_shared<grad_kv_tag<T, kD, kAll>>(kernel);
     if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.cut.runs == 1) return e;
     return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / (1024 * kJoinRounds)), 256, 0, stream, 1, p);
 }
 
+template <typename T, int kD>
+cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    if constexpr (kD == 64)
+        if (grad_kv_makes_dq(a.kv_tokens, a.d)) return launch_form<T, kD, true>(a, stream);
+    return launch_form<T, kD, false>(a, stream);
+}
+
 }  // namespace
+
+// (2 x 4096 queries, 77 keys, 10 heads of 64: the other kernel took 15 us for it, 26 with a mask)
+bool grad_kv_makes_dq(int64_t kv_tokens, int d) { return kv_tokens <= kTileKeys && d <= 64; }
 
 int64_t grad_kv_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads, int d)
 {
@@ -524,7 +617,7 @@ cudaError_t launch_attention_grad_kv(const AttentionGradArgs &a, cudaStream_t st
 int attention_grad_kv_shared(int form, int *columns)
 {
     *columns = 512;
-    return form == 0 ? Cfg<64>::SMEM : form == 1 ? Cfg<128>::SMEM : 0;
+    return form == 0 ? Cfg<64, false>::SMEM : form == 1 ? Cfg<128, false>::SMEM : form == 2 ? Cfg<64, true>::SMEM : 0;
 }
 
 }  // namespace convrot
