@@ -2,11 +2,15 @@
 // few that share a key head, against long states. Reading the keys and values
 // once is all that counts, so a unit is a key head of a sample with all of its
 // query heads' rows (16 at most), its keys are shared out over a cluster of
-// CTAs (and, where one cluster is not enough to fill the GPU, over several),
-// and nothing is staged: each warp multiplies straight from registers that wide
-// loads fill, 16 keys at a time, with the warp-level matrix instruction. (Its
-// rate is of no matter here: 16 keys of 128 elements are 8 KB of loads and 32
-// instructions.)
+// CTAs (and, where one cluster is not enough to fill the GPU, over several).
+// Each warp goes through its keys 16 at a time with the warp-level matrix
+// instruction. (Its rate is of no matter here: 16 keys of 128 elements are 8 KB
+// of loads and 32 instructions.) Its keys and values come through a ring of its
+// own that TMA copies fill, which its first lane starts, so that no warp waits
+// for another and nearly all of an SM's shared memory is on its way. (8
+// sequences of one token, 4096 keys, 40 + 8 heads of 128: 32 us with copies by
+// the lanes, 16 bytes each, from registers or through queues of any length: 5.2
+// TB/s however many were in flight.)
 //
 // Both orders that the fragments ask for are had by renaming, not by moving
 // data. In S = Q K^T the elements of a head are summed in any order: a lane
@@ -24,14 +28,16 @@ namespace {
 
 using namespace mma16;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kRows = 16, kStep = 16;  // keys of a warp's step
+constexpr int kWarps = 12, kThreads = 32 * kWarps, kRows = 16, kStep = 16;  // keys of a warp's step
 constexpr int kMaxSplit = 8;
-constexpr int kPerSm = 2;
+constexpr int kPerSm = 1;
 constexpr float kGrow = 8.0f;
 
 struct FewParams {
-    const void *q, *k, *v;
-    int64_t q_strides[3], k_strides[3], v_strides[3], out_strides[3];
+    HeadsMap k, v;
+    const void *q;
+    int64_t q_strides[3], out_strides[3];
+    int32_t *dev_status;
     const uint8_t *mask;
     int64_t mask_stride;
     void *out;
@@ -86,6 +92,16 @@ __device__ __forceinline__ void finish(const FewParams &p, int b, int hk, int ro
         p.lse[(static_cast<int64_t>(b) * p.q_heads + h) * p.q_tokens + t] = total == 0.0f ? neg_inf() : kLn2 * (most + (log2f(total) - shift));
 }
 
+// A warp's ring: steps of 16 keys and values, each a box of 64 elements (128 bytes, swizzled) a row, or two.
+template <int kD>
+struct Ring {
+    static constexpr int kHalves = kD / 64, kBox = kStep * 128, kStepBytes = 2 * kHalves * kBox;
+    static constexpr int kSteps = kD == 64 ? 4 : 2;
+    static constexpr int kSums = kWarps * kRows * (kD + 2) * 4;
+    static constexpr int kBytes = 1024 + (kWarps * kSteps * kStepBytes > kSums ? kWarps * kSteps * kStepBytes : kSums);
+    static_assert(kPerSm * (kBytes + 2048) <= kSmShared, "resident");
+};
+
 template <typename T, int kD>
 __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const __grid_constant__ FewParams p)
 {
@@ -94,7 +110,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const _
     constexpr int kQ = kChunks / 4;        // of a lane, in S
     constexpr int kV = kChunks / 8;        // of a lane and key, in P V
     constexpr int kPitch = kD + 2;         // of a row in shared memory (its maximum and sum behind it)
-    __shared__ float sums[kWarps][kRows][kPitch];
+    using R = Ring<kD>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[kWarps][R::kSteps];
+    __shared__ volatile int abort_flag;
+    const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)), base = (raw + 1023u) & ~1023u;
+    // the warps' sums, when all their steps are done, over the rings
+    float (&sums)[kWarps][kRows][kPitch] = *reinterpret_cast<float (*)[kWarps][kRows][kPitch]>(smem_raw + (base - raw));
+    const Waits wait{&abort_flag, p.dev_status};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * R::kSteps; ++i) mbar_init(static_cast<uint32_t>(__cvta_generic_to_shared(&bars[0][0])) + 8 * i, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        prefetch_map(&p.k.map);
+        prefetch_map(&p.v.map);
+    }
+    __syncthreads();
     after_previous();
     let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -133,31 +164,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const _
 
     const int64_t begin = (static_cast<int64_t>(part) * split + rank) * p.share;
     const int64_t end = begin + p.share < p.kv_tokens ? begin + p.share : p.kv_tokens;
-    const T *k_base = static_cast<const T *>(p.k) + b * p.k_strides[0] + hk * p.k_strides[2];
-    const T *v_base = static_cast<const T *>(p.v) + b * p.v_strides[0] + hk * p.v_strides[2];
     const uint8_t *mask = p.mask ? p.mask + b * p.mask_stride : nullptr;
-    auto there = [&](int64_t key) { return key < end && (!mask || *reinterpret_cast<const volatile uint8_t *>(mask + key) != 0); };
-
-    uint4 kr[2][kQ], vr[4][kV];
-    bool kept[4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of the step
-    auto load_k = [&](int64_t key0) {
+    const uint32_t ring = base + warp * R::kSteps * R::kStepBytes, bar = static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][0]));
+    auto load = [&](int64_t key0, int at) {  // by one lane
+        mbar_arrive_expect_tx(bar + 8 * at, R::kStepBytes);
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int64_t key = key0 + 8 * n + g;
-            const T *from = k_base + key * p.k_strides[1] + t * 8;
-#pragma unroll
-            for (int i = 0; i < kQ; ++i) kr[n][i] = key < end && t + 4 * i < chunks ? load16(from + 32 * i) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < R::kHalves; ++h) {
+            const uint32_t to = ring + at * R::kStepBytes + h * R::kBox;
+            tma_load_4d(to, &p.k.map, h * kBoxElems, static_cast<int>(key0), hk * p.k.head_step, b * p.k.batch_step, bar + 8 * at);
+            tma_load_4d(to + R::kHalves * R::kBox, &p.v.map, h * kBoxElems, static_cast<int>(key0), hk * p.v.head_step, b * p.v.batch_step, bar + 8 * at);
         }
     };
-    auto load_v = [&](int64_t key0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t key = key0 + 2 * t + (j & 1) + (j >> 1) * 8;
-            kept[j] = there(key);
-            const T *from = v_base + key * p.v_strides[1] + g * 8;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) vr[j][i] = kept[j] && g + 8 * i < chunks ? load16(from + 64 * i) : make_uint4(0, 0, 0, 0);
-        }
+    // piece c (16 bytes) of a row of keys or, behind them, values
+    auto piece = [&](int at, int values, int row, int c) {
+        return shared16(ring + at * R::kStepBytes + (values * R::kHalves + c / 8) * R::kBox + row * 128 + ((c ^ row) & 7) * 16);
     };
 
     float o[8 * kV][4];
@@ -167,22 +187,35 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const _
         for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     float top[2] = {neg_inf(), neg_inf()}, sum[2] = {0.0f, 0.0f};  // rows g and g + 8; the sum over this lane's keys
     const float c = p.scale_log2;
-    const int64_t first = begin + warp * kStep;
-    if (first < end) {
-        load_k(first);
-        load_v(first);
+    const int64_t first = begin + warp * kStep, stride = kWarps * kStep;
+    if (lane == 0) {
+        for (int n = 0; n < R::kSteps; ++n)
+            if (first + n * stride < end) load(first + n * stride, n);
     }
-    for (int64_t key0 = first; key0 < end; key0 += kWarps * kStep) {
+    int at = 0;  // the step's place in the ring
+    int flying = 0;  // steps whose copies were started and not waited for
+    for (int n = 0; n < R::kSteps; ++n) flying += first + n * stride < end;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t key0 = first; key0 < end; key0 += stride) {
+        if (!(ok = wait.together(bar + 8 * at, phase))) break;
+        const int left = end - key0 < kStep ? static_cast<int>(end - key0) : kStep;
+        bool kept[4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            constexpr int kKeys[4] = {0, 1, 8, 9};
+            kept[j] = 2 * t + kKeys[j] < left;
+            if (mask && kept[j]) kept[j] = *reinterpret_cast<const volatile uint8_t *>(mask + key0 + 2 * t + kKeys[j]) != 0;
+        }
         float s[2][4] = {};
 #pragma unroll
         for (int i = 0; i < kQ; ++i)
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                mma_warp<T>(s[n], q[2 * i], kr[n][i].x, kr[n][i].y);
-                mma_warp<T>(s[n], q[2 * i + 1], kr[n][i].z, kr[n][i].w);
+                const uint4 k = piece(at, 0, 8 * n + g, t + 4 * i);
+                mma_warp<T>(s[n], q[2 * i], k.x, k.y);
+                mma_warp<T>(s[n], q[2 * i + 1], k.z, k.w);
             }
-        const bool more = key0 + kWarps * kStep < end;
-        if (more) load_k(key0 + kWarps * kStep);
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -220,16 +253,41 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const _
             }
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&vr[0][i]), *v1 = reinterpret_cast<const uint32_t *>(&vr[1][i]);
-            const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&vr[2][i]), *v3 = reinterpret_cast<const uint32_t *>(&vr[3][i]);
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                constexpr int kKeys[4] = {0, 1, 8, 9};
+                v[j] = piece(at, 1, 2 * t + kKeys[j], g + 8 * i);
+                if (mask && !kept[j]) v[j] = make_uint4(0, 0, 0, 0);  // (0 times NaN)
+            }
+            const uint32_t *v0 = reinterpret_cast<const uint32_t *>(&v[0]), *v1 = reinterpret_cast<const uint32_t *>(&v[1]);
+            const uint32_t *v2 = reinterpret_cast<const uint32_t *>(&v[2]), *v3 = reinterpret_cast<const uint32_t *>(&v[3]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {  // element e of the piece, of two keys a register
                 const uint32_t pick = e & 1 ? 0x7632 : 0x5410;
                 mma_warp<T>(o[8 * i + e], pk, __byte_perm(v0[e / 2], v1[e / 2], pick), __byte_perm(v2[e / 2], v3[e / 2], pick));
             }
         }
-        if (more) load_v(key0 + kWarps * kStep);
+        __syncwarp();  // every lane has read the step
+        --flying;
+        if (key0 + R::kSteps * stride < end) {
+            if (lane == 0) load(key0 + R::kSteps * stride, at);
+            ++flying;
+        }
+        if (++at == R::kSteps) {
+            at = 0;
+            phase ^= 1u;
+        }
     }
+    if (!ok) {
+        wait.fail();
+        // copies in flight land before shared memory goes away
+        for (int n = 0; n < R::kSteps; ++n, at = at + 1 == R::kSteps ? 0 : at + 1) {
+            if (at == 0 && n > 0) phase ^= 1u;
+            if (n < flying) mbar_wait(bar + 8 * at, phase);
+        }
+    }
+    __syncthreads();  // the rings are done with
 
     // this warp's rows: o[8 i + e] has columns 2t and 2t + 1, which are elements (2t + 8 i) 8 + e and (2t + 1 + 8 i) 8 + e
 #pragma unroll
@@ -275,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) attention_few_kernel(const _
     else
         __syncthreads();
     // the cluster's: its CTAs share out the elements
-    const uint32_t at0 = static_cast<uint32_t>(__cvta_generic_to_shared(&sums[0][0][0]));
+    const uint32_t at0 = base;
     for (int i = static_cast<int>(rank) * kThreads + threadIdx.x; i < p.rows * p.d; i += static_cast<int>(split) * kThreads) {
         const int row = i / p.d, e = i - row * p.d;
         const uint32_t at = at0 + row * kPitch * 4;
@@ -328,15 +386,25 @@ struct Cut {
     int64_t share;
 };
 
-// As many CTAs as are resident together, each with 64 keys (a step of its four warps) or more.
+// As many CTAs as are resident together, each with 192 keys (a step of its twelve warps) or more; clusters of 1, 2, 4 or 8,
+// since clusters of 4 and 8 leave some SMs of a GPC over (36 and 15 of them fit), and of other sizes more (64 of 7: two rounds).
 Cut cut_of(int64_t units, int64_t kv_tokens)
 {
-    int64_t want = kPerSm * kSms / units, most = (kv_tokens + kWarps * kStep - 1) / (kWarps * kStep);
-    if (want > most) want = most;
-    if (want < 1) want = 1;
-    Cut c;
-    c.split = static_cast<int>(want < kMaxSplit ? want : kMaxSplit);
-    c.parts = static_cast<int>(want / c.split);
+    const int64_t most = (kv_tokens + kWarps * kStep - 1) / (kWarps * kStep);
+    const int room[4] = {kSms, kSms / 2, 36, 15};
+    Cut c{1, 1, 0};
+    for (int i = 1; i < 4; ++i) {
+        const int split = 1 << i;
+        if (units > room[i] || most < split) break;
+        c.split = split;
+    }
+    // Long states of few heads: pairs, as many as fill the GPU, and the second kernel, where the one cluster would leave
+    // half of the SMs idle for eight steps a warp or more (which take longer than that kernel's 3 us).
+    const int64_t pairs = kSms / 2 / units;
+    if (pairs >= c.split && most / c.split >= 8) {
+        c.split = 2;
+        c.parts = static_cast<int>(pairs < most / 2 ? pairs : most / 2);
+    }
     const int64_t ctas = int64_t{c.split} * c.parts;
     c.share = (kv_tokens + ctas - 1) / ctas;
     c.share = (c.share + kStep - 1) / kStep * kStep;
@@ -344,10 +412,15 @@ Cut cut_of(int64_t units, int64_t kv_tokens)
 }
 
 template <typename T, int kD>
+struct few_tag;
+
+template <typename T, int kD>
 cudaError_t launch(const AttentionArgs &a, const FewParams &p, int64_t units, cudaStream_t stream)
 {
-    cudaError_t e = launch_after(attention_few_kernel<T, kD>, dim3(static_cast<unsigned>(units * p.split * p.parts)), kThreads, 0, stream,
-                                 static_cast<unsigned>(p.split), p);
+    auto kernel = attention_few_kernel<T, kD>;
+    cudaError_t e = allow_shared<few_tag<T, kD>>(kernel);
+    if (e == cudaSuccess)
+        e = launch_after(kernel, dim3(static_cast<unsigned>(units * p.split * p.parts)), kThreads, Ring<kD>::kBytes, stream, static_cast<unsigned>(p.split), p);
     if (e != cudaSuccess || p.parts == 1) return e;
     return launch_after(attention_few_join_kernel<T, kD>, dim3(static_cast<unsigned>(units * p.rows)), kD, 0, stream, 1, p);
 }
@@ -366,14 +439,15 @@ cudaError_t launch_attention_few(const AttentionArgs &a, const uint8_t *mask, in
 {
     FewParams p{};
     p.q = a.q.p;
-    p.k = a.k.p;
-    p.v = a.v.p;
     for (int i = 0; i < 3; ++i) {
         p.q_strides[i] = a.q.strides[i];
-        p.k_strides[i] = a.k.strides[i];
-        p.v_strides[i] = a.v.strides[i];
         p.out_strides[i] = a.out_strides[i];
     }
+    const bool bf16 = a.dtype == CONVROT_BF16;
+    if (!(bf16 ? heads_map<__nv_bfloat16>(&p.k, a.k, a.batch, a.d, kStep) && heads_map<__nv_bfloat16>(&p.v, a.v, a.batch, a.d, kStep)
+               : heads_map<__half>(&p.k, a.k, a.batch, a.d, kStep) && heads_map<__half>(&p.v, a.v, a.batch, a.d, kStep)))
+        return cudaErrorInvalidValue;
+    p.dev_status = a.dev_status;
     p.mask = mask;
     p.mask_stride = mask_stride;
     p.out = a.out;

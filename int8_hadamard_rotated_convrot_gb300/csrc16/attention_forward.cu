@@ -36,17 +36,16 @@ constexpr int kSoftmaxWarps = 16, kThreads = 128 + 32 * kSoftmaxWarps;
 constexpr int kRegsWg0 = 64, kRegsSoftmax = 104;
 static_assert(4 * 32 * kRegsWg0 + 32 * kSoftmaxWarps * kRegsSoftmax <= kThreads * 96, "register split");
 constexpr int kHalfKeys = kTileKeys / 2;
-constexpr int kStageRows = 16, kWarpStage = kStageRows * kStagePitch;  // of a warp's staged outputs
 constexpr float kGrow = 8.0f;  // log2 of what a row's probabilities may grow to before O is rescaled
 
 template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
-    static constexpr int STAGES = kD == 64 ? 8 : 4;
+    static constexpr int STAGES = kD == 64 ? 9 : 4;
     static constexpr int BARS = 3 * STAGES + 2 * 5 + 1;
     static constexpr int BAR_BYTES = 384;
     static constexpr int MEET = 2 * 2 * 4 * 2 * 32 * 4;  // maxima of the two threads of a row: in turn, group, quadrant, half
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + kSoftmaxWarps * kWarpStage + MEET + BAR_BYTES;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + MEET + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, O_COL = 256;  // + 128 g and + kD g
     static_assert(SMEM > kTmemAlone && SMEM <= kMaxShared, "no other tensor memory on this SM");
     static_assert(8 * BARS + 8 <= BAR_BYTES, "barriers fit");
@@ -76,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t raw = static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw));
     const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms are 1024-byte aligned
     uint8_t *gbase = smem_raw + (base - raw);
-    constexpr int kRing = 2 * C::TILE, kOut = kRing + C::STAGES * C::TILE, kMeet = kOut + kSoftmaxWarps * kWarpStage, kBars = kMeet + C::MEET;
+    constexpr int kRing = 2 * C::TILE, kMeet = kRing + C::STAGES * C::TILE, kBars = kMeet + C::MEET;
     const uint32_t bars = base + kBars;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
@@ -382,7 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const int g = (warp - 4) >> 3, half = (warp >> 2) & 1 ^ 1, quad = warp & 3;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const uint32_t s_at = lanes + C::S_COL + 128 * g + kHalfKeys * half, o_at = lanes + C::O_COL + kD * g;
-        const uint32_t stage = base + kOut + (warp - 4) * kWarpStage;
         const float c = p.scale_log2;
         // What this thread and the one with the row's other keys tell each other. A warp whose wait ran out says so at the
         // next meeting (kGone, a NaN that no arithmetic gives), and both leave there: neither waits for one that has left.
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
                 }
                 if (rows > 0 && ok)
-                    store_rows<T, kStageRows>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, stage, lane, v);
+                    store_rows_traded<T>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, lane, v);
             }
             tc_fence_before();  // O is read before the next item's first P is announced
         }

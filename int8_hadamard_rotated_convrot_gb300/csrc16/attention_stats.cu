@@ -26,7 +26,7 @@ struct StatParams {
 };
 
 template <typename T, int kD>
-__global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_constant__ StatParams p)
+__global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_constant__ StatParams p)
 {
     __shared__ float tops[8];
     after_previous();
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) attention_stats_kernel(const __grid_const
     // (the heads of a stretch of tokens lie together, so they are read together)
     const int64_t bt = blockIdx.x / p.kv_heads, hk = blockIdx.x - bt * p.kv_heads, b = bt / p.blocks, block = bt - b * p.blocks, bh = b * p.kv_heads + hk;
     const int64_t t0 = block * kStatTokens;
-    constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 4, kStride = 8 * kPerWarp;  // queries of a block's round
+    constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 2, kStride = 8 * kPerWarp;  // queries of a block's round
     const int sub = lane / kLanes, e0 = lane % kLanes * 8;
     const int queries = kStatTokens * p.group;
     float top = 0.0f;

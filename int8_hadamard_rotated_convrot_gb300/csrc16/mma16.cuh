@@ -361,6 +361,12 @@ __device__ __forceinline__ void store_rows_traded(T *y, int64_t ld, int rows, in
             const int r = lane / 4 * 4 + i;
             if (r < rows) *(reinterpret_cast<uint4 *>(y + r * ld) + lane % 4) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
         }
+    } else if (wide && cols % 8 == 0) {
+        if (lane < rows) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i * 8 < cols) *(reinterpret_cast<uint4 *>(y + lane * ld) + i) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
     } else if (lane < rows) {
         unsigned short *to = reinterpret_cast<unsigned short *>(y + lane * ld);
 #pragma unroll
