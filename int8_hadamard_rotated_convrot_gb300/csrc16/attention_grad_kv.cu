@@ -262,26 +262,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 __syncwarp();
                 for (int t = t0; t < t1; ++t, ++n) {
                     const bool more = t + 1 < t1;
-                    if (!wait.together(p_ready, n & 1)) return false;
+                    // (what the ring brings is waited for ahead of what the threads make: the tensor cores idle meanwhile)
+                    if ((more && !q_there(n + 1)) || !wait.together(p_ready, n & 1)) return false;
                     tc_fence_after();
                     if (one_thread()) {
                         add(tmem + C::DV_COL, tmem + C::S_COL, do_at(n), t == t0);
-                        mma_commit(do_empty(n % C::DS));  // (the tile's dP^T came before)
-                    }
-                    __syncwarp();
-                    if (more) {
-                        if (!q_there(n + 1)) return false;
-                        tc_fence_after();
-                        if (one_thread()) {
+                        if (more) {
                             product(tmem + C::S_COL, base, q_at(n + 1));
                             mma_commit(s_full);
                         }
-                        __syncwarp();
+                        mma_commit(do_empty(n % C::DS));  // (the tile's dP^T came before)
                     }
-                    if (!wait.together(ds_ready, n & 1) || (more && !do_there(n + 1))) return false;
+                    __syncwarp();
+                    if ((more && !do_there(n + 1)) || !wait.together(ds_ready, n & 1)) return false;
                     tc_fence_after();
                     if (one_thread()) {
                         add(tmem + C::DK_COL, tmem + C::DP_COL, q_at(n), t == t0);
+                        if (more) {
+                            product(tmem + C::DP_COL, base + C::TILE, do_at(n + 1));
+                            mma_commit(dp_full);
+                        }
                         mma_commit(q_empty(n % C::QS));
                         if constexpr (kAll) {  // dQ = dS K, over the keys
                             const Desc a(desc_mn(base + kDst + (n & 1) * C::DST, kTileBox)), b(desc_mn(base, kTileBox));
@@ -291,10 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                             for (int kk = 1; kk < kTileKeys / kMmaK; ++kk) mma_ss_step<true>(dq, a, kStepMN * kk, b, kStepMN * kk, id_q);
                             mma_commit(dq_full(n));
                         }
-                        if (more) {
-                            product(tmem + C::DP_COL, base + C::TILE, do_at(n + 1));
-                            mma_commit(dp_full);
-                        } else {
+                        if (!more) {
                             mma_commit(kv_empty);
                             mma_commit(sums_full);
                         }

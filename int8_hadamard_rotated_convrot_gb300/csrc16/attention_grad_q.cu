@@ -194,48 +194,46 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 __syncwarp();
                 for (int j = 0; j < it.tiles; ++j, ++tile_no) {
                     const bool last = j + 1 == it.tiles;
-                    // The next S as soon as its keys are there, which may be before or after this tile's dS: their place
-                    // in the ring became free with the last dQ.
-                    bool next = last;
-                    auto scores = [&]() {
+                    int k_next = 0;
+                    if (!last) {
+                        if (!take(k_next)) break;
                         tc_fence_after();
                         if (one_thread()) {
-                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, stage);
+                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
                             mma_commit(s_full((tile_no + 1) & 1));
                         }
                         __syncwarp();
-                        next = true;
-                    };
-                    bool made = false;
-                    for (int tries = 0; tries < 4096 && !made; ++tries) {
-                        if (!next && wait.now(full_bar(stage), phase)) scores();
-                        made = wait.now(ds_ready, ds_phase);
-                        if (next) break;
                     }
-                    if (!made && !(ok = wait.together(ds_ready, ds_phase))) break;
+                    // dQ of this tile and dP of the next, together where its values are there (their place in the ring became
+                    // free with the last dQ)
+                    bool both = !last && wait.now(full_bar(stage), phase);
+                    if (!(ok = wait.together(ds_ready, ds_phase))) break;
                     ds_phase ^= 1u;
+                    if (!last && !both) both = wait.now(full_bar(stage), phase);
                     tc_fence_after();
+                    v_at = stage;
+                    auto next_dp = [&]() {
+                        product(tmem + C::DP_COL, base + C::TILE, v_at);
+                        mma_commit(dp_full);
+                        mma_commit(empty_bar(v_at));
+                        if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
+                    };
                     if (one_thread()) {
                         // (each quarter of the keys has its own quarter of dP's columns)
                         tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
+                        if (both) next_dp();
                         mma_commit(empty_bar(k_at));
                         if (last) mma_commit(dq_full);
                     }
                     __syncwarp();
                     if (last) continue;
-                    if (!next) {
-                        if (!(ok = wait.together(full_bar(stage), phase))) break;
-                        scores();
+                    if (!take(v_at)) break;
+                    if (!both) {
+                        tc_fence_after();
+                        if (one_thread()) next_dp();
+                        __syncwarp();
                     }
-                    if (!take(k_at) || !take(v_at)) break;  // (the first is the one that scores() used)
-                    tc_fence_after();
-                    if (one_thread()) {
-                        product(tmem + C::DP_COL, base + C::TILE, v_at);
-                        mma_commit(dp_full);
-                        mma_commit(empty_bar(v_at));
-                        if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
-                    }
-                    __syncwarp();
+                    k_at = k_next;
                 }
             }
             if (!ok) wait.fail();
