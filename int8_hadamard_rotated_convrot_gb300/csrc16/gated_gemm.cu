@@ -135,6 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     after_previous();
+    let_next_start();
 
     if (warp == 0 && lane == 0) {
         int stage = 0, issued = 0;

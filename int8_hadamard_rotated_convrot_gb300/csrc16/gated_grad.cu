@@ -57,10 +57,9 @@ struct GradParams {
     int32_t wide;    // rows of gate, up and dy start on 16 bytes
 };
 
-template <typename T, int kAct>
-__global__ void __launch_bounds__(32 * kWarps) gated_grad_kernel(const GradParams p)
+template <typename T, int kAct, bool kSums>
+__global__ void __launch_bounds__(32 * kWarps, kSums ? 2 : 3) gated_grad_kernel(const GradParams p)
 {
-    __shared__ float sums[2][kWarps][kCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t col = static_cast<int64_t>(blockIdx.x) * kCols + lane * kPer;
     const int64_t row0 = static_cast<int64_t>(blockIdx.y) * p.chunk, row1 = row0 + p.chunk < p.m ? row0 + p.chunk : p.m;
@@ -106,8 +105,10 @@ __global__ void __launch_bounds__(32 * kWarps) gated_grad_kernel(const GradParam
                     act_and_slope<kAct>(g[i][e], a, slope);
                     dg[e] = d[i][e] * u[i][e] * slope;
                     du[e] = d[i][e] * a;
-                    sg[e] += dg[e];
-                    su[e] += du[e];
+                    if constexpr (kSums) {
+                        sg[e] += dg[e];
+                        su[e] += du[e];
+                    }
                 }
                 Raw<T, kPer> out;
                 out.pack(dg);
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(32 * kWarps) gated_grad_kernel(const GradParam
             }
         }
     }
-    if (!p.partial) return;
+    if constexpr (!kSums) return;
+    __shared__ float sums[2][kWarps][kCols];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
         sums[0][warp][lane * kPer + e] = sg[e];
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t *x, int6
 template <typename T, int kAct>
 cudaError_t launch_form(const GradParams &p, dim3 grid, cudaStream_t stream)
 {
-    return launch_after(gated_grad_kernel<T, kAct>, grid, 32 * kWarps, 0, stream, 1, p);
+    return launch_after(p.partial ? gated_grad_kernel<T, kAct, true> : gated_grad_kernel<T, kAct, false>, grid, 32 * kWarps, 0, stream, 1, p);
 }
 
 template <typename T>
@@ -197,7 +199,8 @@ cudaError_t launch_gated_grad(const convrot_gated_linear_backward_args &a, void 
 {
     GradParams p{a.gate, a.up, a.dy, a.ldgate, a.ldup, a.lddy, dg, du, ldd, partial, a.m, a.n, 0, 0};
     const int64_t chunks = gated_grad_chunks(a.m, a.n);
-    p.chunk = (a.m + chunks - 1) / chunks;
+    // whole rounds of a block: 16 rows
+    p.chunk = ((a.m + chunks - 1) / chunks + 2 * kWarps - 1) / (2 * kWarps) * (2 * kWarps);
     p.wide = mma16::tma_rows(a.gate, a.ldgate, a.m) && mma16::tma_rows(a.up, a.ldup, a.m) && mma16::tma_rows(a.dy, a.lddy, a.m);
     const dim3 grid(static_cast<unsigned>((a.n + kCols - 1) / kCols), static_cast<unsigned>(chunks));
     cudaError_t e = a.dtype == CONVROT_BF16 ? launch_act<__nv_bfloat16>(a.act, p, grid, stream) : launch_act<__half>(a.act, p, grid, stream);
