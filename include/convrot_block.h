@@ -296,7 +296,8 @@ convrot_status convrot_gated_linear(const convrot_gated_linear_args *a, cudaStre
  *   work       256-byte aligned, convrot_gated_linear_backward_work_bytes(a)
  *              bytes: dg and du, the partial column sums, and copies of operands
  *              whose rows do not start on 16 bytes.
- * m == 0: the gradients of the weights and biases are zero.
+ * m == 0: the gradients of the weights and biases are zero. Outputs must not
+ * overlap inputs.
  */
 typedef struct {
     const void *x, *w_gate, *w_up, *gate, *up, *dy;
@@ -331,11 +332,12 @@ convrot_status convrot_gated_linear_backward(const convrot_gated_linear_backward
  *   mask       uint8 [batch, kv_tokens] with mask_stride elements between
  *              batches: 0 where a key is not there; or NULL.
  *   lse        fp32 [batch, q_heads, q_tokens], dense.
- *   scale      finite, > 0.
+ *   scale      > 0, at most 1.7e38.
  *   work       256-byte aligned, convrot_attention_work_bytes(a) bytes: 0, or
- *              room for the keys that are there (with a mask), and for copies of
- *              tensors whose heads do not start on 16 bytes, and for partial
- *              results of calls with few queries.
+ *              room for the keys that are there (with a mask of more than 128
+ *              keys), for copies of tensors whose heads do not start on 16
+ *              bytes, and for partial results of few queries against long
+ *              states. The function reads no memory.
  *   dev_status as for convrot_linear.
  * 1 <= head_dim <= CONVROT_ATTENTION_MAX_D (CONVROT_ERR_UNSUPPORTED above).
  * Probabilities are rounded to dtype for their product with v, whose operands
@@ -370,8 +372,13 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
  * dq, dk, dv   dense [batch, tokens, heads, head_dim] of type dtype; dk and dv are
  *              summed over the query heads that share a head and are 0 at
  *              masked keys.
- * P and dS are rounded to dtype for their products. Sums are fp32, in an order
- * that depends on the sizes (and, with a mask, on the number of keys) alone.
+ * P and dS are rounded to dtype for their products; for CONVROT_F16 they are
+ * scaled by powers of two first, so that small gradients keep their bits. Sums
+ * are fp32, in an order that depends on the sizes (and, with a mask, on the
+ * number of keys) alone. Outputs must not overlap inputs.
+ *   work       256-byte aligned, convrot_attention_backward_work_bytes(a) bytes:
+ *              8 for each query and head, partial sums (40 MB at most), and what
+ *              the forward call's has room for.
  */
 typedef struct {
     const void *q, *k, *v, *out, *dout;

@@ -97,7 +97,7 @@ convrot_status check_shape(const A &a)
     const int64_t sizes[] = {a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.kv_heads};
     for (int64_t v : sizes)
         if (v < 0 || v > kMaxSize) return CONVROT_ERR_INVALID_ARG;
-    if (a.head_dim < 1 || a.reserved || a.mask_stride < 0 || !(a.scale > 0.0f && a.scale <= FLT_MAX)) return CONVROT_ERR_INVALID_ARG;
+    if (a.head_dim < 1 || a.reserved || a.mask_stride < 0 || !(a.scale > 0.0f && a.scale <= FLT_MAX / 2)) return CONVROT_ERR_INVALID_ARG;
     if (a.q_heads > 0 && (a.kv_heads < 1 || a.q_heads % a.kv_heads)) return CONVROT_ERR_INVALID_ARG;
     if (a.head_dim > CONVROT_ATTENTION_MAX_D) return CONVROT_ERR_UNSUPPORTED;
     // tiles are numbered in 32 bits
@@ -161,7 +161,7 @@ struct BackwardWork {
         const int64_t rows = stat_rows(a.q_tokens);
         base2 = w.take<float>(a.batch * a.q_heads * rows);
         delta = w.take<float>(a.batch * a.q_heads * rows);
-        if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.kv_heads * (rows / kStatTokens));
+        if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.kv_heads * stat_blocks(a.q_tokens));
         partial = w.take<float>(grad_kv_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.kv_heads, a.head_dim) / 4);
         q.plan(w, nullptr, 0, false);
         kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, true);

@@ -66,8 +66,10 @@ cudaError_t launch_attention_few(const AttentionArgs &a, const uint8_t *mask, in
 // Rows of each head's statistics in the backward pass: whole tiles of queries.
 constexpr int kTileQueries = 128;
 inline int64_t stat_rows(int64_t tokens) { return (tokens + kTileQueries - 1) / kTileQueries * kTileQueries; }
-// Tokens of one block of the statistics.
-constexpr int kStatTokens = 64;
+// Tokens of one block of the statistics: 64, and more where a head would have over 256 blocks, since what follows takes the
+// largest value of all of a head's.
+inline int64_t stat_tokens(int64_t tokens) { return (stat_rows(tokens) + 64 * 256 - 1) / (64 * 256) * 64; }
+inline int64_t stat_blocks(int64_t tokens) { return (stat_rows(tokens) + stat_tokens(tokens) - 1) / stat_tokens(tokens); }
 
 struct AttentionGradArgs {
     States q, k, v, dout;     // as the kernels read them

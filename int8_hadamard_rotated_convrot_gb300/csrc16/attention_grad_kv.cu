@@ -561,7 +561,7 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.delta = a.delta;
     p.amax = a.amax;
     p.stat_rows = stat_rows(a.q.tokens);
-    p.amax_blocks = p.stat_rows / kStatTokens;
+    p.amax_blocks = stat_blocks(a.q.tokens);
     p.partial = a.partial;
     p.dk = a.dk;
     p.dv = a.dv;

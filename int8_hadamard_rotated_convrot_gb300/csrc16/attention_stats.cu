@@ -2,7 +2,7 @@
 // -lse in base 2, so that a probability is one multiply-add and one exponential,
 // and -delta = -dout . out, so that dS = P (dP - delta) needs no sum over keys.
 //
-// A block takes the queries of kStatTokens tokens and of the heads that share a
+// A block takes the queries of 64 tokens (or more) and of the heads that share a
 // key head; kLanes lanes take one query, 16 bytes of it each, and kBatch of
 // them are loaded together (8190 x 40 heads of 128: 74 us with a query a warp
 // and one in flight). Rows behind the last query get -infinity
@@ -20,7 +20,7 @@ struct StatParams {
     const float *lse;
     float *base2, *delta, *amax;
     int64_t q_tokens, rows;  // rows of a head's statistics
-    int64_t blocks;
+    int64_t blocks, tokens;  // of a head; of a block
     int32_t q_heads, kv_heads, group, d, wide;
     float shift;
 };
@@ -34,10 +34,10 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (the heads of a stretch of tokens lie together, so they are read together)
     const int64_t bt = blockIdx.x / p.kv_heads, hk = blockIdx.x - bt * p.kv_heads, b = bt / p.blocks, block = bt - b * p.blocks, bh = b * p.kv_heads + hk;
-    const int64_t t0 = block * kStatTokens;
+    const int64_t t0 = block * p.tokens;
     constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 2, kStride = 8 * kPerWarp;  // queries of a block's round
     const int sub = lane / kLanes, e0 = lane % kLanes * 8;
-    const int queries = kStatTokens * p.group;
+    const int queries = static_cast<int>(p.tokens) * p.group;
     float top = 0.0f;
     for (int i0 = warp * kPerWarp + sub; i0 - sub < queries; i0 += kStride * kBatch) {
         Raw<T, 8> ro[kBatch], rg[kBatch];
@@ -122,7 +122,8 @@ cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stre
     p.amax = a.amax;
     p.q_tokens = a.q.tokens;
     p.rows = stat_rows(a.q.tokens);
-    p.blocks = p.rows / kStatTokens;
+    p.blocks = stat_blocks(a.q.tokens);
+    p.tokens = stat_tokens(a.q.tokens);
     p.q_heads = static_cast<int32_t>(a.q.heads);
     p.kv_heads = static_cast<int32_t>(a.k.heads);
     p.group = p.q_heads / p.kv_heads;
