@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     auto p_ready = [&](int g) { return bars + 8u * (2 * C::STAGES + 6 + g); };  // P is there, and O rescaled
     auto o_full = [&](int g) { return bars + 8u * (2 * C::STAGES + 8 + g); };
     const uint32_t done_bar = bars + 8u * (2 * C::STAGES + 10);
-    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of values has its zeros
+    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of values, the i-th, has its zeros: i % STAGES
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const uint32_t id_o = idesc<T>(128, n_o, false, true);
             int stage = 0;
             uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            int cleaned = 0;  // masked tiles of values (which are not always those of a stage)
             bool ok = true;
             auto next = [&]() {
                 if (++stage == C::STAGES) {
@@ -329,7 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int j = 0; j < it.tiles; ++j) {
                     const int v_stage = stage;
                     const bool last = j + 1 == it.tiles;
-                    if (!(ok = wait.together(p.mask ? clean_bar(stage) : full_bar(stage), phase))) break;
+                    if (!(ok = p.mask ? wait.together(clean_bar(cleaned % C::STAGES), (cleaned / C::STAGES) & 1) : wait.together(full_bar(stage), phase))) break;
+                    ++cleaned;
                     next();
                     if (!last && !(ok = wait.together(full_bar(stage), phase))) break;
 #pragma unroll
@@ -364,14 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
         } else if (!kStay && warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
             bool ok = true;
-            int entry = 1;
+            int entry = 1, cleaned = 0;
             MaskedRows rows;
-            for (int i = begin; i < end && ok; i += step, entry += 2) {
+            for (int i = begin; i < end && ok; i += step, entry += 2, ++cleaned) {
                 const int s = entry % C::STAGES;
                 rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
                 if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
                 clean_rows<C::HALVES>(base + kRing + s * C::TILE, rows.there, warp - 2, lane);
-                if (lane == 0) mbar_arrive(clean_bar(s));
+                if (lane == 0) mbar_arrive(clean_bar(cleaned % C::STAGES));
             }
             if (!ok) wait.fail();
         }

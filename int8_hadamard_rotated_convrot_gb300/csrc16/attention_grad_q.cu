@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     auto s_full = [&](int i) { return bars + 8u * (2 * C::STAGES + i); };
     const uint32_t q_full = bars + 8u * (2 * C::STAGES + 2), q_empty = q_full + 8, dp_full = q_full + 16, ds_ready = q_full + 24;
     const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
-    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of keys has its zeros
+    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of keys, the i-th, has its zeros: i % STAGES
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -165,8 +165,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             uint32_t phase = 0, q_phase = 0, ds_phase = 0;
             int tile_no = 0;  // over all items: which of the two S
             bool ok = true;
+            int cleaned = 0;  // masked tiles of keys (which are not always those of a stage)
             auto take = [&](int &at, bool clean = false) {  // the next stage of the ring, once it is there
-                ok = wait.together(clean ? clean_bar(stage) : full_bar(stage), phase);
+                ok = clean ? wait.together(clean_bar(cleaned % C::STAGES), (cleaned / C::STAGES) & 1) : wait.together(full_bar(stage), phase);
+                cleaned += clean;
                 at = stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
@@ -243,14 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             }
         } else if (warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
             bool ok = true;
-            int entry = 0;
+            int entry = 0, cleaned = 0;
             MaskedRows rows;
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2) {
+            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2, ++cleaned) {
                 const int s = entry % C::STAGES;
                 rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
                 if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
                 clean_rows<C::HALVES>(base + kRing + s * C::TILE, rows.there, warp - 2, lane);
-                if (lane == 0) mbar_arrive(clean_bar(s));
+                if (lane == 0) mbar_arrive(clean_bar(cleaned % C::STAGES));
             }
             if (!ok) wait.fail();
         }

@@ -231,6 +231,27 @@ def test_attention_gradient(b, tq, tk, hq, hk, d, mask, dtype):
     assert all(torch.equal(got[name], again[name]) for name in got)
 
 
+@TYPES
+@pytest.mark.parametrize("b,tq,tk,hq,hk,d,mask", [
+    (2, 2600, 20, 24, 2, 72, "padded"), (40, 130, 128, 20, 20, 64, "scattered"), (40, 130, 100, 20, 20, 128, "scattered"), (3, 2100, 90, 20, 4, 64, "padded"),
+    (60, 130, 300, 10, 10, 64, "padded"), (2, 2600, 300, 24, 2, 128, "none"), (2, 2600, 400, 24, 8, 64, "none"), (1, 9000, 700, 8, 1, 128, "scattered")])
+def test_attention_many_items(b, tq, tk, hq, hk, d, mask, dtype):
+    """So many items that each ring and each barrier of a CTA comes round several times."""
+    g, q, k, v, there = attention_inputs(b, tq, tk, hq, hk, d, dtype, mask)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bl.convrot_attention(q, k, v, there, dev_status=status)
+    dout = randn(g, b, tq, hq, d, dtype=dtype)
+    got = bl.convrot_attention_backward(q, k, v, out, lse, dout, there, dev_status=status)
+    assert int(status) == 0
+    for i in range(b):  # (sample by sample: the plain form's matrices are large)
+        at = slice(i, i + 1)
+        want = ref.Attention(q[at], k[at], v[at], None if there is None else there[at])
+        close(out[at], want.out, want.out_bound, "out")
+        grads, bound = want.gradient(dout[at])
+        for name in grads:
+            close(got[name][at], grads[name], bound[name], name)
+
+
 def test_attention_gradient_against_differences():
     b, tq, tk, hq, hk, d = 2, 5, 9, 4, 2, 16
     g, q, k, v, there = attention_inputs(b, tq, tk, hq, hk, d, BF16, "padded", seed=3)
