@@ -10,6 +10,7 @@
 // counts here (2 x 77 tokens of 10 heads of 64: 20 us with 32 tokens a block
 // and a piece at a time).
 #include "attention.h"
+#include "mma16.cuh"
 
 namespace convrot {
 namespace {
@@ -93,14 +94,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
             if (row >= 0) {
                 to[n] = (row * a.heads + h) * a.dp + e0;
                 const uint16_t *from = src + t * a.strides[s][1] + h * a.strides[s][2] + e0;
-                if (wide) {
-                    w[n] = __ldcg(reinterpret_cast<const uint4 *>(from));
-                } else {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = e < left ? *reinterpret_cast<const volatile uint16_t *>(from + e) : 0;
-                    w[n] = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-                }
+                w[n] = wide ? __ldcg(reinterpret_cast<const uint4 *>(from)) : mma16::load8_any(from, left);
             } else if (zero && t < a.tokens) {
                 uint16_t *z = zero + ((b * a.tokens + t) * a.heads + h) * a.d + e0;
                 for (int e = 0; e < left; ++e) z[e] = 0;

@@ -78,7 +78,7 @@ struct Params {
     int32_t *dev_status;
     Cut cut;
     int32_t q_tokens, kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
-    int32_t d, wide, wide_q;
+    int32_t d, wide;
     float scale, scale_log2;
 };
 
@@ -350,17 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * down;
 #pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                    if (p.wide_q) {
-                        if (col + e < p.d)
-                            *reinterpret_cast<uint4 *>(to + e) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
-                                                                            pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
-                    } else {
-#pragma unroll
-                        for (int c = e; c < e + 8; ++c)
-                            if (col + c < p.d) to[c] = from_f32<T>(v[c]);
-                    }
-                }
+                for (int e = 0; e < 16; e += 8)
+                    if (col + e < p.d)
+                        store8_any(to + e, make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7])),
+                                   p.d - col - e);
                 return true;
             };
             for (int t = t0; t < t1; ++t, ++n) {
@@ -453,16 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(shares + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                } else if (there && p.wide) {
+                } else if (there) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         if (k + e < p.d)
-                            *reinterpret_cast<uint4 *>(row + k + e) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
-                                                                                 pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
-                } else if (there) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (k + e < p.d) row[k + e] = from_f32<T>(v[e]);
+                            store8_any(row + k + e, make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]), pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7])),
+                                       p.d - k - e);
                 }
             }
             tc_fence_before();  // the sums are read before the next unit's first P is announced
@@ -575,8 +564,7 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.q_tiles = static_cast<int32_t>((a.q.tokens + kTileQueries - 1) / kTileQueries);
     p.key_tiles = static_cast<int32_t>((a.kv_tokens + kTileKeys - 1) / kTileKeys);
     p.d = a.d;
-    p.wide = aligned_to(a.dk, 16) && aligned_to(a.dv, 16) && a.d % 8 == 0;
-    p.wide_q = aligned_to(a.dq, 16) && a.d % 8 == 0;
+    p.wide = aligned_to(a.dk, 8) && aligned_to(a.dv, 8) && a.d % 4 == 0;  // four elements of the second kernel
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
     auto kernel = attention_grad_kv_kernel<T, kD, kAll>;

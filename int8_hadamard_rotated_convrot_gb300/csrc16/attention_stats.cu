@@ -54,14 +54,9 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
                 ro[n].load_stream(o);
                 rg[n].load(g);
             } else {
-                float vo[8], vg[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    vo[e] = e0 + e < p.d ? to_f32(o[e]) : 0.0f;
-                    vg[e] = e0 + e < p.d ? to_f32(g[e]) : 0.0f;
-                }
-                ro[n].pack(vo);
-                rg[n].pack(vg);
+                const int left = p.d - e0 < 8 ? p.d - e0 : 8;
+                ro[n].bits[0] = load8_any(o, left);
+                rg[n].bits[0] = load8_any(g, left);
             }
         }
 #pragma unroll

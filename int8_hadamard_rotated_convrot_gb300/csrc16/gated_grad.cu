@@ -83,12 +83,7 @@ __global__ void __launch_bounds__(32 * kWarps, kSums ? 2 : 3) gated_grad_kernel(
                     for (int t = 0; t < 3; ++t) in[i][t].load_stream(from[t]);
                 } else {
 #pragma unroll
-                    for (int t = 0; t < 3; ++t) {
-                        float one[kPer];
-#pragma unroll
-                        for (int e = 0; e < kPer; ++e) one[e] = e < cols ? to_f32(from[t][e]) : 0.0f;
-                        in[i][t].pack(one);
-                    }
+                    for (int t = 0; t < 3; ++t) in[i][t].bits[0] = mma16::load8_any(from[t], cols);
                 }
             }
 #pragma unroll
@@ -157,14 +152,7 @@ __global__ void __launch_bounds__(256) align_rows_kernel(const uint16_t *x, int6
     const int64_t groups = ldo / 8, total = rows * groups;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t r = i / groups, c = (i - r * groups) * 8;
-        uint16_t v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? *reinterpret_cast<const volatile uint16_t *>(x + r * ld + c + e) : 0;
-        uint4 w;
-        w.x = v[0] | static_cast<uint32_t>(v[1]) << 16;
-        w.y = v[2] | static_cast<uint32_t>(v[3]) << 16;
-        w.z = v[4] | static_cast<uint32_t>(v[5]) << 16;
-        w.w = v[6] | static_cast<uint32_t>(v[7]) << 16;
+        const uint4 w = mma16::load8_any(x + r * ld + c, cols - c < 8 ? static_cast<int>(cols - c) : 8);
         *reinterpret_cast<uint4 *>(out + r * ldo + c) = w;
     }
 }

@@ -285,6 +285,56 @@ struct Waits {
     }
 };
 
+// Eight 16-bit elements from any address, of which the first n (1 to 8) are wanted and the others become 0. The one or two
+// aligned 16-byte blocks that hold wanted elements are read whole, whoever's the rest of them is, and shifted.
+__device__ __forceinline__ uint4 load8_any(const void *p, int n)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const int skip = static_cast<int>(at & 15) / 2;
+    const uint4 *block = reinterpret_cast<const uint4 *>(at & ~uintptr_t{15});
+    auto load = [](const uint4 *from) {
+        uint4 v;
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(from));
+        return v;
+    };
+    uint4 lo = load(block), hi = make_uint4(0, 0, 0, 0);
+    if (skip + n > 8) hi = load(block + 1);
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = skip & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = skip & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = skip & 1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Its counterpart: the first n of eight elements, in the widest pieces that the address allows.
+__device__ __forceinline__ void store8_any(void *p, uint4 v, int n)
+{
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (n >= 8 && at % 16 == 0) {
+        *static_cast<uint4 *>(p) = v;
+    } else if (n >= 4 && n % 4 == 0 && at % 8 == 0) {
+        static_cast<uint2 *>(p)[0] = make_uint2(w[0], w[1]);
+        if (n >= 8) static_cast<uint2 *>(p)[1] = make_uint2(w[2], w[3]);
+    } else {
+        unsigned short *to = static_cast<unsigned short *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (2 * i + 1 < n && at % 4 == 0) {
+                reinterpret_cast<uint32_t *>(to)[i] = w[i];
+            } else {
+                if (2 * i < n) to[2 * i] = static_cast<unsigned short>(w[i] & 0xffffu);
+                if (2 * i + 1 < n) to[2 * i + 1] = static_cast<unsigned short>(w[i] >> 16);
+            }
+        }
+    }
+}
+
 __device__ __forceinline__ int64_t load_i32(const int32_t *p) { return *reinterpret_cast<const volatile int32_t *>(p); }
 
 // One warp's 32 rows (lane: row) of 32 values each, rounded to T and stored:
@@ -361,17 +411,10 @@ __device__ __forceinline__ void store_rows_traded(T *y, int64_t ld, int rows, in
             const int r = lane / 4 * 4 + i;
             if (r < rows) *(reinterpret_cast<uint4 *>(y + r * ld) + lane % 4) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
         }
-    } else if (wide && cols % 8 == 0) {
-        if (lane < rows) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i * 8 < cols) *(reinterpret_cast<uint4 *>(y + lane * ld) + i) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-        }
     } else if (lane < rows) {
-        unsigned short *to = reinterpret_cast<unsigned short *>(y + lane * ld);
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-            if (c < cols) to[c] = static_cast<unsigned short>(c % 2 ? w[c / 8][c % 8 / 2] >> 16 : w[c / 8][c % 8 / 2] & 0xffffu);
+        for (int i = 0; i < 4; ++i)
+            if (i * 8 < cols) store8_any(y + lane * ld + i * 8, make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]), cols - i * 8);
     }
 }
 
