@@ -161,7 +161,7 @@ struct BackwardWork {
         const int64_t rows = stat_rows(a.q_tokens);
         base2 = w.take<float>(a.batch * a.q_heads * rows);
         delta = w.take<float>(a.batch * a.q_heads * rows);
-        if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.kv_heads * stat_blocks(a.q_tokens));
+        if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.q_heads * stat_blocks(a.q_tokens, a.q_heads / a.kv_heads));
         partial = w.take<float>(grad_kv_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.kv_heads, a.head_dim) / 4);
         q.plan(w, nullptr, 0, false);
         kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, true);

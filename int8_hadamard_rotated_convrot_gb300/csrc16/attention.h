@@ -66,10 +66,10 @@ cudaError_t launch_attention_few(const AttentionArgs &a, const uint8_t *mask, in
 // Rows of each head's statistics in the backward pass: whole tiles of queries.
 constexpr int kTileQueries = 128;
 inline int64_t stat_rows(int64_t tokens) { return (tokens + kTileQueries - 1) / kTileQueries * kTileQueries; }
-// Tokens of one block of the statistics: 64, and more where a head would have over 256 blocks, since what follows takes the
-// largest value of all of a head's.
-inline int64_t stat_tokens(int64_t tokens) { return (stat_rows(tokens) + 64 * 256 - 1) / (64 * 256) * 64; }
-inline int64_t stat_blocks(int64_t tokens) { return (stat_rows(tokens) + stat_tokens(tokens) - 1) / stat_tokens(tokens); }
+// Tokens of one block of the statistics (a block has one query head's): 64, and more where the heads that share a key head
+// would have over 256 blocks together, since what follows takes the largest value of all of them.
+inline int64_t stat_tokens(int64_t tokens, int64_t group) { return (stat_rows(tokens) * group + 64 * 256 - 1) / (64 * 256) * 64; }
+inline int64_t stat_blocks(int64_t tokens, int64_t group) { return (stat_rows(tokens) + stat_tokens(tokens, group) - 1) / stat_tokens(tokens, group); }
 
 struct AttentionGradArgs {
     States q, k, v, dout;     // as the kernels read them
@@ -81,7 +81,7 @@ struct AttentionGradArgs {
     int64_t out_strides[3], dout_own_strides[3];  // the caller's out and dout, for the statistics
     const float *lse;
     float *base2, *delta;     // [batch, q_heads, stat_rows]: -lse in base 2, and -dout . out
-    float *amax;              // float16: [batch, kv_heads, blocks] largest |dout|; else null
+    float *amax;              // float16: [batch, kv_heads, q_heads / kv_heads, blocks] largest |dout|; else null
     float *partial;           // grad_kv_partial_bytes
     void *dq, *dk, *dv;
     int32_t *dev_status;

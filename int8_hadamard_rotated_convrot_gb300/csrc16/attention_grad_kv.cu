@@ -79,6 +79,7 @@ struct Params {
     Cut cut;
     int32_t q_tokens, kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
     int32_t d, wide;
+    int32_t join_rounds;  // of a block of the second kernel
     float scale, scale_log2;
 };
 
@@ -468,8 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
 
 // Units that a cut goes through: the blocks of column r add up the one in which run r's end is the first cut, four
 // elements of dV or dK a thread.
-constexpr int kJoinRounds = 4;  // of a block: what it computes of the cuts costs more than a round
-
 template <typename T, int kD>
 __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_constant__ Params p)
 {
@@ -482,8 +481,8 @@ __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_c
     const Unit u = unit_at(p, n);
     const int64_t count = r1 - r0;
 #pragma unroll 1
-    for (int i = 0; i < kJoinRounds; ++i) {
-        const int at = ((blockIdx.y * kJoinRounds + i) * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
+    for (int i = 0; i < p.join_rounds; ++i) {
+        const int at = ((blockIdx.y * p.join_rounds + i) * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
         const int key = u.tile * kTileKeys + row;
         if (key >= u.keys || col >= p.d) continue;
         // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
@@ -550,7 +549,7 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.delta = a.delta;
     p.amax = a.amax;
     p.stat_rows = stat_rows(a.q.tokens);
-    p.amax_blocks = stat_blocks(a.q.tokens);
+    p.amax_blocks = a.q.heads / a.k.heads * stat_blocks(a.q.tokens, a.q.heads / a.k.heads);
     p.partial = a.partial;
     p.dk = a.dk;
     p.dv = a.dv;
@@ -571,7 +570,10 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     cudaError_t e = allow_shared<grad_kv_tag<T, kD, kAll>>(kernel);
     if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.cut.runs == 1) return e;
-    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / (1024 * kJoinRounds)), 256, 0, stream, 1, p);
+    // Four rounds a block, since what it computes of the cuts costs more than a round; one where few units are cut, each many
+    // times (4 units in 152 runs, heads of 80: 17 us with four).
+    p.join_rounds = p.cut.units >= kSms / 2 ? 4 : 1;
+    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / (1024 * p.join_rounds)), 256, 0, stream, 1, p);
 }
 
 template <typename T, int kD>

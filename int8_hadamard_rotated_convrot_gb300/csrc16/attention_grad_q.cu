@@ -384,7 +384,7 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     p.delta = a.delta;
     p.amax = a.amax;
     p.stat_rows = static_cast<int32_t>(stat_rows(a.q.tokens));
-    p.amax_blocks = stat_blocks(a.q.tokens);
+    p.amax_blocks = a.q.heads / a.k.heads * stat_blocks(a.q.tokens, a.q.heads / a.k.heads);
     p.dq = a.dq;
     p.dev_status = a.dev_status;
     p.q_tokens = static_cast<int32_t>(a.q.tokens);

@@ -2,10 +2,11 @@
 // -lse in base 2, so that a probability is one multiply-add and one exponential,
 // and -delta = -dout . out, so that dS = P (dP - delta) needs no sum over keys.
 //
-// A block takes the queries of 64 tokens (or more) and of the heads that share a
-// key head; kLanes lanes take one query, 16 bytes of it each, and kBatch of
-// them are loaded together (8190 x 40 heads of 128: 74 us with a query a warp
-// and one in flight). Rows behind the last query get -infinity
+// A block takes the queries of 64 tokens (or more) of one head; kLanes lanes
+// take one query, 16 bytes of it each, and kBatch of them are loaded together
+// (8190 x 40 heads of 128: 74 us with a query a warp and one in flight). A
+// block a head, also where heads share keys (4 x 1270 x 43 heads on one of
+// keys: 126 us with a block for all 43). Rows behind the last query get -infinity
 // for the first: their probabilities are 0. Bound by HBM: out and dout once.
 #include "attention.cuh"
 
@@ -21,7 +22,7 @@ struct StatParams {
     float *base2, *delta, *amax;
     int64_t q_tokens, rows;  // rows of a head's statistics
     int64_t blocks, tokens;  // of a head; of a block
-    int32_t q_heads, kv_heads, group, d, wide;
+    int32_t q_heads, d, wide;
     float shift;
 };
 
@@ -33,11 +34,11 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
     let_next_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // (the heads of a stretch of tokens lie together, so they are read together)
-    const int64_t bt = blockIdx.x / p.kv_heads, hk = blockIdx.x - bt * p.kv_heads, b = bt / p.blocks, block = bt - b * p.blocks, bh = b * p.kv_heads + hk;
+    const int64_t bt = blockIdx.x / p.q_heads, h = blockIdx.x - bt * p.q_heads, b = bt / p.blocks, block = bt - b * p.blocks, head = b * p.q_heads + h;
     const int64_t t0 = block * p.tokens;
     constexpr int kLanes = kD / 8, kPerWarp = 32 / kLanes, kBatch = 2, kStride = 8 * kPerWarp;  // queries of a block's round
     const int sub = lane / kLanes, e0 = lane % kLanes * 8;
-    const int queries = static_cast<int>(p.tokens) * p.group;
+    const int queries = static_cast<int>(p.tokens);
     float top = 0.0f;
     for (int i0 = warp * kPerWarp + sub; i0 - sub < queries; i0 += kStride * kBatch) {
         Raw<T, 8> ro[kBatch], rg[kBatch];
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
 #pragma unroll
         for (int n = 0; n < kBatch; ++n) {
             const int i = i0 + n * kStride;
-            const int64_t t = t0 + i / p.group, h = hk * p.group + i % p.group;
+            const int64_t t = t0 + i;
             ro[n].bits[0] = rg[n].bits[0] = make_uint4(0, 0, 0, 0);
             if (i >= queries || t >= p.q_tokens || e0 >= p.d) continue;
             const T *o = static_cast<const T *>(p.out) + b * p.out_strides[0] + t * p.out_strides[1] + h * p.out_strides[2] + e0;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
 #pragma unroll
             for (int n = 0; n < kBatch; ++n) {
                 const int i = i0 + n * kStride;
-                const int64_t t = t0 + i / p.group, head = b * p.q_heads + hk * p.group + i % p.group, at = head * p.rows + t;
+                const int64_t t = t0 + i, at = head * p.rows + t;
                 if (i >= queries || t >= p.rows) continue;
                 p.base2[at] = t < p.q_tokens ? fmaf(load_f32(p.lse + head * p.q_tokens + t), -kLog2e, p.shift) : neg_inf();
                 p.delta[at] = -part[n];
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int w = 1; w < 8; ++w) top = fmaxf(top, tops[w]);
-        p.amax[bh * p.blocks + block] = top;
+        p.amax[head * p.blocks + block] = top;  // (a key head's query heads follow each other)
     }
 }
 
@@ -117,13 +118,11 @@ cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stre
     p.amax = a.amax;
     p.q_tokens = a.q.tokens;
     p.rows = stat_rows(a.q.tokens);
-    p.blocks = stat_blocks(a.q.tokens);
-    p.tokens = stat_tokens(a.q.tokens);
+    p.blocks = stat_blocks(a.q.tokens, a.q.heads / a.k.heads);
+    p.tokens = stat_tokens(a.q.tokens, a.q.heads / a.k.heads);
     p.q_heads = static_cast<int32_t>(a.q.heads);
-    p.kv_heads = static_cast<int32_t>(a.k.heads);
-    p.group = p.q_heads / p.kv_heads;
     p.d = a.d;
-    const int64_t blocks = a.batch * p.kv_heads * p.blocks;
+    const int64_t blocks = a.batch * p.q_heads * p.blocks;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
     if (a.dtype == CONVROT_BF16)
