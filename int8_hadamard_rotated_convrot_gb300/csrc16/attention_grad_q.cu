@@ -7,7 +7,10 @@
 // it is persistent over such items. No sums of a softmax are needed any more,
 // so a tile's dS depends on nothing before it.
 //   warp 0       TMA producer: the item's queries and dout, then tiles of keys
-//                and values in turn, through one ring
+//                and values in turn, through one ring; where one tile holds
+//                all keys and a head has several items (kStay), the keys and
+//                values stay, and the ring is the queries' and dout's (each
+//                CTA has a run of items, so that it meets few heads)
 //   warp 1       tensor memory; one thread issues the MMAs
 //   warps 4-19   dS: four threads a row, 32 of the tile's keys each
 // Tensor memory: two tiles of S = Q K^T in turn, so that the next one is
@@ -54,7 +57,7 @@ struct Params {
     float scale, scale_log2;
 };
 
-template <typename T, int kD>
+template <typename T, int kD, bool kStay>
 __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __grid_constant__ Params p)
 {
     using C = Cfg<kD>;
@@ -68,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
     auto s_full = [&](int i) { return bars + 8u * (2 * C::STAGES + i); };
+    // (what is not in the ring, at `base`: an item's queries and dout, or with kStay a head's keys and values)
     const uint32_t q_full = bars + 8u * (2 * C::STAGES + 2), q_empty = q_full + 8, dp_full = q_full + 16, ds_ready = q_full + 24;
     const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
     auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of keys, the i-th, has its zeros: i % STAGES
@@ -106,13 +110,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
 
     struct Item {
         int b, h, q0, keys, tiles;
+        int head;  // of the keys
     };
+    const int first = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * blockIdx.x / gridDim.x) : blockIdx.x;
+    const int end = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * (blockIdx.x + 1) / gridDim.x) : p.items;
+    const int step = kStay ? 1 : gridDim.x;
     auto item_at = [&](int i) {
         Item it;
         const int bh = i / p.q_tiles;
         it.q0 = (i - bh * p.q_tiles) * kTileQueries;
         it.b = bh / p.q_heads;
         it.h = bh - it.b * p.q_heads;
+        it.head = bh / p.group;
         it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
         it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
         return it;
@@ -121,34 +130,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
         if (warp == 0 && lane == 0) {
-            int stage = 0;
+            int stage = 0, head = -1;
             uint32_t phase = 0, q_phase = 0, armed = 0;
             bool ok = true;
-            auto load = [&](const HeadsMap &m, int tile, const Item &it) {
+            auto load = [&](const HeadsMap &m, int token, int head, int b) {
                 if (!ok || !wait(empty_bar(stage), phase ^ 1u)) return void(ok = false);
                 mbar_arrive_expect_tx(full_bar(stage), C::TILE);
-                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, tile * kTileKeys, it.h / p.group, it.b, full_bar(stage));
+                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, token, head, b, full_bar(stage));
                 armed |= 1u << stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
             };
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+            for (int i = first; i < end && ok; i += step) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
-                if (!wait(q_empty, q_phase ^ 1u)) {
-                    ok = false;
-                    break;
+                if (!kStay || it.head != head) {
+                    head = it.head;
+                    if (!wait(q_empty, q_phase ^ 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    q_phase ^= 1u;
+                    mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+                    load_tile<C::HALVES>(base, kStay ? p.k : p.q, kStay ? 0 : it.q0, kStay ? it.h / p.group : it.h, it.b, q_full);
+                    load_tile<C::HALVES>(base + C::TILE, kStay ? p.v : p.dout, kStay ? 0 : it.q0, kStay ? it.h / p.group : it.h, it.b, q_full);
+                    armed |= 1u << 16;
                 }
-                q_phase ^= 1u;
-                mbar_arrive_expect_tx(q_full, 2 * C::TILE);
-                load_tile<C::HALVES>(base, p.q, it.q0, it.h, it.b, q_full);
-                load_tile<C::HALVES>(base + C::TILE, p.dout, it.q0, it.h, it.b, q_full);
-                armed |= 1u << 16;
-                for (int j = 0; j < it.tiles && ok; ++j) {
-                    load(p.k, j, it);
-                    load(p.v, j, it);
+                if constexpr (kStay) {
+                    load(p.q, it.q0, it.h, it.b);
+                    load(p.dout, it.q0, it.h, it.b);
+                } else {
+                    for (int j = 0; j < it.tiles && ok; ++j) {
+                        load(p.k, j * kTileKeys, it.h / p.group, it.b);
+                        load(p.v, j * kTileKeys, it.h / p.group, it.b);
+                    }
                 }
             }
             if (!ok) {
@@ -176,66 +193,121 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 }
                 return ok;
             };
-            // rows of the item by a tile, over the head's elements
-            auto product = [&](uint32_t to, uint32_t rows, int at) { tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps); };
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
-                const Item it = item_at(i);
-                if (it.tiles == 0) continue;
-                int k_at, v_at;
-                if (!(ok = wait.together(q_full, q_phase)) || !take(k_at, p.mask) || !take(v_at)) break;
-                q_phase ^= 1u;
-                tc_fence_after();
-                if (one_thread()) {
-                    product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
-                    mma_commit(s_full(tile_no & 1));
-                    product(tmem + C::DP_COL, base + C::TILE, v_at);
+            if constexpr (kStay) {
+                // S of an item while dS of the one before is made, where they have the same keys
+                int head = -1;
+                auto s_of = [&](int at) {  // Q of an item by the keys
+                    tc_fence_after();
+                    if (one_thread()) {
+                        tile_product<kD>(tmem + C::S_COL + 128 * (tile_no & 1), base + kRing + at * C::TILE, base, id_s, steps);
+                        mma_commit(s_full(tile_no & 1));
+                        mma_commit(empty_bar(at));
+                    }
+                    __syncwarp();
+                    ++tile_no;
+                };
+                auto dp_of = [&](int at) {  // (one thread) dout of an item by the values
+                    tile_product<kD>(tmem + C::DP_COL, base + kRing + at * C::TILE, base + C::TILE, id_s, steps);
                     mma_commit(dp_full);
-                    mma_commit(empty_bar(v_at));
-                    if (it.tiles == 1) mma_commit(q_empty);
-                }
-                __syncwarp();
-                for (int j = 0; j < it.tiles; ++j, ++tile_no) {
-                    const bool last = j + 1 == it.tiles;
-                    int k_next = 0;
-                    if (!last) {
-                        if (!take(k_next)) break;
+                    mma_commit(empty_bar(at));
+                };
+                for (int i = first; i < end && ok; ++i) {
+                    int at;
+                    const int now = item_at(i).head;
+                    if (now != head) {
+                        head = now;
+                        ok = wait.together(q_full, q_phase) && (!p.mask || wait.together(clean_bar(cleaned % C::STAGES), (cleaned / C::STAGES) & 1));
+                        if (!ok) break;
+                        q_phase ^= 1u;
+                        ++cleaned;
+                        if (!take(at)) break;
+                        s_of(at);
+                        if (!take(at)) break;
                         tc_fence_after();
-                        if (one_thread()) {
-                            product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
-                            mma_commit(s_full((tile_no + 1) & 1));
-                        }
+                        if (one_thread()) dp_of(at);
                         __syncwarp();
                     }
-                    // dQ of this tile and dP of the next, together where its values are there (their place in the ring became
-                    // free with the last dQ)
-                    bool both = !last && wait.now(full_bar(stage), phase);
+                    const bool more = i + 1 < end && item_at(i + 1).head == head;
+                    if (more) {
+                        if (!take(at)) break;
+                        s_of(at);
+                        if (!take(at)) break;
+                    }
                     if (!(ok = wait.together(ds_ready, ds_phase))) break;
                     ds_phase ^= 1u;
-                    if (!last && !both) both = wait.now(full_bar(stage), phase);
                     tc_fence_after();
-                    v_at = stage;
-                    auto next_dp = [&]() {
+                    if (one_thread()) {
+                        tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base, id_o, true);
+                        mma_commit(dq_full);
+                        if (more)
+                            dp_of(at);
+                        else
+                            mma_commit(q_empty);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // rows of the item by a tile, over the head's elements
+                auto product = [&](uint32_t to, uint32_t rows, int at) { tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps); };
+                for (int i = first; i < end && ok; i += step) {
+                    const Item it = item_at(i);
+                    if (it.tiles == 0) continue;
+                    int k_at, v_at;
+                    if (!(ok = wait.together(q_full, q_phase)) || !take(k_at, p.mask) || !take(v_at)) break;
+                    q_phase ^= 1u;
+                    tc_fence_after();
+                    if (one_thread()) {
+                        product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
+                        mma_commit(s_full(tile_no & 1));
                         product(tmem + C::DP_COL, base + C::TILE, v_at);
                         mma_commit(dp_full);
                         mma_commit(empty_bar(v_at));
-                        if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
-                    };
-                    if (one_thread()) {
-                        // (each quarter of the keys has its own quarter of dP's columns)
-                        tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
-                        if (both) next_dp();
-                        mma_commit(empty_bar(k_at));
-                        if (last) mma_commit(dq_full);
+                        if (it.tiles == 1) mma_commit(q_empty);
                     }
                     __syncwarp();
-                    if (last) continue;
-                    if (!take(v_at)) break;
-                    if (!both) {
+                    for (int j = 0; j < it.tiles; ++j, ++tile_no) {
+                        const bool last = j + 1 == it.tiles;
+                        int k_next = 0;
+                        if (!last) {
+                            if (!take(k_next)) break;
+                            tc_fence_after();
+                            if (one_thread()) {
+                                product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
+                                mma_commit(s_full((tile_no + 1) & 1));
+                            }
+                            __syncwarp();
+                        }
+                        // dQ of this tile and dP of the next, together where its values are there (their place in the ring became
+                        // free with the last dQ)
+                        bool both = !last && wait.now(full_bar(stage), phase);
+                        if (!(ok = wait.together(ds_ready, ds_phase))) break;
+                        ds_phase ^= 1u;
+                        if (!last && !both) both = wait.now(full_bar(stage), phase);
                         tc_fence_after();
-                        if (one_thread()) next_dp();
+                        v_at = stage;
+                        auto next_dp = [&]() {
+                            product(tmem + C::DP_COL, base + C::TILE, v_at);
+                            mma_commit(dp_full);
+                            mma_commit(empty_bar(v_at));
+                            if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
+                        };
+                        if (one_thread()) {
+                            // (each quarter of the keys has its own quarter of dP's columns)
+                            tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
+                            if (both) next_dp();
+                            mma_commit(empty_bar(k_at));
+                            if (last) mma_commit(dq_full);
+                        }
                         __syncwarp();
+                        if (last) continue;
+                        if (!take(v_at)) break;
+                        if (!both) {
+                            tc_fence_after();
+                            if (one_thread()) next_dp();
+                            __syncwarp();
+                        }
+                        k_at = k_next;
                     }
-                    k_at = k_next;
                 }
             }
             if (!ok) wait.fail();
@@ -243,11 +315,26 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 mma_commit(done_bar);
                 mbar_wait(done_bar, 0);
             }
-        } else if (warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
+        } else if (kStay && warp >= 2 && p.mask) {
+            bool ok = true;
+            int head = -1, cleaned = 0;
+            MaskedRows rows;
+            for (int i = first; i < end && ok; ++i) {
+                const Item it = item_at(i);
+                if (it.head == head) continue;
+                head = it.head;
+                rows.of(p.mask, p.mask_stride, it.b, p.kv_tokens, warp - 2, lane);
+                if (!(ok = wait.together(q_full, cleaned & 1))) break;
+                clean_rows<C::HALVES>(base, rows.there, warp - 2, lane);
+                if (lane == 0) mbar_arrive(clean_bar(cleaned % C::STAGES));
+                ++cleaned;
+            }
+            if (!ok) wait.fail();
+        } else if (!kStay && warp >= 2 && p.mask) {  // (one tile an item: keys, then values)
             bool ok = true;
             int entry = 0, cleaned = 0;
             MaskedRows rows;
-            for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, entry += 2, ++cleaned) {
+            for (int i = first; i < end && ok; i += step, entry += 2, ++cleaned) {
                 const int s = entry % C::STAGES;
                 rows.of(p.mask, p.mask_stride, item_at(i).b, p.kv_tokens, warp - 2, lane);
                 if (!(ok = wait.together(full_bar(s), (entry / C::STAGES) & 1))) break;
@@ -267,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         int masked = -1;     // its sample
         int tile_no = 0;
         bool ok = true;
-        for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        for (int i = first; i < end && ok; i += step) {
             const Item it = item_at(i);
             const int row0 = it.q0 + quad * 32, rows = p.q_tokens - row0 < 32 ? p.q_tokens - row0 : 32;
             const int64_t at = (static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.stat_rows + row0 + lane;
@@ -365,11 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     if (warp == 1) tmem_free<1>(tmem, 512u);
 }
 
-template <typename T, int kD>
+template <typename T, int kD, bool kStay>
 struct grad_q_tag;
 
-template <typename T, int kD>
-cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+template <typename T, int kD, bool kStay>
+cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
 {
     using C = Cfg<kD>;
     Params p{};
@@ -399,10 +486,22 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
     p.wide = aligned_to(a.dq, 16) && a.d % 8 == 0;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
-    auto kernel = attention_grad_q_kernel<T, kD>;
-    cudaError_t e = allow_shared<grad_q_tag<T, kD>>(kernel);
+    auto kernel = attention_grad_q_kernel<T, kD, kStay>;
+    cudaError_t e = allow_shared<grad_q_tag<T, kD, kStay>>(kernel);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+}
+
+// Keys that stay: as in the forward pass (4 x 1270 queries, 20 keys, 43 heads of 80 on one: 64 us with an item's queries,
+// dout, keys and values read after the item before, 34 so). Heads of up to 64 with a tile of keys never come here (grad_kv_makes_dq).
+template <typename T, int kD>
+cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
+{
+    if constexpr (kD > 64) {
+        const int64_t of_head = a.q.heads / a.k.heads * ((a.q.tokens + kTileQueries - 1) / kTileQueries);
+        if (!a.counts && a.kv_tokens > 0 && a.kv_tokens <= kTileKeys && of_head >= 4) return launch_form<T, kD, true>(a, stream);
+    }
+    return launch_form<T, kD, false>(a, stream);
 }
 
 }  // namespace

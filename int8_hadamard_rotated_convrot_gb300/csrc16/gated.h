@@ -1,4 +1,4 @@
-// Launch interface between the C-ABI layer (api16.cu) and the kernels of the
+// Launch interface between the C-ABI layer (api_gated.cu) and the kernels of the
 // gated feed-forward's projections (include/convrot_block.h). Arguments are
 // validated; operands have rows that start on 16 bytes.
 #pragma once

@@ -56,14 +56,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
                      : "memory");
 }
 
-// A in tensor memory: lane = row, two elements of K a column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accumulate)
-{
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(accumulate)
-                 : "memory");
-}
-
 // The same as parts of a longer sum, for tiles of 128 x 128, whose issue counts: an instruction takes the tensor cores 64
 // cycles, and one thread that computes its operands in a branch of its own took 80 to 140 for its issue. So the issuing
 // warp stays together up to the instruction itself (one_thread), which lets its operands live in uniform registers; the
@@ -94,6 +86,7 @@ __device__ __forceinline__ void mma_ss_step(uint32_t d, Desc a, uint32_t a_step,
                      : "memory");
 }
 
+// A in tensor memory: lane = row, two elements of K a column.
 template <bool kAccumulate>
 __device__ __forceinline__ void mma_ts_step(uint32_t d, uint32_t a, Desc b, uint32_t b_step, uint32_t id)
 {
@@ -204,16 +197,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
-        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
-        "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(v[0]),
@@ -338,43 +321,36 @@ __device__ __forceinline__ void store8_any(void *p, uint4 v, int n)
 __device__ __forceinline__ int64_t load_i32(const int32_t *p) { return *reinterpret_cast<const volatile int32_t *>(p); }
 
 // One warp's 32 rows (lane: row) of 32 values each, rounded to T and stored:
-// staged in shared memory (`stage`, kStageRows x 80 bytes of this warp's own:
-// 16-byte accesses of eight rows meet all banks) and written four lanes a row,
-// 64 bytes of each. `rows` and `cols` of them exist; wide: rows start on 16 bytes; with
-// an index, row r goes to y's row index[r].
+// staged in shared memory (`stage`, kStageBytes of this warp's own: with 80
+// bytes a row, 16-byte accesses of eight rows meet all banks) and written four
+// lanes a row, 64 bytes of each. `rows` and `cols` of them exist; wide: rows
+// start on 16 bytes.
 constexpr int kStagePitch = 80, kStageBytes = 32 * kStagePitch;
 
-template <typename T, int kStageRows = 32>
-__device__ __forceinline__ void store_rows(T *y, int64_t ld, int rows, int cols, bool wide, uint32_t stage, int lane, const float (&v)[32],
-                                           const int32_t *index = nullptr)
+template <typename T>
+__device__ __forceinline__ void store_rows(T *y, int64_t ld, int rows, int cols, bool wide, uint32_t stage, int lane, const float (&v)[32])
 {
-    static_assert(sizeof(T) == 2 && 32 % kStageRows == 0);
+    static_assert(sizeof(T) == 2, "16-bit elements");
+    __syncwarp();  // the last box has been read
 #pragma unroll
-    for (int first = 0; first < 32; first += kStageRows) {
-        __syncwarp();  // the last box has been read
-        if (lane / kStageRows * kStageRows == first) {
+    for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * kStagePitch + 16 * i), "r"(pack2<T>(v[8 * i], v[8 * i + 1])),
+                     "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])), "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
+                     : "memory");
+    __syncwarp();
+    if (wide && cols >= 32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane % kStageRows * kStagePitch + 16 * i),
-                             "r"(pack2<T>(v[8 * i], v[8 * i + 1])), "r"(pack2<T>(v[8 * i + 2], v[8 * i + 3])),
-                             "r"(pack2<T>(v[8 * i + 4], v[8 * i + 5])), "r"(pack2<T>(v[8 * i + 6], v[8 * i + 7]))
-                             : "memory");
+        for (int i = 0; i < 4; ++i) {
+            const int r = i * 8 + lane / 4;
+            const uint4 u = shared16(stage + r * kStagePitch + lane % 4 * 16);
+            if (r < rows) *(reinterpret_cast<uint4 *>(y + r * ld) + lane % 4) = u;
         }
-        __syncwarp();
-        if (wide && cols >= 32) {
-#pragma unroll
-            for (int i = 0; i < kStageRows / 8; ++i) {
-                const int at = i * 8 + lane / 4, r = first + at;
-                const uint4 u = shared16(stage + at * kStagePitch + lane % 4 * 16);
-                if (r < rows) *(reinterpret_cast<uint4 *>(y + (index ? load_i32(index + r) : r) * ld) + lane % 4) = u;
-            }
-        } else if (lane < cols) {
+    } else if (lane < cols) {
 #pragma unroll 4
-            for (int at = 0; at < kStageRows && first + at < rows; ++at) {
-                unsigned short u;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(stage + at * kStagePitch + lane * 2) : "memory");
-                reinterpret_cast<unsigned short *>(y)[(index ? load_i32(index + first + at) : first + at) * ld + lane] = u;
-            }
+        for (int r = 0; r < rows && r < 32; ++r) {
+            unsigned short u;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(stage + r * kStagePitch + lane * 2) : "memory");
+            reinterpret_cast<unsigned short *>(y)[r * ld + lane] = u;
         }
     }
 }
