@@ -79,7 +79,6 @@ struct Params {
     Cut cut;
     int32_t q_tokens, kv_tokens, kv_heads, q_heads, group, q_tiles, key_tiles;
     int32_t d, wide;
-    int32_t join_rounds;  // of a block of the second kernel
     float scale, scale_log2;
 };
 
@@ -467,48 +466,63 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
     if (warp == 1) tmem_free<1>(tmem, 512u);
 }
 
-// Units that a cut goes through: the blocks of column r add up the one in which run r's end is the first cut, four
+// Units that a cut goes through: the blocks of column r add up the one in which run r's end is the first cut (or unit r), four
 // elements of dV or dK a thread.
-template <typename T, int kD>
+template <typename T, int kD, int kRounds>
 __global__ void __launch_bounds__(256) attention_grad_join_kernel(const __grid_constant__ Params p)
 {
     after_previous();
     let_next_start();
-    const int64_t cut_at = p.cut.start(blockIdx.x + 1), n = cut_at / p.cut.per_unit, begin = n * p.cut.per_unit;
-    if (cut_at == begin) return;                     // between units
+    // (a column a unit, where there are fewer of them than cuts)
+    const bool by_cut = p.cut.units >= p.cut.runs;
+    const int64_t cut_at = by_cut ? p.cut.start(blockIdx.x + 1) : 0, n = by_cut ? cut_at / p.cut.per_unit : blockIdx.x, begin = n * p.cut.per_unit;
+    if (by_cut && cut_at == begin) return;           // between units
     const int64_t r0 = p.cut.run_of(begin), r1 = p.cut.run_of(begin + p.cut.per_unit - 1);
-    if (r0 != blockIdx.x) return;                    // an earlier column's
+    if (by_cut ? r0 != blockIdx.x : r0 == r1) return;  // an earlier column's; not cut
     const Unit u = unit_at(p, n);
-    const int64_t count = r1 - r0;
-#pragma unroll 1
-    for (int i = 0; i < p.join_rounds; ++i) {
-        const int at = ((blockIdx.y * p.join_rounds + i) * 256 + threadIdx.x) * 4, half = at / (kTileKeys * kD), row = at / kD % kTileKeys, col = at % kD;
-        const int key = u.tile * kTileKeys + row;
-        if (key >= u.keys || col >= p.d) continue;
-        // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
-        const float *first = p.partial + (r0 * 2 + 1) * 2 * kTileKeys * kD + at, *other = p.partial + (r0 + 1) * 4 * kTileKeys * kD + at;
-        float4 sum = __ldcg(reinterpret_cast<const float4 *>(first));
-        constexpr int kBatch = 8;
-        for (int64_t r = 0; r < count; r += kBatch) {
-            float4 w[kBatch];
+    const int count = static_cast<int>(r1 - r0);
+    // the unit starts in run r0, as its last unit or its only one, and before all others, whose first one it is
+    const float *first = p.partial + (r0 * 2 + 1) * 2 * kTileKeys * kD, *other = p.partial + (r0 + 1) * 4 * kTileKeys * kD;
+    int at[kRounds], key[kRounds];
+    bool here[kRounds];
+    float4 sum[kRounds];
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e)
-                if (r + e < count) w[e] = __ldcg(reinterpret_cast<const float4 *>(other + (r + e) * 4 * kTileKeys * kD));
+    for (int i = 0; i < kRounds; ++i) {
+        at[i] = ((blockIdx.y * kRounds + i) * 256 + threadIdx.x) * 4;
+        key[i] = u.tile * kTileKeys + at[i] / kD % kTileKeys;
+        here[i] = key[i] < u.keys && at[i] % kD < p.d;
+        if (here[i]) sum[i] = __ldcg(reinterpret_cast<const float4 *>(first + at[i]));
+    }
+    constexpr int kBatch = 8 / kRounds;  // of the others at a time, all rounds together: 8 loads in flight
+    for (int r = 0; r < count; r += kBatch) {
+        float4 w[kBatch][kRounds];
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-                if (r + e >= count) break;
-                sum.x += w[e].x;
-                sum.y += w[e].y;
-                sum.z += w[e].z;
-                sum.w += w[e].w;
+        for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i)
+                if (r + e < count && here[i]) w[e][i] = __ldcg(reinterpret_cast<const float4 *>(other + static_cast<int64_t>(r + e) * 4 * kTileKeys * kD + at[i]));
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            if (r + e >= count) break;
+#pragma unroll
+            for (int i = 0; i < kRounds; ++i) {
+                sum[i].x += w[e][i].x;
+                sum[i].y += w[e][i].y;
+                sum[i].z += w[e][i].z;
+                sum[i].w += w[e][i].w;
             }
         }
-        if (key_masked(p, u, key)) sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        T *to = key_row<T>(p, u, half == 0 ? p.dv : p.dk, key) + col;
+    }
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        if (!here[i]) continue;
+        if (key_masked(p, u, key[i])) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int col = at[i] % kD;
+        T *to = key_row<T>(p, u, at[i] / (kTileKeys * kD) == 0 ? p.dv : p.dk, key[i]) + col;
         if (p.wide) {
-            *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
+            *reinterpret_cast<uint2 *>(to) = make_uint2(pack2<T>(sum[i].x, sum[i].y), pack2<T>(sum[i].z, sum[i].w));
         } else {
-            const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+            const float v[4] = {sum[i].x, sum[i].y, sum[i].z, sum[i].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (col + e < p.d) to[e] = from_f32<T>(v[e]);
@@ -570,10 +584,13 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     cudaError_t e = allow_shared<grad_kv_tag<T, kD, kAll>>(kernel);
     if (e == cudaSuccess) e = launch_after(kernel, dim3(static_cast<unsigned>(p.cut.runs)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.cut.runs == 1) return e;
-    // Four rounds a block, since what it computes of the cuts costs more than a round; one where few units are cut, each many
-    // times (4 units in 152 runs, heads of 80: 17 us with four).
-    p.join_rounds = p.cut.units >= kSms / 2 ? 4 : 1;
-    return launch_after(attention_grad_join_kernel<T, kD>, dim3(static_cast<unsigned>(p.cut.runs - 1), 2 * kTileKeys * kD / (1024 * p.join_rounds)), 256, 0, stream, 1, p);
+    // Four rounds a block, since what it computes of the cuts costs more than a round (40 heads of 128, 4 tiles of keys: 16 us
+    // one after the other, 11 together); one where few units are cut, each many times (4 units in 152 runs, heads of 80: 17 us
+    // with four and a column a cut, 7 so).
+    const unsigned columns = static_cast<unsigned>(p.cut.units < p.cut.runs ? p.cut.units : p.cut.runs - 1), rounds = 2 * kTileKeys * kD / 1024;
+    if (columns >= kSms / 2)
+        return launch_after(attention_grad_join_kernel<T, kD, 4>, dim3(columns, rounds / 4), 256, 0, stream, 1, p);
+    return launch_after(attention_grad_join_kernel<T, kD, 1>, dim3(columns, rounds), 256, 0, stream, 1, p);
 }
 
 template <typename T, int kD>

@@ -34,7 +34,7 @@ template <int kD>
 struct Cfg {
     static constexpr int HALVES = kD / 64, TILE = HALVES * kTileBox;
     static constexpr int STAGES = kD == 64 ? 10 : 5;
-    static constexpr int BARS = 3 * STAGES + 8;
+    static constexpr int BARS = 3 * STAGES + 10;
     static constexpr int BAR_BYTES = 384;
     static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + BAR_BYTES;
     static constexpr uint32_t S_COL = 0, DP_COL = 256, DQ_COL = 384;  // S: + 128 for every other tile
@@ -71,10 +71,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (C::STAGES + s); };
     auto s_full = [&](int i) { return bars + 8u * (2 * C::STAGES + i); };
-    // (what is not in the ring, at `base`: an item's queries and dout, or with kStay a head's keys and values)
+    // What is not in the ring, at `base`: an item's queries and, with barriers of their own, dout; or with kStay a head's keys and
+    // values.
     const uint32_t q_full = bars + 8u * (2 * C::STAGES + 2), q_empty = q_full + 8, dp_full = q_full + 16, ds_ready = q_full + 24;
-    const uint32_t dq_full = q_full + 32, done_bar = q_full + 40;
-    auto clean_bar = [&](int s) { return done_bar + 8u * (1 + s); };  // a masked tile of keys, the i-th, has its zeros: i % STAGES
+    const uint32_t dq_full = q_full + 32, done_bar = q_full + 40, dout_full = q_full + 48, dout_empty = q_full + 56;
+    auto clean_bar = [&](int s) { return q_full + 64 + 8u * s; };  // a masked tile of keys, the i-th, has its zeros: i % STAGES
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + kBars + 8 * C::BARS);
     const Waits wait{reinterpret_cast<volatile int *>(tmem_slot + 1), p.dev_status};
     const int warp = warp_number(), lane = threadIdx.x & 31;
@@ -93,6 +94,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         mbar_init(ds_ready, kMathWarps);
         mbar_init(dq_full, 1);
         mbar_init(done_bar, 1);
+        mbar_init(dout_full, 1);
+        mbar_init(dout_empty, 1);
         *wait.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         prefetch_map(&p.q.map);
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWg0));
         if (warp == 0 && lane == 0) {
             int stage = 0, head = -1;
-            uint32_t phase = 0, q_phase = 0, armed = 0;
+            uint32_t phase = 0, q_phase = 0, dout_phase = 0, armed = 0;
             bool ok = true;
             auto load = [&](const HeadsMap &m, int token, int head, int b) {
                 if (!ok || !wait(empty_bar(stage), phase ^ 1u)) return void(ok = false);
@@ -146,23 +149,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             for (int i = first; i < end && ok; i += step) {
                 const Item it = item_at(i);
                 if (it.tiles == 0) continue;
-                if (!kStay || it.head != head) {
-                    head = it.head;
-                    if (!wait(q_empty, q_phase ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    q_phase ^= 1u;
-                    mbar_arrive_expect_tx(q_full, 2 * C::TILE);
-                    load_tile<C::HALVES>(base, kStay ? p.k : p.q, kStay ? 0 : it.q0, kStay ? it.h / p.group : it.h, it.b, q_full);
-                    load_tile<C::HALVES>(base + C::TILE, kStay ? p.v : p.dout, kStay ? 0 : it.q0, kStay ? it.h / p.group : it.h, it.b, q_full);
-                    armed |= 1u << 16;
-                }
                 if constexpr (kStay) {
+                    if (it.head != head) {
+                        head = it.head;
+                        if (!(ok = wait(q_empty, q_phase ^ 1u))) break;
+                        q_phase ^= 1u;
+                        mbar_arrive_expect_tx(q_full, 2 * C::TILE);
+                        load_tile<C::HALVES>(base, p.k, 0, it.h / p.group, it.b, q_full);
+                        load_tile<C::HALVES>(base + C::TILE, p.v, 0, it.h / p.group, it.b, q_full);
+                        armed |= 1u << 16;
+                    }
                     load(p.q, it.q0, it.h, it.b);
                     load(p.dout, it.q0, it.h, it.b);
                 } else {
-                    for (int j = 0; j < it.tiles && ok; ++j) {
+                    load(p.k, 0, it.h / p.group, it.b);
+                    if (!ok || !(ok = wait(q_empty, q_phase ^ 1u))) break;
+                    mbar_arrive_expect_tx(q_full, C::TILE);
+                    load_tile<C::HALVES>(base, p.q, it.q0, it.h, it.b, q_full);
+                    armed |= 1u << 16;
+                    q_phase ^= 1u;
+                    load(p.v, 0, it.h / p.group, it.b);
+                    if (!ok || !(ok = wait(dout_empty, dout_phase ^ 1u))) break;
+                    mbar_arrive_expect_tx(dout_full, C::TILE);
+                    load_tile<C::HALVES>(base + C::TILE, p.dout, it.q0, it.h, it.b, dout_full);
+                    armed |= 1u << 17;
+                    dout_phase ^= 1u;
+                    for (int j = 1; j < it.tiles && ok; ++j) {
                         load(p.k, j * kTileKeys, it.h / p.group, it.b);
                         load(p.v, j * kTileKeys, it.h / p.group, it.b);
                     }
@@ -172,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 wait.fail();
                 for (int s = 0; s < C::STAGES; ++s)  // copies in flight land before shared memory goes away
                     if (armed >> s & 1u) mbar_wait(full_bar(s), s < stage ? phase : phase ^ 1u);
-                if (armed >> 16) mbar_wait(q_full, q_phase ^ 1u);
+                if (armed >> 16 & 1u) mbar_wait(q_full, q_phase ^ 1u);
+                if (armed >> 17 & 1u) mbar_wait(dout_full, dout_phase ^ 1u);
             }
         } else if (warp == 1) {
             const uint32_t id_s = idesc<T>(128, 128, false, false);
@@ -247,67 +260,119 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     __syncwarp();
                 }
             } else {
-                // rows of the item by a tile, over the head's elements
-                auto product = [&](uint32_t to, uint32_t rows, int at) { tile_product<kD>(to, rows, base + kRing + at * C::TILE, id_s, steps); };
-                for (int i = first; i < end && ok; i += step) {
-                    const Item it = item_at(i);
-                    if (it.tiles == 0) continue;
-                    int k_at, v_at;
-                    if (!(ok = wait.together(q_full, q_phase)) || !take(k_at, p.mask) || !take(v_at)) break;
+                uint32_t dout_phase = 0;
+                auto s_of = [&](int at) {  // (one thread) the item's queries by a tile of keys
+                    tile_product<kD>(tmem + C::S_COL + 128 * (tile_no & 1), base, base + kRing + at * C::TILE, id_s, steps);
+                    mma_commit(s_full(tile_no & 1));
+                };
+                auto dp_of = [&](int at, bool last) {  // (one thread) its dout by the values; last: of the item
+                    tile_product<kD>(tmem + C::DP_COL, base + C::TILE, base + kRing + at * C::TILE, id_s, steps);
+                    mma_commit(dp_full);
+                    mma_commit(empty_bar(at));
+                    if (last) mma_commit(dout_empty);
+                };
+                int i = first - step;
+                auto item_after = [&]() {  // the next item that has keys; without one, tiles is 0
+                    Item it{};
+                    for (i += step; i < end; i += step) {
+                        it = item_at(i);
+                        if (it.tiles > 0) break;
+                    }
+                    if (i >= end) it.tiles = 0;
+                    return it;
+                };
+                Item it = item_after();
+                int k_at = 0, v_at = 0;
+                if (it.tiles > 0 && (ok = wait.together(q_full, q_phase)) && take(k_at, p.mask)) {
                     q_phase ^= 1u;
                     tc_fence_after();
                     if (one_thread()) {
-                        product(tmem + C::S_COL + 128 * (tile_no & 1), base, k_at);
-                        mma_commit(s_full(tile_no & 1));
-                        product(tmem + C::DP_COL, base + C::TILE, v_at);
-                        mma_commit(dp_full);
-                        mma_commit(empty_bar(v_at));
+                        s_of(k_at);
                         if (it.tiles == 1) mma_commit(q_empty);
                     }
                     __syncwarp();
-                    for (int j = 0; j < it.tiles; ++j, ++tile_no) {
-                        const bool last = j + 1 == it.tiles;
+                    ++tile_no;
+                    if ((ok = wait.together(dout_full, dout_phase)) && take(v_at)) {
+                        dout_phase ^= 1u;
+                        tc_fence_after();
+                        if (one_thread()) dp_of(v_at, it.tiles == 1);
+                        __syncwarp();
+                    }
+                }
+                while (ok && it.tiles > 0) {
+                    const Item then = item_after();
+                    for (int j = 0; j + 1 < it.tiles; ++j) {
+                        const int left = it.tiles - j - 1;  // tiles of the item after this one
                         int k_next = 0;
-                        if (!last) {
-                            if (!take(k_next)) break;
-                            tc_fence_after();
-                            if (one_thread()) {
-                                product(tmem + C::S_COL + 128 * ((tile_no + 1) & 1), base, k_next);
-                                mma_commit(s_full((tile_no + 1) & 1));
-                            }
-                            __syncwarp();
+                        if (!take(k_next)) break;
+                        tc_fence_after();
+                        if (one_thread()) {
+                            s_of(k_next);
+                            if (left == 1) mma_commit(q_empty);
                         }
+                        __syncwarp();
+                        ++tile_no;
                         // dQ of this tile and dP of the next, together where its values are there (their place in the ring became
                         // free with the last dQ)
-                        bool both = !last && wait.now(full_bar(stage), phase);
+                        bool both = wait.now(full_bar(stage), phase);
                         if (!(ok = wait.together(ds_ready, ds_phase))) break;
                         ds_phase ^= 1u;
-                        if (!last && !both) both = wait.now(full_bar(stage), phase);
+                        if (!both) both = wait.now(full_bar(stage), phase);
                         tc_fence_after();
                         v_at = stage;
-                        auto next_dp = [&]() {
-                            product(tmem + C::DP_COL, base + C::TILE, v_at);
-                            mma_commit(dp_full);
-                            mma_commit(empty_bar(v_at));
-                            if (j + 2 == it.tiles) mma_commit(q_empty);  // (the last S came before)
-                        };
                         if (one_thread()) {
                             // (each quarter of the keys has its own quarter of dP's columns)
                             tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, j == 0);
-                            if (both) next_dp();
+                            if (both) dp_of(v_at, left == 1);
                             mma_commit(empty_bar(k_at));
-                            if (last) mma_commit(dq_full);
                         }
                         __syncwarp();
-                        if (last) continue;
                         if (!take(v_at)) break;
                         if (!both) {
                             tc_fence_after();
-                            if (one_thread()) next_dp();
+                            if (one_thread()) dp_of(v_at, left == 1);
                             __syncwarp();
                         }
                         k_at = k_next;
                     }
+                    if (!ok) break;
+                    // After the last tile, S and dP of the next item's first: its queries came since the last S, its dout since
+                    // the last dP.
+                    const bool more = then.tiles > 0;
+                    int k_next = 0;
+                    auto next_s = [&]() {
+                        if (!(ok = wait.together(q_full, q_phase)) || !take(k_next, p.mask)) return false;
+                        q_phase ^= 1u;
+                        tc_fence_after();
+                        if (one_thread()) {
+                            s_of(k_next);
+                            if (then.tiles == 1) mma_commit(q_empty);
+                        }
+                        __syncwarp();
+                        ++tile_no;
+                        return true;
+                    };
+                    const bool early = more && !p.mask && wait.now(q_full, q_phase) && wait.now(full_bar(stage), phase);
+                    if (early && !next_s()) break;
+                    if (!(ok = wait.together(ds_ready, ds_phase))) break;
+                    ds_phase ^= 1u;
+                    tc_fence_after();
+                    if (one_thread()) {
+                        tile_add<4>(tmem + C::DQ_COL, tmem + C::DP_COL, base + kRing + k_at * C::TILE, id_o, it.tiles == 1);
+                        mma_commit(dq_full);
+                        mma_commit(empty_bar(k_at));
+                    }
+                    __syncwarp();
+                    if (more) {
+                        if (!early && !next_s()) break;
+                        if (!(ok = wait.together(dout_full, dout_phase)) || !take(v_at)) break;
+                        dout_phase ^= 1u;
+                        tc_fence_after();
+                        if (one_thread()) dp_of(v_at, then.tiles == 1);
+                        __syncwarp();
+                    }
+                    k_at = k_next;
+                    it = then;
                 }
             }
             if (!ok) wait.fail();
