@@ -376,6 +376,10 @@ def convrot_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: t
 # ---------------------------------------------------------------- attention to other states
 
 
+def _scale(q: torch.Tensor, scale: float | None) -> float:
+    return (q.shape[-1] or 1)**-0.5 if scale is None else scale  # (heads of no elements are refused with the other arguments)
+
+
 def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: torch.Tensor | None = None, *,
                       scale: float | None = None, out: torch.Tensor | None = None, work: torch.Tensor | None = None,
                       dev_status: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -386,7 +390,7 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: t
     mask [batch, keys' tokens] (bool or uint8) says which keys are there; a query without any has out 0 and lse -inf, and
     what stands at a masked key does not count, whatever it is. scale: head_dim^-0.5 by default. Each query attends to all
     keys that are there. ``work`` (uint8) is allocated here when not given."""
-    got = load().attention(q, k, v, mask, q.shape[-1]**-0.5 if scale is None else scale, out, work, dev_status, stream)
+    got = load().attention(q, k, v, mask, _scale(q, scale), out, work, dev_status, stream)
     if isinstance(got, int):
         raise ConvrotError(got, "convrot_attention")
     return got
@@ -398,7 +402,7 @@ def convrot_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
                                stream=None) -> dict[str, torch.Tensor]:
     """The gradients dq, dk and dv (a dict) of convrot_attention's inputs, from its results and the gradient dout of out;
     mask and scale are the forward call's. dk and dv are those of the shared heads, and 0 at masked keys."""
-    got = load().attention_backward(q, k, v, out, lse, dout, mask, q.shape[-1]**-0.5 if scale is None else scale, work, dev_status, stream)
+    got = load().attention_backward(q, k, v, out, lse, dout, mask, _scale(q, scale), work, dev_status, stream)
     if not isinstance(got, dict):
         raise ConvrotError(got, "convrot_attention_backward")
     return got

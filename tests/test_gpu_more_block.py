@@ -341,6 +341,14 @@ def test_attention_without_queries_or_keys(dtype):
         assert not any(t.any() for t in got.values())
 
 
+def test_attention_of_no_elements_is_refused():
+    q = torch.empty(1, 2, 1, 0, dtype=BF16, device="cuda")
+    with pytest.raises(cr.ConvrotError):
+        bl.convrot_attention(q, q, q)
+    with pytest.raises(cr.ConvrotError):
+        bl.convrot_attention_backward(q, q, q, q, torch.empty(1, 1, 2, device="cuda"), q)
+
+
 def test_attention_mask_layouts():
     """uint8 masks with any value, one for all samples, and rows that start anywhere."""
     g, q, k, v, _ = attention_inputs(3, 20, 203, 2, 2, 32, BF16)
