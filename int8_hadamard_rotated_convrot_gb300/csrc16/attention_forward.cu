@@ -22,6 +22,15 @@
 // (probabilities may be up to 2^8 meanwhile, the sums are fp32). float16 has few
 // exponents below 1, so there P is 2^7 times as large, which the division by the
 // sum takes back.
+//
+// 32760 queries, heads of 128: 1520 TFLOP/s at 4096 keys and 10 heads, 1210 at 512
+// keys and 40 heads (283 us), where an item is four tiles. Neither the tensor cores
+// (48 % busy there) nor the issue slots (50 %) bound it: a group's softmax waits for
+// P V and S, one behind the other, and these for it, 1.7 us a tile for both
+// groups, of which 1.05 are products. A second S for each group would need 640
+// columns. Issuing S of the next item before this one's outputs, or fetching its
+// queries to L2 ahead, changed nothing: the softmax warps are what an item's end
+// waits for.
 #include "attention.cuh"
 
 namespace convrot {

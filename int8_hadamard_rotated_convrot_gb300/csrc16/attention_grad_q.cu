@@ -17,6 +17,10 @@
 // multiplied while dS is made, dP, whose columns then hold dS (16 bits, the A
 // operand of dS K), and the sums dQ. The tile of keys is read K-major for S
 // and MN-major for dQ from the same bytes.
+//
+// 8190 queries, 512 keys, 40 heads of 128: 116 us, 47 % of it products; each tile's dS
+// stands between its dP and its dQ. The last tile of an item has code of its own,
+// since conditions for it in the loop cost the issuing warp 5 % of the time of all.
 #include "attention.cuh"
 
 namespace convrot {

@@ -7,7 +7,8 @@
 // (8190 x 40 heads of 128: 74 us with a query a warp and one in flight). A
 // block a head, also where heads share keys (4 x 1270 x 43 heads on one of
 // keys: 126 us with a block for all 43). Rows behind the last query get -infinity
-// for the first: their probabilities are 0. Bound by HBM: out and dout once.
+// for the first: their probabilities are 0. Bound by HBM: out and dout once
+// (8190 x 40 heads of 128: 33 us, 5.1 TB/s).
 #include "attention.cuh"
 
 namespace convrot {
