@@ -23,14 +23,14 @@
 // exponents below 1, so there P is 2^7 times as large, which the division by the
 // sum takes back.
 //
-// 32760 queries, heads of 128: 1520 TFLOP/s at 4096 keys and 10 heads, 1210 at 512
-// keys and 40 heads (283 us), where an item is four tiles. Neither the tensor cores
-// (48 % busy there) nor the issue slots (50 %) bound it: a group's softmax waits for
-// P V and S, one behind the other, and these for it, 1.7 us a tile for both
-// groups, of which 1.05 are products. A second S for each group would need 640
-// columns. Issuing S of the next item before this one's outputs, or fetching its
-// queries to L2 ahead, changed nothing: the softmax warps are what an item's end
-// waits for.
+// 32760 queries, heads of 128: 1515 TFLOP/s at 4096 keys and 10 heads (453 us), 1210 at
+// 512 keys and 40 heads (283 us), where an item is four tiles. The products with
+// their copies and waits, without a softmax, take 415 and 245 us of these, so the
+// softmax is nearly hidden: half of the exponentials, the maxima and the exchange
+// between a row's threads are 3 % together. Two CTAs that share each tile of keys
+// (products of 256 x 128) were slower, 665 us: every turn waits for both. Issuing
+// S of the next item before this one's outputs, or fetching its queries to L2
+// ahead, changed nothing.
 #include "attention.cuh"
 
 namespace convrot {
