@@ -235,7 +235,8 @@ def test_attention_gradient(b, tq, tk, hq, hk, d, mask, dtype):
 @pytest.mark.parametrize("b,tq,tk,hq,hk,d,mask", [
     (2, 2600, 20, 24, 2, 72, "padded"), (40, 130, 128, 20, 20, 64, "scattered"), (40, 130, 100, 20, 20, 128, "scattered"), (3, 2100, 90, 20, 4, 64, "padded"),
     (60, 130, 300, 10, 10, 64, "padded"), (2, 2600, 300, 24, 2, 128, "none"), (2, 2600, 400, 24, 8, 64, "none"), (1, 9000, 700, 8, 1, 128, "scattered"),
-    (30, 500, 100, 20, 20, 128, "scattered"), (2, 2600, 90, 24, 2, 80, "none")])
+    (30, 500, 100, 20, 20, 128, "scattered"), (2, 2600, 90, 24, 2, 80, "none"),
+    (5, 4000, 130, 1, 1, 100, "none")])
 def test_attention_many_items(b, tq, tk, hq, hk, d, mask, dtype):
     """So many items that each ring and each barrier of a CTA comes round several times."""
     g, q, k, v, there = attention_inputs(b, tq, tk, hq, hk, d, dtype, mask)
