@@ -377,7 +377,7 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
  * are fp32, in an order that depends on the sizes (and, with a mask, on the
  * number of keys) alone. Outputs must not overlap inputs.
  *   work       256-byte aligned, convrot_attention_backward_work_bytes(a) bytes:
- *              8 for each query and head, partial sums (40 MB at most), and what
+ *              8 for each query and head, partial sums (50 MB at most), and what
  *              the forward call's has room for.
  */
 typedef struct {

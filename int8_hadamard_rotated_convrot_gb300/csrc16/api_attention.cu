@@ -144,6 +144,7 @@ struct ForwardWork {
         } else {
             q.plan(w, nullptr, 0, false);
             kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, false);
+            partial = w.take<float>(attention_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.head_dim) / 4);
         }
         bytes = w.used;
     }
@@ -151,7 +152,7 @@ struct ForwardWork {
 
 struct BackwardWork {
     Operands q, kv;  // queries and dout
-    float *base2, *delta, *amax = nullptr, *partial;
+    float *base2, *delta, *amax = nullptr, *partial, *partial_q;
     int64_t bytes;
     explicit BackwardWork(const convrot_attention_backward_args &a, char *base = nullptr)
         : q(a.batch, a.head_dim, states(a.q, a.q_tokens, a.q_heads, a.q_strides), states(a.dout, a.q_tokens, a.q_heads, a.dout_strides)),
@@ -163,6 +164,7 @@ struct BackwardWork {
         delta = w.take<float>(a.batch * a.q_heads * rows);
         if (a.dtype == CONVROT_F16) amax = w.take<float>(a.batch * a.q_heads * stat_blocks(a.q_tokens, a.q_heads / a.kv_heads));
         partial = w.take<float>(grad_kv_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.kv_heads, a.head_dim) / 4);
+        partial_q = w.take<float>(grad_q_partial_bytes(a.batch, a.q_tokens, a.kv_tokens, a.q_heads, a.head_dim) / 4);
         q.plan(w, nullptr, 0, false);
         kv.plan(w, mask_in_place(a.kv_tokens) ? nullptr : a.mask, a.mask_stride, true);
         bytes = w.used;
@@ -217,6 +219,8 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
     b.scale = a->scale;
     b.d = a->head_dim;
     b.dtype = a->dtype;
+    b.splits = attention_splits(a->batch, a->q_tokens, a->kv_tokens, a->q_heads);
+    b.partial = w.partial;
     return done(w.few ? launch_attention_few(b, a->mask, a->mask_stride, w.partial, stream) : launch_attention(b, stream));
 }
 
@@ -271,6 +275,7 @@ convrot_status convrot_attention_backward(const convrot_attention_backward_args 
     b.delta = w.delta;
     b.amax = w.amax;
     b.partial = w.partial;
+    b.partial_q = w.partial_q;
     b.dq = a->dq;
     b.dk = a->dk;
     b.dv = a->dv;

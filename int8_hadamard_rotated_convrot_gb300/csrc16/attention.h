@@ -55,8 +55,24 @@ struct AttentionArgs {
     int64_t kv_tokens;      // at most
     float scale;
     int32_t d, dtype;
+    int32_t splits;         // shares of the keys, each with items of its own: attention_splits
+    float *partial;         // attention_partial_bytes, where there are several
 };
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t stream);
+// Shares of the keys, where the items (some queries of a head each) are few and the keys long: as many as the SMs take at once,
+// if that saves an item six tiles of keys or more, since the second kernel that puts the shares together costs as much as about
+// five (16 items of 64 queries, 4096 keys: 38 -> 15 us; 64 items, 1000 keys: 12.6 us whole, 13.1 in two; 72 items, 600 keys:
+// 11.4 and 14.8). A second kernel's warp has one lane a share.
+inline int32_t key_shares(int64_t items, int64_t kv_tokens)
+{
+    const int64_t tiles = (kv_tokens + kTileKeys - 1) / kTileKeys;
+    if (items == 0 || items > kSms / 2) return 1;
+    int64_t shares = kSms / items < tiles / 2 ? kSms / items : tiles / 2;
+    if (shares > 32) shares = 32;
+    return shares > 1 && tiles - (tiles + shares - 1) / shares >= 6 ? static_cast<int32_t>(shares) : 1;
+}
+int32_t attention_splits(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads);
+int64_t attention_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int d);
 
 // Few queries: keys and values whose heads start on 16 bytes (queries may start anywhere), the mask read as it is.
 bool attention_few_takes(int64_t q_tokens, int64_t q_heads, int64_t kv_heads);
@@ -83,6 +99,7 @@ struct AttentionGradArgs {
     float *base2, *delta;     // [batch, q_heads, stat_rows]: -lse in base 2, and -dout . out
     float *amax;              // float16: [batch, kv_heads, q_heads / kv_heads, blocks] largest |dout|; else null
     float *partial;           // grad_kv_partial_bytes
+    float *partial_q;         // grad_q_partial_bytes
     void *dq, *dk, *dv;
     int32_t *dev_status;
     int64_t batch, kv_tokens;
@@ -90,6 +107,7 @@ struct AttentionGradArgs {
     int32_t d, dtype;
 };
 int64_t grad_kv_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int64_t kv_heads, int d);
+int64_t grad_q_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int d);
 // Whether launch_attention_grad_kv makes dq too.
 bool grad_kv_makes_dq(int64_t kv_tokens, int d);
 cudaError_t launch_attention_stats(const AttentionGradArgs &a, cudaStream_t stream);

@@ -23,6 +23,11 @@
 // exponents below 1, so there P is 2^7 times as large, which the division by the
 // sum takes back.
 //
+// Where the items are fewer than half the SMs and the keys long, the keys are
+// shared out: an item is some queries and a share of their keys, its outputs stay
+// fp32, and a second kernel weighs the shares by their lse (key_shares; 64 queries,
+// 8 heads of 128, 77000 keys: 811 us whole, 62 so).
+//
 // 32760 queries, heads of 128: 1515 TFLOP/s at 4096 keys and 10 heads (453 us), 1210 at
 // 512 keys and 40 heads (283 us), where an item is four tiles. The products with
 // their copies and waits, without a softmax, take 415 and 245 us of these, so the
@@ -73,6 +78,10 @@ struct Params {
     int32_t q_tiles, items;
     int32_t d, wide;
     float scale_log2;
+    int32_t splits;
+    float *partial;  // [splits][rows of all heads][pitch]: a share's outputs, and behind them [splits][rows] its lse
+    int64_t rows;
+    int32_t pitch;
 };
 
 template <typename T, int kD, bool kStay>
@@ -130,15 +139,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     // item -> (sample, head, first query); the tiles of one head follow each other and share its keys in L2
     struct Item {
         int b, h, q0, keys, tiles, groups;
+        int first, share;  // tile; of the keys
     };
     auto item_at = [&](int i) {
         Item it;
+        it.share = kStay ? 0 : i % p.splits;
+        if (!kStay) i /= p.splits;
         const int bh = i / p.q_tiles;
         it.q0 = (i - bh * p.q_tiles) * kItemRows;
         it.b = bh / p.q_heads;
         it.h = bh - it.b * p.q_heads;
         it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
         it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
+        it.first = 0;
+        if (!kStay && p.splits > 1) {
+            it.first = static_cast<int>(static_cast<int64_t>(it.tiles) * it.share / p.splits);
+            it.tiles = static_cast<int>(static_cast<int64_t>(it.tiles) * (it.share + 1) / p.splits) - it.first;
+        }
         it.groups = p.q_tokens - it.q0 > kGroupRows ? 2 : 1;
         return it;
     };
@@ -265,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             auto load = [&](const HeadsMap &m, int tile, const Item &it) {
                 if (!ok || !wait(empty_bar(stage), phase ^ 1u)) return void(ok = false);
                 mbar_arrive_expect_tx(full_bar(stage), C::TILE);
-                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, tile * kTileKeys, it.h / p.group, it.b, full_bar(stage));
+                load_tile<C::HALVES>(base + kRing + stage * C::TILE, m, (it.first + tile) * kTileKeys, it.h / p.group, it.b, full_bar(stage));
                 armed |= 1u << stage;
                 if (++stage == C::STAGES) {
                     stage = 0;
@@ -428,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < kHalfKeys; k += 32) tmem_ld32_async(s_at + k, r + k);
                 tmem_ld_wait(r);
-                const int keys = it.keys - j * kTileKeys - half * kHalfKeys;
+                const int keys = it.keys - (it.first + j) * kTileKeys - half * kHalfKeys;
                 if (p.mask) {
 #pragma unroll
                     for (int k = 0; k < kHalfKeys; ++k)
@@ -489,9 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             if (gone) break;
             sum = half == 0 ? sum + theirs : theirs + sum;
             const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
+            // (of this share, where there are several: the second kernel puts them together)
+            const int64_t row = it.share * p.rows + (static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane;
             if (half == 0 && lane < rows)
-                p.lse[(static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane] =
-                    sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
+                (p.splits > 1 ? p.partial + p.splits * p.rows * p.pitch : p.lse)[row] = sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
             T *out = static_cast<T *>(p.out) + it.b * p.out_strides[0] + row0 * p.out_strides[1] + it.h * p.out_strides[2];
             if (it.tiles > 0) {
                 ok = __all_sync(0xffffffffu, wait(o_full(g), o_phase));
@@ -511,6 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
                 }
+                if (!kStay && p.splits > 1) {
+                    if (lane < rows && ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (k + e < p.pitch) *reinterpret_cast<float4 *>(p.partial + row * p.pitch + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                    continue;
+                }
                 if (rows > 0 && ok)
                     store_rows_traded<T>(out + k, p.out_strides[1], rows, p.d - k < 32 ? p.d - k : 32, p.wide, lane, v);
             }
@@ -523,6 +549,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_free<1>(tmem, 512u);
+}
+
+struct JoinParams {
+    const float *partial;
+    int32_t splits, pitch, d, q_heads;
+    int64_t rows, q_tokens;
+    void *out;
+    int64_t out_strides[3];
+    float *lse;
+};
+
+// A row of the outputs from its shares, weighted by e^(lse of the share - lse): a warp a row, four elements a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ JoinParams p)
+{
+    after_previous();
+    let_next_start();
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31, e0 = lane * 4;
+    if (row >= p.rows) return;
+    const float *lses = p.partial + p.splits * p.rows * p.pitch;
+    const float mine = lane < p.splits ? load_f32(lses + lane * p.rows + row) : neg_inf();
+    float top = mine;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float weight = top == neg_inf() && mine == top ? 0.0f : ex2((mine - top) * kLog2e);  // (NaN stays)
+    float sum = weight;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < p.splits; ++s) {
+        const float w = __shfl_sync(0xffffffffu, weight, s);
+        if (e0 >= p.d) continue;
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.partial + (s * p.rows + row) * p.pitch + e0));
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    if (lane == 0) p.lse[row] = sum == 0.0f ? neg_inf() : top + logf(sum);
+    const int64_t bh = row / p.q_tokens, t = row - bh * p.q_tokens, b = bh / p.q_heads, h = bh - b * p.q_heads;
+    T *out = static_cast<T *>(p.out) + b * p.out_strides[0] + t * p.out_strides[1] + h * p.out_strides[2] + e0;
+    const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e0 + e < p.d) out[e] = from_f32<T>(v[e]);
 }
 
 template <typename T, int kD, bool kStay>
@@ -548,7 +621,11 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
     p.q_heads = static_cast<int32_t>(a.q.heads);
     p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
     p.q_tiles = static_cast<int32_t>((a.q.tokens + kItemRows - 1) / kItemRows);
-    const int64_t items = a.batch * a.q.heads * p.q_tiles;
+    p.splits = kStay ? 1 : a.splits;
+    p.partial = a.partial;
+    p.rows = a.batch * a.q.heads * a.q.tokens;
+    p.pitch = (a.d + 3) / 4 * 4;
+    const int64_t items = a.batch * a.q.heads * p.q_tiles * p.splits;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     p.items = static_cast<int32_t>(items);
     p.d = a.d;
@@ -557,7 +634,10 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
     auto kernel = attention_kernel<T, kD, kStay>;
     cudaError_t e = allow_shared<attention_tag<T, kD, kStay>>(kernel);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+    e = launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    JoinParams j{a.partial, p.splits, p.pitch, p.d, p.q_heads, p.rows, a.q.tokens, a.out, {a.out_strides[0], a.out_strides[1], a.out_strides[2]}, a.lse};
+    return launch_after(attention_join_kernel<T>, dim3(static_cast<unsigned>((p.rows + 7) / 8)), 256, 0, stream, 1, j);
 }
 
 // Keys of one tile stay with a CTA where a key head has four items or more: changing heads stops it for a copy (1.5 us),
@@ -576,6 +656,17 @@ cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t stream)
 {
     if (a.dtype == CONVROT_BF16) return a.d <= 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
     return a.d <= 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+}
+
+int32_t attention_splits(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads)
+{
+    return key_shares(batch * q_heads * ((q_tokens + kItemRows - 1) / kItemRows), kv_tokens);
+}
+
+int64_t attention_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int d)
+{
+    const int32_t splits = attention_splits(batch, q_tokens, kv_tokens, q_heads);
+    return splits > 1 ? splits * batch * q_heads * q_tokens * ((d + 3) / 4 * 4 + 1) * 4 : 0;
 }
 
 int attention_shared(int form, int *columns)

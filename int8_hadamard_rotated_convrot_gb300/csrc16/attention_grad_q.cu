@@ -18,6 +18,10 @@
 // operand of dS K), and the sums dQ. The tile of keys is read K-major for S
 // and MN-major for dQ from the same bytes.
 //
+// Few items and long keys: shares of the keys as in the forward pass, added up in
+// order by a second kernel (64 queries, 8 heads of 128, 77000 keys: the gradient
+// took 937 us, 288 so).
+//
 // 8190 queries, 512 keys, 40 heads of 128: 116 us, 47 % of it products; each tile's dS
 // stands between its dP and its dQ. The last tile of an item has code of its own,
 // since conditions for it in the loop cost the issuing warp 5 % of the time of all.
@@ -59,6 +63,10 @@ struct Params {
     int32_t q_tiles, items;
     int32_t d, wide;
     float scale, scale_log2;
+    int32_t splits;
+    float *partial;  // [splits][rows of dq][pitch]: what a share of the keys gives, where there are several
+    int64_t rows;
+    int32_t pitch;
 };
 
 template <typename T, int kD, bool kStay>
@@ -118,12 +126,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     struct Item {
         int b, h, q0, keys, tiles;
         int head;  // of the keys
+        int first_tile, share;
     };
     const int first = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * blockIdx.x / gridDim.x) : blockIdx.x;
     const int end = kStay ? static_cast<int>(static_cast<int64_t>(p.items) * (blockIdx.x + 1) / gridDim.x) : p.items;
     const int step = kStay ? 1 : gridDim.x;
     auto item_at = [&](int i) {
         Item it;
+        it.share = kStay ? 0 : i % p.splits;
+        if (!kStay) i /= p.splits;
         const int bh = i / p.q_tiles;
         it.q0 = (i - bh * p.q_tiles) * kTileQueries;
         it.b = bh / p.q_heads;
@@ -131,6 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         it.head = bh / p.group;
         it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
         it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
+        it.first_tile = 0;
+        if (!kStay && p.splits > 1) {
+            it.first_tile = static_cast<int>(static_cast<int64_t>(it.tiles) * it.share / p.splits);
+            it.tiles = static_cast<int>(static_cast<int64_t>(it.tiles) * (it.share + 1) / p.splits) - it.first_tile;
+        }
         return it;
     };
 
@@ -166,21 +182,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     load(p.q, it.q0, it.h, it.b);
                     load(p.dout, it.q0, it.h, it.b);
                 } else {
-                    load(p.k, 0, it.h / p.group, it.b);
+                    load(p.k, it.first_tile * kTileKeys, it.h / p.group, it.b);
                     if (!ok || !(ok = wait(q_empty, q_phase ^ 1u))) break;
                     mbar_arrive_expect_tx(q_full, C::TILE);
                     load_tile<C::HALVES>(base, p.q, it.q0, it.h, it.b, q_full);
                     armed |= 1u << 16;
                     q_phase ^= 1u;
-                    load(p.v, 0, it.h / p.group, it.b);
+                    load(p.v, it.first_tile * kTileKeys, it.h / p.group, it.b);
                     if (!ok || !(ok = wait(dout_empty, dout_phase ^ 1u))) break;
                     mbar_arrive_expect_tx(dout_full, C::TILE);
                     load_tile<C::HALVES>(base + C::TILE, p.dout, it.q0, it.h, it.b, dout_full);
                     armed |= 1u << 17;
                     dout_phase ^= 1u;
                     for (int j = 1; j < it.tiles && ok; ++j) {
-                        load(p.k, j * kTileKeys, it.h / p.group, it.b);
-                        load(p.v, j * kTileKeys, it.h / p.group, it.b);
+                        load(p.k, (it.first_tile + j) * kTileKeys, it.h / p.group, it.b);
+                        load(p.v, (it.first_tile + j) * kTileKeys, it.h / p.group, it.b);
                     }
                 }
             }
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 uint32_t s[kPart], g[kPart];
                 tmem_ld32_async(lanes + C::S_COL + 128 * b + kPart * part, s);
                 tmem_ld_wait(s);
-                const int keys = it.keys - j * kTileKeys - part * kPart;
+                const int keys = it.keys - (it.first_tile + j) * kTileKeys - part * kPart;
 #pragma unroll
                 for (int k = 0; k < kPart; k += 2) {
                     const F2 x = fma2(F2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2, off2);
@@ -507,6 +523,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = it.tiles > 0 ? __uint_as_float(o[e]) * down : 0.0f;
+                if (!kStay && p.splits > 1) {
+                    const int64_t row = it.share * p.rows + (static_cast<int64_t>(it.b) * p.q_tokens + row0 + lane) * p.q_heads + it.h;
+                    if (lane < rows) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (k + e < p.pitch) *reinterpret_cast<float4 *>(p.partial + row * p.pitch + k + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    }
+                    continue;
+                }
                 if (rows > 0)
                     store_rows_traded<T>(dq + k, static_cast<int64_t>(p.q_heads) * p.d, rows, p.d - k < 32 ? p.d - k : 32, p.wide, lane, v);
             }
@@ -519,6 +544,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_free<1>(tmem, 512u);
+}
+
+// dq from the shares, in their order, four elements a thread.
+template <typename T>
+__global__ void __launch_bounds__(256) attention_grad_q_join_kernel(const float *partial, int splits, int64_t rows, int pitch, int d, T *dq)
+{
+    after_previous();
+    let_next_start();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, row = i / (pitch / 4);
+    const int e0 = static_cast<int>(i - row * (pitch / 4)) * 4;
+    if (row >= rows) return;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(partial + (s * rows + row) * pitch + e0));
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e0 + e < d) dq[row * d + e0 + e] = from_f32<T>(v[e]);
+}
+
+int32_t splits_of(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads)
+{
+    return key_shares(batch * q_heads * ((q_tokens + kTileQueries - 1) / kTileQueries), kv_tokens);
 }
 
 template <typename T, int kD, bool kStay>
@@ -548,7 +602,11 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.q_heads = static_cast<int32_t>(a.q.heads);
     p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
     p.q_tiles = static_cast<int32_t>((a.q.tokens + kTileQueries - 1) / kTileQueries);
-    const int64_t items = a.batch * a.q.heads * p.q_tiles;
+    p.splits = kStay ? 1 : splits_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads);
+    p.partial = a.partial_q;
+    p.rows = a.batch * a.q.tokens * a.q.heads;
+    p.pitch = (a.d + 3) / 4 * 4;
+    const int64_t items = a.batch * a.q.heads * p.q_tiles * p.splits;
     if (items > INT32_MAX) return cudaErrorInvalidValue;
     p.items = static_cast<int32_t>(items);
     p.d = a.d;
@@ -558,7 +616,11 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     auto kernel = attention_grad_q_kernel<T, kD, kStay>;
     cudaError_t e = allow_shared<grad_q_tag<T, kD, kStay>>(kernel);
     if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+    e = launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t blocks = (p.rows * (p.pitch / 4) + 255) / 256;
+    return launch_after(attention_grad_q_join_kernel<T>, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, 1, a.partial_q, p.splits, p.rows, p.pitch, p.d,
+                        static_cast<T *>(a.dq));
 }
 
 // Keys that stay: as in the forward pass (4 x 1270 queries, 20 keys, 43 heads of 80 on one: 64 us with an item's queries,
@@ -579,6 +641,12 @@ cudaError_t launch_attention_grad_q(const AttentionGradArgs &a, cudaStream_t str
 {
     if (a.dtype == CONVROT_BF16) return a.d <= 64 ? launch<__nv_bfloat16, 64>(a, stream) : launch<__nv_bfloat16, 128>(a, stream);
     return a.d <= 64 ? launch<__half, 64>(a, stream) : launch<__half, 128>(a, stream);
+}
+
+int64_t grad_q_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int d)
+{
+    const int32_t splits = splits_of(batch, q_tokens, kv_tokens, q_heads);
+    return splits > 1 ? splits * batch * q_tokens * q_heads * ((d + 3) / 4 * 4) * 4 : 0;
 }
 
 int attention_grad_q_shared(int form, int *columns)

@@ -254,6 +254,30 @@ def test_attention_many_items(b, tq, tk, hq, hk, d, mask, dtype):
             close(got[name][at], grads[name], bound[name], name)
 
 
+@TYPES
+@pytest.mark.parametrize("b,tq,tk,hq,hk,d,mask", [
+    (1, 64, 4096, 16, 16, 64, "none"), (2, 200, 1500, 4, 2, 128, "scattered"), (3, 40, 900, 2, 1, 50, "padded"), (1, 300, 257, 1, 1, 33, "none"),
+    (1, 17, 20000, 1, 1, 128, "padded"), (1, 257, 513, 30, 3, 72, "none"), (5, 100, 700, 3, 3, 1, "scattered")])
+def test_attention_keys_shared_out(b, tq, tk, hq, hk, d, mask, dtype):
+    """Few queries and long keys: the keys are shared out, samples with fewer of them than shares among them."""
+    g, q, k, v, there = attention_inputs(b, tq, tk, hq, hk, d, dtype, mask)
+    if there is not None:
+        there[-1, 100:] = False
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bl.convrot_attention(q, k, v, there, dev_status=status)
+    dout = randn(g, b, tq, hq, d, dtype=dtype)
+    got = bl.convrot_attention_backward(q, k, v, out, lse, dout, there, dev_status=status)
+    assert int(status) == 0
+    want = ref.Attention(q, k, v, there)
+    close(out, want.out, want.out_bound, "out")
+    empty = want.lse == -float("inf")
+    assert torch.equal(lse == -float("inf"), empty)
+    close(lse[~empty], want.lse[~empty], want.lse_bound[~empty], "lse")
+    grads, bound = want.gradient(dout)
+    for name in grads:
+        close(got[name], grads[name], bound[name], name)
+
+
 def test_attention_gradient_against_differences():
     b, tq, tk, hq, hk, d = 2, 5, 9, 4, 2, 16
     g, q, k, v, there = attention_inputs(b, tq, tk, hq, hk, d, BF16, "padded", seed=3)
