@@ -71,6 +71,9 @@ inline int32_t key_shares(int64_t items, int64_t kv_tokens)
     if (shares > 32) shares = 32;
     return shares > 1 && tiles - (tiles + shares - 1) / shares >= 6 ? static_cast<int32_t>(shares) : 1;
 }
+// A kernel's forms: all tiles of a head's keys pass by; one tile stays with a CTA; shares of the keys have items of their own.
+// (A form each: the shares' arithmetic in the first one cost it 2 %.)
+enum KeyForm { kPass, kStays, kShared };
 int32_t attention_splits(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads);
 int64_t attention_partial_bytes(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_heads, int d);
 

@@ -84,9 +84,10 @@ struct Params {
     int32_t pitch;
 };
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ Params p)
 {
+    constexpr bool kStay = kForm == kStays, kShares = kForm == kShared;
     using C = Cfg<kD>;
     constexpr float kShift = std::is_same_v<T, __half> ? 7.0f : 0.0f;
     extern __shared__ uint8_t smem_raw[];
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     auto item_at = [&](int i) {
         Item it;
-        it.share = kStay ? 0 : i % p.splits;
-        if (!kStay) i /= p.splits;
+        it.share = kShares ? i % p.splits : 0;
+        if (kShares) i /= p.splits;
         const int bh = i / p.q_tiles;
         it.q0 = (i - bh * p.q_tiles) * kItemRows;
         it.b = bh / p.q_heads;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
         it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
         it.first = 0;
-        if (!kStay && p.splits > 1) {
+        if (kShares) {
             it.first = static_cast<int>(static_cast<int64_t>(it.tiles) * it.share / p.splits);
             it.tiles = static_cast<int>(static_cast<int64_t>(it.tiles) * (it.share + 1) / p.splits) - it.first;
         }
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             // (of this share, where there are several: the second kernel puts them together)
             const int64_t row = it.share * p.rows + (static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane;
             if (half == 0 && lane < rows)
-                (p.splits > 1 ? p.partial + p.splits * p.rows * p.pitch : p.lse)[row] = sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
+                (kShares ? p.partial + p.splits * p.rows * p.pitch : p.lse)[row] = sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
             T *out = static_cast<T *>(p.out) + it.b * p.out_strides[0] + row0 * p.out_strides[1] + it.h * p.out_strides[2];
             if (it.tiles > 0) {
                 ok = __all_sync(0xffffffffu, wait(o_full(g), o_phase));
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.0f;
                 }
-                if (!kStay && p.splits > 1) {
+                if (kShares) {
                     if (lane < rows && ok) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -598,10 +599,10 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
         if (e0 + e < p.d) out[e] = from_f32<T>(v[e]);
 }
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 struct attention_tag;
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
 {
     using C = Cfg<kD>;
@@ -621,7 +622,7 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
     p.q_heads = static_cast<int32_t>(a.q.heads);
     p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
     p.q_tiles = static_cast<int32_t>((a.q.tokens + kItemRows - 1) / kItemRows);
-    p.splits = kStay ? 1 : a.splits;
+    p.splits = kForm == kShared ? a.splits : 1;
     p.partial = a.partial;
     p.rows = a.batch * a.q.heads * a.q.tokens;
     p.pitch = (a.d + 3) / 4 * 4;
@@ -631,8 +632,8 @@ cudaError_t launch_form(const AttentionArgs &a, cudaStream_t stream)
     p.d = a.d;
     p.wide = heads_wide(a.out, a.out_strides, a.batch, a.q.tokens, a.q.heads);
     p.scale_log2 = a.scale * kLog2e;
-    auto kernel = attention_kernel<T, kD, kStay>;
-    cudaError_t e = allow_shared<attention_tag<T, kD, kStay>>(kernel);
+    auto kernel = attention_kernel<T, kD, kForm>;
+    cudaError_t e = allow_shared<attention_tag<T, kD, kForm>>(kernel);
     if (e != cudaSuccess) return e;
     e = launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.splits == 1) return e;
@@ -647,7 +648,8 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t stream)
 {
     const int64_t of_head = a.q.heads / a.k.heads * ((a.q.tokens + kItemRows - 1) / kItemRows);
     const bool stay = !a.counts && a.kv_tokens > 0 && a.kv_tokens <= kTileKeys && of_head >= 4;
-    return stay ? launch_form<T, kD, true>(a, stream) : launch_form<T, kD, false>(a, stream);
+    if (stay) return launch_form<T, kD, kStays>(a, stream);
+    return a.splits > 1 ? launch_form<T, kD, kShared>(a, stream) : launch_form<T, kD, kPass>(a, stream);
 }
 
 }  // namespace

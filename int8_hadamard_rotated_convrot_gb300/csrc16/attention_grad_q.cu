@@ -20,7 +20,7 @@
 //
 // Few items and long keys: shares of the keys as in the forward pass, added up in
 // order by a second kernel (64 queries, 8 heads of 128, 77000 keys: the gradient
-// took 937 us, 288 so).
+// took 937 us, 290 so).
 //
 // 8190 queries, 512 keys, 40 heads of 128: 116 us, 47 % of it products; each tile's dS
 // stands between its dP and its dQ. The last tile of an item has code of its own,
@@ -69,9 +69,10 @@ struct Params {
     int32_t pitch;
 };
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __grid_constant__ Params p)
 {
+    constexpr bool kStay = kForm == kStays, kShares = kForm == kShared;
     using C = Cfg<kD>;
     constexpr bool kHalf = std::is_same_v<T, __half>;
     extern __shared__ uint8_t smem_raw[];
@@ -133,8 +134,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
     const int step = kStay ? 1 : gridDim.x;
     auto item_at = [&](int i) {
         Item it;
-        it.share = kStay ? 0 : i % p.splits;
-        if (!kStay) i /= p.splits;
+        it.share = kShares ? i % p.splits : 0;
+        if (kShares) i /= p.splits;
         const int bh = i / p.q_tiles;
         it.q0 = (i - bh * p.q_tiles) * kTileQueries;
         it.b = bh / p.q_heads;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
         it.keys = p.counts ? static_cast<int>(load_i32(p.counts + it.b)) : p.kv_tokens;
         it.tiles = (it.keys + kTileKeys - 1) / kTileKeys;
         it.first_tile = 0;
-        if (!kStay && p.splits > 1) {
+        if (kShares) {
             it.first_tile = static_cast<int>(static_cast<int64_t>(it.tiles) * it.share / p.splits);
             it.tiles = static_cast<int>(static_cast<int64_t>(it.tiles) * (it.share + 1) / p.splits) - it.first_tile;
         }
@@ -523,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = it.tiles > 0 ? __uint_as_float(o[e]) * down : 0.0f;
-                if (!kStay && p.splits > 1) {
+                if (kShares) {
                     const int64_t row = it.share * p.rows + (static_cast<int64_t>(it.b) * p.q_tokens + row0 + lane) * p.q_heads + it.h;
                     if (lane < rows) {
 #pragma unroll
@@ -575,10 +576,10 @@ int32_t splits_of(int64_t batch, int64_t q_tokens, int64_t kv_tokens, int64_t q_
     return key_shares(batch * q_heads * ((q_tokens + kTileQueries - 1) / kTileQueries), kv_tokens);
 }
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 struct grad_q_tag;
 
-template <typename T, int kD, bool kStay>
+template <typename T, int kD, KeyForm kForm>
 cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
 {
     using C = Cfg<kD>;
@@ -602,7 +603,7 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.q_heads = static_cast<int32_t>(a.q.heads);
     p.group = static_cast<int32_t>(a.q.heads / a.k.heads);
     p.q_tiles = static_cast<int32_t>((a.q.tokens + kTileQueries - 1) / kTileQueries);
-    p.splits = kStay ? 1 : splits_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads);
+    p.splits = kForm == kShared ? splits_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads) : 1;
     p.partial = a.partial_q;
     p.rows = a.batch * a.q.tokens * a.q.heads;
     p.pitch = (a.d + 3) / 4 * 4;
@@ -613,8 +614,8 @@ cudaError_t launch_form(const AttentionGradArgs &a, cudaStream_t stream)
     p.wide = aligned_to(a.dq, 16) && a.d % 8 == 0;
     p.scale = a.scale;
     p.scale_log2 = a.scale * kLog2e;
-    auto kernel = attention_grad_q_kernel<T, kD, kStay>;
-    cudaError_t e = allow_shared<grad_q_tag<T, kD, kStay>>(kernel);
+    auto kernel = attention_grad_q_kernel<T, kD, kForm>;
+    cudaError_t e = allow_shared<grad_q_tag<T, kD, kForm>>(kernel);
     if (e != cudaSuccess) return e;
     e = launch_after(kernel, dim3(static_cast<unsigned>(items < kSms ? items : kSms)), kThreads, C::SMEM, stream, 1, p);
     if (e != cudaSuccess || p.splits == 1) return e;
@@ -630,9 +631,9 @@ cudaError_t launch(const AttentionGradArgs &a, cudaStream_t stream)
 {
     if constexpr (kD > 64) {
         const int64_t of_head = a.q.heads / a.k.heads * ((a.q.tokens + kTileQueries - 1) / kTileQueries);
-        if (!a.counts && a.kv_tokens > 0 && a.kv_tokens <= kTileKeys && of_head >= 4) return launch_form<T, kD, true>(a, stream);
+        if (!a.counts && a.kv_tokens > 0 && a.kv_tokens <= kTileKeys && of_head >= 4) return launch_form<T, kD, kStays>(a, stream);
     }
-    return launch_form<T, kD, false>(a, stream);
+    return splits_of(a.batch, a.q.tokens, a.kv_tokens, a.q.heads) > 1 ? launch_form<T, kD, kShared>(a, stream) : launch_form<T, kD, kPass>(a, stream);
 }
 
 }  // namespace
