@@ -39,8 +39,8 @@ cudaError_t launch_gather(const GatherArgs &a, cudaStream_t stream);
 
 // Masks of one tile's keys are applied where they are (the gathering kernel's 5 us are more than what a shorter tile saves),
 // longer ones by gathering the keys that are there (3 samples of 1363 queries, 24 heads, a third to all of 333 keys: 22 us with
-// it against 28 over all tiles).
-inline bool mask_in_place(int64_t kv_tokens) { return kv_tokens <= kTileKeys; }
+// it against 28 over all tiles). A mask of no keys is none: where it is applied, each item has its tile.
+inline bool mask_in_place(int64_t kv_tokens) { return kv_tokens > 0 && kv_tokens <= kTileKeys; }
 
 struct AttentionArgs {
     States q, k, v;
