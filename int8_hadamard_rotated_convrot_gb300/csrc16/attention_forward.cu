@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
             float top = neg_inf(), sum = 0.0f;  // the reference, and this thread's sum of 2^(c (s - top) + kShift)
             for (int j = 0; j < it.tiles; ++j) {
-                ok = __all_sync(0xffffffffu, ok && wait(s_full(g), s_phase));
+                ok = ok && wait.together(s_full(g), s_phase);
                 s_phase ^= 1u;
                 tc_fence_after();
                 uint32_t r[kHalfKeys];
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 (kShares ? p.partial + p.splits * p.rows * p.pitch : p.lse)[row] = sum == 0.0f ? neg_inf() : kLn2 * (top * c + (log2f(sum) - kShift));
             T *out = static_cast<T *>(p.out) + it.b * p.out_strides[0] + row0 * p.out_strides[1] + it.h * p.out_strides[2];
             if (it.tiles > 0) {
-                ok = __all_sync(0xffffffffu, wait(o_full(g), o_phase));
+                ok = wait.together(o_full(g), o_phase);
                 o_phase ^= 1u;
                 tc_fence_after();
             }

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             const bool there = key < u.keys, masked = there && key_masked(p, u, key);
             // dQ of tile t of this unit, the m-th of this run: 16 elements of a query
             auto read_dq = [&](int t, int m) {
-                if (!wait(dq_full(m), (m >> 1) & 1)) return false;
+                if (!wait.together(dq_full(m), (m >> 1) & 1)) return false;
                 tc_fence_after();
                 const int h = u.h * p.group + t / p.q_tiles, row = t % p.q_tiles * kTileQueries + quad * 32 + lane, col = part * 16;
                 if (col >= p.d) return true;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
             };
             for (int t = t0; t < t1; ++t, ++n) {
                 const int ds = n % C::DS;
-                if (!wait(st_full(ds), (n / C::DS) & 1) || !wait(s_full, n & 1)) return false;
+                if (!wait.together(st_full(ds), (n / C::DS) & 1) || !wait.together(s_full, n & 1)) return false;
                 tc_fence_after();
                 const uint32_t stats = base + kStats + ds * C::STATS + part * kPart * 4;
                 uint32_t s[kPart], g[kPart], pk[kPart / 2];
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready);
-                if (!wait(dp_full, n & 1)) return false;
+                if (!wait.together(dp_full, n & 1)) return false;
                 tc_fence_after();
                 tmem_ld32_async(lanes + C::DP_COL + kPart * part, g);
                 tmem_ld_wait(g);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_kv_kernel(const __
                 if (kAll && t > t0 && !read_dq(t - 1, n - 1)) return false;
             }
             if (kAll && !read_dq(t1 - 1, n - 1)) return false;
-            if (!wait(sums_full, sums_phase)) return false;
+            if (!wait.together(sums_full, sums_phase)) return false;
             sums_phase ^= 1u;
             tc_fence_after();
             // the first eight warps have dV, the others dK

@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             }
             for (int j = 0; j < it.tiles; ++j, ++tile_no) {
                 const int b = tile_no & 1;
-                if (!wait(s_full(b), (tile_no >> 1) & 1)) {
+                if (!wait.together(s_full(b), (tile_no >> 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
                     for (int k = 0; k < kPart; ++k)
                         if (k >= keys) s[k] = 0u;
                 }
-                if (!wait(dp_full, dp_phase)) {
+                if (!wait.together(dp_full, dp_phase)) {
                     ok = false;
                     break;
                 }
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_grad_q_kernel(const __g
             }
             if (!ok) break;
             if (it.tiles > 0) {
-                if (!wait(dq_full, dq_phase)) {
+                if (!wait.together(dq_full, dq_phase)) {
                     ok = false;
                     break;
                 }

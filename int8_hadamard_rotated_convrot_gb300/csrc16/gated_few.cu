@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         }
     } else if (warp < 6) {
         const int q = warp & 3;  // tensor-memory lanes of this warp
-        ok = wait(done_bar, 0);
+        ok = wait.together(done_bar, 0);
         tc_fence_after();
         if (!ok) wait.fail();
         // this CTA's sums, [row of x][row of the weights], over the ring's stages: every MMA has read them

@@ -256,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (second) mt -= p.tiles_m;
             const int64_t row0 = static_cast<int64_t>(mt) * 2 * kBM + rank * kBM + q * 32;
             const int rows = p.rows - row0 < 32 ? static_cast<int>(p.rows - row0) : 32;
-            if (!wait(sum_bar(buf), buf_phase)) {
+            if (!wait.together(sum_bar(buf), buf_phase)) {
                 ok = false;
                 break;
             }

@@ -232,7 +232,9 @@ __device__ __forceinline__ F2 gate_act2(F2 v)
     }
 }
 
-// The kernels' bounded wait: gives up early once another role of the block has.
+// The kernels' bounded wait: gives up early once another role of the block has. It is one thread's; a warp that goes on to an
+// instruction that all its lanes have to reach (tcgen05.ld, a shuffle, a barrier) waits together, since each lane reads the
+// timer for itself.
 struct Waits {
     volatile int *abort_flag;
     int32_t *dev_status;
@@ -252,7 +254,7 @@ struct Waits {
         asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 100000;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
         return ok != 0;
     }
-    // by a whole warp: true for all lanes or for none
+    // by a whole warp: true for all lanes or for none, so that it leaves as a whole or not at all
     __device__ __forceinline__ bool together(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, (*this)(bar, parity)); }
     // whether it is there now
     __device__ __forceinline__ bool now(uint32_t bar, uint32_t parity) const
