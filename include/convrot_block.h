@@ -322,6 +322,8 @@ convrot_status convrot_gated_linear_backward(const convrot_gated_linear_backward
  *
  * A query without keys (all masked, or kv_tokens == 0) has out 0 and lse -infinity.
  * What stands in a masked key or value (NaN too) does not reach any result.
+ * Scores past the floats are infinite: a query with one of +infinity (or NaN)
+ * has NaN, one whose scores are all -infinity counts as one without keys.
  *
  *   q, out     [batch, q_tokens, q_heads, head_dim] of type dtype (CONVROT_BF16
  *              or CONVROT_F16; CONVROT_F32 is CONVROT_ERR_UNSUPPORTED),

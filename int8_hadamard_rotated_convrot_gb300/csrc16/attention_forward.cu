@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         tmem_st16(o_at + k, o);
                     }
                 }
-                // (a row of infinite scores below: no term at all)
-                const float off = top == neg_inf() ? 0.0f : kShift - top * c;
+                // (a row of scores that are all -infinity so far, also where c s is past the floats: no term at all)
+                const float most = top * c, off = most == neg_inf() ? 0.0f : kShift - most;
                 const F2 c2(c), off2(off);
                 F2 add[2] = {F2(0.0f), F2(0.0f)};
 #pragma unroll
@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const float theirs = other(sum);
             if (gone) break;
             sum = half == 0 ? sum + theirs : theirs + sum;
+            if (top * c == -neg_inf()) sum = __uint_as_float(0x7fffffffu);  // infinity less itself, as for infinite S (no term was left)
             const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;  // NaN stays
             // (of this share, where there are several: the second kernel puts them together)
             const int64_t row = it.share * p.rows + (static_cast<int64_t>(it.b) * p.q_heads + it.h) * p.q_tokens + row0 + lane;

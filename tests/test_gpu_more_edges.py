@@ -41,3 +41,41 @@ def test_a_mask_of_no_keys(lib, tq, hq, hk, d, dtype):
     assert lib.convrot_attention(args, None) == cr.OK
     torch.cuda.synchronize()
     assert int(status) == 0 and not out.any() and torch.all(lse == -float("inf"))
+
+
+# queries, keys, heads, key heads, head_dim, mask: few rows, a cluster's and several; tiles that pass by, that stay, that are shared out; masks in place and gathered
+FORMS = [(3, 300, 4, 2, 64, False), (3, 40000, 2, 1, 128, True), (90, 300, 2, 2, 64, False), (300, 100, 4, 4, 128, True), (1500, 100, 4, 1, 64, True),
+         (60, 4096, 2, 2, 64, False), (60, 4096, 2, 2, 128, True), (300, 500, 2, 2, 72, True)]
+
+
+def infinite_scores(tq, tk, hq, hk, d, masked, dtype, of_q, of_k):
+    """Queries of -1, 0 and 1 in turn, times of_q, to keys that are all of_k."""
+    g = torch.Generator(device="cuda").manual_seed(tq + tk)
+    kind = (torch.arange(tq, device="cuda") % 3 - 1)[None, :, None, None]
+    q = (kind * of_q).expand(2, tq, hq, d).to(dtype).contiguous()
+    k = torch.full((2, tk, hk, d), of_k, device="cuda", dtype=dtype)
+    v = torch.randn(2, tk, hk, d, generator=g, device="cuda").to(dtype)
+    mask = torch.rand(2, tk, generator=g, device="cuda") < 0.7 if masked else None
+    there = torch.ones(2, tk, dtype=torch.bool, device="cuda") if mask is None else mask
+    mean = torch.stack([v[i, there[i]].double().mean(0) for i in range(2)]).repeat_interleave(hq // hk, 1)  # [2, hq, d]
+    return q, k, v, mask, kind[0, :, 0, 0], there.sum(1).double(), mean
+
+
+def check_infinite_scores(out, lse, kind, count, mean, dtype):
+    assert torch.isnan(out[:, kind == 1]).all() and torch.isnan(lse[:, :, kind == 1]).all()
+    assert not out[:, kind == -1].any() and torch.all(lse[:, :, kind == -1] == -float("inf"))
+    # equal probabilities, exact but for the sums of up to 40000 terms in fp32 (each off by 2^-23 of the sum of their sizes at most,
+    # and no more than 3000 after one another) and the rounding of results of up to 4
+    assert (out[:, kind == 0].double() - mean[:, None]).abs().max() <= 4 * torch.finfo(dtype).eps / 2 + 3000 * 2.0**-23
+    assert (lse[:, :, kind == 0].double() - count.log()[:, None, None]).abs().max() <= 2.0**-18
+
+
+@TYPES
+@pytest.mark.parametrize("tq,tk,hq,hk,d,masked", FORMS)
+def test_scores_past_the_floats(lib, tq, tk, hq, hk, d, masked, dtype):
+    """The largest scale takes scores of +-d past the floats: they are infinite, and those of 0 stay."""
+    q, k, v, mask, *want = infinite_scores(tq, tk, hq, hk, d, masked, dtype, 1.0, 1.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = bl.convrot_attention(q, k, v, mask, scale=1.7e38, dev_status=status)
+    assert int(status) == 0
+    check_infinite_scores(out, lse, *want, dtype)
