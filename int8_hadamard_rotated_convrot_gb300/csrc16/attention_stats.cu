@@ -7,7 +7,8 @@
 // (8190 x 40 heads of 128: 74 us with a query a warp and one in flight). A
 // block a head, also where heads share keys (4 x 1270 x 43 heads on one of
 // keys: 126 us with a block for all 43). Rows behind the last query get -infinity
-// for the first: their probabilities are 0. Bound by HBM: out and dout once
+// for the first, and queries whose lse is -infinity (without keys, or with
+// none that counts) too: their probabilities are 0. Bound by HBM: out and dout once
 // (8190 x 40 heads of 128: 33 us, 5.1 TB/s).
 #include "attention.cuh"
 
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(256, 5) attention_stats_kernel(const __grid_co
                 const int i = i0 + n * kStride;
                 const int64_t t = t0 + i, at = head * p.rows + t;
                 if (i >= queries || t >= p.rows) continue;
-                p.base2[at] = t < p.q_tokens ? fmaf(load_f32(p.lse + head * p.q_tokens + t), -kLog2e, p.shift) : neg_inf();
+                const float lse = t < p.q_tokens ? load_f32(p.lse + head * p.q_tokens + t) : neg_inf();
+                p.base2[at] = lse == neg_inf() ? lse : fmaf(lse, -kLog2e, p.shift);
                 p.delta[at] = -part[n];
             }
         }

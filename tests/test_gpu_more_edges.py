@@ -79,3 +79,20 @@ def test_scores_past_the_floats(lib, tq, tk, hq, hk, d, masked, dtype):
     out, lse = bl.convrot_attention(q, k, v, mask, scale=1.7e38, dev_status=status)
     assert int(status) == 0
     check_infinite_scores(out, lse, *want, dtype)
+
+
+@pytest.mark.parametrize("tq,tk,hq,hk,d,masked", FORMS)
+def test_infinite_scores_and_their_gradients(lib, tq, tk, hq, hk, d, masked):
+    """Products of 2^126 a term are past the floats themselves. A query whose scores are all -infinity has no part in a gradient."""
+    q, k, v, mask, kind, count, mean = infinite_scores(tq, tk, hq, hk, d, masked, BF16, 2.0**63, 2.0**63)
+    out, lse = bl.convrot_attention(q, k, v, mask)
+    check_infinite_scores(out, lse, kind, count, mean, BF16)
+    q[:, kind == 1] = 0
+    out, lse = bl.convrot_attention(q, k, v, mask)
+    dout = torch.ones_like(out)
+    got = bl.convrot_attention_backward(q, k, v, out, lse, dout, mask)
+    assert not got["dq"][:, kind == -1].any() and not got["dk"].any()
+    there = torch.ones(2, tk, dtype=torch.bool, device="cuda") if mask is None else mask
+    want = torch.where(there, (hq // hk) * int((kind != -1).sum()) / count[:, None], 0.0)[:, :, None, None]
+    # sums of equal terms, whose probability is one exponential of an lse that is off by up to 2^-18, rounded to 8 bits; fp32 sums as above
+    assert ((got["dv"].double() - want).abs() <= want * (2 * 2.0**-8 + 2.0**-17 + 3000 * 2.0**-23)).all()
