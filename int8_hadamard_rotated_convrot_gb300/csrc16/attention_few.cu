@@ -20,7 +20,9 @@
 //
 // Warps keep a maximum, a sum and sums of their own; they meet in shared
 // memory, the cluster's CTAs in distributed shared memory, clusters in a second
-// kernel, always added in the same order. A masked key is not read.
+// kernel, always added in the same order. The copies bring every key, masked or
+// not; a mask takes a key's score and value out where they are used, so it saves
+// no time (4 x 2 queries, 8192 keys, half of them masked: 29.5 us).
 #include "attention.cuh"
 
 namespace convrot {
@@ -29,7 +31,6 @@ namespace {
 using namespace mma16;
 
 constexpr int kWarps = 12, kThreads = 32 * kWarps, kRows = 16, kStep = 16;  // keys of a warp's step
-constexpr int kMaxSplit = 8;
 constexpr int kPerSm = 1;
 constexpr float kGrow = 8.0f;
 
