@@ -263,6 +263,12 @@ convrot_status convrot_rotary_table(const double *positions, int64_t rows, int32
  *              tensors' addresses and leading dimensions, and no memory.
  *   dev_status as for convrot_linear.
  * m == 0 or n == 0 launches nothing; 1 <= k. Outputs must not overlap inputs.
+ *
+ * From here on to the end of this header, 16-bit inputs are read in aligned
+ * blocks of 16 bytes: those that hold an element of a tensor may be read whole,
+ * so up to 14 bytes before its first element and behind its last one (in the
+ * same 16 bytes, so in memory that is there). Nothing depends on what they are,
+ * and nothing beside a tensor's elements is written.
  */
 enum { CONVROT_ACT_SILU = 3 };
 
@@ -344,6 +350,7 @@ convrot_status convrot_gated_linear_backward(const convrot_gated_linear_backward
  * 1 <= head_dim <= CONVROT_ATTENTION_MAX_D (CONVROT_ERR_UNSUPPORTED above).
  * Probabilities are rounded to dtype for their product with v, whose operands
  * have one type; the sums of a softmax are fp32, of the unrounded values.
+ * Outputs must not overlap inputs.
  */
 #define CONVROT_ATTENTION_MAX_D 128
 
@@ -375,9 +382,11 @@ convrot_status convrot_attention(const convrot_attention_args *a, cudaStream_t s
  *              summed over the query heads that share a head and are 0 at
  *              masked keys.
  * P and dS are rounded to dtype for their products; for CONVROT_F16 they are
- * scaled by powers of two first, so that small gradients keep their bits. Sums
- * are fp32, in an order that depends on the sizes (and, with a mask, on the
- * number of keys) alone. Outputs must not overlap inputs.
+ * scaled by powers of two first, so that small gradients keep their bits. That
+ * of dS is one for all queries of a key head: beside its rounding, dS is off by up
+ * to 2^-22 of their largest |dout|, and it is infinite past 2^18 of that (which
+ * takes values v past 4096). Sums are fp32, in an order that depends on the sizes
+ * (and, with a mask, on the number of keys) alone. Outputs must not overlap inputs.
  *   work       256-byte aligned, convrot_attention_backward_work_bytes(a) bytes:
  *              8 for each query and head, partial sums (50 MB at most), and what
  *              the forward call's has room for.

@@ -271,7 +271,8 @@ struct Waits {
 };
 
 // Eight 16-bit elements from any address, of which the first n (1 to 8) are wanted and the others become 0. The one or two
-// aligned 16-byte blocks that hold wanted elements are read whole, whoever's the rest of them is, and shifted.
+// aligned 16-byte blocks that hold wanted elements are read whole, whoever's the rest of them is, and shifted. (A block is in
+// one page, so its rest is there too; the header tells callers.)
 __device__ __forceinline__ uint4 load8_any(const void *p, int n)
 {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
