@@ -9,7 +9,9 @@ pytestmark = pytest.mark.gpu
 from int8_hadamard_rotated_convrot_gb300 import block as bl  # noqa: E402
 from int8_hadamard_rotated_convrot_gb300 import convrot as cr  # noqa: E402
 
+from . import more_reference as more  # noqa: E402
 from . import test_more_block_abi as abi  # noqa: E402
+from . import test_more_reference as plain  # noqa: E402
 
 BF16, F16 = torch.bfloat16, torch.float16
 TYPES = pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
@@ -96,3 +98,29 @@ def test_infinite_scores_and_their_gradients(lib, tq, tk, hq, hk, d, masked):
     want = torch.where(there, (hq // hk) * int((kind != -1).sum()) / count[:, None], 0.0)[:, :, None, None]
     # sums of equal terms, whose probability is one exponential of an lse that is off by up to 2^-18, rounded to 8 bits; fp32 sums as above
     assert ((got["dv"].double() - want).abs() <= want * (2 * 2.0**-8 + 2.0**-17 + 3000 * 2.0**-23)).all()
+
+
+@TYPES
+@pytest.mark.parametrize("tq,tk,hq,hk,d", [(5, 9, 4, 2, 16), (150, 77, 4, 2, 64), (20, 200, 4, 1, 128), (40, 130, 2, 2, 72)])
+def test_attention_gradient_against_differences_where_it_is_large(lib, tq, tk, hq, hk, d, dtype):
+    """The twelve largest elements of each gradient, keys in every sample, against central differences of the formula in 64 bits.
+    A result may be off by the elementwise bound of its roundings, which is a few percent to a quarter of these elements, under half of them in any case."""
+    g = torch.Generator(device="cuda").manual_seed(tq)
+    q, k, v, dout = (torch.randn(2, t, h, d, generator=g, device="cuda") for t, h in ((tq, hq), (tk, hk), (tk, hk), (tq, hq)))
+    q, k, v, dout = (t.to(dtype) for t in (1.5 * q, k, v, dout))
+    mask = torch.rand(2, tk, generator=g, device="cuda") < 0.6
+    mask[:, 0] = True
+    out, lse = bl.convrot_attention(q, k, v, mask, scale=0.4)
+    got = bl.convrot_attention_backward(q, k, v, out, lse, dout, mask, scale=0.4)
+    grads, bound = more.Attention(q, k, v, mask, scale=0.4).gradient(dout)
+    wide = [t.double() for t in (q, k, v)]
+    for i, name in enumerate(("dq", "dk", "dv")):
+        for at in grads[name].abs().flatten().topk(12).indices.tolist():
+            step = torch.zeros_like(wide[i])
+            step.view(-1)[at] = 1e-4
+            up, down = (float((plain.attention(*(t + s * step if j == i else t for j, t in enumerate(wide)), mask, 0.4) * dout.double()).sum())
+                        for s in (1, -1))
+            want, off = (up - down) / 2e-4, float(bound[name].reshape(-1)[at])
+            assert off < 0.5 * abs(want), (name, at)
+            # (the differences' own error: 1e-8 of a third derivative, 1e-12 / 1e-4 of roundings)
+            assert abs(float(got[name].reshape(-1)[at]) - want) <= off + 1e-5 * max(1.0, abs(want)), (name, at, want, off)
