@@ -124,7 +124,7 @@ convrot_status convrot_gated_linear(const convrot_gated_linear_args *a, cudaStre
     b.ldw_gate = w.wg.ld;
     b.w_up = w.wu.p;
     b.ldw_up = w.wu.ld;
-    return done(gated_few_takes(a->m) ? launch_gated_few(b, stream) : launch_gated_gemm(b, stream));
+    return done(gated_few_takes(a->m, a->n, a->k) ? launch_gated_few(b, stream) : launch_gated_gemm(b, stream));
 }
 
 int64_t convrot_gated_linear_backward_work_bytes(const convrot_gated_linear_backward_args *a)

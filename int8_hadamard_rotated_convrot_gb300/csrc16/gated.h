@@ -9,7 +9,7 @@ namespace convrot {
 
 // y (and gate, up): many rows, and few.
 cudaError_t launch_gated_gemm(const convrot_gated_linear_args &a, cudaStream_t stream);
-bool gated_few_takes(int64_t m);
+bool gated_few_takes(int64_t m, int64_t n, int64_t k);
 cudaError_t launch_gated_few(const convrot_gated_linear_args &a, cudaStream_t stream);
 
 // dx = dg w_gate + du w_up (partial: gated_dx_partial_bytes) and dw = dg^T x, du^T x from dg and du [m, ldd].

@@ -2,7 +2,7 @@
 // where reading the weights counts, not the arithmetic.
 //
 // The weights are the MMA's M side: a CTA takes 64 rows of w_gate and the same
-// 64 of w_up as its 128 lanes, and up to 128 rows of x as the N side, so that
+// 64 of w_up as its 128 lanes, and up to 256 rows of x as the N side, so that
 // the weights are read once and no tensor-core row is wasted. k is split over a
 // cluster of up to eight CTAs where there are few columns of y; the partial
 // sums meet in distributed shared memory, added in a fixed order, and there the
@@ -25,20 +25,20 @@ constexpr int kBK = 64, kRows = 64;  // of k a stage; of each weight a CTA
 constexpr int kWeightBytes = 2 * kRows * kBK * 2;
 constexpr int kWarps = 8, kThreads = 64 + 32 * kWarps;
 constexpr int kMaxSplit = 8;
-constexpr int kCols = 128;  // of tensor memory
-constexpr int kPerSm = 2;
 
 template <int kTok>
 struct Shape {
     static constexpr int STAGE = kWeightBytes + kTok * kBK * 2;
+    static constexpr int COLS = kTok <= 128 ? 128 : 256;  // of tensor memory
+    static constexpr int PER_SM = kTok <= 128 ? 2 : 1;
     static constexpr int BARS = 256;
-    static constexpr int FIT = (kMaxShared / kPerSm - 2048 - BARS) / STAGE;
+    static constexpr int FIT = (kMaxShared / PER_SM - 2048 - BARS) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
     static constexpr int USED = 1024 + STAGES * STAGE + BARS;
-    static constexpr int SMEM = USED > tmem_share(kCols) ? USED : tmem_share(kCols);
+    static constexpr int SMEM = USED > tmem_share(COLS) ? USED : tmem_share(COLS);
     static_assert(STAGES * STAGE >= kTok * 2 * kRows * 4, "the sums fit over the stages");
     static_assert(8 * (2 * STAGES + 1) + 8 <= BARS, "barriers fit");
-    static_assert(kPerSm * (SMEM + 1024) <= kSmShared && SMEM <= kMaxShared, "resident");
+    static_assert(PER_SM * (SMEM + 1024) <= kSmShared && SMEM <= kMaxShared, "resident");
 };
 
 struct FewParams {
@@ -70,7 +70,7 @@ __device__ __forceinline__ void store2(T *to, float a, float b, int cols, bool t
 }
 
 template <int kTok, typename T>
-__global__ void __launch_bounds__(kThreads, kPerSm)
+__global__ void __launch_bounds__(kThreads, Shape<kTok>::PER_SM)
     gated_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
                      const __grid_constant__ FewParams p)
 {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         prefetch_map(&tmG);
         prefetch_map(&tmU);
     }
-    if (warp == 1) tmem_alloc<1>(tmem_slot, kCols);
+    if (warp == 1) tmem_alloc<1>(tmem_slot, S::COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         __syncthreads();
     tc_fence_after();
     if (warp == 1) {
-        tmem_free<1>(tmem, kCols);
+        tmem_free<1>(tmem, S::COLS);
     } else if (warp > 1) {
         // the cluster's warps share out the rows of x, two columns of y a lane
         const int64_t col = col0 + lane * 2;
@@ -230,7 +230,7 @@ struct few_tag;
 
 // Columns of the products (the stages of 80 are four instead of three: 66 to 80 rows of 1280 x 5120 take 9.3 us with them and
 // 10.0 with 128, of 2056 x 3080 10.9 and 11.6; 96, three stages again, gained 1 %).
-int tokens_of(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 80 ? 80 : 128; }
+int tokens_of(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : m <= 80 ? 80 : m <= 128 ? 128 : 256; }
 
 template <int kTok>
 int split_of(int64_t n, int64_t k)
@@ -243,7 +243,7 @@ int split_of(int64_t n, int64_t k)
     int split = 1;
     for (int i = 1; i < 4; ++i) {
         const int next = 1 << i;
-        if (units * next > kPerSm * room[i] || steps < 4 * next) break;
+        if (units * next > S::PER_SM * room[i] || steps < 4 * next) break;
         split = next;
     }
     return split;
@@ -291,15 +291,25 @@ cudaError_t launch_type(const convrot_gated_linear_args &a, cudaStream_t stream)
     case 32: return launch<32, T>(a, stream);
     case 64: return launch<64, T>(a, stream);
     case 80: return launch<80, T>(a, stream);
-    default: return launch<128, T>(a, stream);
+    case 128: return launch<128, T>(a, stream);
+    default: return launch<256, T>(a, stream);
     }
 }
 
 }  // namespace
 
-// 128 rows of 5120 x 13824 take 51 us here and 60 in the many-row kernel, 129 (in a form for 256 rows that is gone) 70 and 61;
-// 1280 x 5120: 11.0 and 12.4, 12.1 and 11.9; 4096 x 11008: 37 and 49, 56 and 49.
-bool gated_few_takes(int64_t m) { return m <= 128; }
+// Up to 128 rows always: 128 of 5120 x 13824 take 51 us here and 60 in the many-row kernel, of 1280 x 5120 11.0 and 12.4, of
+// 4096 x 11008 37 and 49. 129 to 256 rows, whose products have an SM's tensor memory to themselves, where sharing k out saves
+// a CTA fifteen steps or more: the many-row kernel has as few tiles then, does not share k, and takes 0.28 us a step. (129 to
+// 256 rows, here and there: 13824 x 640 16 to 18 us and 62, 5120 x 3840 22 to 25 and 27, 2560 x 3840 14 to 17 and 16, all with
+// 20 steps saved or more; 1280 x 1920, 15 saved, 7.6 to 9.7 and 10.2. 1280 x 2560, 10 saved, 9.8 to 12.4 and 10.5; 640 x 2560,
+// 5 saved, 7.7 to 10.3 and 7.5; none: 5120 x 13824 70 to 83 and 62, 1280 x 5120 12.6 to 15 and 12.3.)
+bool gated_few_takes(int64_t m, int64_t n, int64_t k)
+{
+    if (m <= 128) return true;
+    const int64_t steps = (k + kBK - 1) / kBK, split = split_of<256>(n, k);
+    return m <= 256 && steps - (steps + split - 1) / split >= 15;
+}
 
 cudaError_t launch_gated_few(const convrot_gated_linear_args &a, cudaStream_t stream)
 {
@@ -308,9 +318,9 @@ cudaError_t launch_gated_few(const convrot_gated_linear_args &a, cudaStream_t st
 
 int gated_few_shared(int form, int *columns)
 {
-    const int bytes[5] = {Shape<16>::SMEM, Shape<32>::SMEM, Shape<64>::SMEM, Shape<80>::SMEM, Shape<128>::SMEM};
-    *columns = kCols;
-    return form < 5 ? bytes[form] : 0;
+    const int bytes[6] = {Shape<16>::SMEM, Shape<32>::SMEM, Shape<64>::SMEM, Shape<80>::SMEM, Shape<128>::SMEM, Shape<256>::SMEM};
+    *columns = form < 5 ? Shape<128>::COLS : Shape<256>::COLS;
+    return form < 6 ? bytes[form] : 0;
 }
 
 }  // namespace convrot

@@ -124,3 +124,24 @@ def test_attention_gradient_against_differences_where_it_is_large(lib, tq, tk, h
             assert off < 0.5 * abs(want), (name, at)
             # (the differences' own error: 1e-8 of a third derivative, 1e-12 / 1e-4 of roundings)
             assert abs(float(got[name].reshape(-1)[at]) - want) <= off + 1e-5 * max(1.0, abs(want)), (name, at, want, off)
+
+
+@TYPES
+@pytest.mark.parametrize("m,k,n", [(129, 2560, 130), (200, 5120, 77), (256, 1500, 640), (255, 2056, 1), (130, 13824, 640), (192, 1289, 1920), (256, 5120, 3840)])
+def test_gated_linear_of_long_narrow_layers(lib, m, k, n, dtype):
+    """129 to 256 rows whose k is shared out over a cluster, each activation once."""
+    for i, act in enumerate((bl.ACT_SILU, bl.ACT_GELU_ERF, bl.ACT_GELU_TANH, bl.ACT_NONE)):
+        g = torch.Generator(device="cuda").manual_seed(m + i)
+        pad = (0, 8, 3, 1)[i]
+        x, wg, wu = (torch.randn(r, k + pad, generator=g, device="cuda") for r in (m, n, n))
+        x, wg, wu = (t.to(dtype)[:, :k] for t in (x, wg * k**-0.5, wu * k**-0.5))
+        bg, bu = (torch.randn(n, generator=g, device="cuda") if i % 2 else None for _ in range(2))
+        big = torch.full((m + 1, n + 5), -3.0, dtype=dtype, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = bl.convrot_gated_linear(x, wg, wu, bg, bu, act, keep=True, out=big[:m, :n], dev_status=status)
+        want, bound = more.gated(x, wg, wu, bg, bu, act)
+        for name, a, b, c in zip(("y", "gate", "up"), got, want, bound):
+            off = (a.double() - b).abs()
+            assert (off <= c).all(), (name, act, float((off - c).max()))
+        assert int(status) == 0 and torch.all(big[m] == -3.0) and torch.all(big[:, n:] == -3.0)
+        assert torch.equal(bl.convrot_gated_linear(x, wg, wu, bg, bu, act), got[0])
