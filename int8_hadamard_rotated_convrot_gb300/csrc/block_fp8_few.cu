@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool ok = true;
             for (int j = 0; j < count; ++j) {
                 const int buf = j % S::BUFS;
-                if (!wait(sum_bar(buf), (j / S::BUFS) & 1)) {
+                if (!all_lanes(wait(sum_bar(buf), (j / S::BUFS) & 1))) {
                     ok = false;
                     break;
                 }

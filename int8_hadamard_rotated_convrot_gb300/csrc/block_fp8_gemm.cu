@@ -391,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     next_x = load_f32(sx);
                     next_w = load_f32(++sw);
                 }
-                if (!wait(empty_bar(stage), phase)) {
+                if (!all_lanes(wait(empty_bar(stage), phase))) {
                     ok = false;
                     break;
                 }

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
         int s = 0;
         uint32_t ph = 0;
         for (int i = 0; i < nks; ++i) {
-            if (*abort_flag || !mbar_wait(full_bar(s), ph)) {
+            if (!all_lanes(!*abort_flag && mbar_wait(full_bar(s), ph))) {
                 ok = false;
                 break;
             }
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(LD_THREADS, 1)
     const uint32_t part_addr = base;
     bool ok = true;
     if (warp >= 2) {  // eight warps: two a TMEM lane quadrant, alternate 32-column blocks
-        ok = mbar_wait(accf_bar, 0) && !*abort_flag;
+        ok = all_lanes(mbar_wait(accf_bar, 0) && !*abort_flag);
         if (ok) {
             tc_fence_after();
             const int q = warp & 3, half = (warp - 2) >> 2;

@@ -55,6 +55,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// What all lanes of a warp go by: each of them reads the timer and the flag of a wait for itself, and a warp goes on to
+// instructions that all have to reach (tcgen05.ld, shuffles, barriers).
+__device__ __forceinline__ bool all_lanes(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -255,7 +255,7 @@ struct Waits {
         return ok != 0;
     }
     // by a whole warp: true for all lanes or for none, so that it leaves as a whole or not at all
-    __device__ __forceinline__ bool together(uint32_t bar, uint32_t parity) const { return __all_sync(0xffffffffu, (*this)(bar, parity)); }
+    __device__ __forceinline__ bool together(uint32_t bar, uint32_t parity) const { return all_lanes((*this)(bar, parity)); }
     // whether it is there now
     __device__ __forceinline__ bool now(uint32_t bar, uint32_t parity) const
     {
