@@ -388,8 +388,10 @@ def convrot_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mask: t
     lse [batch, heads, tokens] float32 is the logarithm of each row's sum, for the gradient.
 
     mask [batch, keys' tokens] (bool or uint8) says which keys are there; a query without any has out 0 and lse -inf, and
-    what stands at a masked key does not count, whatever it is. scale: head_dim^-0.5 by default. Each query attends to all
-    keys that are there. ``work`` (uint8) is allocated here when not given."""
+    what stands at a masked key does not count, whatever it is. scale (above 0): head_dim^-0.5 by default; scores that it takes
+    past the floats are infinite. Each query attends to all
+    keys that are there. ``out`` may have any batch, token and head strides, its heads apart from one another and from the
+    inputs. ``work`` (uint8) is allocated here when not given."""
     got = load().attention(q, k, v, mask, _scale(q, scale), out, work, dev_status, stream)
     if isinstance(got, int):
         raise ConvrotError(got, "convrot_attention")

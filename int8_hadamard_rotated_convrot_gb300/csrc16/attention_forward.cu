@@ -28,8 +28,9 @@
 // fp32, and a second kernel weighs the shares by their lse (key_shares; 64 queries,
 // 8 heads of 128, 77000 keys: 811 us whole, 62 so).
 //
-// 32760 queries, heads of 128: 1515 TFLOP/s at 4096 keys and 10 heads (453 us), 1210 at
-// 512 keys and 40 heads (283 us), where an item is four tiles. The products with
+// 32760 queries, heads of 128: 1515 TFLOP/s at 4096 keys and 10 heads (453 us), 1145 to
+// 1215 at 512 keys and 40 heads (283 to 300 us in different runs), where an item is four
+// tiles. The products with
 // their copies and waits, without a softmax, take 415 and 245 us of these, so the
 // softmax is nearly hidden: half of the exponentials, the maxima and the exchange
 // between a row's threads are 3 % together. Two CTAs that share each tile of keys
