@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < 128; ++i) acc[i] = 0;
             for (int c = 0; c < n_chunks; ++c, ++chunk_iter) {
                 const uint32_t buf = chunk_iter & 1u;
-                // (the flag is one load for the whole warp; inside the vote it cost the int8 form 1.6 % in spills)
-                if (*abort_flag || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
+                // (two votes: one over both cost the int8 form 1.6 % in spills)
+                if (!all_lanes(!*abort_flag) || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
                     ok = false;
                     break;
                 }
@@ -1200,7 +1200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8 ? PAIR_THREADS_I
             for (int i = 0; i < PAIR_COLS; ++i) acc[i] = 0;
             for (int c = 0; c < n_chunks; ++c, ++chunk_iter) {
                 const uint32_t buf = chunk_iter & 1u;
-                if (*abort_flag || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
+                if (!all_lanes(!*abort_flag) || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
                     ok = false;
                     break;
                 }
@@ -1221,7 +1221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8 ? PAIR_THREADS_I
             if (!ok) break;
             if constexpr (kLora) {
                 const uint32_t buf = chunk_iter & 1u;
-                if (*abort_flag || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
+                if (!all_lanes(!*abort_flag) || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
                     ok = false;
                     break;
                 }
@@ -1260,7 +1260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8 ? PAIR_THREADS_I
                 for (int i = 0; i < PAIR_COLS; ++i) acc[i] = 0;
                 for (int c = 0; c < n_chunks; ++c, ++chunk_iter) {
                     const uint32_t buf = chunk_iter & 1u;
-                    if (*abort_flag || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
+                    if (!all_lanes(!*abort_flag) || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
                         ok = false;
                         break;
                     }
@@ -1281,7 +1281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8 ? PAIR_THREADS_I
                 if (!ok) break;
                 if constexpr (kLora) {
                     const uint32_t buf = chunk_iter & 1u;
-                    if (*abort_flag || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
+                    if (!all_lanes(!*abort_flag) || !all_lanes(mbar_wait(accf_bar(buf), (chunk_iter >> 1) & 1u))) {
                         ok = false;
                         break;
                     }
